@@ -705,6 +705,230 @@ int xs_debug_bounds_failures(int reset);
  */
 int xs_debug_wait_injection(int64_t wait_limit_ns, int skip_page);
 
+/*
+ * xs_qk_norm_rope - what a model does to q and k between their projection
+ * and the cache: an RMSNorm of every head by itself and the rotation by the
+ * token's position, in one pass.
+ *
+ * For every token t < T and head h, with x = q[t, h, :] (k the same):
+ *     y = x / sqrt(mean(x^2) + eps) * q_weight        (q_weight NULL: y = x)
+ *     (y_a, y_b) = (y_a c_i - y_b s_i, y_b c_i + y_a s_i)
+ * for the rotary_dim / 2 pairs (a, b) = (i, i + rotary_dim / 2), or
+ * (2 i, 2 i + 1) with XS_ROPE_INTERLEAVED, where c_i = cos_sin[p][i] and
+ * s_i = cos_sin[p][rotary_dim / 2 + i], p = positions[t].  The dims from
+ * rotary_dim on are not rotated; rotary_dim 0 rotates nothing (cos_sin and
+ * positions may then be NULL).  fp32 throughout, one rounding to dtype.
+ *
+ * q, k: head h of token t starts t * q_stride + h * D (k_stride) elements
+ * from the pointer, so that they may be slices of one projection's output;
+ * strides are multiples of 16 bytes and at least Hq * D (Hkv * D).  q_out
+ * [T, Hq, D] and k_out [T, Hkv, D] are contiguous; q_out may be q itself
+ * where that is contiguous, and k_out k; they overlap nothing else.
+ * q_weight, k_weight [D] in dtype, or NULL.  cos_sin fp32 [max_pos,
+ * rotary_dim].  positions int32 [T]: a negative one skips its token (nothing
+ * is written for it); one >= max_pos skips it and raises XS_FLAG_BAD_LEN.
+ *
+ * D in {64, 128}; rotary_dim a multiple of 16, at most D; any Hq, Hkv > 0.
+ */
+#define XS_ROPE_INTERLEAVED 1
+#define XS_CACHE_KV4 2
+int xs_qk_norm_rope(void *q_out, void *k_out, const void *q, int64_t q_stride, const void *k,
+                    int64_t k_stride, const void *q_weight, const void *k_weight, float eps,
+                    const float *cos_sin, int max_pos, int rotary_dim, const int32_t *positions,
+                    int T, int Hq, int Hkv, int D, int flags, int dtype, int *err_flag,
+                    cudaStream_t stream);
+
+/*
+ * xs_qk_norm_rope_append, xs_qk_norm_rope_append_paged - the same pass with
+ * the append in it: the normed and rotated k rows, and the v rows as they
+ * are, go to the pages instead of k_out (what xs_qk_norm_rope followed by
+ * xs_kv_append / xs_kv_append_paged would store, bit for bit).  v is strided
+ * like k.
+ *
+ * _append: token t goes to slot_mapping[t] (int64; negative: not appended,
+ * q is still written; at or beyond the pool: XS_FLAG_BAD_SLOT, not appended).
+ * positions and slot_mapping are independent of one another; a token whose
+ * position skips it is not appended.  Slots must be distinct.
+ * _append_paged: row b is the new token of sequence b, at position
+ * context_lens[b] - 1 of its block table; context_lens[b] <= 0 skips the row
+ * (q_out keeps what it held).  A position beyond the table (XS_FLAG_BAD_LEN)
+ * or a block outside the pool (XS_FLAG_BAD_BLOCK) is not appended.
+ *
+ * With XS_CACHE_KV4 the pools are 4-bit pools (below; bf16 only), and the
+ * rows are stored as xs_kv4_append would store them.
+ */
+int xs_qk_norm_rope_append(void *q_out, const void *q, int64_t q_stride, const void *k,
+                           int64_t k_stride, const void *v, int64_t v_stride, const void *q_weight,
+                           const void *k_weight, float eps, const float *cos_sin, int max_pos,
+                           int rotary_dim, const int32_t *positions, void *k_cache, void *v_cache,
+                           const int64_t *slot_mapping, int T, int Hq, int Hkv, int D,
+                           int block_size, int64_t num_blocks, int flags, int dtype, int *err_flag,
+                           cudaStream_t stream);
+int xs_qk_norm_rope_append_paged(void *q_out, const void *q, int64_t q_stride, const void *k,
+                                 int64_t k_stride, const void *v, int64_t v_stride,
+                                 const void *q_weight, const void *k_weight, float eps,
+                                 const float *cos_sin, int max_pos, int rotary_dim, void *k_cache,
+                                 void *v_cache, const int32_t *block_tables,
+                                 int max_blocks_per_seq, const int32_t *context_lens, int B,
+                                 int Hq, int Hkv, int D, int block_size, int64_t num_blocks,
+                                 int flags, int dtype, int *err_flag, cudaStream_t stream);
+
+/*
+ * The 4-bit cache.  A pool is bytes, [num_blocks, Hkv, xs_kv4_page_bytes(D)]:
+ * each block and KV head has a page of 9 D bytes for its 16 rows, 8 D of
+ * codes and D of bf16 scales.  A row is cut into NG = D / 32 groups of 32
+ * dims.  With e the group's element of largest magnitude (the positive one
+ * of a tie) its scale is s = bf16(-e / 8); a value x has the code
+ * n = clamp(rne(x / s), -8, 7) + 8 (8 where s is 0) and stands for s (n - 8).
+ * A group that holds an infinity or a NaN reads back as NaN.
+ *   K page: row o is D / 8 32-bit words; word t NG + c (t < 4, c < NG) has
+ *           dims 32 c + 8 t + i (i < 8) in bits 4 i .. 4 i + 3.  Scales [o][c].
+ *   V page: rows 2 i and 2 i + 1 share D / 4 words; word g NG + c (g < 8) has
+ *           dims 32 c + 4 g + j (j < 4) of row 2 i in bits 4 j .. 4 j + 3, and
+ *           of row 2 i + 1 in bits 16 + 4 j .. .  Scales [i][c][row parity].
+ * A whole block is Hkv * 9 D bytes, which xs_kv_swap and xs_block_copy copy
+ * like any other.  bf16 rows only (XS_F32 is XS_EUNSUPPORTED); D in {64, 128}.
+ *
+ * xs_kv4_page_bytes - 9 D, or XS_EUNSUPPORTED for another D.
+ */
+int64_t xs_kv4_page_bytes(int D);
+
+/*
+ * xs_kv4_append, xs_kv4_append_paged - xs_kv_append / xs_kv_append_paged for
+ * 4-bit pools.  k_new, v_new are strided as in xs_qk_norm_rope (a token's
+ * Hkv rows of D are contiguous).  Errors as the calls they mirror.
+ */
+int xs_kv4_append(const void *k_new, int64_t k_stride, const void *v_new, int64_t v_stride,
+                  void *k_cache, void *v_cache, const int64_t *slot_mapping, int T, int Hkv, int D,
+                  int block_size, int64_t num_blocks, int dtype, int *err_flag,
+                  cudaStream_t stream);
+int xs_kv4_append_paged(const void *k_new, int64_t k_stride, const void *v_new, int64_t v_stride,
+                        void *k_cache, void *v_cache, const int32_t *block_tables,
+                        int max_blocks_per_seq, const int32_t *context_lens, int B, int Hkv, int D,
+                        int block_size, int64_t num_blocks, int dtype, int *err_flag,
+                        cudaStream_t stream);
+
+/*
+ * xs_kv4_unpack - pages of a 4-bit cache as pages of dtype rows: block
+ * block_ids[i] of the 4-bit pools becomes block i of k_out and v_out
+ * ([n, Hkv, 16, D], dtype XS_BF16 or XS_F32), which a prompt chunk's
+ * attention (xs_paged_prefill, xs_paged_prefill_tc) reads with the ids 0, 1,
+ * 2, ....  Each value is s (n - 8) rounded once.  A negative id leaves its
+ * page as it was; one >= num_blocks does too and raises XS_FLAG_BAD_BLOCK.
+ */
+int xs_kv4_unpack(void *k_out, void *v_out, const void *k_cache, const void *v_cache,
+                  const int32_t *block_ids, int n, int Hkv, int D, int block_size,
+                  int64_t num_blocks, int dtype, int *err_flag, cudaStream_t stream);
+
+/*
+ * xs_kv4_decode - decode attention over a 4-bit cache, with optional sinks
+ * and sliding window: the arguments and the result of xs_paged_decode_sinks
+ * (window 0 and sinks NULL: xs_paged_decode) on the values that the pages
+ * stand for.  One call does the whole of it; how a batch is cut is decided on
+ * the device from the lengths.  context_lens[b] <= 0 gives out[b] = 0.
+ * Whatever the pages hold in rows at and behind a sequence's length, or in
+ * front of its window, has no influence.
+ *
+ * workspace: at least xs_kv4_decode_workspace_bytes(B, Hq, Hkv, D) bytes, 16-
+ * byte aligned, zero before the first call that uses it; every completed call
+ * leaves it fit for the next.  Calls that share one must be ordered (one
+ * stream, or one CUDA graph).  A workspace for B sequences serves smaller
+ * batches of the same heads too.  bf16 only; block_size 16; D in {64, 128};
+ * Hq / Hkv in {1, 2, 4, 8}.
+ * Device-side errors: XS_FLAG_BAD_BLOCK (block 0 was read instead),
+ * XS_FLAG_BAD_LEN (the length was clamped to the table).
+ */
+size_t xs_kv4_decode_workspace_bytes(int B, int Hq, int Hkv, int D);
+int xs_kv4_decode(void *out, const void *q, const void *k_cache, const void *v_cache,
+                  const int32_t *block_tables, int max_blocks_per_seq, const int32_t *context_lens,
+                  const void *sinks, int window, int B, int Hq, int Hkv, int D, int block_size,
+                  int64_t num_blocks, float scale, void *workspace, size_t workspace_bytes,
+                  int dtype, int *err_flag, cudaStream_t stream);
+
+/*
+ * Shared pages.  extra_refs int32 [num_blocks], zero at first, counts each
+ * block's owners beyond the first; blocks that the other allocator calls hand
+ * out have 0 and need no change.  Only whole pages are shared (a fork copies
+ * an unfinished one), so an append never meets a shared page.  A sequence
+ * that was forked, or forked from, is released with xs_block_release:
+ * xs_block_free knows nothing of extra_refs.
+ *
+ * xs_block_fork - for every i < n the empty slot children[i] (a negative
+ * length) becomes a copy of the sequence in slot parents[i]: its table lists
+ * the parent's full pages, each counted once more in extra_refs, and, where
+ * the parent's last page is unfinished, a block of its own from the top of
+ * the free stack (entries take them in the order of i).  copies (int64
+ * [n, 2]) gets that page's (parent's block, child's block), or (-1, -1):
+ * xs_block_copy takes it from there, before either sequence appends.  The
+ * rest of the child's row is -1.
+ * An entry is skipped with XS_FLAG_BAD_SLOT (an id outside [0, B), a parent
+ * without a sequence, a child with one, a child that an earlier entry named),
+ * XS_FLAG_BAD_LEN (a parent longer than its table) or XS_FLAG_POOL_EMPTY (no
+ * free block); the child's slot is left as it was, and its copies are -1.
+ * XS_FLAG_BAD_BLOCK: the parent's table or the stack holds an id outside the
+ * pool; it is handed on uncounted and not copied.
+ */
+int xs_block_fork(const int32_t *parents, const int32_t *children, int n, int32_t *block_tables,
+                  int max_blocks_per_seq, int32_t *context_lens, int B, int block_size,
+                  const int32_t *free_stack, int32_t *free_top, int32_t *extra_refs,
+                  int64_t num_blocks, int64_t *copies, int *err_flag, cudaStream_t stream);
+
+/*
+ * xs_block_release - xs_block_free for sequences that may share pages: each
+ * page of a listed slot loses one owner, and the pages that lost their last
+ * one go back on the free stack, the highest id first, so that the lowest is
+ * the next one taken.  The slots' rows and lengths become -1.  A slot listed
+ * twice, or empty, is released once, or not at all.  XS_FLAG_BAD_SLOT as
+ * xs_block_free; XS_FLAG_BAD_BLOCK for a table entry outside the pool, which
+ * is dropped; XS_FLAG_POOL_EMPTY where the stack is full (the blocks that do
+ * not fit are lost).
+ */
+int xs_block_release(const int32_t *seq_ids, int n, int32_t *block_tables, int max_blocks_per_seq,
+                     int32_t *context_lens, int B, int block_size, int32_t *free_stack,
+                     int32_t *free_top, int64_t stack_capacity, int32_t *extra_refs,
+                     int64_t num_blocks, int *err_flag, cudaStream_t stream);
+
+/*
+ * xs_block_compact - closes up a fragmented pool.  A block is live if a
+ * sequence's table lists it among its pages.  With L live blocks, the live
+ * ones with ids >= L move, in ascending order, to the dead ids < L, in
+ * ascending order; afterwards exactly the blocks 0 .. L - 1 are live.
+ *   block_tables_out  the tables with the new ids; entries past a sequence's
+ *                     pages are copied as they are.  May be block_tables.
+ *   extra_refs_out    the counts under the new ids (0 for the dead).  May be
+ *                     extra_refs.
+ *   free_stack        [num_blocks]: num_blocks - 1 down to L, so that the
+ *                     lowest is taken first; the rest is left as it was.
+ *   free_top          num_blocks - L.
+ *   remap             int32 [num_blocks]: each block's new id, -1 if dead.
+ *   moves             int64 [num_blocks / 2, 2]: the (from, to) pairs, then
+ *                     (-1, -1); n_moves is their count.
+ * No pair's target is another's source, so xs_block_copy(moves, n =
+ * num_blocks / 2, count = n_moves) moves the contents in place; it must run
+ * before the pages are used under their new ids.  XS_FLAG_BAD_LEN (a length
+ * beyond its table counts as the table's), XS_FLAG_BAD_BLOCK (an id outside
+ * the pool is copied as it is).
+ */
+int xs_block_compact(const int32_t *block_tables, int32_t *block_tables_out,
+                     int max_blocks_per_seq, const int32_t *context_lens, int B, int block_size,
+                     const int32_t *extra_refs, int32_t *extra_refs_out, int32_t *free_stack,
+                     int32_t *free_top, int64_t num_blocks, int32_t *remap, int64_t *moves,
+                     int32_t *n_moves, int *err_flag, cudaStream_t stream);
+
+/*
+ * xs_block_copy - copies whole blocks within the pools of every layer: for
+ * i < n (or < *count where count, an int32 on the device, is given and
+ * smaller) and (s, d) = pairs[i] (int64 [n, 2]), block s is copied to block d
+ * in layer l's K pool (k_pools + l * layer_stride_bytes) and V pool, l <
+ * layers.  Pairs with a negative id are skipped; ids >= num_blocks raise
+ * XS_FLAG_BAD_BLOCK and are skipped.  Targets must be distinct, and no target
+ * another pair's source.  block_bytes and layer_stride_bytes are multiples of
+ * 16; a layer's pool is num_blocks * block_bytes.  Bit-exact, any page format.
+ */
+int xs_block_copy(void *k_pools, void *v_pools, int layers, int64_t layer_stride_bytes,
+                  const int64_t *pairs, int64_t n, const int32_t *count, int64_t block_bytes,
+                  int64_t num_blocks, int *err_flag, cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -23,7 +23,8 @@ LIB_PATH = os.path.join(BUILD_DIR, LIB_NAME)
 # computed global-memory index is checked in the kernels (XS_FLAG_BOUNDS).
 DEBUG_BUILD_DIR = os.path.join(PKG, "_build_debug")
 DEBUG_LIB_PATH = os.path.join(DEBUG_BUILD_DIR, "libxs_paged_debug.so")
-SOURCES = ["kv_append.cu", "paged_decode.cu", "kv_swap.cu", "block_alloc.cu", "paged_prefill_tc.cu"]
+SOURCES = ["kv_append.cu", "paged_decode.cu", "kv_swap.cu", "block_alloc.cu", "paged_prefill_tc.cu",
+           "qk_norm_rope.cu", "kv4_cache.cu", "kv4_decode.cu", "block_share.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

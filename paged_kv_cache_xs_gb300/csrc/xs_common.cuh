@@ -86,10 +86,15 @@ __device__ __forceinline__ bool bounds_ok(bool ok, int *err_flag) {
 #define XS_DEFINE_BOUNDS_COUNTER(fn) \
     int fn(int) { return 0; }
 #endif
-// Per translation unit (kv_append.cu, paged_decode.cu, paged_prefill_tc.cu).
+// Per translation unit (kv_append.cu, paged_decode.cu, paged_prefill_tc.cu,
+// qk_norm_rope.cu, kv4_cache.cu, kv4_decode.cu, block_share.cu).
 int bounds_failures_append(int reset);
 int bounds_failures_decode(int reset);
 int bounds_failures_prefill_tc(int reset);
+int bounds_failures_rope(int reset);
+int bounds_failures_kv4_cache(int reset);
+int bounds_failures_kv4_decode(int reset);
+int bounds_failures_share(int reset);
 
 // ------------------------------------------------------------------ mbarrier + bulk copy
 

@@ -168,3 +168,40 @@ class CapturedStep:
 
     def replay(self):
         self.graph.replay()
+
+
+class Kv4DecodeStep:
+    """The decode step on a 4-bit cache, from one layer's q, k and v as they
+    leave their projection: norm of each head and rotation, append into the
+    4-bit pages, attention (``xs_qk_norm_rope_append_paged``, then
+    ``xs_kv4_decode``).
+
+    Owns the attention's workspace and the rotated q.  q_weight, k_weight
+    ([D], bf16, or None: no norm) and cos_sin (``ops.rope_table``, or None: no
+    rotation) are arguments of ``run``, since they differ from layer to layer;
+    sinks and window as in PagedDecodeStep."""
+
+    def __init__(self, B: int, Hq: int, Hkv: int, D: int, device, eps: float = 1e-6,
+                 interleaved: bool = False, sinks=None, window: int = 0):
+        self.B, self.Hq, self.Hkv, self.D = B, Hq, Hkv, D
+        self.eps, self.interleaved = float(eps), bool(interleaved)
+        self.sinks, self.window = sinks, int(window)
+        self.device = torch.device(device)
+        self.ws = ops.Kv4Workspace(B, Hq, Hkv, D, self.device)
+        self.q = torch.zeros(B, Hq, D, dtype=torch.bfloat16, device=self.device)
+        self.err_flag = torch.zeros(1, dtype=torch.int32, device=self.device)
+
+    def run(self, out, q, k_new, v_new, q_weight, k_weight, cos_sin, k_cache, v_cache,
+            block_tables, context_lens, scale):
+        """q [B, Hq, D], k_new and v_new [B, Hkv, D] may be slices of one
+        projection's output; sequence b's new token is at position
+        context_lens[b] - 1."""
+        ops.xs_qk_norm_rope_append_paged(self.q, q, k_new, v_new, q_weight, k_weight, self.eps,
+                                         cos_sin, k_cache, v_cache, block_tables, context_lens,
+                                         interleaved=self.interleaved, err_flag=self.err_flag)
+        ops.xs_kv4_decode(out, self.q, k_cache, v_cache, block_tables, context_lens, scale,
+                          self.ws, sinks=self.sinks, window=self.window, err_flag=self.err_flag)
+
+    def error_flags(self) -> int:
+        """Device error bits raised so far (synchronises)."""
+        return int(self.err_flag.item())

@@ -452,62 +452,75 @@ XS_ROPE_INTERLEAVED = 1
 XS_CACHE_KV4 = 2
 
 
-def _want(ok: bool, what: str) -> None:
-    if not ok:
-        raise ValueError(what)
+def _refuse(what: str):
+    raise ValueError(what)
 
 
-def _same_device(first, *others) -> None:
-    """All tensors on the current CUDA device, where the launch goes."""
-    dev = first.device
-    _want(dev.type == "cuda" and dev.index == torch.cuda.current_device(),
-          f"tensors must be on the current CUDA device, got {dev}")
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _here(first, *others):
+    """The current stream, after a check that all tensors (None: not given) are
+    on the current CUDA device, where the launch goes."""
+    dev = first.get_device()
+    if dev < 0:
+        _refuse("tensors must be on a CUDA device")
+    if dev != _current_device():
+        _refuse(f"tensors are on cuda:{dev}, the current device is cuda:{_current_device()}")
     for t in others:
-        _want(t is None or t.device == dev, "tensors are on different devices")
+        if t is not None and t.get_device() != dev:
+            _refuse("tensors are on different devices")
+    return _raw_stream(dev) if _raw_stream else torch.cuda.current_stream().cuda_stream
 
 
 def _rows(x, what: str) -> int:
     """Token stride of rows [T, H, D] whose heads lie next to one another."""
+    a, b, c = x.stride()
     T, H, D = x.shape
-    _want(x.stride(2) == 1 and (H == 1 or x.stride(1) == D),
-          f"{what}: the heads of a token must be contiguous")
-    return x.stride(0) if T > 1 else H * D
+    if c != 1 or (b != D and H != 1):
+        _refuse(f"{what}: the heads of a token must be contiguous")
+    return a if T > 1 else H * D
 
 
 def _typed(t, dtype, shape, what: str):
-    if t is not None:
-        _want(t.dtype == dtype and tuple(t.shape) == shape,
-              f"{what} must be {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
+    if t is not None and (t.dtype != dtype or t.shape != shape):
+        _refuse(f"{what} must be {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
 
 
 def _pools(k_cache, v_cache, dtype, Hkv: int, D: int):
     """(num_blocks, flags) of a pair of pools for rows of `dtype`: 4-bit pools
     are uint8 [num_blocks, Hkv, 9 D], others dtype [num_blocks, Hkv, 16, D]."""
-    _want(k_cache.dtype == v_cache.dtype and k_cache.shape == v_cache.shape,
-          "k_cache and v_cache differ in type or shape")
-    if k_cache.dtype == torch.uint8:
-        _want(tuple(k_cache.shape[1:]) == (Hkv, 9 * D),
-              f"4-bit pools must be [num_blocks, {Hkv}, {9 * D}], got {list(k_cache.shape)}")
-        return k_cache.shape[0], XS_CACHE_KV4
-    _want(k_cache.dtype == dtype and tuple(k_cache.shape[1:]) == (Hkv, BLOCK_SIZE, D),
-          f"pools must be {dtype} [num_blocks, {Hkv}, {BLOCK_SIZE}, {D}], "
-          f"got {k_cache.dtype} {list(k_cache.shape)}")
-    return k_cache.shape[0], 0
+    shape, kind = k_cache.shape, k_cache.dtype
+    if v_cache.dtype != kind or v_cache.shape != shape:
+        _refuse("k_cache and v_cache differ in type or shape")
+    if kind == torch.uint8:
+        if shape[1:] != (Hkv, 9 * D):
+            _refuse(f"4-bit pools must be [num_blocks, {Hkv}, {9 * D}], got {list(shape)}")
+        return shape[0], XS_CACHE_KV4
+    if kind != dtype or shape[1:] != (Hkv, BLOCK_SIZE, D):
+        _refuse(f"pools must be {dtype} [num_blocks, {Hkv}, {BLOCK_SIZE}, {D}], "
+                f"got {kind} {list(shape)}")
+    return shape[0], 0
 
 
 def _norm_rope_args(q_out, q, k, q_weight, k_weight, cos_sin):
     T, Hq, D = q.shape
     dt = q.dtype
     _typed(q_out, dt, (T, Hq, D), "q_out")
-    _want(k.dtype == dt and k.dim() == 3 and k.shape[0] == T and k.shape[2] == D,
-          f"k must be {dt} [{T}, Hkv, {D}], got {k.dtype} {list(k.shape)}")
+    if k.dtype != dt or k.dim() != 3:
+        _refuse(f"k must be {dt} [{T}, Hkv, {D}], got {k.dtype} {list(k.shape)}")
+    Tk, Hkv, Dk = k.shape
+    if Tk != T or Dk != D:
+        _refuse(f"k must be {dt} [{T}, Hkv, {D}], got {k.dtype} {list(k.shape)}")
     _typed(q_weight, dt, (D,), "q_weight")
     _typed(k_weight, dt, (D,), "k_weight")
     if cos_sin is None:
-        return T, Hq, k.shape[1], D, 0, 0
-    _want(cos_sin.dtype == torch.float32 and cos_sin.dim() == 2,
-          "cos_sin must be float32 [max_pos, rotary_dim]")
-    return T, Hq, k.shape[1], D, cos_sin.shape[0], cos_sin.shape[1]
+        return T, Hq, Hkv, D, 0, 0
+    if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2:
+        _refuse("cos_sin must be float32 [max_pos, rotary_dim]")
+    max_pos, rot = cos_sin.shape
+    return T, Hq, Hkv, D, max_pos, rot
 
 
 def xs_qk_norm_rope(q_out, k_out, q, k, q_weight, k_weight, eps, cos_sin, positions,
@@ -519,13 +532,13 @@ def xs_qk_norm_rope(q_out, k_out, q, k, q_weight, k_weight, eps, cos_sin, positi
     T, Hq, Hkv, D, max_pos, rot = _norm_rope_args(q_out, q, k, q_weight, k_weight, cos_sin)
     _typed(k_out, q.dtype, (T, Hkv, D), "k_out")
     _typed(positions, torch.int32, (T,), "positions")
-    _same_device(q, k, q_out, k_out, q_weight, k_weight, cos_sin, positions, err_flag)
+    here = _here(q, k, q_out, k_out, q_weight, k_weight, cos_sin, positions, err_flag)
     if T == 0:
         return
     _call("xs_qk_norm_rope", _ptr(q_out), _ptr(k_out), q.data_ptr(), _rows(q, "q"), k.data_ptr(),
           _rows(k, "k"), _ptr(q_weight), _ptr(k_weight), float(eps), _ptr(cos_sin), max_pos, rot,
           _ptr(positions), T, Hq, Hkv, D, XS_ROPE_INTERLEAVED if interleaved else 0,
-          dtype_code(q.dtype), _ptr(err_flag), _stream(stream))
+          dtype_code(q.dtype), _ptr(err_flag), here if stream is None else _stream(stream))
 
 
 def xs_qk_norm_rope_append(q_out, q, k, v, q_weight, k_weight, eps, cos_sin, positions, k_cache,
@@ -538,7 +551,7 @@ def xs_qk_norm_rope_append(q_out, q, k, v, q_weight, k_weight, eps, cos_sin, pos
     _typed(positions, torch.int32, (T,), "positions")
     _typed(slot_mapping, torch.int64, (T,), "slot_mapping")
     nb, flags = _pools(k_cache, v_cache, q.dtype, Hkv, D)
-    _same_device(q, k, v, q_out, q_weight, k_weight, cos_sin, positions, slot_mapping, k_cache,
+    here = _here(q, k, v, q_out, q_weight, k_weight, cos_sin, positions, slot_mapping, k_cache,
                  v_cache, err_flag)
     if T == 0:
         return
@@ -547,7 +560,7 @@ def xs_qk_norm_rope_append(q_out, q, k, v, q_weight, k_weight, eps, cos_sin, pos
           _ptr(cos_sin), max_pos, rot, _ptr(positions), _ptr(k_cache), _ptr(v_cache),
           _ptr(slot_mapping), T, Hq, Hkv, D, BLOCK_SIZE, nb,
           flags | (XS_ROPE_INTERLEAVED if interleaved else 0), dtype_code(q.dtype),
-          _ptr(err_flag), _stream(stream))
+          _ptr(err_flag), here if stream is None else _stream(stream))
 
 
 def xs_qk_norm_rope_append_paged(q_out, q, k, v, q_weight, k_weight, eps, cos_sin, k_cache,
@@ -559,7 +572,7 @@ def xs_qk_norm_rope_append_paged(q_out, q, k, v, q_weight, k_weight, eps, cos_si
     _typed(v, q.dtype, (B, Hkv, D), "v")
     _tables(block_tables, context_lens, B)
     nb, flags = _pools(k_cache, v_cache, q.dtype, Hkv, D)
-    _same_device(q, k, v, q_out, q_weight, k_weight, cos_sin, k_cache, v_cache, block_tables,
+    here = _here(q, k, v, q_out, q_weight, k_weight, cos_sin, k_cache, v_cache, block_tables,
                  context_lens, err_flag)
     if B == 0:
         return
@@ -568,12 +581,13 @@ def xs_qk_norm_rope_append_paged(q_out, q, k, v, q_weight, k_weight, eps, cos_si
           _ptr(cos_sin), max_pos, rot, _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
           block_tables.shape[1], _ptr(context_lens), B, Hq, Hkv, D, BLOCK_SIZE, nb,
           flags | (XS_ROPE_INTERLEAVED if interleaved else 0), dtype_code(q.dtype),
-          _ptr(err_flag), _stream(stream))
+          _ptr(err_flag), here if stream is None else _stream(stream))
 
 
 def _tables(block_tables, context_lens, B: int) -> None:
-    _want(block_tables.dtype == torch.int32 and block_tables.dim() == 2 and
-          block_tables.shape[0] == B, f"block_tables must be int32 [{B}, max_blocks]")
+    if (block_tables.dtype != torch.int32 or block_tables.dim() != 2 or
+            block_tables.shape[0] != B):
+        _refuse(f"block_tables must be int32 [{B}, max_blocks]")
     _typed(context_lens, torch.int32, (B,), "context_lens")
 
 
@@ -605,7 +619,8 @@ def kv4_pools(num_blocks: int, Hkv: int, D: int, device, layers: int | None = No
 
 
 def _kv4_pools(k_cache, v_cache, Hkv: int, D: int) -> int:
-    _want(k_cache.dtype == torch.uint8, "k_cache and v_cache must be 4-bit (uint8) pools")
+    if k_cache.dtype != torch.uint8:
+        _refuse("k_cache and v_cache must be 4-bit (uint8) pools")
     return _pools(k_cache, v_cache, None, Hkv, D)[0]
 
 
@@ -616,12 +631,12 @@ def xs_kv4_append(k_new, v_new, k_cache, v_cache, slot_mapping, err_flag=None, s
     _typed(v_new, k_new.dtype, (T, Hkv, D), "v_new")
     _typed(slot_mapping, torch.int64, (T,), "slot_mapping")
     nb = _kv4_pools(k_cache, v_cache, Hkv, D)
-    _same_device(k_new, v_new, k_cache, v_cache, slot_mapping, err_flag)
+    here = _here(k_new, v_new, k_cache, v_cache, slot_mapping, err_flag)
     if T == 0:
         return
     _call("xs_kv4_append", k_new.data_ptr(), _rows(k_new, "k_new"), v_new.data_ptr(),
           _rows(v_new, "v_new"), _ptr(k_cache), _ptr(v_cache), _ptr(slot_mapping), T, Hkv, D,
-          BLOCK_SIZE, nb, dtype_code(k_new.dtype), _ptr(err_flag), _stream(stream))
+          BLOCK_SIZE, nb, dtype_code(k_new.dtype), _ptr(err_flag), here if stream is None else _stream(stream))
 
 
 def xs_kv4_append_paged(k_new, v_new, k_cache, v_cache, block_tables, context_lens, err_flag=None,
@@ -631,13 +646,13 @@ def xs_kv4_append_paged(k_new, v_new, k_cache, v_cache, block_tables, context_le
     _typed(v_new, k_new.dtype, (B, Hkv, D), "v_new")
     _tables(block_tables, context_lens, B)
     nb = _kv4_pools(k_cache, v_cache, Hkv, D)
-    _same_device(k_new, v_new, k_cache, v_cache, block_tables, context_lens, err_flag)
+    here = _here(k_new, v_new, k_cache, v_cache, block_tables, context_lens, err_flag)
     if B == 0:
         return
     _call("xs_kv4_append_paged", k_new.data_ptr(), _rows(k_new, "k_new"), v_new.data_ptr(),
           _rows(v_new, "v_new"), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
           block_tables.shape[1], _ptr(context_lens), B, Hkv, D, BLOCK_SIZE, nb,
-          dtype_code(k_new.dtype), _ptr(err_flag), _stream(stream))
+          dtype_code(k_new.dtype), _ptr(err_flag), here if stream is None else _stream(stream))
 
 
 def xs_kv4_unpack(k_out, v_out, k_cache, v_cache, block_ids, err_flag=None, stream=None):
@@ -645,16 +660,17 @@ def xs_kv4_unpack(k_out, v_out, k_cache, v_cache, block_ids, err_flag=None, stre
     k_out, v_out [n, Hkv, 16, D] (bf16 or fp32): what xs_paged_prefill and
     xs_paged_prefill_tc read for a prompt chunk over a 4-bit cache."""
     n, Hkv, bs, D = k_out.shape
-    _want(bs == BLOCK_SIZE, f"k_out must be [n, Hkv, {BLOCK_SIZE}, D]")
+    if bs != BLOCK_SIZE:
+        _refuse(f"k_out must be [n, Hkv, {BLOCK_SIZE}, D]")
     _typed(v_out, k_out.dtype, (n, Hkv, bs, D), "v_out")
     _typed(block_ids, torch.int32, (n,), "block_ids")
     nb = _kv4_pools(k_cache, v_cache, Hkv, D)
-    _same_device(k_out, v_out, k_cache, v_cache, block_ids, err_flag)
+    here = _here(k_out, v_out, k_cache, v_cache, block_ids, err_flag)
     if n == 0:
         return
     _call("xs_kv4_unpack", _ptr(k_out), _ptr(v_out), _ptr(k_cache), _ptr(v_cache),
           _ptr(block_ids), n, Hkv, D, bs, nb, dtype_code(k_out.dtype), _ptr(err_flag),
-          _stream(stream))
+          here if stream is None else _stream(stream))
 
 
 class Kv4Workspace:
@@ -662,7 +678,7 @@ class Kv4Workspace:
     (zeroed) once; calls that share one must be ordered."""
 
     def __init__(self, B: int, Hq: int, Hkv: int, D: int, device):
-        self.B, self.Hq, self.Hkv, self.D = B, Hq, Hkv, D
+        self.B, self.heads = B, (Hq, Hkv, D)
         self.nbytes = int(load().xs_kv4_decode_workspace_bytes(B, Hq, Hkv, D))
         self.buf = torch.zeros(max(self.nbytes, 16), dtype=torch.uint8, device=device)
 
@@ -673,21 +689,22 @@ def xs_kv4_decode(out, q, k_cache, v_cache, block_tables, context_lens, scale, w
     optional sinks ([Hq], bf16) and sliding window, in one call."""
     B, Hq, D = q.shape
     _typed(out, q.dtype, (B, Hq, D), "out")
-    _want(k_cache.dim() == 3, "4-bit pools must be [num_blocks, Hkv, 9 D]")
+    if k_cache.dim() != 3:
+        _refuse("4-bit pools must be [num_blocks, Hkv, 9 D]")
     Hkv = k_cache.shape[1]
     nb = _kv4_pools(k_cache, v_cache, Hkv, D)
     _tables(block_tables, context_lens, B)
     _typed(sinks, q.dtype, (Hq,), "sinks")
-    _want((workspace.Hq, workspace.Hkv, workspace.D) == (Hq, Hkv, D) and B <= workspace.B,
-          "the workspace is for other heads or a smaller batch")
+    if workspace.heads != (Hq, Hkv, D) or B > workspace.B:
+        _refuse("the workspace is for other heads or a smaller batch")
     buf = workspace.buf
-    _same_device(q, out, k_cache, v_cache, block_tables, context_lens, sinks, buf, err_flag)
+    here = _here(q, out, k_cache, v_cache, block_tables, context_lens, sinks, buf, err_flag)
     if B == 0:
         return
     _call("xs_kv4_decode", _ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
           block_tables.shape[1], _ptr(context_lens), _ptr(sinks), int(window), B, Hq, Hkv, D,
           BLOCK_SIZE, nb, float(scale), buf.data_ptr(), workspace.nbytes, dtype_code(q.dtype),
-          _ptr(err_flag), _stream(stream))
+          _ptr(err_flag), here if stream is None else _stream(stream))
 
 
 # ---------------------------------------------------------------- shared pages
@@ -704,14 +721,14 @@ def xs_block_fork(parents, children, block_tables, context_lens, free_stack, fre
     _typed(copies, torch.int64, (n, 2), "copies")
     _tables(block_tables, context_lens, B)
     _share(free_stack, free_top, extra_refs)
-    _same_device(parents, children, block_tables, context_lens, free_stack, free_top, extra_refs,
+    here = _here(parents, children, block_tables, context_lens, free_stack, free_top, extra_refs,
                  copies, err_flag)
     if n == 0:
         return
     _call("xs_block_fork", _ptr(parents), _ptr(children), n, _ptr(block_tables),
           block_tables.shape[1], _ptr(context_lens), B, block_size, _ptr(free_stack),
           _ptr(free_top), _ptr(extra_refs), extra_refs.numel(), _ptr(copies), _ptr(err_flag),
-          _stream(stream))
+          here if stream is None else _stream(stream))
 
 
 def xs_block_release(seq_ids, block_tables, context_lens, free_stack, free_top, extra_refs,
@@ -722,20 +739,21 @@ def xs_block_release(seq_ids, block_tables, context_lens, free_stack, free_top, 
     _typed(seq_ids, torch.int32, (seq_ids.numel(),), "seq_ids")
     _tables(block_tables, context_lens, B)
     _share(free_stack, free_top, extra_refs)
-    _same_device(seq_ids, block_tables, context_lens, free_stack, free_top, extra_refs, err_flag)
+    here = _here(seq_ids, block_tables, context_lens, free_stack, free_top, extra_refs, err_flag)
     if seq_ids.numel() == 0:
         return
     _call("xs_block_release", _ptr(seq_ids), seq_ids.numel(), _ptr(block_tables),
           block_tables.shape[1], _ptr(context_lens), B, block_size, _ptr(free_stack),
           _ptr(free_top), free_stack.numel(), _ptr(extra_refs), extra_refs.numel(),
-          _ptr(err_flag), _stream(stream))
+          _ptr(err_flag), here if stream is None else _stream(stream))
 
 
 def _share(free_stack, free_top, extra_refs) -> None:
-    for t, what in ((free_stack, "free_stack"), (free_top, "free_top"),
-                    (extra_refs, "extra_refs")):
-        _want(t.dtype == torch.int32, f"{what} must be int32")
-    _want(free_top.numel() == 1, "free_top must be one int32")
+    i32 = torch.int32
+    if free_stack.dtype != i32 or free_top.dtype != i32 or extra_refs.dtype != i32:
+        _refuse("free_stack, free_top and extra_refs must be int32")
+    if free_top.numel() != 1:
+        _refuse("free_top must be one int32")
 
 
 def xs_block_compact(block_tables, block_tables_out, context_lens, extra_refs, extra_refs_out,
@@ -755,30 +773,31 @@ def xs_block_compact(block_tables, block_tables_out, context_lens, extra_refs, e
     _typed(remap, torch.int32, (nb,), "remap")
     _typed(moves, torch.int64, (nb // 2, 2), "moves")
     _typed(n_moves, torch.int32, (1,), "n_moves")
-    _same_device(block_tables, block_tables_out, context_lens, extra_refs, extra_refs_out,
+    here = _here(block_tables, block_tables_out, context_lens, extra_refs, extra_refs_out,
                  free_stack, free_top, remap, moves, n_moves, err_flag)
     _call("xs_block_compact", _ptr(block_tables), _ptr(block_tables_out), block_tables.shape[1],
           _ptr(context_lens), B, block_size, _ptr(extra_refs), _ptr(extra_refs_out),
           _ptr(free_stack), _ptr(free_top), nb, _ptr(remap), _ptr(moves), _ptr(n_moves),
-          _ptr(err_flag), _stream(stream))
+          _ptr(err_flag), here if stream is None else _stream(stream))
 
 
 def xs_block_copy(k_pools, v_pools, pairs, count=None, err_flag=None, stream=None):
     """Copy block s to block d for every row (s, d) of pairs (int64 [n, 2]; the
     first `count` (int32 [1], device) of them if given) within the K and V
     pools of every layer: [layers, num_blocks, Hkv, ...], any page format."""
-    _want(k_pools.dim() >= 3 and k_pools.dtype == v_pools.dtype and
-          k_pools.shape == v_pools.shape, "k_pools and v_pools differ in type or shape")
-    layers, nb = k_pools.shape[:2]
+    shape = k_pools.shape
+    if v_pools.shape != shape or v_pools.dtype != k_pools.dtype or len(shape) < 3:
+        _refuse("k_pools and v_pools must be [layers, num_blocks, ...] of one type and shape")
+    layers, nb = shape[0], shape[1]
     n = pairs.shape[0]
     _typed(pairs, torch.int64, (n, 2), "pairs")
     _typed(count, torch.int32, (1,), "count")
-    _same_device(k_pools, v_pools, pairs, count, err_flag)
+    here = _here(k_pools, v_pools, pairs, count, err_flag)
     if layers == 0 or nb == 0 or n == 0:
         return
     block = k_pools.numel() // (layers * nb) * k_pools.element_size()
     _call("xs_block_copy", _ptr(k_pools), _ptr(v_pools), layers, nb * block, _ptr(pairs), n,
-          _ptr(count), block, nb, _ptr(err_flag), _stream(stream))
+          _ptr(count), block, nb, _ptr(err_flag), here if stream is None else _stream(stream))
 
 
 def xs_version() -> int:

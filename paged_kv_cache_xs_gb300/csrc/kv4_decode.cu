@@ -4,36 +4,70 @@
 //     out[b, h] = sum_t softmax_t(scale q[b, h] . K_t) V_t
 //     K_t = s_tc (n_td - 8) for d in group c, V_t the same
 //
-// A page of one KV head serves the G = Hq / Hkv query heads of its group.
-// With keys (or dims) on the 16 rows of m16n8k16 and heads on its 8 columns:
+// A page of one KV head serves the G = Hq / Hkv query heads of its group, on
+// m16n8k16 matrix instructions:
 //
-//   logits   S[t, h] = sum_c s_tc (sum_{d in c} (128 + n_td) q_hd - 136 sum_{d in c} q_hd)
-//            A code becomes the bf16 128 + n by one bitwise operation
-//            (0x4300 | n); the -136 sum q is the accumulator's initial value,
-//            and the group's scale is applied to the fp32 result.  128 + n
-//            and q are exact, so the logits are fp32 sums of exact products.
-//   values   O[d, h] = sum_t (n_td - 8) (p_th s_tc)
-//            p is rounded to bf16 (2^-9) and its product with the scale once
-//            more, as the operand of the matrix instruction has to be; n - 8
-//            is exact.  p meets the scale, not the codes: 4 roundings for a
-//            token and head in place of D.
+//   logits   S[h, t] = sum_c s_tc (sum_{d in c} n_td q_hd - 8 sum_{d in c} q_hd),
+//            heads on the 16 rows (8 used), keys on the 8 columns, fp16.  A
+//            pair of codes masked out of its word is the fp16 pair n 2^-24
+//            (or n 2^-20 one nibble higher), exactly: no conversion.  q is
+//            scaled by a power of two to below 2^16, by 1 / 16 more where it
+//            meets the higher nibbles; its bf16 significand fits fp16.  The
+//            - 8 sum q is the accumulator's initial value, and the group's
+//            scale is applied to the fp32 sum, so a logit is an fp32 sum of
+//            exact products.  (Keys on the rows would take half the matrix
+//            instructions, but leave p where the second product cannot use
+//            it; this way p is in place, in fp32.)
+//   values   O[d, h] = sum_t (n_td - 8) (p_th s_tc), dims on the rows, heads on
+//            the columns, bf16, whose range p s needs.  p s is one product in
+//            fp32 and one rounding (2^-9); n - 8 is exact.  The scale meets p,
+//            not the codes: 4 products for a token and head in place of D.
 //
-// The softmax is online, in fp32, with a running maximum that is a multiple
-// of nothing: it follows the true one only when a logit exceeds it by 2^8, so
-// that most pages take no exchange between lanes (p up to 2^8 is harmless in
-// fp32 and bf16).
+// The softmax is online, in fp32.  Its reference follows the running maximum
+// only when a logit exceeds it by 2^8, so most pages take no exchange between
+// lanes; p up to 2^8 is harmless in fp32 and bf16.
 //
-// A lane's share of a page lies at one place of it (16 bytes of K codes for
-// each of two rows, 16 of V codes for each of two row pairs), so pages go
-// straight from global memory to registers, the next one while the current
-// one is worked on.
+// Each warp works on pages of its own, which reach its ring of kStages places
+// in shared memory by bulk copies (one for K, one for V) that lane 0 starts
+// kStages pages ahead.  A lane's share of a page is a few 16-byte pieces that
+// need no further exchange, so a page is waited for, read and given back with
+// no barrier but the warp's own.
+//
+// Split: the pages of all sequences and KV heads form one line, each sequence
+// and head ("segment") with kSegmentCost more for its start and end.  The line
+// is cut into equal shares, one for each CTA, whatever the lengths are: CTA i
+// finds its place from the lengths themselves, so the host needs to know none
+// of them and a captured call follows them.  A segment that lies within a
+// share is written at once.  One that is cut leaves fp32 partials in the
+// workspace, at most two for each CTA whatever the batch, and the CTA that
+// finishes it last joins them in order: the result does not depend on which
+// that is.
+#include <atomic>
+
+#include <cuda_fp16.h>
+
 #include "kv4.cuh"
 
 namespace xs {
 namespace {
 
-constexpr int kDecWarps = 8;
+constexpr int kDecWarps = 4;
+constexpr int kDecThreads = kDecWarps * 32;
+constexpr int kDecCtasPerSm = 4;
+constexpr int kMaxCtas = 1024;     // the workspace holds partials for so many
+constexpr int kSegmentCost = 4;    // pages
+constexpr int kMinShare = 16;      // pages
+constexpr int kStages = 4;         // pages of a warp's ring
+constexpr uint64_t kWaitLimitNs = 4000000000ull;
 
+__device__ __forceinline__ void mma_f16(float *c, uint32_t a0, uint32_t a2, uint32_t b0,
+                                        uint32_t b1) {  // rows 8..15 of A are zero
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%5}, "
+        "{%7,%8}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(0), "r"(a2), "r"(b0), "r"(b1));
+}
 __device__ __forceinline__ void mma_bf16(float *c, uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
     asm volatile(
@@ -42,43 +76,53 @@ __device__ __forceinline__ void mma_bf16(float *c, uint32_t a0, uint32_t a1, uin
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
-    uint32_t y;
-    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
-    return y;
+
+// Two fp32 values in one operation.
+struct F2 {
+    float x, y;
+};
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+    F2 r;
+    asm("{\n .reg .b64 p, q, s;\n mov.b64 p, {%2, %3};\n mov.b64 q, {%4, %5};\n"
+        " mul.rn.f32x2 s, p, q;\n mov.b64 {%0, %1}, s;\n}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
 }
-// Codes j of both halves of a word as the bf16 pair 128 + n.
-__device__ __forceinline__ uint32_t codes128(uint32_t w, int j) {
-    return ((w >> (4 * j)) & 0x000f000fu) | 0x43004300u;
-}
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
-__device__ __forceinline__ __nv_bfloat162 as_bf162(uint32_t x) {
-    return *reinterpret_cast<const __nv_bfloat162 *>(&x);
-}
-__device__ __forceinline__ uint32_t as_u32(__nv_bfloat162 x) {
-    return *reinterpret_cast<const uint32_t *>(&x);
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("{\n .reg .b64 p, q, s;\n mov.b64 p, {%2, %3};\n mov.b64 q, {%4, %5};\n"
+        " mov.b64 s, {%6, %7};\n fma.rn.f32x2 s, p, q, s;\n mov.b64 {%0, %1}, s;\n}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return r;
 }
 
-// A lane's registers of one page.  NG = D / 32 words of each row / row pair.
-template <int NG> struct PageRegs {
-    uint32_t k[2][NG];   // rows g, g + 8
-    uint32_t v[2][NG];   // row pairs t, t + 4
-    uint32_t ks[2][(NG + 1) / 2];  // scales of rows g, g + 8: bf16 [NG]
-    uint32_t vs[2][NG];  // scale pairs of row pairs t, t + 4
-};
+// Codes j and j + 4 of a word, as fp16: n 2^-24 for even j, n 2^-20 for odd.
+__device__ __forceinline__ uint32_t codes_f16(uint32_t w, int j) {
+    return (j & 2 ? w >> 8 : w) & (j & 1 ? 0x00f000f0u : 0x000f000fu);
+}
+// The same codes as bf16 n - 8: 0x4300 | n is 128 + n, and the difference is exact.
+__device__ __forceinline__ uint32_t codes_bf16(uint32_t w, int j) {
+    const uint32_t x = ((w >> (4 * j)) & 0x000f000fu) | 0x43004300u, off = 0x43084308u;
+    const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&x),
+                                     *reinterpret_cast<const __nv_bfloat162 *>(&off));
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+__device__ __forceinline__ uint32_t pack_bf16(F2 v) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(v.x, v.y);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
 template <int N> __device__ __forceinline__ void load_words(uint32_t *r, const uint8_t *p) {
     if constexpr (N == 4) {
-        const uint4 x = __ldg(reinterpret_cast<const uint4 *>(p));
+        const uint4 x = *reinterpret_cast<const uint4 *>(p);
         r[0] = x.x, r[1] = x.y, r[2] = x.z, r[3] = x.w;
-    } else if constexpr (N == 2) {
-        const uint2 x = __ldg(reinterpret_cast<const uint2 *>(p));
-        r[0] = x.x, r[1] = x.y;
     } else {
-        r[0] = __ldg(reinterpret_cast<const uint32_t *>(p));
+        const uint2 x = *reinterpret_cast<const uint2 *>(p);
+        r[0] = x.x, r[1] = x.y;
     }
 }
 
@@ -91,210 +135,447 @@ struct Kv4DecodeParams {
     int max_blocks, window, B, Hq, Hkv, G;
     int64_t num_blocks;
     float scale_log2;
+    int *counters;      // [gridDim.x]: arrivals at the segment that CTA i begins and does not end
+    float *partials;    // [gridDim.x][2][G (D + 2)]: o, then m, then l
     int *err_flag;
 };
 
-template <int D>
-__global__ void __launch_bounds__(kDecWarps * 32) kv4_decode_kernel(const Kv4DecodeParams p) {
-    constexpr int NG = D / 32;
-    __shared__ float sm_m[kDecWarps][8], sm_l[kDecWarps][8];
-    __shared__ float sm_o[kDecWarps][8][D];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-    const int hk = blockIdx.x, b = blockIdx.y;
-    int n = p.lens[b];
-    if (n > p.max_blocks * 16) {
-        if (threadIdx.x == 0 && hk == 0) raise_flag(p.err_flag, XS_FLAG_BAD_LEN);
-        n = p.max_blocks * 16;
+// The pages that sequence b's window covers: the first, and how many.
+struct Span {
+    int n, first, page0, pages;  // tokens [first, n)
+};
+__device__ __forceinline__ Span span_of(const Kv4DecodeParams &p, int b) {
+    Span s;
+    s.n = p.lens[b];
+    if (s.n > p.max_blocks * 16) {
+        if (blockIdx.x == 0) raise_flag(p.err_flag, XS_FLAG_BAD_LEN);
+        s.n = p.max_blocks * 16;
     }
-    const int h0 = hk * p.G;
-    __nv_bfloat16 *out = p.out + (static_cast<int64_t>(b) * p.Hq + h0) * D;
-    if (n <= 0) {
-        for (int i = threadIdx.x; i < p.G * D; i += blockDim.x) out[i] = __float2bfloat16_rn(0.0f);
-        return;
-    }
-    const int first = p.window > 0 && n > p.window ? n - p.window : 0;
-    const int page0 = first >> 4, pages = ((n + 15) >> 4) - page0;
-    const int32_t *row = p.tables + static_cast<int64_t>(b) * p.max_blocks + page0;
+    s.n = max(s.n, 0);
+    s.first = p.window > 0 && s.n > p.window ? s.n - p.window : 0;
+    s.page0 = s.first >> 4;
+    s.pages = ((s.n + 15) >> 4) - s.page0;
+    return s;
+}
 
-    // q as the second operand: for group c and step ks, words j = 2 ks and
-    // 2 ks + 1 hold dims 32 c + 8 t + j and + j + 4 of head g.
+template <int D> struct alignas(16) DecodeSmem {
+    uint8_t ring[kDecWarps][kStages][2][kv4_page_bytes(D)];  // K page, V page
+    uint64_t full[kDecWarps][kStages];
+    float o[kDecWarps][8][D];
+    float m[kDecWarps][8], l[kDecWarps][8];
+    int64_t scan[kDecWarps + 1];
+    int64_t start;
+    int b, last;
+};
+
+// Inclusive sum over the CTA's threads; *total gets the sum of all.
+template <int D>
+__device__ __forceinline__ int64_t cta_scan(int64_t v, int64_t *total, DecodeSmem<D> &sm) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, v, d);
+        if (lane >= d) v += y;
+    }
+    __syncthreads();
+    if (lane == 31) sm.scan[warp] = v;
+    __syncthreads();
+    int64_t before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < kDecWarps; ++w) {
+        if (w < warp) before += sm.scan[w];
+        all += sm.scan[w];
+    }
+    *total = all;
+    return v + before;
+}
+
+// A warp's place in its ring: pages started and pages taken since the launch.
+struct RingState {
+    uint32_t started = 0, taken = 0;
+    bool dead = false;   // a wait ran out: nothing more is started or waited for
+};
+
+// Pages [a, e) of one segment: what the CTA's warps leave in shared memory is
+// joined and either written out (whole) or left as the CTA's partial `slot`.
+template <int D>
+__device__ __forceinline__ void run_segment(const Kv4DecodeParams &p, DecodeSmem<D> &sm,
+                                            RingState &ring, int b, int hk, const Span &sp, int a,
+                                            int e, bool whole, int slot) {
+    constexpr int NG = D / 32;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+    const int h0 = hk * p.G;
+    const int32_t *row = p.tables + static_cast<int64_t>(b) * p.max_blocks + sp.page0;
+
+    // Lane k holds the id of the warp's page k of each 32.
+    const int mine = (e - a - warp + kDecWarps - 1) / kDecWarps;   // pages of this warp (or <= 0)
+    auto load_ids = [&](int k0) {
+        const int i = a + warp + (k0 + lane) * kDecWarps;
+        int32_t id = 0;
+        if (i < e && XS_BOUNDS(i >= 0 && sp.page0 + i < p.max_blocks, p.err_flag)) {
+            id = __ldg(row + i);
+            if (id < 0 || id >= p.num_blocks) {
+                raise_flag(p.err_flag, XS_FLAG_BAD_BLOCK);
+                id = 0;
+            }
+        }
+        return id;
+    };
+    int32_t ids = load_ids(0), ids_next = 0;
+    if (mine > 32) ids_next = load_ids(32);
+    int asked = 0;      // pages of this segment started
+    auto start = [&]() {
+        if (asked >= mine || ring.dead) return;
+        if (asked && (asked & 31) == 0) {
+            ids = ids_next;
+            if (asked + 32 < mine) ids_next = load_ids(asked + 32);
+        }
+        const int32_t id = __shfl_sync(0xffffffffu, ids, asked & 31);
+        if (lane == 0) {
+            const int st = ring.started % kStages;
+            uint64_t *bar = &sm.full[warp][st];
+            const int64_t at = (static_cast<int64_t>(id) * p.Hkv + hk) * kv4_page_bytes(D);
+            mbar_arrive_expect_tx(bar, 2 * kv4_page_bytes(D));
+            bulk_g2s(sm.ring[warp][st][0], p.k_cache + at, kv4_page_bytes(D), bar);
+            bulk_g2s(sm.ring[warp][st][1], p.v_cache + at, kv4_page_bytes(D), bar);
+        }
+        ++ring.started;
+        ++asked;
+    };
+#pragma unroll
+    for (int k = 0; k < kStages; ++k) start();
+
+    // q as the first operand: row g is head g (heads past G are zero); words
+    // j = 0..3 of group c hold dims 32 c + 8 t + j and + j + 4.
     uint32_t qf[NG][4];
-    float cinit[NG][2];
+    float cinit[NG], to_log2;
     {
         const bool head = g < p.G;
         const __nv_bfloat16 *q = p.q + (static_cast<int64_t>(b) * p.Hq + h0 + (head ? g : 0)) * D;
+        float f[NG][8], top = 0.0f;
 #pragma unroll
         for (int c = 0; c < NG; ++c) {
             uint4 x = *reinterpret_cast<const uint4 *>(q + 32 * c + 8 * t);
             if (!head) x = make_uint4(0, 0, 0, 0);
-            // x holds dims 0..7 in pairs (0,1) (2,3) (4,5) (6,7)
-            qf[c][0] = __byte_perm(x.x, x.z, 0x5410);
-            qf[c][1] = __byte_perm(x.x, x.z, 0x7632);
-            qf[c][2] = __byte_perm(x.y, x.w, 0x5410);
-            qf[c][3] = __byte_perm(x.y, x.w, 0x7632);
-            float f[8], s = 0.0f;
-            unpack16(x, f, static_cast<__nv_bfloat16 *>(nullptr));
+            unpack16(x, f[c], static_cast<__nv_bfloat16 *>(nullptr));
 #pragma unroll
-            for (int i = 0; i < 8; ++i) s += f[i];
+            for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(f[c][k]));
+        }
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        // 2^15 <= top 2^up < 2^16; a subnormal or zero head counts as 2^-126.
+        const int ex = max(static_cast<int>(__float_as_uint(top) >> 23), 1) - 127;
+        const int up = 15 - ex;
+        const float u0 = __uint_as_float(static_cast<uint32_t>(up / 2 + 127) << 23);
+        const float u1 = __uint_as_float(static_cast<uint32_t>(up - up / 2 + 127) << 23);
+        to_log2 = ldexpf(p.scale_log2, 24 - up);
+#pragma unroll
+        for (int c = 0; c < NG; ++c) {
+            float s = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float d = j & 1 ? 0.0625f : 1.0f;
+                const __half2 h = __floats2half2_rn(f[c][j] * u0 * u1 * d, f[c][j + 4] * u0 * u1 * d);
+                qf[c][j] = *reinterpret_cast<const uint32_t *>(&h);
+                const float2 back = __half22float2(h);
+                s += (back.x + back.y) * (j & 1 ? 16.0f : 1.0f);
+            }
             s += __shfl_xor_sync(0xffffffffu, s, 1);
             s += __shfl_xor_sync(0xffffffffu, s, 2);
-            cinit[c][0] = -136.0f * __shfl_sync(0xffffffffu, s, 8 * t);
-            cinit[c][1] = -136.0f * __shfl_sync(0xffffffffu, s, 8 * t + 4);
+            cinit[c] = s * -0x1p-21f;
         }
     }
 
-    float m[2] = {0.0f, 0.0f}, l[2] = {0.0f, 0.0f};
-    bool fresh = true;  // no finite maximum yet
-    float acc[NG][2][4];
+    float m = 0.0f, l = 0.0f;   // head g: reference, and this lane's share of the sum
+    bool fresh = true;
+    float acc[NG][2][4];        // dims 32 c + 4 g + 2 jj (+ 1) of heads 2 t, 2 t + 1
 #pragma unroll
     for (int c = 0; c < NG; ++c)
 #pragma unroll
         for (int jj = 0; jj < 2; ++jj)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) acc[c][jj][i] = 0.0f;
+            for (int k = 0; k < 4; ++k) acc[c][jj][k] = 0.0f;
 
-    auto page_id = [&](int i) {
-        if (!XS_BOUNDS(i >= 0 && page0 + i < p.max_blocks, p.err_flag)) return 0;
-        int32_t id = __ldg(row + i);
-        if (id < 0 || id >= p.num_blocks) {
-            if (lane == 0) raise_flag(p.err_flag, XS_FLAG_BAD_BLOCK);
-            id = 0;
+    for (int k = 0; k < mine; ++k) {
+        const int tok0 = (sp.page0 + a + warp + k * kDecWarps) * 16;
+        const int st = ring.taken % kStages;
+        if (ring.dead) break;
+        if (!mbar_wait_bounded(&sm.full[warp][st], (ring.taken / kStages) & 1, kWaitLimitNs))
+            ring.dead = true;
+        if (__any_sync(0xffffffffu, ring.dead)) {
+            ring.dead = true;
+            if (lane == 0) raise_flag(p.err_flag, XS_FLAG_TIMEOUT);
+            break;
         }
-        return id;
-    };
-    PageRegs<NG> cur, nxt;
-    auto load = [&](PageRegs<NG> &r, int32_t id) {
-        const int64_t at = (static_cast<int64_t>(id) * p.Hkv + hk) * kv4_page_bytes(D);
-        const uint8_t *kp = p.k_cache + at, *vp = p.v_cache + at;
+        const uint8_t *kp = sm.ring[warp][st][0], *vp = sm.ring[warp][st][1];
+        F2 x[2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};  // keys 2 t, 2 t + 1, and 8 more
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-            load_words<NG>(r.k[u], kp + (g + 8 * u) * (D / 2) + t * (4 * NG));
-            load_words<NG>(r.v[u], vp + (t + 4 * u) * D + g * (4 * NG));
-            load_words<NG / 2>(r.ks[u], kp + 8 * D + (g + 8 * u) * (2 * NG));
-            load_words<NG>(r.vs[u], vp + 8 * D + (t + 4 * u) * (4 * NG));
+            uint32_t kw[NG], ks[NG];  // row g + 8 u; scales of rows 2 t + 8 u, 2 t + 1 + 8 u
+            load_words<NG>(kw, kp + (g + 8 * u) * (D / 2) + t * (4 * NG));
+            load_words<NG>(ks, kp + 8 * D + (t + 4 * u) * (4 * NG));
+#pragma unroll
+            for (int c = 0; c < NG; ++c) {
+                float s[4] = {cinit[c], cinit[c], 0.0f, 0.0f};
+                const uint32_t w = kw[c];
+                mma_f16(s, qf[c][0], qf[c][1], codes_f16(w, 0), codes_f16(w, 1));
+                mma_f16(s, qf[c][2], qf[c][3], codes_f16(w, 2), codes_f16(w, 3));
+                const uint32_t a0 = ks[c / 2], a1 = ks[NG / 2 + c / 2];
+                const F2 z = c & 1 ? F2{bf_hi(a0), bf_hi(a1)} : F2{bf_lo(a0), bf_lo(a1)};
+                x[u] = fma2(z, F2{s[0], s[1]}, x[u]);
+            }
         }
-    };
-    auto work = [&](PageRegs<NG> &r, int tok0) {
-        float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int c = 0; c < NG; ++c) {
-            float s[4] = {cinit[c][0], cinit[c][1], cinit[c][0], cinit[c][1]};
-#pragma unroll
-            for (int ks = 0; ks < 2; ++ks)
-                mma_bf16(s, codes128(r.k[0][c], 2 * ks), codes128(r.k[1][c], 2 * ks),
-                         codes128(r.k[0][c], 2 * ks + 1), codes128(r.k[1][c], 2 * ks + 1),
-                         qf[c][2 * ks], qf[c][2 * ks + 1]);
-            const uint32_t w0 = r.ks[0][c / 2], w1 = r.ks[1][c / 2];
-            const float s0 = __uint_as_float(c & 1 ? w0 & 0xffff0000u : w0 << 16);
-            const float s1 = __uint_as_float(c & 1 ? w1 & 0xffff0000u : w1 << 16);
-            x[0] = fmaf(s0, s[0], x[0]);
-            x[1] = fmaf(s0, s[1], x[1]);
-            x[2] = fmaf(s1, s[2], x[2]);
-            x[3] = fmaf(s1, s[3], x[3]);
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] *= p.scale_log2;
-        if (tok0 < first || tok0 + 16 > n) {  // rows outside [first, n): whatever the page holds there
-            const float none = -INFINITY;
-            if (tok0 + g < first || tok0 + g >= n) x[0] = x[1] = none;
-            if (tok0 + g + 8 < first || tok0 + g + 8 >= n) x[2] = x[3] = none;
+        x[0] = mul2(x[0], F2{to_log2, to_log2});
+        x[1] = mul2(x[1], F2{to_log2, to_log2});
+        const bool ragged = tok0 < sp.first || tok0 + 16 > sp.n;
+        if (ragged) {  // rows outside [first, n) hold whatever they hold
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 const int ta = tok0 + 2 * t + 8 * u;
-                const uint32_t keep = (ta >= first && ta < n ? 0x0000ffffu : 0u) |
-                                      (ta + 1 >= first && ta + 1 < n ? 0xffff0000u : 0u);
-#pragma unroll
-                for (int c = 0; c < NG; ++c) r.vs[u][c] &= keep;
+                const bool in0 = ta >= sp.first && ta < sp.n;
+                const bool in1 = ta + 1 >= sp.first && ta + 1 < sp.n;
+                if (!in0) x[u].x = -INFINITY;
+                if (!in1) x[u].y = -INFINITY;
             }
         }
-        const float hi0 = fmaxf(x[0], x[2]), hi1 = fmaxf(x[1], x[3]);
-        if (__any_sync(0xffffffffu, fresh || hi0 > m[0] + 8.0f || hi1 > m[1] + 8.0f)) {
-            float h[2] = {hi0, hi1};
+        float hi = fmaxf(fmaxf(x[0].x, x[0].y), fmaxf(x[1].x, x[1].y));
+        if (__any_sync(0xffffffffu, fresh || hi > m + 8.0f)) {
+            hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, 1));
+            hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, 2));
+            // No usable maximum (nothing, or NaN): any finite reference does.
+            const float to = hi > -INFINITY ? (fresh ? hi : fmaxf(m, hi)) : m;
+            const float f = fresh ? 1.0f : fast_exp2(m - to);
+            m = to;
+            l *= f;
+            const float f0 = __shfl_sync(0xffffffffu, f, 8 * t);
+            const float f1 = __shfl_sync(0xffffffffu, f, 8 * t + 4);
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
+            for (int c = 0; c < NG; ++c)
 #pragma unroll
-                for (int d = 4; d < 32; d <<= 1)
-                    h[i] = fmaxf(h[i], __shfl_xor_sync(0xffffffffu, h[i], d));
-                // No usable maximum (nothing, or NaN): any finite reference does.
-                const float to = h[i] > -INFINITY ? (fresh ? h[i] : fmaxf(m[i], h[i])) : m[i];
-                const float f = fresh ? 1.0f : fast_exp2(m[i] - to);
-                m[i] = to;
-                l[i] *= f;
-#pragma unroll
-                for (int c = 0; c < NG; ++c)
-#pragma unroll
-                    for (int jj = 0; jj < 2; ++jj) {
-                        acc[c][jj][i] *= f;
-                        acc[c][jj][i + 2] *= f;
-                    }
-            }
+                for (int jj = 0; jj < 2; ++jj) {
+                    acc[c][jj][0] *= f0;
+                    acc[c][jj][1] *= f1;
+                    acc[c][jj][2] *= f0;
+                    acc[c][jj][3] *= f1;
+                }
             fresh = false;
         }
-        const float p0 = fast_exp2(x[0] - m[0]), p1 = fast_exp2(x[1] - m[1]);
-        const float p2 = fast_exp2(x[2] - m[0]), p3 = fast_exp2(x[3] - m[1]);
-        l[0] += p0 + p2;
-        l[1] += p1 + p3;
-        const __nv_bfloat162 b0 = as_bf162(movmatrix_trans(pack_bf16(p0, p1)));
-        const __nv_bfloat162 b1 = as_bf162(movmatrix_trans(pack_bf16(p2, p3)));
-        const __nv_bfloat162 off = as_bf162(0x43084308u);  // 136
+        F2 pr[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            pr[u] = F2{fast_exp2(x[u].x - m), fast_exp2(x[u].y - m)};
+            l += pr[u].x + pr[u].y;
+        }
+        uint32_t vw[2][NG], vs[2][NG];  // row pairs t, t + 4: dims 32 c + 4 g .., scale pairs
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            load_words<NG>(vw[u], vp + (t + 4 * u) * D + g * (4 * NG));
+            load_words<NG>(vs[u], vp + 8 * D + (t + 4 * u) * (4 * NG));
+        }
+        if (ragged) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int ta = tok0 + 2 * t + 8 * u;
+                const uint32_t keep = (ta >= sp.first && ta < sp.n ? 0x0000ffffu : 0u) |
+                                      (ta + 1 >= sp.first && ta + 1 < sp.n ? 0xffff0000u : 0u);
+#pragma unroll
+                for (int c = 0; c < NG; ++c) vs[u][c] &= keep;
+            }
+        }
+        ++ring.taken;
+        __syncwarp();
+        start();
 #pragma unroll
         for (int c = 0; c < NG; ++c) {
-            const uint32_t w0 = as_u32(__hmul2(b0, as_bf162(r.vs[0][c])));
-            const uint32_t w1 = as_u32(__hmul2(b1, as_bf162(r.vs[1][c])));
+            uint32_t w[2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+                w[u] = pack_bf16(mul2(pr[u], F2{bf_lo(vs[u][c]), bf_hi(vs[u][c])}));
 #pragma unroll
             for (int jj = 0; jj < 2; ++jj)
-                mma_bf16(acc[c][jj], as_u32(__hsub2(as_bf162(codes128(r.v[0][c], 2 * jj)), off)),
-                         as_u32(__hsub2(as_bf162(codes128(r.v[0][c], 2 * jj + 1)), off)),
-                         as_u32(__hsub2(as_bf162(codes128(r.v[1][c], 2 * jj)), off)),
-                         as_u32(__hsub2(as_bf162(codes128(r.v[1][c], 2 * jj + 1)), off)), w0, w1);
+                mma_bf16(acc[c][jj], codes_bf16(vw[0][c], 2 * jj),
+                         codes_bf16(vw[0][c], 2 * jj + 1), codes_bf16(vw[1][c], 2 * jj),
+                         codes_bf16(vw[1][c], 2 * jj + 1), w[0], w[1]);
         }
-    };
-
-    int i = warp;
-    if (i < pages) load(cur, page_id(i));
-    for (; i < pages; i += kDecWarps) {
-        const int next = i + kDecWarps;
-        if (next < pages) load(nxt, page_id(next));
-        work(cur, (page0 + i) * 16);
-        cur = nxt;
     }
 
     // The warps' shares meet in shared memory.  A warp without pages counts
     // as l = 0 under the lowest reference.
-#pragma unroll
-    for (int i2 = 0; i2 < 2; ++i2) {
-#pragma unroll
-        for (int d = 4; d < 32; d <<= 1) l[i2] += __shfl_xor_sync(0xffffffffu, l[i2], d);
-        if (g == 0) {
-            sm_m[warp][2 * t + i2] = fresh ? -3.0e38f : m[i2];
-            sm_l[warp][2 * t + i2] = l[i2];
-        }
-#pragma unroll
-        for (int c = 0; c < NG; ++c)
-#pragma unroll
-            for (int jj = 0; jj < 2; ++jj) {
-                sm_o[warp][2 * t + i2][32 * c + 4 * g + 2 * jj] = acc[c][jj][i2];
-                sm_o[warp][2 * t + i2][32 * c + 4 * g + 2 * jj + 1] = acc[c][jj][i2 + 2];
-            }
+    l += __shfl_xor_sync(0xffffffffu, l, 1);
+    l += __shfl_xor_sync(0xffffffffu, l, 2);
+    __syncthreads();   // the last segment's have been read
+    if (t == 0) {
+        sm.m[warp][g] = fresh ? -3.0e38f : m;
+        sm.l[warp][g] = l;
     }
+#pragma unroll
+    for (int c = 0; c < NG; ++c)
+#pragma unroll
+        for (int jj = 0; jj < 2; ++jj)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                sm.o[warp][2 * t + k][32 * c + 4 * g + 2 * jj] = acc[c][jj][k];
+                sm.o[warp][2 * t + k][32 * c + 4 * g + 2 * jj + 1] = acc[c][jj][k + 2];
+            }
     __syncthreads();
-    for (int e = threadIdx.x; e < p.G * D; e += blockDim.x) {
-        const int h = e / D, d = e % D;
+    const int64_t slot_floats = static_cast<int64_t>(p.G) * (D + 2);
+    float *part = p.partials + (2 * static_cast<int64_t>(blockIdx.x) + slot) * slot_floats;
+    __nv_bfloat16 *out = p.out + (static_cast<int64_t>(b) * p.Hq + h0) * D;
+    for (int x = threadIdx.x; x < p.G * D; x += kDecThreads) {
+        const int h = x / D, d = x % D;
         float top = -3.0e38f;
-        for (int w = 0; w < kDecWarps; ++w) top = fmaxf(top, sm_m[w][h]);
+#pragma unroll
+        for (int w = 0; w < kDecWarps; ++w) top = fmaxf(top, sm.m[w][h]);
+        float sink = 0.0f;
+        const bool sinks = whole && p.sinks;
+        if (sinks) {
+            sink = __bfloat162float(p.sinks[h0 + h]) * 1.4426950408889634f;
+            top = fmaxf(top, sink);
+        }
+        float o = 0.0f, total = sinks ? fast_exp2(sink - top) : 0.0f;
+#pragma unroll
+        for (int w = 0; w < kDecWarps; ++w) {
+            const float f = fast_exp2(sm.m[w][h] - top);
+            o = fmaf(f, sm.o[w][h][d], o);
+            total = fmaf(f, sm.l[w][h], total);
+        }
+        if (whole) {
+            out[x] = __float2bfloat16_rn(o / total);
+        } else {
+            __stcg(part + x, o);
+            if (d == 0) {
+                __stcg(part + p.G * D + h, top);
+                __stcg(part + p.G * (D + 1) + h, total);
+            }
+        }
+    }
+}
+
+// The partials of a segment that CTAs f .. last share, joined in order: CTA f
+// left its second, the others their first.
+template <int D>
+__device__ __forceinline__ void join_partials(const Kv4DecodeParams &p, int b, int hk, int f,
+                                              int last) {
+    const int64_t slot_floats = static_cast<int64_t>(p.G) * (D + 2);
+    const int h0 = hk * p.G;
+    __nv_bfloat16 *out = p.out + (static_cast<int64_t>(b) * p.Hq + h0) * D;
+    for (int x = threadIdx.x; x < p.G * D; x += kDecThreads) {
+        const int h = x / D;
+        float top = -3.0e38f;
+        for (int i = f; i <= last; ++i)
+            top = fmaxf(top, __ldcg(p.partials + (2 * static_cast<int64_t>(i) + (i == f)) * slot_floats +
+                                    p.G * D + h));
         float sink = 0.0f;
         if (p.sinks) {
             sink = __bfloat162float(p.sinks[h0 + h]) * 1.4426950408889634f;
             top = fmaxf(top, sink);
         }
         float o = 0.0f, total = p.sinks ? fast_exp2(sink - top) : 0.0f;
-        for (int w = 0; w < kDecWarps; ++w) {
-            const float f = fast_exp2(sm_m[w][h] - top);
-            o += f * sm_o[w][h][d];
-            total += f * sm_l[w][h];
+#pragma unroll 4
+        for (int i = f; i <= last; ++i) {
+            const float *part = p.partials + (2 * static_cast<int64_t>(i) + (i == f)) * slot_floats;
+            const float w = fast_exp2(__ldcg(part + p.G * D + h) - top);
+            o = fmaf(w, __ldcg(part + x), o);
+            total = fmaf(w, __ldcg(part + p.G * (D + 1) + h), total);
         }
-        out[e] = __float2bfloat16_rn(o / total);
+        out[x] = __float2bfloat16_rn(o / total);
     }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm)
+    kv4_decode_kernel(const Kv4DecodeParams p) {
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    DecodeSmem<D> &sm = *reinterpret_cast<DecodeSmem<D> *>(smem_raw);
+    if (threadIdx.x < kDecWarps * kStages) mbar_init(&sm.full[0][0] + threadIdx.x, 1);
+    mbar_fence_init();
+    __syncthreads();
+    RingState ring;
+    // The line's length, this CTA's share of it, and the sequence it begins in.
+    int64_t line = 0;
+    for (int base = 0; base < p.B; base += kDecThreads) {
+        const int b = base + threadIdx.x;
+        int64_t all;
+        cta_scan(b < p.B ? span_of(p, b).pages + kSegmentCost : 0, &all, sm);
+        line += all;
+    }
+    line *= p.Hkv;
+    const int64_t share = max((line + gridDim.x - 1) / gridDim.x, static_cast<int64_t>(kMinShare));
+    const int64_t lo = share * blockIdx.x, hi = min(lo + share, line);
+    if (lo >= hi) return;
+    int64_t before = 0;
+    for (int base = 0; base < p.B && before <= lo; base += kDecThreads) {
+        const int b = base + threadIdx.x;
+        const int64_t v = b < p.B ? static_cast<int64_t>(span_of(p, b).pages + kSegmentCost) * p.Hkv : 0;
+        int64_t all;
+        const int64_t end = before + cta_scan(v, &all, sm);
+        if (lo >= end - v && lo < end) {
+            sm.b = b;
+            sm.start = end - v;
+        }
+        before += all;
+    }
+    __syncthreads();
+    int b = sm.b;
+    int64_t s = sm.start;   // where segment (b, hk) starts
+    Span sp = span_of(p, b);
+    int hk = static_cast<int>((lo - s) / (sp.pages + kSegmentCost));
+    s += static_cast<int64_t>(hk) * (sp.pages + kSegmentCost);
+    while (true) {
+        const int a = static_cast<int>(min(max(lo - s, int64_t(0)), static_cast<int64_t>(sp.pages)));
+        const int e = static_cast<int>(min(hi - s, static_cast<int64_t>(sp.pages)));
+        if (sp.pages == 0) {
+            if (s >= lo) {
+                __nv_bfloat16 *out = p.out + (static_cast<int64_t>(b) * p.Hq + hk * p.G) * D;
+                for (int x = threadIdx.x; x < p.G * D; x += kDecThreads)
+                    out[x] = __float2bfloat16_rn(0.0f);
+            }
+        } else if (a < e) {
+            const bool whole = a == 0 && e == sp.pages;
+            run_segment<D>(p, sm, ring, b, hk, sp, a, e, whole, s >= lo);
+            if (!whole) {
+                const int f = static_cast<int>(s / share);
+                const int last = static_cast<int>((s + sp.pages - 1) / share);
+                __threadfence();
+                __syncthreads();
+                if (threadIdx.x == 0) {
+                    sm.last = atomic_add_acq_rel_gpu(p.counters + f, 1) == last - f;
+                    if (sm.last) p.counters[f] = 0;
+                }
+                __syncthreads();
+                if (sm.last) {
+                    __threadfence();
+                    join_partials<D>(p, b, hk, f, last);
+                }
+            }
+        }
+        s += sp.pages + kSegmentCost;
+        if (s >= hi) break;
+        if (++hk == p.Hkv) {
+            hk = 0;
+            if (++b == p.B) break;
+            sp = span_of(p, b);
+        }
+    }
+    // After a wait that ran out, copies may still be on their way here.
+    if (ring.dead)
+        for (; ring.taken != ring.started; ++ring.taken)
+            mbar_wait_bounded(&sm.full[threadIdx.x >> 5][ring.taken % kStages],
+                              (ring.taken / kStages) & 1, kWaitLimitNs);
+}
+
+// Lets the kernel have its shared memory, once for each device.
+template <int D> int configure(int dev) {
+    static std::atomic<uint64_t> done{0};
+    const uint64_t bit = uint64_t(1) << (dev & 63);
+    if (dev < 64 && (done.load(std::memory_order_acquire) & bit)) return XS_OK;
+    if (cudaFuncSetAttribute(kv4_decode_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             sizeof(DecodeSmem<D>)) != cudaSuccess) {
+        cudaGetLastError();
+        return XS_EDEVICE;
+    }
+    done.fetch_or(bit, std::memory_order_release);
+    return XS_OK;
 }
 
 }  // namespace
@@ -304,7 +585,8 @@ XS_DEFINE_BOUNDS_COUNTER(bounds_failures_kv4_decode)
 
 extern "C" size_t xs_kv4_decode_workspace_bytes(int B, int Hq, int Hkv, int D) {
     if (B <= 0 || Hq <= 0 || Hkv <= 0 || D <= 0) return 0;
-    return 256;
+    const size_t counters = xs::kMaxCtas * sizeof(int);
+    return counters + static_cast<size_t>(xs::kMaxCtas) * 2 * (Hq / Hkv) * (D + 2) * sizeof(float);
 }
 
 extern "C" int xs_kv4_decode(void *out, const void *q, const void *k_cache, const void *v_cache,
@@ -340,10 +622,23 @@ extern "C" int xs_kv4_decode(void *out, const void *q, const void *k_cache, cons
     p.B = B, p.Hq = Hq, p.Hkv = Hkv, p.G = G, p.num_blocks = num_blocks;
     p.scale_log2 = scale * 1.4426950408889634f;
     p.err_flag = err_flag;
-    const dim3 grid(Hkv, B);
+    p.counters = static_cast<int *>(workspace);
+    p.partials = reinterpret_cast<float *>(p.counters + xs::kMaxCtas);
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return XS_EDEVICE;
+    // The line is at most so long, and no CTA takes less than kMinShare of it.
+    const int64_t most = static_cast<int64_t>(B) * Hkv * (max_blocks_per_seq + xs::kSegmentCost);
+    const int64_t want = (most + xs::kMinShare - 1) / xs::kMinShare;
+    const int fill = sms * xs::kDecCtasPerSm < xs::kMaxCtas ? sms * xs::kDecCtasPerSm : xs::kMaxCtas;
+    const int grid = static_cast<int>(want < fill ? want : fill);
+    const int rc = D == 128 ? xs::configure<128>(dev) : xs::configure<64>(dev);
+    if (rc != XS_OK) return rc;
     if (D == 128)
-        xs::kv4_decode_kernel<128><<<grid, xs::kDecWarps * 32, 0, stream>>>(p);
+        xs::kv4_decode_kernel<128>
+            <<<grid, xs::kDecThreads, sizeof(xs::DecodeSmem<128>), stream>>>(p);
     else
-        xs::kv4_decode_kernel<64><<<grid, xs::kDecWarps * 32, 0, stream>>>(p);
+        xs::kv4_decode_kernel<64><<<grid, xs::kDecThreads, sizeof(xs::DecodeSmem<64>), stream>>>(p);
     return xs::launch_status();
 }

@@ -13,9 +13,8 @@
 //            (or n 2^-20 one nibble higher), exactly: no conversion.  q is
 //            scaled by a power of two to below 2^16, by 1 / 16 more where it
 //            meets the higher nibbles; its bf16 significand fits fp16.  The
-//            - 8 sum q is the accumulator's initial value, and the group's
-//            scale is applied to the fp32 sum, so a logit is an fp32 sum of
-//            exact products.  (Keys on the rows would take half the matrix
+//            group's scale is applied to the fp32 sum, so a logit is an fp32
+//            sum of exact products.  (Keys on the rows would take half the matrix
 //            instructions, but leave p where the second product cannot use
 //            it; this way p is in place, in fp32.)
 //   values   O[d, h] = sum_t (n_td - 8) (p_th s_tc), dims on the rows, heads on
@@ -60,23 +59,6 @@ constexpr int kMinShare = 16;      // pages
 constexpr int kStages = 4;         // pages of a warp's ring
 constexpr uint64_t kWaitLimitNs = 4000000000ull;
 
-__device__ __forceinline__ void mma_f16(float *c, uint32_t a0, uint32_t a2, uint32_t b0,
-                                        uint32_t b1) {  // rows 8..15 of A are zero
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%5}, "
-        "{%7,%8}, {%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(0), "r"(a2), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ void mma_bf16(float *c, uint32_t a0, uint32_t a1, uint32_t a2,
-                                         uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-        "{%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
 // Two fp32 values in one operation.
 struct F2 {
     float x, y;
@@ -89,6 +71,14 @@ __device__ __forceinline__ F2 mul2(F2 a, F2 b) {
         : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
     return r;
 }
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+    F2 r;
+    asm("{\n .reg .b64 p, q, s;\n mov.b64 p, {%2, %3};\n mov.b64 q, {%4, %5};\n"
+        " add.rn.f32x2 s, p, q;\n mov.b64 {%0, %1}, s;\n}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
 __device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
     F2 r;
     asm("{\n .reg .b64 p, q, s;\n mov.b64 p, {%2, %3};\n mov.b64 q, {%4, %5};\n"
@@ -96,6 +86,29 @@ __device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
         : "=f"(r.x), "=f"(r.y)
         : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
     return r;
+}
+
+// d = A B (+ d) with rows 8..15 of A zero: d[2] and d[3] stay 0.
+__device__ __forceinline__ void mma_f16_first(float *d, uint32_t a0, uint32_t a2, uint32_t b0,
+                                              uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%5}, "
+        "{%7,%8}, {%9,%9,%9,%9};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(0), "r"(a2), "r"(b0), "r"(b1), "f"(0.0f));
+}
+__device__ __forceinline__ void mma_f16(float *d, uint32_t a0, uint32_t a2, uint32_t b0,
+                                        uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%5}, "
+        "{%7,%8}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(0), "r"(a2), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_bf16(float *c, uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
 // Codes j and j + 4 of a word, as fp16: n 2^-24 for even j, n 2^-20 for odd.
@@ -116,14 +129,15 @@ __device__ __forceinline__ uint32_t pack_bf16(F2 v) {
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
-template <int N> __device__ __forceinline__ void load_words(uint32_t *r, const uint8_t *p) {
-    if constexpr (N == 4) {
-        const uint4 x = *reinterpret_cast<const uint4 *>(p);
-        r[0] = x.x, r[1] = x.y, r[2] = x.z, r[3] = x.w;
-    } else {
-        const uint2 x = *reinterpret_cast<const uint2 *>(p);
-        r[0] = x.x, r[1] = x.y;
-    }
+// N 32-bit words (8 or 16 bytes) at shared address a.
+template <int N> __device__ __forceinline__ void load_words(uint32_t *r, uint32_t a) {
+    if constexpr (N == 4)
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                     : "r"(a)
+                     : "memory");
+    else
+        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(a) : "memory");
 }
 
 struct Kv4DecodeParams {
@@ -163,9 +177,10 @@ template <int D> struct alignas(16) DecodeSmem {
     uint64_t full[kDecWarps][kStages];
     float o[kDecWarps][8][D];
     float m[kDecWarps][8], l[kDecWarps][8];
-    int64_t scan[kDecWarps + 1];
-    int64_t start;
-    int b, last;
+    float weight[kDecThreads];
+    int64_t scan[kDecWarps];
+    int64_t start, share, line;
+    int b, hk, last;
 };
 
 // Inclusive sum over the CTA's threads; *total gets the sum of all.
@@ -190,10 +205,31 @@ __device__ __forceinline__ int64_t cta_scan(int64_t v, int64_t *total, DecodeSme
     return v + before;
 }
 
-// A warp's place in its ring: pages started and pages taken since the launch.
+// Copies of a K and a V page to shared address dst and behind it, counted on
+// the barrier at shared address bar.  Each byte is read once: evict first.
+__device__ __forceinline__ void start_copy(uint32_t dst, const uint8_t *k, int bytes,
+                                           const uint8_t *v, uint32_t bar) {
+    asm volatile(
+        "{\n .reg .b64 pol;\n createpolicy.fractional.L2::evict_first.b64 pol, 1.0;\n"
+        " mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%4], %5;\n"
+        " cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes.L2::cache_hint "
+        "[%0], [%1], %2, [%4], pol;\n"
+        " cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes.L2::cache_hint "
+        "[%6], [%3], %2, [%4], pol;\n}" ::"r"(dst),
+        "l"(k), "r"(bytes), "l"(v), "r"(bar), "r"(2 * bytes), "r"(dst + bytes)
+        : "memory");
+}
+
+// Waits for a ring place with a limit, all lanes alike: false if it ran out.
+__device__ __noinline__ bool warp_waits(uint64_t *bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, kWaitLimitNs));
+}
+
+// A warp's ring since the launch: the pages taken from it, and how many more
+// were started when a wait ran out (then nothing more is started).
 struct RingState {
-    uint32_t started = 0, taken = 0;
-    bool dead = false;   // a wait ran out: nothing more is started or waited for
+    uint32_t taken = 0, behind = 0;
+    bool dead = false;
 };
 
 // Pages [a, e) of one segment: what the CTA's warps leave in shared memory is
@@ -207,10 +243,10 @@ __device__ __forceinline__ void run_segment(const Kv4DecodeParams &p, DecodeSmem
     const int h0 = hk * p.G;
     const int32_t *row = p.tables + static_cast<int64_t>(b) * p.max_blocks + sp.page0;
 
-    // Lane k holds the id of the warp's page k of each 32.
     const int mine = (e - a - warp + kDecWarps - 1) / kDecWarps;   // pages of this warp (or <= 0)
-    auto load_ids = [&](int k0) {
-        const int i = a + warp + (k0 + lane) * kDecWarps;
+    // Lane j holds the id of the warp's page k + j, for the k last loaded at.
+    auto load_ids = [&](int k) {
+        const int i = a + warp + (k + lane) * kDecWarps;
         int32_t id = 0;
         if (i < e && XS_BOUNDS(i >= 0 && sp.page0 + i < p.max_blocks, p.err_flag)) {
             id = __ldg(row + i);
@@ -221,29 +257,25 @@ __device__ __forceinline__ void run_segment(const Kv4DecodeParams &p, DecodeSmem
         }
         return id;
     };
-    int32_t ids = load_ids(0), ids_next = 0;
-    if (mine > 32) ids_next = load_ids(32);
-    int asked = 0;      // pages of this segment started
-    auto start = [&]() {
-        if (asked >= mine || ring.dead) return;
-        if (asked && (asked & 31) == 0) {
-            ids = ids_next;
-            if (asked + 32 < mine) ids_next = load_ids(asked + 32);
-        }
-        const int32_t id = __shfl_sync(0xffffffffu, ids, asked & 31);
+    int32_t ids = load_ids(0);
+    // Starts the copies of the warp's page k into the ring's next place.
+    const uint32_t ring0 = smem_addr(sm.ring[warp]), bar0 = smem_addr(sm.full[warp]);
+    const uint32_t base = ring.taken;
+    auto start = [&](int k) {
+        if (k >= mine) return;
+        if (k && (k & 31) == 0) ids = load_ids(k);
+        const int32_t id = __shfl_sync(0xffffffffu, ids, k & 31);
         if (lane == 0) {
-            const int st = ring.started % kStages;
-            uint64_t *bar = &sm.full[warp][st];
+            const uint32_t st = (base + k) % kStages;
+            const uint32_t dst = ring0 + st * (2 * kv4_page_bytes(D)), bar = bar0 + 8 * st;
             const int64_t at = (static_cast<int64_t>(id) * p.Hkv + hk) * kv4_page_bytes(D);
-            mbar_arrive_expect_tx(bar, 2 * kv4_page_bytes(D));
-            bulk_g2s(sm.ring[warp][st][0], p.k_cache + at, kv4_page_bytes(D), bar);
-            bulk_g2s(sm.ring[warp][st][1], p.v_cache + at, kv4_page_bytes(D), bar);
+            start_copy(dst, p.k_cache + at, kv4_page_bytes(D), p.v_cache + at, bar);
         }
-        ++ring.started;
-        ++asked;
     };
-#pragma unroll
-    for (int k = 0; k < kStages; ++k) start();
+    if (!ring.dead) {
+#pragma unroll 1
+        for (int k = 0; k < kStages; ++k) start(k);
+    }
 
     // q as the first operand: row g is head g (heads past G are zero); words
     // j = 0..3 of group c hold dims 32 c + 8 t + j and + j + 4.
@@ -296,18 +328,17 @@ __device__ __forceinline__ void run_segment(const Kv4DecodeParams &p, DecodeSmem
 #pragma unroll
             for (int k = 0; k < 4; ++k) acc[c][jj][k] = 0.0f;
 
-    for (int k = 0; k < mine; ++k) {
+    for (int k = 0; k < mine && !ring.dead; ++k) {
         const int tok0 = (sp.page0 + a + warp + k * kDecWarps) * 16;
-        const int st = ring.taken % kStages;
-        if (ring.dead) break;
-        if (!mbar_wait_bounded(&sm.full[warp][st], (ring.taken / kStages) & 1, kWaitLimitNs))
+        const uint32_t st = (base + k) % kStages, parity = ((base + k) / kStages) & 1;
+        if (!__all_sync(0xffffffffu, mbar_try_wait(&sm.full[warp][st], parity)) &&
+            !warp_waits(&sm.full[warp][st], parity)) {
             ring.dead = true;
-        if (__any_sync(0xffffffffu, ring.dead)) {
-            ring.dead = true;
+            ring.behind = min(mine - k, kStages);
             if (lane == 0) raise_flag(p.err_flag, XS_FLAG_TIMEOUT);
             break;
         }
-        const uint8_t *kp = sm.ring[warp][st][0], *vp = sm.ring[warp][st][1];
+        const uint32_t kp = ring0 + st * (2 * kv4_page_bytes(D)), vp = kp + kv4_page_bytes(D);
         F2 x[2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};  // keys 2 t, 2 t + 1, and 8 more
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
@@ -316,17 +347,17 @@ __device__ __forceinline__ void run_segment(const Kv4DecodeParams &p, DecodeSmem
             load_words<NG>(ks, kp + 8 * D + (t + 4 * u) * (4 * NG));
 #pragma unroll
             for (int c = 0; c < NG; ++c) {
-                float s[4] = {cinit[c], cinit[c], 0.0f, 0.0f};
                 const uint32_t w = kw[c];
-                mma_f16(s, qf[c][0], qf[c][1], codes_f16(w, 0), codes_f16(w, 1));
+                float s[4];
+                mma_f16_first(s, qf[c][0], qf[c][1], codes_f16(w, 0), codes_f16(w, 1));
                 mma_f16(s, qf[c][2], qf[c][3], codes_f16(w, 2), codes_f16(w, 3));
                 const uint32_t a0 = ks[c / 2], a1 = ks[NG / 2 + c / 2];
                 const F2 z = c & 1 ? F2{bf_hi(a0), bf_hi(a1)} : F2{bf_lo(a0), bf_lo(a1)};
-                x[u] = fma2(z, F2{s[0], s[1]}, x[u]);
+                x[u] = fma2(z, add2(F2{s[0], s[1]}, F2{cinit[c], cinit[c]}), x[u]);
             }
         }
-        x[0] = mul2(x[0], F2{to_log2, to_log2});
-        x[1] = mul2(x[1], F2{to_log2, to_log2});
+        x[0].x *= to_log2, x[0].y *= to_log2;
+        x[1].x *= to_log2, x[1].y *= to_log2;
         const bool ragged = tok0 < sp.first || tok0 + 16 > sp.n;
         if (ragged) {  // rows outside [first, n) hold whatever they hold
 #pragma unroll
@@ -382,9 +413,9 @@ __device__ __forceinline__ void run_segment(const Kv4DecodeParams &p, DecodeSmem
                 for (int c = 0; c < NG; ++c) vs[u][c] &= keep;
             }
         }
-        ++ring.taken;
+        ring.taken = base + k + 1;
         __syncwarp();
-        start();
+        start(k + kStages);
 #pragma unroll
         for (int c = 0; c < NG; ++c) {
             uint32_t w[2];
@@ -452,33 +483,64 @@ __device__ __forceinline__ void run_segment(const Kv4DecodeParams &p, DecodeSmem
 }
 
 // The partials of a segment that CTAs f .. last share, joined in order: CTA f
-// left its second, the others their first.
+// left its second, the others their first.  Weights first, by one thread for
+// each partial and head, then the values.
 template <int D>
-__device__ __forceinline__ void join_partials(const Kv4DecodeParams &p, int b, int hk, int f,
-                                              int last) {
-    const int64_t slot_floats = static_cast<int64_t>(p.G) * (D + 2);
-    const int h0 = hk * p.G;
-    __nv_bfloat16 *out = p.out + (static_cast<int64_t>(b) * p.Hq + h0) * D;
-    for (int x = threadIdx.x; x < p.G * D; x += kDecThreads) {
-        const int h = x / D;
-        float top = -3.0e38f;
-        for (int i = f; i <= last; ++i)
-            top = fmaxf(top, __ldcg(p.partials + (2 * static_cast<int64_t>(i) + (i == f)) * slot_floats +
-                                    p.G * D + h));
-        float sink = 0.0f;
-        if (p.sinks) {
-            sink = __bfloat162float(p.sinks[h0 + h]) * 1.4426950408889634f;
-            top = fmaxf(top, sink);
+__device__ __forceinline__ void join_partials(const Kv4DecodeParams &p, DecodeSmem<D> &sm, int b,
+                                              int hk, int f, int last) {
+    const int G = p.G, per = kDecThreads / G;   // G divides 32
+    const int64_t slot_floats = static_cast<int64_t>(G) * (D + 2);
+    auto part_of = [&](int i) {
+        return p.partials + (2 * static_cast<int64_t>(i) + (i == f)) * slot_floats;
+    };
+    const int h = threadIdx.x % G, k = threadIdx.x / G, lane = threadIdx.x & 31;
+    float sink = 0.0f, top = -3.0e38f;
+    if (p.sinks) top = sink = __bfloat162float(p.sinks[hk * G + h]) * 1.4426950408889634f;
+    for (int i = f + k; i <= last; i += per) top = fmaxf(top, __ldcg(part_of(i) + G * D + h));
+    for (int d = G; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+    if (lane < G) sm.m[threadIdx.x >> 5][lane] = top;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kDecWarps; ++w) top = fmaxf(top, sm.m[w][h]);
+    float total = p.sinks && k == 0 ? fast_exp2(sink - top) : 0.0f;
+    constexpr int kPer = (8 * D) / kDecThreads;     // values of a thread, at most
+    float o[kPer];
+#pragma unroll
+    for (int x = 0; x < kPer; ++x) o[x] = 0.0f;
+    for (int base = f; base <= last; base += per) {
+        float w = 0.0f;
+        if (base + k <= last) {
+            const float *part = part_of(base + k);
+            w = fast_exp2(__ldcg(part + G * D + h) - top);
+            total = fmaf(w, __ldcg(part + G * (D + 1) + h), total);
         }
-        float o = 0.0f, total = p.sinks ? fast_exp2(sink - top) : 0.0f;
+        __syncthreads();
+        sm.weight[threadIdx.x] = w;                 // [k][h]
+        __syncthreads();
+        const int n = min(last - base + 1, per);
 #pragma unroll 4
-        for (int i = f; i <= last; ++i) {
-            const float *part = p.partials + (2 * static_cast<int64_t>(i) + (i == f)) * slot_floats;
-            const float w = fast_exp2(__ldcg(part + p.G * D + h) - top);
-            o = fmaf(w, __ldcg(part + x), o);
-            total = fmaf(w, __ldcg(part + p.G * (D + 1) + h), total);
+        for (int i = 0; i < n; ++i) {
+            const float *part = part_of(base + i);
+#pragma unroll
+            for (int x = 0; x < kPer; ++x) {
+                const int e = threadIdx.x + x * kDecThreads;
+                if (e < G * D) o[x] = fmaf(sm.weight[i * G + e / D], __ldcg(part + e), o[x]);
+            }
         }
-        out[x] = __float2bfloat16_rn(o / total);
+    }
+    for (int d = G; d < 32; d <<= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
+    if (lane < G) sm.l[threadIdx.x >> 5][lane] = total;
+    __syncthreads();
+    __nv_bfloat16 *out = p.out + (static_cast<int64_t>(b) * p.Hq + hk * G) * D;
+#pragma unroll
+    for (int x = 0; x < kPer; ++x) {
+        const int e = threadIdx.x + x * kDecThreads;
+        if (e < G * D) {
+            float sum = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kDecWarps; ++w) sum += sm.l[w][e / D];
+            out[e] = __float2bfloat16_rn(o[x] / sum);
+        }
     }
 }
 
@@ -516,52 +578,67 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm)
         before += all;
     }
     __syncthreads();
-    int b = sm.b;
-    int64_t s = sm.start;   // where segment (b, hk) starts
-    Span sp = span_of(p, b);
-    int hk = static_cast<int>((lo - s) / (sp.pages + kSegmentCost));
-    s += static_cast<int64_t>(hk) * (sp.pages + kSegmentCost);
+    // The place on the line: segment (b, hk), which starts at sm.start.  Kept in
+    // shared memory, so that it holds no registers while a segment runs.
+    if (threadIdx.x == 0) {
+        const Span sp = span_of(p, sm.b);
+        const int hk = static_cast<int>((lo - sm.start) / (sp.pages + kSegmentCost));
+        sm.start += static_cast<int64_t>(hk) * (sp.pages + kSegmentCost);
+        sm.hk = hk;
+        sm.share = share;
+        sm.line = line;
+    }
+    __syncthreads();
     while (true) {
-        const int a = static_cast<int>(min(max(lo - s, int64_t(0)), static_cast<int64_t>(sp.pages)));
-        const int e = static_cast<int>(min(hi - s, static_cast<int64_t>(sp.pages)));
-        if (sp.pages == 0) {
-            if (s >= lo) {
-                __nv_bfloat16 *out = p.out + (static_cast<int64_t>(b) * p.Hq + hk * p.G) * D;
-                for (int x = threadIdx.x; x < p.G * D; x += kDecThreads)
-                    out[x] = __float2bfloat16_rn(0.0f);
+        const int b = sm.b, hk = sm.hk;
+        const Span sp = span_of(p, b);
+        {
+            const int64_t s = sm.start, share = sm.share, lo = share * blockIdx.x;
+            const int64_t hi = min(lo + share, sm.line);
+            const int a = static_cast<int>(min(max(lo - s, int64_t(0)), static_cast<int64_t>(sp.pages)));
+            const int e = static_cast<int>(min(hi - s, static_cast<int64_t>(sp.pages)));
+            if (sp.pages == 0) {
+                if (s >= lo) {
+                    __nv_bfloat16 *out = p.out + (static_cast<int64_t>(b) * p.Hq + hk * p.G) * D;
+                    for (int x = threadIdx.x; x < p.G * D; x += kDecThreads)
+                        out[x] = __float2bfloat16_rn(0.0f);
+                }
+            } else if (a < e) {
+                run_segment<D>(p, sm, ring, b, hk, sp, a, e, a == 0 && e == sp.pages, s >= lo);
             }
-        } else if (a < e) {
-            const bool whole = a == 0 && e == sp.pages;
-            run_segment<D>(p, sm, ring, b, hk, sp, a, e, whole, s >= lo);
-            if (!whole) {
-                const int f = static_cast<int>(s / share);
-                const int last = static_cast<int>((s + sp.pages - 1) / share);
+        }
+        const int64_t s = sm.start, share = sm.share, lo = share * blockIdx.x;
+        const int64_t hi = min(lo + share, sm.line);
+        const bool some = sp.pages > 0 && max(lo - s, int64_t(0)) < min(hi - s, static_cast<int64_t>(sp.pages));
+        if (some && (s < lo || s + sp.pages > hi)) {   // a part: the last of its CTAs joins them
+            const int f = static_cast<int>(s / share);
+            const int last = static_cast<int>((s + sp.pages - 1) / share);
+            __threadfence();
+            __syncthreads();
+            if (threadIdx.x == 0) {
+                sm.last = atomic_add_acq_rel_gpu(p.counters + f, 1) == last - f;
+                if (sm.last) p.counters[f] = 0;
+            }
+            __syncthreads();
+            if (sm.last) {
                 __threadfence();
-                __syncthreads();
-                if (threadIdx.x == 0) {
-                    sm.last = atomic_add_acq_rel_gpu(p.counters + f, 1) == last - f;
-                    if (sm.last) p.counters[f] = 0;
-                }
-                __syncthreads();
-                if (sm.last) {
-                    __threadfence();
-                    join_partials<D>(p, b, hk, f, last);
-                }
+                join_partials<D>(p, sm, b, hk, f, last);
             }
         }
-        s += sp.pages + kSegmentCost;
-        if (s >= hi) break;
-        if (++hk == p.Hkv) {
-            hk = 0;
-            if (++b == p.B) break;
-            sp = span_of(p, b);
+        const int64_t next = s + sp.pages + kSegmentCost;
+        if (next >= hi) break;
+        __syncthreads();   // all have read the old place
+        if (threadIdx.x == 0) {
+            sm.start = next;
+            sm.hk = hk + 1 == p.Hkv ? 0 : hk + 1;
+            sm.b = hk + 1 == p.Hkv ? b + 1 : b;
         }
+        __syncthreads();
     }
     // After a wait that ran out, copies may still be on their way here.
-    if (ring.dead)
-        for (; ring.taken != ring.started; ++ring.taken)
-            mbar_wait_bounded(&sm.full[threadIdx.x >> 5][ring.taken % kStages],
-                              (ring.taken / kStages) & 1, kWaitLimitNs);
+    for (; ring.behind > 0; --ring.behind, ++ring.taken)
+        mbar_wait_bounded(&sm.full[threadIdx.x >> 5][ring.taken % kStages],
+                          (ring.taken / kStages) & 1, kWaitLimitNs);
 }
 
 // Lets the kernel have its shared memory, once for each device.

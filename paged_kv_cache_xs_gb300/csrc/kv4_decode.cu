@@ -36,11 +36,12 @@
 // and head ("segment") with kSegmentCost more for its start and end.  The line
 // is cut into equal shares, one for each CTA, whatever the lengths are: CTA i
 // finds its place from the lengths themselves, so the host needs to know none
-// of them and a captured call follows them.  A segment that lies within a
-// share is written at once.  One that is cut leaves fp32 partials in the
-// workspace, at most two for each CTA whatever the batch, and the CTA that
-// finishes it last joins them in order: the result does not depend on which
-// that is.
+// of them and a captured call follows them.  Where the segments are few
+// (kFewSegments), each is cut into equal pieces of its own instead, one for a
+// CTA, so that no CTA does two in a row.  A segment that one CTA does is
+// written at once.  One that is cut leaves fp32 partials in the workspace, at
+// most two for each CTA whatever the batch, and the CTA that finishes it last
+// joins them in order: the result does not depend on which that is.
 #include <atomic>
 
 #include <cuda_fp16.h>
@@ -54,8 +55,9 @@ constexpr int kDecWarps = 4;
 constexpr int kDecThreads = kDecWarps * 32;
 constexpr int kDecCtasPerSm = 4;
 constexpr int kMaxCtas = 1024;     // the workspace holds partials for so many
-constexpr int kSegmentCost = 4;    // pages
+constexpr int kSegmentCost = 16;   // pages
 constexpr int kMinShare = 16;      // pages
+constexpr int kFewSegments = 8;    // at least so many CTAs for each segment
 constexpr int kStages = 4;         // pages of a warp's ring
 constexpr uint64_t kWaitLimitNs = 4000000000ull;
 
@@ -88,13 +90,13 @@ __device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
     return r;
 }
 
-// d = A B (+ d) with rows 8..15 of A zero: d[2] and d[3] stay 0.
+// d = A B + c, then d = A B + d, with rows 8..15 of A zero.
 __device__ __forceinline__ void mma_f16_first(float *d, uint32_t a0, uint32_t a2, uint32_t b0,
-                                              uint32_t b1) {
+                                              uint32_t b1, const float *c) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%5}, "
-        "{%7,%8}, {%9,%9,%9,%9};"
+        "{%7,%8}, {%9,%10,%11,%12};"
         : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-        : "r"(a0), "r"(0), "r"(a2), "r"(b0), "r"(b1), "f"(0.0f));
+        : "r"(a0), "r"(0), "r"(a2), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
 }
 __device__ __forceinline__ void mma_f16(float *d, uint32_t a0, uint32_t a2, uint32_t b0,
                                         uint32_t b1) {
@@ -117,7 +119,9 @@ __device__ __forceinline__ uint32_t codes_f16(uint32_t w, int j) {
 }
 // The same codes as bf16 n - 8: 0x4300 | n is 128 + n, and the difference is exact.
 __device__ __forceinline__ uint32_t codes_bf16(uint32_t w, int j) {
-    const uint32_t x = ((w >> (4 * j)) & 0x000f000fu) | 0x43004300u, off = 0x43084308u;
+    uint32_t x;
+    const uint32_t off = 0x43084308u;
+    asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(x) : "r"(w >> (4 * j)), "r"(0x000f000fu), "r"(0x43004300u));
     const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&x),
                                      *reinterpret_cast<const __nv_bfloat162 *>(&off));
     return *reinterpret_cast<const uint32_t *>(&r);
@@ -150,7 +154,7 @@ struct Kv4DecodeParams {
     int64_t num_blocks;
     float scale_log2;
     int *counters;      // [gridDim.x]: arrivals at the segment that CTA i begins and does not end
-    float *partials;    // [gridDim.x][2][G (D + 2)]: o, then m, then l
+    float *partials;    // [gridDim.x][2] of partial_floats(G, D)
     int *err_flag;
 };
 
@@ -172,15 +176,23 @@ __device__ __forceinline__ Span span_of(const Kv4DecodeParams &p, int b) {
     return s;
 }
 
+// Floats of one CTA's partial: o [G][D], then m [G] and l [G]; whole 16 bytes.
+__host__ __device__ constexpr int64_t partial_floats(int G, int D) {
+    return (static_cast<int64_t>(G) * (D + 2) + 3) / 4 * 4;
+}
+
 template <int D> struct alignas(16) DecodeSmem {
     uint8_t ring[kDecWarps][kStages][2][kv4_page_bytes(D)];  // K page, V page
     uint64_t full[kDecWarps][kStages];
-    float o[kDecWarps][8][D];
+    uint4 q[D / 32][32];                // first operand of the logits: [group][lane]
+    float o[kDecWarps][8][D + 4];       // a warp's values; padded, for the banks
     float m[kDecWarps][8], l[kDecWarps][8];
     float weight[kDecThreads];
     int64_t scan[kDecWarps];
-    int64_t start, share, line;
-    int b, hk, last;
+    // The CTA's place: segment (b, hk), pages [a, e) of it, shared by the CTAs
+    // f .. last.  Here so that it holds no registers while a segment runs.
+    int b, hk, a, e, f, last, joins;
+    int64_t start, share, line;         // on a line: where the segment starts, ...
 };
 
 // Inclusive sum over the CTA's threads; *total gets the sum of all.
@@ -221,7 +233,7 @@ __device__ __forceinline__ void start_copy(uint32_t dst, const uint8_t *k, int b
 }
 
 // Waits for a ring place with a limit, all lanes alike: false if it ran out.
-__device__ __noinline__ bool warp_waits(uint64_t *bar, uint32_t parity) {
+__device__ __forceinline__ bool warp_waits(uint64_t *bar, uint32_t parity) {
     return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, kWaitLimitNs));
 }
 
@@ -279,7 +291,6 @@ __device__ __forceinline__ void run_segment(const Kv4DecodeParams &p, DecodeSmem
 
     // q as the first operand: row g is head g (heads past G are zero); words
     // j = 0..3 of group c hold dims 32 c + 8 t + j and + j + 4.
-    uint32_t qf[NG][4];
     float cinit[NG], to_log2;
     {
         const bool head = g < p.G;
@@ -304,19 +315,29 @@ __device__ __forceinline__ void run_segment(const Kv4DecodeParams &p, DecodeSmem
 #pragma unroll
         for (int c = 0; c < NG; ++c) {
             float s = 0.0f;
+            uint32_t qf[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const float d = j & 1 ? 0.0625f : 1.0f;
                 const __half2 h = __floats2half2_rn(f[c][j] * u0 * u1 * d, f[c][j + 4] * u0 * u1 * d);
-                qf[c][j] = *reinterpret_cast<const uint32_t *>(&h);
+                qf[j] = *reinterpret_cast<const uint32_t *>(&h);
                 const float2 back = __half22float2(h);
                 s += (back.x + back.y) * (j & 1 ? 16.0f : 1.0f);
             }
             s += __shfl_xor_sync(0xffffffffu, s, 1);
             s += __shfl_xor_sync(0xffffffffu, s, 2);
             cinit[c] = s * -0x1p-21f;
+            if (warp == 0) sm.q[c][lane] = make_uint4(qf[0], qf[1], qf[2], qf[3]);
         }
     }
+    __syncthreads();
+    const uint32_t q0 = smem_addr(&sm.q[0][lane]);
+
+    // Four registers of zeros that the compiler takes for variables: it would
+    // set constants anew for every product.
+    float zero[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) asm volatile("mov.f32 %0, 0f00000000;" : "=f"(zero[k]));
 
     float m = 0.0f, l = 0.0f;   // head g: reference, and this lane's share of the sum
     bool fresh = true;
@@ -328,6 +349,7 @@ __device__ __forceinline__ void run_segment(const Kv4DecodeParams &p, DecodeSmem
 #pragma unroll
             for (int k = 0; k < 4; ++k) acc[c][jj][k] = 0.0f;
 
+#pragma unroll 1
     for (int k = 0; k < mine && !ring.dead; ++k) {
         const int tok0 = (sp.page0 + a + warp + k * kDecWarps) * 16;
         const uint32_t st = (base + k) % kStages, parity = ((base + k) / kStages) & 1;
@@ -340,18 +362,23 @@ __device__ __forceinline__ void run_segment(const Kv4DecodeParams &p, DecodeSmem
         }
         const uint32_t kp = ring0 + st * (2 * kv4_page_bytes(D)), vp = kp + kv4_page_bytes(D);
         F2 x[2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};  // keys 2 t, 2 t + 1, and 8 more
+        uint32_t kw[2][NG], ks[2][NG];  // rows g, g + 8; scales of rows 2 t, 2 t + 1, and 8 more
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-            uint32_t kw[NG], ks[NG];  // row g + 8 u; scales of rows 2 t + 8 u, 2 t + 1 + 8 u
-            load_words<NG>(kw, kp + (g + 8 * u) * (D / 2) + t * (4 * NG));
-            load_words<NG>(ks, kp + 8 * D + (t + 4 * u) * (4 * NG));
+            load_words<NG>(kw[u], kp + (g + 8 * u) * (D / 2) + t * (4 * NG));
+            load_words<NG>(ks[u], kp + 8 * D + (t + 4 * u) * (4 * NG));
+        }
 #pragma unroll
-            for (int c = 0; c < NG; ++c) {
-                const uint32_t w = kw[c];
+        for (int c = 0; c < NG; ++c) {
+            uint32_t qf[4];
+            load_words<4>(qf, q0 + c * 512);
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const uint32_t w = kw[u][c];
                 float s[4];
-                mma_f16_first(s, qf[c][0], qf[c][1], codes_f16(w, 0), codes_f16(w, 1));
-                mma_f16(s, qf[c][2], qf[c][3], codes_f16(w, 2), codes_f16(w, 3));
-                const uint32_t a0 = ks[c / 2], a1 = ks[NG / 2 + c / 2];
+                mma_f16_first(s, qf[0], qf[1], codes_f16(w, 0), codes_f16(w, 1), zero);
+                mma_f16(s, qf[2], qf[3], codes_f16(w, 2), codes_f16(w, 3));
+                const uint32_t a0 = ks[u][c / 2], a1 = ks[u][NG / 2 + c / 2];
                 const F2 z = c & 1 ? F2{bf_hi(a0), bf_hi(a1)} : F2{bf_lo(a0), bf_lo(a1)};
                 x[u] = fma2(z, add2(F2{s[0], s[1]}, F2{cinit[c], cinit[c]}), x[u]);
             }
@@ -434,7 +461,6 @@ __device__ __forceinline__ void run_segment(const Kv4DecodeParams &p, DecodeSmem
     // as l = 0 under the lowest reference.
     l += __shfl_xor_sync(0xffffffffu, l, 1);
     l += __shfl_xor_sync(0xffffffffu, l, 2);
-    __syncthreads();   // the last segment's have been read
     if (t == 0) {
         sm.m[warp][g] = fresh ? -3.0e38f : m;
         sm.l[warp][g] = l;
@@ -444,189 +470,224 @@ __device__ __forceinline__ void run_segment(const Kv4DecodeParams &p, DecodeSmem
 #pragma unroll
         for (int jj = 0; jj < 2; ++jj)
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                sm.o[warp][2 * t + k][32 * c + 4 * g + 2 * jj] = acc[c][jj][k];
-                sm.o[warp][2 * t + k][32 * c + 4 * g + 2 * jj + 1] = acc[c][jj][k + 2];
-            }
+            for (int k = 0; k < 2; ++k)
+                *reinterpret_cast<float2 *>(&sm.o[warp][2 * t + k][32 * c + 4 * g + 2 * jj]) =
+                    make_float2(acc[c][jj][k], acc[c][jj][k + 2]);
     __syncthreads();
-    const int64_t slot_floats = static_cast<int64_t>(p.G) * (D + 2);
-    float *part = p.partials + (2 * static_cast<int64_t>(blockIdx.x) + slot) * slot_floats;
-    __nv_bfloat16 *out = p.out + (static_cast<int64_t>(b) * p.Hq + h0) * D;
-    for (int x = threadIdx.x; x < p.G * D; x += kDecThreads) {
-        const int h = x / D, d = x % D;
-        float top = -3.0e38f;
+    const bool sinks = whole && p.sinks;
+    float *part = p.partials + (2 * static_cast<int64_t>(blockIdx.x) + slot) * partial_floats(p.G, D);
+    if (threadIdx.x < kDecWarps * 8) {      // (warp, head): its weight, over the sum if whole
+        const int w = threadIdx.x >> 3, h = threadIdx.x & 7;
+        float top = sm.m[0][h];
 #pragma unroll
-        for (int w = 0; w < kDecWarps; ++w) top = fmaxf(top, sm.m[w][h]);
+        for (int k = 1; k < kDecWarps; ++k) top = fmaxf(top, sm.m[k][h]);
         float sink = 0.0f;
-        const bool sinks = whole && p.sinks;
-        if (sinks) {
+        if (sinks && h < p.G) {
             sink = __bfloat162float(p.sinks[h0 + h]) * 1.4426950408889634f;
             top = fmaxf(top, sink);
         }
-        float o = 0.0f, total = sinks ? fast_exp2(sink - top) : 0.0f;
+        float total = sinks ? fast_exp2(sink - top) : 0.0f;
+#pragma unroll
+        for (int k = 0; k < kDecWarps; ++k) total = fmaf(fast_exp2(sm.m[k][h] - top), sm.l[k][h], total);
+        const float f = fast_exp2(sm.m[w][h] - top);
+        sm.weight[threadIdx.x] = whole ? f / total : f;
+        if (!whole && w == 0 && h < p.G) {
+            __stcg(part + p.G * D + h, top);
+            __stcg(part + p.G * (D + 1) + h, total);
+        }
+    }
+    __syncthreads();
+    __nv_bfloat16 *out = p.out + (static_cast<int64_t>(b) * p.Hq + h0) * D;
+    for (int x = 4 * threadIdx.x; x < p.G * D; x += 4 * kDecThreads) {
+        const int h = x / D, d = x % D;
+        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
         for (int w = 0; w < kDecWarps; ++w) {
-            const float f = fast_exp2(sm.m[w][h] - top);
-            o = fmaf(f, sm.o[w][h][d], o);
-            total = fmaf(f, sm.l[w][h], total);
+            const float f = sm.weight[8 * w + h];
+            const float4 v = *reinterpret_cast<const float4 *>(&sm.o[w][h][d]);
+            o.x = fmaf(f, v.x, o.x), o.y = fmaf(f, v.y, o.y);
+            o.z = fmaf(f, v.z, o.z), o.w = fmaf(f, v.w, o.w);
         }
-        if (whole) {
-            out[x] = __float2bfloat16_rn(o / total);
-        } else {
-            __stcg(part + x, o);
-            if (d == 0) {
-                __stcg(part + p.G * D + h, top);
-                __stcg(part + p.G * (D + 1) + h, total);
-            }
-        }
+        if (whole)
+            *reinterpret_cast<uint2 *>(out + x) =
+                make_uint2(pack_bf16(F2{o.x, o.y}), pack_bf16(F2{o.z, o.w}));
+        else
+            *reinterpret_cast<float4 *>(part + x) = o;
     }
 }
 
 // The partials of a segment that CTAs f .. last share, joined in order: CTA f
-// left its second, the others their first.  Weights first, by one thread for
-// each partial and head, then the values.
+// left its second, the others their first.  As many as the rings hold come at
+// once (an access to another CTA's fresh results takes about 1 us, so one
+// after the other is what a join must not do); each thread then follows its
+// own four values through them.
 template <int D>
-__device__ __forceinline__ void join_partials(const Kv4DecodeParams &p, DecodeSmem<D> &sm, int b,
-                                              int hk, int f, int last) {
-    const int G = p.G, per = kDecThreads / G;   // G divides 32
-    const int64_t slot_floats = static_cast<int64_t>(G) * (D + 2);
-    auto part_of = [&](int i) {
-        return p.partials + (2 * static_cast<int64_t>(i) + (i == f)) * slot_floats;
-    };
-    const int h = threadIdx.x % G, k = threadIdx.x / G, lane = threadIdx.x & 31;
-    float sink = 0.0f, top = -3.0e38f;
-    if (p.sinks) top = sink = __bfloat162float(p.sinks[hk * G + h]) * 1.4426950408889634f;
-    for (int i = f + k; i <= last; i += per) top = fmaxf(top, __ldcg(part_of(i) + G * D + h));
-    for (int d = G; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-    if (lane < G) sm.m[threadIdx.x >> 5][lane] = top;
-    __syncthreads();
+__device__ __noinline__ void join_partials(const Kv4DecodeParams &p, DecodeSmem<D> &sm, int b,
+                                           int hk, int f, int last) {
+    const int G = p.G, floats = static_cast<int>(partial_floats(G, D)), chunks = floats / 4;
+    float *buf = reinterpret_cast<float *>(sm.ring);
+    const int room = static_cast<int>(sizeof(sm.ring) / (4 * floats));
+    constexpr int kPer = (8 * D / 4 + kDecThreads - 1) / kDecThreads;
+    float4 o[kPer];
+    float top[kPer], total[kPer];
 #pragma unroll
-    for (int w = 0; w < kDecWarps; ++w) top = fmaxf(top, sm.m[w][h]);
-    float total = p.sinks && k == 0 ? fast_exp2(sink - top) : 0.0f;
-    constexpr int kPer = (8 * D) / kDecThreads;     // values of a thread, at most
-    float o[kPer];
-#pragma unroll
-    for (int x = 0; x < kPer; ++x) o[x] = 0.0f;
-    for (int base = f; base <= last; base += per) {
-        float w = 0.0f;
-        if (base + k <= last) {
-            const float *part = part_of(base + k);
-            w = fast_exp2(__ldcg(part + G * D + h) - top);
-            total = fmaf(w, __ldcg(part + G * (D + 1) + h), total);
-        }
-        __syncthreads();
-        sm.weight[threadIdx.x] = w;                 // [k][h]
-        __syncthreads();
-        const int n = min(last - base + 1, per);
-#pragma unroll 4
-        for (int i = 0; i < n; ++i) {
-            const float *part = part_of(base + i);
-#pragma unroll
-            for (int x = 0; x < kPer; ++x) {
-                const int e = threadIdx.x + x * kDecThreads;
-                if (e < G * D) o[x] = fmaf(sm.weight[i * G + e / D], __ldcg(part + e), o[x]);
-            }
+    for (int x = 0; x < kPer; ++x) {
+        const int e = threadIdx.x + x * kDecThreads, h = 4 * e / D;
+        o[x] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        top[x] = -3.0e38f, total[x] = 0.0f;
+        if (p.sinks && h < G) {
+            top[x] = __bfloat162float(p.sinks[hk * G + h]) * 1.4426950408889634f;
+            total[x] = 1.0f;
         }
     }
-    for (int d = G; d < 32; d <<= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
-    if (lane < G) sm.l[threadIdx.x >> 5][lane] = total;
+    for (int base = f; base <= last; base += room) {
+        const int n = min(room, last - base + 1);
+        for (int c = threadIdx.x; c < n * chunks; c += kDecThreads) {
+            const int i = c / chunks, at = c - i * chunks;
+            const float *src = p.partials + (2 * static_cast<int64_t>(base + i) + (base + i == f)) * floats;
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(buf + 4 * c)),
+                         "l"(src + 4 * at)
+                         : "memory");
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        __syncthreads();
+#pragma unroll
+        for (int x = 0; x < kPer; ++x) {
+            const int e = threadIdx.x + x * kDecThreads, h = 4 * e / D;
+            if (h >= G) continue;
+            float to = top[x];
+            for (int i = 0; i < n; ++i) to = fmaxf(to, buf[i * floats + G * D + h]);
+            const float w0 = fast_exp2(top[x] - to);
+            top[x] = to;
+            total[x] *= w0;
+            o[x].x *= w0, o[x].y *= w0, o[x].z *= w0, o[x].w *= w0;
+#pragma unroll 4
+            for (int i = 0; i < n; ++i) {
+                const float w = fast_exp2(buf[i * floats + G * D + h] - to);
+                const float4 v = *reinterpret_cast<const float4 *>(buf + i * floats + 4 * e);
+                total[x] = fmaf(w, buf[i * floats + G * (D + 1) + h], total[x]);
+                o[x].x = fmaf(w, v.x, o[x].x), o[x].y = fmaf(w, v.y, o[x].y);
+                o[x].z = fmaf(w, v.z, o[x].z), o[x].w = fmaf(w, v.w, o[x].w);
+            }
+        }
+        __syncthreads();
+    }
+    // The rings go back to the bulk copies.
+    fence_proxy_async_shared();
     __syncthreads();
     __nv_bfloat16 *out = p.out + (static_cast<int64_t>(b) * p.Hq + hk * G) * D;
 #pragma unroll
     for (int x = 0; x < kPer; ++x) {
         const int e = threadIdx.x + x * kDecThreads;
-        if (e < G * D) {
-            float sum = 0.0f;
-#pragma unroll
-            for (int w = 0; w < kDecWarps; ++w) sum += sm.l[w][e / D];
-            out[e] = __float2bfloat16_rn(o[x] / sum);
-        }
+        if (4 * e / D < G)
+            reinterpret_cast<uint2 *>(out)[e] =
+                make_uint2(pack_bf16(F2{o[x].x / total[x], o[x].y / total[x]}),
+                           pack_bf16(F2{o[x].z / total[x], o[x].w / total[x]}));
     }
 }
 
 template <int D>
 __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm)
-    kv4_decode_kernel(const Kv4DecodeParams p) {
+    kv4_decode_kernel(const __grid_constant__ Kv4DecodeParams p) {
     extern __shared__ __align__(16) uint8_t smem_raw[];
     DecodeSmem<D> &sm = *reinterpret_cast<DecodeSmem<D> *>(smem_raw);
     if (threadIdx.x < kDecWarps * kStages) mbar_init(&sm.full[0][0] + threadIdx.x, 1);
     mbar_fence_init();
     __syncthreads();
     RingState ring;
-    // The line's length, this CTA's share of it, and the sequence it begins in.
-    int64_t line = 0;
+    // This CTA's place.  A sequence has so many units for each KV head: pieces
+    // (one of them is this CTA's), or the length of its segments on the line.
+    // The lengths of the first kDecThreads sequences stay in registers.
+    const int64_t segments = static_cast<int64_t>(p.B) * p.Hkv;
+    const bool few = segments * kFewSegments <= gridDim.x;
+    int pages0 = 0;
+    int64_t total = 0;
     for (int base = 0; base < p.B; base += kDecThreads) {
         const int b = base + threadIdx.x;
+        const int pages = b < p.B ? span_of(p, b).pages : 0;
+        if (base == 0) pages0 = pages;
         int64_t all;
-        cta_scan(b < p.B ? span_of(p, b).pages + kSegmentCost : 0, &all, sm);
-        line += all;
+        cta_scan(pages, &all, sm);
+        total += all;
     }
-    line *= p.Hkv;
-    const int64_t share = max((line + gridDim.x - 1) / gridDim.x, static_cast<int64_t>(kMinShare));
-    const int64_t lo = share * blockIdx.x, hi = min(lo + share, line);
-    if (lo >= hi) return;
+    int64_t share, line = (total + static_cast<int64_t>(p.B) * kSegmentCost) * p.Hkv;
+    if (few) {
+        const int64_t ctas = gridDim.x - segments;
+        share = max((total * p.Hkv + ctas - 1) / ctas, static_cast<int64_t>(kMinShare));
+    } else {
+        share = max((line + gridDim.x - 1) / gridDim.x, static_cast<int64_t>(kMinShare));
+    }
+    const int64_t target = few ? blockIdx.x : share * blockIdx.x;
+    if (threadIdx.x == 0) sm.b = -1;
     int64_t before = 0;
-    for (int base = 0; base < p.B && before <= lo; base += kDecThreads) {
+    for (int base = 0; base < p.B && before * p.Hkv <= target; base += kDecThreads) {
         const int b = base + threadIdx.x;
-        const int64_t v = b < p.B ? static_cast<int64_t>(span_of(p, b).pages + kSegmentCost) * p.Hkv : 0;
+        const int pages = base ? (b < p.B ? span_of(p, b).pages : 0) : pages0;
+        const int64_t units = b >= p.B ? 0
+                              : few    ? max((pages + share - 1) / share, int64_t(1))
+                                       : pages + kSegmentCost;
         int64_t all;
-        const int64_t end = before + cta_scan(v, &all, sm);
-        if (lo >= end - v && lo < end) {
+        const int64_t end = (before + cta_scan(units, &all, sm)) * p.Hkv;
+        const int64_t s = end - units * p.Hkv;
+        if (target >= s && target < end) {
+            const int hk = static_cast<int>((target - s) / units);
             sm.b = b;
-            sm.start = end - v;
+            sm.hk = hk;
+            sm.start = s + hk * units;
+            sm.share = share;
+            sm.line = line;
+            if (few) {
+                const int j = static_cast<int>(target - sm.start), n = static_cast<int>(units);
+                const int piece = (pages + n - 1) / n;
+                sm.a = j * piece;
+                sm.e = min((j + 1) * piece, pages);
+                sm.f = blockIdx.x - j;
+                sm.last = sm.f + n - 1;
+            }
         }
         before += all;
     }
     __syncthreads();
-    // The place on the line: segment (b, hk), which starts at sm.start.  Kept in
-    // shared memory, so that it holds no registers while a segment runs.
-    if (threadIdx.x == 0) {
-        const Span sp = span_of(p, sm.b);
-        const int hk = static_cast<int>((lo - sm.start) / (sp.pages + kSegmentCost));
-        sm.start += static_cast<int64_t>(hk) * (sp.pages + kSegmentCost);
-        sm.hk = hk;
-        sm.share = share;
-        sm.line = line;
-    }
-    __syncthreads();
+    if (sm.b < 0) return;
     while (true) {
-        const int b = sm.b, hk = sm.hk;
-        const Span sp = span_of(p, b);
         {
-            const int64_t s = sm.start, share = sm.share, lo = share * blockIdx.x;
-            const int64_t hi = min(lo + share, sm.line);
-            const int a = static_cast<int>(min(max(lo - s, int64_t(0)), static_cast<int64_t>(sp.pages)));
-            const int e = static_cast<int>(min(hi - s, static_cast<int64_t>(sp.pages)));
+            const int b = sm.b, hk = sm.hk;
+            const Span sp = span_of(p, b);
+            if (!few && threadIdx.x == 0) {
+                const int64_t s = sm.start, share = sm.share, lo = share * blockIdx.x;
+                const int64_t hi = min(lo + share, sm.line);
+                sm.a = static_cast<int>(min(max(lo - s, int64_t(0)), static_cast<int64_t>(sp.pages)));
+                sm.e = static_cast<int>(min(hi - s, static_cast<int64_t>(sp.pages)));
+                sm.f = static_cast<int>(s / share);
+                sm.last = static_cast<int>((s + sp.pages - 1) / share);
+            }
+            __syncthreads();
+            const int a = sm.a, e = sm.e;
             if (sp.pages == 0) {
-                if (s >= lo) {
+                if (few || sm.start >= sm.share * blockIdx.x) {
                     __nv_bfloat16 *out = p.out + (static_cast<int64_t>(b) * p.Hq + hk * p.G) * D;
                     for (int x = threadIdx.x; x < p.G * D; x += kDecThreads)
                         out[x] = __float2bfloat16_rn(0.0f);
                 }
             } else if (a < e) {
-                run_segment<D>(p, sm, ring, b, hk, sp, a, e, a == 0 && e == sp.pages, s >= lo);
+                run_segment<D>(p, sm, ring, b, hk, sp, a, e, a == 0 && e == sp.pages, a == 0);
             }
         }
-        const int64_t s = sm.start, share = sm.share, lo = share * blockIdx.x;
-        const int64_t hi = min(lo + share, sm.line);
-        const bool some = sp.pages > 0 && max(lo - s, int64_t(0)) < min(hi - s, static_cast<int64_t>(sp.pages));
-        if (some && (s < lo || s + sp.pages > hi)) {   // a part: the last of its CTAs joins them
-            const int f = static_cast<int>(s / share);
-            const int last = static_cast<int>((s + sp.pages - 1) / share);
-            __threadfence();
+        if (sm.a < sm.e && sm.f != sm.last) {   // a part: the last of its CTAs joins them
+            // The barrier and the atomic's release carry all threads' partials,
+            // its acquire and the next barrier the other CTAs'.
             __syncthreads();
             if (threadIdx.x == 0) {
-                sm.last = atomic_add_acq_rel_gpu(p.counters + f, 1) == last - f;
-                if (sm.last) p.counters[f] = 0;
+                sm.joins = atomic_add_acq_rel_gpu(p.counters + sm.f, 1) == sm.last - sm.f;
+                if (sm.joins) p.counters[sm.f] = 0;
             }
             __syncthreads();
-            if (sm.last) {
-                __threadfence();
-                join_partials<D>(p, sm, b, hk, f, last);
-            }
+            if (sm.joins) join_partials<D>(p, sm, sm.b, sm.hk, sm.f, sm.last);
         }
-        const int64_t next = s + sp.pages + kSegmentCost;
-        if (next >= hi) break;
+        if (few) break;
+        const int b = sm.b, hk = sm.hk;
+        const int64_t next = sm.start + span_of(p, b).pages + kSegmentCost;
+        if (next >= min(sm.share * (blockIdx.x + 1), sm.line)) break;
         __syncthreads();   // all have read the old place
         if (threadIdx.x == 0) {
             sm.start = next;
@@ -663,7 +724,7 @@ XS_DEFINE_BOUNDS_COUNTER(bounds_failures_kv4_decode)
 extern "C" size_t xs_kv4_decode_workspace_bytes(int B, int Hq, int Hkv, int D) {
     if (B <= 0 || Hq <= 0 || Hkv <= 0 || D <= 0) return 0;
     const size_t counters = xs::kMaxCtas * sizeof(int);
-    return counters + static_cast<size_t>(xs::kMaxCtas) * 2 * (Hq / Hkv) * (D + 2) * sizeof(float);
+    return counters + static_cast<size_t>(xs::kMaxCtas) * 2 * xs::partial_floats(Hq / Hkv, D) * sizeof(float);
 }
 
 extern "C" int xs_kv4_decode(void *out, const void *q, const void *k_cache, const void *v_cache,
@@ -707,7 +768,7 @@ extern "C" int xs_kv4_decode(void *out, const void *q, const void *k_cache, cons
         return XS_EDEVICE;
     // The line is at most so long, and no CTA takes less than kMinShare of it.
     const int64_t most = static_cast<int64_t>(B) * Hkv * (max_blocks_per_seq + xs::kSegmentCost);
-    const int64_t want = (most + xs::kMinShare - 1) / xs::kMinShare;
+    const int64_t want = static_cast<int64_t>(B) * Hkv + (most + xs::kMinShare - 1) / xs::kMinShare;
     const int fill = sms * xs::kDecCtasPerSm < xs::kMaxCtas ? sms * xs::kDecCtasPerSm : xs::kMaxCtas;
     const int grid = static_cast<int>(want < fill ? want : fill);
     const int rc = D == 128 ? xs::configure<128>(dev) : xs::configure<64>(dev);

@@ -10,6 +10,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -19,6 +20,10 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB_NAME = "libxs_paged.so"
 LIB_PATH = os.path.join(BUILD_DIR, LIB_NAME)
+# Python binding (checks tensors, calls the library by entry address): host
+# C++ against PyTorch's headers, one for both libraries.
+BIND_PATH = os.path.join(BUILD_DIR, "xs_bind.so")
+BIND_SOURCE = "bind.cpp"
 # The debug library: the same sources compiled with -DXS_DEBUG_BOUNDS, so every
 # computed global-memory index is checked in the kernels (XS_FLAG_BOUNDS).
 DEBUG_BUILD_DIR = os.path.join(PKG, "_build_debug")
@@ -42,11 +47,30 @@ def _deps() -> list[str]:
 
 
 def up_to_date(debug_bounds: bool = False) -> bool:
-    lib = DEBUG_LIB_PATH if debug_bounds else LIB_PATH
-    if not os.path.exists(lib):
+    libs = [DEBUG_LIB_PATH] if debug_bounds else [LIB_PATH, BIND_PATH]
+    if not all(os.path.exists(lib) for lib in libs):
         return False
-    t = os.path.getmtime(lib)
+    t = min(os.path.getmtime(lib) for lib in libs)
     return all(os.path.getmtime(f) <= t for f in _deps())
+
+
+def build_bind() -> str:
+    """Build xs_bind.so with the host compiler."""
+    import torch
+
+    top = os.path.join(torch.__path__[0], "include")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
+    tmp = BIND_PATH + f".tmp{os.getpid()}"
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-I", INCLUDE,
+           "-I", top, "-I", os.path.join(top, "torch", "csrc", "api", "include"), "-I", cuda,
+           "-I", sysconfig.get_paths()["include"], os.path.join(CSRC, BIND_SOURCE), "-o", tmp,
+           "-L", os.path.join(torch.__path__[0], "lib"), "-lc10", "-ltorch_cpu", "-lc10_cuda",
+           "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {BIND_SOURCE}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BIND_PATH)
+    return BIND_PATH
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | None = None,
@@ -74,8 +98,11 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
             sys.stderr.write(r.stderr)
         return obj
 
-    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        bind = None if debug_bounds else ex.submit(build_bind)
         objs = list(ex.map(compile_one, SOURCES))
+        if bind is not None:
+            bind.result()
     tmp = lib_path + f".tmp{os.getpid()}"
     cmd = [exe, *ARCH, "-shared", "-cudart", "shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)

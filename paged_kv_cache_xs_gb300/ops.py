@@ -9,6 +9,7 @@ if the shared library is missing or a call fails, an exception is raised.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 import threading
 
@@ -104,6 +105,8 @@ SIGNATURES = {
 
 _lock = threading.Lock()
 _lib = None
+_bound = None        # the xs_bind module
+_entries = {}        # entry point addresses of _lib, by name
 
 
 class XsError(RuntimeError):
@@ -132,6 +135,7 @@ def load(path: str | None = None):
             fn.argtypes = args
         if path is None:
             _lib = lib
+            _entries.clear()
         return lib
 
 
@@ -446,82 +450,43 @@ def xs_paged_prefill(out, part_o, part_m, part_l, q, k_cache, v_cache, block_ids
           dtype_code(q.dtype), _ptr(err_flag), _ptr(work_counters), _stream(stream))
 
 
+# ---------------------------------------------------------------- bound calls
+# The calls below go through xs_bind (csrc/bind.cpp), which checks the tensors
+# (type, shape, layout, device; a refusal is a ValueError) and calls the
+# library's entry point.
+
+def _entry(name: str) -> int:
+    """Address of an entry point of the library in use."""
+    a = _entries.get(name)
+    if a is None:
+        a = _entries[name] = ctypes.cast(getattr(load(), name), ctypes.c_void_p).value
+    return a
+
+
+def _bind():
+    global _bound
+    if _bound is None:
+        p = _build.BIND_PATH
+        if not os.path.exists(p):
+            raise ImportError(f"{p} is missing: build it with paged_kv_cache_xs_gb300.build.build()")
+        spec = importlib.util.spec_from_file_location("xs_bind", p)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        _bound = module
+    return _bound
+
+
+def _handle(stream) -> int | None:
+    """What xs_bind takes for a stream: None is the current one."""
+    return None if stream is None else _stream(stream)
+
+
+def _done(name: str, code: int) -> None:
+    if code != 0:
+        raise XsError(name, code)
+
+
 # ---------------------------------------------------------------- norm + rotation + append
-
-XS_ROPE_INTERLEAVED = 1
-XS_CACHE_KV4 = 2
-
-
-def _refuse(what: str):
-    raise ValueError(what)
-
-
-_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-
-
-def _here(first, *others):
-    """The current stream, after a check that all tensors (None: not given) are
-    on the current CUDA device, where the launch goes."""
-    dev = first.get_device()
-    if dev < 0:
-        _refuse("tensors must be on a CUDA device")
-    if dev != _current_device():
-        _refuse(f"tensors are on cuda:{dev}, the current device is cuda:{_current_device()}")
-    for t in others:
-        if t is not None and t.get_device() != dev:
-            _refuse("tensors are on different devices")
-    return _raw_stream(dev) if _raw_stream else torch.cuda.current_stream().cuda_stream
-
-
-def _rows(x, what: str) -> int:
-    """Token stride of rows [T, H, D] whose heads lie next to one another."""
-    a, b, c = x.stride()
-    T, H, D = x.shape
-    if c != 1 or (b != D and H != 1):
-        _refuse(f"{what}: the heads of a token must be contiguous")
-    return a if T > 1 else H * D
-
-
-def _typed(t, dtype, shape, what: str):
-    if t is not None and (t.dtype != dtype or t.shape != shape):
-        _refuse(f"{what} must be {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
-
-
-def _pools(k_cache, v_cache, dtype, Hkv: int, D: int):
-    """(num_blocks, flags) of a pair of pools for rows of `dtype`: 4-bit pools
-    are uint8 [num_blocks, Hkv, 9 D], others dtype [num_blocks, Hkv, 16, D]."""
-    shape, kind = k_cache.shape, k_cache.dtype
-    if v_cache.dtype != kind or v_cache.shape != shape:
-        _refuse("k_cache and v_cache differ in type or shape")
-    if kind == torch.uint8:
-        if shape[1:] != (Hkv, 9 * D):
-            _refuse(f"4-bit pools must be [num_blocks, {Hkv}, {9 * D}], got {list(shape)}")
-        return shape[0], XS_CACHE_KV4
-    if kind != dtype or shape[1:] != (Hkv, BLOCK_SIZE, D):
-        _refuse(f"pools must be {dtype} [num_blocks, {Hkv}, {BLOCK_SIZE}, {D}], "
-                f"got {kind} {list(shape)}")
-    return shape[0], 0
-
-
-def _norm_rope_args(q_out, q, k, q_weight, k_weight, cos_sin):
-    T, Hq, D = q.shape
-    dt = q.dtype
-    _typed(q_out, dt, (T, Hq, D), "q_out")
-    if k.dtype != dt or k.dim() != 3:
-        _refuse(f"k must be {dt} [{T}, Hkv, {D}], got {k.dtype} {list(k.shape)}")
-    Tk, Hkv, Dk = k.shape
-    if Tk != T or Dk != D:
-        _refuse(f"k must be {dt} [{T}, Hkv, {D}], got {k.dtype} {list(k.shape)}")
-    _typed(q_weight, dt, (D,), "q_weight")
-    _typed(k_weight, dt, (D,), "k_weight")
-    if cos_sin is None:
-        return T, Hq, Hkv, D, 0, 0
-    if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2:
-        _refuse("cos_sin must be float32 [max_pos, rotary_dim]")
-    max_pos, rot = cos_sin.shape
-    return T, Hq, Hkv, D, max_pos, rot
-
 
 def xs_qk_norm_rope(q_out, k_out, q, k, q_weight, k_weight, eps, cos_sin, positions,
                     interleaved=False, err_flag=None, stream=None):
@@ -529,16 +494,9 @@ def xs_qk_norm_rope(q_out, k_out, q, k, q_weight, k_weight, eps, cos_sin, positi
     None for no norm), then the rotation by positions (int32 [T]) with the
     fp32 table cos_sin [max_pos, rotary_dim] (None: no rotation).  q and k may
     be slices of one projection's output; q_out and k_out may be q and k."""
-    T, Hq, Hkv, D, max_pos, rot = _norm_rope_args(q_out, q, k, q_weight, k_weight, cos_sin)
-    _typed(k_out, q.dtype, (T, Hkv, D), "k_out")
-    _typed(positions, torch.int32, (T,), "positions")
-    here = _here(q, k, q_out, k_out, q_weight, k_weight, cos_sin, positions, err_flag)
-    if T == 0:
-        return
-    _call("xs_qk_norm_rope", _ptr(q_out), _ptr(k_out), q.data_ptr(), _rows(q, "q"), k.data_ptr(),
-          _rows(k, "k"), _ptr(q_weight), _ptr(k_weight), float(eps), _ptr(cos_sin), max_pos, rot,
-          _ptr(positions), T, Hq, Hkv, D, XS_ROPE_INTERLEAVED if interleaved else 0,
-          dtype_code(q.dtype), _ptr(err_flag), here if stream is None else _stream(stream))
+    _done("xs_qk_norm_rope", (_bound or _bind()).xs_qk_norm_rope(
+        _entry("xs_qk_norm_rope"), q_out, k_out, q, k, q_weight, k_weight, eps, cos_sin, positions,
+        interleaved, err_flag, _handle(stream)))
 
 
 def xs_qk_norm_rope_append(q_out, q, k, v, q_weight, k_weight, eps, cos_sin, positions, k_cache,
@@ -546,21 +504,9 @@ def xs_qk_norm_rope_append(q_out, q, k, v, q_weight, k_weight, eps, cos_sin, pos
     """xs_qk_norm_rope with the append in it: the k rows, and v [T, Hkv, D] as
     it is, go to slot_mapping (int64 [T], negative: not appended) of the pools
     - of q's dtype, or 4-bit (uint8) ones."""
-    T, Hq, Hkv, D, max_pos, rot = _norm_rope_args(q_out, q, k, q_weight, k_weight, cos_sin)
-    _typed(v, q.dtype, (T, Hkv, D), "v")
-    _typed(positions, torch.int32, (T,), "positions")
-    _typed(slot_mapping, torch.int64, (T,), "slot_mapping")
-    nb, flags = _pools(k_cache, v_cache, q.dtype, Hkv, D)
-    here = _here(q, k, v, q_out, q_weight, k_weight, cos_sin, positions, slot_mapping, k_cache,
-                 v_cache, err_flag)
-    if T == 0:
-        return
-    _call("xs_qk_norm_rope_append", _ptr(q_out), q.data_ptr(), _rows(q, "q"), k.data_ptr(),
-          _rows(k, "k"), v.data_ptr(), _rows(v, "v"), _ptr(q_weight), _ptr(k_weight), float(eps),
-          _ptr(cos_sin), max_pos, rot, _ptr(positions), _ptr(k_cache), _ptr(v_cache),
-          _ptr(slot_mapping), T, Hq, Hkv, D, BLOCK_SIZE, nb,
-          flags | (XS_ROPE_INTERLEAVED if interleaved else 0), dtype_code(q.dtype),
-          _ptr(err_flag), here if stream is None else _stream(stream))
+    _done("xs_qk_norm_rope_append", (_bound or _bind()).xs_qk_norm_rope_append(
+        _entry("xs_qk_norm_rope_append"), q_out, q, k, v, q_weight, k_weight, eps, cos_sin,
+        positions, k_cache, v_cache, slot_mapping, interleaved, err_flag, _handle(stream)))
 
 
 def xs_qk_norm_rope_append_paged(q_out, q, k, v, q_weight, k_weight, eps, cos_sin, k_cache,
@@ -568,27 +514,9 @@ def xs_qk_norm_rope_append_paged(q_out, q, k, v, q_weight, k_weight, eps, cos_si
                                  err_flag=None, stream=None):
     """The decode step's form: row b is sequence b's new token, at position
     context_lens[b] - 1 of its block table (a length <= 0 skips the row)."""
-    B, Hq, Hkv, D, max_pos, rot = _norm_rope_args(q_out, q, k, q_weight, k_weight, cos_sin)
-    _typed(v, q.dtype, (B, Hkv, D), "v")
-    _tables(block_tables, context_lens, B)
-    nb, flags = _pools(k_cache, v_cache, q.dtype, Hkv, D)
-    here = _here(q, k, v, q_out, q_weight, k_weight, cos_sin, k_cache, v_cache, block_tables,
-                 context_lens, err_flag)
-    if B == 0:
-        return
-    _call("xs_qk_norm_rope_append_paged", _ptr(q_out), q.data_ptr(), _rows(q, "q"), k.data_ptr(),
-          _rows(k, "k"), v.data_ptr(), _rows(v, "v"), _ptr(q_weight), _ptr(k_weight), float(eps),
-          _ptr(cos_sin), max_pos, rot, _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
-          block_tables.shape[1], _ptr(context_lens), B, Hq, Hkv, D, BLOCK_SIZE, nb,
-          flags | (XS_ROPE_INTERLEAVED if interleaved else 0), dtype_code(q.dtype),
-          _ptr(err_flag), here if stream is None else _stream(stream))
-
-
-def _tables(block_tables, context_lens, B: int) -> None:
-    if (block_tables.dtype != torch.int32 or block_tables.dim() != 2 or
-            block_tables.shape[0] != B):
-        _refuse(f"block_tables must be int32 [{B}, max_blocks]")
-    _typed(context_lens, torch.int32, (B,), "context_lens")
+    _done("xs_qk_norm_rope_append_paged", (_bound or _bind()).xs_qk_norm_rope_append_paged(
+        _entry("xs_qk_norm_rope_append_paged"), q_out, q, k, v, q_weight, k_weight, eps, cos_sin,
+        k_cache, v_cache, block_tables, context_lens, interleaved, err_flag, _handle(stream)))
 
 
 def rope_table(max_pos: int, rotary_dim: int, theta: float, device) -> torch.Tensor:
@@ -618,59 +546,29 @@ def kv4_pools(num_blocks: int, Hkv: int, D: int, device, layers: int | None = No
             torch.zeros(shape, dtype=torch.uint8, device=device))
 
 
-def _kv4_pools(k_cache, v_cache, Hkv: int, D: int) -> int:
-    if k_cache.dtype != torch.uint8:
-        _refuse("k_cache and v_cache must be 4-bit (uint8) pools")
-    return _pools(k_cache, v_cache, None, Hkv, D)[0]
-
-
 def xs_kv4_append(k_new, v_new, k_cache, v_cache, slot_mapping, err_flag=None, stream=None):
     """xs_kv_append for 4-bit pools; k_new and v_new [T, Hkv, D] may be slices
     of one projection's output."""
-    T, Hkv, D = k_new.shape
-    _typed(v_new, k_new.dtype, (T, Hkv, D), "v_new")
-    _typed(slot_mapping, torch.int64, (T,), "slot_mapping")
-    nb = _kv4_pools(k_cache, v_cache, Hkv, D)
-    here = _here(k_new, v_new, k_cache, v_cache, slot_mapping, err_flag)
-    if T == 0:
-        return
-    _call("xs_kv4_append", k_new.data_ptr(), _rows(k_new, "k_new"), v_new.data_ptr(),
-          _rows(v_new, "v_new"), _ptr(k_cache), _ptr(v_cache), _ptr(slot_mapping), T, Hkv, D,
-          BLOCK_SIZE, nb, dtype_code(k_new.dtype), _ptr(err_flag), here if stream is None else _stream(stream))
+    _done("xs_kv4_append", (_bound or _bind()).xs_kv4_append(
+        _entry("xs_kv4_append"), k_new, v_new, k_cache, v_cache, slot_mapping, err_flag,
+        _handle(stream)))
 
 
 def xs_kv4_append_paged(k_new, v_new, k_cache, v_cache, block_tables, context_lens, err_flag=None,
                         stream=None):
     """xs_kv_append_paged for 4-bit pools."""
-    B, Hkv, D = k_new.shape
-    _typed(v_new, k_new.dtype, (B, Hkv, D), "v_new")
-    _tables(block_tables, context_lens, B)
-    nb = _kv4_pools(k_cache, v_cache, Hkv, D)
-    here = _here(k_new, v_new, k_cache, v_cache, block_tables, context_lens, err_flag)
-    if B == 0:
-        return
-    _call("xs_kv4_append_paged", k_new.data_ptr(), _rows(k_new, "k_new"), v_new.data_ptr(),
-          _rows(v_new, "v_new"), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
-          block_tables.shape[1], _ptr(context_lens), B, Hkv, D, BLOCK_SIZE, nb,
-          dtype_code(k_new.dtype), _ptr(err_flag), here if stream is None else _stream(stream))
+    _done("xs_kv4_append_paged", (_bound or _bind()).xs_kv4_append_paged(
+        _entry("xs_kv4_append_paged"), k_new, v_new, k_cache, v_cache, block_tables, context_lens,
+        err_flag, _handle(stream)))
 
 
 def xs_kv4_unpack(k_out, v_out, k_cache, v_cache, block_ids, err_flag=None, stream=None):
     """Blocks block_ids (int32 [n]) of 4-bit pools as blocks 0 .. n - 1 of
     k_out, v_out [n, Hkv, 16, D] (bf16 or fp32): what xs_paged_prefill and
     xs_paged_prefill_tc read for a prompt chunk over a 4-bit cache."""
-    n, Hkv, bs, D = k_out.shape
-    if bs != BLOCK_SIZE:
-        _refuse(f"k_out must be [n, Hkv, {BLOCK_SIZE}, D]")
-    _typed(v_out, k_out.dtype, (n, Hkv, bs, D), "v_out")
-    _typed(block_ids, torch.int32, (n,), "block_ids")
-    nb = _kv4_pools(k_cache, v_cache, Hkv, D)
-    here = _here(k_out, v_out, k_cache, v_cache, block_ids, err_flag)
-    if n == 0:
-        return
-    _call("xs_kv4_unpack", _ptr(k_out), _ptr(v_out), _ptr(k_cache), _ptr(v_cache),
-          _ptr(block_ids), n, Hkv, D, bs, nb, dtype_code(k_out.dtype), _ptr(err_flag),
-          here if stream is None else _stream(stream))
+    _done("xs_kv4_unpack", (_bound or _bind()).xs_kv4_unpack(
+        _entry("xs_kv4_unpack"), k_out, v_out, k_cache, v_cache, block_ids, err_flag,
+        _handle(stream)))
 
 
 class Kv4Workspace:
@@ -678,33 +576,19 @@ class Kv4Workspace:
     (zeroed) once; calls that share one must be ordered."""
 
     def __init__(self, B: int, Hq: int, Hkv: int, D: int, device):
-        self.B, self.heads = B, (Hq, Hkv, D)
-        self.nbytes = int(load().xs_kv4_decode_workspace_bytes(B, Hq, Hkv, D))
-        self.buf = torch.zeros(max(self.nbytes, 16), dtype=torch.uint8, device=device)
+        self.B, self.Hq, self.Hkv, self.D = B, Hq, Hkv, D
+        nbytes = int(load().xs_kv4_decode_workspace_bytes(B, Hq, Hkv, D))
+        self.buf = torch.zeros(max(nbytes, 16), dtype=torch.uint8, device=device)
 
 
 def xs_kv4_decode(out, q, k_cache, v_cache, block_tables, context_lens, scale, workspace,
                   sinks=None, window=0, err_flag=None, stream=None):
     """Decode attention over a 4-bit cache (q, out [B, Hq, D] bf16), with
     optional sinks ([Hq], bf16) and sliding window, in one call."""
-    B, Hq, D = q.shape
-    _typed(out, q.dtype, (B, Hq, D), "out")
-    if k_cache.dim() != 3:
-        _refuse("4-bit pools must be [num_blocks, Hkv, 9 D]")
-    Hkv = k_cache.shape[1]
-    nb = _kv4_pools(k_cache, v_cache, Hkv, D)
-    _tables(block_tables, context_lens, B)
-    _typed(sinks, q.dtype, (Hq,), "sinks")
-    if workspace.heads != (Hq, Hkv, D) or B > workspace.B:
-        _refuse("the workspace is for other heads or a smaller batch")
-    buf = workspace.buf
-    here = _here(q, out, k_cache, v_cache, block_tables, context_lens, sinks, buf, err_flag)
-    if B == 0:
-        return
-    _call("xs_kv4_decode", _ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
-          block_tables.shape[1], _ptr(context_lens), _ptr(sinks), int(window), B, Hq, Hkv, D,
-          BLOCK_SIZE, nb, float(scale), buf.data_ptr(), workspace.nbytes, dtype_code(q.dtype),
-          _ptr(err_flag), here if stream is None else _stream(stream))
+    w = workspace
+    _done("xs_kv4_decode", (_bound or _bind()).xs_kv4_decode(
+        _entry("xs_kv4_decode"), out, q, k_cache, v_cache, block_tables, context_lens, scale,
+        w.buf, w.B, w.Hq, w.Hkv, w.D, sinks, window, err_flag, _handle(stream)))
 
 
 # ---------------------------------------------------------------- shared pages
@@ -715,45 +599,18 @@ def xs_block_fork(parents, children, block_tables, context_lens, free_stack, fre
     parents: full pages shared (counted in extra_refs, int32 [num_blocks]), an
     unfinished last page replaced by a free block, with the pair to copy in
     copies (int64 [n, 2]; -1: none) for xs_block_copy."""
-    n, B = parents.numel(), context_lens.numel()
-    _typed(parents, torch.int32, (n,), "parents")
-    _typed(children, torch.int32, (n,), "children")
-    _typed(copies, torch.int64, (n, 2), "copies")
-    _tables(block_tables, context_lens, B)
-    _share(free_stack, free_top, extra_refs)
-    here = _here(parents, children, block_tables, context_lens, free_stack, free_top, extra_refs,
-                 copies, err_flag)
-    if n == 0:
-        return
-    _call("xs_block_fork", _ptr(parents), _ptr(children), n, _ptr(block_tables),
-          block_tables.shape[1], _ptr(context_lens), B, block_size, _ptr(free_stack),
-          _ptr(free_top), _ptr(extra_refs), extra_refs.numel(), _ptr(copies), _ptr(err_flag),
-          here if stream is None else _stream(stream))
+    _done("xs_block_fork", (_bound or _bind()).xs_block_fork(
+        _entry("xs_block_fork"), parents, children, block_tables, context_lens, free_stack,
+        free_top, extra_refs, copies, block_size, err_flag, _handle(stream)))
 
 
 def xs_block_release(seq_ids, block_tables, context_lens, free_stack, free_top, extra_refs,
                      block_size=BLOCK_SIZE, err_flag=None, stream=None):
     """xs_block_free for sequences that may share pages: blocks go back on the
     stack with their last owner, the highest id first."""
-    B = context_lens.numel()
-    _typed(seq_ids, torch.int32, (seq_ids.numel(),), "seq_ids")
-    _tables(block_tables, context_lens, B)
-    _share(free_stack, free_top, extra_refs)
-    here = _here(seq_ids, block_tables, context_lens, free_stack, free_top, extra_refs, err_flag)
-    if seq_ids.numel() == 0:
-        return
-    _call("xs_block_release", _ptr(seq_ids), seq_ids.numel(), _ptr(block_tables),
-          block_tables.shape[1], _ptr(context_lens), B, block_size, _ptr(free_stack),
-          _ptr(free_top), free_stack.numel(), _ptr(extra_refs), extra_refs.numel(),
-          _ptr(err_flag), here if stream is None else _stream(stream))
-
-
-def _share(free_stack, free_top, extra_refs) -> None:
-    i32 = torch.int32
-    if free_stack.dtype != i32 or free_top.dtype != i32 or extra_refs.dtype != i32:
-        _refuse("free_stack, free_top and extra_refs must be int32")
-    if free_top.numel() != 1:
-        _refuse("free_top must be one int32")
+    _done("xs_block_release", (_bound or _bind()).xs_block_release(
+        _entry("xs_block_release"), seq_ids, block_tables, context_lens, free_stack, free_top,
+        extra_refs, block_size, err_flag, _handle(stream)))
 
 
 def xs_block_compact(block_tables, block_tables_out, context_lens, extra_refs, extra_refs_out,
@@ -764,40 +621,18 @@ def xs_block_compact(block_tables, block_tables_out, context_lens, extra_refs, e
     (int32 [num_blocks]) and the (from, to) pairs moves (int64 [num_blocks // 2,
     2], n_moves of them); xs_block_copy(k, v, moves, count=n_moves) then moves
     the contents."""
-    B, nb = context_lens.numel(), extra_refs.numel()
-    _tables(block_tables, context_lens, B)
-    _typed(block_tables_out, torch.int32, tuple(block_tables.shape), "block_tables_out")
-    _share(free_stack, free_top, extra_refs)
-    _typed(extra_refs_out, torch.int32, (nb,), "extra_refs_out")
-    _typed(free_stack, torch.int32, (nb,), "free_stack")
-    _typed(remap, torch.int32, (nb,), "remap")
-    _typed(moves, torch.int64, (nb // 2, 2), "moves")
-    _typed(n_moves, torch.int32, (1,), "n_moves")
-    here = _here(block_tables, block_tables_out, context_lens, extra_refs, extra_refs_out,
-                 free_stack, free_top, remap, moves, n_moves, err_flag)
-    _call("xs_block_compact", _ptr(block_tables), _ptr(block_tables_out), block_tables.shape[1],
-          _ptr(context_lens), B, block_size, _ptr(extra_refs), _ptr(extra_refs_out),
-          _ptr(free_stack), _ptr(free_top), nb, _ptr(remap), _ptr(moves), _ptr(n_moves),
-          _ptr(err_flag), here if stream is None else _stream(stream))
+    _done("xs_block_compact", (_bound or _bind()).xs_block_compact(
+        _entry("xs_block_compact"), block_tables, block_tables_out, context_lens, extra_refs,
+        extra_refs_out, free_stack, free_top, remap, moves, n_moves, block_size, err_flag,
+        _handle(stream)))
 
 
 def xs_block_copy(k_pools, v_pools, pairs, count=None, err_flag=None, stream=None):
     """Copy block s to block d for every row (s, d) of pairs (int64 [n, 2]; the
     first `count` (int32 [1], device) of them if given) within the K and V
     pools of every layer: [layers, num_blocks, Hkv, ...], any page format."""
-    shape = k_pools.shape
-    if v_pools.shape != shape or v_pools.dtype != k_pools.dtype or len(shape) < 3:
-        _refuse("k_pools and v_pools must be [layers, num_blocks, ...] of one type and shape")
-    layers, nb = shape[0], shape[1]
-    n = pairs.shape[0]
-    _typed(pairs, torch.int64, (n, 2), "pairs")
-    _typed(count, torch.int32, (1,), "count")
-    here = _here(k_pools, v_pools, pairs, count, err_flag)
-    if layers == 0 or nb == 0 or n == 0:
-        return
-    block = k_pools.numel() // (layers * nb) * k_pools.element_size()
-    _call("xs_block_copy", _ptr(k_pools), _ptr(v_pools), layers, nb * block, _ptr(pairs), n,
-          _ptr(count), block, nb, _ptr(err_flag), here if stream is None else _stream(stream))
+    _done("xs_block_copy", (_bound or _bind()).xs_block_copy(
+        _entry("xs_block_copy"), k_pools, v_pools, pairs, count, err_flag, _handle(stream)))
 
 
 def xs_version() -> int:
@@ -832,6 +667,7 @@ def use_library(lib):
     global _lib
     with _lock:
         prev, _lib = _lib, lib
+        _entries.clear()
     return prev
 
 

@@ -160,16 +160,25 @@ def test_binding_refuses(lib):
                 dict(cos_sin=meta(64, 128)), dict(k_weight=meta(128, dtype=torch.float32))):
         with pytest.raises(ValueError):
             ops.xs_qk_norm_rope(**{**good, **bad})
-    assert ops._rows(meta(4, 10, 128)[:, :8], "q") == 1280
+    # Slices of a projection are taken (and refused only for being on the CPU);
+    # rows whose heads are apart are not.
+    with pytest.raises(ValueError, match="CUDA"):
+        ops.xs_qk_norm_rope(**{**good, "q": meta(4, 10, 128)[:, :8]})
     for odd in (meta(4, 128, 8).transpose(1, 2), meta(4, 8, 256)[..., :128], meta(4, 16, 128)[:, ::2]):
-        with pytest.raises(ValueError):
-            ops._rows(odd, "q")
+        with pytest.raises(ValueError, match="contiguous"):
+            ops.xs_qk_norm_rope(**{**good, "q": odd})
+    with pytest.raises(ValueError, match="tensor"):
+        ops.xs_qk_norm_rope(**{**good, "k": None})
+    slots = meta(4, dtype=torch.int64)
+    app = dict(q_out=q, q=q, k=k, v=k, q_weight=w, k_weight=w, eps=1e-6, cos_sin=cs, positions=pos,
+               slot_mapping=slots)
     for kc in (meta(9, 2, 16, 64), meta(9, 3, 16, 128), meta(9, 2, 16, 128, dtype=torch.float32),
-               meta(9, 2, 1024, dtype=torch.uint8)):
-        with pytest.raises(ValueError):
-            ops._pools(kc, kc, torch.bfloat16, 2, 128)
-    assert ops._pools(meta(9, 2, 1152, dtype=torch.uint8), meta(9, 2, 1152, dtype=torch.uint8),
-                      torch.bfloat16, 2, 128) == (9, ops.XS_CACHE_KV4)
+               meta(9, 2, 1024, dtype=torch.uint8), meta(9, 2, 16, 144, dtype=torch.uint8)):
+        with pytest.raises(ValueError, match="pool"):
+            ops.xs_qk_norm_rope_append(**app, k_cache=kc, v_cache=kc)
+    for kc in (meta(9, 2, 16, 128), meta(9, 2, 1152, dtype=torch.uint8)):
+        with pytest.raises(ValueError, match="CUDA"):
+            ops.xs_qk_norm_rope_append(**app, k_cache=kc, v_cache=kc)
     kc = meta(9, 2, 1152, dtype=torch.uint8)
     bt, lens = meta(4, 3, dtype=torch.int32), meta(4, dtype=torch.int32)
     ws = ops.Kv4Workspace(4, 8, 2, 128, "cpu")

@@ -38,22 +38,50 @@ __device__ __forceinline__ uint32_t kv4_key(float x) {
     const uint32_t u = __float_as_uint(x);
     return (u << 1) | ((u >> 31) ^ 1u);
 }
+// The key of the extreme of four bf16 values, two to a word.
+__device__ __forceinline__ uint32_t kv4_key4(uint32_t w0, uint32_t w1) {
+    const __nv_bfloat162 a = *reinterpret_cast<const __nv_bfloat162 *>(&w0);
+    const __nv_bfloat162 b = *reinterpret_cast<const __nv_bfloat162 *>(&w1);
+    const float2 hi = __bfloat1622float2(__hmax2_nan(a, b)), lo = __bfloat1622float2(__hmin2_nan(a, b));
+    float mx, mn;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(mx) : "f"(hi.x), "f"(hi.y));
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(mn) : "f"(lo.x), "f"(lo.y));
+    return kv4_key(mx >= -mn ? mx : mn);
+}
 __device__ __forceinline__ float kv4_scale(uint32_t key) {
     const float e = __uint_as_float((key >> 1) | ((key & 1u) ? 0u : 0x80000000u));
     return __bfloat162float(__float2bfloat16_rn(e * -0.125f));
 }
-// The code of x under s.  A group with an infinity or a NaN has an infinite or
-// NaN scale; its codes become 8 (a NaN converts to 0), and it reads as NaN.
-__device__ __forceinline__ uint32_t kv4_code(float x, float s) {
-    const int n = s == 0.0f ? 0 : __float2int_rn(__fdiv_rn(x, s));
-    return static_cast<uint32_t>(min(max(n, -8), 7) + 8);
-}
-// Eight dims (a chunk: dims 8 ch .. 8 ch + 7) as one word, the first lowest.
-__device__ __forceinline__ uint32_t kv4_pack8(const float *x, float s) {
+// The codes of four dims under s, the first lowest: rne(x / s), clamped.  The
+// quotient is x times an approximate 1 / s, corrected by its own remainder:
+// where x / s is a half integer (or any fp32 number) that gives it exactly, and
+// elsewhere x / s is at least 1/512 away from a tie, so the rounding is that of
+// the true quotient.  Adding 1.5 2^23 + 8 rounds to the nearest even integer
+// and leaves the code in the low bits; the four are joined by one multiply-add
+// each, and what the constant adds up to is taken off at the end.
+// Scales without a usable reciprocal (0, tiny, infinite, NaN) divide instead; a
+// group with an infinity or a NaN gets codes of 8 (a NaN converts to 0) under
+// an infinite or NaN scale, and reads as NaN.
+__device__ __forceinline__ uint32_t kv4_pack4(const float *x, float s) {
     uint32_t w = 0;
+    if (!(fabsf(s) >= 0x1p-120f && fabsf(s) < INFINITY)) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) w |= kv4_code(x[i], s) << (4 * i);
-    return w;
+        for (int i = 0; i < 4; ++i) {
+            const int n = s == 0.0f ? 0 : __float2int_rn(__fdiv_rn(x[i], s));
+            w |= static_cast<uint32_t>(min(max(n, -8), 7) + 8) << (4 * i);
+        }
+        return w;
+    }
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+    constexpr uint32_t kBits = 0x4b400000u;     // of 1.5 2^23
+#pragma unroll
+    for (int i = 3; i >= 0; --i) {
+        float q = x[i] * r;
+        q = fmaf(fmaf(-q, s, x[i]), r, q);
+        w = w * 16u + __float_as_uint(fminf(fmaxf(q, -8.0f), 7.0f) + (0x1.8p23f + 8.0f));
+    }
+    return w - kBits * 0x1111u;
 }
 
 // Stores chunk `ch` (8 dims) of row `o` of a page, and the group's scale with
@@ -75,6 +103,22 @@ __device__ __forceinline__ void kv4_store_chunk(uint8_t *page, bool is_v, int o,
         reinterpret_cast<uint32_t *>(page)[o * (D / 8) + t * NG + c] = w;
         if (t == 0) reinterpret_cast<__nv_bfloat16 *>(scales)[o * NG + c] = sb;
     }
+}
+
+// The same for row o of a V page by the lanes of both rows of its pair at
+// once: `mine` is this row's word of chunk ch, `theirs` the other row's; the
+// even row's lane stores the words of the chunk's first four dims, the odd
+// row's those of its last four.
+template <int D>
+__device__ __forceinline__ void kv4_store_pair(uint8_t *page, int o, int ch, uint32_t mine,
+                                               uint32_t theirs, float s) {
+    constexpr int NG = D / kKv4Group;
+    const int c = ch >> 2, t = ch & 3, pair = o >> 1, r = o & 1;
+    const uint32_t w = r ? __byte_perm(theirs, mine, 0x7632) : __byte_perm(mine, theirs, 0x5410);
+    reinterpret_cast<uint32_t *>(page)[(pair * 8 + 2 * t + r) * NG + c] = w;
+    if (t == 0)
+        reinterpret_cast<__nv_bfloat16 *>(page + 8 * D)[(pair * NG + c) * 2 + r] =
+            __float2bfloat16_rn(s);
 }
 
 }  // namespace xs

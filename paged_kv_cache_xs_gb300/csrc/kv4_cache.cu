@@ -12,70 +12,142 @@ namespace {
 
 constexpr int kUnpackThreads = 256;
 
-template <typename T> struct Store8;
-template <> struct Store8<__nv_bfloat16> {
-    static __device__ __forceinline__ void put(__nv_bfloat16 *p, const float *f) {
-        uint32_t w[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-            w[i] = *reinterpret_cast<const uint32_t *>(&h);
-        }
-        *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-    }
-};
-template <> struct Store8<float> {
-    static __device__ __forceinline__ void put(float *p, const float *f) {
-        reinterpret_cast<float4 *>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
-        reinterpret_cast<float4 *>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
-    }
-};
+__device__ __forceinline__ __nv_bfloat162 as_bf162(uint32_t x) {
+    return *reinterpret_cast<const __nv_bfloat162 *>(&x);
+}
+__device__ __forceinline__ uint32_t as_u32(__nv_bfloat162 x) {
+    return *reinterpret_cast<const uint32_t *>(&x);
+}
+// n - 8 for the low nibbles n of both halves of a word, as bf16: 0x4300 | n is
+// 128 + n, and the difference is exact.
+__device__ __forceinline__ uint32_t centred(uint32_t w) {
+    uint32_t x;
+    asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(x) : "r"(w), "r"(0x000f000fu), "r"(0x43004300u));
+    return as_u32(__hsub2(as_bf162(x), as_bf162(0x43084308u)));
+}
+__device__ __forceinline__ uint32_t times(uint32_t x, uint32_t s) {
+    return as_u32(__hmul2(as_bf162(x), as_bf162(s)));   // one rounding
+}
+__device__ __forceinline__ float lo_f32(uint32_t x) { return __uint_as_float(x << 16); }
+__device__ __forceinline__ float hi_f32(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
 
-// One thread turns one chunk of 8 dims (a word of a K page, two half words of
-// a V page) into 8 values; a warp's stores are contiguous.
+// Eight values of a K row: d[j] holds n - 8 of dims j and j + 4, s2 the scale twice.
+__device__ __forceinline__ void store_k(__nv_bfloat16 *p, const uint32_t *d, uint32_t s2) {
+    uint32_t v[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = times(d[j], s2);
+    *reinterpret_cast<uint4 *>(p) =
+        make_uint4(__byte_perm(v[0], v[1], 0x5410), __byte_perm(v[2], v[3], 0x5410),
+                   __byte_perm(v[0], v[1], 0x7632), __byte_perm(v[2], v[3], 0x7632));
+}
+__device__ __forceinline__ void store_k(float *p, const uint32_t *d, uint32_t s2) {
+    const float s = lo_f32(s2);
+    reinterpret_cast<float4 *>(p)[0] =
+        make_float4(lo_f32(d[0]) * s, lo_f32(d[1]) * s, lo_f32(d[2]) * s, lo_f32(d[3]) * s);
+    reinterpret_cast<float4 *>(p)[1] =
+        make_float4(hi_f32(d[0]) * s, hi_f32(d[1]) * s, hi_f32(d[2]) * s, hi_f32(d[3]) * s);
+}
+// Eight dims of two V rows, `step` elements apart: d[j] holds n - 8 of dim j of
+// both, s2 their scales.
+__device__ __forceinline__ void store_v(__nv_bfloat16 *p, int step, const uint32_t *d, uint32_t s2) {
+    uint32_t v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = times(d[j], s2);
+    *reinterpret_cast<uint4 *>(p) =
+        make_uint4(__byte_perm(v[0], v[1], 0x5410), __byte_perm(v[2], v[3], 0x5410),
+                   __byte_perm(v[4], v[5], 0x5410), __byte_perm(v[6], v[7], 0x5410));
+    *reinterpret_cast<uint4 *>(p + step) =
+        make_uint4(__byte_perm(v[0], v[1], 0x7632), __byte_perm(v[2], v[3], 0x7632),
+                   __byte_perm(v[4], v[5], 0x7632), __byte_perm(v[6], v[7], 0x7632));
+}
+__device__ __forceinline__ void store_v(float *p, int step, const uint32_t *d, uint32_t s2) {
+    const float a = lo_f32(s2), b = hi_f32(s2);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const uint32_t *e = d + 4 * k;
+        reinterpret_cast<float4 *>(p)[k] =
+            make_float4(lo_f32(e[0]) * a, lo_f32(e[1]) * a, lo_f32(e[2]) * a, lo_f32(e[3]) * a);
+        reinterpret_cast<float4 *>(p + step)[k] =
+            make_float4(hi_f32(e[0]) * b, hi_f32(e[1]) * b, hi_f32(e[2]) * b, hi_f32(e[3]) * b);
+    }
+}
+
+// Words of a lane's 16 (D = 128) or 8 (D = 64) bytes of codes.
+template <int NG> __device__ __forceinline__ void load_codes(uint32_t *w, const uint8_t *p) {
+    if constexpr (NG == 4) {
+        const uint4 x = *reinterpret_cast<const uint4 *>(p);
+        w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+    } else {
+        const uint2 x = *reinterpret_cast<const uint2 *>(p);
+        w[0] = x.x, w[1] = x.y;
+    }
+}
+
+// A warp turns one page (16 rows of one head, K or V), two passes of 8 rows.
+// Its loads are whole lines; its stores are 64 contiguous bytes (bf16) for
+// each row and group of 32 dims.
 template <typename T, int D>
 __global__ void __launch_bounds__(kUnpackThreads)
     kv4_unpack_kernel(T *__restrict__ k_out, T *__restrict__ v_out,
                       const uint8_t *__restrict__ k_cache, const uint8_t *__restrict__ v_cache,
                       const int32_t *__restrict__ ids, int n, int Hkv, int64_t num_blocks,
                       int *err_flag) {
-    constexpr int NG = D / kKv4Group, kChunks = 16 * D / 8;
-    const int64_t total = static_cast<int64_t>(n) * Hkv * 2 * kChunks;
-    const int64_t stride = static_cast<int64_t>(gridDim.x) * blockDim.x;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < total;
-         i += stride) {
-        const int at = static_cast<int>(i % kChunks);
-        const int64_t item = i / kChunks;           // ((page, K or V), head)
-        const int64_t pv = item / Hkv;
+    constexpr int NG = D / kKv4Group;
+    const int lane = threadIdx.x & 31;
+    const int64_t total = static_cast<int64_t>(n) * Hkv * 2;
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * (kUnpackThreads / 32);
+    for (int64_t item = static_cast<int64_t>(blockIdx.x) * (kUnpackThreads / 32) + (threadIdx.x >> 5);
+         item < total; item += stride) {
+        const int64_t pv = total < (int64_t(1) << 32)
+                               ? static_cast<uint32_t>(item) / static_cast<uint32_t>(Hkv)
+                               : item / Hkv;                    // (page, K or V)
         const int h = static_cast<int>(item - pv * Hkv);
         const bool is_v = pv & 1;
         const int32_t blk = ids[pv >> 1];
-        if (blk < 0) continue;                      // no page here: left as it was
+        if (blk < 0) continue;                                  // no page here: left as it was
         if (blk >= num_blocks) {
-            if (at == 0 && h == 0) raise_flag(err_flag, XS_FLAG_BAD_BLOCK);
+            if (lane == 0 && h == 0) raise_flag(err_flag, XS_FLAG_BAD_BLOCK);
             continue;
         }
         const uint8_t *page = (is_v ? v_cache : k_cache) +
                               (static_cast<int64_t>(blk) * Hkv + h) * kv4_page_bytes(D);
-        const __nv_bfloat16 *scales = reinterpret_cast<const __nv_bfloat16 *>(page + 8 * D);
-        const int o = at / (D / 8), ch = at % (D / 8), c = ch >> 2, t = ch & 3;
-        uint32_t w;
-        float s;
-        if (is_v) {
-            const uint16_t *half = reinterpret_cast<const uint16_t *>(page);
-            const int pair = o >> 1, r = o & 1;
-            w = half[((pair * 8 + 2 * t) * NG + c) * 2 + r] |
-                static_cast<uint32_t>(half[((pair * 8 + 2 * t + 1) * NG + c) * 2 + r]) << 16;
-            s = __bfloat162float(scales[(pair * NG + c) * 2 + r]);
-        } else {
-            w = reinterpret_cast<const uint32_t *>(page)[o * (D / 8) + t * NG + c];
-            s = __bfloat162float(scales[o * NG + c]);
-        }
-        float f[8];
+        T *out = (is_v ? v_out : k_out) + ((pv >> 1) * Hkv + h) * (16 * D);
+        uint32_t w[2][NG];
+        if (!is_v) {
+            // Lane (g, t): row g (+ 8), dims 32 c + 8 t .. + 7.
+            const int g = lane >> 2, t = lane & 3;
+            uint16_t s[2][NG];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = s * static_cast<float>(static_cast<int>((w >> (4 * e)) & 15) - 8);
-        T *dst = (is_v ? v_out : k_out) + (((pv >> 1) * Hkv + h) * 16 + o) * D + 8 * ch;
-        Store8<T>::put(dst, f);
+            for (int u = 0; u < 2; ++u) {
+                load_codes<NG>(w[u], page + (g + 8 * u) * (D / 2) + t * (4 * NG));
+#pragma unroll
+                for (int c = 0; c < NG; ++c)
+                    s[u][c] = reinterpret_cast<const uint16_t *>(page + 8 * D)[(g + 8 * u) * NG + c];
+            }
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int c = 0; c < NG; ++c) {
+                    uint32_t d[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) d[j] = centred(w[u][c] >> (4 * j));
+                    store_k(out + (g + 8 * u) * D + 32 * c + 8 * t, d, s[u][c] * 0x10001u);
+                }
+        } else {
+            // Lane (i, q): dims 32 c + 8 q .. + 7 of rows 2 i and 2 i + 1.
+            const int i = lane >> 2, q = lane & 3;
+            uint32_t s2[NG];
+            load_codes<NG>(w[0], page + i * D + (2 * q) * (4 * NG));
+            load_codes<NG>(w[1], page + i * D + (2 * q + 1) * (4 * NG));
+            load_codes<NG>(s2, page + 8 * D + i * (4 * NG));
+#pragma unroll
+            for (int c = 0; c < NG; ++c) {
+                uint32_t d[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) d[j] = centred(w[j >> 2][c] >> (4 * (j & 3)));
+                store_v(out + 2 * i * D + 32 * c + 8 * q, D, d, s2[c]);
+            }
+        }
     }
 }
 
@@ -99,8 +171,8 @@ extern "C" int xs_kv4_unpack(void *k_out, void *v_out, const void *k_cache, cons
         !xs::aligned16(v_cache))
         return XS_EALIGN;
     if (n == 0) return XS_OK;
-    const int64_t total = static_cast<int64_t>(n) * Hkv * 2 * (2 * D);
-    const int64_t want = (total + xs::kUnpackThreads - 1) / xs::kUnpackThreads;
+    const int64_t total = static_cast<int64_t>(n) * Hkv * 2;     // a warp each
+    const int64_t want = (total + xs::kUnpackThreads / 32 - 1) / (xs::kUnpackThreads / 32);
     const int grid = static_cast<int>(want < (1 << 20) ? want : (1 << 20));
     auto kc = static_cast<const uint8_t *>(k_cache), vc = static_cast<const uint8_t *>(v_cache);
     auto go = [&](auto kernel, auto *ko, auto *vo) {

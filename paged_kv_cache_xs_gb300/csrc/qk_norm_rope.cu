@@ -13,18 +13,35 @@
 // quantises that rounded row, so the fused append stores what an append of
 // the rotated rows would.
 //
-// A row is D / 16 lanes.  Each lane holds two chunks of 8 dims that the
-// rotation pairs with one another (dims 8 j.. and rotary_dim / 2 + 8 j.. of
-// split halves, 16 j.. of neighbouring pairs), so the rotation needs no
-// exchange and every access is 16 bytes.  Nothing is read twice but the table
-// and the weights, which stay in the caches: the pass is bound by the bytes of
-// the rows, or for a decode batch by the latency of length -> table -> page.
+// A row is D / 8 lanes.  Each lane holds two chunks of 4 dims that the
+// rotation pairs with one another (dims 4 j.. and rotary_dim / 2 + 4 j.. of
+// split halves, 8 j.. of neighbouring pairs), so the rotation needs no
+// exchange.  A prompt's pass is short of issue slots and of rows on their way
+// before it is short of bytes: fp32 goes two to an operation, the weights lie
+// in shared memory as fp32, addresses advance by a step, and a lane holds so
+// little that many warps are resident.  (8K tokens of 32q/8kv x 128 in bf16:
+// 58 us with one value to an operation, 47 us with one row ahead, 40 us so; a copy of
+// as many bytes takes 32 us.)
+//
+// A warp takes kRows consecutive tokens, one for each of its lane groups, and
+// a run of heads: position, page, cosines and sines are fetched once for the
+// run, and the next head's row while the current one is worked on.  A prompt
+// is bound by the bytes of its rows; a decode batch by the latency of length
+// -> table -> page, so its runs are single heads.  Consecutive tokens also lie
+// in one page, where two rows of 4-bit V share their words: a pair of groups
+// writes whole words.
+#include <climits>
+
 #include "kv4.cuh"
 
 namespace xs {
 namespace {
 
-constexpr int kRopeThreads = 256;
+constexpr int kRopeThreads = 128;
+constexpr int kRopeCtas = 8;        // on an SM
+constexpr int kRopeAheadBytes = 8;  // rows of a lane on their way, times the size of a value
+constexpr int kRopeRun = 16;
+constexpr int kRopeWarpsPerSm = 24;
 
 struct RopeParams {
     const void *q, *k, *v;      // rows of head h of token t at t * stride + h * D
@@ -43,40 +60,99 @@ struct RopeParams {
     int64_t num_blocks;
     int T, Hq, Hkv;
     int rows_per_token;         // Hq + Hkv, and Hkv more for V with an append
+    int run;                    // heads that a warp takes one after the other
     bool interleaved, kv4;
     int *err_flag;
 };
 
-// Chunk of 8 values at p (16-byte aligned) as fp32, and back.
-__device__ __forceinline__ void load8(const __nv_bfloat16 *p, float *f) {
-    unpack16(*reinterpret_cast<const uint4 *>(p), f, static_cast<__nv_bfloat16 *>(nullptr));
-}
-__device__ __forceinline__ void load8(const float *p, float *f) {
-    unpack16(reinterpret_cast<const uint4 *>(p)[0], f, static_cast<float *>(nullptr));
-    unpack16(reinterpret_cast<const uint4 *>(p)[1], f + 4, static_cast<float *>(nullptr));
-}
-__device__ __forceinline__ void store8(__nv_bfloat16 *p, const float *f) {
-    uint32_t w[4];
+// N values at p as they come from memory (8 to 32 bytes, as aligned), and as fp32.
+template <typename T, int N> struct Chunk {
+    static constexpr int kWords = N * sizeof(T) / 4;
+    uint32_t w[kWords];
+    __device__ __forceinline__ void load(const T *p) {
+        if constexpr (kWords == 2) {
+            const uint2 v = *reinterpret_cast<const uint2 *>(p);
+            w[0] = v.x, w[1] = v.y;
+        } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-        w[i] = *reinterpret_cast<const uint32_t *>(&h);
+            for (int i = 0; i < kWords / 4; ++i) {
+                const uint4 v = reinterpret_cast<const uint4 *>(p)[i];
+                w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
+            }
+        }
     }
-    *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    __device__ __forceinline__ void store(T *p) const {
+        if constexpr (kWords == 2) {
+            *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kWords / 4; ++i)
+                reinterpret_cast<uint4 *>(p)[i] =
+                    make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+        }
+    }
+    __device__ __forceinline__ void to_f32(float *f) const {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) {
+            if constexpr (sizeof(T) == 4) {
+                f[i] = __uint_as_float(w[i]);
+            } else {
+                f[2 * i] = __uint_as_float(w[i] << 16);
+                f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+            }
+        }
+    }
+    __device__ __forceinline__ void from_f32(const float *f) {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) {
+            if constexpr (sizeof(T) == 4) {
+                w[i] = __float_as_uint(f[i]);
+            } else {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+                w[i] = *reinterpret_cast<const uint32_t *>(&h);
+            }
+        }
+    }
+};
+
+// Two fp32 values in one operation.
+struct F2 {
+    float x, y;
+};
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+    F2 r;
+    asm("{\n .reg .b64 p, q, s;\n mov.b64 p, {%2, %3};\n mov.b64 q, {%4, %5};\n"
+        " mul.rn.f32x2 s, p, q;\n mov.b64 {%0, %1}, s;\n}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
 }
-__device__ __forceinline__ void store8(float *p, const float *f) {
-    reinterpret_cast<float4 *>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
-    reinterpret_cast<float4 *>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+__device__ __forceinline__ F2 sub2(F2 a, F2 b) {
+    F2 r;
+    asm("{\n .reg .b64 p, q, s;\n mov.b64 p, {%2, %3};\n mov.b64 q, {%4, %5};\n"
+        " sub.rn.f32x2 s, p, q;\n mov.b64 {%0, %1}, s;\n}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("{\n .reg .b64 p, q, s;\n mov.b64 p, {%2, %3};\n mov.b64 q, {%4, %5};\n"
+        " mov.b64 s, {%6, %7};\n fma.rn.f32x2 s, p, q, s;\n mov.b64 {%0, %1}, s;\n}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return r;
 }
 
-// Mean of the squares of a row, of which each of its lanes holds 16 values.
-template <int kLanes> __device__ __forceinline__ float mean_square(const float *x) {
-    float sum = 0.0f;
+// Mean of the squares of a row, of which each of its lanes holds 8 values.
+template <int kLanes> __device__ __forceinline__ float mean_square(const F2 *x) {
+    F2 sum = mul2(x[0], x[0]);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) sum = fmaf(x[i], x[i], sum);
+    for (int i = 1; i < 4; ++i) sum = fma2(x[i], x[i], sum);
+    float s = sum.x + sum.y;
 #pragma unroll
-    for (int m = kLanes / 2; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
-    return sum * (1.0f / (16 * kLanes));
+    for (int m = kLanes / 2; m > 0; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
+    return s * (1.0f / (8 * kLanes));
 }
 
 // The slot that row t's token is appended to, or -1 (none, or flagged).
@@ -103,143 +179,226 @@ __device__ __forceinline__ int64_t append_slot(const RopeParams &p, int64_t t, i
     return static_cast<int64_t>(blk) * 16 + (pos & 15);
 }
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(const RopeParams p) {
-    constexpr int kLanes = D / 16;              // lanes of a row
+template <typename T, int D, bool kKv4>
+__global__ void __launch_bounds__(kRopeThreads, kRopeCtas)
+    qk_norm_rope_kernel(const __grid_constant__ RopeParams p) {
+    constexpr int kLanes = D / 8;               // lanes of a row
     constexpr int kRows = 32 / kLanes;          // rows of a warp
-    __shared__ uint32_t keys[kRopeThreads / 32][kRows][D / 8];
+    __shared__ __align__(16) uint32_t keys[kKv4 ? kRopeThreads / 32 : 1][kRows][D / 4];
+    __shared__ __align__(16) float weights[2][D];
+    constexpr int kMine = 2 * D / kRopeThreads;     // weights of a thread
+    float weight[kMine];    // on their way to shared memory while the first rows are found
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+        const int e = threadIdx.x + i * kRopeThreads;
+        const T *w = static_cast<const T *>(e < D ? p.q_weight : p.k_weight);
+        weight[i] = w ? Elem<T>::to_f32(w[e % D]) : 1.0f;
+    }
     const int lane = threadIdx.x & 31, j = lane % kLanes, warp = threadIdx.x >> 5;
-    const int64_t total = static_cast<int64_t>(p.T) * p.rows_per_token;
-    const int64_t step = static_cast<int64_t>(gridDim.x) * (kRopeThreads / kLanes);
-    for (int64_t base = (static_cast<int64_t>(blockIdx.x) * (kRopeThreads / 32) + warp) * kRows;
-         base < total; base += step) {
-        const int64_t r = base + lane / kLanes;
-        bool on = r < total;
-        const int64_t t = !on ? 0
-                          : total < (int64_t(1) << 32)
-                              ? static_cast<uint32_t>(r) / static_cast<uint32_t>(p.rows_per_token)
-                              : r / p.rows_per_token;
-        const int h = static_cast<int>(on ? r - t * p.rows_per_token : 0);
-        const bool is_q = h < p.Hq, is_v = h >= p.Hq + p.Hkv;
-        int64_t pos = 0;
-        if (on) {
-            if (p.lens)
-                pos = static_cast<int64_t>(p.lens[t]) - 1;
-            else if (p.positions)
-                pos = p.positions[t];
-            on = pos >= 0;
-        }
-        const bool turned = p.rot > 0 && !is_v;
-        if (on && turned && pos >= p.max_pos) {
-            if (j == 0) raise_flag(p.err_flag, XS_FLAG_BAD_LEN);
-            on = false;
-        }
-        // The lane's two chunks, and the index of its first pair's angle.
-        const bool rotates = turned && j < p.rot / 16;
-        const bool split = rotates && !p.interleaved;
-        const int c0 = split ? j : 2 * j, c1 = split ? p.rot / 16 + j : 2 * j + 1;
-        const T *src = is_q   ? static_cast<const T *>(p.q) + t * p.q_stride + h * D
-                       : is_v ? static_cast<const T *>(p.v) + t * p.v_stride + (h - p.Hq - p.Hkv) * D
-                              : static_cast<const T *>(p.k) + t * p.k_stride + (h - p.Hq) * D;
-        float x[16];
-        if (on) {
-            load8(src + 8 * c0, x);
-            load8(src + 8 * c1, x + 8);
+    const int runs = (p.rows_per_token + p.run - 1) / p.run;
+    const int64_t item = static_cast<int64_t>(blockIdx.x) * (kRopeThreads / 32) + warp;
+    const int64_t block = item < (int64_t(1) << 32)
+                              ? static_cast<uint32_t>(item) / static_cast<uint32_t>(runs)
+                              : item / runs;
+    const int run_begin = static_cast<int>(item - block * runs) * p.run;
+    const int run_end = min(run_begin + p.run, p.rows_per_token);
+    const int64_t t = block * kRows + lane / kLanes;    // past T for an item past the last
+    bool live = t < p.T;
+    int64_t pos = 0;
+    if (live) {
+        if (p.lens)
+            pos = static_cast<int64_t>(p.lens[t]) - 1;
+        else if (p.positions)
+            pos = p.positions[t];
+        live = pos >= 0;
+    }
+    if (live && p.rot > 0 && pos >= p.max_pos) {
+        if (j == 0 && run_begin == 0) raise_flag(p.err_flag, XS_FLAG_BAD_LEN);
+        live = false;
+    }
+    int64_t slot = -1;
+    if (live && p.k_cache && run_end > p.Hq)
+        slot = append_slot(p, t, pos, j == 0 && run_begin <= p.Hq ? p.err_flag : nullptr);
+    if (slot >= 0 && !XS_BOUNDS((slot >> 4) < p.num_blocks, p.err_flag)) slot = -1;
+    const int64_t page0 = slot < 0 ? 0 : (slot >> 4) * p.Hkv;
+    const int o = static_cast<int>(slot & 15);
+
+    // The lane's chunks of a rotated row, and its cosines and sines.
+    const bool rotates = j < p.rot / 8;
+    const bool halves = rotates && !p.interleaved;
+    const int r0 = halves ? j : 2 * j, r1 = halves ? p.rot / 8 + j : 2 * j + 1;
+    F2 c[2], s[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) c[i] = F2{1.0f, 1.0f}, s[i] = F2{0.0f, 0.0f};
+    if (live && rotates && run_begin < p.Hq + p.Hkv) {
+        const float *row = p.cos_sin + pos * p.rot + 4 * j;
+        Chunk<float, 4> v;
+        v.load(row);
+        v.to_f32(&c[0].x);
+        v.load(row + p.rot / 2);
+        v.to_f32(&s[0].x);
+    }
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) (&weights[0][0])[threadIdx.x + i * kRopeThreads] = weight[i];
+    __syncthreads();
+
+    // q, then k, then v heads of the run.
+#pragma unroll 1
+    for (int kind = 0; kind < 3; ++kind) {
+        const int first = kind == 0 ? 0 : kind == 1 ? p.Hq : p.Hq + p.Hkv;
+        const int last = kind == 0 ? p.Hq : min(first + p.Hkv, p.rows_per_token);
+        const int begin = max(run_begin, first), count = min(run_end, last) - begin;
+        if (count <= 0) continue;
+        const int h = begin - first;
+        const int c0 = kind < 2 ? r0 : 2 * j, c1 = kind < 2 ? r1 : 2 * j + 1;
+        const T *src = kind == 0   ? static_cast<const T *>(p.q) + t * p.q_stride
+                       : kind == 1 ? static_cast<const T *>(p.k) + t * p.k_stride
+                                   : static_cast<const T *>(p.v) + t * p.v_stride;
+        src += h * D;
+        const bool paged = kind > 0 && p.k_cache;
+        const bool norm = kind == 0 ? p.q_weight != nullptr : kind == 1 && p.k_weight != nullptr;
+        const bool turn = kind < 2 && rotates;
+        const bool writes = paged ? slot >= 0 : live;
+        // Where the row goes, and how far on the next head's does.
+        T *dst;
+        uint8_t *page = nullptr;
+        int step = D;
+        if (!paged) {
+            dst = kind == 0 ? static_cast<T *>(p.q_out) + (t * p.Hq + h) * D
+                            : static_cast<T *>(p.k_out) + (t * p.Hkv + h) * D;
         } else {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) x[i] = 0.0f;
+            void *cache = kind == 1 ? p.k_cache : p.v_cache;
+            dst = static_cast<T *>(cache) + ((page0 + h) * 16 + o) * D;
+            page = static_cast<uint8_t *>(cache) + (page0 + h) * kv4_page_bytes(D);
+            step = 16 * D;
         }
-        const T *w = static_cast<const T *>(is_v ? nullptr : is_q ? p.q_weight : p.k_weight);
-        float mean = mean_square<kLanes>(x) + p.eps;
-        // Squares that leave fp32 (|x| beyond 2^60, or below 2^-50 under an eps
-        // that does not cover it) are taken of x 2^-96 or x 2^96 instead.
-        const float lift = mean > 0x1p125f ? 0x1p-96f : mean < 0x1p-100f ? 0x1p96f : 1.0f;
-        if (__any_sync(0xffffffffu, lift != 1.0f)) {
-            float y[16];
+        // Whether the next group's row (an even one's), or the one before (an
+        // odd one's), is the other row of this one's V pair.
+        const bool paired =
+            kKv4 && __shfl_xor_sync(0xffffffffu, slot, kLanes) == (slot ^ 1) && slot >= 0;
+        const float *g = weights[kind == 0 ? 0 : 1];
+
+        // The rows of the next kAhead heads are on their way (a row that is not
+        // there counts as zeros).
+        constexpr int kAhead = kKv4 ? 2 : kRopeAheadBytes / sizeof(T);
+        Chunk<T, 4> ahead[kAhead][2];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) y[i] = x[i] * lift;
-            mean = mean_square<kLanes>(y) + p.eps * lift * lift;
-            if (w) {
+        for (int i = 0; i < kAhead; ++i) {
 #pragma unroll
-                for (int i = 0; i < 16; ++i) x[i] = y[i];
+            for (int w = 0; w < Chunk<T, 4>::kWords; ++w) ahead[i][0].w[w] = ahead[i][1].w[w] = 0;
+            if (live && i < count) {
+                ahead[i][0].load(src + i * D + 4 * c0);
+                ahead[i][1].load(src + i * D + 4 * c1);
             }
         }
-        if (on && w) {
-            const float rms = rsqrtf(mean);
-            float g[16];
-            load8(w + 8 * c0, g);
-            load8(w + 8 * c1, g + 8);
+        src += kAhead * D;
+#pragma unroll 1
+        for (int k0 = 0; k0 < count; k0 += kAhead)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) x[i] *= rms * g[i];
-        }
-        if (on && rotates) {
-            float c[8], s[8];
-            const float *row = p.cos_sin + pos * p.rot + 8 * j;
-            load8(row, c);
-            load8(row + p.rot / 2, s);
-            if (p.interleaved) {
+        for (int i0 = 0; i0 < kAhead; ++i0) {
+            if (k0 + i0 >= count) break;
+            F2 x[4];
+            ahead[i0][0].to_f32(&x[0].x);
+            ahead[i0][1].to_f32(&x[2].x);
+            if (live && k0 + i0 + kAhead < count) {
+                ahead[i0][0].load(src + 4 * c0);
+                ahead[i0][1].load(src + 4 * c1);
+            }
+            src += D;
+            if (norm) {
+                float mean = mean_square<kLanes>(x) + p.eps;
+                // Squares that leave fp32 (|x| beyond 2^60, or below 2^-50 under an
+                // eps that does not cover it) are taken of x 2^-96 or x 2^96 instead.
+                const float lift = mean > 0x1p125f ? 0x1p-96f : mean < 0x1p-100f ? 0x1p96f : 1.0f;
+                if (__any_sync(0xffffffffu, lift != 1.0f)) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float a = x[2 * i], b = x[2 * i + 1];
-                    x[2 * i] = a * c[i] - b * s[i];
-                    x[2 * i + 1] = b * c[i] + a * s[i];
+                    for (int i = 0; i < 4; ++i) x[i] = mul2(x[i], F2{lift, lift});
+                    mean = mean_square<kLanes>(x) + p.eps * lift * lift;
                 }
-            } else {
+                const float rms = rsqrtf(mean);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float a = x[i], b = x[8 + i];
-                    x[i] = a * c[i] - b * s[i];
-                    x[8 + i] = b * c[i] + a * s[i];
+                for (int i = 0; i < 4; i += 2) {
+                    const float4 v = *reinterpret_cast<const float4 *>(g + 4 * (i ? c1 : c0));
+                    x[i] = mul2(mul2(x[i], F2{rms, rms}), F2{v.x, v.y});
+                    x[i + 1] = mul2(mul2(x[i + 1], F2{rms, rms}), F2{v.z, v.w});
                 }
             }
-        }
-        if (is_q || !p.k_cache) {
-            if (on) {
-                T *dst = is_q ? static_cast<T *>(p.q_out) + (t * p.Hq + h) * D
-                              : static_cast<T *>(p.k_out) + (t * p.Hkv + h - p.Hq) * D;
-                store8(dst + 8 * c0, x);
-                store8(dst + 8 * c1, x + 8);
+            if (turn) {
+                if (p.interleaved) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float cc = i & 1 ? c[i / 2].y : c[i / 2].x;
+                        const float ss = i & 1 ? s[i / 2].y : s[i / 2].x;
+                        x[i] = F2{x[i].x * cc - x[i].y * ss, x[i].y * cc + x[i].x * ss};
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const F2 a = x[i], b = x[2 + i];
+                        x[i] = sub2(mul2(a, c[i]), mul2(b, s[i]));
+                        x[2 + i] = fma2(b, c[i], mul2(a, s[i]));
+                    }
+                }
             }
-            on = false;
-        }
-        int64_t slot = -1;
-        if (on) slot = append_slot(p, t, pos, j == 0 && !is_v ? p.err_flag : nullptr);
-        const int hk = is_v ? h - p.Hq - p.Hkv : h - p.Hq;
-        const int64_t page = slot < 0 ? 0 : (slot >> 4) * p.Hkv + hk;
-        const int o = static_cast<int>(slot & 15);
-        if (slot >= 0 && !XS_BOUNDS(page >= 0 && page < p.num_blocks * p.Hkv, p.err_flag)) slot = -1;
-        uint8_t *cache = static_cast<uint8_t *>(is_v ? p.v_cache : p.k_cache);
-        if (!p.kv4) {
-            if (slot >= 0) {
-                T *dst = reinterpret_cast<T *>(cache) + (page * 16 + o) * D;
-                store8(dst + 8 * c0, x);
-                store8(dst + 8 * c1, x + 8);
+            Chunk<T, 4> y0, y1;
+            y0.from_f32(&x[0].x);
+            y1.from_f32(&x[2].x);
+            if (!kKv4 || !paged) {
+                if (writes) {
+                    y0.store(dst + 4 * c0);
+                    y1.store(dst + 4 * c1);
+                }
+                dst += step;
+                continue;
             }
-            continue;
-        }
-        // 4 bits: the extremes of the row's chunks meet in shared memory (a
-        // group's four chunks are not always the lanes of one row's half).
+            if constexpr (kKv4) {
+                y0.to_f32(&x[0].x);
+                y1.to_f32(&x[2].x);
+                uint32_t key[2] = {kv4_key4(y0.w[0], y0.w[1]), kv4_key4(y1.w[0], y1.w[1])};
+                if (kind == 2) {        // the lane's chunks are neighbours: four lanes a group
+                    key[0] = max(key[0], key[1]);
+                    key[0] = max(key[0], __shfl_xor_sync(0xffffffffu, key[0], 1));
+                    key[0] = max(key[0], __shfl_xor_sync(0xffffffffu, key[0], 2));
+                    key[1] = key[0];
+                } else {                // they meet in shared memory
+                    uint32_t *row_keys = keys[warp][lane / kLanes];
+                    __syncwarp();
+                    row_keys[c0] = key[0];
+                    row_keys[c1] = key[1];
+                    __syncwarp();
 #pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] = Elem<T>::to_f32(Elem<T>::from_f32(x[i]));
-        uint32_t m0 = 0, m1 = 0;
+                    for (int u = 0; u < 2; ++u) {
+                        const uint4 *k4 = reinterpret_cast<const uint4 *>(row_keys + ((u ? c1 : c0) & ~7));
+                        const uint4 a = k4[0], b = k4[1];
+                        key[u] = max(max(max(a.x, a.y), max(a.z, a.w)), max(max(b.x, b.y), max(b.z, b.w)));
+                    }
+                }
+                float scale[2];
+                uint32_t half[2];       // four codes each
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            m0 = max(m0, kv4_key(x[i]));
-            m1 = max(m1, kv4_key(x[8 + i]));
-        }
-        uint32_t *row_keys = keys[warp][lane / kLanes];
-        __syncwarp();
-        row_keys[c0] = m0;
-        row_keys[c1] = m1;
-        __syncwarp();
-        if (slot >= 0) {
-            uint8_t *dst = cache + page * kv4_page_bytes(D);
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const int ch = u ? c1 : c0;
-                const uint32_t *k4 = row_keys + (ch & ~3);
-                const float s = kv4_scale(max(max(k4[0], k4[1]), max(k4[2], k4[3])));
-                kv4_store_chunk<D>(dst, is_v, o, ch, kv4_pack8(x + 8 * u, s), s);
+                for (int u = 0; u < 2; ++u) {
+                    scale[u] = kv4_scale(key[u]);
+                    half[u] = kv4_pack4(&x[2 * u].x, scale[u]);
+                }
+                // The word (8 dims) this lane stores: its own two chunks, or, of
+                // split halves, the first chunk's with the next lane's, or the
+                // second's with the lane before's.
+                uint32_t word = half[0] | half[1] << 16;
+                const uint32_t other = __shfl_xor_sync(0xffffffffu, j & 1 ? half[0] : half[1], 1);
+                int ch = j;
+                if (kind == 1 && halves) {
+                    word = j & 1 ? other | half[1] << 16 : half[0] | other << 16;
+                    ch = (j & 1 ? c1 : c0) >> 1;
+                }
+                const float word_scale = kind == 1 && halves && (j & 1) ? scale[1] : scale[0];
+                const uint32_t theirs = __shfl_xor_sync(0xffffffffu, word, kLanes);
+                if (writes) {
+                    if (kind == 2 && paired)
+                        kv4_store_pair<D>(page, o, ch, word, theirs, word_scale);
+                    else
+                        kv4_store_chunk<D>(page, kind == 2, o, ch, word, word_scale);
+                }
+                page += kv4_page_bytes(D);
             }
         }
     }
@@ -251,21 +410,29 @@ bool strided_ok(const void *ptr, int64_t stride, int eb) {
 
 int launch(RopeParams &p, int D, int dtype, cudaStream_t stream) {
     p.rows_per_token = p.Hq + p.Hkv + (p.k_cache ? p.Hkv : 0);
-    const int rows_per_cta = kRopeThreads / (D / 16);
-    const int64_t want =
-        (static_cast<int64_t>(p.T) * p.rows_per_token + rows_per_cta - 1) / rows_per_cta;
-    const int grid = static_cast<int>(want < (1 << 20) ? want : (1 << 20));
-    if (dtype == XS_F32) {
-        if (D == 128)
-            qk_norm_rope_kernel<float, 128><<<grid, kRopeThreads, 0, stream>>>(p);
-        else
-            qk_norm_rope_kernel<float, 64><<<grid, kRopeThreads, 0, stream>>>(p);
-    } else {
-        if (D == 128)
-            qk_norm_rope_kernel<__nv_bfloat16, 128><<<grid, kRopeThreads, 0, stream>>>(p);
-        else
-            qk_norm_rope_kernel<__nv_bfloat16, 64><<<grid, kRopeThreads, 0, stream>>>(p);
-    }
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return XS_EDEVICE;
+    // Runs as long as leave kRopeWarpsPerSm warps for every SM, of kRopeRun heads at most.
+    const int rows = 256 / D;   // tokens of a warp
+    const int64_t blocks = (static_cast<int64_t>(p.T) + rows - 1) / rows;
+    const int64_t all = blocks * p.rows_per_token, least = static_cast<int64_t>(sms) * kRopeWarpsPerSm;
+    p.run = static_cast<int>(all / least < 1 ? 1 : all / least > kRopeRun ? kRopeRun : all / least);
+    const int64_t items = blocks * ((p.rows_per_token + p.run - 1) / p.run);
+    const int64_t want = (items + kRopeThreads / 32 - 1) / (kRopeThreads / 32);
+    if (want > INT_MAX) return XS_EUNSUPPORTED;
+    const int grid = static_cast<int>(want);
+    auto go = [&](auto kernel) { kernel<<<grid, kRopeThreads, 0, stream>>>(p); };
+    if (dtype == XS_F32)
+        D == 128 ? go(qk_norm_rope_kernel<float, 128, false>)
+                 : go(qk_norm_rope_kernel<float, 64, false>);
+    else if (p.kv4)
+        D == 128 ? go(qk_norm_rope_kernel<__nv_bfloat16, 128, true>)
+                 : go(qk_norm_rope_kernel<__nv_bfloat16, 64, true>);
+    else
+        D == 128 ? go(qk_norm_rope_kernel<__nv_bfloat16, 128, false>)
+                 : go(qk_norm_rope_kernel<__nv_bfloat16, 64, false>);
     return launch_status();
 }
 

@@ -11,14 +11,98 @@
 // Every result is the same on every run: entries are ranked by scans over
 // the caller's order or over the block ids, never by the order in which
 // atomics arrive.
+//
+// The integer work is a few kilobytes to a few megabytes and bound by latency:
+// one launch each, whose phases are separated by barriers of one thread-block
+// cluster (a single CTA for a small pool).  Releasing and compacting rank the
+// block ids: each CTA of the cluster has a contiguous part of them, each warp
+// of it a contiguous part of that, which it counts, then (after the counts
+// have met in shared memory, across the cluster) writes in order.
 #include <climits>
+
+#include <cooperative_groups.h>
 
 #include "xs_common.cuh"
 
 namespace xs {
 namespace {
 
+namespace cg = cooperative_groups;
+
 constexpr int kShareThreads = 1024;
+constexpr int kShareWarps = kShareThreads / 32;
+constexpr int kShareCluster = 8;
+constexpr int64_t kShareSmall = 4096;   // block ids, and table entries, of a single CTA
+
+// One warp's part [lo, hi) of [0, n), cut over the cluster's CTAs and warps.
+struct Part {
+    int64_t lo, hi;
+};
+__device__ __forceinline__ Part warp_part(int64_t n, int rank, int ranks) {
+    const int warps = blockDim.x >> 5;
+    const int64_t w = static_cast<int64_t>(rank) * warps + (threadIdx.x >> 5);
+    const int64_t all = static_cast<int64_t>(ranks) * warps;
+    const int64_t per = ((n + all - 1) / all + 31) / 32 * 32;
+    return Part{min(w * per, n), min(w * per + per, n)};
+}
+
+// How many of the warp's part satisfy pred; every lane gets the count.
+template <typename F> __device__ __forceinline__ int count_part(const Part &part, F &&pred) {
+    const int lane = threadIdx.x & 31;
+    int count = 0;
+#pragma unroll 4
+    for (int64_t i = part.lo; i < part.hi; i += 32)
+        count += __popc(__ballot_sync(0xffffffffu, i + lane < part.hi && pred(i + lane)));
+    return count;
+}
+// put(k, i) for the k-th (from `at` on) element i of the part that satisfies pred.
+template <typename F, typename P>
+__device__ __forceinline__ void write_part(const Part &part, int64_t at, F &&pred, P &&put) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll 4
+    for (int64_t i = part.lo; i < part.hi; i += 32) {
+        const bool yes = i + lane < part.hi && pred(i + lane);
+        const uint32_t all = __ballot_sync(0xffffffffu, yes);
+        if (yes) put(at + __popc(all & ((1u << lane) - 1)), i + lane);
+        at += __popc(all);
+    }
+}
+
+// Counts of every warp of the cluster, in order.
+struct ShareCounts {
+    int of[kShareCluster * kShareWarps];
+};
+// The sum before this warp, and of all; `mine` alike in the warp's lanes.
+// Synchronises the cluster.
+__device__ __forceinline__ int64_t cluster_scan(cg::cluster_group &cluster, ShareCounts &counts,
+                                                int mine, int64_t *total) {
+    const int rank = cluster.block_rank(), ranks = cluster.num_blocks();
+    const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
+    const int me = rank * warps + (threadIdx.x >> 5);
+    if (ranks == 1) {
+        if (lane == 0) counts.of[me] = mine;
+        __syncthreads();
+    } else {
+        if (lane < ranks) cluster.map_shared_rank(&counts, lane)->of[me] = mine;
+        cluster.sync();
+    }
+    // Block ids, so also their counts, fit 31 bits.
+    int before = 0, all = 0;
+    for (int i = lane; i < ranks * warps; i += 32) {
+        const int v = counts.of[i];
+        all += v;
+        if (i < me) before += v;
+    }
+    *total = __reduce_add_sync(0xffffffffu, all);
+    return __reduce_add_sync(0xffffffffu, before);
+}
+// All threads of the launch, and what they wrote.
+__device__ __forceinline__ void launch_sync(cg::cluster_group &cluster) {
+    if (cluster.num_blocks() == 1)
+        __syncthreads();
+    else
+        cluster.sync();
+}
 
 // Exclusive sum of v over the block's threads; `total` gets the sum.
 __device__ __forceinline__ int block_scan(int v, int *total, int *sm /* 33 ints */) {
@@ -130,6 +214,7 @@ __global__ void __launch_bounds__(kShareThreads)
             const int32_t *from = tables + static_cast<int64_t>(row_from[k]) * max_blocks;
             int32_t *to = tables + static_cast<int64_t>(row_to[k]) * max_blocks;
             const int full = row_len[k] / bs;
+#pragma unroll 4
             for (int col = lane; col < max_blocks; col += 32) {
                 int32_t id = -1;
                 if (col < full) {
@@ -151,16 +236,19 @@ __global__ void __launch_bounds__(kShareThreads)
     if (threadIdx.x == 0) *free_top = top - min(popped, top);
 }
 
-// One CTA.  A block whose count falls below zero is marked by that (-1) until
-// the scan over the block ids has pushed it.
+// A block whose count falls below zero is marked by that until the scan over
+// the block ids has pushed it.
 __global__ void __launch_bounds__(kShareThreads)
     block_release_kernel(const int32_t *__restrict__ seq_ids, int n, int32_t *tables,
                          int max_blocks, int32_t *lens, int B, int bs, int32_t *free_stack,
                          int32_t *free_top, int64_t capacity, int32_t *extra_refs,
                          int64_t num_blocks, int *err_flag) {
-    __shared__ int sm[33];
-    const int warp = threadIdx.x >> 5, warps = blockDim.x >> 5, lane = threadIdx.x & 31;
-    for (int k = warp; k < n; k += warps) {
+    __shared__ ShareCounts counts;
+    cg::cluster_group cluster = cg::this_cluster();
+    const int rank = cluster.block_rank(), ranks = cluster.num_blocks();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t top = *free_top;
+    for (int k = rank + warp * ranks; k < n; k += ranks * static_cast<int>(blockDim.x >> 5)) {
         const int b = seq_ids[k];
         if (b < 0 || b >= B) {
             if (lane == 0) raise_flag(err_flag, XS_FLAG_BAD_SLOT);
@@ -172,6 +260,7 @@ __global__ void __launch_bounds__(kShareThreads)
         if (len < 0) continue;
         int32_t *row = tables + static_cast<int64_t>(b) * max_blocks;
         const int pages = pages_of(len, bs, max_blocks);
+#pragma unroll 4
         for (int col = lane; col < max_blocks; col += 32) {
             if (col < pages) {
                 const int32_t id = row[col];
@@ -183,103 +272,141 @@ __global__ void __launch_bounds__(kShareThreads)
             row[col] = -1;
         }
     }
-    __syncthreads();
+    launch_sync(cluster);
     // Highest id first, so that the lowest is the next one taken.
-    int64_t at = *free_top;
-    for (int64_t base = num_blocks; base > 0; base -= blockDim.x) {
-        const int64_t id = base - 1 - threadIdx.x;
-        const bool freed = id >= 0 && *static_cast<volatile int32_t *>(extra_refs + id) < 0;
-        int count;
-        const int64_t idx = at + block_scan(freed, &count, sm);
-        if (freed) {
-            extra_refs[id] = 0;
-            if (idx < capacity)
-                free_stack[idx] = static_cast<int32_t>(id);
-            else
-                raise_flag(err_flag, XS_FLAG_POOL_EMPTY);
-        }
-        at += count;
-    }
-    if (threadIdx.x == 0) *free_top = static_cast<int32_t>(min(at, capacity));
+    const Part part = warp_part(num_blocks, rank, ranks);
+    auto freed = [&](int64_t i) { return __ldcg(extra_refs + (num_blocks - 1 - i)) < 0; };
+    int64_t total;
+    const int64_t before = cluster_scan(cluster, counts, count_part(part, freed), &total);
+    write_part(part, top + before, freed, [&](int64_t k, int64_t i) {
+        const int64_t id = num_blocks - 1 - i;
+        if (k < capacity)
+            free_stack[k] = static_cast<int32_t>(id);
+        else
+            raise_flag(err_flag, XS_FLAG_POOL_EMPTY);
+        extra_refs[id] = 0;
+    });
+    if (rank == 0 && threadIdx.x == 0) *free_top = static_cast<int32_t>(min(top + total, capacity));
 }
 
-// One CTA.  remap first marks the live blocks (0), then holds the new ids.
+// remap first marks the live blocks (0), then holds the new ids.
 __global__ void __launch_bounds__(kShareThreads)
     block_compact_kernel(const int32_t *tables, int32_t *tables_out, int max_blocks,
                          const int32_t *__restrict__ lens, int B, int bs, const int32_t *extra,
                          int32_t *extra_out, int32_t *free_stack, int32_t *free_top,
                          int64_t num_blocks, int32_t *remap, int64_t *moves, int32_t *n_moves,
                          int *err_flag) {
-    __shared__ int sm[33];
-    const int warp = threadIdx.x >> 5, warps = blockDim.x >> 5, lane = threadIdx.x & 31;
-    for (int64_t id = threadIdx.x; id < num_blocks; id += blockDim.x) remap[id] = -1;
-    __syncthreads();
-    for (int b = warp; b < B; b += warps) {
+    __shared__ ShareCounts counts[3];
+    cg::cluster_group cluster = cg::this_cluster();
+    const int rank = cluster.block_rank(), ranks = cluster.num_blocks();
+    const int64_t thread = static_cast<int64_t>(rank) * blockDim.x + threadIdx.x;
+    const int64_t threads = static_cast<int64_t>(ranks) * blockDim.x;
+    const int64_t warp = thread >> 5, warps = threads >> 5;
+    const int lane = threadIdx.x & 31;
+    for (int64_t id = thread; id < num_blocks; id += threads) remap[id] = -1;
+    launch_sync(cluster);
+    // A warp takes 128 columns of a row at a time.
+    const int pieces = (max_blocks + 127) / 128;
+    for (int64_t piece = warp; piece < static_cast<int64_t>(B) * pieces; piece += warps) {
+        const int b = static_cast<int>(piece / pieces), col0 = static_cast<int>(piece % pieces) * 128;
         const int n = lens[b];
-        if (n > 0 && (static_cast<int64_t>(n) + bs - 1) / bs > max_blocks && lane == 0)
+        if (col0 == 0 && n > 0 && (static_cast<int64_t>(n) + bs - 1) / bs > max_blocks && lane == 0)
             raise_flag(err_flag, XS_FLAG_BAD_LEN);
         const int pages = pages_of(n, bs, max_blocks);
-        for (int col = lane; col < pages; col += 32) {
-            const int32_t id = tables[static_cast<int64_t>(b) * max_blocks + col];
-            if (id >= 0 && id < num_blocks)
-                remap[id] = 0;
+        int32_t id[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int col = col0 + 32 * u + lane;
+            id[u] = col < pages ? tables[static_cast<int64_t>(b) * max_blocks + col] : 0;
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            if (col0 + 32 * u + lane >= pages) continue;
+            if (id[u] >= 0 && id[u] < num_blocks)
+                remap[id[u]] = 0;
             else
                 raise_flag(err_flag, XS_FLAG_BAD_BLOCK);
         }
     }
-    __syncthreads();
-    int64_t live = 0;
-    int count;
-    for (int64_t base = 0; base < num_blocks; base += blockDim.x) {
-        const int64_t id = base + threadIdx.x;
-        block_scan(id < num_blocks && remap[id] == 0, &count, sm);
-        live += count;
-    }
-    int64_t movers = 0, holes = 0;
-    for (int64_t base = 0; base < num_blocks; base += blockDim.x) {
-        const int64_t id = base + threadIdx.x;
-        const bool in = id < num_blocks, used = in && remap[id] == 0;
-        const bool mover = used && id >= live, hole = in && !used && id < live;
-        int64_t k = movers + block_scan(mover, &count, sm);
-        movers += count;
-        if (mover) moves[2 * k] = id;
-        k = holes + block_scan(hole, &count, sm);
-        holes += count;
-        if (hole) moves[2 * k + 1] = id;
-    }
-    __syncthreads();
-    for (int64_t id = threadIdx.x; id < live; id += blockDim.x)
-        if (remap[id] == 0) remap[id] = static_cast<int32_t>(id);
-    for (int64_t k = threadIdx.x; k < num_blocks / 2; k += blockDim.x) {
+    launch_sync(cluster);
+    const Part part = warp_part(num_blocks, rank, ranks);
+    auto used = [&](int64_t id) { return __ldcg(remap + id) == 0; };
+    int64_t live, movers, holes;
+    cluster_scan(cluster, counts[0], count_part(part, used), &live);
+    auto mover = [&](int64_t id) { return id >= live && used(id); };
+    auto hole = [&](int64_t id) { return id < live && !used(id); };
+    const int64_t m0 = cluster_scan(cluster, counts[1], count_part(part, mover), &movers);
+    const int64_t h0 = cluster_scan(cluster, counts[2], count_part(part, hole), &holes);
+    write_part(part, m0, mover, [&](int64_t k, int64_t id) { moves[2 * k] = id; });
+    write_part(part, h0, hole, [&](int64_t k, int64_t id) { moves[2 * k + 1] = id; });
+    launch_sync(cluster);
+    for (int64_t id = thread; id < live; id += threads)
+        if (__ldcg(remap + id) == 0) remap[id] = static_cast<int32_t>(id);
+    for (int64_t k = thread; k < num_blocks / 2; k += threads) {
         if (k < movers) {
-            const int64_t src = moves[2 * k], dst = moves[2 * k + 1];
+            const int64_t src = __ldcg(moves + 2 * k), dst = __ldcg(moves + 2 * k + 1);
             remap[src] = static_cast<int32_t>(dst);
             extra_out[dst] = extra[src];
         } else {
             moves[2 * k] = moves[2 * k + 1] = -1;
         }
     }
-    __syncthreads();
-    for (int64_t id = threadIdx.x; id < num_blocks; id += blockDim.x) {
+    launch_sync(cluster);
+    for (int64_t id = thread; id < num_blocks; id += threads) {
         if (id >= live)
             extra_out[id] = 0;
-        else if (remap[id] >= 0)
+        else if (__ldcg(remap + id) == id)      // (a hole's came with its mover)
             extra_out[id] = extra[id];
         if (id < num_blocks - live) free_stack[id] = static_cast<int32_t>(num_blocks - 1 - id);
     }
-    for (int b = warp; b < B; b += warps) {
+    for (int64_t piece = warp; piece < static_cast<int64_t>(B) * pieces; piece += warps) {
+        const int b = static_cast<int>(piece / pieces), col0 = static_cast<int>(piece % pieces) * 128;
         const int pages = pages_of(lens[b], bs, max_blocks);
-        for (int col = lane; col < max_blocks; col += 32) {
-            const int64_t e = static_cast<int64_t>(b) * max_blocks + col;
-            int32_t id = tables[e];
-            if (col < pages && id >= 0 && id < num_blocks) id = remap[id];
-            tables_out[e] = id;
+        int32_t id[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int col = col0 + 32 * u + lane;
+            id[u] = col < max_blocks ? tables[static_cast<int64_t>(b) * max_blocks + col] : 0;
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int col = col0 + 32 * u + lane;
+            if (col < pages && id[u] >= 0 && id[u] < num_blocks) id[u] = __ldcg(remap + id[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int col = col0 + 32 * u + lane;
+            if (col < max_blocks) tables_out[static_cast<int64_t>(b) * max_blocks + col] = id[u];
         }
     }
-    if (threadIdx.x == 0) {
+    if (thread == 0) {
         *free_top = static_cast<int32_t>(num_blocks - live);
         *n_moves = static_cast<int32_t>(movers);
     }
+}
+
+// Launches `kernel` as one cluster, or as a single CTA if the work is small
+// (a cluster's barriers cost more than it saves: releasing 4 sequences of a
+// pool of 100 blocks takes 3.5 us as a CTA of 8 warps, 6 us as a cluster; at
+// 8K blocks and 33K table entries compacting takes 31 us as one CTA, 16 us as
+// a cluster).
+template <typename K, typename... A>
+int launch_share(K kernel, int64_t work, cudaStream_t stream, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(work <= kShareSmall ? 1 : kShareCluster);
+    cfg.blockDim = dim3(work <= kShareSmall / 4 ? kShareThreads / 4 : kShareThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = kShareCluster;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = work <= kShareSmall ? 0 : 1;
+    if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) {
+        cudaGetLastError();
+        return XS_ELAUNCH;
+    }
+    return launch_status();
 }
 
 constexpr int kCopyThreads = 256, kCopyUnroll = 8;
@@ -337,7 +464,8 @@ extern "C" int xs_block_fork(const int32_t *parents, const int32_t *children, in
         num_blocks > INT_MAX)
         return XS_ESHAPE;
     if (n == 0) return XS_OK;
-    xs::block_fork_kernel<<<1, xs::kShareThreads, 0, stream>>>(
+    const int threads = n <= 8 ? xs::kShareThreads / 4 : xs::kShareThreads;
+    xs::block_fork_kernel<<<1, threads, 0, stream>>>(
         parents, children, n, block_tables, max_blocks_per_seq, context_lens, B, block_size,
         free_stack, free_top, extra_refs, num_blocks, copies, err_flag);
     return xs::launch_status();
@@ -354,10 +482,11 @@ extern "C" int xs_block_release(const int32_t *seq_ids, int n, int32_t *block_ta
         num_blocks < 0 || num_blocks > INT_MAX)
         return XS_ESHAPE;
     if (n == 0) return XS_OK;
-    xs::block_release_kernel<<<1, xs::kShareThreads, 0, stream>>>(
-        seq_ids, n, block_tables, max_blocks_per_seq, context_lens, B, block_size, free_stack,
-        free_top, stack_capacity, extra_refs, num_blocks, err_flag);
-    return xs::launch_status();
+    const int64_t entries = static_cast<int64_t>(n) * max_blocks_per_seq;
+    return xs::launch_share(xs::block_release_kernel, num_blocks > entries ? num_blocks : entries,
+                            stream, seq_ids, n, block_tables, max_blocks_per_seq, context_lens, B,
+                            block_size, free_stack, free_top, stack_capacity, extra_refs,
+                            num_blocks, err_flag);
 }
 
 extern "C" int xs_block_compact(const int32_t *block_tables, int32_t *block_tables_out,
@@ -372,11 +501,11 @@ extern "C" int xs_block_compact(const int32_t *block_tables, int32_t *block_tabl
     if (B < 0 || max_blocks_per_seq < 0 || block_size <= 0 || num_blocks < 0 ||
         num_blocks > INT_MAX)
         return XS_ESHAPE;
-    xs::block_compact_kernel<<<1, xs::kShareThreads, 0, stream>>>(
-        block_tables, block_tables_out, max_blocks_per_seq, context_lens, B, block_size,
-        extra_refs, extra_refs_out, free_stack, free_top, num_blocks, remap, moves, n_moves,
-        err_flag);
-    return xs::launch_status();
+    const int64_t entries = static_cast<int64_t>(B) * max_blocks_per_seq;
+    return xs::launch_share(xs::block_compact_kernel, num_blocks > entries ? num_blocks : entries,
+                            stream, block_tables, block_tables_out, max_blocks_per_seq,
+                            context_lens, B, block_size, extra_refs, extra_refs_out, free_stack,
+                            free_top, num_blocks, remap, moves, n_moves, err_flag);
 }
 
 extern "C" int xs_block_copy(void *k_pools, void *v_pools, int layers, int64_t layer_stride_bytes,

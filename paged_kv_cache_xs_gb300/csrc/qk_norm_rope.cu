@@ -38,7 +38,7 @@ namespace xs {
 namespace {
 
 constexpr int kRopeThreads = 128;
-constexpr int kRopeCtas = 8;        // on an SM
+constexpr int kRopeCtas = 6;        // on an SM
 constexpr int kRopeAheadBytes = 8;  // rows of a lane on their way, times the size of a value
 constexpr int kRopeRun = 16;
 constexpr int kRopeWarpsPerSm = 24;
@@ -203,6 +203,40 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas)
     const int run_begin = static_cast<int>(item - block * runs) * p.run;
     const int run_end = min(run_begin + p.run, p.rows_per_token);
     const int64_t t = block * kRows + lane / kLanes;    // past T for an item past the last
+    // A lane's chunks of a rotated row.
+    const bool rotates = j < p.rot / 8;
+    const bool halves = rotates && !p.interleaved;
+    const int r0 = halves ? j : 2 * j, r1 = halves ? p.rot / 8 + j : 2 * j + 1;
+    // The rows of the next kAhead heads are on their way (a row that is not
+    // there counts as zeros): q's, k's or v's, the run's first ones before
+    // anything else is known of the token.
+    constexpr int kAhead = kKv4 ? 2 : kRopeAheadBytes / sizeof(T);
+    Chunk<T, 4> ahead[kAhead][2];
+    auto fetch = [&](int kind, int h, int count) {
+        const int c0 = kind < 2 ? r0 : 2 * j, c1 = kind < 2 ? r1 : 2 * j + 1;
+        const T *src = kind == 0   ? static_cast<const T *>(p.q) + t * p.q_stride
+                       : kind == 1 ? static_cast<const T *>(p.k) + t * p.k_stride
+                                   : static_cast<const T *>(p.v) + t * p.v_stride;
+        src += h * D;
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+#pragma unroll
+            for (int w = 0; w < Chunk<T, 4>::kWords; ++w) ahead[i][0].w[w] = ahead[i][1].w[w] = 0;
+            if (t < p.T && i < count) {
+                ahead[i][0].load(src + i * D + 4 * c0);
+                ahead[i][1].load(src + i * D + 4 * c1);
+            }
+        }
+        return src + kAhead * D;
+    };
+    auto first_of = [&](int kind) { return kind == 0 ? 0 : kind == 1 ? p.Hq : p.Hq + p.Hkv; };
+    auto count_of = [&](int kind) {     // heads of the kind in the run
+        const int first = first_of(kind), last = kind == 0 ? p.Hq : min(first + p.Hkv, p.rows_per_token);
+        return min(run_end, last) - max(run_begin, first);
+    };
+    const int kind0 = run_begin < p.Hq ? 0 : run_begin < p.Hq + p.Hkv ? 1 : 2;
+    const T *src = fetch(kind0, run_begin - first_of(kind0), count_of(kind0));
+
     bool live = t < p.T;
     int64_t pos = 0;
     if (live) {
@@ -223,10 +257,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas)
     const int64_t page0 = slot < 0 ? 0 : (slot >> 4) * p.Hkv;
     const int o = static_cast<int>(slot & 15);
 
-    // The lane's chunks of a rotated row, and its cosines and sines.
-    const bool rotates = j < p.rot / 8;
-    const bool halves = rotates && !p.interleaved;
-    const int r0 = halves ? j : 2 * j, r1 = halves ? p.rot / 8 + j : 2 * j + 1;
+    // The lane's cosines and sines.
     F2 c[2], s[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) c[i] = F2{1.0f, 1.0f}, s[i] = F2{0.0f, 0.0f};
@@ -244,17 +275,12 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas)
 
     // q, then k, then v heads of the run.
 #pragma unroll 1
-    for (int kind = 0; kind < 3; ++kind) {
-        const int first = kind == 0 ? 0 : kind == 1 ? p.Hq : p.Hq + p.Hkv;
-        const int last = kind == 0 ? p.Hq : min(first + p.Hkv, p.rows_per_token);
-        const int begin = max(run_begin, first), count = min(run_end, last) - begin;
-        if (count <= 0) continue;
-        const int h = begin - first;
+    for (int kind = kind0; kind < 3; ++kind) {
+        const int count = count_of(kind);
+        if (count <= 0) break;
+        const int h = max(run_begin - first_of(kind), 0);
         const int c0 = kind < 2 ? r0 : 2 * j, c1 = kind < 2 ? r1 : 2 * j + 1;
-        const T *src = kind == 0   ? static_cast<const T *>(p.q) + t * p.q_stride
-                       : kind == 1 ? static_cast<const T *>(p.k) + t * p.k_stride
-                                   : static_cast<const T *>(p.v) + t * p.v_stride;
-        src += h * D;
+        if (kind != kind0) src = fetch(kind, h, count);
         const bool paged = kind > 0 && p.k_cache;
         const bool norm = kind == 0 ? p.q_weight != nullptr : kind == 1 && p.k_weight != nullptr;
         const bool turn = kind < 2 && rotates;
@@ -278,20 +304,6 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas)
             kKv4 && __shfl_xor_sync(0xffffffffu, slot, kLanes) == (slot ^ 1) && slot >= 0;
         const float *g = weights[kind == 0 ? 0 : 1];
 
-        // The rows of the next kAhead heads are on their way (a row that is not
-        // there counts as zeros).
-        constexpr int kAhead = kKv4 ? 2 : kRopeAheadBytes / sizeof(T);
-        Chunk<T, 4> ahead[kAhead][2];
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-#pragma unroll
-            for (int w = 0; w < Chunk<T, 4>::kWords; ++w) ahead[i][0].w[w] = ahead[i][1].w[w] = 0;
-            if (live && i < count) {
-                ahead[i][0].load(src + i * D + 4 * c0);
-                ahead[i][1].load(src + i * D + 4 * c1);
-            }
-        }
-        src += kAhead * D;
 #pragma unroll 1
         for (int k0 = 0; k0 < count; k0 += kAhead)
 #pragma unroll
@@ -300,7 +312,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas)
             F2 x[4];
             ahead[i0][0].to_f32(&x[0].x);
             ahead[i0][1].to_f32(&x[2].x);
-            if (live && k0 + i0 + kAhead < count) {
+            if (t < p.T && k0 + i0 + kAhead < count) {
                 ahead[i0][0].load(src + 4 * c0);
                 ahead[i0][1].load(src + 4 * c1);
             }

@@ -73,14 +73,6 @@ __device__ __forceinline__ F2 mul2(F2 a, F2 b) {
         : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
     return r;
 }
-__device__ __forceinline__ F2 add2(F2 a, F2 b) {
-    F2 r;
-    asm("{\n .reg .b64 p, q, s;\n mov.b64 p, {%2, %3};\n mov.b64 q, {%4, %5};\n"
-        " add.rn.f32x2 s, p, q;\n mov.b64 {%0, %1}, s;\n}"
-        : "=f"(r.x), "=f"(r.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return r;
-}
 __device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
     F2 r;
     asm("{\n .reg .b64 p, q, s;\n mov.b64 p, {%2, %3};\n mov.b64 q, {%4, %5};\n"
@@ -90,20 +82,12 @@ __device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
     return r;
 }
 
-// d = A B + c, then d = A B + d, with rows 8..15 of A zero.
-__device__ __forceinline__ void mma_f16_first(float *d, uint32_t a0, uint32_t a2, uint32_t b0,
-                                              uint32_t b1, const float *c) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%5}, "
-        "{%7,%8}, {%9,%10,%11,%12};"
-        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-        : "r"(a0), "r"(0), "r"(a2), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
-}
-__device__ __forceinline__ void mma_f16(float *d, uint32_t a0, uint32_t a2, uint32_t b0,
-                                        uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%5}, "
-        "{%7,%8}, {%0,%1,%2,%3};"
+// d = A B + d
+__device__ __forceinline__ void mma_f16(float *d, const uint32_t *a, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(0), "r"(a2), "r"(b0), "r"(b1));
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ void mma_bf16(float *c, uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -182,10 +166,17 @@ __host__ __device__ constexpr int64_t partial_floats(int G, int D) {
 }
 
 template <int D> struct alignas(16) DecodeSmem {
-    uint8_t ring[kDecWarps][kStages][2][kv4_page_bytes(D)];  // K page, V page
+    // The pages on their way (K page, V page).  Between segments, when none are,
+    // the warps' values meet there (rows padded, for the banks).
+    union {
+        uint8_t ring[kDecWarps][kStages][2][kv4_page_bytes(D)];
+        float o[kDecWarps][8][D + 4];
+    };
     uint64_t full[kDecWarps][kStages];
-    uint4 q[D / 32][32];                // first operand of the logits: [group][lane]
-    float o[kDecWarps][8][D + 4];       // a warp's values; padded, for the banks
+    // The logits' first operand for each group, two steps of 16 dims, as a lane's
+    // four registers (rows 8 to 15 are zero), and what a head's sums start at.
+    uint4 q[D / 32][2][32];
+    float4 start_at[D / 32][8];
     float m[kDecWarps][8], l[kDecWarps][8];
     float weight[kDecThreads];
     int64_t scan[kDecWarps];
@@ -291,7 +282,7 @@ __device__ __forceinline__ void run_segment(const Kv4DecodeParams &p, DecodeSmem
 
     // q as the first operand: row g is head g (heads past G are zero); words
     // j = 0..3 of group c hold dims 32 c + 8 t + j and + j + 4.
-    float cinit[NG], to_log2;
+    float to_log2;
     {
         const bool head = g < p.G;
         const __nv_bfloat16 *q = p.q + (static_cast<int64_t>(b) * p.Hq + h0 + (head ? g : 0)) * D;
@@ -326,18 +317,15 @@ __device__ __forceinline__ void run_segment(const Kv4DecodeParams &p, DecodeSmem
             }
             s += __shfl_xor_sync(0xffffffffu, s, 1);
             s += __shfl_xor_sync(0xffffffffu, s, 2);
-            cinit[c] = s * -0x1p-21f;
-            if (warp == 0) sm.q[c][lane] = make_uint4(qf[0], qf[1], qf[2], qf[3]);
+            if (warp == 0) {
+                sm.q[c][0][lane] = make_uint4(qf[0], 0, qf[1], 0);
+                sm.q[c][1][lane] = make_uint4(qf[2], 0, qf[3], 0);
+                if (t == 0) sm.start_at[c][g] = make_float4(s * -0x1p-21f, s * -0x1p-21f, 0.0f, 0.0f);
+            }
         }
     }
     __syncthreads();
-    const uint32_t q0 = smem_addr(&sm.q[0][lane]);
-
-    // Four registers of zeros that the compiler takes for variables: it would
-    // set constants anew for every product.
-    float zero[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) asm volatile("mov.f32 %0, 0f00000000;" : "=f"(zero[k]));
+    const uint32_t q0 = smem_addr(&sm.q[0][0][lane]), s0 = smem_addr(&sm.start_at[0][g]);
 
     float m = 0.0f, l = 0.0f;   // head g: reference, and this lane's share of the sum
     bool fresh = true;
@@ -370,17 +358,19 @@ __device__ __forceinline__ void run_segment(const Kv4DecodeParams &p, DecodeSmem
         }
 #pragma unroll
         for (int c = 0; c < NG; ++c) {
-            uint32_t qf[4];
-            load_words<4>(qf, q0 + c * 512);
+            uint32_t qa[4], qb[4];
+            load_words<4>(qa, q0 + c * 1024);
+            load_words<4>(qb, q0 + c * 1024 + 512);
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 const uint32_t w = kw[u][c];
                 float s[4];
-                mma_f16_first(s, qf[0], qf[1], codes_f16(w, 0), codes_f16(w, 1), zero);
-                mma_f16(s, qf[2], qf[3], codes_f16(w, 2), codes_f16(w, 3));
+                load_words<4>(reinterpret_cast<uint32_t *>(s), s0 + c * 128);
+                mma_f16(s, qa, codes_f16(w, 0), codes_f16(w, 1));
+                mma_f16(s, qb, codes_f16(w, 2), codes_f16(w, 3));
                 const uint32_t a0 = ks[u][c / 2], a1 = ks[u][NG / 2 + c / 2];
                 const F2 z = c & 1 ? F2{bf_hi(a0), bf_hi(a1)} : F2{bf_lo(a0), bf_lo(a1)};
-                x[u] = fma2(z, add2(F2{s[0], s[1]}, F2{cinit[c], cinit[c]}), x[u]);
+                x[u] = fma2(z, F2{s[0], s[1]}, x[u]);
             }
         }
         x[0].x *= to_log2, x[0].y *= to_log2;
@@ -461,6 +451,7 @@ __device__ __forceinline__ void run_segment(const Kv4DecodeParams &p, DecodeSmem
     // as l = 0 under the lowest reference.
     l += __shfl_xor_sync(0xffffffffu, l, 1);
     l += __shfl_xor_sync(0xffffffffu, l, 2);
+    __syncthreads();    // all warps have read their last pages
     if (t == 0) {
         sm.m[warp][g] = fresh ? -3.0e38f : m;
         sm.l[warp][g] = l;
@@ -514,6 +505,7 @@ __device__ __forceinline__ void run_segment(const Kv4DecodeParams &p, DecodeSmem
         else
             *reinterpret_cast<float4 *>(part + x) = o;
     }
+    fence_proxy_async_shared();     // the rings go back to the bulk copies (after the next barrier)
 }
 
 // The partials of a segment that CTAs f .. last share, joined in order: CTA f

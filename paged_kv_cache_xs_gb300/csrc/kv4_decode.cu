@@ -51,13 +51,16 @@
 namespace xs {
 namespace {
 
-constexpr int kDecWarps = 4;
-constexpr int kDecThreads = kDecWarps * 32;
-constexpr int kDecCtasPerSm = 4;
+// Warps of a CTA, and CTAs on an SM (16 warps of 128 registers): small CTAs
+// where segments are many and often end, larger ones where a segment has many
+// CTAs and their partials are what the join waits for (one stream at 4K tokens:
+// 10.4 us with 8 warps, 11.5 us with 4; a 64-sequence step 49 us and 41 us).
+__host__ __device__ constexpr int dec_warps(bool few) { return few ? 8 : 4; }
+__host__ __device__ constexpr int ctas_per_sm(bool few) { return 16 / dec_warps(few); }
 constexpr int kMaxCtas = 1024;     // the workspace holds partials for so many
 constexpr int kSegmentCost = 16;   // pages
 constexpr int kMinShare = 16;      // pages
-constexpr int kFewSegments = 8;    // at least so many CTAs for each segment
+constexpr int kFewSegments = 8;    // few: at least so many (large) CTAs for each segment
 constexpr int kStages = 4;         // pages of a warp's ring
 constexpr uint64_t kWaitLimitNs = 4000000000ull;
 
@@ -165,7 +168,8 @@ __host__ __device__ constexpr int64_t partial_floats(int G, int D) {
     return (static_cast<int64_t>(G) * (D + 2) + 3) / 4 * 4;
 }
 
-template <int D> struct alignas(16) DecodeSmem {
+template <int D, bool kFew> struct alignas(16) DecodeSmem {
+    static constexpr int kDecWarps = dec_warps(kFew), kDecThreads = 32 * kDecWarps;
     // The pages on their way (K page, V page).  Between segments, when none are,
     // the warps' values meet there (rows padded, for the banks).
     union {
@@ -187,8 +191,9 @@ template <int D> struct alignas(16) DecodeSmem {
 };
 
 // Inclusive sum over the CTA's threads; *total gets the sum of all.
-template <int D>
-__device__ __forceinline__ int64_t cta_scan(int64_t v, int64_t *total, DecodeSmem<D> &sm) {
+template <int D, bool kFew>
+__device__ __forceinline__ int64_t cta_scan(int64_t v, int64_t *total, DecodeSmem<D, kFew> &sm) {
+    constexpr int kDecWarps = dec_warps(kFew);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -237,11 +242,11 @@ struct RingState {
 
 // Pages [a, e) of one segment: what the CTA's warps leave in shared memory is
 // joined and either written out (whole) or left as the CTA's partial `slot`.
-template <int D>
-__device__ __forceinline__ void run_segment(const Kv4DecodeParams &p, DecodeSmem<D> &sm,
+template <int D, bool kFew>
+__device__ __forceinline__ void run_segment(const Kv4DecodeParams &p, DecodeSmem<D, kFew> &sm,
                                             RingState &ring, int b, int hk, const Span &sp, int a,
                                             int e, bool whole, int slot) {
-    constexpr int NG = D / 32;
+    constexpr int NG = D / 32, kDecWarps = dec_warps(kFew), kDecThreads = 32 * kDecWarps;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
     const int h0 = hk * p.G;
     const int32_t *row = p.tables + static_cast<int64_t>(b) * p.max_blocks + sp.page0;
@@ -513,9 +518,10 @@ __device__ __forceinline__ void run_segment(const Kv4DecodeParams &p, DecodeSmem
 // once (an access to another CTA's fresh results takes about 1 us, so one
 // after the other is what a join must not do); each thread then follows its
 // own four values through them.
-template <int D>
-__device__ __noinline__ void join_partials(const Kv4DecodeParams &p, DecodeSmem<D> &sm, int b,
+template <int D, bool kFew>
+__device__ __noinline__ void join_partials(const Kv4DecodeParams &p, DecodeSmem<D, kFew> &sm, int b,
                                            int hk, int f, int last) {
+    constexpr int kDecThreads = 32 * dec_warps(kFew);
     const int G = p.G, floats = static_cast<int>(partial_floats(G, D)), chunks = floats / 4;
     float *buf = reinterpret_cast<float *>(sm.ring);
     const int room = static_cast<int>(sizeof(sm.ring) / (4 * floats));
@@ -578,11 +584,12 @@ __device__ __noinline__ void join_partials(const Kv4DecodeParams &p, DecodeSmem<
     }
 }
 
-template <int D>
-__global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm)
+template <int D, bool kFew>
+__global__ void __launch_bounds__(32 * dec_warps(kFew), ctas_per_sm(kFew))
     kv4_decode_kernel(const __grid_constant__ Kv4DecodeParams p) {
+    constexpr int kDecWarps = dec_warps(kFew), kDecThreads = 32 * kDecWarps;
     extern __shared__ __align__(16) uint8_t smem_raw[];
-    DecodeSmem<D> &sm = *reinterpret_cast<DecodeSmem<D> *>(smem_raw);
+    DecodeSmem<D, kFew> &sm = *reinterpret_cast<DecodeSmem<D, kFew> *>(smem_raw);
     if (threadIdx.x < kDecWarps * kStages) mbar_init(&sm.full[0][0] + threadIdx.x, 1);
     mbar_fence_init();
     __syncthreads();
@@ -591,7 +598,6 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm)
     // (one of them is this CTA's), or the length of its segments on the line.
     // The lengths of the first kDecThreads sequences stay in registers.
     const int64_t segments = static_cast<int64_t>(p.B) * p.Hkv;
-    const bool few = segments * kFewSegments <= gridDim.x;
     int pages0 = 0;
     int64_t total = 0;
     for (int base = 0; base < p.B; base += kDecThreads) {
@@ -603,20 +609,20 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm)
         total += all;
     }
     int64_t share, line = (total + static_cast<int64_t>(p.B) * kSegmentCost) * p.Hkv;
-    if (few) {
+    if constexpr (kFew) {
         const int64_t ctas = gridDim.x - segments;
         share = max((total * p.Hkv + ctas - 1) / ctas, static_cast<int64_t>(kMinShare));
     } else {
         share = max((line + gridDim.x - 1) / gridDim.x, static_cast<int64_t>(kMinShare));
     }
-    const int64_t target = few ? blockIdx.x : share * blockIdx.x;
+    const int64_t target = kFew ? blockIdx.x : share * blockIdx.x;
     if (threadIdx.x == 0) sm.b = -1;
     int64_t before = 0;
     for (int base = 0; base < p.B && before * p.Hkv <= target; base += kDecThreads) {
         const int b = base + threadIdx.x;
         const int pages = base ? (b < p.B ? span_of(p, b).pages : 0) : pages0;
         const int64_t units = b >= p.B ? 0
-                              : few    ? max((pages + share - 1) / share, int64_t(1))
+                              : kFew ? max((pages + share - 1) / share, int64_t(1))
                                        : pages + kSegmentCost;
         int64_t all;
         const int64_t end = (before + cta_scan(units, &all, sm)) * p.Hkv;
@@ -628,7 +634,7 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm)
             sm.start = s + hk * units;
             sm.share = share;
             sm.line = line;
-            if (few) {
+            if constexpr (kFew) {
                 const int j = static_cast<int>(target - sm.start), n = static_cast<int>(units);
                 const int piece = (pages + n - 1) / n;
                 sm.a = j * piece;
@@ -645,7 +651,7 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm)
         {
             const int b = sm.b, hk = sm.hk;
             const Span sp = span_of(p, b);
-            if (!few && threadIdx.x == 0) {
+            if (!kFew && threadIdx.x == 0) {
                 const int64_t s = sm.start, share = sm.share, lo = share * blockIdx.x;
                 const int64_t hi = min(lo + share, sm.line);
                 sm.a = static_cast<int>(min(max(lo - s, int64_t(0)), static_cast<int64_t>(sp.pages)));
@@ -656,13 +662,13 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm)
             __syncthreads();
             const int a = sm.a, e = sm.e;
             if (sp.pages == 0) {
-                if (few || sm.start >= sm.share * blockIdx.x) {
+                if (kFew || sm.start >= sm.share * blockIdx.x) {
                     __nv_bfloat16 *out = p.out + (static_cast<int64_t>(b) * p.Hq + hk * p.G) * D;
                     for (int x = threadIdx.x; x < p.G * D; x += kDecThreads)
                         out[x] = __float2bfloat16_rn(0.0f);
                 }
             } else if (a < e) {
-                run_segment<D>(p, sm, ring, b, hk, sp, a, e, a == 0 && e == sp.pages, a == 0);
+                run_segment<D, kFew>(p, sm, ring, b, hk, sp, a, e, a == 0 && e == sp.pages, a == 0);
             }
         }
         if (sm.a < sm.e && sm.f != sm.last) {   // a part: the last of its CTAs joins them
@@ -674,9 +680,9 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm)
                 if (sm.joins) p.counters[sm.f] = 0;
             }
             __syncthreads();
-            if (sm.joins) join_partials<D>(p, sm, sm.b, sm.hk, sm.f, sm.last);
+            if (sm.joins) join_partials<D, kFew>(p, sm, sm.b, sm.hk, sm.f, sm.last);
         }
-        if (few) break;
+        if constexpr (kFew) break;
         const int b = sm.b, hk = sm.hk;
         const int64_t next = sm.start + span_of(p, b).pages + kSegmentCost;
         if (next >= min(sm.share * (blockIdx.x + 1), sm.line)) break;
@@ -695,17 +701,31 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm)
 }
 
 // Lets the kernel have its shared memory, once for each device.
-template <int D> int configure(int dev) {
+template <int D, bool kFew> int configure(int dev) {
     static std::atomic<uint64_t> done{0};
     const uint64_t bit = uint64_t(1) << (dev & 63);
     if (dev < 64 && (done.load(std::memory_order_acquire) & bit)) return XS_OK;
-    if (cudaFuncSetAttribute(kv4_decode_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             sizeof(DecodeSmem<D>)) != cudaSuccess) {
+    if (cudaFuncSetAttribute(kv4_decode_kernel<D, kFew>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             sizeof(DecodeSmem<D, kFew>)) != cudaSuccess) {
         cudaGetLastError();
         return XS_EDEVICE;
     }
     done.fetch_or(bit, std::memory_order_release);
     return XS_OK;
+}
+
+template <int D, bool kFew>
+int launch(const Kv4DecodeParams &p, int dev, int sms, cudaStream_t stream) {
+    const int rc = configure<D, kFew>(dev);
+    if (rc != XS_OK) return rc;
+    // The line is at most so long, and no CTA takes less than kMinShare of it.
+    const int64_t segments = static_cast<int64_t>(p.B) * p.Hkv;
+    const int64_t want =
+        segments + (segments * (p.max_blocks + kSegmentCost) + kMinShare - 1) / kMinShare;
+    const int fill = min(sms * ctas_per_sm(kFew), kMaxCtas);
+    kv4_decode_kernel<D, kFew><<<static_cast<int>(want < fill ? want : fill), 32 * dec_warps(kFew),
+                                 sizeof(DecodeSmem<D, kFew>), stream>>>(p);
+    return launch_status();
 }
 
 }  // namespace
@@ -758,17 +778,10 @@ extern "C" int xs_kv4_decode(void *out, const void *q, const void *k_cache, cons
     if (cudaGetDevice(&dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
         return XS_EDEVICE;
-    // The line is at most so long, and no CTA takes less than kMinShare of it.
-    const int64_t most = static_cast<int64_t>(B) * Hkv * (max_blocks_per_seq + xs::kSegmentCost);
-    const int64_t want = static_cast<int64_t>(B) * Hkv + (most + xs::kMinShare - 1) / xs::kMinShare;
-    const int fill = sms * xs::kDecCtasPerSm < xs::kMaxCtas ? sms * xs::kDecCtasPerSm : xs::kMaxCtas;
-    const int grid = static_cast<int>(want < fill ? want : fill);
-    const int rc = D == 128 ? xs::configure<128>(dev) : xs::configure<64>(dev);
-    if (rc != XS_OK) return rc;
+    // Many segments: CTAs of 4 warps on a common line; few: of 8, in pieces.
+    const bool few = static_cast<int64_t>(B) * Hkv * xs::kFewSegments <=
+                     static_cast<int64_t>(sms) * xs::ctas_per_sm(true);
     if (D == 128)
-        xs::kv4_decode_kernel<128>
-            <<<grid, xs::kDecThreads, sizeof(xs::DecodeSmem<128>), stream>>>(p);
-    else
-        xs::kv4_decode_kernel<64><<<grid, xs::kDecThreads, sizeof(xs::DecodeSmem<64>), stream>>>(p);
-    return xs::launch_status();
+        return few ? xs::launch<128, true>(p, dev, sms, stream) : xs::launch<128, false>(p, dev, sms, stream);
+    return few ? xs::launch<64, true>(p, dev, sms, stream) : xs::launch<64, false>(p, dev, sms, stream);
 }

@@ -206,6 +206,22 @@ def test_decode_split(lens, D, Hq, Hkv):
     check_decode(*setup(lens, Hq, Hkv, D, seed=len(lens)), 1 / math.sqrt(D))
 
 
+@pytest.mark.parametrize("B,Hkv,G,D", [(300, 1, 2, 64), (150, 2, 4, 128), (1, 1, 1, 64), (2, 1, 8, 128)])
+def test_decode_many_or_few_sequences(B, Hkv, G, D):
+    # More sequences than a CTA has threads, empty ones among them, first and
+    # last; and the fewest.
+    g = torch.Generator().manual_seed(B)
+    lens = torch.randint(0, 90, (B,), generator=g).tolist()
+    if B > 10:
+        lens[0] = lens[-1] = lens[128] = lens[129] = 0
+        lens[7], lens[B - 2] = 1200, 700
+    else:
+        lens[0] = 3333
+    check_decode(*setup(lens, G * Hkv, Hkv, D, seed=B), 1 / math.sqrt(D))
+    check_decode(*setup(lens, G * Hkv, Hkv, D, seed=B), 1 / math.sqrt(D), window=33,
+                 sinks=torch.randn(G * Hkv, generator=gen(2), device=device()).to(BF))
+
+
 @pytest.mark.parametrize("n", [5, 40, 300, 5000])
 def test_every_token_counts_once(n):
     # q = 0: all weights are 1 / n; V is zero but for one token, so the result

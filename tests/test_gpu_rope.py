@@ -229,3 +229,46 @@ def test_many_rows_of_one_head_and_wide_strides():
     ops.xs_qk_norm_rope(qo, ko, q, k, None, None, 1e-6, tab, pos)
     check_rows(qo, q, None, 1e-6, tab, pos, D, False, "q")
     check_rows(ko, k, None, 1e-6, tab, pos, D, False, "k")
+
+
+@pytest.mark.parametrize("T,Hq,Hkv,D,rot,inter,dtype", [
+    (20000, 5, 3, 64, 32, False, BF), (9001, 7, 2, 128, 48, True, BF), (5000, 5, 5, 128, 128, False, F32),
+    (12003, 1, 1, 64, 64, False, BF),
+])
+@pytest.mark.parametrize("cache", ["none", "same", "kv4"])
+def test_long_calls_equal_short_ones(T, Hq, Hkv, D, rot, inter, dtype, cache):
+    # A long call takes several heads of a token at a time, across the borders
+    # between q, k and v; calls of 50 tokens take one.  Bit for bit the same.
+    if cache == "kv4" and dtype == F32:
+        pytest.skip("4-bit pools take bf16 rows")
+    dev = device()
+    _, q, k, v, qw, kw = inputs(T, Hq, Hkv, D, dtype, seed=T, wide=64)
+    tab = table(T + 5, rot)
+    pos = torch.randperm(T + 5, generator=torch.Generator().manual_seed(T))[:T].to(torch.int32).to(dev)
+    pos[17] = -1
+    nb = T // 16 + 2
+    slots = torch.randperm(nb * 16, generator=torch.Generator().manual_seed(T + 1))[:T].to(dev)
+    slots[:4000] = slots[:4000].sort().values           # consecutive tokens that share a V pair, and not
+    slots[40] = -1
+    out = []
+    for step in (T, 50):
+        qo = torch.zeros(T, Hq, D, dtype=dtype, device=dev)
+        if cache == "none":
+            kc = vc = torch.zeros(T, Hkv, D, dtype=dtype, device=dev)
+        elif cache == "same":
+            kc, vc = (torch.zeros(nb, Hkv, 16, D, dtype=dtype, device=dev) for _ in range(2))
+        else:
+            kc, vc = ops.kv4_pools(nb, Hkv, D, dev)
+        for a in range(0, T, step):
+            s = slice(a, a + step)
+            if cache == "none":
+                ops.xs_qk_norm_rope(qo[s], kc[s], q[s], k[s], qw, kw, 1e-6, tab, pos[s], interleaved=inter)
+            else:
+                ops.xs_qk_norm_rope_append(qo[s], q[s], k[s], v[s], qw, kw, 1e-6, tab, pos[s], kc, vc, slots[s],
+                                           interleaved=inter)
+        out.append((qo, kc, vc))
+    for a, b in zip(*out):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+    on = torch.arange(100, device=dev)
+    on = on[pos[:100] >= 0]
+    check_rows(out[0][0][on], q[on], qw, 1e-6, tab, pos[on], rot, inter, "q")

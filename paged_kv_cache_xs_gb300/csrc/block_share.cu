@@ -146,6 +146,7 @@ __global__ void __launch_bounds__(kShareThreads)
                       int n, int32_t *tables, int max_blocks, int32_t *lens, int B, int bs,
                       const int32_t *__restrict__ free_stack, int32_t *free_top,
                       int32_t *extra_refs, int64_t num_blocks, int64_t *copies, int *err_flag) {
+    after_previous();
     __shared__ int sm[33];
     __shared__ int32_t row_from[kShareThreads], row_to[kShareThreads], row_len[kShareThreads],
         row_new[kShareThreads];
@@ -243,6 +244,7 @@ __global__ void __launch_bounds__(kShareThreads)
                          int max_blocks, int32_t *lens, int B, int bs, int32_t *free_stack,
                          int32_t *free_top, int64_t capacity, int32_t *extra_refs,
                          int64_t num_blocks, int *err_flag) {
+    after_previous();
     __shared__ ShareCounts counts;
     cg::cluster_group cluster = cg::this_cluster();
     const int rank = cluster.block_rank(), ranks = cluster.num_blocks();
@@ -296,6 +298,7 @@ __global__ void __launch_bounds__(kShareThreads)
                          int32_t *extra_out, int32_t *free_stack, int32_t *free_top,
                          int64_t num_blocks, int32_t *remap, int64_t *moves, int32_t *n_moves,
                          int *err_flag) {
+    after_previous();
     __shared__ ShareCounts counts[3];
     cg::cluster_group cluster = cg::this_cluster();
     const int rank = cluster.block_rank(), ranks = cluster.num_blocks();
@@ -392,21 +395,9 @@ __global__ void __launch_bounds__(kShareThreads)
 // a cluster).
 template <typename K, typename... A>
 int launch_share(K kernel, int64_t work, cudaStream_t stream, A... args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(work <= kShareSmall ? 1 : kShareCluster);
-    cfg.blockDim = dim3(work <= kShareSmall / 4 ? kShareThreads / 4 : kShareThreads);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = kShareCluster;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = work <= kShareSmall ? 0 : 1;
-    if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) {
-        cudaGetLastError();
-        return XS_ELAUNCH;
-    }
-    return launch_status();
+    const int ctas = work <= kShareSmall ? 1 : kShareCluster;
+    return launch_after(kernel, dim3(ctas), work <= kShareSmall / 4 ? kShareThreads / 4 : kShareThreads,
+                        0, stream, ctas, args...);
 }
 
 constexpr int kCopyThreads = 256, kCopyUnroll = 8;
@@ -417,6 +408,7 @@ __global__ void __launch_bounds__(kCopyThreads)
                       const int64_t *__restrict__ pairs, int64_t n,
                       const int32_t *__restrict__ count, int64_t block_chunks, int64_t num_blocks,
                       int *err_flag) {
+    after_previous();
     constexpr int64_t kPiece = kCopyThreads * kCopyUnroll;
     if (count) n = min(n, max(static_cast<int64_t>(*count), int64_t(0)));
     const int64_t pieces = (block_chunks + kPiece - 1) / kPiece;
@@ -465,10 +457,8 @@ extern "C" int xs_block_fork(const int32_t *parents, const int32_t *children, in
         return XS_ESHAPE;
     if (n == 0) return XS_OK;
     const int threads = n <= 8 ? xs::kShareThreads / 4 : xs::kShareThreads;
-    xs::block_fork_kernel<<<1, threads, 0, stream>>>(
-        parents, children, n, block_tables, max_blocks_per_seq, context_lens, B, block_size,
+    return xs::launch_after(xs::block_fork_kernel, dim3(1), threads, 0, stream, 1, parents, children, n, block_tables, max_blocks_per_seq, context_lens, B, block_size,
         free_stack, free_top, extra_refs, num_blocks, copies, err_flag);
-    return xs::launch_status();
 }
 
 extern "C" int xs_block_release(const int32_t *seq_ids, int n, int32_t *block_tables,
@@ -529,8 +519,7 @@ extern "C" int xs_block_copy(void *k_pools, void *v_pools, int layers, int64_t l
     const int64_t per_pair = (chunks + piece - 1) / piece * layers * 2;
     const int64_t most = static_cast<int64_t>(sms) * 8;
     const int grid = static_cast<int>(n < most / per_pair + 1 ? n * per_pair < most ? n * per_pair : most : most);
-    xs::block_copy_kernel<<<grid, xs::kCopyThreads, 0, stream>>>(
-        static_cast<uint4 *>(k_pools), static_cast<uint4 *>(v_pools), layers,
+    return xs::launch_after(xs::block_copy_kernel, dim3(grid), xs::kCopyThreads, 0, stream, 1,
+                            static_cast<uint4 *>(k_pools), static_cast<uint4 *>(v_pools), layers,
         layer_stride_bytes / 16, pairs, n, count, chunks, num_blocks, err_flag);
-    return xs::launch_status();
 }

@@ -93,6 +93,7 @@ __global__ void __launch_bounds__(kUnpackThreads)
                       const int32_t *__restrict__ ids, int n, int Hkv, int64_t num_blocks,
                       int *err_flag) {
     constexpr int NG = D / kKv4Group;
+    after_previous();
     const int lane = threadIdx.x & 31;
     const int64_t total = static_cast<int64_t>(n) * Hkv * 2;
     const int64_t stride = static_cast<int64_t>(gridDim.x) * (kUnpackThreads / 32);
@@ -176,17 +177,15 @@ extern "C" int xs_kv4_unpack(void *k_out, void *v_out, const void *k_cache, cons
     const int grid = static_cast<int>(want < (1 << 20) ? want : (1 << 20));
     auto kc = static_cast<const uint8_t *>(k_cache), vc = static_cast<const uint8_t *>(v_cache);
     auto go = [&](auto kernel, auto *ko, auto *vo) {
-        kernel<<<grid, xs::kUnpackThreads, 0, stream>>>(ko, vo, kc, vc, block_ids, n, Hkv,
-                                                        num_blocks, err_flag);
+        return xs::launch_after(kernel, dim3(grid), xs::kUnpackThreads, 0, stream, 1, ko, vo, kc, vc,
+                                block_ids, n, Hkv, num_blocks, err_flag);
     };
     if (dtype == XS_BF16) {
         auto *ko = static_cast<__nv_bfloat16 *>(k_out), *vo = static_cast<__nv_bfloat16 *>(v_out);
-        D == 128 ? go(xs::kv4_unpack_kernel<__nv_bfloat16, 128>, ko, vo)
-                 : go(xs::kv4_unpack_kernel<__nv_bfloat16, 64>, ko, vo);
-    } else {
-        auto *ko = static_cast<float *>(k_out), *vo = static_cast<float *>(v_out);
-        D == 128 ? go(xs::kv4_unpack_kernel<float, 128>, ko, vo)
-                 : go(xs::kv4_unpack_kernel<float, 64>, ko, vo);
+        return D == 128 ? go(xs::kv4_unpack_kernel<__nv_bfloat16, 128>, ko, vo)
+                        : go(xs::kv4_unpack_kernel<__nv_bfloat16, 64>, ko, vo);
     }
-    return xs::launch_status();
+    auto *ko = static_cast<float *>(k_out), *vo = static_cast<float *>(v_out);
+    return D == 128 ? go(xs::kv4_unpack_kernel<float, 128>, ko, vo)
+                    : go(xs::kv4_unpack_kernel<float, 64>, ko, vo);
 }

@@ -85,7 +85,15 @@ __device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
     return r;
 }
 
-// d = A B + d
+// d = A B + c, and d = A B + d
+__device__ __forceinline__ void mma_f16(float *d, const uint32_t *a, uint32_t b0, uint32_t b1,
+                                        const float *c) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%10,%11,%12,%13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]),
+          "f"(c[2]), "f"(c[3]));
+}
 __device__ __forceinline__ void mma_f16(float *d, const uint32_t *a, uint32_t b0, uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
         "{%8,%9}, {%0,%1,%2,%3};"
@@ -364,14 +372,15 @@ __device__ __forceinline__ void run_segment(const Kv4DecodeParams &p, DecodeSmem
 #pragma unroll
         for (int c = 0; c < NG; ++c) {
             uint32_t qa[4], qb[4];
+            float from[4];
             load_words<4>(qa, q0 + c * 1024);
             load_words<4>(qb, q0 + c * 1024 + 512);
+            load_words<4>(reinterpret_cast<uint32_t *>(from), s0 + c * 128);
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 const uint32_t w = kw[u][c];
                 float s[4];
-                load_words<4>(reinterpret_cast<uint32_t *>(s), s0 + c * 128);
-                mma_f16(s, qa, codes_f16(w, 0), codes_f16(w, 1));
+                mma_f16(s, qa, codes_f16(w, 0), codes_f16(w, 1), from);
                 mma_f16(s, qb, codes_f16(w, 2), codes_f16(w, 3));
                 const uint32_t a0 = ks[u][c / 2], a1 = ks[u][NG / 2 + c / 2];
                 const F2 z = c & 1 ? F2{bf_hi(a0), bf_hi(a1)} : F2{bf_lo(a0), bf_lo(a1)};
@@ -588,6 +597,10 @@ template <int D, bool kFew>
 __global__ void __launch_bounds__(32 * dec_warps(kFew), ctas_per_sm(kFew))
     kv4_decode_kernel(const __grid_constant__ Kv4DecodeParams p) {
     constexpr int kDecWarps = dec_warps(kFew), kDecThreads = 32 * kDecWarps;
+    // Placed while the kernel before it ends.  It never lets the next one be
+    // placed early: waiting CTAs of the next call on some SMs and not on others
+    // upset the even spread of this call's (a 64-sequence step 40 -> 44 us).
+    griddep_wait();
     extern __shared__ __align__(16) uint8_t smem_raw[];
     DecodeSmem<D, kFew> &sm = *reinterpret_cast<DecodeSmem<D, kFew> *>(smem_raw);
     if (threadIdx.x < kDecWarps * kStages) mbar_init(&sm.full[0][0] + threadIdx.x, 1);
@@ -723,9 +736,8 @@ int launch(const Kv4DecodeParams &p, int dev, int sms, cudaStream_t stream) {
     const int64_t want =
         segments + (segments * (p.max_blocks + kSegmentCost) + kMinShare - 1) / kMinShare;
     const int fill = min(sms * ctas_per_sm(kFew), kMaxCtas);
-    kv4_decode_kernel<D, kFew><<<static_cast<int>(want < fill ? want : fill), 32 * dec_warps(kFew),
-                                 sizeof(DecodeSmem<D, kFew>), stream>>>(p);
-    return launch_status();
+    return launch_after(kv4_decode_kernel<D, kFew>, dim3(static_cast<int>(want < fill ? want : fill)),
+                        32 * dec_warps(kFew), sizeof(DecodeSmem<D, kFew>), stream, 1, p);
 }
 
 }  // namespace

@@ -186,6 +186,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas)
     constexpr int kRows = 32 / kLanes;          // rows of a warp
     __shared__ __align__(16) uint32_t keys[kKv4 ? kRopeThreads / 32 : 1][kRows][D / 4];
     __shared__ __align__(16) float weights[2][D];
+    after_previous();
     constexpr int kMine = 2 * D / kRopeThreads;     // weights of a thread
     float weight[kMine];    // on their way to shared memory while the first rows are found
 #pragma unroll
@@ -435,17 +436,17 @@ int launch(RopeParams &p, int D, int dtype, cudaStream_t stream) {
     const int64_t want = (items + kRopeThreads / 32 - 1) / (kRopeThreads / 32);
     if (want > INT_MAX) return XS_EUNSUPPORTED;
     const int grid = static_cast<int>(want);
-    auto go = [&](auto kernel) { kernel<<<grid, kRopeThreads, 0, stream>>>(p); };
+    auto go = [&](auto kernel) {
+        return launch_after(kernel, dim3(grid), kRopeThreads, 0, stream, 1, p);
+    };
     if (dtype == XS_F32)
-        D == 128 ? go(qk_norm_rope_kernel<float, 128, false>)
-                 : go(qk_norm_rope_kernel<float, 64, false>);
-    else if (p.kv4)
-        D == 128 ? go(qk_norm_rope_kernel<__nv_bfloat16, 128, true>)
-                 : go(qk_norm_rope_kernel<__nv_bfloat16, 64, true>);
-    else
-        D == 128 ? go(qk_norm_rope_kernel<__nv_bfloat16, 128, false>)
-                 : go(qk_norm_rope_kernel<__nv_bfloat16, 64, false>);
-    return launch_status();
+        return D == 128 ? go(qk_norm_rope_kernel<float, 128, false>)
+                        : go(qk_norm_rope_kernel<float, 64, false>);
+    if (p.kv4)
+        return D == 128 ? go(qk_norm_rope_kernel<__nv_bfloat16, 128, true>)
+                        : go(qk_norm_rope_kernel<__nv_bfloat16, 64, true>);
+    return D == 128 ? go(qk_norm_rope_kernel<__nv_bfloat16, 128, false>)
+                    : go(qk_norm_rope_kernel<__nv_bfloat16, 64, false>);
 }
 
 // Checks that every form shares; fills the fields they share.  `append`: the

@@ -182,6 +182,15 @@ __device__ __forceinline__ void griddep_launch_dependents() {
 }
 __device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// The start of a kernel launched with launch_after(): it may have been placed
+// while the kernel before it ended; it reads and writes nothing before that one
+// has completed, and only then lets the next one be placed - so that a kernel
+// that does not wait for this one still comes after everything before it.
+__device__ __forceinline__ void after_previous() {
+    griddep_wait();
+    griddep_launch_dependents();
+}
+
 // Bring `bytes` (a multiple of 16, 16-byte aligned) at global `src` into L2;
 // a hint with no completion to wait for.
 __device__ __forceinline__ void prefetch_l2(const void *src, uint32_t bytes) {
@@ -265,6 +274,32 @@ inline int elem_bytes(int dtype) {
 
 inline int launch_status() {
     return cudaGetLastError() == cudaSuccess ? XS_OK : XS_ELAUNCH;
+}
+
+// Launches a kernel that begins with after_previous() or griddep_wait(): its CTAs are placed
+// while the kernel before it on the stream ends, which takes 0.7 to 2 us off a
+// sequence of short launches that are not in a graph.
+template <typename... P, typename... A>
+inline int launch_after(void (*kernel)(P...), dim3 grid, int threads, size_t smem,
+                        cudaStream_t stream, int cluster, A &&...args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    if (cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...) != cudaSuccess) {
+        cudaGetLastError();
+        return XS_ELAUNCH;
+    }
+    return launch_status();
 }
 
 }  // namespace xs

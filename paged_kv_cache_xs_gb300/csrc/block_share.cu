@@ -138,9 +138,11 @@ __device__ __forceinline__ int pages_of(int n, int bs, int max_blocks) {
                  : 0;
 }
 
-// One CTA.  A child slot named twice goes to the first entry that names it:
-// the slot's length holds the lowest index of its claimants (INT_MIN + i)
-// between the two passes.
+// One CTA.  A child slot named twice goes to the first entry that may have it.
+// Up to kForkDirect entries are compared with one another in shared memory; of
+// more, a slot's length holds the lowest index of its claimants (INT_MIN + i)
+// between two passes, at the cost of two more trips to memory.
+constexpr int kForkDirect = 256;
 __global__ void __launch_bounds__(kShareThreads)
     block_fork_kernel(const int32_t *__restrict__ parents, const int32_t *__restrict__ children,
                       int n, int32_t *tables, int max_blocks, int32_t *lens, int B, int bs,
@@ -150,17 +152,21 @@ __global__ void __launch_bounds__(kShareThreads)
     __shared__ int sm[33];
     __shared__ int32_t row_from[kShareThreads], row_to[kShareThreads], row_len[kShareThreads],
         row_new[kShareThreads];
+    auto length = [&](int b) { return *static_cast<volatile int32_t *>(lens + b); };
     auto usable = [&](int i, int &p, int &c, int &len) {
         p = parents[i], c = children[i];
         if (p < 0 || p >= B || c < 0 || c >= B) return false;
-        len = *static_cast<volatile int32_t *>(lens + p);
-        return len >= 0 && *static_cast<volatile int32_t *>(lens + c) < 0;
+        len = length(p);
+        return len >= 0 && length(c) < 0;
     };
-    for (int i = threadIdx.x; i < n; i += blockDim.x) {
-        int p, c, len;
-        if (usable(i, p, c, len)) atomicMin(lens + c, INT_MIN + i);
+    const bool direct = n <= kForkDirect && n <= static_cast<int>(blockDim.x);
+    if (!direct) {
+        for (int i = threadIdx.x; i < n; i += blockDim.x) {
+            int p, c, len;
+            if (usable(i, p, c, len)) atomicMin(lens + c, INT_MIN + i);
+        }
+        __syncthreads();
     }
-    __syncthreads();
     const int top = *free_top;
     int popped = 0;
     for (int base = 0; base < n; base += blockDim.x) {
@@ -168,14 +174,23 @@ __global__ void __launch_bounds__(kShareThreads)
         int p = -1, c = -1, len = 0;
         bool ok = false;
         if (i < n) {
-            p = parents[i], c = children[i];
-            ok = p >= 0 && p < B && c >= 0 && c < B;
-            if (ok) {
-                len = *static_cast<volatile int32_t *>(lens + p);
-                ok = len >= 0 && *static_cast<volatile int32_t *>(lens + c) == INT_MIN + i;
+            if (direct) {
+                ok = usable(i, p, c, len);
+            } else {
+                p = parents[i], c = children[i];
+                ok = p >= 0 && p < B && c >= 0 && c < B;
+                if (ok) {
+                    len = length(p);
+                    ok = len >= 0 && length(c) == INT_MIN + i;
+                }
             }
-            if (!ok) raise_flag(err_flag, XS_FLAG_BAD_SLOT);
         }
+        if (direct) {
+            row_to[threadIdx.x] = ok ? c : -1;
+            __syncthreads();
+            for (int k = 0; ok && k < i; ++k) ok = row_to[k] != c;
+        }
+        if (i < n && !ok) raise_flag(err_flag, XS_FLAG_BAD_SLOT);
         bool fits = ok;
         if (ok && (static_cast<int64_t>(len) + bs - 1) / bs > max_blocks) {
             raise_flag(err_flag, XS_FLAG_BAD_LEN);
@@ -256,23 +271,29 @@ __global__ void __launch_bounds__(kShareThreads)
             if (lane == 0) raise_flag(err_flag, XS_FLAG_BAD_SLOT);
             continue;
         }
+        int32_t *row = tables + static_cast<int64_t>(b) * max_blocks;
         int len = 0;
         if (lane == 0) len = atomicExch(lens + b, -1);  // a slot listed twice is released once
+        int32_t early[4];       // the row's first entries, while the length comes
+#pragma unroll
+        for (int u = 0; u < 4; ++u) early[u] = 32 * u + lane < max_blocks ? row[32 * u + lane] : -1;
         len = __shfl_sync(0xffffffffu, len, 0);
         if (len < 0) continue;
-        int32_t *row = tables + static_cast<int64_t>(b) * max_blocks;
         const int pages = pages_of(len, bs, max_blocks);
-#pragma unroll 4
-        for (int col = lane; col < max_blocks; col += 32) {
+        auto drop = [&](int col, int32_t id) {
             if (col < pages) {
-                const int32_t id = row[col];
                 if (id >= 0 && id < num_blocks)
                     atomicSub(extra_refs + id, 1);
                 else
                     raise_flag(err_flag, XS_FLAG_BAD_BLOCK);
             }
             row[col] = -1;
-        }
+        };
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            if (32 * u + lane < max_blocks) drop(32 * u + lane, early[u]);
+#pragma unroll 4
+        for (int col = 128 + lane; col < max_blocks; col += 32) drop(col, row[col]);
     }
     launch_sync(cluster);
     // Highest id first, so that the lowest is the next one taken.

@@ -8,19 +8,30 @@
 // m16n8k16 matrix instructions:
 //
 //   logits   S[h, t] = sum_c s_tc (sum_{d in c} n_td q_hd - 8 sum_{d in c} q_hd),
-//            heads on the 16 rows (8 used), keys on the 8 columns, fp16.  A
+//            keys on the 16 rows, heads on the 8 columns, fp16.  A
 //            pair of codes masked out of its word is the fp16 pair n 2^-24
 //            (or n 2^-20 one nibble higher), exactly: no conversion.  q is
 //            scaled by a power of two to below 2^16, by 1 / 16 more where it
 //            meets the higher nibbles; its bf16 significand fits fp16.  The
 //            group's scale is applied to the fp32 sum, so a logit is an fp32
-//            sum of exact products.  (Keys on the rows would take half the matrix
-//            instructions, but leave p where the second product cannot use
-//            it; this way p is in place, in fp32.)
+//            sum of exact products.  - 8 sum q is what the sum starts at.  The
+//            16 x 8 logits are then turned over between the lanes (8 shuffles),
+//            since the second product wants p with its keys along a lane.
+//            (Heads on the rows need no turning, but half of the rows and twice
+//            the matrix instructions: 158 us, where this takes 154 us.)
 //   values   O[d, h] = sum_t (n_td - 8) (p_th s_tc), dims on the rows, heads on
 //            the columns, bf16, whose range p s needs.  p s is one product in
 //            fp32 and one rounding (2^-9); n - 8 is exact.  The scale meets p,
 //            not the codes: 4 products for a token and head in place of D.
+//
+// What bounds it (32 sequences of 4K to 32K tokens, 32q/8kv x 128, 680 MB): 154 us,
+// 4.4 TB/s, by the instructions of a page and their latencies.  An earlier form
+// took 113 us with both products left out (copies, waits and softmax alone).  A
+// page takes 358 instructions of a warp, about 165 of them on the integer pipe,
+// which takes one every other cycle and is busy 54% of the time; issue slots are
+// 59% busy, the matrix pipe 21%, DRAM 55%.  More or fewer warps, two pages at a
+// time, the next page's logits beside this one's values, multiplications for
+// shifts, and 8-bit matrix instructions all measured the same or slower.
 //
 // The softmax is online, in fp32.  Its reference follows the running maximum
 // only when a logit exceeds it by 2^8, so most pages take no exchange between
@@ -76,29 +87,14 @@ __device__ __forceinline__ F2 mul2(F2 a, F2 b) {
         : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
     return r;
 }
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
-    F2 r;
-    asm("{\n .reg .b64 p, q, s;\n mov.b64 p, {%2, %3};\n mov.b64 q, {%4, %5};\n"
-        " mov.b64 s, {%6, %7};\n fma.rn.f32x2 s, p, q, s;\n mov.b64 {%0, %1}, s;\n}"
-        : "=f"(r.x), "=f"(r.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-    return r;
-}
 
-// d = A B + c, and d = A B + d
-__device__ __forceinline__ void mma_f16(float *d, const uint32_t *a, uint32_t b0, uint32_t b1,
-                                        const float *c) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-        "{%8,%9}, {%10,%11,%12,%13};"
-        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]),
-          "f"(c[2]), "f"(c[3]));
-}
-__device__ __forceinline__ void mma_f16(float *d, const uint32_t *a, uint32_t b0, uint32_t b1) {
+// d = A B + d
+__device__ __forceinline__ void mma_f16(float *d, uint32_t a0, uint32_t a1, uint32_t a2,
+                                        uint32_t a3, uint32_t b0, uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
         "{%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ void mma_bf16(float *c, uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -130,7 +126,9 @@ __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 
 
 // N 32-bit words (8 or 16 bytes) at shared address a.
 template <int N> __device__ __forceinline__ void load_words(uint32_t *r, uint32_t a) {
-    if constexpr (N == 4)
+    if constexpr (N == 1)
+        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(r[0]) : "r"(a) : "memory");
+    else if constexpr (N == 4)
         asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                      : "r"(a)
@@ -185,10 +183,10 @@ template <int D, bool kFew> struct alignas(16) DecodeSmem {
         float o[kDecWarps][8][D + 4];
     };
     uint64_t full[kDecWarps][kStages];
-    // The logits' first operand for each group, two steps of 16 dims, as a lane's
-    // four registers (rows 8 to 15 are zero), and what a head's sums start at.
-    uint4 q[D / 32][2][32];
-    float4 start_at[D / 32][8];
+    // The logits' second operand for each group, two steps of 16 dims, as a lane's
+    // four registers, and what the sums of heads 2 t, 2 t + 1 start at, twice.
+    uint4 q[D / 32][32];
+    float4 start_at[D / 32][4];
     float m[kDecWarps][8], l[kDecWarps][8];
     float weight[kDecThreads];
     int64_t scan[kDecWarps];
@@ -293,7 +291,7 @@ __device__ __forceinline__ void run_segment(const Kv4DecodeParams &p, DecodeSmem
         for (int k = 0; k < kStages; ++k) start(k);
     }
 
-    // q as the first operand: row g is head g (heads past G are zero); words
+    // q as the second operand: column g is head g (heads past G are zero); words
     // j = 0..3 of group c hold dims 32 c + 8 t + j and + j + 4.
     float to_log2;
     {
@@ -331,14 +329,16 @@ __device__ __forceinline__ void run_segment(const Kv4DecodeParams &p, DecodeSmem
             s += __shfl_xor_sync(0xffffffffu, s, 1);
             s += __shfl_xor_sync(0xffffffffu, s, 2);
             if (warp == 0) {
-                sm.q[c][0][lane] = make_uint4(qf[0], 0, qf[1], 0);
-                sm.q[c][1][lane] = make_uint4(qf[2], 0, qf[3], 0);
-                if (t == 0) sm.start_at[c][g] = make_float4(s * -0x1p-21f, s * -0x1p-21f, 0.0f, 0.0f);
+                sm.q[c][lane] = make_uint4(qf[0], qf[1], qf[2], qf[3]);
+                if (t == 0) {
+                    float *to = &sm.start_at[c][g >> 1].x + (g & 1);
+                    to[0] = to[2] = s * -0x1p-21f;
+                }
             }
         }
     }
     __syncthreads();
-    const uint32_t q0 = smem_addr(&sm.q[0][0][lane]), s0 = smem_addr(&sm.start_at[0][g]);
+    const uint32_t q0 = smem_addr(&sm.q[0][lane]), s0 = smem_addr(&sm.start_at[0][t]);
 
     float m = 0.0f, l = 0.0f;   // head g: reference, and this lane's share of the sum
     bool fresh = true;
@@ -362,30 +362,38 @@ __device__ __forceinline__ void run_segment(const Kv4DecodeParams &p, DecodeSmem
             break;
         }
         const uint32_t kp = ring0 + st * (2 * kv4_page_bytes(D)), vp = kp + kv4_page_bytes(D);
-        F2 x[2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};  // keys 2 t, 2 t + 1, and 8 more
-        uint32_t kw[2][NG], ks[2][NG];  // rows g, g + 8; scales of rows 2 t, 2 t + 1, and 8 more
+        uint32_t kw[2][NG], ks[2][NG / 2];  // rows g, g + 8, and their scales
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
             load_words<NG>(kw[u], kp + (g + 8 * u) * (D / 2) + t * (4 * NG));
-            load_words<NG>(ks[u], kp + 8 * D + (t + 4 * u) * (4 * NG));
+            load_words<NG / 2>(ks[u], kp + 8 * D + (g + 8 * u) * (2 * NG));
         }
+        float y[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // (key g, heads 2 t, 2 t + 1), (key g + 8, the same)
 #pragma unroll
         for (int c = 0; c < NG; ++c) {
-            uint32_t qa[4], qb[4];
-            float from[4];
-            load_words<4>(qa, q0 + c * 1024);
-            load_words<4>(qb, q0 + c * 1024 + 512);
-            load_words<4>(reinterpret_cast<uint32_t *>(from), s0 + c * 128);
+            uint32_t qf[4];
+            float s[4];
+            load_words<4>(qf, q0 + c * 512);
+            load_words<4>(reinterpret_cast<uint32_t *>(s), s0 + c * 64);
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const uint32_t w = kw[u][c];
-                float s[4];
-                mma_f16(s, qa, codes_f16(w, 0), codes_f16(w, 1), from);
-                mma_f16(s, qb, codes_f16(w, 2), codes_f16(w, 3));
-                const uint32_t a0 = ks[u][c / 2], a1 = ks[u][NG / 2 + c / 2];
-                const F2 z = c & 1 ? F2{bf_hi(a0), bf_hi(a1)} : F2{bf_lo(a0), bf_lo(a1)};
-                x[u] = fma2(z, F2{s[0], s[1]}, x[u]);
-            }
+            for (int j = 0; j < 4; j += 2)
+                mma_f16(s, codes_f16(kw[0][c], j), codes_f16(kw[1][c], j), codes_f16(kw[0][c], j + 1),
+                        codes_f16(kw[1][c], j + 1), qf[j], qf[j + 1]);
+            const float z0 = c & 1 ? bf_hi(ks[0][c / 2]) : bf_lo(ks[0][c / 2]);
+            const float z1 = c & 1 ? bf_hi(ks[1][c / 2]) : bf_lo(ks[1][c / 2]);
+            y[0] = fmaf(z0, s[0], y[0]), y[1] = fmaf(z0, s[1], y[1]);
+            y[2] = fmaf(z1, s[2], y[2]), y[3] = fmaf(z1, s[3], y[3]);
+        }
+        // Turned over: keys 2 t, 2 t + 1, and 8 more, of head g.
+        F2 x[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int from = 8 * t + (g >> 1);
+            const float a0 = __shfl_sync(0xffffffffu, y[2 * u], from);
+            const float a1 = __shfl_sync(0xffffffffu, y[2 * u + 1], from);
+            const float b0 = __shfl_sync(0xffffffffu, y[2 * u], from + 4);
+            const float b1 = __shfl_sync(0xffffffffu, y[2 * u + 1], from + 4);
+            x[u] = F2{g & 1 ? a1 : a0, g & 1 ? b1 : b0};
         }
         x[0].x *= to_log2, x[0].y *= to_log2;
         x[1].x *= to_log2, x[1].y *= to_log2;

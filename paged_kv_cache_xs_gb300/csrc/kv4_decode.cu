@@ -294,6 +294,7 @@ __device__ __forceinline__ void run_segment(const Kv4DecodeParams &p, DecodeSmem
     // q as the second operand: column g is head g (heads past G are zero); words
     // j = 0..3 of group c hold dims 32 c + 8 t + j and + j + 4.
     float to_log2;
+    bool far;
     {
         const bool head = g < p.G;
         const __nv_bfloat16 *q = p.q + (static_cast<int64_t>(b) * p.Hq + h0 + (head ? g : 0)) * D;
@@ -313,7 +314,9 @@ __device__ __forceinline__ void run_segment(const Kv4DecodeParams &p, DecodeSmem
         const int up = 15 - ex;
         const float u0 = __uint_as_float(static_cast<uint32_t>(up / 2 + 127) << 23);
         const float u1 = __uint_as_float(static_cast<uint32_t>(up - up / 2 + 127) << 23);
-        to_log2 = ldexpf(p.scale_log2, 24 - up);
+        // For q near the end of bf16 (beyond 2^100) in two factors, since one overflows.
+        far = up < -85;
+        to_log2 = ldexpf(p.scale_log2, (far ? 24 - 64 : 24) - up);
 #pragma unroll
         for (int c = 0; c < NG; ++c) {
             float s = 0.0f;
@@ -398,14 +401,14 @@ __device__ __forceinline__ void run_segment(const Kv4DecodeParams &p, DecodeSmem
         x[0].x *= to_log2, x[0].y *= to_log2;
         x[1].x *= to_log2, x[1].y *= to_log2;
         const bool ragged = tok0 < sp.first || tok0 + 16 > sp.n;
-        if (ragged) {  // rows outside [first, n) hold whatever they hold
+        if (ragged || far) {  // rows outside [first, n) hold whatever they hold
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 const int ta = tok0 + 2 * t + 8 * u;
                 const bool in0 = ta >= sp.first && ta < sp.n;
                 const bool in1 = ta + 1 >= sp.first && ta + 1 < sp.n;
-                if (!in0) x[u].x = -INFINITY;
-                if (!in1) x[u].y = -INFINITY;
+                x[u].x = in0 ? x[u].x * (far ? 0x1p64f : 1.0f) : -INFINITY;
+                x[u].y = in1 ? x[u].y * (far ? 0x1p64f : 1.0f) : -INFINITY;
             }
         }
         float hi = fmaxf(fmaxf(x[0].x, x[0].y), fmaxf(x[1].x, x[1].y));

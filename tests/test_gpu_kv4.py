@@ -91,7 +91,7 @@ def test_all_bf16_quotients_round_as_in_64_bits():
     vals = torch.nn.functional.pad(vals, (0, -vals.numel() % 31)).view(-1, 31)
     x = torch.cat([(ext[:, None, None] * 1.0).expand(-1, vals.shape[0], 1),
                    vals[None].expand(128, -1, -1)], -1)
-    x = torch.where(x.abs() > ext[:, None, None], torch.zeros(()), x).reshape(-1, 1, 64 if False else 32)
+    x = torch.where(x.abs() > ext[:, None, None], torch.zeros(()), x).reshape(-1, 1, 32)
     x = torch.cat([x, -x], -1).to(BF)                      # [N, 1, 64]
     n = x.shape[0]
     kc, vc = ops.kv4_pools(-(-n // 16), 1, 64, dev)
@@ -258,6 +258,74 @@ def test_sharp_and_rising_logits():
         q = torch.full((1, 8, 128), 1.0, dtype=BF, device=dev)
         check_decode(q, kc, vc, bt, lens, 8.0 / 16, what=str(sign))
     check_decode(*setup([900, 33, 5000], 8, 2, 128, seed=9, k_std=6.0), 1.0)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("e", [-120, -100, -60, 60, 100, 112, 120, 125])
+def test_queries_of_any_magnitude(e, D):
+    # q times 2^e under keys times 2^-e (exact, but for keys that become
+    # subnormal, whose values are what the pages then hold): ordinary logits.
+    # And under keys of zero: all weights alike, whatever q is.
+    a = setup([300, 77], 8, 2, D, seed=abs(e))
+    q, kc, vc, bt, lens = a
+    q = (q.float() * 2.0 ** e).to(BF)
+    x = torch.randn(kc.shape[0], 2, 16, D, generator=gen(e + 200), device=device())
+    kc = plain.pack_pages((x * 2.0 ** -e).to(BF), False)
+    check_decode(q, kc, vc, bt, lens, 0.1)
+    out = check_decode(q, torch.zeros_like(kc), vc, bt, lens, 0.1)
+    assert bool(out.isfinite().all())
+
+
+def test_captured_beside_other_streams():
+    """One captured graph with two branches: a bf16 append by itself on a side
+    stream, norm + rotation + 4-bit append and attention on the other; a copy
+    before and a torch operation behind; then the same once more in a row.
+    Replays follow the inputs and equal the calls made one by one."""
+    dev = device()
+    Hq, Hkv, D, B = 8, 2, 128, 5
+    nb = 40
+    bt = torch.randperm(nb, generator=torch.Generator().manual_seed(3))[:B * 6].to(torch.int32).view(B, 6).to(dev)
+    tab = ops.rope_table(96, D, 1e4, dev)
+    src = torch.randn(B, Hq + 2 * Hkv, D, generator=gen(1), device=dev).to(BF)
+
+    def buffers():
+        x = torch.zeros_like(src)
+        lens = torch.zeros(B, dtype=torch.int32, device=dev)
+        bf = torch.zeros(2, nb, Hkv, 16, D, dtype=BF, device=dev)
+        return x, lens, bf, ops.kv4_pools(nb, Hkv, D, dev), torch.zeros(2, B, Hq, D, dtype=BF, device=dev)
+
+    def work(x, lens, bf, kv4, out, step, side):
+        for _ in range(2):
+            x.copy_(src)
+            lens.add_(1)
+            q, k, v = x[:, :Hq], x[:, Hq:Hq + Hkv], x[:, Hq + Hkv:]
+            main = torch.cuda.current_stream()
+            side.wait_stream(main)
+            with torch.cuda.stream(side):
+                ops.xs_kv_append_paged(k.contiguous(), v.contiguous(), bf[0], bf[1], bt, lens)
+            step.run(out[0], q, k, v, None, None, tab, kv4[0], kv4[1], bt, lens, 0.09)
+            main.wait_stream(side)
+            ops.xs_kv4_decode(out[1], out[0], kv4[0], kv4[1], bt, lens, 0.09, step.ws)
+            x.add_(1.0)
+
+    a, b = buffers(), buffers()
+    step = Kv4DecodeStep(B, Hq, Hkv, D, dev)
+    side = torch.cuda.Stream()
+    work(*a, step, side)                    # builds what a first call builds
+    torch.cuda.synchronize()
+    for x in (a[0], a[1], a[2], *a[3], a[4]):
+        x.zero_()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        work(*a, step, side)
+    other = Kv4DecodeStep(B, Hq, Hkv, D, dev)
+    for i in range(30):
+        src.copy_(torch.randn(src.shape, generator=gen(i), device=dev))
+        graph.replay()
+        work(*b, other, torch.cuda.current_stream())
+        for x, y in zip((a[0], a[1], a[2], *a[3], a[4]), (b[0], b[1], b[2], *b[3], b[4])):
+            assert torch.equal(x, y), i
+    assert step.error_flags() == 0 and int(a[1][0]) == 60
 
 
 def test_nan_in_a_sequence_stays_in_its_head():

@@ -5,6 +5,8 @@
 // lengths (they already count the token written in this step) follow the xserv pages
 // ("xserv compare phase10...cf1e9e4", crates/xserv-kernels/src/attention.rs,
 // reshape_and_cache_bf16 / reshape_and_cache_batched_bf16).
+#include <initializer_list>
+
 #include "xs_common.cuh"
 
 namespace xs {
@@ -167,7 +169,18 @@ int launch_append(bool from_table, const void *k_new, const void *v_new, void *k
 }
 
 }  // namespace
-XS_DEFINE_BOUNDS_COUNTER(bounds_failures_append)
+XS_DEFINE_BOUNDS_COUNTER(bounds_failures_append_only)
+// With the counts of the norm + rotation, 4-bit cache and shared-page kernels.
+int bounds_failures_append(int reset) {
+    int total = 0;
+    for (const int v : {bounds_failures_append_only(reset), bounds_failures_rope(reset),
+                        bounds_failures_kv4_cache(reset), bounds_failures_kv4_decode(reset),
+                        bounds_failures_share(reset)}) {
+        if (v < 0) return v;
+        total += v;
+    }
+    return total;
+}
 
 }  // namespace xs
 

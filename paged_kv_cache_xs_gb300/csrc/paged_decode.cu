@@ -2573,9 +2573,7 @@ extern "C" int xs_debug_bounds_failures(int reset) {
 #ifdef XS_DEBUG_BOUNDS
     int total = 0;
     for (const int v : {bounds_failures_append(reset), bounds_failures_decode(reset),
-                        bounds_failures_prefill_tc(reset), bounds_failures_rope(reset),
-                        bounds_failures_kv4_cache(reset), bounds_failures_kv4_decode(reset),
-                        bounds_failures_share(reset)}) {
+                        bounds_failures_prefill_tc(reset)}) {
         if (v < 0) return v;
         total += v;
     }

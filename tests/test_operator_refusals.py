@@ -207,3 +207,11 @@ def test_rope_table():
     assert t[99999, 1] == torch.tensor(a, dtype=torch.float64).cos().float()
     assert t[99999, 5] == torch.tensor(a, dtype=torch.float64).sin().float()
     assert bool((t[0] == torch.tensor([1.0] * 4 + [0.0] * 4)).all())
+
+
+def test_bench_finds_the_counters_of_its_kernel():
+    # The committed counters belong to the decode kernel's source as it is.
+    import bench
+
+    for workload in ("qwen3_8b_long_batch", "qwen3_8b_cb_mix", "qwen3_8b_single_stream", "gpt2_bf16_12layer"):
+        assert bench.kernel_traffic(workload) is not None, workload

@@ -189,34 +189,20 @@ template <int D, bool kFew> struct alignas(16) DecodeSmem {
     float4 start_at[D / 32][4];
     float m[kDecWarps][8], l[kDecWarps][8];
     float weight[kDecThreads];
-    int64_t scan[kDecWarps];
     // The CTA's place: segment (b, hk), pages [a, e) of it, shared by the CTAs
     // f .. last.  Here so that it holds no registers while a segment runs.
     int b, hk, a, e, f, last, joins;
     int64_t start, share, line;         // on a line: where the segment starts, ...
 };
 
-// Inclusive sum over the CTA's threads; *total gets the sum of all.
-template <int D, bool kFew>
-__device__ __forceinline__ int64_t cta_scan(int64_t v, int64_t *total, DecodeSmem<D, kFew> &sm) {
-    constexpr int kDecWarps = dec_warps(kFew);
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+// Inclusive sum over the warp's lanes.
+__device__ __forceinline__ uint32_t warp_scan(uint32_t v) {
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, v, d);
-        if (lane >= d) v += y;
+        const uint32_t y = __shfl_up_sync(0xffffffffu, v, d);
+        if (static_cast<int>(threadIdx.x & 31) >= d) v += y;
     }
-    __syncthreads();
-    if (lane == 31) sm.scan[warp] = v;
-    __syncthreads();
-    int64_t before = 0, all = 0;
-#pragma unroll
-    for (int w = 0; w < kDecWarps; ++w) {
-        if (w < warp) before += sm.scan[w];
-        all += sm.scan[w];
-    }
-    *total = all;
-    return v + before;
+    return v;
 }
 
 // Copies of a K and a V page to shared address dst and behind it, counted on
@@ -272,6 +258,13 @@ __device__ __forceinline__ void run_segment(const Kv4DecodeParams &p, DecodeSmem
         return id;
     };
     int32_t ids = load_ids(0);
+    // Lane (g, t): 8 dims of every group of head g's query (on its way while the ids are).
+    uint4 qx[NG];
+    {
+        const __nv_bfloat16 *q = p.q + (static_cast<int64_t>(b) * p.Hq + h0 + (g < p.G ? g : 0)) * D;
+#pragma unroll
+        for (int c = 0; c < NG; ++c) qx[c] = *reinterpret_cast<const uint4 *>(q + 32 * c + 8 * t);
+    }
     // Starts the copies of the warp's page k into the ring's next place.
     const uint32_t ring0 = smem_addr(sm.ring[warp]), bar0 = smem_addr(sm.full[warp]);
     const uint32_t base = ring.taken;
@@ -297,12 +290,10 @@ __device__ __forceinline__ void run_segment(const Kv4DecodeParams &p, DecodeSmem
     bool far;
     {
         const bool head = g < p.G;
-        const __nv_bfloat16 *q = p.q + (static_cast<int64_t>(b) * p.Hq + h0 + (head ? g : 0)) * D;
         float f[NG][8], top = 0.0f;
 #pragma unroll
         for (int c = 0; c < NG; ++c) {
-            uint4 x = *reinterpret_cast<const uint4 *>(q + 32 * c + 8 * t);
-            if (!head) x = make_uint4(0, 0, 0, 0);
+            const uint4 x = head ? qx[c] : make_uint4(0, 0, 0, 0);
             unpack16(x, f[c], static_cast<__nv_bfloat16 *>(nullptr));
 #pragma unroll
             for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(f[c][k]));
@@ -616,61 +607,63 @@ __global__ void __launch_bounds__(32 * dec_warps(kFew), ctas_per_sm(kFew))
     DecodeSmem<D, kFew> &sm = *reinterpret_cast<DecodeSmem<D, kFew> *>(smem_raw);
     if (threadIdx.x < kDecWarps * kStages) mbar_init(&sm.full[0][0] + threadIdx.x, 1);
     mbar_fence_init();
-    __syncthreads();
     RingState ring;
-    // This CTA's place.  A sequence has so many units for each KV head: pieces
-    // (one of them is this CTA's), or the length of its segments on the line.
-    // The lengths of the first kDecThreads sequences stay in registers.
+    // This CTA's place, found by every warp for itself (a load of the lengths
+    // and a few shuffles; with barriers between the warps it took 0.2 us more).
+    // A sequence has so many units for each KV head: pieces (one of them is
+    // this CTA's), or the length of its segments on the line.  The sums of 32
+    // sequences fit 32 bits.
+    const int lane = threadIdx.x & 31;
     const int64_t segments = static_cast<int64_t>(p.B) * p.Hkv;
-    int pages0 = 0;
+    auto pages_at = [&](int b) { return b < p.B ? static_cast<uint32_t>(span_of(p, b).pages) : 0u; };
+    uint32_t pages0[4];     // of the first 128 sequences
     int64_t total = 0;
-    for (int base = 0; base < p.B; base += kDecThreads) {
-        const int b = base + threadIdx.x;
-        const int pages = b < p.B ? span_of(p, b).pages : 0;
-        if (base == 0) pages0 = pages;
-        int64_t all;
-        cta_scan(pages, &all, sm);
-        total += all;
-    }
-    int64_t share, line = (total + static_cast<int64_t>(p.B) * kSegmentCost) * p.Hkv;
-    if constexpr (kFew) {
-        const int64_t ctas = gridDim.x - segments;
-        share = max((total * p.Hkv + ctas - 1) / ctas, static_cast<int64_t>(kMinShare));
-    } else {
-        share = max((line + gridDim.x - 1) / gridDim.x, static_cast<int64_t>(kMinShare));
-    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) pages0[u] = pages_at(32 * u + lane);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) total += __reduce_add_sync(0xffffffffu, pages0[u]);
+#pragma unroll 4
+    for (int base = 128; base < p.B; base += 32)
+        total += __reduce_add_sync(0xffffffffu, pages_at(base + lane));
+    const int64_t line = (total + static_cast<int64_t>(p.B) * kSegmentCost) * p.Hkv;
+    const int64_t ctas = kFew ? gridDim.x - segments : gridDim.x;
+    const int64_t share = max(((kFew ? total * p.Hkv : line) + ctas - 1) / ctas, static_cast<int64_t>(kMinShare));
     const int64_t target = kFew ? blockIdx.x : share * blockIdx.x;
-    if (threadIdx.x == 0) sm.b = -1;
     int64_t before = 0;
-    for (int base = 0; base < p.B && before * p.Hkv <= target; base += kDecThreads) {
-        const int b = base + threadIdx.x;
-        const int pages = base ? (b < p.B ? span_of(p, b).pages : 0) : pages0;
-        const int64_t units = b >= p.B ? 0
-                              : kFew ? max((pages + share - 1) / share, int64_t(1))
-                                       : pages + kSegmentCost;
-        int64_t all;
-        const int64_t end = (before + cta_scan(units, &all, sm)) * p.Hkv;
-        const int64_t s = end - units * p.Hkv;
-        if (target >= s && target < end) {
+    bool found = false;
+    auto look = [&](int base, uint32_t pages) {     // among sequences base .. base + 31
+        uint32_t units = 0;
+        if (base + lane < p.B)
+            units = !kFew ? pages + kSegmentCost
+                          : max((pages + static_cast<uint32_t>(share) - 1) / static_cast<uint32_t>(share), 1u);
+        const uint32_t sum = warp_scan(units);
+        const int64_t end = (before + sum) * p.Hkv, s = end - static_cast<int64_t>(units) * p.Hkv;
+        before += __shfl_sync(0xffffffffu, sum, 31);
+        const bool mine = target >= s && target < end;
+        found = __any_sync(0xffffffffu, mine);
+        if (mine && threadIdx.x < 32) {
             const int hk = static_cast<int>((target - s) / units);
-            sm.b = b;
+            sm.b = base + lane;
             sm.hk = hk;
-            sm.start = s + hk * units;
+            sm.start = s + static_cast<int64_t>(hk) * units;
             sm.share = share;
             sm.line = line;
             if constexpr (kFew) {
                 const int j = static_cast<int>(target - sm.start), n = static_cast<int>(units);
-                const int piece = (pages + n - 1) / n;
+                const int piece = (static_cast<int>(pages) + n - 1) / n;
                 sm.a = j * piece;
-                sm.e = min((j + 1) * piece, pages);
+                sm.e = min((j + 1) * piece, static_cast<int>(pages));
                 sm.f = blockIdx.x - j;
                 sm.last = sm.f + n - 1;
             }
         }
-        before += all;
-    }
+    };
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+        if (!found && 32 * u < p.B) look(32 * u, pages0[u]);
+    for (int base = 128; !found && base < p.B; base += 32) look(base, pages_at(base + lane));
+    if (!found) return;
     __syncthreads();
-    if (sm.b < 0) return;
     while (true) {
         {
             const int b = sm.b, hk = sm.hk;

@@ -47,12 +47,11 @@
 // and head ("segment") with kSegmentCost more for its start and end.  The line
 // is cut into equal shares, one for each CTA, whatever the lengths are: CTA i
 // finds its place from the lengths themselves, so the host needs to know none
-// of them and a captured call follows them.  Where the segments are few
-// (kFewSegments), each is cut into equal pieces of its own instead, one for a
-// CTA, so that no CTA does two in a row.  A segment that one CTA does is
+// of them and a captured call follows them.  A segment that one CTA does is
 // written at once.  One that is cut leaves fp32 partials in the workspace, at
 // most two for each CTA whatever the batch, and the CTA that finishes it last
-// joins them in order: the result does not depend on which that is.
+// joins them in order: the result does not depend on which that is.  Where
+// segments are few, thread-block clusters take them (kv4_decode_few_kernel).
 #include <atomic>
 
 #include <cuda_fp16.h>
@@ -64,14 +63,18 @@ namespace {
 
 // Warps of a CTA, and CTAs on an SM (16 warps of 128 registers): small CTAs
 // where segments are many and often end, larger ones where a segment has many
-// CTAs and their partials are what the join waits for (one stream at 4K tokens:
-// 10.4 us with 8 warps, 11.5 us with 4; a 64-sequence step 49 us and 41 us).
+// CTAs and what they leave is joined (a 64-sequence step 49 us with 8 warps, 41 us with 4).
 __host__ __device__ constexpr int dec_warps(bool few) { return few ? 8 : 4; }
 __host__ __device__ constexpr int ctas_per_sm(bool few) { return 16 / dec_warps(few); }
 constexpr int kMaxCtas = 1024;     // the workspace holds partials for so many
 constexpr int kSegmentCost = 16;   // pages
 constexpr int kMinShare = 16;      // pages
-constexpr int kFewSegments = 8;    // few: at least so many (large) CTAs for each segment
+// Segments up to so many pages are not cut: a join costs more (64 segments of
+// 100, 300, 500 tokens 5.7, 7.5, 8.9 us so, 8.5, 9.7, 10.0 us cut; of 1000 17 us so, 11.4 us).
+constexpr int kWholePages = 32;
+constexpr int kCluster = 8;        // CTAs of a cluster (of 16: 1.5 us more for a start)
+constexpr int kClusterPages = 256; // of a segment: up to so many a cluster always does it
+constexpr int kAlonePages = 16;    // and up to so many one CTA
 constexpr int kStages = 4;         // pages of a warp's ring
 constexpr uint64_t kWaitLimitNs = 4000000000ull;
 
@@ -174,8 +177,13 @@ __host__ __device__ constexpr int64_t partial_floats(int G, int D) {
     return (static_cast<int64_t>(G) * (D + 2) + 3) / 4 * 4;
 }
 
+// Partial `slot` of CTA i.
+__device__ __forceinline__ float *partial_of(const Kv4DecodeParams &p, int D, int64_t i, int slot) {
+    return p.partials + (2 * i + slot) * partial_floats(p.G, D);
+}
+
 template <int D, bool kFew> struct alignas(16) DecodeSmem {
-    static constexpr int kDecWarps = dec_warps(kFew), kDecThreads = 32 * kDecWarps;
+    static constexpr int kDecWarps = dec_warps(kFew);
     // The pages on their way (K page, V page).  Between segments, when none are,
     // the warps' values meet there (rows padded, for the banks).
     union {
@@ -188,7 +196,8 @@ template <int D, bool kFew> struct alignas(16) DecodeSmem {
     uint4 q[D / 32][32];
     float4 start_at[D / 32][4];
     float m[kDecWarps][8], l[kDecWarps][8];
-    float weight[kDecThreads];
+    float weight[kDecWarps * 8];
+    alignas(16) float part[kFew ? 8 * (D + 2) : 4];     // what the CTA leaves for its cluster
     // The CTA's place: segment (b, hk), pages [a, e) of it, shared by the CTAs
     // f .. last.  Here so that it holds no registers while a segment runs.
     int b, hk, a, e, f, last, joins;
@@ -233,11 +242,11 @@ struct RingState {
 };
 
 // Pages [a, e) of one segment: what the CTA's warps leave in shared memory is
-// joined and either written out (whole) or left as the CTA's partial `slot`.
+// joined and either written out (whole) or left at `part`.
 template <int D, bool kFew>
 __device__ __forceinline__ void run_segment(const Kv4DecodeParams &p, DecodeSmem<D, kFew> &sm,
                                             RingState &ring, int b, int hk, const Span &sp, int a,
-                                            int e, bool whole, int slot) {
+                                            int e, bool whole, float *part) {
     constexpr int NG = D / 32, kDecWarps = dec_warps(kFew), kDecThreads = 32 * kDecWarps;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
     const int h0 = hk * p.G;
@@ -482,7 +491,6 @@ __device__ __forceinline__ void run_segment(const Kv4DecodeParams &p, DecodeSmem
                     make_float2(acc[c][jj][k], acc[c][jj][k + 2]);
     __syncthreads();
     const bool sinks = whole && p.sinks;
-    float *part = p.partials + (2 * static_cast<int64_t>(blockIdx.x) + slot) * partial_floats(p.G, D);
     if (threadIdx.x < kDecWarps * 8) {      // (warp, head): its weight, over the sum if whole
         const int w = threadIdx.x >> 3, h = threadIdx.x & 7;
         float top = sm.m[0][h];
@@ -499,8 +507,8 @@ __device__ __forceinline__ void run_segment(const Kv4DecodeParams &p, DecodeSmem
         const float f = fast_exp2(sm.m[w][h] - top);
         sm.weight[threadIdx.x] = whole ? f / total : f;
         if (!whole && w == 0 && h < p.G) {
-            __stcg(part + p.G * D + h, top);
-            __stcg(part + p.G * (D + 1) + h, total);
+            part[p.G * D + h] = top;
+            part[p.G * (D + 1) + h] = total;
         }
     }
     __syncthreads();
@@ -553,7 +561,7 @@ __device__ __noinline__ void join_partials(const Kv4DecodeParams &p, DecodeSmem<
         const int n = min(room, last - base + 1);
         for (int c = threadIdx.x; c < n * chunks; c += kDecThreads) {
             const int i = c / chunks, at = c - i * chunks;
-            const float *src = p.partials + (2 * static_cast<int64_t>(base + i) + (base + i == f)) * floats;
+            const float *src = partial_of(p, D, base + i, base + i == f);
             asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(buf + 4 * c)),
                          "l"(src + 4 * at)
                          : "memory");
@@ -595,28 +603,47 @@ __device__ __noinline__ void join_partials(const Kv4DecodeParams &p, DecodeSmem<
     }
 }
 
+// A part of a segment is done: the last of its CTAs joins them.
 template <int D, bool kFew>
-__global__ void __launch_bounds__(32 * dec_warps(kFew), ctas_per_sm(kFew))
+__device__ __forceinline__ void arrive_and_join(const Kv4DecodeParams &p, DecodeSmem<D, kFew> &sm) {
+    // The barrier and the atomic's release carry all threads' partials, its
+    // acquire and the next barrier the other CTAs'.
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        sm.joins = atomic_add_acq_rel_gpu(p.counters + sm.f, 1) == sm.last - sm.f;
+        if (sm.joins) p.counters[sm.f] = 0;
+    }
+    __syncthreads();
+    if (sm.joins) join_partials<D, kFew>(p, sm, sm.b, sm.hk, sm.f, sm.last);
+}
+
+// The last copies of a warp whose wait ran out are still on their way here.
+template <int D, bool kFew>
+__device__ __forceinline__ void drain(DecodeSmem<D, kFew> &sm, RingState &ring) {
+    for (; ring.behind > 0; --ring.behind, ++ring.taken)
+        mbar_wait_bounded(&sm.full[threadIdx.x >> 5][ring.taken % kStages],
+                          (ring.taken / kStages) & 1, kWaitLimitNs);
+}
+
+// A CTA's place is found by every warp for itself (a load of the lengths and a
+// few shuffles; with barriers between the warps it took 0.2 us more).
+template <int D>
+__global__ void __launch_bounds__(32 * dec_warps(false), ctas_per_sm(false))
     kv4_decode_kernel(const __grid_constant__ Kv4DecodeParams p) {
-    constexpr int kDecWarps = dec_warps(kFew), kDecThreads = 32 * kDecWarps;
+    constexpr int kDecWarps = dec_warps(false), kDecThreads = 32 * kDecWarps;
     // Placed while the kernel before it ends.  It never lets the next one be
     // placed early: waiting CTAs of the next call on some SMs and not on others
     // upset the even spread of this call's (a 64-sequence step 40 -> 44 us).
     griddep_wait();
     extern __shared__ __align__(16) uint8_t smem_raw[];
-    DecodeSmem<D, kFew> &sm = *reinterpret_cast<DecodeSmem<D, kFew> *>(smem_raw);
+    DecodeSmem<D, false> &sm = *reinterpret_cast<DecodeSmem<D, false> *>(smem_raw);
     if (threadIdx.x < kDecWarps * kStages) mbar_init(&sm.full[0][0] + threadIdx.x, 1);
     mbar_fence_init();
     RingState ring;
-    // This CTA's place, found by every warp for itself (a load of the lengths
-    // and a few shuffles; with barriers between the warps it took 0.2 us more).
-    // A sequence has so many units for each KV head: pieces (one of them is
-    // this CTA's), or the length of its segments on the line.  The sums of 32
-    // sequences fit 32 bits.
+    // The line's length, then the segment in which this CTA's share begins.
     const int lane = threadIdx.x & 31;
-    const int64_t segments = static_cast<int64_t>(p.B) * p.Hkv;
     auto pages_at = [&](int b) { return b < p.B ? static_cast<uint32_t>(span_of(p, b).pages) : 0u; };
-    uint32_t pages0[4];     // of the first 128 sequences
+    uint32_t pages0[4];     // of the first 128 sequences; the sums of 32 fit 32 bits
     int64_t total = 0;
 #pragma unroll
     for (int u = 0; u < 4; ++u) pages0[u] = pages_at(32 * u + lane);
@@ -626,16 +653,12 @@ __global__ void __launch_bounds__(32 * dec_warps(kFew), ctas_per_sm(kFew))
     for (int base = 128; base < p.B; base += 32)
         total += __reduce_add_sync(0xffffffffu, pages_at(base + lane));
     const int64_t line = (total + static_cast<int64_t>(p.B) * kSegmentCost) * p.Hkv;
-    const int64_t ctas = kFew ? gridDim.x - segments : gridDim.x;
-    const int64_t share = max(((kFew ? total * p.Hkv : line) + ctas - 1) / ctas, static_cast<int64_t>(kMinShare));
-    const int64_t target = kFew ? blockIdx.x : share * blockIdx.x;
+    const int64_t share = max((line + gridDim.x - 1) / gridDim.x, static_cast<int64_t>(kMinShare));
+    const int64_t target = share * blockIdx.x;
     int64_t before = 0;
     bool found = false;
     auto look = [&](int base, uint32_t pages) {     // among sequences base .. base + 31
-        uint32_t units = 0;
-        if (base + lane < p.B)
-            units = !kFew ? pages + kSegmentCost
-                          : max((pages + static_cast<uint32_t>(share) - 1) / static_cast<uint32_t>(share), 1u);
+        const uint32_t units = base + lane < p.B ? pages + kSegmentCost : 0;
         const uint32_t sum = warp_scan(units);
         const int64_t end = (before + sum) * p.Hkv, s = end - static_cast<int64_t>(units) * p.Hkv;
         before += __shfl_sync(0xffffffffu, sum, 31);
@@ -648,14 +671,6 @@ __global__ void __launch_bounds__(32 * dec_warps(kFew), ctas_per_sm(kFew))
             sm.start = s + static_cast<int64_t>(hk) * units;
             sm.share = share;
             sm.line = line;
-            if constexpr (kFew) {
-                const int j = static_cast<int>(target - sm.start), n = static_cast<int>(units);
-                const int piece = (static_cast<int>(pages) + n - 1) / n;
-                sm.a = j * piece;
-                sm.e = min((j + 1) * piece, static_cast<int>(pages));
-                sm.f = blockIdx.x - j;
-                sm.last = sm.f + n - 1;
-            }
         }
     };
 #pragma unroll
@@ -668,38 +683,30 @@ __global__ void __launch_bounds__(32 * dec_warps(kFew), ctas_per_sm(kFew))
         {
             const int b = sm.b, hk = sm.hk;
             const Span sp = span_of(p, b);
-            if (!kFew && threadIdx.x == 0) {
+            if (threadIdx.x == 0) {
                 const int64_t s = sm.start, share = sm.share, lo = share * blockIdx.x;
                 const int64_t hi = min(lo + share, sm.line);
                 sm.a = static_cast<int>(min(max(lo - s, int64_t(0)), static_cast<int64_t>(sp.pages)));
                 sm.e = static_cast<int>(min(hi - s, static_cast<int64_t>(sp.pages)));
                 sm.f = static_cast<int>(s / share);
                 sm.last = static_cast<int>((s + sp.pages - 1) / share);
+                if (sp.pages <= kWholePages)    // its first CTA does all of it
+                    sm.last = sm.f, sm.a = 0, sm.e = s >= lo ? sp.pages : 0;
             }
             __syncthreads();
             const int a = sm.a, e = sm.e;
             if (sp.pages == 0) {
-                if (kFew || sm.start >= sm.share * blockIdx.x) {
+                if (sm.start >= sm.share * blockIdx.x) {
                     __nv_bfloat16 *out = p.out + (static_cast<int64_t>(b) * p.Hq + hk * p.G) * D;
                     for (int x = threadIdx.x; x < p.G * D; x += kDecThreads)
                         out[x] = __float2bfloat16_rn(0.0f);
                 }
             } else if (a < e) {
-                run_segment<D, kFew>(p, sm, ring, b, hk, sp, a, e, a == 0 && e == sp.pages, a == 0);
+                run_segment<D, false>(p, sm, ring, b, hk, sp, a, e, a == 0 && e == sp.pages,
+                                      partial_of(p, D, blockIdx.x, a == 0));
             }
         }
-        if (sm.a < sm.e && sm.f != sm.last) {   // a part: the last of its CTAs joins them
-            // The barrier and the atomic's release carry all threads' partials,
-            // its acquire and the next barrier the other CTAs'.
-            __syncthreads();
-            if (threadIdx.x == 0) {
-                sm.joins = atomic_add_acq_rel_gpu(p.counters + sm.f, 1) == sm.last - sm.f;
-                if (sm.joins) p.counters[sm.f] = 0;
-            }
-            __syncthreads();
-            if (sm.joins) join_partials<D, kFew>(p, sm, sm.b, sm.hk, sm.f, sm.last);
-        }
-        if constexpr (kFew) break;
+        if (sm.a < sm.e && sm.f != sm.last) arrive_and_join(p, sm);
         const int b = sm.b, hk = sm.hk;
         const int64_t next = sm.start + span_of(p, b).pages + kSegmentCost;
         if (next >= min(sm.share * (blockIdx.x + 1), sm.line)) break;
@@ -711,37 +718,218 @@ __global__ void __launch_bounds__(32 * dec_warps(kFew), ctas_per_sm(kFew))
         }
         __syncthreads();
     }
-    // After a wait that ran out, copies may still be on their way here.
-    for (; ring.behind > 0; --ring.behind, ++ring.taken)
-        mbar_wait_bounded(&sm.full[threadIdx.x >> 5][ring.taken % kStages],
-                          (ring.taken / kStages) & 1, kWaitLimitNs);
+    drain(sm, ring);
 }
 
-// Lets the kernel have its shared memory, once for each device.
-template <int D, bool kFew> int configure(int dev) {
-    static std::atomic<uint64_t> done{0};
-    const uint64_t bit = uint64_t(1) << (dev & 63);
-    if (dev < 64 && (done.load(std::memory_order_acquire) & bit)) return XS_OK;
-    if (cudaFuncSetAttribute(kv4_decode_kernel<D, kFew>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             sizeof(DecodeSmem<D, kFew>)) != cudaSuccess) {
+// ---- few segments: clusters
+
+__device__ __forceinline__ uint32_t peer_addr(const void *own, int rank) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(own)), "r"(rank));
+    return a;
+}
+__device__ __forceinline__ float peer_f32(uint32_t a) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ float4 peer_f32x4(uint32_t a) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(a)
+                 : "memory");
+    return v;
+}
+// Few segments, in clusters of kCluster CTAs.  Either each segment has a cluster,
+// whose CTAs cut it evenly and join their parts through shared memory (a
+// short one its first CTA alone); or, where that leaves too much to one
+// cluster, all segments are cut for all CTAs, as many as there are, and joined
+// through the workspace.  Which, the lengths decide.  (32q/8kv x 128, us, clusters and
+// pieces: one sequence of 300 tokens 5.4 and 7.9, of 2K 6.3 and 8.7, 4K 8.2 and
+// 9.5, 8K 11.2 and 11.9, 12K 14.6 and 13.8; two of 4K 10.3 and 11.0, of 8K 14.7 and
+// 13.1; four of 8K 15.2 and 16.6.)
+template <int D>
+__global__ void __launch_bounds__(32 * dec_warps(true), ctas_per_sm(true))
+    kv4_decode_few_kernel(const __grid_constant__ Kv4DecodeParams p) {
+    constexpr int kDecWarps = dec_warps(true), kDecThreads = 32 * kDecWarps;
+    griddep_wait();
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    DecodeSmem<D, true> &sm = *reinterpret_cast<DecodeSmem<D, true> *>(smem_raw);
+    if (threadIdx.x < kDecWarps * kStages) mbar_init(&sm.full[0][0] + threadIdx.x, 1);
+    mbar_fence_init();
+    RingState ring;
+    const int lane = threadIdx.x & 31, rank = blockIdx.x % kCluster;
+    uint32_t pages0[2], longest = 0;
+    int64_t total = 0;
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+        pages0[u] = 32 * u + lane < p.B ? static_cast<uint32_t>(span_of(p, 32 * u + lane).pages) : 0u;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        total += __reduce_add_sync(0xffffffffu, pages0[u]);
+        longest = max(longest, __reduce_max_sync(0xffffffffu, pages0[u]));
+    }
+    const int64_t segments = static_cast<int64_t>(p.B) * p.Hkv;
+    total *= p.Hkv;
+    // In units of a page of a warp, three times: a cluster's time is that of its longest
+    // segment over 64 warps (less where CTAs have their SM for themselves);
+    // with pieces all warps share the pages, and the join costs 4 pages more.
+    const int weight = segments * kCluster * 4 > gridDim.x ? 3 : 2;
+    const bool clusters =
+        longest <= kClusterPages ||
+        static_cast<int64_t>(longest) * weight <= 3 * (64 * 4 + total * kCluster / gridDim.x);
+    int b = 0, hk = 0, a, e, whole;
+    if (clusters) {
+        const int segment = blockIdx.x / kCluster;
+        b = segment / p.Hkv, hk = segment - b * p.Hkv;
+        if (b >= p.B) return;           // the whole cluster
+        const int pages = static_cast<int>(b < 32 ? __shfl_sync(0xffffffffu, pages0[0], b)
+                                                  : __shfl_sync(0xffffffffu, pages0[1], b - 32));
+        whole = pages <= kAlonePages;
+        a = whole ? 0 : static_cast<int>(static_cast<int64_t>(pages) * rank / kCluster);
+        e = whole ? pages : static_cast<int>(static_cast<int64_t>(pages) * (rank + 1) / kCluster);
+        if (whole && rank) return;      // all but one
+    } else {
+        // Equal pieces of at least kMinShare pages, one for a CTA: as small as the
+        // CTAs suffice for, or as they surely do (a sum of ceil(x) is at most
+        // their number and the sum of x).
+        auto pieces = [&](int u, uint32_t share) {
+            return 32 * u + lane < p.B ? max((pages0[u] + share - 1) / share, 1u) : 0u;
+        };
+        auto share_for = [&](int64_t ctas) {
+            return max(static_cast<uint32_t>((total + ctas - 1) / ctas), static_cast<uint32_t>(kMinShare));
+        };
+        uint32_t share = share_for(gridDim.x);
+        const uint32_t all = __reduce_add_sync(0xffffffffu, pieces(0, share) + pieces(1, share));
+        if (static_cast<int64_t>(all) * p.Hkv > gridDim.x) share = share_for(gridDim.x - segments);
+        int before = 0;
+        bool found = false;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            if (found) break;
+            const uint32_t units = pieces(u, share), sum = warp_scan(units);
+            const int end = (before + static_cast<int>(sum)) * p.Hkv, s = end - static_cast<int>(units) * p.Hkv;
+            before += __shfl_sync(0xffffffffu, static_cast<int>(sum), 31);
+            const int cta = blockIdx.x;
+            const bool mine = cta >= s && cta < end;
+            found = __any_sync(0xffffffffu, mine);
+            if (mine && threadIdx.x < 32) {
+                const int n = static_cast<int>(units), h = (cta - s) / n, j = cta - s - h * n;
+                const int pages = static_cast<int>(pages0[u]), piece = (pages + n - 1) / n;
+                sm.b = 32 * u + lane;
+                sm.hk = h;
+                sm.a = j * piece;
+                sm.e = min((j + 1) * piece, pages);
+                sm.f = cta - j;
+                sm.last = sm.f + n - 1;
+            }
+        }
+        if (!found) return;
+    }
+    __syncthreads();
+    if (!clusters) b = sm.b, hk = sm.hk, a = sm.a, e = sm.e, whole = sm.f == sm.last;
+    const int G = p.G;
+    const Span sp = span_of(p, b);
+    __nv_bfloat16 *out = p.out + (static_cast<int64_t>(b) * p.Hq + hk * G) * D;
+    if (sp.pages == 0) {
+        for (int x = threadIdx.x; x < G * D; x += kDecThreads) out[x] = __float2bfloat16_rn(0.0f);
+        return;
+    }
+    run_segment<D, true>(p, sm, ring, b, hk, sp, a, e, whole,
+                         clusters ? sm.part : partial_of(p, D, blockIdx.x, a == 0));
+    drain(sm, ring);
+    if (whole) return;
+    if (!clusters) {
+        arrive_and_join(p, sm);
+        return;
+    }
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+    // This CTA's part of the output, four values from each CTA of the cluster
+    // by neighbouring lanes.
+    const int chunks = G * D / 4, per = (chunks + kCluster - 1) / kCluster;
+    const int from = threadIdx.x % kCluster, i = threadIdx.x / kCluster, chunk = rank * per + i;
+    const bool valid = i < per && chunk < chunks;
+    const int h = 4 * chunk / D;
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    float top = -3.0e38f, sum = 0.0f, sink = 0.0f;
+    if (valid) {
+        const uint32_t part = peer_addr(sm.part, from);
+        o = peer_f32x4(part + 16 * chunk);
+        top = peer_f32(part + 4 * (G * D + h));
+        sum = peer_f32(part + 4 * (G * (D + 1) + h));
+    }
+    float to = top;
+#pragma unroll
+    for (int d = kCluster / 2; d > 0; d >>= 1) to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, d));
+    if (valid && p.sinks) {
+        sink = __bfloat162float(p.sinks[hk * G + h]) * 1.4426950408889634f;
+        to = fmaxf(to, sink);
+    }
+    const float f = fast_exp2(top - to);
+    sum *= f;
+    o.x *= f, o.y *= f, o.z *= f, o.w *= f;
+#pragma unroll
+    for (int d = kCluster / 2; d > 0; d >>= 1) {
+        sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        o.x += __shfl_xor_sync(0xffffffffu, o.x, d), o.y += __shfl_xor_sync(0xffffffffu, o.y, d);
+        o.z += __shfl_xor_sync(0xffffffffu, o.z, d), o.w += __shfl_xor_sync(0xffffffffu, o.w, d);
+    }
+    // No CTA leaves before all have read its shared memory.
+    asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+    if (valid && from == 0) {
+        if (p.sinks) sum += fast_exp2(sink - to);
+        reinterpret_cast<uint2 *>(out)[chunk] = make_uint2(pack_bf16(F2{o.x / sum, o.y / sum}),
+                                                           pack_bf16(F2{o.z / sum, o.w / sum}));
+    }
+    asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+}
+
+// Lets the kernels have their shared memory, once for each device; the clusters
+// of kv4_decode_few_kernel that the device holds at once (as many as whole
+// groups of SMs have room for), or a negative status.
+template <int D> int configure(int dev) {
+    static std::atomic<int> held[64];   // and 1 more; 0: not known yet
+    int n = dev < 64 ? held[dev].load(std::memory_order_acquire) - 1 : -1;
+    if (n >= 0) return n;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(kCluster);
+    cfg.blockDim = dim3(32 * dec_warps(true));
+    cfg.dynamicSmemBytes = sizeof(DecodeSmem<D, true>);
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = kCluster;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (cudaFuncSetAttribute(kv4_decode_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             sizeof(DecodeSmem<D, false>)) != cudaSuccess ||
+        cudaFuncSetAttribute(kv4_decode_few_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             sizeof(DecodeSmem<D, true>)) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, kv4_decode_few_kernel<D>, &cfg) != cudaSuccess) {
         cudaGetLastError();
         return XS_EDEVICE;
     }
-    done.fetch_or(bit, std::memory_order_release);
-    return XS_OK;
+    n = min(n, kMaxCtas / kCluster);
+    if (dev < 64) held[dev].store(n + 1, std::memory_order_release);
+    return n;
 }
 
-template <int D, bool kFew>
-int launch(const Kv4DecodeParams &p, int dev, int sms, cudaStream_t stream) {
-    const int rc = configure<D, kFew>(dev);
-    if (rc != XS_OK) return rc;
-    // The line is at most so long, and no CTA takes less than kMinShare of it.
+template <int D> int launch(const Kv4DecodeParams &p, int dev, int sms, cudaStream_t stream) {
+    const int few = configure<D>(dev);
+    if (few < 0) return few;
     const int64_t segments = static_cast<int64_t>(p.B) * p.Hkv;
+    if (segments < few && p.B <= 64) {
+        const int clusters = p.max_blocks <= kClusterPages ? static_cast<int>(segments) : few;
+        return launch_after(kv4_decode_few_kernel<D>, dim3(clusters * kCluster), 32 * dec_warps(true),
+                            sizeof(DecodeSmem<D, true>), stream, kCluster, p);
+    }
+    // The line is at most so long, and no CTA takes less than kMinShare of it.
     const int64_t want =
         segments + (segments * (p.max_blocks + kSegmentCost) + kMinShare - 1) / kMinShare;
-    const int fill = min(sms * ctas_per_sm(kFew), kMaxCtas);
-    return launch_after(kv4_decode_kernel<D, kFew>, dim3(static_cast<int>(want < fill ? want : fill)),
-                        32 * dec_warps(kFew), sizeof(DecodeSmem<D, kFew>), stream, 1, p);
+    const int fill = min(sms * ctas_per_sm(false), kMaxCtas);
+    return launch_after(kv4_decode_kernel<D>, dim3(static_cast<int>(want < fill ? want : fill)),
+                        32 * dec_warps(false), sizeof(DecodeSmem<D, false>), stream, 1, p);
 }
 
 }  // namespace
@@ -794,10 +982,5 @@ extern "C" int xs_kv4_decode(void *out, const void *q, const void *k_cache, cons
     if (cudaGetDevice(&dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
         return XS_EDEVICE;
-    // Many segments: CTAs of 4 warps on a common line; few: of 8, in pieces.
-    const bool few = static_cast<int64_t>(B) * Hkv * xs::kFewSegments <=
-                     static_cast<int64_t>(sms) * xs::ctas_per_sm(true);
-    if (D == 128)
-        return few ? xs::launch<128, true>(p, dev, sms, stream) : xs::launch<128, false>(p, dev, sms, stream);
-    return few ? xs::launch<64, true>(p, dev, sms, stream) : xs::launch<64, false>(p, dev, sms, stream);
+    return D == 128 ? xs::launch<128>(p, dev, sms, stream) : xs::launch<64>(p, dev, sms, stream);
 }

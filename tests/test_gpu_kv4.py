@@ -222,6 +222,19 @@ def test_decode_many_or_few_sequences(B, Hkv, G, D):
                  sinks=torch.randn(G * Hkv, generator=gen(2), device=device()).to(BF))
 
 
+@pytest.mark.parametrize("Hkv,G,D", [(8, 4, 128), (8, 8, 64), (1, 1, 64), (5, 2, 128)])
+@pytest.mark.parametrize("lens", [[240], [257], [4096], [4097], [8100, 3], [12000], [16, 0, 4500, 300],
+                                  [5000, 0, 9, 700]])
+def test_decode_few_sequences(lens, Hkv, G, D):
+    # One CTA, one cluster, or all CTAs to a segment, and empty sequences
+    # among them; with tables that hold no more, and with wider ones.
+    a = setup(lens, G * Hkv, Hkv, D, seed=sum(lens))
+    check_decode(*a, 1 / math.sqrt(D))
+    z = torch.randn(G * Hkv, generator=gen(4), device=device()).to(BF) * 3
+    check_decode(*setup(lens, G * Hkv, Hkv, D, seed=sum(lens), width=900), 1 / math.sqrt(D), sinks=z,
+                 window=max(lens) - 5)
+
+
 @pytest.mark.parametrize("n", [5, 40, 300, 5000])
 def test_every_token_counts_once(n):
     # q = 0: all weights are 1 / n; V is zero but for one token, so the result

@@ -29,59 +29,107 @@
 
 namespace xs {
 
+// Two fp32 values in one operation.
+struct F2 {
+    float x, y;
+};
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+    F2 r;
+    asm("{\n .reg .b64 p, q, s;\n mov.b64 p, {%2, %3};\n mov.b64 q, {%4, %5};\n"
+        " mul.rn.f32x2 s, p, q;\n mov.b64 {%0, %1}, s;\n}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+    F2 r;
+    asm("{\n .reg .b64 p, q, s;\n mov.b64 p, {%2, %3};\n mov.b64 q, {%4, %5};\n"
+        " add.rn.f32x2 s, p, q;\n mov.b64 {%0, %1}, s;\n}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+__device__ __forceinline__ F2 sub2(F2 a, F2 b) {
+    F2 r;
+    asm("{\n .reg .b64 p, q, s;\n mov.b64 p, {%2, %3};\n mov.b64 q, {%4, %5};\n"
+        " sub.rn.f32x2 s, p, q;\n mov.b64 {%0, %1}, s;\n}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("{\n .reg .b64 p, q, s;\n mov.b64 p, {%2, %3};\n mov.b64 q, {%4, %5};\n"
+        " mov.b64 s, {%6, %7};\n fma.rn.f32x2 s, p, q, s;\n mov.b64 {%0, %1}, s;\n}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return r;
+}
+
 constexpr int kKv4Group = 32;
 __host__ __device__ constexpr int kv4_page_bytes(int D) { return 9 * D; }
 
-// Order of magnitude first, the positive of two equal ones above, NaN above all:
-// the maximum of the keys is the key of a group's extreme.
-__device__ __forceinline__ uint32_t kv4_key(float x) {
-    const uint32_t u = __float_as_uint(x);
-    return (u << 1) | ((u >> 31) ^ 1u);
+// Keys of bf16 values, two to a word: order of magnitude first, the positive of
+// two equal ones above, NaN above all.  The maximum of the keys is the key of a
+// group's extreme.
+__device__ __forceinline__ uint32_t kv4_keys(uint32_t w) {
+    return ((w << 1) & 0xfffefffeu) | (~(w >> 15) & 0x00010001u);
 }
-// The key of the extreme of four bf16 values, two to a word.
-__device__ __forceinline__ uint32_t kv4_key4(uint32_t w0, uint32_t w1) {
-    const __nv_bfloat162 a = *reinterpret_cast<const __nv_bfloat162 *>(&w0);
-    const __nv_bfloat162 b = *reinterpret_cast<const __nv_bfloat162 *>(&w1);
-    const float2 hi = __bfloat1622float2(__hmax2_nan(a, b)), lo = __bfloat1622float2(__hmin2_nan(a, b));
-    float mx, mn;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(mx) : "f"(hi.x), "f"(hi.y));
-    asm("min.NaN.f32 %0, %1, %2;" : "=f"(mn) : "f"(lo.x), "f"(lo.y));
-    return kv4_key(mx >= -mn ? mx : mn);
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
 }
+__device__ __forceinline__ uint32_t kv4_fold(uint32_t keys) { return max(keys & 0xffffu, keys >> 16); }
+// The scale of a group from its extreme's key (in the low half).
 __device__ __forceinline__ float kv4_scale(uint32_t key) {
-    const float e = __uint_as_float((key >> 1) | ((key & 1u) ? 0u : 0x80000000u));
+    const float e = __uint_as_float(((key >> 1) << 16) | ((key & 1u) ? 0u : 0x80000000u));
     return __bfloat162float(__float2bfloat16_rn(e * -0.125f));
 }
-// The codes of four dims under s, the first lowest: rne(x / s), clamped.  The
-// quotient is x times an approximate 1 / s, corrected by its own remainder:
-// where x / s is a half integer (or any fp32 number) that gives it exactly, and
-// elsewhere x / s is at least 1/512 away from a tie, so the rounding is that of
-// the true quotient.  Adding 1.5 2^23 + 8 rounds to the nearest even integer
-// and leaves the code in the low bits; the four are joined by one multiply-add
-// each, and what the constant adds up to is taken off at the end.
+// The codes of four dims under s[0] and of four under s[1] (the same one if
+// `alike`), the first lowest: rne(x / s), clamped.  x
+// times an approximate 1 / s is within 2^-19 of the quotient, which is a half
+// integer or at least 1/512 away from one.  Rounded to a multiple of 2^-10 (by the
+// addition of 1.5 2^13 in one multiply-add) it is exactly the half integer or
+// still on its side of it, and the addition of 1.5 2^23 + 8 - 1.5 2^13, which
+// is exact before its rounding, leaves the code in the low bits.  The quotient is
+// at least -8 (a group's extreme is exactly that), so only the upper end is cut.  The four are joined
+// by one multiply-add each, and what the constant adds up to is taken off at the end.
 // Scales without a usable reciprocal (0, tiny, infinite, NaN) divide instead; a
 // group with an infinity or a NaN gets codes of 8 (a NaN converts to 0) under
 // an infinite or NaN scale, and reads as NaN.
-__device__ __forceinline__ uint32_t kv4_pack4(const float *x, float s) {
-    uint32_t w = 0;
-    if (!(fabsf(s) >= 0x1p-120f && fabsf(s) < INFINITY)) {
+__device__ __forceinline__ void kv4_pack(uint32_t *codes, const float *x, const float *s, bool alike) {
+    const float lo = fminf(fabsf(s[0]), fabsf(s[1])), hi = fabsf(s[0]) + fabsf(s[1]);
+    if (!(lo >= 0x1p-120f && hi < INFINITY)) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int n = s == 0.0f ? 0 : __float2int_rn(__fdiv_rn(x[i], s));
-            w |= static_cast<uint32_t>(min(max(n, -8), 7) + 8) << (4 * i);
+        for (int u = 0; u < 2; ++u) {
+            codes[u] = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int n = s[u] == 0.0f ? 0 : __float2int_rn(__fdiv_rn(x[4 * u + i], s[u]));
+                codes[u] |= static_cast<uint32_t>(min(max(n, -8), 7) + 8) << (4 * i);
+            }
         }
-        return w;
+        return;
     }
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+    float r[2];
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r[0]) : "f"(s[0]));
+    r[1] = r[0];
+    if (!alike) asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r[1]) : "f"(s[1]));
     constexpr uint32_t kBits = 0x4b400000u;     // of 1.5 2^23
+    constexpr float kFine = 0x1.8p13f, kWhole = 0x1.8p23f + 8.0f;
 #pragma unroll
-    for (int i = 3; i >= 0; --i) {
-        float q = x[i] * r;
-        q = fmaf(fmaf(-q, s, x[i]), r, q);
-        w = w * 16u + __float_as_uint(fminf(fmaxf(q, -8.0f), 7.0f) + (0x1.8p23f + 8.0f));
+    for (int u = 0; u < 2; ++u) {
+        uint32_t w = 0;
+#pragma unroll
+        for (int i = 2; i >= 0; i -= 2) {
+            const F2 q = fma2(F2{x[4 * u + i], x[4 * u + i + 1]}, F2{r[u], r[u]}, F2{kFine, kFine});
+            const F2 n = add2(q, F2{kWhole - kFine, kWhole - kFine});
+            w = w * 16u + __float_as_uint(fminf(n.y, kWhole + 7.0f));
+            w = w * 16u + __float_as_uint(fminf(n.x, kWhole + 7.0f));
+        }
+        codes[u] = w - kBits * 0x1111u;
     }
-    return w - kBits * 0x1111u;
 }
 
 // Stores chunk `ch` (8 dims) of row `o` of a page, and the group's scale with

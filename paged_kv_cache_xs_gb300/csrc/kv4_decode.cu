@@ -78,19 +78,6 @@ constexpr int kAlonePages = 16;    // and up to so many one CTA
 constexpr int kStages = 4;         // pages of a warp's ring
 constexpr uint64_t kWaitLimitNs = 4000000000ull;
 
-// Two fp32 values in one operation.
-struct F2 {
-    float x, y;
-};
-__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
-    F2 r;
-    asm("{\n .reg .b64 p, q, s;\n mov.b64 p, {%2, %3};\n mov.b64 q, {%4, %5};\n"
-        " mul.rn.f32x2 s, p, q;\n mov.b64 {%0, %1}, s;\n}"
-        : "=f"(r.x), "=f"(r.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return r;
-}
-
 // d = A B + d
 __device__ __forceinline__ void mma_f16(float *d, uint32_t a0, uint32_t a1, uint32_t a2,
                                         uint32_t a3, uint32_t b0, uint32_t b1) {

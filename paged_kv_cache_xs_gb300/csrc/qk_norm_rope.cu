@@ -115,35 +115,6 @@ template <typename T, int N> struct Chunk {
     }
 };
 
-// Two fp32 values in one operation.
-struct F2 {
-    float x, y;
-};
-__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
-    F2 r;
-    asm("{\n .reg .b64 p, q, s;\n mov.b64 p, {%2, %3};\n mov.b64 q, {%4, %5};\n"
-        " mul.rn.f32x2 s, p, q;\n mov.b64 {%0, %1}, s;\n}"
-        : "=f"(r.x), "=f"(r.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return r;
-}
-__device__ __forceinline__ F2 sub2(F2 a, F2 b) {
-    F2 r;
-    asm("{\n .reg .b64 p, q, s;\n mov.b64 p, {%2, %3};\n mov.b64 q, {%4, %5};\n"
-        " sub.rn.f32x2 s, p, q;\n mov.b64 {%0, %1}, s;\n}"
-        : "=f"(r.x), "=f"(r.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return r;
-}
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
-    F2 r;
-    asm("{\n .reg .b64 p, q, s;\n mov.b64 p, {%2, %3};\n mov.b64 q, {%4, %5};\n"
-        " mov.b64 s, {%6, %7};\n fma.rn.f32x2 s, p, q, s;\n mov.b64 {%0, %1}, s;\n}"
-        : "=f"(r.x), "=f"(r.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-    return r;
-}
-
 // Mean of the squares of a row, of which each of its lanes holds 8 values.
 template <int kLanes> __device__ __forceinline__ float mean_square(const F2 *x) {
     F2 sum = mul2(x[0], x[0]);
@@ -367,13 +338,25 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas)
             if constexpr (kKv4) {
                 y0.to_f32(&x[0].x);
                 y1.to_f32(&x[2].x);
-                uint32_t key[2] = {kv4_key4(y0.w[0], y0.w[1]), kv4_key4(y1.w[0], y1.w[1])};
-                if (kind == 2) {        // the lane's chunks are neighbours: four lanes a group
-                    key[0] = max(key[0], key[1]);
-                    key[0] = max(key[0], __shfl_xor_sync(0xffffffffu, key[0], 1));
-                    key[0] = max(key[0], __shfl_xor_sync(0xffffffffu, key[0], 2));
-                    key[1] = key[0];
-                } else {                // they meet in shared memory
+                uint32_t key[2] = {max_u16x2(kv4_keys(y0.w[0]), kv4_keys(y0.w[1])),
+                                   max_u16x2(kv4_keys(y1.w[0]), kv4_keys(y1.w[1]))};
+                // Where the lane's chunks are neighbours, four lanes hold a group; where
+                // they are of the halves of a whole row, eight lanes hold two; else they
+                // meet in shared memory.
+                const bool near = kind == 2 || p.interleaved || p.rot == 0;
+                if (near) {
+                    uint32_t k = max_u16x2(key[0], key[1]);
+                    k = max_u16x2(k, __shfl_xor_sync(0xffffffffu, k, 1));
+                    k = max_u16x2(k, __shfl_xor_sync(0xffffffffu, k, 2));
+                    key[0] = key[1] = kv4_fold(k);
+                } else if (p.rot == D) {
+                    uint32_t k = max_u16x2(__byte_perm(key[0], key[1], 0x5410),
+                                           __byte_perm(key[0], key[1], 0x7632));
+                    k = max_u16x2(k, __shfl_xor_sync(0xffffffffu, k, 1));
+                    k = max_u16x2(k, __shfl_xor_sync(0xffffffffu, k, 2));
+                    k = max_u16x2(k, __shfl_xor_sync(0xffffffffu, k, 4));
+                    key[0] = k & 0xffffu, key[1] = k >> 16;
+                } else {
                     uint32_t *row_keys = keys[warp][lane / kLanes];
                     __syncwarp();
                     row_keys[c0] = key[0];
@@ -383,16 +366,13 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas)
                     for (int u = 0; u < 2; ++u) {
                         const uint4 *k4 = reinterpret_cast<const uint4 *>(row_keys + ((u ? c1 : c0) & ~7));
                         const uint4 a = k4[0], b = k4[1];
-                        key[u] = max(max(max(a.x, a.y), max(a.z, a.w)), max(max(b.x, b.y), max(b.z, b.w)));
+                        key[u] = kv4_fold(max_u16x2(max_u16x2(max_u16x2(a.x, a.y), max_u16x2(a.z, a.w)),
+                                                    max_u16x2(max_u16x2(b.x, b.y), max_u16x2(b.z, b.w))));
                     }
                 }
-                float scale[2];
+                float scale[2] = {kv4_scale(key[0]), kv4_scale(key[1])};
                 uint32_t half[2];       // four codes each
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    scale[u] = kv4_scale(key[u]);
-                    half[u] = kv4_pack4(&x[2 * u].x, scale[u]);
-                }
+                kv4_pack(half, &x[0].x, scale, near);
                 // The word (8 dims) this lane stores: its own two chunks, or, of
                 // split halves, the first chunk's with the next lane's, or the
                 // second's with the lane before's.

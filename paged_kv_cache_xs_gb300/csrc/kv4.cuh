@@ -11,8 +11,8 @@
 // where s is 0.  The extreme is stored exactly (n = 0), and the sign in s lets
 // the one code that has no partner (-8) serve whichever side is longer.  x and
 // s have 8-bit significands, so x / s is a tie or at least 1/512 away from
-// one: the fp32 quotient rounds as the true one does, and the codes are the
-// same on any machine.
+// one: a quotient in fp32, even an approximate one, can be rounded as the true
+// one is (kv4_pack), and the codes are the same on any machine.
 //
 // The words lie in the order in which the decode attention's matrix
 // instructions want them, so that a lane's fragment of a page is one 16-byte
@@ -80,50 +80,55 @@ __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
     asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
-__device__ __forceinline__ uint32_t kv4_fold(uint32_t keys) { return max(keys & 0xffffu, keys >> 16); }
-// The scale of a group from its extreme's key (in the low half).
-__device__ __forceinline__ float kv4_scale(uint32_t key) {
-    const float e = __uint_as_float(((key >> 1) << 16) | ((key & 1u) ? 0u : 0x80000000u));
-    return __bfloat162float(__float2bfloat16_rn(e * -0.125f));
+// The larger of a word's two keys, in both halves.
+__device__ __forceinline__ uint32_t kv4_fold(uint32_t keys) {
+    return max_u16x2(keys, __byte_perm(keys, keys, 0x1032));
 }
-// The codes of four dims under s[0] and of four under s[1] (the same one if
-// `alike`), the first lowest: rne(x / s), clamped.  x
-// times an approximate 1 / s is within 2^-19 of the quotient, which is a half
-// integer or at least 1/512 away from one.  Rounded to a multiple of 2^-10 (by the
-// addition of 1.5 2^13 in one multiply-add) it is exactly the half integer or
-// still on its side of it, and the addition of 1.5 2^23 + 8 - 1.5 2^13, which
-// is exact before its rounding, leaves the code in the low bits.  The quotient is
-// at least -8 (a group's extreme is exactly that), so only the upper end is cut.  The four are joined
-// by one multiply-add each, and what the constant adds up to is taken off at the end.
-// Scales without a usable reciprocal (0, tiny, infinite, NaN) divide instead; a
-// group with an infinity or a NaN gets codes of 8 (a NaN converts to 0) under
-// an infinite or NaN scale, and reads as NaN.
-__device__ __forceinline__ void kv4_pack(uint32_t *codes, const float *x, const float *s, bool alike) {
-    const float lo = fminf(fabsf(s[0]), fabsf(s[1])), hi = fabsf(s[0]) + fabsf(s[1]);
-    if (!(lo >= 0x1p-120f && hi < INFINITY)) {
+// The bf16 scales of two groups from their extremes' keys.
+__device__ __forceinline__ uint32_t kv4_scales(uint32_t keys) {
+    const uint32_t e = ((keys >> 1) & 0x7fff7fffu) | (~(keys << 15) & 0x80008000u);
+    const __nv_bfloat162 s = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&e),
+                                     __floats2bfloat162_rn(-0.125f, -0.125f));
+    return *reinterpret_cast<const uint32_t *>(&s);
+}
+// The codes of x[0..3] under the low scale and of x[4..7] under the high one,
+// the first lowest: rne(x / s), clamped.  x times an approximate 1 / s is within
+// 2^-19 of the quotient, which is a half integer or at least 1/512 away from
+// one.  Rounded to a multiple of 2^-10 (by the addition of 1.5 2^13 in one
+// multiply-add) it is exactly the half integer or still on its side of it, and
+// the addition of 1.5 2^23 + 8 - 1.5 2^13, which is exact before its rounding,
+// leaves the code in the low bits.  The quotient is at least -8 (a group's
+// extreme is exactly that), so only the upper end is cut.  The four are joined by one
+// multiply-add each, and what the constant adds up to is taken off at the end.
+// Scales without a usable reciprocal are met first: tiny ones (whose own
+// rounding may leave quotients beyond 8) and their values are lifted by 2^64;
+// under 0, infinity or NaN all codes are 8, so that a group with an infinity or
+// a NaN reads as NaN.
+__device__ __forceinline__ void kv4_pack(uint32_t *codes, float *x, uint32_t scales) {
+    float s[2] = {__uint_as_float(scales << 16), __uint_as_float(scales & 0xffff0000u)};
+    if (!(fminf(fabsf(s[0]), fabsf(s[1])) >= 0x1p-120f && fabsf(s[0]) + fabsf(s[1]) < INFINITY)) {
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-            codes[u] = 0;
+            const float a = fabsf(s[u]);
+            const bool none = !(a > 0.0f && a < INFINITY);
+            const float lift = a < 0x1p-120f ? 0x1p64f : 1.0f;
+            s[u] = none ? 1.0f : s[u] * lift;
+            const float most = 8.0f * fabsf(s[u]);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int n = s[u] == 0.0f ? 0 : __float2int_rn(__fdiv_rn(x[4 * u + i], s[u]));
-                codes[u] |= static_cast<uint32_t>(min(max(n, -8), 7) + 8) << (4 * i);
-            }
+            for (int i = 0; i < 4; ++i)
+                x[4 * u + i] = none ? 0.0f : fminf(fmaxf(x[4 * u + i] * lift, -most), most);
         }
-        return;
     }
-    float r[2];
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r[0]) : "f"(s[0]));
-    r[1] = r[0];
-    if (!alike) asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r[1]) : "f"(s[1]));
     constexpr uint32_t kBits = 0x4b400000u;     // of 1.5 2^23
     constexpr float kFine = 0x1.8p13f, kWhole = 0x1.8p23f + 8.0f;
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
+        float r;
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s[u]));
         uint32_t w = 0;
 #pragma unroll
         for (int i = 2; i >= 0; i -= 2) {
-            const F2 q = fma2(F2{x[4 * u + i], x[4 * u + i + 1]}, F2{r[u], r[u]}, F2{kFine, kFine});
+            const F2 q = fma2(F2{x[4 * u + i], x[4 * u + i + 1]}, F2{r, r}, F2{kFine, kFine});
             const F2 n = add2(q, F2{kWhole - kFine, kWhole - kFine});
             w = w * 16u + __float_as_uint(fminf(n.y, kWhole + 7.0f));
             w = w * 16u + __float_as_uint(fminf(n.x, kWhole + 7.0f));
@@ -136,20 +141,19 @@ __device__ __forceinline__ void kv4_pack(uint32_t *codes, const float *x, const 
 // its first chunk.  `page` is the page's first byte.
 template <int D>
 __device__ __forceinline__ void kv4_store_chunk(uint8_t *page, bool is_v, int o, int ch,
-                                                uint32_t w, float s) {
+                                                uint32_t w, uint16_t s) {
     constexpr int NG = D / kKv4Group;
     const int c = ch >> 2, t = ch & 3;
     uint8_t *scales = page + 8 * D;
-    const __nv_bfloat16 sb = __float2bfloat16_rn(s);
     if (is_v) {
         uint16_t *h = reinterpret_cast<uint16_t *>(page);
         const int pair = o >> 1, r = o & 1;
         h[((pair * 8 + 2 * t) * NG + c) * 2 + r] = static_cast<uint16_t>(w);
         h[((pair * 8 + 2 * t + 1) * NG + c) * 2 + r] = static_cast<uint16_t>(w >> 16);
-        if (t == 0) reinterpret_cast<__nv_bfloat16 *>(scales)[(pair * NG + c) * 2 + r] = sb;
+        if (t == 0) reinterpret_cast<uint16_t *>(scales)[(pair * NG + c) * 2 + r] = s;
     } else {
         reinterpret_cast<uint32_t *>(page)[o * (D / 8) + t * NG + c] = w;
-        if (t == 0) reinterpret_cast<__nv_bfloat16 *>(scales)[o * NG + c] = sb;
+        if (t == 0) reinterpret_cast<uint16_t *>(scales)[o * NG + c] = s;
     }
 }
 
@@ -159,14 +163,13 @@ __device__ __forceinline__ void kv4_store_chunk(uint8_t *page, bool is_v, int o,
 // row's those of its last four.
 template <int D>
 __device__ __forceinline__ void kv4_store_pair(uint8_t *page, int o, int ch, uint32_t mine,
-                                               uint32_t theirs, float s) {
+                                               uint32_t theirs, uint16_t s) {
     constexpr int NG = D / kKv4Group;
     const int c = ch >> 2, t = ch & 3, pair = o >> 1, r = o & 1;
-    const uint32_t w = r ? __byte_perm(theirs, mine, 0x7632) : __byte_perm(mine, theirs, 0x5410);
+    const uint32_t w = __byte_perm(mine, theirs, r ? 0x3276 : 0x5410);
     reinterpret_cast<uint32_t *>(page)[(pair * 8 + 2 * t + r) * NG + c] = w;
     if (t == 0)
-        reinterpret_cast<__nv_bfloat16 *>(page + 8 * D)[(pair * NG + c) * 2 + r] =
-            __float2bfloat16_rn(s);
+        reinterpret_cast<uint16_t *>(page + 8 * D)[(pair * NG + c) * 2 + r] = s;
 }
 
 }  // namespace xs

@@ -343,19 +343,19 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas)
                 // Where the lane's chunks are neighbours, four lanes hold a group; where
                 // they are of the halves of a whole row, eight lanes hold two; else they
                 // meet in shared memory.
-                const bool near = kind == 2 || p.interleaved || p.rot == 0;
-                if (near) {
+                uint32_t both;          // the keys of the two chunks' groups
+                if (kind == 2 || p.interleaved || p.rot == 0) {
                     uint32_t k = max_u16x2(key[0], key[1]);
                     k = max_u16x2(k, __shfl_xor_sync(0xffffffffu, k, 1));
                     k = max_u16x2(k, __shfl_xor_sync(0xffffffffu, k, 2));
-                    key[0] = key[1] = kv4_fold(k);
+                    both = kv4_fold(k);
                 } else if (p.rot == D) {
                     uint32_t k = max_u16x2(__byte_perm(key[0], key[1], 0x5410),
                                            __byte_perm(key[0], key[1], 0x7632));
                     k = max_u16x2(k, __shfl_xor_sync(0xffffffffu, k, 1));
                     k = max_u16x2(k, __shfl_xor_sync(0xffffffffu, k, 2));
                     k = max_u16x2(k, __shfl_xor_sync(0xffffffffu, k, 4));
-                    key[0] = k & 0xffffu, key[1] = k >> 16;
+                    both = k;
                 } else {
                     uint32_t *row_keys = keys[warp][lane / kLanes];
                     __syncwarp();
@@ -369,10 +369,11 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas)
                         key[u] = kv4_fold(max_u16x2(max_u16x2(max_u16x2(a.x, a.y), max_u16x2(a.z, a.w)),
                                                     max_u16x2(max_u16x2(b.x, b.y), max_u16x2(b.z, b.w))));
                     }
+                    both = __byte_perm(key[0], key[1], 0x5410);
                 }
-                float scale[2] = {kv4_scale(key[0]), kv4_scale(key[1])};
+                const uint32_t scales = kv4_scales(both);
                 uint32_t half[2];       // four codes each
-                kv4_pack(half, &x[0].x, scale, near);
+                kv4_pack(half, &x[0].x, scales);
                 // The word (8 dims) this lane stores: its own two chunks, or, of
                 // split halves, the first chunk's with the next lane's, or the
                 // second's with the lane before's.
@@ -383,7 +384,8 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas)
                     word = j & 1 ? other | half[1] << 16 : half[0] | other << 16;
                     ch = (j & 1 ? c1 : c0) >> 1;
                 }
-                const float word_scale = kind == 1 && halves && (j & 1) ? scale[1] : scale[0];
+                const uint16_t word_scale =
+                    static_cast<uint16_t>(kind == 1 && halves && (j & 1) ? scales >> 16 : scales);
                 const uint32_t theirs = __shfl_xor_sync(0xffffffffu, word, kLanes);
                 if (writes) {
                     if (kind == 2 && paired)

@@ -75,6 +75,8 @@ constexpr int kWholePages = 32;
 constexpr int kCluster = 8;        // CTAs of a cluster (of 16: 1.5 us more for a start)
 constexpr int kClusterPages = 256; // of a segment: up to so many a cluster always does it
 constexpr int kAlonePages = 16;    // and up to so many one CTA
+constexpr int kLineCluster = 4;    // CTAs of 4 warps of a cluster, for tables of up to
+constexpr int kShortTable = 128;   // so many pages
 constexpr int kStages = 4;         // pages of a warp's ring
 constexpr uint64_t kWaitLimitNs = 4000000000ull;
 
@@ -184,7 +186,7 @@ template <int D, bool kFew> struct alignas(16) DecodeSmem {
     float4 start_at[D / 32][4];
     float m[kDecWarps][8], l[kDecWarps][8];
     float weight[kDecWarps * 8];
-    alignas(16) float part[kFew ? 8 * (D + 2) : 4];     // what the CTA leaves for its cluster
+    alignas(16) float part[8 * (D + 2)];    // what the CTA leaves for its cluster
     // The CTA's place: segment (b, hk), pages [a, e) of it, shared by the CTAs
     // f .. last.  Here so that it holds no registers while a segment runs.
     int b, hk, a, e, f, last, joins;
@@ -590,6 +592,74 @@ __device__ __noinline__ void join_partials(const Kv4DecodeParams &p, DecodeSmem<
     }
 }
 
+__device__ __forceinline__ uint32_t peer_addr(const void *own, int rank) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(own)), "r"(rank));
+    return a;
+}
+__device__ __forceinline__ float peer_f32(uint32_t a) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ float4 peer_f32x4(uint32_t a) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(a)
+                 : "memory");
+    return v;
+}
+// Joins the parts that the CTAs of a cluster hold at `own`, and writes the output.
+template <int kCtas, int kThreads>
+__device__ __forceinline__ void join_cluster(const Kv4DecodeParams &p, const float *own,
+                                             __nv_bfloat16 *out, int hk, int rank, int D) {
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+    // This CTA's part of the output, four values from each CTA of the cluster
+    // by neighbouring lanes.
+    const int G = p.G, chunks = G * D / 4, per = (chunks + kCtas - 1) / kCtas;
+    const int from = threadIdx.x % kCtas;
+    constexpr int kSlots = kThreads / kCtas, kTrips = 256 / kCtas / kSlots;    // G D / 4 <= 256
+#pragma unroll
+    for (int n = 0; n < kTrips; ++n) {
+        if (n * kSlots >= per) break;
+        const int i = n * kSlots + threadIdx.x / kCtas, chunk = rank * per + i, h = 4 * chunk / D;
+        const bool valid = i < per && chunk < chunks;
+        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        float top = -3.0e38f, sum = 0.0f, sink = 0.0f;
+        if (valid) {
+            const uint32_t part = peer_addr(own, from);
+            o = peer_f32x4(part + 16 * chunk);
+            top = peer_f32(part + 4 * (G * D + h));
+            sum = peer_f32(part + 4 * (G * (D + 1) + h));
+        }
+        float to = top;
+#pragma unroll
+        for (int d = kCtas / 2; d > 0; d >>= 1) to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, d));
+        if (valid && p.sinks) {
+            sink = __bfloat162float(p.sinks[hk * G + h]) * 1.4426950408889634f;
+            to = fmaxf(to, sink);
+        }
+        const float f = fast_exp2(top - to);
+        sum *= f;
+        o.x *= f, o.y *= f, o.z *= f, o.w *= f;
+#pragma unroll
+        for (int d = kCtas / 2; d > 0; d >>= 1) {
+            sum += __shfl_xor_sync(0xffffffffu, sum, d);
+            o.x += __shfl_xor_sync(0xffffffffu, o.x, d), o.y += __shfl_xor_sync(0xffffffffu, o.y, d);
+            o.z += __shfl_xor_sync(0xffffffffu, o.z, d), o.w += __shfl_xor_sync(0xffffffffu, o.w, d);
+        }
+        if (valid && from == 0) {
+            if (p.sinks) sum += fast_exp2(sink - to);
+            reinterpret_cast<uint2 *>(out)[chunk] = make_uint2(pack_bf16(F2{o.x / sum, o.y / sum}),
+                                                               pack_bf16(F2{o.z / sum, o.w / sum}));
+        }
+    }
+    // No CTA leaves before all have read its shared memory (what they read is in
+    // registers; the barrier need not wait for the output).
+    asm volatile("barrier.cluster.arrive.relaxed;\n\tbarrier.cluster.wait;" ::: "memory");
+}
+
 // A part of a segment is done: the last of its CTAs joins them.
 template <int D, bool kFew>
 __device__ __forceinline__ void arrive_and_join(const Kv4DecodeParams &p, DecodeSmem<D, kFew> &sm) {
@@ -708,26 +778,6 @@ __global__ void __launch_bounds__(32 * dec_warps(false), ctas_per_sm(false))
     drain(sm, ring);
 }
 
-// ---- few segments: clusters
-
-__device__ __forceinline__ uint32_t peer_addr(const void *own, int rank) {
-    uint32_t a;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(own)), "r"(rank));
-    return a;
-}
-__device__ __forceinline__ float peer_f32(uint32_t a) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
-    return v;
-}
-__device__ __forceinline__ float4 peer_f32x4(uint32_t a) {
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(a)
-                 : "memory");
-    return v;
-}
 // Few segments, in clusters of kCluster CTAs.  Either each segment has a cluster,
 // whose CTAs cut it evenly and join their parts through shared memory (a
 // short one its first CTA alone); or, where that leaves too much to one
@@ -831,45 +881,44 @@ __global__ void __launch_bounds__(32 * dec_warps(true), ctas_per_sm(true))
         arrive_and_join(p, sm);
         return;
     }
-    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
-    // This CTA's part of the output, four values from each CTA of the cluster
-    // by neighbouring lanes.
-    const int chunks = G * D / 4, per = (chunks + kCluster - 1) / kCluster;
-    const int from = threadIdx.x % kCluster, i = threadIdx.x / kCluster, chunk = rank * per + i;
-    const bool valid = i < per && chunk < chunks;
-    const int h = 4 * chunk / D;
-    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    float top = -3.0e38f, sum = 0.0f, sink = 0.0f;
-    if (valid) {
-        const uint32_t part = peer_addr(sm.part, from);
-        o = peer_f32x4(part + 16 * chunk);
-        top = peer_f32(part + 4 * (G * D + h));
-        sum = peer_f32(part + 4 * (G * (D + 1) + h));
+    join_cluster<kCluster, kDecThreads>(p, sm.part, out, hk, rank, D);
+}
+
+// Short segments, not too many: a cluster of kLineCluster CTAs for each, in the line's
+// form of a CTA (4 of them fill an SM).  A segment of up to kAlonePages its
+// first CTA does alone.  (12 sequences of 100, 300, 1K, 2K tokens, 32q/8kv x 128: 5.7, 7.1,
+// 9.3, 13.4 us; on the line 5.8, 7.6, 13.0, 16.4.  The line's kernel itself cannot be launched
+// in clusters for the sake of short calls: it then takes 134 us where it takes 98,
+// for 18 sequences of 20K tokens.)
+template <int D>
+__global__ void __launch_bounds__(32 * dec_warps(false), ctas_per_sm(false))
+    kv4_decode_short_kernel(const __grid_constant__ Kv4DecodeParams p) {
+    constexpr int kDecWarps = dec_warps(false), kDecThreads = 32 * kDecWarps;
+    griddep_wait();
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    DecodeSmem<D, false> &sm = *reinterpret_cast<DecodeSmem<D, false> *>(smem_raw);
+    const int rank = blockIdx.x % kLineCluster, segment = blockIdx.x / kLineCluster;
+    const int b = segment / p.Hkv, hk = segment - b * p.Hkv;
+    // A length past its table is told of by the first CTA alone: it looks at all.
+    if (blockIdx.x == 0)
+        for (int i = threadIdx.x; i < p.B; i += kDecThreads) span_of(p, i);
+    const Span sp = span_of(p, b);
+    const bool alone = sp.pages <= kAlonePages;
+    if (alone && rank) return;          // all but one of the cluster
+    __nv_bfloat16 *out = p.out + (static_cast<int64_t>(b) * p.Hq + hk * p.G) * D;
+    if (sp.pages == 0) {
+        for (int x = threadIdx.x; x < p.G * D; x += kDecThreads) out[x] = __float2bfloat16_rn(0.0f);
+        return;
     }
-    float to = top;
-#pragma unroll
-    for (int d = kCluster / 2; d > 0; d >>= 1) to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, d));
-    if (valid && p.sinks) {
-        sink = __bfloat162float(p.sinks[hk * G + h]) * 1.4426950408889634f;
-        to = fmaxf(to, sink);
-    }
-    const float f = fast_exp2(top - to);
-    sum *= f;
-    o.x *= f, o.y *= f, o.z *= f, o.w *= f;
-#pragma unroll
-    for (int d = kCluster / 2; d > 0; d >>= 1) {
-        sum += __shfl_xor_sync(0xffffffffu, sum, d);
-        o.x += __shfl_xor_sync(0xffffffffu, o.x, d), o.y += __shfl_xor_sync(0xffffffffu, o.y, d);
-        o.z += __shfl_xor_sync(0xffffffffu, o.z, d), o.w += __shfl_xor_sync(0xffffffffu, o.w, d);
-    }
-    // No CTA leaves before all have read its shared memory.
-    asm volatile("barrier.cluster.arrive.release;" ::: "memory");
-    if (valid && from == 0) {
-        if (p.sinks) sum += fast_exp2(sink - to);
-        reinterpret_cast<uint2 *>(out)[chunk] = make_uint2(pack_bf16(F2{o.x / sum, o.y / sum}),
-                                                           pack_bf16(F2{o.z / sum, o.w / sum}));
-    }
-    asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+    if (threadIdx.x < kDecWarps * kStages) mbar_init(&sm.full[0][0] + threadIdx.x, 1);
+    mbar_fence_init();
+    __syncthreads();
+    RingState ring;
+    const int a = alone ? 0 : sp.pages * rank / kLineCluster;
+    const int e = alone ? sp.pages : sp.pages * (rank + 1) / kLineCluster;
+    run_segment<D, false>(p, sm, ring, b, hk, sp, a, e, alone, sm.part);
+    drain(sm, ring);
+    if (!alone) join_cluster<kLineCluster, kDecThreads>(p, sm.part, out, hk, rank, D);
 }
 
 // Lets the kernels have their shared memory, once for each device; the clusters
@@ -893,6 +942,8 @@ template <int D> int configure(int dev) {
                              sizeof(DecodeSmem<D, false>)) != cudaSuccess ||
         cudaFuncSetAttribute(kv4_decode_few_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              sizeof(DecodeSmem<D, true>)) != cudaSuccess ||
+        cudaFuncSetAttribute(kv4_decode_short_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             sizeof(DecodeSmem<D, false>)) != cudaSuccess ||
         cudaOccupancyMaxActiveClusters(&n, kv4_decode_few_kernel<D>, &cfg) != cudaSuccess) {
         cudaGetLastError();
         return XS_EDEVICE;
@@ -911,10 +962,13 @@ template <int D> int launch(const Kv4DecodeParams &p, int dev, int sms, cudaStre
         return launch_after(kv4_decode_few_kernel<D>, dim3(clusters * kCluster), 32 * dec_warps(true),
                             sizeof(DecodeSmem<D, true>), stream, kCluster, p);
     }
+    const int fill = min(sms * ctas_per_sm(false), kMaxCtas);
+    if (segments * kLineCluster <= fill && p.max_blocks <= kShortTable)
+        return launch_after(kv4_decode_short_kernel<D>, dim3(static_cast<int>(segments) * kLineCluster),
+                            32 * dec_warps(false), sizeof(DecodeSmem<D, false>), stream, kLineCluster, p);
     // The line is at most so long, and no CTA takes less than kMinShare of it.
     const int64_t want =
         segments + (segments * (p.max_blocks + kSegmentCost) + kMinShare - 1) / kMinShare;
-    const int fill = min(sms * ctas_per_sm(false), kMaxCtas);
     return launch_after(kv4_decode_kernel<D>, dim3(static_cast<int>(want < fill ? want : fill)),
                         32 * dec_warps(false), sizeof(DecodeSmem<D, false>), stream, 1, p);
 }

@@ -74,9 +74,11 @@ constexpr int kMinShare = 16;      // pages
 constexpr int kWholePages = 32;
 constexpr int kCluster = 8;        // CTAs of a cluster (of 16: 1.5 us more for a start)
 constexpr int kClusterPages = 256; // of a segment: up to so many a cluster always does it
-constexpr int kAlonePages = 16;    // and up to so many one CTA
 constexpr int kLineCluster = 4;    // CTAs of 4 warps of a cluster, for tables of up to
 constexpr int kShortTable = 128;   // so many pages
+// Of a cluster's segment: up to so many pages (2 of a warp) one CTA does alone (18
+// sequences of 200 tokens, 13 pages: 7.8 us so, 6.3 us by a cluster).
+__host__ __device__ constexpr int alone_pages(int warps) { return 2 * warps; }
 constexpr int kStages = 4;         // pages of a warp's ring
 constexpr uint64_t kWaitLimitNs = 4000000000ull;
 
@@ -823,7 +825,7 @@ __global__ void __launch_bounds__(32 * dec_warps(true), ctas_per_sm(true))
         if (b >= p.B) return;           // the whole cluster
         const int pages = static_cast<int>(b < 32 ? __shfl_sync(0xffffffffu, pages0[0], b)
                                                   : __shfl_sync(0xffffffffu, pages0[1], b - 32));
-        whole = pages <= kAlonePages;
+        whole = pages <= alone_pages(kDecWarps);
         a = whole ? 0 : static_cast<int>(static_cast<int64_t>(pages) * rank / kCluster);
         e = whole ? pages : static_cast<int>(static_cast<int64_t>(pages) * (rank + 1) / kCluster);
         if (whole && rank) return;      // all but one
@@ -885,7 +887,7 @@ __global__ void __launch_bounds__(32 * dec_warps(true), ctas_per_sm(true))
 }
 
 // Short segments, not too many: a cluster of kLineCluster CTAs for each, in the line's
-// form of a CTA (4 of them fill an SM).  A segment of up to kAlonePages its
+// form of a CTA (4 of them fill an SM).  A segment of up to alone_pages its
 // first CTA does alone.  (12 sequences of 100, 300, 1K, 2K tokens, 32q/8kv x 128: 5.7, 7.1,
 // 9.3, 13.4 us; on the line 5.8, 7.6, 13.0, 16.4.  The line's kernel itself cannot be launched
 // in clusters for the sake of short calls: it then takes 134 us where it takes 98,
@@ -903,7 +905,7 @@ __global__ void __launch_bounds__(32 * dec_warps(false), ctas_per_sm(false))
     if (blockIdx.x == 0)
         for (int i = threadIdx.x; i < p.B; i += kDecThreads) span_of(p, i);
     const Span sp = span_of(p, b);
-    const bool alone = sp.pages <= kAlonePages;
+    const bool alone = sp.pages <= alone_pages(kDecWarps);
     if (alone && rank) return;          // all but one of the cluster
     __nv_bfloat16 *out = p.out + (static_cast<int64_t>(b) * p.Hq + hk * p.G) * D;
     if (sp.pages == 0) {
@@ -921,54 +923,73 @@ __global__ void __launch_bounds__(32 * dec_warps(false), ctas_per_sm(false))
     if (!alone) join_cluster<kLineCluster, kDecThreads>(p, sm.part, out, hk, rank, D);
 }
 
-// Lets the kernels have their shared memory, once for each device; the clusters
-// of kv4_decode_few_kernel that the device holds at once (as many as whole
-// groups of SMs have room for), or a negative status.
-template <int D> int configure(int dev) {
-    static std::atomic<int> held[64];   // and 1 more; 0: not known yet
-    int n = dev < 64 ? held[dev].load(std::memory_order_acquire) - 1 : -1;
-    if (n >= 0) return n;
+// The clusters of a kernel that the device holds at once (as many as whole
+// groups of SMs have room for), once it may have its shared memory; or -1.
+template <typename K> int clusters_held(K kernel, int ctas, int threads, int smem) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(kCluster);
-    cfg.blockDim = dim3(32 * dec_warps(true));
-    cfg.dynamicSmemBytes = sizeof(DecodeSmem<D, true>);
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = kCluster;
+    attr.val.clusterDim.x = ctas;
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        return -1;
+    }
+    return min(n, kMaxCtas / ctas);
+}
+struct Held {
+    int few, brief;     // clusters of the few and of the short kernel
+};
+// Asked for once for each device (by two threads at once: twice, with one answer).
+template <int D> int configure(int dev, Held *held) {
+    static std::atomic<uint32_t> known[64];     // few and brief, and 1 more each; 0: not yet
+    const uint32_t v = dev < 64 ? known[dev].load(std::memory_order_acquire) : 0;
+    if (v) {
+        *held = Held{static_cast<int>(v & 0xffff) - 1, static_cast<int>(v >> 16) - 1};
+        return XS_OK;
+    }
     if (cudaFuncSetAttribute(kv4_decode_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             sizeof(DecodeSmem<D, false>)) != cudaSuccess ||
-        cudaFuncSetAttribute(kv4_decode_few_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             sizeof(DecodeSmem<D, true>)) != cudaSuccess ||
-        cudaFuncSetAttribute(kv4_decode_short_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             sizeof(DecodeSmem<D, false>)) != cudaSuccess ||
-        cudaOccupancyMaxActiveClusters(&n, kv4_decode_few_kernel<D>, &cfg) != cudaSuccess) {
+                             sizeof(DecodeSmem<D, false>)) != cudaSuccess) {
         cudaGetLastError();
         return XS_EDEVICE;
     }
-    n = min(n, kMaxCtas / kCluster);
-    if (dev < 64) held[dev].store(n + 1, std::memory_order_release);
-    return n;
+    held->few = clusters_held(kv4_decode_few_kernel<D>, kCluster, 32 * dec_warps(true),
+                              sizeof(DecodeSmem<D, true>));
+    held->brief = clusters_held(kv4_decode_short_kernel<D>, kLineCluster, 32 * dec_warps(false),
+                                sizeof(DecodeSmem<D, false>));
+    if (held->few < 0 || held->brief < 0) return XS_EDEVICE;
+    if (dev < 64)
+        known[dev].store(static_cast<uint32_t>(held->few + 1) | static_cast<uint32_t>(held->brief + 1) << 16,
+                         std::memory_order_release);
+    return XS_OK;
 }
 
 template <int D> int launch(const Kv4DecodeParams &p, int dev, int sms, cudaStream_t stream) {
-    const int few = configure<D>(dev);
-    if (few < 0) return few;
+    Held held = {};
+    const int rc = configure<D>(dev, &held);
+    if (rc != XS_OK) return rc;
     const int64_t segments = static_cast<int64_t>(p.B) * p.Hkv;
-    if (segments < few && p.B <= 64) {
-        const int clusters = p.max_blocks <= kClusterPages ? static_cast<int>(segments) : few;
+    // The pages of a segment are at most those of the table, and of the window.
+    const int most = p.window > 0 ? min(p.max_blocks, p.window / 16 + 2) : p.max_blocks;     // pages
+    if (segments < held.few && p.B <= 64) {
+        const int clusters = most <= kClusterPages ? static_cast<int>(segments) : held.few;
         return launch_after(kv4_decode_few_kernel<D>, dim3(clusters * kCluster), 32 * dec_warps(true),
                             sizeof(DecodeSmem<D, true>), stream, kCluster, p);
     }
-    const int fill = min(sms * ctas_per_sm(false), kMaxCtas);
-    if (segments * kLineCluster <= fill && p.max_blocks <= kShortTable)
+    if (segments <= held.brief && most <= kShortTable)
         return launch_after(kv4_decode_short_kernel<D>, dim3(static_cast<int>(segments) * kLineCluster),
                             32 * dec_warps(false), sizeof(DecodeSmem<D, false>), stream, kLineCluster, p);
     // The line is at most so long, and no CTA takes less than kMinShare of it.
     const int64_t want =
         segments + (segments * (p.max_blocks + kSegmentCost) + kMinShare - 1) / kMinShare;
+    const int fill = min(sms * ctas_per_sm(false), kMaxCtas);
     return launch_after(kv4_decode_kernel<D>, dim3(static_cast<int>(want < fill ? want : fill)),
                         32 * dec_warps(false), sizeof(DecodeSmem<D, false>), stream, 1, p);
 }

@@ -235,6 +235,24 @@ def test_decode_few_sequences(lens, Hkv, G, D):
                  window=max(lens) - 5)
 
 
+@pytest.mark.parametrize("B,Hkv,G,D", [(5, 8, 4, 128), (17, 8, 8, 128), (18, 8, 8, 64), (70, 2, 1, 64), (100, 1, 2, 128)])
+def test_decode_batches_of_short_tables(B, Hkv, G, D):
+    # From empty to 128 pages, a CTA or a cluster for each; and a table one wider.
+    lens = [(0, 1, 16, 255, 256, 257, 600, 2048, 1999, 3)[i % 10] for i in range(B)]
+    z = torch.randn(G * Hkv, generator=gen(4), device=device()).to(BF) * 3
+    for width in (128, 129):
+        a = setup(lens, G * Hkv, Hkv, D, seed=B, width=width)
+        one = check_decode(*a, 1 / math.sqrt(D))
+        two = check_decode(*a, 1 / math.sqrt(D), sinks=z, window=300)
+        assert not torch.equal(one, two)
+    q, kc, vc, bt, n = setup(lens, G * Hkv, Hkv, D, seed=B, width=128)
+    n[B - 1] = 128 * 16 + 1                 # past the table: told, and clamped
+    bt[B - 1] = bt[7 % B][:1]
+    out, err = torch.empty_like(q), flag()
+    ops.xs_kv4_decode(out, q, kc, vc, bt, n, 0.1, ops.Kv4Workspace(B, G * Hkv, Hkv, D, device()), err_flag=err)
+    assert int(err) == ops.FLAG_BAD_LEN
+
+
 @pytest.mark.parametrize("n", [5, 40, 300, 5000])
 def test_every_token_counts_once(n):
     # q = 0: all weights are 1 / n; V is zero but for one token, so the result

@@ -372,6 +372,68 @@ def test_nan_in_a_sequence_stays_in_its_head():
     check_decode(q, kc, vc, bt, lens, 0.125, ws=ws, what="the workspace is clean afterwards")
 
 
+@pytest.mark.parametrize("lens,Hkv,D", [([900, 40], 2, 64), ([9000, 40], 2, 128), ([300] * 50, 2, 128),
+                                        ([600, 1200] * 40, 4, 64)])
+def test_infinities_stay_where_they_are(lens, Hkv, D):
+    # A NaN in one head's query, an infinity in one sequence's K and a NaN in a
+    # group of its V, in every form of the call: other heads, sequences and (for
+    # V) groups are as without them.
+    q, kc, vc, bt, n = setup(lens, 4 * Hkv, Hkv, D, seed=11)
+    good = check_decode(q, kc, vc, bt, n, 0.1)
+    ws = ops.Kv4Workspace(len(lens), 4 * Hkv, Hkv, D, device())
+    q[0, 1] = float("nan")
+    one = int(bt[1, 1])                         # block of tokens 16 .. 31 of sequence 1
+    row = torch.zeros(1, Hkv, D, dtype=BF, device=device())
+    row[0, 0, 3] = float("inf")
+    value = torch.zeros(1, Hkv, D, dtype=BF, device=device())
+    value[0, 1, 40] = float("nan")
+    ops.xs_kv4_append(row, value, kc, vc, torch.tensor([16 * one + 5], device=device()))
+    out = torch.empty_like(q)
+    ops.xs_kv4_decode(out, q, kc, vc, bt, n, 0.1, ws)
+    bad = out.isnan()
+    want = torch.zeros_like(bad)
+    want[0, 1] = True
+    want[1, :4] = True                          # KV head 0 of sequence 1
+    want[1, 4:8, 32:64] = True                  # the group of dim 40 of its KV head 1
+    assert torch.equal(bad, want)
+    same = torch.ones(len(lens), 4 * Hkv, dtype=torch.bool, device=device())
+    same[0, 1] = False
+    same[1] = False
+    assert torch.equal(out[same], good[same])
+
+
+def test_calls_from_several_threads():
+    # Each thread with its stream and workspace, in each of the call's forms.
+    import threading
+
+    dev = device()
+    cases = [setup([290], 8, 2, 128, seed=1), setup([6000, 20], 64, 8, 128, seed=2),
+             setup([310 - i for i in range(9)], 64, 8, 64, seed=3),
+             setup([100 + i for i in range(40)], 64, 8, 128, seed=4)]
+    want = [check_decode(*c, 0.1) for c in cases]
+    torch.cuda.synchronize()
+    got = [None] * 8
+
+    def work(i):
+        q, kc, vc, bt, n = cases[i % 4]
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            ws = ops.Kv4Workspace(q.shape[0], q.shape[1], kc.shape[1], q.shape[2], dev)
+            out = torch.empty_like(q)
+            for _ in range(100):
+                ops.xs_kv4_decode(out, q, kc, vc, bt, n, 0.1, ws)
+            s.synchronize()
+        got[i] = out
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(8)]
+    for x in threads:
+        x.start()
+    for x in threads:
+        x.join()
+    for i in range(8):
+        assert torch.equal(got[i], want[i % 4]), i
+
+
 def test_same_result_every_time_and_across_batches():
     # Bit-identical on repetition, on a reused workspace after other batches,
     # on a side stream and from a graph whose lengths change between replays.

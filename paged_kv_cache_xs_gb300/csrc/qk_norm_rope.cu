@@ -20,7 +20,7 @@
 // before it is short of bytes: fp32 goes two to an operation, the weights lie
 // in shared memory as fp32, addresses advance by a step, and a lane holds so
 // little that many warps are resident.  (8K tokens of 32q/8kv x 128 in bf16:
-// 58 us with one value to an operation, 47 us with one row ahead, 40 us so; a copy of
+// 58 us with one value to an operation, 47 us with one row ahead, 35 us so; a copy of
 // as many bytes takes 32 us.)
 //
 // A warp takes kRows consecutive tokens, one for each of its lane groups, and
@@ -38,10 +38,11 @@ namespace xs {
 namespace {
 
 constexpr int kRopeThreads = 128;
-constexpr int kRopeCtas = 6;        // on an SM
+constexpr int kRopeCtas = 7;        // on an SM: 72 registers, a few of them spilled (with
+                                    // 6 and none spilled 39 us where it is 36)
 constexpr int kRopeAheadBytes = 8;  // rows of a lane on their way, times the size of a value
-constexpr int kRopeRun = 16;
-constexpr int kRopeWarpsPerSm = 24;
+constexpr int kRopeRun = 48;        // heads of a run at most
+constexpr int kRopeStart = 4;       // rows that a warp's start costs as much as
 
 struct RopeParams {
     const void *q, *k, *v;      // rows of head h of token t at t * stride + h * D
@@ -409,11 +410,20 @@ int launch(RopeParams &p, int D, int dtype, cudaStream_t stream) {
     if (cudaGetDevice(&dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
         return XS_EDEVICE;
-    // Runs as long as leave kRopeWarpsPerSm warps for every SM, of kRopeRun heads at most.
+    // Single heads while the warps all fit; else the run whose waves of warps take the
+    // fewest rows (4K tokens into a 4-bit cache, two runs of 24 heads in one
+    // wave: 23.6 us; three of 16 in two: 28.4 us).
     const int rows = 256 / D;   // tokens of a warp
     const int64_t blocks = (static_cast<int64_t>(p.T) + rows - 1) / rows;
-    const int64_t all = blocks * p.rows_per_token, least = static_cast<int64_t>(sms) * kRopeWarpsPerSm;
-    p.run = static_cast<int>(all / least < 1 ? 1 : all / least > kRopeRun ? kRopeRun : all / least);
+    const int64_t held = static_cast<int64_t>(sms) * (kRopeCtas * kRopeThreads / 32);
+    p.run = 1;
+    if (blocks * p.rows_per_token > held) {
+        int64_t least = INT64_MAX;
+        for (int run = 1; run <= kRopeRun && run <= p.rows_per_token; ++run) {
+            const int64_t runs = (p.rows_per_token + run - 1) / run, waves = (blocks * runs + held - 1) / held;
+            if (waves * (run + kRopeStart) < least) least = waves * (run + kRopeStart), p.run = run;
+        }
+    }
     const int64_t items = blocks * ((p.rows_per_token + p.run - 1) / p.run);
     const int64_t want = (items + kRopeThreads / 32 - 1) / (kRopeThreads / 32);
     if (want > INT_MAX) return XS_EUNSUPPORTED;

@@ -478,8 +478,9 @@ extern "C" int xs_block_fork(const int32_t *parents, const int32_t *children, in
         return XS_ESHAPE;
     if (n == 0) return XS_OK;
     const int threads = n <= 8 ? xs::kShareThreads / 4 : xs::kShareThreads;
-    return xs::launch_after(xs::block_fork_kernel, dim3(1), threads, 0, stream, 1, parents, children, n, block_tables, max_blocks_per_seq, context_lens, B, block_size,
-        free_stack, free_top, extra_refs, num_blocks, copies, err_flag);
+    return xs::launch_after(xs::block_fork_kernel, dim3(1), threads, 0, stream, 1, parents, children,
+                            n, block_tables, max_blocks_per_seq, context_lens, B, block_size,
+                            free_stack, free_top, extra_refs, num_blocks, copies, err_flag);
 }
 
 extern "C" int xs_block_release(const int32_t *seq_ids, int n, int32_t *block_tables,
@@ -539,8 +540,10 @@ extern "C" int xs_block_copy(void *k_pools, void *v_pools, int layers, int64_t l
     const int64_t piece = static_cast<int64_t>(xs::kCopyThreads) * xs::kCopyUnroll;
     const int64_t per_pair = (chunks + piece - 1) / piece * layers * 2;
     const int64_t most = static_cast<int64_t>(sms) * 8;
-    const int grid = static_cast<int>(n < most / per_pair + 1 ? n * per_pair < most ? n * per_pair : most : most);
-    return xs::launch_after(xs::block_copy_kernel, dim3(grid), xs::kCopyThreads, 0, stream, 1,
-                            static_cast<uint4 *>(k_pools), static_cast<uint4 *>(v_pools), layers,
-        layer_stride_bytes / 16, pairs, n, count, chunks, num_blocks, err_flag);
+    int64_t grid = most;
+    if (n <= most / per_pair && n * per_pair < most) grid = n * per_pair;
+    return xs::launch_after(xs::block_copy_kernel, dim3(static_cast<int>(grid)), xs::kCopyThreads, 0,
+                            stream, 1, static_cast<uint4 *>(k_pools), static_cast<uint4 *>(v_pools),
+                            layers, layer_stride_bytes / 16, pairs, n, count, chunks, num_blocks,
+                            err_flag);
 }

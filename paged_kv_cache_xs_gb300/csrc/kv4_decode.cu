@@ -51,7 +51,8 @@
 // written at once.  One that is cut leaves fp32 partials in the workspace, at
 // most two for each CTA whatever the batch, and the CTA that finishes it last
 // joins them in order: the result does not depend on which that is.  Where
-// segments are few, thread-block clusters take them (kv4_decode_few_kernel).
+// segments are few, or short and not too many, thread-block clusters take them
+// (kv4_decode_few_kernel, kv4_decode_short_kernel).
 #include <atomic>
 
 #include <cuda_fp16.h>

@@ -827,7 +827,8 @@ int xs_kv4_unpack(void *k_out, void *v_out, const void *k_cache, const void *v_c
  * stand for.  One call does the whole of it; how a batch is cut is decided on
  * the device from the lengths.  context_lens[b] <= 0 gives out[b] = 0.
  * Whatever the pages hold in rows at and behind a sequence's length, or in
- * front of its window, has no influence.
+ * front of its window, has no influence.  Logits, weights and sums are held in
+ * fp32 (a weight times a V scale to 16 bits); the output is rounded once.
  *
  * workspace: at least xs_kv4_decode_workspace_bytes(B, Hq, Hkv, D) bytes, 16-
  * byte aligned, zero before the first call that uses it; every completed call

@@ -21,8 +21,12 @@
 //            the matrix instructions: 158 us, where this takes 154 us.)
 //   values   O[d, h] = sum_t (n_td - 8) (p_th s_tc), dims on the rows, heads on
 //            the columns, bf16, whose range p s needs.  p s is one product in
-//            fp32 and one rounding (2^-9); n - 8 is exact.  The scale meets p,
-//            not the codes: 4 products for a token and head in place of D.
+//            fp32, which enters as the sum of two bf16 values, what it rounds to
+//            and what that leaves (2^-16 of it is lost): with the first alone
+//            (2^-8) the output was off by 0.0023 of its size where fp32 weights
+//            leave 0.0017, its own rounding, and the long batch took 154 us in
+//            place of 169.  n - 8 is exact.  The scale meets p, not the codes:
+//            4 products for a token and head in place of D.
 //
 // What bounds it (32 sequences of 4K to 32K tokens, 32q/8kv x 128, 680 MB): 154 us,
 // 4.4 TB/s, by the instructions of a page and their latencies.  An earlier form
@@ -452,15 +456,20 @@ __device__ __forceinline__ void run_segment(const Kv4DecodeParams &p, DecodeSmem
         start(k + kStages);
 #pragma unroll
         for (int c = 0; c < NG; ++c) {
-            uint32_t w[2];
+            uint32_t w[2], rest[2];     // the weights times the scales: w + rest
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
-                w[u] = pack_bf16(mul2(pr[u], F2{bf_lo(vs[u][c]), bf_hi(vs[u][c])}));
+            for (int u = 0; u < 2; ++u) {
+                const F2 ps = mul2(pr[u], F2{bf_lo(vs[u][c]), bf_hi(vs[u][c])});
+                w[u] = pack_bf16(ps);
+                rest[u] = pack_bf16(sub2(ps, F2{bf_lo(w[u]), bf_hi(w[u])}));
+            }
 #pragma unroll
-            for (int jj = 0; jj < 2; ++jj)
-                mma_bf16(acc[c][jj], codes_bf16(vw[0][c], 2 * jj),
-                         codes_bf16(vw[0][c], 2 * jj + 1), codes_bf16(vw[1][c], 2 * jj),
-                         codes_bf16(vw[1][c], 2 * jj + 1), w[0], w[1]);
+            for (int jj = 0; jj < 2; ++jj) {
+                const uint32_t n0 = codes_bf16(vw[0][c], 2 * jj), n1 = codes_bf16(vw[0][c], 2 * jj + 1);
+                const uint32_t n2 = codes_bf16(vw[1][c], 2 * jj), n3 = codes_bf16(vw[1][c], 2 * jj + 1);
+                mma_bf16(acc[c][jj], n0, n1, n2, n3, w[0], w[1]);
+                mma_bf16(acc[c][jj], n0, n1, n2, n3, rest[0], rest[1]);
+            }
         }
     }
 

@@ -1,0 +1,105 @@
+"""Decode attention over a 4-bit cache: what its weights are rounded to, and
+values at the ends of their types."""
+import math
+
+import pytest
+import torch
+
+from paged_kv_cache_xs_gb300 import ops
+from paged_kv_cache_xs_gb300.step import Kv4DecodeStep
+from tests import plain_ops as plain
+from tests.gpu_helpers import device
+
+pytestmark = pytest.mark.gpu
+
+BF = torch.bfloat16
+
+
+def gen(seed):
+    return torch.Generator(device=device()).manual_seed(seed)
+
+
+def pages_of(rows, is_v):
+    """Rows [B, pages, Hkv, 16, D] as a pool with the pages in order."""
+    return plain.pack_pages(rows.flatten(0, 1).to(BF), is_v)
+
+
+def tables_of(B, pages, width=None):
+    t = torch.full((B, width or pages), -1, dtype=torch.int32, device=device())
+    t[:, :pages] = torch.arange(B * pages, dtype=torch.int32, device=device()).view(B, pages)
+    return t
+
+
+def attend_fine(q, kc, vc, pages, lens, scale, sinks=None, window=0):
+    """(out, bound) in fp64 where the weights are not rounded to 8 bits.
+
+    The bound: a logit is an fp32 sum of exact products s n q and -8 s q, 34
+    additions to a group of 32, each off by at most 2^-22 of the magnitudes
+    that meet in it (matrix instructions may cut where fp32 would round),
+    which changes a weight by that amount; the exponential and its argument
+    add 2^-21 of the logit's size and 2^-21.  A weight times its scale is a
+    sum of two bf16 values, of which the second is off by half a step of a
+    step: 2^-16.  It enters a sum of up to 64 additions, cut at 2^-22 each:
+    2^-16.  The sum of the weights, the join and the division add under
+    2^-18.  So 2^-14 of the magnitudes in all, and the output is rounded once
+    (2^-8)."""
+    B, Hq, D = q.shape
+    Hkv = kc.shape[1]
+    out = torch.zeros(B, Hq, D, dtype=torch.float64, device=q.device)
+    bound = torch.zeros_like(out)
+    for b, n in enumerate(lens):
+        if n <= 0:
+            continue
+        a = max(0, n - window) if window else 0
+        k, v = (plain.page_values(p[b * pages:b * pages + pages], D, is_v).transpose(0, 1).flatten(1, 2)[:, a:n]
+                for p, is_v in ((kc, False), (vc, True)))                # [Hkv, n, D]
+        qd = q[b].double().view(Hkv, Hq // Hkv, D)
+        x = qd @ k.transpose(1, 2) * scale
+        m = x.amax(-1, keepdim=True)
+        z = None
+        if sinks is not None:
+            z = sinks.double().view(Hkv, Hq // Hkv, 1)
+            m = torch.maximum(m, z)
+        p = torch.exp(x - m)
+        w = p / (p.sum(-1, keepdim=True) + (torch.exp(z - m) if z is not None else 0))
+        out[b] = (w @ v).view(Hq, D)
+        s = k.abs().reshape(*k.shape[:-1], -1, 32).amax(-1) / 7
+        sq = qd.abs().reshape(Hkv, Hq // Hkv, -1, 32).sum(-1)
+        size = abs(scale) * 23 * (sq @ s.transpose(1, 2))
+        off = 34 * 2.0 ** -22 * size + 2.0 ** -21 * (x - m).abs() + 2.0 ** -21
+        off = off + (w * off).sum(-1, keepdim=True)
+        mag = w @ v.abs()
+        bound[b] = ((w * off) @ v.abs() + 2.0 ** -14 * mag).view(Hq, D) + 2.0 ** -8 * out[b].abs() + 1e-37
+    return out, bound
+
+
+def decode(q, kc, vc, bt, lens, scale, sinks=None, window=0):
+    ws = ops.Kv4Workspace(q.shape[0], q.shape[1], kc.shape[1], q.shape[2], q.device)
+    out = torch.full_like(q, 5.0)
+    err = torch.zeros(1, dtype=torch.int32, device=q.device)
+    ops.xs_kv4_decode(out, q, kc, vc, bt, torch.tensor(lens, dtype=torch.int32, device=q.device), scale, ws,
+                      sinks=sinks, window=window, err_flag=err)
+    assert int(err) == 0
+    return out
+
+
+@pytest.mark.parametrize("lens,width,Hkv,G,D", [
+    ([500], None, 2, 4, 128),                       # one cluster
+    ([490, 3, 17], 900, 8, 1, 64),                  # few sequences under a wide table
+    ([1000] * 9, 63, 8, 8, 128),                    # short segments
+    ([400, 513, 0, 33] * 12, 200, 8, 4, 128),       # the line
+    ([16 * 40 + 7] * 40, 300, 8, 2, 64),            # the line, segments cut
+])
+@pytest.mark.parametrize("sinks,window", [(False, 0), (True, 290)])
+def test_weights_are_not_rounded_to_8_bits(lens, width, Hkv, G, D, sinks, window):
+    # Many tokens of like weight: the output is far smaller than what it is
+    # summed from, so that a rounding of the weights shows beside its own.
+    B, pages = len(lens), -(-max(lens) // 16)
+    k, v = (torch.randn(B, pages, Hkv, 16, D, generator=gen(i + B), device=device()) for i in (1, 2))
+    kc, vc = pages_of(k, False), pages_of(v, True)
+    q = torch.randn(B, G * Hkv, D, generator=gen(3), device=device()).to(BF)
+    z = torch.randn(G * Hkv, generator=gen(4), device=device()).to(BF) if sinks else None
+    scale = 0.5 / math.sqrt(D)
+    out = decode(q, kc, vc, tables_of(B, pages, width), lens, scale, z, window)
+    ref, bound = attend_fine(q, kc, vc, pages, lens, scale, z, window)
+    plain.check(out, ref, bound)

@@ -828,7 +828,8 @@ int xs_kv4_unpack(void *k_out, void *v_out, const void *k_cache, const void *v_c
  * the device from the lengths.  context_lens[b] <= 0 gives out[b] = 0.
  * Whatever the pages hold in rows at and behind a sequence's length, or in
  * front of its window, has no influence.  Logits, weights and sums are held in
- * fp32 (a weight times a V scale to 16 bits); the output is rounded once.
+ * fp32 (a weight times a V scale to 16 bits), the weights at most 1 before
+ * their sum divides them; the output is rounded once.
  *
  * workspace: at least xs_kv4_decode_workspace_bytes(B, Hq, Hkv, D) bytes, 16-
  * byte aligned, zero before the first call that uses it; every completed call

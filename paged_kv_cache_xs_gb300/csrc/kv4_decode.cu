@@ -37,9 +37,10 @@
 // time, the next page's logits beside this one's values, multiplications for
 // shifts, and 8-bit matrix instructions all measured the same or slower.
 //
-// The softmax is online, in fp32.  Its reference follows the running maximum
-// only when a logit exceeds it by 2^8, so most pages take no exchange between
-// lanes; p up to 2^8 is harmless in fp32 and bf16.
+// The softmax is online, in fp32.  Its reference is set 8 above the running
+// maximum (of logits in powers of two), and again only when a logit exceeds it, so
+// most pages take no exchange between lanes, and no weight is above 1: a weight
+// times the scale of a V group near the end of bf16 stays finite.
 //
 // Each warp works on pages of its own, which reach its ring of kStages places
 // in shared memory by bulk copies (one for K, one for V) that lane 0 starts
@@ -85,6 +86,7 @@ constexpr int kShortTable = 128;   // so many pages
 // sequences of 200 tokens, 13 pages: 7.8 us so, 6.3 us by a cluster).
 __host__ __device__ constexpr int alone_pages(int warps) { return 2 * warps; }
 constexpr int kStages = 4;         // pages of a warp's ring
+constexpr float kLead = 8.0f;      // of a reference before the largest logit
 constexpr uint64_t kWaitLimitNs = 4000000000ull;
 
 // d = A B + d
@@ -408,11 +410,11 @@ __device__ __forceinline__ void run_segment(const Kv4DecodeParams &p, DecodeSmem
             }
         }
         float hi = fmaxf(fmaxf(x[0].x, x[0].y), fmaxf(x[1].x, x[1].y));
-        if (__any_sync(0xffffffffu, fresh || hi > m + 8.0f)) {
+        if (__any_sync(0xffffffffu, fresh || hi > m)) {
             hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, 1));
             hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, 2));
             // No usable maximum (nothing, or NaN): any finite reference does.
-            const float to = hi > -INFINITY ? (fresh ? hi : fmaxf(m, hi)) : m;
+            const float to = hi > -INFINITY && (fresh || hi > m) ? hi + kLead : m;
             const float f = fresh ? 1.0f : fast_exp2(m - to);
             m = to;
             l *= f;

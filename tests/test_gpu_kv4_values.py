@@ -103,3 +103,39 @@ def test_weights_are_not_rounded_to_8_bits(lens, width, Hkv, G, D, sinks, window
     out = decode(q, kc, vc, tables_of(B, pages, width), lens, scale, z, window)
     ref, bound = attend_fine(q, kc, vc, pages, lens, scale, z, window)
     plain.check(out, ref, bound)
+
+
+FORMS = [(1, None), (1, 2000), (9, 100), (70, 2000)]     # (sequences, table width): few, few, short, the line
+
+
+@pytest.mark.parametrize("B,width", FORMS)
+def test_values_near_the_end_of_bf16(B, width):
+    # Each group of V holds 3 2^122 (a scale of 3 2^119), and the logits of the
+    # second half are 7.9 powers of two above those of the first: a weight
+    # above 1 times the scale would be infinite.  As xs_paged_decode_sinks, whose
+    # weights are at most 1.
+    dev, D, Hkv, G, pages = device(), 128, 8, 2, 16
+    k = torch.zeros(B, pages, Hkv, 16, D, device=dev)
+    k[:, pages // 2:, ..., 0] = 7.9 * math.log(2.0)
+    v = torch.randn(B, pages, Hkv, 16, D, generator=gen(1), device=dev).clamp(-2, 2) * 2.0 ** 120
+    sign = torch.randint(0, 2, (B, pages, Hkv, 16, 4), generator=gen(2), device=dev) * 2.0 - 1
+    v[..., 5::32] = sign * 3 * 2.0 ** 122
+    kc, vc = pages_of(k, False), pages_of(v, True)
+    q = torch.zeros(B, G * Hkv, D, dtype=BF, device=dev)
+    q[..., 0] = 1
+    lens = [16 * pages] * B
+    out = decode(q, kc, vc, tables_of(B, pages, width), lens, 1.0)
+    assert bool(out.isfinite().all())
+    ref, bound = attend_fine(q, kc, vc, pages, lens, 1.0)
+    plain.check(out, ref, bound)
+
+
+@pytest.mark.parametrize("e", [-100, -60, 60, 110])
+def test_values_of_any_magnitude(e):
+    dev, D, Hkv, G, lens = device(), 64, 2, 4, [700, 45, 16]
+    k, v = (torch.randn(3, 44, Hkv, 16, D, generator=gen(i), device=dev) for i in (5, 6))
+    kc, vc = pages_of(k, False), pages_of(v * 2.0 ** e, True)
+    q = torch.randn(3, G * Hkv, D, generator=gen(7), device=dev).to(BF)
+    out = decode(q, kc, vc, tables_of(3, 44), lens, 0.2)
+    ref, bound = attend_fine(q, kc, vc, 44, lens, 0.2)
+    plain.check(out, ref, bound)

@@ -87,6 +87,7 @@ constexpr int kShortTable = 128;   // so many pages
 __host__ __device__ constexpr int alone_pages(int warps) { return 2 * warps; }
 constexpr int kStages = 4;         // pages of a warp's ring
 constexpr float kLead = 8.0f;      // of a reference before the largest logit
+constexpr float kLowest = -3.402823466e38f;     // a reference before any logit above it
 constexpr uint64_t kWaitLimitNs = 4000000000ull;
 
 // d = A B + d
@@ -99,7 +100,7 @@ __device__ __forceinline__ void mma_f16(float *d, uint32_t a0, uint32_t a1, uint
 }
 __device__ __forceinline__ void mma_bf16(float *c, uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
         "{%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -341,8 +342,7 @@ __device__ __forceinline__ void run_segment(const Kv4DecodeParams &p, DecodeSmem
     __syncthreads();
     const uint32_t q0 = smem_addr(&sm.q[0][lane]), s0 = smem_addr(&sm.start_at[0][t]);
 
-    float m = 0.0f, l = 0.0f;   // head g: reference, and this lane's share of the sum
-    bool fresh = true;
+    float m = kLowest, l = 0.0f;    // head g: reference, and this lane's share of the sum
     float acc[NG][2][4];        // dims 32 c + 4 g + 2 jj (+ 1) of heads 2 t, 2 t + 1
 #pragma unroll
     for (int c = 0; c < NG; ++c)
@@ -410,12 +410,13 @@ __device__ __forceinline__ void run_segment(const Kv4DecodeParams &p, DecodeSmem
             }
         }
         float hi = fmaxf(fmaxf(x[0].x, x[0].y), fmaxf(x[1].x, x[1].y));
-        if (__any_sync(0xffffffffu, fresh || hi > m)) {
+        if (__any_sync(0xffffffffu, hi > m)) {
             hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, 1));
             hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, 2));
-            // No usable maximum (nothing, or NaN): any finite reference does.
-            const float to = hi > -INFINITY && (fresh || hi > m) ? hi + kLead : m;
-            const float f = fresh ? 1.0f : fast_exp2(m - to);
+            // A head without a logit above -infinity (or with NaN alone) stays at kLowest,
+            // below every logit to come.
+            const float to = hi > m ? hi + kLead : m;
+            const float f = fast_exp2(m - to);
             m = to;
             l *= f;
             const float f0 = __shfl_sync(0xffffffffu, f, 8 * t);
@@ -429,7 +430,6 @@ __device__ __forceinline__ void run_segment(const Kv4DecodeParams &p, DecodeSmem
                     acc[c][jj][2] *= f0;
                     acc[c][jj][3] *= f1;
                 }
-            fresh = false;
         }
         F2 pr[2];
 #pragma unroll
@@ -465,23 +465,26 @@ __device__ __forceinline__ void run_segment(const Kv4DecodeParams &p, DecodeSmem
                 w[u] = pack_bf16(ps);
                 rest[u] = pack_bf16(sub2(ps, F2{bf_lo(w[u]), bf_hi(w[u])}));
             }
+            uint32_t n[2][4];
 #pragma unroll
             for (int jj = 0; jj < 2; ++jj) {
-                const uint32_t n0 = codes_bf16(vw[0][c], 2 * jj), n1 = codes_bf16(vw[0][c], 2 * jj + 1);
-                const uint32_t n2 = codes_bf16(vw[1][c], 2 * jj), n3 = codes_bf16(vw[1][c], 2 * jj + 1);
-                mma_bf16(acc[c][jj], n0, n1, n2, n3, w[0], w[1]);
-                mma_bf16(acc[c][jj], n0, n1, n2, n3, rest[0], rest[1]);
+                n[jj][0] = codes_bf16(vw[0][c], 2 * jj), n[jj][1] = codes_bf16(vw[0][c], 2 * jj + 1);
+                n[jj][2] = codes_bf16(vw[1][c], 2 * jj), n[jj][3] = codes_bf16(vw[1][c], 2 * jj + 1);
+                mma_bf16(acc[c][jj], n[jj][0], n[jj][1], n[jj][2], n[jj][3], w[0], w[1]);
             }
+#pragma unroll
+            for (int jj = 0; jj < 2; ++jj)
+                mma_bf16(acc[c][jj], n[jj][0], n[jj][1], n[jj][2], n[jj][3], rest[0], rest[1]);
         }
     }
 
     // The warps' shares meet in shared memory.  A warp without pages counts
-    // as l = 0 under the lowest reference.
+    // as l = 0 under kLowest.
     l += __shfl_xor_sync(0xffffffffu, l, 1);
     l += __shfl_xor_sync(0xffffffffu, l, 2);
     __syncthreads();    // all warps have read their last pages
     if (t == 0) {
-        sm.m[warp][g] = fresh ? -3.0e38f : m;
+        sm.m[warp][g] = m;
         sm.l[warp][g] = l;
     }
 #pragma unroll
@@ -554,7 +557,7 @@ __device__ __noinline__ void join_partials(const Kv4DecodeParams &p, DecodeSmem<
     for (int x = 0; x < kPer; ++x) {
         const int e = threadIdx.x + x * kDecThreads, h = 4 * e / D;
         o[x] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        top[x] = -3.0e38f, total[x] = 0.0f;
+        top[x] = kLowest, total[x] = 0.0f;
         if (p.sinks && h < G) {
             top[x] = __bfloat162float(p.sinks[hk * G + h]) * 1.4426950408889634f;
             total[x] = 1.0f;
@@ -640,7 +643,7 @@ __device__ __forceinline__ void join_cluster(const Kv4DecodeParams &p, const flo
         const int i = n * kSlots + threadIdx.x / kCtas, chunk = rank * per + i, h = 4 * chunk / D;
         const bool valid = i < per && chunk < chunks;
         float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        float top = -3.0e38f, sum = 0.0f, sink = 0.0f;
+        float top = kLowest, sum = 0.0f, sink = 0.0f;
         if (valid) {
             const uint32_t part = peer_addr(own, from);
             o = peer_f32x4(part + 16 * chunk);

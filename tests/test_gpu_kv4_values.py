@@ -139,3 +139,32 @@ def test_values_of_any_magnitude(e):
     out = decode(q, kc, vc, tables_of(3, 44), lens, 0.2)
     ref, bound = attend_fine(q, kc, vc, 44, lens, 0.2)
     plain.check(out, ref, bound)
+
+
+@pytest.mark.parametrize("pages", [2, 16, 40])
+@pytest.mark.parametrize("B,width", FORMS)
+def test_logits_of_minus_infinity_beside_very_low_ones(B, width, pages):
+    # Logits below fp32 in the first half's pages, of -1024 or a little less in
+    # the second's: the softmax is that of the second.
+    dev, D, Hkv, G = device(), 64, 8, 1
+    k = torch.zeros(B, pages, Hkv, 16, D, device=dev)
+    k[:, :pages // 2, ..., 0] = -2.0 ** 100
+    k[:, pages // 2:, ..., 0] = -2.0 ** -50
+    k[:, -1, :, 3, 0] = -(2.0 ** -50 + 2.0 ** -57)
+    v = torch.randn(B, pages, Hkv, 16, D, generator=gen(3), device=dev)
+    kc, vc = pages_of(k, False), pages_of(v, True)
+    q = torch.zeros(B, G * Hkv, D, dtype=BF, device=dev)
+    q[..., 0] = 2.0 ** 60
+    q[:, 1, 0] = -2.0 ** -60         # a head with ordinary logits beside it
+    lens = [16 * pages - 1] * B
+    out = decode(q, kc, vc, tables_of(B, pages, width), lens, 1.0)
+    assert bool(out.isfinite().all())
+    mean = plain.page_values(vc, D, True).view(B, pages, Hkv, 16, D)
+    low = mean[:, pages // 2:].transpose(1, 2).flatten(2, 3)[:, :, :-1]       # [B, Hkv, n, D]
+    w = torch.ones(low.shape[2], dtype=torch.float64, device=dev)
+    w[low.shape[2] - 15 + 3] = math.exp(-8.0)
+    ref = (low * (w / w.sum())[:, None]).sum(2)
+    mag = (low.abs() * (w / w.sum())[:, None]).sum(2)
+    others = [0, 2, 3, 4, 5, 6, 7]
+    # (logits of 2^10.5 to 2^-22 of their size: 2^-11.5)
+    plain.check(out[:, others], ref[:, others], (2.0 ** -8 * ref.abs() + 2.0 ** -10 * mag)[:, others])

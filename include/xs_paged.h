@@ -780,7 +780,8 @@ int xs_qk_norm_rope_append_paged(void *q_out, const void *q, int64_t q_stride, c
  * dims.  With e the group's element of largest magnitude (the positive one
  * of a tie) its scale is s = bf16(-e / 8); a value x has the code
  * n = clamp(rne(x / s), -8, 7) + 8 (8 where s is 0) and stands for s (n - 8).
- * A group that holds an infinity or a NaN reads back as NaN.
+ * A group that holds an infinity or a NaN has NaN for its scale, codes of 8, and
+ * reads back as NaN; a page's scales are finite or NaN.
  *   K page: row o is D / 8 32-bit words; word t NG + c (t < 4, c < NG) has
  *           dims 32 c + 8 t + i (i < 8) in bits 4 i .. 4 i + 3.  Scales [o][c].
  *   V page: rows 2 i and 2 i + 1 share D / 4 words; word g NG + c (g < 8) has

@@ -8,7 +8,7 @@
 //
 // Quantisation of a group: e = its element of largest magnitude (the positive
 // one of a tie), s = bf16(-e / 8), n = clamp(rne(x / s), -8, 7) + 8; n = 8
-// where s is 0.  The extreme is stored exactly (n = 0), and the sign in s lets
+// where s is 0, and s is NaN where e is an infinity or NaN.  The extreme is stored exactly (n = 0), and the sign in s lets
 // the one code that has no partner (-8) serve whichever side is longer.  x and
 // s have 8-bit significands, so x / s is a tie or at least 1/512 away from
 // one: a quotient in fp32, even an approximate one, can be rounded as the true
@@ -102,9 +102,10 @@ __device__ __forceinline__ uint32_t kv4_scales(uint32_t keys) {
 // multiply-add each, and what the constant adds up to is taken off at the end.
 // Scales without a usable reciprocal are met first: tiny ones (whose own
 // rounding may leave quotients beyond 8) and their values are lifted by 2^64;
-// under 0, infinity or NaN all codes are 8, so that a group with an infinity or
-// a NaN reads as NaN.
-__device__ __forceinline__ void kv4_pack(uint32_t *codes, float *x, uint32_t scales) {
+// under 0, infinity or NaN all codes are 8, and an infinite scale becomes NaN: a
+// group with an infinity or a NaN is NaN to whatever multiplies by its scale (a
+// sum of n - 8 need not come out as exactly 0).
+__device__ __forceinline__ void kv4_pack(uint32_t *codes, float *x, uint32_t &scales) {
     float s[2] = {__uint_as_float(scales << 16), __uint_as_float(scales & 0xffff0000u)};
     if (!(fminf(fabsf(s[0]), fabsf(s[1])) >= 0x1p-120f && fabsf(s[0]) + fabsf(s[1]) < INFINITY)) {
 #pragma unroll
@@ -112,6 +113,7 @@ __device__ __forceinline__ void kv4_pack(uint32_t *codes, float *x, uint32_t sca
             const float a = fabsf(s[u]);
             const bool none = !(a > 0.0f && a < INFINITY);
             const float lift = a < 0x1p-120f ? 0x1p64f : 1.0f;
+            if (!(a < INFINITY)) scales |= u ? 0x7fff0000u : 0x7fffu;
             s[u] = none ? 1.0f : s[u] * lift;
             const float most = 8.0f * fabsf(s[u]);
 #pragma unroll

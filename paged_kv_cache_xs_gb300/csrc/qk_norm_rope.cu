@@ -372,7 +372,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas)
                     }
                     both = __byte_perm(key[0], key[1], 0x5410);
                 }
-                const uint32_t scales = kv4_scales(both);
+                uint32_t scales = kv4_scales(both);
                 uint32_t half[2];       // four codes each
                 kv4_pack(half, &x[0].x, scales);
                 // The word (8 dims) this lane stores: its own two chunks, or, of

@@ -168,3 +168,23 @@ def test_logits_of_minus_infinity_beside_very_low_ones(B, width, pages):
     others = [0, 2, 3, 4, 5, 6, 7]
     # (logits of 2^10.5 to 2^-22 of their size: 2^-11.5)
     plain.check(out[:, others], ref[:, others], (2.0 ** -8 * ref.abs() + 2.0 ** -10 * mag)[:, others])
+
+
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf")])
+@pytest.mark.parametrize("B,width", FORMS)
+def test_infinite_key_is_nan_whatever_the_query(B, width, bad):
+    # Queries whose products do not sum exactly: a group with an infinity
+    # stands for NaN, and so does its logit.
+    dev, D, Hkv, G, pages = device(), 64, 8, 8, 3
+    k, v = (torch.randn(B, pages, Hkv, 16, D, generator=gen(i), device=dev) for i in (1, 2))
+    kc, vc = pages_of(k, False), pages_of(v, True)
+    row = torch.ones(1, Hkv, D, dtype=BF, device=dev)
+    row[0, 3, 7] = bad
+    ops.xs_kv4_append(row, row * 0, kc, vc, torch.tensor([16 + 5], device=dev))    # token 21 of sequence 0
+    q = 2.0 ** -14 * (1 + torch.rand(B, G * Hkv, D, generator=gen(3), device=dev))
+    q[..., 0::32] = 1
+    q[:, 1::2] *= -1
+    out = decode(q.to(BF), kc, vc, tables_of(B, pages, width), [40] * B, 0.5)
+    want = torch.zeros_like(out, dtype=torch.bool)
+    want[0, 3 * G:4 * G] = True
+    assert torch.equal(out.isnan(), want) and bool(out[~want].isfinite().all())

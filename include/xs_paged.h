@@ -752,7 +752,9 @@ int xs_qk_norm_rope(void *q_out, void *k_out, const void *q, int64_t q_stride, c
  * _append_paged: row b is the new token of sequence b, at position
  * context_lens[b] - 1 of its block table; context_lens[b] <= 0 skips the row
  * (q_out keeps what it held).  A position beyond the table (XS_FLAG_BAD_LEN)
- * or a block outside the pool (XS_FLAG_BAD_BLOCK) is not appended.
+ * or a block outside the pool (XS_FLAG_BAD_BLOCK) is not appended.  A position
+ * >= max_pos is not appended and makes its row of q_out NaN (XS_FLAG_BAD_LEN),
+ * so that an attention that follows gives NaN for it.
  *
  * With XS_CACHE_KV4 the pools are 4-bit pools (below; bf16 only), and the
  * rows are stored as xs_kv4_append would store them.

@@ -222,6 +222,14 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas)
     if (live && p.rot > 0 && pos >= p.max_pos) {
         if (j == 0 && run_begin == 0) raise_flag(p.err_flag, XS_FLAG_BAD_LEN);
         live = false;
+        // A step's attention goes on with q_out: NaN, not an earlier step's query.
+        if (p.lens)
+            for (int h = run_begin; h < min(run_end, p.Hq); ++h) {
+                Chunk<T, 8> none;
+#pragma unroll
+                for (int w = 0; w < Chunk<T, 8>::kWords; ++w) none.w[w] = 0x7fffffffu;
+                none.store(static_cast<T *>(p.q_out) + (t * p.Hq + h) * D + 8 * j);
+            }
     }
     int64_t slot = -1;
     if (live && p.k_cache && run_end > p.Hq)

@@ -513,7 +513,8 @@ def xs_qk_norm_rope_append_paged(q_out, q, k, v, q_weight, k_weight, eps, cos_si
                                  v_cache, block_tables, context_lens, interleaved=False,
                                  err_flag=None, stream=None):
     """The decode step's form: row b is sequence b's new token, at position
-    context_lens[b] - 1 of its block table (a length <= 0 skips the row)."""
+    context_lens[b] - 1 of its block table (a length <= 0 skips the row; a
+    position behind cos_sin makes q_out's row NaN)."""
     _done("xs_qk_norm_rope_append_paged", (_bound or _bind()).xs_qk_norm_rope_append_paged(
         _entry("xs_qk_norm_rope_append_paged"), q_out, q, k, v, q_weight, k_weight, eps, cos_sin,
         k_cache, v_cache, block_tables, context_lens, interleaved, err_flag, _handle(stream)))

@@ -176,7 +176,9 @@ class Kv4DecodeStep:
     4-bit pages, attention (``xs_qk_norm_rope_append_paged``, then
     ``xs_kv4_decode``).
 
-    Owns the attention's workspace and the rotated q.  q_weight, k_weight
+    Owns the attention's workspace and the rotated q.  A sequence whose new
+    token lies behind cos_sin is not appended and its output is NaN (with
+    XS_FLAG_BAD_LEN).  q_weight, k_weight
     ([D], bf16, or None: no norm) and cos_sin (``ops.rope_table``, or None: no
     rotation) are arguments of ``run``, since they differ from layer to layer;
     sinks and window as in PagedDecodeStep."""

@@ -188,3 +188,55 @@ def test_infinite_key_is_nan_whatever_the_query(B, width, bad):
     want = torch.zeros_like(out, dtype=torch.bool)
     want[0, 3 * G:4 * G] = True
     assert torch.equal(out.isnan(), want) and bool(out[~want].isfinite().all())
+
+
+def test_position_behind_the_rotation_table():
+    """A sequence longer than the table of cosines and sines: its row of the
+    step is neither rotated nor appended, and its output is NaN, not what an
+    earlier call's query gives.  The others are as ever."""
+    dev, B, Hq, Hkv, D, nb = device(), 4, 8, 2, 128, 40
+    tab = ops.rope_table(40, D, 1e4, dev)
+    kc, vc = ops.kv4_pools(nb, Hkv, D, dev)
+    bt = torch.arange(nb, dtype=torch.int32, device=dev).view(B, 10)
+    x = torch.randn(2, B, Hq + 2 * Hkv, D, generator=gen(1), device=dev).to(BF)
+    step, alone = Kv4DecodeStep(B, Hq, Hkv, D, dev), Kv4DecodeStep(B, Hq, Hkv, D, dev)
+    lens = torch.tensor([39, 40, 1, 0], dtype=torch.int32, device=dev)
+    out = torch.empty(B, Hq, D, dtype=BF, device=dev)
+
+    def run(s, i):
+        q, k, v = x[i].split([Hq, Hkv, Hkv], 1)
+        s.run(out, q, k, v, None, None, tab, kc, vc, bt, lens, 0.1)
+
+    run(step, 0)
+    assert step.error_flags() == 0 and bool((out[3] == 0).all()) and bool(out.isfinite().all())
+    lens += 1                                              # sequence 1's position is 40
+    before = kc.clone(), vc.clone()
+    run(step, 1)
+    assert step.error_flags() == ops.FLAG_BAD_LEN
+    assert bool(out[1].isnan().all()) and bool(out[[0, 2, 3]].isfinite().all())
+    for pool, was in zip((kc, vc), before):                # nothing of sequence 1's new row
+        assert torch.equal(pool[10:20], was[10:20])
+    got = out.clone()
+    lens[1] = -1
+    run(alone, 1)
+    assert torch.equal(out[[0, 2, 3]], got[[0, 2, 3]]) and alone.error_flags() == 0
+
+
+@pytest.mark.parametrize("dtype", [BF, torch.float32])
+@pytest.mark.parametrize("rot,T,Hq", [(128, 3, 4), (32, 3, 4), (64, 3000, 9)])
+def test_refused_rows_of_the_paged_form_are_nan(rot, T, Hq, dtype):
+    # In q's buffer and in place; rows without a sequence keep what they held.
+    dev, Hkv, D = device(), 1, 128
+    tab = ops.rope_table(20, rot, 1e4, dev)
+    kc, vc = (torch.zeros(T, Hkv, 16, D, dtype=dtype, device=dev) for _ in range(2))
+    bt = torch.arange(T, dtype=torch.int32, device=dev)[:, None].expand(T, 3).contiguous()
+    lens = torch.full((T,), 5, dtype=torch.int32, device=dev)
+    lens[0], lens[1] = 21, 0
+    q, k, v = (torch.randn(T, h, D, generator=gen(h), device=dev).to(dtype) for h in (Hq, 1, 1))
+    for qo in (torch.full_like(q, 3.0), q):
+        err = torch.zeros(1, dtype=torch.int32, device=dev)
+        was = qo[1].clone()
+        ops.xs_qk_norm_rope_append_paged(qo, q, k, v, None, None, 1e-6, tab, kc, vc, bt, lens, err_flag=err)
+        assert int(err) == ops.FLAG_BAD_LEN
+        assert bool(qo[0].isnan().all()) and torch.equal(qo[1], was) and bool(qo[2:].isfinite().all())
+        assert bool((kc[0] == 0).all()) and bool((vc[0] == 0).all()) and bool((vc[2, :, 4] == v[2]).all())

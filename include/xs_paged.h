@@ -841,7 +841,10 @@ int xs_kv4_unpack(void *k_out, void *v_out, const void *k_cache, const void *v_c
  * batches of the same heads too.  bf16 only; block_size 16; D in {64, 128};
  * Hq / Hkv in {1, 2, 4, 8}.
  * Device-side errors: XS_FLAG_BAD_BLOCK (block 0 was read instead),
- * XS_FLAG_BAD_LEN (the length was clamped to the table).
+ * XS_FLAG_BAD_LEN (the length was clamped to the table), XS_FLAG_TIMEOUT (a
+ * page did not arrive within 4 s: the outputs of the sequence and KV head it
+ * belongs to, and of those that its CTA did after it, are NaN; the workspace is
+ * fit for the next call).
  */
 size_t xs_kv4_decode_workspace_bytes(int B, int Hq, int Hkv, int D);
 int xs_kv4_decode(void *out, const void *q, const void *k_cache, const void *v_cache,
@@ -849,6 +852,15 @@ int xs_kv4_decode(void *out, const void *q, const void *k_cache, const void *v_c
                   const void *sinks, int window, int B, int Hq, int Hkv, int D, int block_size,
                   int64_t num_blocks, float scale, void *workspace, size_t workspace_bytes,
                   int dtype, int *err_flag, cudaStream_t stream);
+
+/*
+ * xs_debug_kv4_wait_injection - xs_debug_wait_injection for xs_kv4_decode: the
+ * limit of its waits for pages, and (skip_page >= 0) the page whose copies the
+ * first warp of CTA 0 does not issue in every later launch, counted from 0 over
+ * the pages that this warp takes.  Nothing is in flight for it, so its wait runs
+ * out.  Debug library only; returns as xs_debug_wait_injection.
+ */
+int xs_debug_kv4_wait_injection(int64_t wait_limit_ns, int skip_page);
 
 /*
  * Shared pages.  extra_refs int32 [num_blocks], zero at first, counts each

@@ -89,6 +89,19 @@ constexpr int kStages = 4;         // pages of a warp's ring
 constexpr float kLead = 8.0f;      // of a reference before the largest logit
 constexpr float kLowest = -3.402823466e38f;     // a reference before any logit above it
 constexpr uint64_t kWaitLimitNs = 4000000000ull;
+// In the debug library the limit can be set, and a page of CTA 0's first warp
+// left out, so that its wait runs out (xs_debug_kv4_wait_injection).
+#ifdef XS_DEBUG_BOUNDS
+__device__ unsigned long long g_wait_limit_ns = kWaitLimitNs;
+__device__ int g_skip_page = -1;    // the warp's page, counted since the launch
+__device__ __forceinline__ uint64_t wait_limit() { return g_wait_limit_ns; }
+__device__ __forceinline__ bool skip_page(uint32_t page) {
+    return blockIdx.x == 0 && threadIdx.x == 0 && static_cast<int>(page) == g_skip_page;
+}
+#else
+__device__ __forceinline__ constexpr uint64_t wait_limit() { return kWaitLimitNs; }
+__device__ __forceinline__ constexpr bool skip_page(uint32_t) { return false; }
+#endif
 
 // d = A B + d
 __device__ __forceinline__ void mma_f16(float *d, uint32_t a0, uint32_t a1, uint32_t a2,
@@ -230,13 +243,13 @@ __device__ __forceinline__ void start_copy(uint32_t dst, const uint8_t *k, int b
 
 // Waits for a ring place with a limit, all lanes alike: false if it ran out.
 __device__ __forceinline__ bool warp_waits(uint64_t *bar, uint32_t parity) {
-    return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, kWaitLimitNs));
+    return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, wait_limit()));
 }
 
-// A warp's ring since the launch: the pages taken from it, and how many more
-// were started when a wait ran out (then nothing more is started).
+// A warp's ring since the launch: the pages taken from it, and whether a wait
+// ran out (then nothing more is started, and all that the CTA does is NaN).
 struct RingState {
-    uint32_t taken = 0, behind = 0;
+    uint32_t taken = 0;
     bool dead = false;
 };
 
@@ -280,7 +293,7 @@ __device__ __forceinline__ void run_segment(const Kv4DecodeParams &p, DecodeSmem
         if (k >= mine) return;
         if (k && (k & 31) == 0) ids = load_ids(k);
         const int32_t id = __shfl_sync(0xffffffffu, ids, k & 31);
-        if (lane == 0) {
+        if (lane == 0 && !skip_page(base + k)) {
             const uint32_t st = (base + k) % kStages;
             const uint32_t dst = ring0 + st * (2 * kv4_page_bytes(D)), bar = bar0 + 8 * st;
             const int64_t at = (static_cast<int64_t>(id) * p.Hkv + hk) * kv4_page_bytes(D);
@@ -358,8 +371,10 @@ __device__ __forceinline__ void run_segment(const Kv4DecodeParams &p, DecodeSmem
         if (!__all_sync(0xffffffffu, mbar_try_wait(&sm.full[warp][st], parity)) &&
             !warp_waits(&sm.full[warp][st], parity)) {
             ring.dead = true;
-            ring.behind = min(mine - k, kStages);
             if (lane == 0) raise_flag(p.err_flag, XS_FLAG_TIMEOUT);
+            // Its copies and those behind it land before the ring serves another use.
+            for (int i = 0; i < min(mine - k, kStages); ++i)
+                warp_waits(&sm.full[warp][(base + k + i) % kStages], ((base + k + i) / kStages) & 1);
             break;
         }
         const uint32_t kp = ring0 + st * (2 * kv4_page_bytes(D)), vp = kp + kv4_page_bytes(D);
@@ -482,6 +497,7 @@ __device__ __forceinline__ void run_segment(const Kv4DecodeParams &p, DecodeSmem
     // as l = 0 under kLowest.
     l += __shfl_xor_sync(0xffffffffu, l, 1);
     l += __shfl_xor_sync(0xffffffffu, l, 2);
+    if (ring.dead) l = NAN;     // this segment's output, and what the CTA does after it
     __syncthreads();    // all warps have read their last pages
     if (t == 0) {
         sm.m[warp][g] = m;
@@ -691,14 +707,6 @@ __device__ __forceinline__ void arrive_and_join(const Kv4DecodeParams &p, Decode
     if (sm.joins) join_partials<D, kFew>(p, sm, sm.b, sm.hk, sm.f, sm.last);
 }
 
-// The last copies of a warp whose wait ran out are still on their way here.
-template <int D, bool kFew>
-__device__ __forceinline__ void drain(DecodeSmem<D, kFew> &sm, RingState &ring) {
-    for (; ring.behind > 0; --ring.behind, ++ring.taken)
-        mbar_wait_bounded(&sm.full[threadIdx.x >> 5][ring.taken % kStages],
-                          (ring.taken / kStages) & 1, kWaitLimitNs);
-}
-
 // A CTA's place is found by every warp for itself (a load of the lengths and a
 // few shuffles; with barriers between the warps it took 0.2 us more).
 template <int D>
@@ -792,7 +800,6 @@ __global__ void __launch_bounds__(32 * dec_warps(false), ctas_per_sm(false))
         }
         __syncthreads();
     }
-    drain(sm, ring);
 }
 
 // Few segments, in clusters of kCluster CTAs.  Either each segment has a cluster,
@@ -892,7 +899,6 @@ __global__ void __launch_bounds__(32 * dec_warps(true), ctas_per_sm(true))
     }
     run_segment<D, true>(p, sm, ring, b, hk, sp, a, e, whole,
                          clusters ? sm.part : partial_of(p, D, blockIdx.x, a == 0));
-    drain(sm, ring);
     if (whole) return;
     if (!clusters) {
         arrive_and_join(p, sm);
@@ -934,7 +940,6 @@ __global__ void __launch_bounds__(32 * dec_warps(false), ctas_per_sm(false))
     const int a = alone ? 0 : sp.pages * rank / kLineCluster;
     const int e = alone ? sp.pages : sp.pages * (rank + 1) / kLineCluster;
     run_segment<D, false>(p, sm, ring, b, hk, sp, a, e, alone, sm.part);
-    drain(sm, ring);
     if (!alone) join_cluster<kLineCluster, kDecThreads>(p, sm.part, out, hk, rank, D);
 }
 
@@ -1013,6 +1018,23 @@ template <int D> int launch(const Kv4DecodeParams &p, int dev, int sms, cudaStre
 XS_DEFINE_BOUNDS_COUNTER(bounds_failures_kv4_decode)
 
 }  // namespace xs
+
+extern "C" int xs_debug_kv4_wait_injection(int64_t wait_limit_ns, int skip_page) {
+#ifdef XS_DEBUG_BOUNDS
+    if (wait_limit_ns <= 0 || skip_page < -1) return XS_ESHAPE;
+    const unsigned long long limit = static_cast<unsigned long long>(wait_limit_ns);
+    if (cudaMemcpyToSymbol(xs::g_wait_limit_ns, &limit, sizeof(limit)) != cudaSuccess ||
+        cudaMemcpyToSymbol(xs::g_skip_page, &skip_page, sizeof(skip_page)) != cudaSuccess) {
+        cudaGetLastError();
+        return XS_EDEVICE;
+    }
+    return XS_OK;
+#else
+    (void)wait_limit_ns;
+    (void)skip_page;
+    return XS_EUNSUPPORTED;
+#endif
+}
 
 extern "C" size_t xs_kv4_decode_workspace_bytes(int B, int Hq, int Hkv, int D) {
     if (B <= 0 || Hq <= 0 || Hkv <= 0 || D <= 0) return 0;

@@ -101,6 +101,7 @@ SIGNATURES = {
     "xs_version": (_I, []),
     "xs_debug_bounds_failures": (_I, [_I]),
     "xs_debug_wait_injection": (_I, [_L, _I]),
+    "xs_debug_kv4_wait_injection": (_I, [_L, _I]),
 }
 
 _lock = threading.Lock()
@@ -653,6 +654,15 @@ def xs_debug_wait_injection(wait_limit_ns: int, skip_page: int = -1, lib=None) -
     code = lib.xs_debug_wait_injection(int(wait_limit_ns), int(skip_page))
     if code != 0:
         raise XsError("xs_debug_wait_injection", code)
+
+
+def xs_debug_kv4_wait_injection(wait_limit_ns: int, skip_page: int = -1, lib=None) -> None:
+    """The same for xs_kv4_decode's waits for pages: the page is one of the
+    first warp of CTA 0."""
+    lib = lib or load()
+    code = lib.xs_debug_kv4_wait_injection(int(wait_limit_ns), int(skip_page))
+    if code != 0:
+        raise XsError("xs_debug_kv4_wait_injection", code)
 
 
 def load_debug():

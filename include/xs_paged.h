@@ -186,7 +186,10 @@ int xs_prefill_append(const void *k_src, const void *v_src, void *k_cache, void 
  * chain append(c), attention(c), append(c + 1), ... never lets a launch read
  * rows whose append has not completed: each attention's wait covers its own
  * chunk's append, which started only after the previous attention's wait
- * covered the append before it.
+ * covered the append before it.  The append itself completes only after the
+ * attention that it ran beside, so any call may follow the chain, at any point
+ * and in a CUDA graph too: what waits for the chain's last launch comes after
+ * all of it.
  *
  * flags 0 is xs_prefill_append / xs_paged_prefill_tc; unknown bits are
  * XS_EUNSUPPORTED.

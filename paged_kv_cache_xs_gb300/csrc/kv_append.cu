@@ -91,7 +91,8 @@ __global__ void __launch_bounds__(kAppendThreads)
 }
 
 // Prefill append: chunk rows src[h, i, :] ([Hkv, T, D], the pages' layout)
-// to position start + i of one sequence.  One thread per 16-byte chunk.
+// to position start + i of one sequence.  One thread per 16-byte chunk; the last
+// block appends nothing (below).
 __global__ void __launch_bounds__(kAppendThreads)
     prefill_append_kernel(const uint4 *__restrict__ k_src, const uint4 *__restrict__ v_src,
                           uint4 *__restrict__ k_cache, uint4 *__restrict__ v_cache,
@@ -103,10 +104,18 @@ __global__ void __launch_bounds__(kAppendThreads)
     // the next launch (this chunk's attention) may be placed at once.  (A
     // no-op in a launch made without the attribute.)
     griddep_launch_dependents();
+    // The grid completes only after the kernel that its appends do not wait for:
+    // a launch behind it that waits for this grid alone, or for this chunk's
+    // attention, which waits for this grid, then comes after everything before it.
+    const unsigned workers = gridDim.x - 1;
+    if (blockIdx.x == workers) {
+        griddep_wait();
+        return;
+    }
     const int64_t per_token = static_cast<int64_t>(Hkv) * chunks_per_row;
     const int64_t total = static_cast<int64_t>(T) * 2 * per_token;
     for (int64_t i = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; i < total;
-         i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
+         i += static_cast<int64_t>(workers) * blockDim.x) {
         const int64_t t = i / (2 * per_token);
         const int64_t r = i - t * 2 * per_token;
         const bool is_v = r >= per_token;
@@ -245,7 +254,7 @@ extern "C" int xs_prefill_append_ex(const void *k_src, const void *v_src, void *
     const int64_t blocks64 = (total + xs::kAppendThreads - 1) / xs::kAppendThreads;
     const int grid = static_cast<int>(blocks64 < (1 << 20) ? blocks64 : (1 << 20));
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
+    cfg.gridDim = dim3(grid + 1);
     cfg.blockDim = dim3(xs::kAppendThreads);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];

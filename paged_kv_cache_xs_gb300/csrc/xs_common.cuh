@@ -278,7 +278,9 @@ inline int launch_status() {
 
 // Launches a kernel that begins with after_previous() or griddep_wait(): its CTAs are placed
 // while the kernel before it on the stream ends, which takes 0.7 to 2 us off a
-// sequence of short launches that are not in a graph.
+// sequence of short launches that are not in a graph.  Its wait is for the kernel
+// before it alone, so every kernel of this library that may run beside its
+// predecessor completes only after that one.
 template <typename... P, typename... A>
 inline int launch_after(void (*kernel)(P...), dim3 grid, int threads, size_t smem,
                         cudaStream_t stream, int cluster, A &&...args) {

@@ -677,11 +677,12 @@ int xs_version(void);
  * the same sources compiled with -DXS_DEBUG_BOUNDS), the number of in-kernel
  * bounds checks that failed on the current device since the last reset
  * (reset != 0 clears the count after reading it).  Every global-memory index
- * the kernels compute is checked there against its buffer's extent before
- * the access; a failure skips the access and raises XS_FLAG_BOUNDS.  The
- * paper has no counterpart of this entry point: the checks are a test aid
- * standing in for a device memory checker.  Synchronous (it copies the
- * counters).
+ * the kernels compute is checked there against its buffer's extent, as far as
+ * the kernel knows it (a free stack's is taken as num_blocks where the call has
+ * no capacity), before the access; a failure skips the access and raises
+ * XS_FLAG_BOUNDS.  The paper has no counterpart of this entry point: the checks
+ * are a test aid standing in for a device memory checker.  Synchronous (it
+ * copies the counters).
  * Returns XS_EUNSUPPORTED in the release library, XS_EDEVICE if the copy
  * failed.
  */

@@ -154,6 +154,7 @@ __global__ void __launch_bounds__(kShareThreads)
         row_new[kShareThreads];
     auto length = [&](int b) { return *static_cast<volatile int32_t *>(lens + b); };
     auto usable = [&](int i, int &p, int &c, int &len) {
+        if (!XS_BOUNDS(i >= 0 && i < n, err_flag)) return false;
         p = parents[i], c = children[i];
         if (p < 0 || p >= B || c < 0 || c >= B) return false;
         len = length(p);
@@ -207,14 +208,16 @@ __global__ void __launch_bounds__(kShareThreads)
         int32_t blk = -1;
         int64_t src = -1;
         if (tail && fits) {
-            blk = free_stack[top - 1 - rank];
-            src = tables[static_cast<int64_t>(p) * max_blocks + len / bs];
+            const int at = top - 1 - rank;      // a stack holds a block at most once
+            if (XS_BOUNDS(at >= 0 && at < num_blocks, err_flag)) blk = free_stack[at];
+            if (XS_BOUNDS(p >= 0 && p < B && len / bs < max_blocks, err_flag))
+                src = tables[static_cast<int64_t>(p) * max_blocks + len / bs];
             if (src < 0 || src >= num_blocks || blk < 0 || blk >= num_blocks) {
                 raise_flag(err_flag, XS_FLAG_BAD_BLOCK);
                 src = -1;
             }
         }
-        if (i < n) {
+        if (i < n && XS_BOUNDS(i >= 0, err_flag)) {
             copies[2 * static_cast<int64_t>(i)] = src;
             copies[2 * static_cast<int64_t>(i) + 1] = src < 0 ? -1 : blk;
         }
@@ -230,6 +233,9 @@ __global__ void __launch_bounds__(kShareThreads)
             const int32_t *from = tables + static_cast<int64_t>(row_from[k]) * max_blocks;
             int32_t *to = tables + static_cast<int64_t>(row_to[k]) * max_blocks;
             const int full = row_len[k] / bs;
+            if (!XS_BOUNDS(row_from[k] >= 0 && row_from[k] < B && row_to[k] < B && full <= max_blocks,
+                           err_flag))
+                continue;
 #pragma unroll 4
             for (int col = lane; col < max_blocks; col += 32) {
                 int32_t id = -1;
@@ -246,7 +252,7 @@ __global__ void __launch_bounds__(kShareThreads)
             }
         }
         __syncthreads();
-        if (ok) lens[c] = fits ? len : -1;
+        if (ok && XS_BOUNDS(c >= 0 && c < B, err_flag)) lens[c] = fits ? len : -1;
         __syncthreads();
     }
     if (threadIdx.x == 0) *free_top = top - min(popped, top);
@@ -287,7 +293,7 @@ __global__ void __launch_bounds__(kShareThreads)
                 else
                     raise_flag(err_flag, XS_FLAG_BAD_BLOCK);
             }
-            row[col] = -1;
+            if (XS_BOUNDS(col >= 0 && col < max_blocks, err_flag)) row[col] = -1;
         };
 #pragma unroll
         for (int u = 0; u < 4; ++u)
@@ -303,6 +309,7 @@ __global__ void __launch_bounds__(kShareThreads)
     const int64_t before = cluster_scan(cluster, counts, count_part(part, freed), &total);
     write_part(part, top + before, freed, [&](int64_t k, int64_t i) {
         const int64_t id = num_blocks - 1 - i;
+        if (!XS_BOUNDS(k >= 0 && id >= 0 && id < num_blocks, err_flag)) return;
         if (k < capacity)
             free_stack[k] = static_cast<int32_t>(id);
         else
@@ -346,6 +353,7 @@ __global__ void __launch_bounds__(kShareThreads)
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
             if (col0 + 32 * u + lane >= pages) continue;
+            if (!XS_BOUNDS(b < B && col0 + 32 * u + lane < max_blocks, err_flag)) continue;
             if (id[u] >= 0 && id[u] < num_blocks)
                 remap[id[u]] = 0;
             else
@@ -361,14 +369,20 @@ __global__ void __launch_bounds__(kShareThreads)
     auto hole = [&](int64_t id) { return id < live && !used(id); };
     const int64_t m0 = cluster_scan(cluster, counts[1], count_part(part, mover), &movers);
     const int64_t h0 = cluster_scan(cluster, counts[2], count_part(part, hole), &holes);
-    write_part(part, m0, mover, [&](int64_t k, int64_t id) { moves[2 * k] = id; });
-    write_part(part, h0, hole, [&](int64_t k, int64_t id) { moves[2 * k + 1] = id; });
+    auto in_moves = [&](int64_t k) { return XS_BOUNDS(k >= 0 && k < num_blocks / 2, err_flag); };
+    write_part(part, m0, mover, [&](int64_t k, int64_t id) {
+        if (in_moves(k)) moves[2 * k] = id;
+    });
+    write_part(part, h0, hole, [&](int64_t k, int64_t id) {
+        if (in_moves(k)) moves[2 * k + 1] = id;
+    });
     launch_sync(cluster);
     for (int64_t id = thread; id < live; id += threads)
         if (__ldcg(remap + id) == 0) remap[id] = static_cast<int32_t>(id);
     for (int64_t k = thread; k < num_blocks / 2; k += threads) {
         if (k < movers) {
             const int64_t src = __ldcg(moves + 2 * k), dst = __ldcg(moves + 2 * k + 1);
+            if (!XS_BOUNDS(src >= live && src < num_blocks && dst >= 0 && dst < live, err_flag)) continue;
             remap[src] = static_cast<int32_t>(dst);
             extra_out[dst] = extra[src];
         } else {
@@ -381,7 +395,8 @@ __global__ void __launch_bounds__(kShareThreads)
             extra_out[id] = 0;
         else if (__ldcg(remap + id) == id)      // (a hole's came with its mover)
             extra_out[id] = extra[id];
-        if (id < num_blocks - live) free_stack[id] = static_cast<int32_t>(num_blocks - 1 - id);
+        if (id < num_blocks - live && XS_BOUNDS(live >= 0, err_flag))
+            free_stack[id] = static_cast<int32_t>(num_blocks - 1 - id);
     }
     for (int64_t piece = warp; piece < static_cast<int64_t>(B) * pieces; piece += warps) {
         const int b = static_cast<int>(piece / pieces), col0 = static_cast<int>(piece % pieces) * 128;
@@ -400,7 +415,8 @@ __global__ void __launch_bounds__(kShareThreads)
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
             const int col = col0 + 32 * u + lane;
-            if (col < max_blocks) tables_out[static_cast<int64_t>(b) * max_blocks + col] = id[u];
+            if (col < max_blocks && XS_BOUNDS(b >= 0 && b < B, err_flag))
+                tables_out[static_cast<int64_t>(b) * max_blocks + col] = id[u];
         }
     }
     if (thread == 0) {
@@ -443,6 +459,9 @@ __global__ void __launch_bounds__(kCopyThreads)
             if (rest == 0 && threadIdx.x == 0) raise_flag(err_flag, XS_FLAG_BAD_BLOCK);
             continue;
         }
+        if (!XS_BOUNDS(pair < n && (lv >> 1) < layers && piece < pieces &&
+                           (layers == 1 || num_blocks * block_chunks <= layer_chunks), err_flag))
+            continue;
         uint4 *pool = ((lv & 1) ? v_pools : k_pools) + (lv >> 1) * layer_chunks;
         const uint4 *from = pool + s * block_chunks;
         uint4 *to = pool + d * block_chunks;

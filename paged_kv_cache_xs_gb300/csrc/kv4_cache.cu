@@ -112,6 +112,7 @@ __global__ void __launch_bounds__(kUnpackThreads)
         }
         const uint8_t *page = (is_v ? v_cache : k_cache) +
                               (static_cast<int64_t>(blk) * Hkv + h) * kv4_page_bytes(D);
+        if (!XS_BOUNDS((pv >> 1) < n && h >= 0 && h < Hkv, err_flag)) continue;
         T *out = (is_v ? v_out : k_out) + ((pv >> 1) * Hkv + h) * (16 * D);
         uint32_t w[2][NG];
         if (!is_v) {

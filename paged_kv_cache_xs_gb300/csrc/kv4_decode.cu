@@ -172,7 +172,7 @@ struct Span {
 };
 __device__ __forceinline__ Span span_of(const Kv4DecodeParams &p, int b) {
     Span s;
-    s.n = p.lens[b];
+    s.n = XS_BOUNDS(b >= 0 && b < p.B, p.err_flag) ? p.lens[b] : 0;
     if (s.n > p.max_blocks * 16) {
         if (blockIdx.x == 0) raise_flag(p.err_flag, XS_FLAG_BAD_LEN);
         s.n = p.max_blocks * 16;
@@ -191,6 +191,7 @@ __host__ __device__ constexpr int64_t partial_floats(int G, int D) {
 
 // Partial `slot` of CTA i.
 __device__ __forceinline__ float *partial_of(const Kv4DecodeParams &p, int D, int64_t i, int slot) {
+    if (!XS_BOUNDS(i >= 0 && i < gridDim.x && gridDim.x <= kMaxCtas, p.err_flag)) i = 0;
     return p.partials + (2 * i + slot) * partial_floats(p.G, D);
 }
 
@@ -284,7 +285,10 @@ __device__ __forceinline__ void run_segment(const Kv4DecodeParams &p, DecodeSmem
     {
         const __nv_bfloat16 *q = p.q + (static_cast<int64_t>(b) * p.Hq + h0 + (g < p.G ? g : 0)) * D;
 #pragma unroll
-        for (int c = 0; c < NG; ++c) qx[c] = *reinterpret_cast<const uint4 *>(q + 32 * c + 8 * t);
+        for (int c = 0; c < NG; ++c)
+            qx[c] = XS_BOUNDS(b < p.B && hk < p.Hkv && h0 + p.G <= p.Hq, p.err_flag)
+                        ? *reinterpret_cast<const uint4 *>(q + 32 * c + 8 * t)
+                        : make_uint4(0, 0, 0, 0);
     }
     // Starts the copies of the warp's page k into the ring's next place.
     const uint32_t ring0 = smem_addr(sm.ring[warp]), bar0 = smem_addr(sm.full[warp]);
@@ -293,7 +297,8 @@ __device__ __forceinline__ void run_segment(const Kv4DecodeParams &p, DecodeSmem
         if (k >= mine) return;
         if (k && (k & 31) == 0) ids = load_ids(k);
         const int32_t id = __shfl_sync(0xffffffffu, ids, k & 31);
-        if (lane == 0 && !skip_page(base + k)) {
+        if (lane == 0 && !skip_page(base + k) &&
+            XS_BOUNDS(id >= 0 && id < p.num_blocks && hk >= 0 && hk < p.Hkv, p.err_flag)) {
             const uint32_t st = (base + k) % kStages;
             const uint32_t dst = ring0 + st * (2 * kv4_page_bytes(D)), bar = bar0 + 8 * st;
             const int64_t at = (static_cast<int64_t>(id) * p.Hkv + hk) * kv4_page_bytes(D);
@@ -529,13 +534,16 @@ __device__ __forceinline__ void run_segment(const Kv4DecodeParams &p, DecodeSmem
         const float f = fast_exp2(sm.m[w][h] - top);
         sm.weight[threadIdx.x] = whole ? f / total : f;
         if (!whole && w == 0 && h < p.G) {
-            part[p.G * D + h] = top;
-            part[p.G * (D + 1) + h] = total;
+            if (XS_BOUNDS(p.G * (D + 1) + h < partial_floats(p.G, D), p.err_flag)) {
+                part[p.G * D + h] = top;
+                part[p.G * (D + 1) + h] = total;
+            }
         }
     }
     __syncthreads();
     __nv_bfloat16 *out = p.out + (static_cast<int64_t>(b) * p.Hq + h0) * D;
     for (int x = 4 * threadIdx.x; x < p.G * D; x += 4 * kDecThreads) {
+        if (!XS_BOUNDS(b < p.B && h0 + p.G <= p.Hq, p.err_flag)) continue;
         const int h = x / D, d = x % D;
         float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
@@ -618,7 +626,7 @@ __device__ __noinline__ void join_partials(const Kv4DecodeParams &p, DecodeSmem<
 #pragma unroll
     for (int x = 0; x < kPer; ++x) {
         const int e = threadIdx.x + x * kDecThreads;
-        if (4 * e / D < G)
+        if (4 * e / D < G && XS_BOUNDS(b < p.B && hk < p.Hkv, p.err_flag))
             reinterpret_cast<uint2 *>(out)[e] =
                 make_uint2(pack_bf16(F2{o[x].x / total[x], o[x].y / total[x]}),
                            pack_bf16(F2{o[x].z / total[x], o[x].w / total[x]}));
@@ -657,7 +665,7 @@ __device__ __forceinline__ void join_cluster(const Kv4DecodeParams &p, const flo
     for (int n = 0; n < kTrips; ++n) {
         if (n * kSlots >= per) break;
         const int i = n * kSlots + threadIdx.x / kCtas, chunk = rank * per + i, h = 4 * chunk / D;
-        const bool valid = i < per && chunk < chunks;
+        const bool valid = i < per && chunk < chunks && XS_BOUNDS(rank < kCtas && hk < p.Hkv, p.err_flag);
         float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         float top = kLowest, sum = 0.0f, sink = 0.0f;
         if (valid) {
@@ -700,6 +708,7 @@ __device__ __forceinline__ void arrive_and_join(const Kv4DecodeParams &p, Decode
     // acquire and the next barrier the other CTAs'.
     __syncthreads();
     if (threadIdx.x == 0) {
+        if (!XS_BOUNDS(sm.f >= 0 && sm.f <= sm.last && sm.last < gridDim.x, p.err_flag)) sm.f = sm.last = 0;
         sm.joins = atomic_add_acq_rel_gpu(p.counters + sm.f, 1) == sm.last - sm.f;
         if (sm.joins) p.counters[sm.f] = 0;
     }

@@ -143,6 +143,7 @@ __device__ __forceinline__ int64_t append_slot(const RopeParams &p, int64_t t, i
         raise_flag(err_flag, XS_FLAG_BAD_LEN);
         return -1;
     }
+    if (!XS_BOUNDS(t >= 0 && t < p.T && page >= 0, p.err_flag)) return -1;
     const int32_t blk = p.tables[t * p.max_blocks + page];
     if (blk < 0 || blk >= p.num_blocks) {
         raise_flag(err_flag, XS_FLAG_BAD_BLOCK);
@@ -185,6 +186,11 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas)
     // anything else is known of the token.
     constexpr int kAhead = kKv4 ? 2 : kRopeAheadBytes / sizeof(T);
     Chunk<T, 4> ahead[kAhead][2];
+    // Whether chunks c0 and c1 of head h of the token's q, k or v are its own.
+    auto inside = [&](int kind, int h, int c0, int c1) {
+        return XS_BOUNDS(t >= 0 && t < p.T && h >= 0 && h < (kind == 0 ? p.Hq : p.Hkv) && c0 >= 0 &&
+                             4 * c0 + 4 <= D && c1 >= 0 && 4 * c1 + 4 <= D, p.err_flag);
+    };
     auto fetch = [&](int kind, int h, int count) {
         const int c0 = kind < 2 ? r0 : 2 * j, c1 = kind < 2 ? r1 : 2 * j + 1;
         const T *src = kind == 0   ? static_cast<const T *>(p.q) + t * p.q_stride
@@ -195,7 +201,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas)
         for (int i = 0; i < kAhead; ++i) {
 #pragma unroll
             for (int w = 0; w < Chunk<T, 4>::kWords; ++w) ahead[i][0].w[w] = ahead[i][1].w[w] = 0;
-            if (t < p.T && i < count) {
+            if (t < p.T && i < count && inside(kind, h + i, c0, c1)) {
                 ahead[i][0].load(src + i * D + 4 * c0);
                 ahead[i][1].load(src + i * D + 4 * c1);
             }
@@ -228,13 +234,15 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas)
                 Chunk<T, 8> none;
 #pragma unroll
                 for (int w = 0; w < Chunk<T, 8>::kWords; ++w) none.w[w] = 0x7fffffffu;
-                none.store(static_cast<T *>(p.q_out) + (t * p.Hq + h) * D + 8 * j);
+                if (inside(0, h, 2 * j, 2 * j + 1))
+                    none.store(static_cast<T *>(p.q_out) + (t * p.Hq + h) * D + 8 * j);
             }
     }
     int64_t slot = -1;
     if (live && p.k_cache && run_end > p.Hq)
         slot = append_slot(p, t, pos, j == 0 && run_begin <= p.Hq ? p.err_flag : nullptr);
-    if (slot >= 0 && !XS_BOUNDS((slot >> 4) < p.num_blocks, p.err_flag)) slot = -1;
+    if (slot >= 0 && !XS_BOUNDS((slot >> 4) < p.num_blocks && run_end <= p.rows_per_token, p.err_flag))
+        slot = -1;
     const int64_t page0 = slot < 0 ? 0 : (slot >> 4) * p.Hkv;
     const int o = static_cast<int>(slot & 15);
 
@@ -242,7 +250,8 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas)
     F2 c[2], s[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) c[i] = F2{1.0f, 1.0f}, s[i] = F2{0.0f, 0.0f};
-    if (live && rotates && run_begin < p.Hq + p.Hkv) {
+    if (live && rotates && run_begin < p.Hq + p.Hkv &&
+        XS_BOUNDS(pos < p.max_pos && 4 * j + 4 <= p.rot / 2, p.err_flag)) {
         const float *row = p.cos_sin + pos * p.rot + 4 * j;
         Chunk<float, 4> v;
         v.load(row);
@@ -293,7 +302,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas)
             F2 x[4];
             ahead[i0][0].to_f32(&x[0].x);
             ahead[i0][1].to_f32(&x[2].x);
-            if (t < p.T && k0 + i0 + kAhead < count) {
+            if (t < p.T && k0 + i0 + kAhead < count && inside(kind, h + k0 + i0 + kAhead, c0, c1)) {
                 ahead[i0][0].load(src + 4 * c0);
                 ahead[i0][1].load(src + 4 * c1);
             }
@@ -337,7 +346,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas)
             y0.from_f32(&x[0].x);
             y1.from_f32(&x[2].x);
             if (!kKv4 || !paged) {
-                if (writes) {
+                if (writes && inside(kind, h + k0 + i0, c0, c1)) {
                     y0.store(dst + 4 * c0);
                     y1.store(dst + 4 * c1);
                 }
@@ -396,7 +405,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas)
                 const uint16_t word_scale =
                     static_cast<uint16_t>(kind == 1 && halves && (j & 1) ? scales >> 16 : scales);
                 const uint32_t theirs = __shfl_xor_sync(0xffffffffu, word, kLanes);
-                if (writes) {
+                if (writes && inside(kind, h + k0 + i0, 2 * ch, 2 * ch + 1)) {
                     if (kind == 2 && paired)
                         kv4_store_pair<D>(page, o, ch, word, theirs, word_scale);
                     else

@@ -6,6 +6,8 @@ device) with PyTorch.
 """
 from __future__ import annotations
 
+import importlib.metadata
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -21,7 +23,8 @@ BUILD_DIR = os.path.join(PKG, "_build")
 LIB_NAME = "libxs_paged.so"
 LIB_PATH = os.path.join(BUILD_DIR, LIB_NAME)
 # Python binding (checks tensors, calls the library by entry address): host
-# C++ against PyTorch's headers, one for both libraries.
+# C++ against PyTorch's headers, one for both libraries.  The library needs
+# neither; where PyTorch is not installed, it is all that is built.
 BIND_PATH = os.path.join(BUILD_DIR, "xs_bind.so")
 BIND_SOURCE = "bind.cpp"
 # The debug library: the same sources compiled with -DXS_DEBUG_BOUNDS, so every
@@ -41,23 +44,54 @@ def nvcc() -> str:
 
 
 def _deps() -> list[str]:
-    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
+    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f != BIND_SOURCE]
     files.append(os.path.join(INCLUDE, "xs_paged.h"))
     return files
 
 
-def up_to_date(debug_bounds: bool = False) -> bool:
-    libs = [DEBUG_LIB_PATH] if debug_bounds else [LIB_PATH, BIND_PATH]
-    if not all(os.path.exists(lib) for lib in libs):
+def _newer(path: str, files: list[str]) -> bool:
+    return os.path.exists(path) and all(os.path.getmtime(f) <= os.path.getmtime(path) for f in files)
+
+
+def _bind_against() -> str | None:
+    """What xs_bind.so is built against: this Python and the PyTorch that it
+    finds (None: there is none)."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        return None
+    try:
+        version = importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:
+        version = str(os.path.getmtime(spec.origin))
+    return f"{sys.version}\n{version}\n{spec.origin}\n"
+
+
+def bind_up_to_date() -> bool:
+    """Whether xs_bind.so is newer than its sources and was built against the
+    installed PyTorch (or there is none to build it against)."""
+    against = _bind_against()
+    if against is None:
+        return True
+    if not _newer(BIND_PATH, [os.path.join(CSRC, BIND_SOURCE), os.path.join(INCLUDE, "xs_paged.h")]):
         return False
-    t = min(os.path.getmtime(lib) for lib in libs)
-    return all(os.path.getmtime(f) <= t for f in _deps())
+    try:
+        with open(BIND_PATH + ".against") as f:
+            return f.read() == against
+    except OSError:
+        return False
+
+
+def up_to_date(debug_bounds: bool = False) -> bool:
+    if debug_bounds:
+        return _newer(DEBUG_LIB_PATH, _deps())
+    return _newer(LIB_PATH, _deps()) and bind_up_to_date()
 
 
 def build_bind() -> str:
     """Build xs_bind.so with the host compiler."""
     import torch
 
+    os.makedirs(BUILD_DIR, exist_ok=True)
     top = os.path.join(torch.__path__[0], "include")
     cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
     tmp = BIND_PATH + f".tmp{os.getpid()}"
@@ -70,13 +104,17 @@ def build_bind() -> str:
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed for {BIND_SOURCE}:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, BIND_PATH)
+    with open(BIND_PATH + ".against", "w") as f:
+        f.write(_bind_against() or "")
     return BIND_PATH
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | None = None,
           debug_bounds: bool = False) -> str:
     """Build the release library (or, with debug_bounds, the debug library with
-    in-kernel bounds checks) unless it is newer than every source; returns its path."""
+    in-kernel bounds checks) unless it is newer than every source, and with the
+    release library the Python binding where PyTorch is installed; returns the
+    library's path."""
     build_dir = DEBUG_BUILD_DIR if debug_bounds else BUILD_DIR
     lib_path = DEBUG_LIB_PATH if debug_bounds else LIB_PATH
     if not force and up_to_date(debug_bounds):
@@ -99,16 +137,19 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
         return obj
 
     with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        bind = None if debug_bounds else ex.submit(build_bind)
-        objs = list(ex.map(compile_one, SOURCES))
+        bind = None
+        if not debug_bounds and _bind_against() is not None and (force or not bind_up_to_date()):
+            bind = ex.submit(build_bind)
+        if force or not _newer(lib_path, _deps()):
+            objs = list(ex.map(compile_one, SOURCES))
+            tmp = lib_path + f".tmp{os.getpid()}"
+            cmd = [exe, *ARCH, "-shared", "-cudart", "shared", "-o", tmp, *objs]
+            r = subprocess.run(cmd, capture_output=True, text=True)
+            if r.returncode != 0:
+                raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+            os.replace(tmp, lib_path)
         if bind is not None:
-            bind.result()
-    tmp = lib_path + f".tmp{os.getpid()}"
-    cmd = [exe, *ARCH, "-shared", "-cudart", "shared", "-o", tmp, *objs]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, lib_path)
+            bind.result()       # (after the library is in place: it does not need the binding)
     return lib_path
 
 

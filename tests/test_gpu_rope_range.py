@@ -1,0 +1,55 @@
+"""Norm + rotation of rows whose squares leave fp32."""
+import pytest
+import torch
+
+from paged_kv_cache_xs_gb300 import ops
+from tests import plain_ops as plain
+from tests.gpu_helpers import device
+
+pytestmark = pytest.mark.gpu
+
+BF, F32 = torch.bfloat16, torch.float32
+SIZES = [1e25, 1.0, 1e37, 1e-25, 1e-36, 3.0, 1e19, 1e-16, 2e-38, 1e18, 1e-14]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("eps", [0.0, 1e-34, 1e-6, 1e30])
+def test_rows_of_any_size(D, eps, dtype):
+    # Rows of these sizes next to one another: two or four of them share a warp, so
+    # that one is scaled before its squares are taken and its neighbour is not.  One row
+    # has a single large value among ordinary ones.
+    dev, Hq, Hkv = device(), 3, 2
+    T = 3 * len(SIZES) + 1
+    g = torch.Generator(device=dev).manual_seed(D)
+    size = torch.tensor((SIZES * 3 + [1.0]), device=dev)
+    q, k = (torch.randn(T, h, D, generator=g, device=dev) for h in (Hq, Hkv))
+    q, k = (x / x.abs().amax(-1, keepdim=True) * size[:, None, None] for x in (q, k))
+    q[-1, 0, 7] = 1e30
+    q, k = q.to(dtype), k.to(dtype)
+    qw, kw = ((1 + 0.2 * torch.randn(D, generator=g, device=dev)).to(dtype) for _ in range(2))
+    tab, pos = ops.rope_table(T, D, 1e4, dev), torch.arange(T, dtype=torch.int32, device=dev)
+    qo, ko = torch.empty_like(q), torch.empty_like(k)
+    ops.xs_qk_norm_rope(qo, ko, q, k, qw, kw, eps, tab, pos)
+    for out, x, w in ((qo, q, qw), (ko, k, kw)):
+        ref, mag = plain.norm_rope(x, w, eps, tab, pos, D, False)
+        assert bool(ref.isfinite().all()) and bool(out.isfinite().all())
+        plain.check(out, ref, plain.norm_rope_bound(ref, mag, dtype), f"eps {eps}")
+
+
+def test_same_row_in_any_company():
+    # A row's result does not depend on what the other rows of its warp need.
+    dev, D = device(), 64
+    g = torch.Generator(device=dev).manual_seed(1)
+    row = torch.randn(1, 1, D, generator=g, device=dev).to(BF)
+    tab = ops.rope_table(4, D, 1e4, dev)
+    w = torch.ones(D, dtype=BF, device=dev)
+    pos = torch.ones(4, dtype=torch.int32, device=dev)
+    seen = []
+    for other in (1.0, 1e30, 1e-30):
+        x = row.expand(4, 1, D).clone()
+        x[[0, 2, 3]] *= other
+        out, ko = torch.empty_like(x), torch.empty_like(x)
+        ops.xs_qk_norm_rope(out, ko, x, x, w, w, 1e-6, tab, pos)
+        seen.append(out[1].clone())
+    assert torch.equal(seen[0], seen[1]) and torch.equal(seen[0], seen[2])

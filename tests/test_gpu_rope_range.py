@@ -53,3 +53,28 @@ def test_same_row_in_any_company():
         ops.xs_qk_norm_rope(out, ko, x, x, w, w, 1e-6, tab, pos)
         seen.append(out[1].clone())
     assert torch.equal(seen[0], seen[1]) and torch.equal(seen[0], seen[2])
+
+
+@pytest.mark.parametrize("T", [70, 9000])
+@pytest.mark.parametrize("D,rot", [(128, 128), (128, 48), (64, 64), (64, 16)])
+@pytest.mark.parametrize("inter", [False, True])
+def test_4_bit_append_equals_separate_calls(D, rot, inter, T):
+    # Bit for bit, pairs of either kind: the rows that the fused call quantises
+    # are those that the call without pages writes.
+    dev, Hq, Hkv = device(), 5, 3
+    g = torch.Generator(device=dev).manual_seed(T + rot)
+    x = torch.randn(T, (Hq + 2 * Hkv) * D, generator=g, device=dev).to(BF)
+    q, k, v = (y.view(T, -1, D) for y in x.split([Hq * D, Hkv * D, Hkv * D], 1))
+    qw, kw = ((1 + 0.2 * torch.randn(D, generator=g, device=dev)).to(BF) for _ in range(2))
+    tab, pos = ops.rope_table(T, rot, 1e6, dev), torch.randperm(T, device=dev).to(torch.int32)
+    nb = T // 16 + 1
+    slots = torch.randperm(nb * 16, generator=torch.Generator().manual_seed(T))[:T].to(dev)
+    kc, vc = ops.kv4_pools(nb, Hkv, D, dev)
+    kr, vr = ops.kv4_pools(nb, Hkv, D, dev)
+    qo, qr = (torch.empty(T, Hq, D, dtype=BF, device=dev) for _ in range(2))
+    ko = torch.empty(T, Hkv, D, dtype=BF, device=dev)
+    ops.xs_qk_norm_rope_append(qo, q, k, v, qw, kw, 1e-6, tab, pos, kc, vc, slots, interleaved=inter)
+    ops.xs_qk_norm_rope(qr, ko, q, k, qw, kw, 1e-6, tab, pos, interleaved=inter)
+    ops.xs_kv4_append(ko, v, kr, vr, slots)
+    assert torch.equal(qo.view(torch.int16), qr.view(torch.int16))
+    assert torch.equal(kc, kr) and torch.equal(vc, vr)

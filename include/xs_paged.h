@@ -559,9 +559,11 @@ int xs_paged_decode_step(void *out, const void *q, const void *k_new, const void
  * k_cache/v_cache this launch attends to (other than the rows it appends
  * itself), and neither does any earlier kernel that kernel lets run beside
  * it - true, for instance, when the previous kernel is a projection GEMM or
- * the attention step of another layer.  (No launch of this library lets its
- * successor start before its own wait has returned, so behind one of them
- * only that launch can still be running.)
+ * the attention step of another layer.  (No launch of this library but
+ * xs_prefill_append_ex with XS_PREFILL_OVERLAP lets its successor start before
+ * its own wait has returned, so behind one of them only that launch can still
+ * be running, and behind that append the attention before it, which writes
+ * neither.)
  */
 #define XS_STEP_EARLY_READS 1
 /*
@@ -677,9 +679,10 @@ int xs_version(void);
  * the same sources compiled with -DXS_DEBUG_BOUNDS), the number of in-kernel
  * bounds checks that failed on the current device since the last reset
  * (reset != 0 clears the count after reading it).  Every global-memory index
- * the kernels compute is checked there against its buffer's extent, as far as
- * the kernel knows it (a free stack's is taken as num_blocks where the call has
- * no capacity), before the access; a failure skips the access and raises
+ * the kernels compute (but for those of xs_kv_swap, xs_block_alloc_decode and
+ * xs_block_free) is checked there against its buffer's extent, as far as the
+ * kernel knows it (a free stack's is taken as num_blocks where the call has no
+ * capacity), before the access; a failure skips the access and raises
  * XS_FLAG_BOUNDS.  The paper has no counterpart of this entry point: the checks
  * are a test aid standing in for a device memory checker.  Synchronous (it
  * copies the counters).

@@ -28,7 +28,8 @@ LIB_PATH = os.path.join(BUILD_DIR, LIB_NAME)
 BIND_PATH = os.path.join(BUILD_DIR, "xs_bind.so")
 BIND_SOURCE = "bind.cpp"
 # The debug library: the same sources compiled with -DXS_DEBUG_BOUNDS, so every
-# computed global-memory index is checked in the kernels (XS_FLAG_BOUNDS).
+# computed global-memory index is checked in the kernels (XS_FLAG_BOUNDS; those
+# of kv_swap.cu and block_alloc.cu have no checks).
 DEBUG_BUILD_DIR = os.path.join(PKG, "_build_debug")
 DEBUG_LIB_PATH = os.path.join(DEBUG_BUILD_DIR, "libxs_paged_debug.so")
 SOURCES = ["kv_append.cu", "paged_decode.cu", "kv_swap.cu", "block_alloc.cu", "paged_prefill_tc.cu",

@@ -18,22 +18,23 @@
 //            16 x 8 logits are then turned over between the lanes (8 shuffles),
 //            since the second product wants p with its keys along a lane.
 //            (Heads on the rows need no turning, but half of the rows and twice
-//            the matrix instructions: 158 us, where this takes 154 us.)
+//            the matrix instructions: 158 us where this took 154 us, both with
+//            weights of a single rounding.)
 //   values   O[d, h] = sum_t (n_td - 8) (p_th s_tc), dims on the rows, heads on
 //            the columns, bf16, whose range p s needs.  p s is one product in
 //            fp32, which enters as the sum of two bf16 values, what it rounds to
 //            and what that leaves (2^-16 of it is lost): with the first alone
 //            (2^-8) the output was off by 0.0023 of its size where fp32 weights
 //            leave 0.0017, its own rounding, and the long batch took 154 us in
-//            place of 169.  n - 8 is exact.  The scale meets p, not the codes:
+//            place of 171.  n - 8 is exact.  The scale meets p, not the codes:
 //            4 products for a token and head in place of D.
 //
-// What bounds it (32 sequences of 4K to 32K tokens, 32q/8kv x 128, 680 MB): 154 us,
-// 4.4 TB/s, by the instructions of a page and their latencies.  An earlier form
+// What bounds it (32 sequences of 4K to 32K tokens, 32q/8kv x 128, 680 MB): 171 us,
+// 4.0 TB/s, by the instructions of a page and their latencies.  An earlier form
 // took 113 us with both products left out (copies, waits and softmax alone).  A
-// page takes 358 instructions of a warp, about 165 of them on the integer pipe,
-// which takes one every other cycle and is busy 54% of the time; issue slots are
-// 59% busy, the matrix pipe 21%, DRAM 55%.  More or fewer warps, two pages at a
+// page takes 397 instructions of a warp; the integer pipe, which takes one every
+// other cycle, is busy 55% of the time, issue slots 59%, the matrix pipe 29%, DRAM
+// 50%.  With weights of a single rounding, more or fewer warps, two pages at a
 // time, the next page's logits beside this one's values, multiplications for
 // shifts, and 8-bit matrix instructions all measured the same or slower.
 //
@@ -69,21 +70,21 @@ namespace {
 
 // Warps of a CTA, and CTAs on an SM (16 warps of 128 registers): small CTAs
 // where segments are many and often end, larger ones where a segment has many
-// CTAs and what they leave is joined (a 64-sequence step 49 us with 8 warps, 41 us with 4).
+// CTAs and what they leave is joined (a 64-sequence step 48 us with 8 warps, 41 us with 4).
 __host__ __device__ constexpr int dec_warps(bool few) { return few ? 8 : 4; }
 __host__ __device__ constexpr int ctas_per_sm(bool few) { return 16 / dec_warps(few); }
 constexpr int kMaxCtas = 1024;     // the workspace holds partials for so many
 constexpr int kSegmentCost = 16;   // pages
 constexpr int kMinShare = 16;      // pages
 // Segments up to so many pages are not cut: a join costs more (64 segments of
-// 100, 300, 500 tokens 5.7, 7.5, 8.9 us so, 8.5, 9.7, 10.0 us cut; of 1000 17 us so, 11.4 us).
+// 100, 300, 500 tokens 5.9, 8.0, 9.5 us so, 8.7, 10.3, 10.7 us cut; of 1000 15.4 us so, 11.9 us).
 constexpr int kWholePages = 32;
 constexpr int kCluster = 8;        // CTAs of a cluster (of 16: 1.5 us more for a start)
 constexpr int kClusterPages = 256; // of a segment: up to so many a cluster always does it
 constexpr int kLineCluster = 4;    // CTAs of 4 warps of a cluster, for tables of up to
 constexpr int kShortTable = 128;   // so many pages
 // Of a cluster's segment: up to so many pages (2 of a warp) one CTA does alone (18
-// sequences of 200 tokens, 13 pages: 7.8 us so, 6.3 us by a cluster).
+// sequences of 200 tokens, 13 pages: 8.3 us so, 6.3 us by a cluster).
 __host__ __device__ constexpr int alone_pages(int warps) { return 2 * warps; }
 constexpr int kStages = 4;         // pages of a warp's ring
 constexpr float kLead = 8.0f;      // of a reference before the largest logit
@@ -724,7 +725,8 @@ __global__ void __launch_bounds__(32 * dec_warps(false), ctas_per_sm(false))
     constexpr int kDecWarps = dec_warps(false), kDecThreads = 32 * kDecWarps;
     // Placed while the kernel before it ends.  It never lets the next one be
     // placed early: waiting CTAs of the next call on some SMs and not on others
-    // upset the even spread of this call's (a 64-sequence step 40 -> 44 us).
+    // upset the even spread of this call's (a 64-sequence step from 40 to 44 us
+    // with weights of a single rounding).
     griddep_wait();
     extern __shared__ __align__(16) uint8_t smem_raw[];
     DecodeSmem<D, false> &sm = *reinterpret_cast<DecodeSmem<D, false> *>(smem_raw);
@@ -816,9 +818,9 @@ __global__ void __launch_bounds__(32 * dec_warps(false), ctas_per_sm(false))
 // short one its first CTA alone); or, where that leaves too much to one
 // cluster, all segments are cut for all CTAs, as many as there are, and joined
 // through the workspace.  Which, the lengths decide.  (32q/8kv x 128, us, clusters and
-// pieces: one sequence of 300 tokens 5.4 and 7.9, of 2K 6.3 and 8.7, 4K 8.2 and
-// 9.5, 8K 11.2 and 11.9, 12K 14.6 and 13.8; two of 4K 10.3 and 11.0, of 8K 14.7 and
-// 13.1; four of 8K 15.2 and 16.6.)
+// pieces: one sequence of 300 tokens 5.2 and 8.2, of 2K 6.4 and 8.8, 4K 8.4 and
+// 10.8, 8K 12.1 and 12.3, 12K 15.5 and 14.7; two of 4K 10.9 and 11.2, of 8K 15.8 and
+// 13.9; four of 8K 16.3 and 17.5.)
 template <int D>
 __global__ void __launch_bounds__(32 * dec_warps(true), ctas_per_sm(true))
     kv4_decode_few_kernel(const __grid_constant__ Kv4DecodeParams p) {
@@ -918,10 +920,11 @@ __global__ void __launch_bounds__(32 * dec_warps(true), ctas_per_sm(true))
 
 // Short segments, not too many: a cluster of kLineCluster CTAs for each, in the line's
 // form of a CTA (4 of them fill an SM).  A segment of up to alone_pages its
-// first CTA does alone.  (12 sequences of 100, 300, 1K, 2K tokens, 32q/8kv x 128: 5.7, 7.1,
-// 9.3, 13.4 us; on the line 5.8, 7.6, 13.0, 16.4.  The line's kernel itself cannot be launched
-// in clusters for the sake of short calls: it then takes 134 us where it takes 98,
-// for 18 sequences of 20K tokens.)
+// first CTA does alone.  (12 sequences of 100, 300, 1K, 2K tokens, 32q/8kv x 128: 5.4, 6.2,
+// 8.6, 13.1 us; on the line, which also takes them under a table or window of more
+// pages, 6.0, 8.1, 13.5, 17.0.  The line's kernel itself cannot be launched in
+// clusters for the sake of short calls: it then took 134 us where it took 98, for 18
+// sequences of 20K tokens and weights of a single rounding.)
 template <int D>
 __global__ void __launch_bounds__(32 * dec_warps(false), ctas_per_sm(false))
     kv4_decode_short_kernel(const __grid_constant__ Kv4DecodeParams p) {

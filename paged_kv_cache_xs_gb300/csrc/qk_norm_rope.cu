@@ -38,8 +38,9 @@ namespace xs {
 namespace {
 
 constexpr int kRopeThreads = 128;
-constexpr int kRopeCtas = 7;        // on an SM: 72 registers, a few of them spilled (with
-                                    // 6 and none spilled 39 us where it is 36)
+constexpr int kRopeCtas = 7;        // on an SM: 72 registers, a few of them spilled (6 and
+                                    // none spilled: 8K tokens 39 us, 7: 36, before runs
+                                    // were chosen by their waves, which made it 35)
 constexpr int kRopeAheadBytes = 8;  // rows of a lane on their way, times the size of a value
 constexpr int kRopeRun = 48;        // heads of a run at most
 constexpr int kRopeStart = 4;       // rows that a warp's start costs as much as

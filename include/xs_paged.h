@@ -953,6 +953,80 @@ int xs_block_copy(void *k_pools, void *v_pools, int layers, int64_t layer_stride
                   const int64_t *pairs, int64_t n, const int32_t *count, int64_t block_bytes,
                   int64_t num_blocks, int *err_flag, cudaStream_t stream);
 
+/*
+ * Bounded caches: attention to a window and the first tokens, attention that
+ * counts what weight each cached token got, eviction by that count, and giving
+ * back the pages behind a shorter length.
+ *
+ * xs_paged_decode_first - decode attention in which sequence b's query (its
+ * token n - 1, n = context_lens[b]) sees the tokens t < first and t >= n -
+ * window; window 0: every token.  Block table entries of pages without a seen
+ * token are never read (they may be -1: such pages can be given back).  sinks
+ * [Hq] as in xs_paged_decode_sinks, or NULL.  context_lens[b] <= 0 gives out[b]
+ * = 0.  Whatever the pages hold in hidden rows has no influence.  Logits,
+ * weights and sums are held in fp32 (bf16: a weight enters the product with V
+ * with 16 bits); the output is rounded once.
+ *
+ * q: head h of sequence b starts b * q_stride + h * D elements from the pointer,
+ * so that it may be a slice of a projection's output; q_stride is a multiple of
+ * 16 bytes and at least Hq * D.
+ *
+ * workspace: at least xs_paged_decode_first_workspace_bytes(B, Hq, Hkv, D) bytes,
+ * 16-byte aligned, zero before the first call that uses it; every completed call
+ * leaves it fit for the next.  Calls that share one must be ordered (one stream,
+ * or one CUDA graph).
+ * dtype XS_BF16 or XS_F32; block_size 16; D in {64, 128}; Hq / Hkv in {1, 2, 4,
+ * 8}; num_blocks * Hkv < 2^31.
+ * Device-side errors: XS_FLAG_BAD_BLOCK (block 0 was read instead),
+ * XS_FLAG_BAD_LEN (the length was clamped to the table), XS_FLAG_TIMEOUT (a
+ * page did not arrive within 4 s: the outputs of the sequence and KV head it
+ * belongs to, and of those that its warp or CTA did after it, are NaN; the
+ * workspace is fit for the next call).
+ */
+size_t xs_paged_decode_first_workspace_bytes(int B, int Hq, int Hkv, int D);
+int xs_paged_decode_first(void *out, const void *q, int64_t q_stride, const void *k_cache,
+                          const void *v_cache, const int32_t *block_tables, int max_blocks_per_seq,
+                          const int32_t *context_lens, const void *sinks, int first, int window,
+                          int B, int Hq, int Hkv, int D, int block_size, int64_t num_blocks,
+                          float scale, void *workspace, size_t workspace_bytes, int dtype,
+                          int *err_flag, cudaStream_t stream);
+
+/*
+ * xs_paged_decode_weights - decode attention over all of each sequence's cache,
+ * which also adds up the weight that each cached token gets: for t < n =
+ * context_lens[b] and every KV head hk,
+ *     scores[b, hk, t] = (t < scored_lens[b] ? scores[b, hk, t] : 0)
+ *                        + sum over the query heads h of hk of p_ht,
+ * p the softmax weights of the call (a sink takes its share of them).
+ * scores fp32 [B, Hkv, max_blocks_per_seq * 16], rows by sequence slot, not by
+ * page, so that sequences that share pages keep their own; the tokens from n on
+ * are left as they are.  scored_lens int32 [B]: how many tokens have a score
+ * from earlier calls (0 starts a sequence: nothing that the row held counts);
+ * NULL: n - 1, all but the new one.  A token whose logit is NaN, and every token
+ * of a head that has one, gets a NaN.
+ * To count the weights of a prompt's last rows, list its table once for each of
+ * them, with their lengths, and add their rows of scores up.
+ *
+ * The rest as xs_paged_decode_first with window 0.  workspace: at least
+ * xs_paged_decode_weights_workspace_bytes(B, Hq, Hkv, D, max_blocks_per_seq)
+ * bytes; that of a wider table or a larger batch serves smaller ones of the
+ * same heads.
+ */
+size_t xs_paged_decode_weights_workspace_bytes(int B, int Hq, int Hkv, int D,
+                                               int max_blocks_per_seq);
+int xs_paged_decode_weights(void *out, float *scores, const int32_t *scored_lens, const void *q,
+                            int64_t q_stride, const void *k_cache, const void *v_cache,
+                            const int32_t *block_tables, int max_blocks_per_seq,
+                            const int32_t *context_lens, const void *sinks, int B, int Hq, int Hkv,
+                            int D, int block_size, int64_t num_blocks, float scale, void *workspace,
+                            size_t workspace_bytes, int dtype, int *err_flag, cudaStream_t stream);
+
+/*
+ * xs_debug_bounded_wait_injection - xs_debug_kv4_wait_injection for
+ * xs_paged_decode_first and xs_paged_decode_weights.
+ */
+int xs_debug_bounded_wait_injection(int64_t wait_limit_ns, int skip_page);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,4 +1,4 @@
-// Python binding of the norm + rotation, 4-bit cache and shared-page calls:
+// Python binding of the norm + rotation, 4-bit cache, shared-page and bounded-cache calls:
 // checks the tensors and passes their addresses to the library's entry point,
 // whose address each call is given.  A decode step makes these calls once for
 // every layer, and their kernels run for a few microseconds: the checks take
@@ -505,6 +505,58 @@ PyObject *block_copy(Args a) {
     });
 }
 
+// ------------------------------------------------------------------ bounded caches
+
+PyObject *decode_bounded(Args a, bool weights) {
+    void *entry = a.entry();
+    const at::Tensor &out = a.tensor("out");
+    const at::Tensor *scores = weights ? &a.tensor("scores") : nullptr;
+    const at::Tensor &q = a.tensor("q");
+    const at::Tensor &kc = a.tensor("k_cache"), &vc = a.tensor("v_cache");
+    const at::Tensor &tables = a.tensor("block_tables"), &lens = a.tensor("context_lens");
+    const float scale = static_cast<float>(a.number());
+    const at::Tensor &ws = a.tensor("workspace");
+    const int ws_hq = a.integer("workspace"), ws_hkv = a.integer("workspace"), ws_d = a.integer("workspace");
+    const int first = weights ? 0 : a.integer("first"), window = weights ? 0 : a.integer("window");
+    const at::Tensor *scored = weights ? a.maybe("scored_lens") : nullptr;
+    const at::Tensor *sinks = a.maybe("sinks"), *err = a.maybe("err_flag");
+    PyObject *stream = a.next();
+    dims(q, 3, "q"), dims(kc, 4, "a pool");
+    const int64_t B = q.size(0), Hq = q.size(1), D = q.size(2), Hkv = kc.size(1);
+    want(out, q.scalar_type(), {B, Hq, D}, "out");
+    bool kv4 = false;
+    const int64_t blocks = pools(kc, vc, q.scalar_type(), Hkv, D, &kv4);
+    if (kv4) refuse("a 4-bit pool is not supported here");
+    const int width = table_width(tables, lens, B);
+    want(scores, at::kFloat, {B, Hkv, static_cast<int64_t>(width) * kPage}, "scores");
+    want(scored, at::kInt, {B}, "scored_lens");
+    want(sinks, q.scalar_type(), {Hq}, "sinks");
+    want(err, at::kInt, {1}, "err_flag");
+    if (ws_hq != Hq || ws_hkv != Hkv || ws_d != D) refuse("the workspace is for other heads");
+    const int code = dtype_code(q), b = as_int(B, "q"), hq = as_int(Hq, "q"),
+              hkv = as_int(Hkv, "k_cache"), d = as_int(D, "q");
+    const int64_t q_stride = rows(q, "q");
+    const cudaStream_t s = stream_for(stream, {&q, &out, scores, &kc, &vc, &tables, &lens, &ws, scored, sinks, err});
+    void *op = whole(out, "out"), *wp = whole(ws, "workspace");
+    float *sp = static_cast<float *>(whole(scores, "scores"));
+    const int32_t *np = static_cast<int32_t *>(whole(scored, "scored_lens"));
+    const void *qp = q.data_ptr(), *kcp = whole(kc, "k_cache"), *vcp = whole(vc, "v_cache");
+    const int32_t *tp = static_cast<int32_t *>(whole(tables, "block_tables"));
+    const int32_t *lp = static_cast<int32_t *>(whole(lens, "context_lens"));
+    const void *zp = whole(sinks, "sinks");
+    int *flag = static_cast<int *>(whole(err, "err_flag"));
+    if (B == 0) return PyLong_FromLong(XS_OK);
+    const size_t bytes = static_cast<size_t>(ws.numel()) * ws.element_size();
+    return status([&] {
+        return weights ? reinterpret_cast<decltype(&xs_paged_decode_weights)>(entry)(
+                             op, sp, np, qp, q_stride, kcp, vcp, tp, width, lp, zp, b, hq, hkv, d, kPage, blocks,
+                             scale, wp, bytes, code, flag, s)
+                       : reinterpret_cast<decltype(&xs_paged_decode_first)>(entry)(
+                             op, qp, q_stride, kcp, vcp, tp, width, lp, zp, first, window, b, hq, hkv, d, kPage,
+                             blocks, scale, wp, bytes, code, flag, s);
+    });
+}
+
 // ------------------------------------------------------------------ the module
 
 template <typename F> PyObject *guarded(PyObject *const *args, Py_ssize_t n, F &&f) {
@@ -534,6 +586,8 @@ XS_BIND(xs_block_fork, block_fork(a))
 XS_BIND(xs_block_release, block_release(a))
 XS_BIND(xs_block_compact, block_compact(a))
 XS_BIND(xs_block_copy, block_copy(a))
+XS_BIND(xs_paged_decode_first, decode_bounded(a, false))
+XS_BIND(xs_paged_decode_weights, decode_bounded(a, true))
 
 #define XS_METHOD(name) \
     {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(py_##name)), METH_FASTCALL, nullptr}
@@ -548,6 +602,8 @@ PyMethodDef methods[] = {XS_METHOD(xs_qk_norm_rope),
                          XS_METHOD(xs_block_release),
                          XS_METHOD(xs_block_compact),
                          XS_METHOD(xs_block_copy),
+                         XS_METHOD(xs_paged_decode_first),
+                         XS_METHOD(xs_paged_decode_weights),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "xs_bind", nullptr, -1, methods,
                       nullptr,               nullptr,   nullptr, nullptr};

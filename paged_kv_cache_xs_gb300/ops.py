@@ -98,10 +98,17 @@ SIGNATURES = {
     "xs_block_release": (_I, [_P, _I, _P, _I, _P, _I, _I, _P, _P, _L, _P, _L, _P, _P]),
     "xs_block_compact": (_I, [_P, _P, _I, _P, _I, _I, _P, _P, _P, _P, _L, _P, _P, _P, _P, _P]),
     "xs_block_copy": (_I, [_P, _P, _I, _L, _P, _L, _P, _L, _L, _P, _P]),
+    "xs_paged_decode_first_workspace_bytes": (_S, [_I, _I, _I, _I]),
+    "xs_paged_decode_first": (_I, [_P, _P, _L, _P, _P, _P, _I, _P, _P, _I, _I, _I, _I, _I, _I, _I,
+                                   _L, _F, _P, _S, _I, _P, _P]),
+    "xs_paged_decode_weights_workspace_bytes": (_S, [_I, _I, _I, _I, _I]),
+    "xs_paged_decode_weights": (_I, [_P, _P, _P, _P, _L, _P, _P, _P, _I, _P, _P, _I, _I, _I, _I,
+                                     _I, _L, _F, _P, _S, _I, _P, _P]),
     "xs_version": (_I, []),
     "xs_debug_bounds_failures": (_I, [_I]),
     "xs_debug_wait_injection": (_I, [_L, _I]),
     "xs_debug_kv4_wait_injection": (_I, [_L, _I]),
+    "xs_debug_bounded_wait_injection": (_I, [_L, _I]),
 }
 
 _lock = threading.Lock()
@@ -637,6 +644,49 @@ def xs_block_copy(k_pools, v_pools, pairs, count=None, err_flag=None, stream=Non
         _entry("xs_block_copy"), k_pools, v_pools, pairs, count, err_flag, _handle(stream)))
 
 
+# ---------------------------------------------------------------- bounded caches
+
+class BoundedWorkspace:
+    """Workspace of xs_paged_decode_first, and with max_blocks_per_seq also of
+    xs_paged_decode_weights, for batches of up to B sequences (and tables of up
+    to so many blocks), allocated (zeroed) once; calls that share one must be
+    ordered."""
+
+    def __init__(self, B: int, Hq: int, Hkv: int, D: int, device, max_blocks_per_seq: int = 0):
+        self.B, self.Hq, self.Hkv, self.D = B, Hq, Hkv, D
+        if max_blocks_per_seq:
+            nbytes = int(load().xs_paged_decode_weights_workspace_bytes(B, Hq, Hkv, D,
+                                                                        max_blocks_per_seq))
+        else:
+            nbytes = int(load().xs_paged_decode_first_workspace_bytes(B, Hq, Hkv, D))
+        self.buf = torch.zeros(max(nbytes, 16), dtype=torch.uint8, device=device)
+
+
+def xs_paged_decode_first(out, q, k_cache, v_cache, block_tables, context_lens, scale, workspace,
+                          first=0, window=0, sinks=None, err_flag=None, stream=None):
+    """Decode attention to the first ``first`` tokens and the last ``window``
+    ones of each sequence (window 0: all), with optional sinks ([Hq]); q [B,
+    Hq, D] may be a slice of a projection's output.  Table entries of pages
+    without a visible token are not read."""
+    w = workspace
+    _done("xs_paged_decode_first", (_bound or _bind()).xs_paged_decode_first(
+        _entry("xs_paged_decode_first"), out, q, k_cache, v_cache, block_tables, context_lens,
+        scale, w.buf, w.Hq, w.Hkv, w.D, first, window, sinks, err_flag, _handle(stream)))
+
+
+def xs_paged_decode_weights(out, scores, q, k_cache, v_cache, block_tables, context_lens, scale,
+                            workspace, scored_lens=None, sinks=None, err_flag=None, stream=None):
+    """Decode attention that adds the weight each cached token gets from a KV
+    head's query heads to scores (fp32 [B, Hkv, max_blocks * 16]).  Tokens at
+    and behind scored_lens (int32 [B]; None: context_lens - 1) start from
+    zero; q may be a slice of a projection's output."""
+    w = workspace
+    _done("xs_paged_decode_weights", (_bound or _bind()).xs_paged_decode_weights(
+        _entry("xs_paged_decode_weights"), out, scores, q, k_cache, v_cache, block_tables,
+        context_lens, scale, w.buf, w.Hq, w.Hkv, w.D, scored_lens, sinks, err_flag,
+        _handle(stream)))
+
+
 def xs_version() -> int:
     return load().xs_version()
 
@@ -663,6 +713,14 @@ def xs_debug_kv4_wait_injection(wait_limit_ns: int, skip_page: int = -1, lib=Non
     code = lib.xs_debug_kv4_wait_injection(int(wait_limit_ns), int(skip_page))
     if code != 0:
         raise XsError("xs_debug_kv4_wait_injection", code)
+
+
+def xs_debug_bounded_wait_injection(wait_limit_ns: int, skip_page: int = -1, lib=None) -> None:
+    """The same for xs_paged_decode_first and xs_paged_decode_weights."""
+    lib = lib or load()
+    code = lib.xs_debug_bounded_wait_injection(int(wait_limit_ns), int(skip_page))
+    if code != 0:
+        raise XsError("xs_debug_bounded_wait_injection", code)
 
 
 def load_debug():

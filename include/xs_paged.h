@@ -91,6 +91,9 @@ extern "C" {
 #define XS_FLAG_POOL_EMPTY 32 /* the free-block stack was empty (allocation)
                                  or full (release); that sequence was left
                                  as it was                                    */
+#define XS_FLAG_SHARED 128  /* a page that would be written belongs to another
+                               sequence too (xs_kv_evict); the sequence was left
+                               as it was                                      */
 #define XS_FLAG_BOUNDS 64   /* only in the debug build (libxs_paged_debug.so,
                                compiled with -DXS_DEBUG_BOUNDS): a computed
                                global-memory index fell outside its buffer;
@@ -1020,6 +1023,60 @@ int xs_paged_decode_weights(void *out, float *scores, const int32_t *scored_lens
                             const int32_t *context_lens, const void *sinks, int B, int Hq, int Hkv,
                             int D, int block_size, int64_t num_blocks, float scale, void *workspace,
                             size_t workspace_bytes, int dtype, int *err_flag, cudaStream_t stream);
+
+/*
+ * xs_kv_evict - cuts sequences to a budget of tokens by their scores, as
+ * xs_paged_decode_weights counts them.  For every listed slot b = seq_ids[i]
+ * with n = context_lens[b] > limit, in every layer and for every KV head by
+ * itself, `budget` positions are kept: t < first, t >= n - recent, and the
+ * budget - first - recent of those between whose scores are largest (of equal
+ * ones the lower positions; NaN counts as -infinity).  In order, they become
+ * positions 0 .. budget - 1: their K and V rows move in the sequence's pages,
+ * bit for bit, and their scores in its rows of scores.  What lies at and behind
+ * position budget is left as it is.
+ *   k_pools, v_pools  `layers` pools [num_blocks, Hkv, 16, D] of dtype,
+ *                     layer_stride_bytes apart (a multiple of 16)
+ *   scores            fp32 [layers, B, Hkv, max_blocks_per_seq * 16]
+ *   kept              int32 [layers, n, Hkv, budget]: the positions kept, ascending
+ *                     (-1 throughout for an entry that is not cut)
+ *   new_lens          int32 [n]: budget for the entries that were cut, -1 for
+ *                     the others, as xs_block_truncate takes them
+ * Lengths and tables are left as they are: xs_block_truncate(seq_ids, new_lens)
+ * shortens them and gives the pages back, and has to come before the next append
+ * or attention.  A token keeps the rotation of the position that it had; later
+ * tokens are rotated by their own (xs_qk_norm_rope_append with positions).
+ * extra_refs (int32 [num_blocks], or NULL: nothing is shared): a sequence of
+ * which a page that is written has further owners is not cut (XS_FLAG_SHARED);
+ * it has to have pages of its own first.  Not cut either: an id outside [0, B)
+ * or one that an earlier entry has (XS_FLAG_BAD_SLOT), and a sequence with a table
+ * entry outside the pool behind the first tokens' whole pages (XS_FLAG_BAD_BLOCK).
+ * A length beyond the table counts as the table's (XS_FLAG_BAD_LEN).
+ * first, recent >= 0, first + recent <= budget <= limit, budget > 0; D in {64,
+ * 128}; block_size 16.
+ */
+int xs_kv_evict(const int32_t *seq_ids, int n, void *k_pools, void *v_pools, int layers,
+                int64_t layer_stride_bytes, float *scores, const int32_t *block_tables,
+                int max_blocks_per_seq, const int32_t *context_lens, int B,
+                const int32_t *extra_refs, int first, int recent, int budget, int limit, int Hkv,
+                int D, int block_size, int64_t num_blocks, int dtype, int32_t *kept,
+                int32_t *new_lens, int *err_flag, cudaStream_t stream);
+
+/*
+ * xs_block_truncate - shortens sequences: slot seq_ids[i] gets length new_lens[i]
+ * if that is not negative and below its length.  The pages behind the new
+ * length lose one owner and leave its table (-1); those that lost their last one
+ * go back on the free stack as by xs_block_release.  After an eviction, a
+ * rejected draft or a rolled-back request.  An unfinished last page stays the
+ * sequence's; one that is shared (a length cut into a forked prefix) must be
+ * replaced before an append to it.
+ * XS_FLAG_BAD_SLOT: an id outside [0, B), or one that an earlier entry has (the
+ * earlier one counts).  XS_FLAG_BAD_BLOCK, XS_FLAG_POOL_EMPTY as
+ * xs_block_release.
+ */
+int xs_block_truncate(const int32_t *seq_ids, const int32_t *new_lens, int n, int32_t *block_tables,
+                      int max_blocks_per_seq, int32_t *context_lens, int B, int block_size,
+                      int32_t *free_stack, int32_t *free_top, int64_t stack_capacity,
+                      int32_t *extra_refs, int64_t num_blocks, int *err_flag, cudaStream_t stream);
 
 /*
  * xs_debug_bounded_wait_injection - xs_debug_kv4_wait_injection for

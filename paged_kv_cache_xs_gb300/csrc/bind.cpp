@@ -413,9 +413,11 @@ PyObject *block_fork(Args a) {
     });
 }
 
-PyObject *block_release(Args a) {
+// cut: to new lengths (xs_block_truncate).
+PyObject *block_release(Args a, bool cut) {
     void *entry = a.entry();
     const at::Tensor &ids = a.tensor("seq_ids");
+    const at::Tensor *to = cut ? &a.tensor("new_lens") : nullptr;
     const at::Tensor &tables = a.tensor("block_tables"), &lens = a.tensor("context_lens");
     const Share sh(a);
     const int bs = a.integer("block_size");
@@ -423,11 +425,13 @@ PyObject *block_release(Args a) {
     PyObject *stream = a.next();
     const int64_t n = ids.numel(), B = lens.numel();
     want(ids, at::kInt, {n}, "seq_ids");
+    want(to, at::kInt, {n}, "new_lens");
     want(err, at::kInt, {1}, "err_flag");
     const int width = table_width(tables, lens, B);
     const cudaStream_t s =
-        stream_for(stream, {&ids, &tables, &lens, &sh.stack, &sh.top, &sh.extra, err});
+        stream_for(stream, {&ids, to, &tables, &lens, &sh.stack, &sh.top, &sh.extra, err});
     const int32_t *ip = static_cast<int32_t *>(whole(ids, "seq_ids"));
+    const int32_t *np = static_cast<int32_t *>(whole(to, "new_lens"));
     int32_t *tp = static_cast<int32_t *>(whole(tables, "block_tables"));
     int32_t *lp = static_cast<int32_t *>(whole(lens, "context_lens"));
     int32_t *sp = sh.ptr(sh.stack, "free_stack"), *top = sh.ptr(sh.top, "free_top"),
@@ -436,8 +440,12 @@ PyObject *block_release(Args a) {
     if (n == 0) return PyLong_FromLong(XS_OK);
     const int count = as_int(n, "seq_ids"), b = as_int(B, "context_lens");
     return status([&] {
-        return reinterpret_cast<decltype(&xs_block_release)>(entry)(
-            ip, count, tp, width, lp, b, bs, sp, top, sh.stack.numel(), ep, sh.extra.numel(), flag, s);
+        return cut ? reinterpret_cast<decltype(&xs_block_truncate)>(entry)(
+                         ip, np, count, tp, width, lp, b, bs, sp, top, sh.stack.numel(), ep,
+                         sh.extra.numel(), flag, s)
+                   : reinterpret_cast<decltype(&xs_block_release)>(entry)(
+                         ip, count, tp, width, lp, b, bs, sp, top, sh.stack.numel(), ep,
+                         sh.extra.numel(), flag, s);
     });
 }
 
@@ -557,6 +565,48 @@ PyObject *decode_bounded(Args a, bool weights) {
     });
 }
 
+PyObject *kv_evict(Args a) {
+    void *entry = a.entry();
+    const at::Tensor &ids = a.tensor("seq_ids");
+    const at::Tensor &k = a.tensor("k_pools"), &v = a.tensor("v_pools"), &scores = a.tensor("scores");
+    const at::Tensor &tables = a.tensor("block_tables"), &lens = a.tensor("context_lens");
+    const at::Tensor &kept = a.tensor("kept"), &new_lens = a.tensor("new_lens");
+    const int first = a.integer("first"), recent = a.integer("recent"), limit = a.integer("limit");
+    const at::Tensor *extra = a.maybe("extra_refs"), *err = a.maybe("err_flag");
+    PyObject *stream = a.next();
+    dims(k, 5, "k_pools");
+    const int64_t n = ids.numel(), B = lens.numel(), L = k.size(0), nb = k.size(1), Hkv = k.size(2), D = k.size(4);
+    want(k, k.scalar_type(), {L, nb, Hkv, kPage, D}, "k_pools");
+    want(v, k.scalar_type(), {L, nb, Hkv, kPage, D}, "v_pools");
+    const int width = table_width(tables, lens, B);
+    want(scores, at::kFloat, {L, B, Hkv, static_cast<int64_t>(width) * kPage}, "scores");
+    want(ids, at::kInt, {n}, "seq_ids");
+    dims(kept, 4, "kept");
+    const int64_t budget = kept.size(3);
+    want(kept, at::kInt, {L, n, Hkv, budget}, "kept");
+    want(new_lens, at::kInt, {n}, "new_lens");
+    want(extra, at::kInt, {nb}, "extra_refs");
+    want(err, at::kInt, {1}, "err_flag");
+    const int code = dtype_code(k), count = as_int(n, "seq_ids"), layers = as_int(L, "k_pools"),
+              b = as_int(B, "context_lens"), hkv = as_int(Hkv, "k_pools"), d = as_int(D, "k_pools"),
+              keep = as_int(budget, "kept");
+    const cudaStream_t s = stream_for(stream, {&ids, &k, &v, &scores, &tables, &lens, &kept, &new_lens, extra, err});
+    const int32_t *ip = static_cast<int32_t *>(whole(ids, "seq_ids"));
+    void *kp = whole(k, "k_pools"), *vp = whole(v, "v_pools");
+    float *sp = static_cast<float *>(whole(scores, "scores"));
+    const int32_t *tp = static_cast<int32_t *>(whole(tables, "block_tables"));
+    const int32_t *lp = static_cast<int32_t *>(whole(lens, "context_lens"));
+    const int32_t *ep = static_cast<int32_t *>(whole(extra, "extra_refs"));
+    int32_t *at = static_cast<int32_t *>(whole(kept, "kept")), *np = static_cast<int32_t *>(whole(new_lens, "new_lens"));
+    int *flag = static_cast<int *>(whole(err, "err_flag"));
+    if (n == 0 || L == 0) return PyLong_FromLong(XS_OK);
+    return status([&] {
+        return reinterpret_cast<decltype(&xs_kv_evict)>(entry)(
+            ip, count, kp, vp, layers, nb * hkv * kPage * d * k.element_size(), sp, tp, width, lp, b, ep, first,
+            recent, keep, limit, hkv, d, kPage, nb, code, at, np, flag, s);
+    });
+}
+
 // ------------------------------------------------------------------ the module
 
 template <typename F> PyObject *guarded(PyObject *const *args, Py_ssize_t n, F &&f) {
@@ -583,7 +633,9 @@ XS_BIND(xs_kv4_append_paged, kv4_append(a, true))
 XS_BIND(xs_kv4_unpack, kv4_unpack(a))
 XS_BIND(xs_kv4_decode, kv4_decode(a))
 XS_BIND(xs_block_fork, block_fork(a))
-XS_BIND(xs_block_release, block_release(a))
+XS_BIND(xs_block_release, block_release(a, false))
+XS_BIND(xs_block_truncate, block_release(a, true))
+XS_BIND(xs_kv_evict, kv_evict(a))
 XS_BIND(xs_block_compact, block_compact(a))
 XS_BIND(xs_block_copy, block_copy(a))
 XS_BIND(xs_paged_decode_first, decode_bounded(a, false))
@@ -600,6 +652,8 @@ PyMethodDef methods[] = {XS_METHOD(xs_qk_norm_rope),
                          XS_METHOD(xs_kv4_decode),
                          XS_METHOD(xs_block_fork),
                          XS_METHOD(xs_block_release),
+                         XS_METHOD(xs_block_truncate),
+                         XS_METHOD(xs_kv_evict),
                          XS_METHOD(xs_block_compact),
                          XS_METHOD(xs_block_copy),
                          XS_METHOD(xs_paged_decode_first),

@@ -260,6 +260,29 @@ __global__ void __launch_bounds__(kShareThreads)
     if (threadIdx.x == 0) *free_top = top - min(popped, top);
 }
 
+// The blocks whose count fell below zero go on the free stack, the highest id
+// first, so that the lowest is the next one taken; their counts become 0.
+__device__ __forceinline__ void push_freed(cg::cluster_group &cluster, ShareCounts &counts,
+                                           int32_t *free_stack, int64_t top, int32_t *free_top,
+                                           int64_t capacity, int32_t *extra_refs, int64_t num_blocks,
+                                           int *err_flag) {
+    const int rank = cluster.block_rank(), ranks = cluster.num_blocks();
+    const Part part = warp_part(num_blocks, rank, ranks);
+    auto freed = [&](int64_t i) { return __ldcg(extra_refs + (num_blocks - 1 - i)) < 0; };
+    int64_t total;
+    const int64_t before = cluster_scan(cluster, counts, count_part(part, freed), &total);
+    write_part(part, top + before, freed, [&](int64_t k, int64_t i) {
+        const int64_t id = num_blocks - 1 - i;
+        if (!XS_BOUNDS(k >= 0 && id >= 0 && id < num_blocks, err_flag)) return;
+        if (k < capacity)
+            free_stack[k] = static_cast<int32_t>(id);
+        else
+            raise_flag(err_flag, XS_FLAG_POOL_EMPTY);
+        extra_refs[id] = 0;
+    });
+    if (rank == 0 && threadIdx.x == 0) *free_top = static_cast<int32_t>(min(top + total, capacity));
+}
+
 // A block whose count falls below zero is marked by that until the scan over
 // the block ids has pushed it.
 __global__ void __launch_bounds__(kShareThreads)
@@ -304,21 +327,48 @@ __global__ void __launch_bounds__(kShareThreads)
         for (int col = 128 + lane; col < max_blocks; col += 32) drop(col, row[col]);
     }
     launch_sync(cluster);
-    // Highest id first, so that the lowest is the next one taken.
-    const Part part = warp_part(num_blocks, rank, ranks);
-    auto freed = [&](int64_t i) { return __ldcg(extra_refs + (num_blocks - 1 - i)) < 0; };
-    int64_t total;
-    const int64_t before = cluster_scan(cluster, counts, count_part(part, freed), &total);
-    write_part(part, top + before, freed, [&](int64_t k, int64_t i) {
-        const int64_t id = num_blocks - 1 - i;
-        if (!XS_BOUNDS(k >= 0 && id >= 0 && id < num_blocks, err_flag)) return;
-        if (k < capacity)
-            free_stack[k] = static_cast<int32_t>(id);
-        else
-            raise_flag(err_flag, XS_FLAG_POOL_EMPTY);
-        extra_refs[id] = 0;
-    });
-    if (rank == 0 && threadIdx.x == 0) *free_top = static_cast<int32_t>(min(top + total, capacity));
+    push_freed(cluster, counts, free_stack, top, free_top, capacity, extra_refs, num_blocks, err_flag);
+}
+
+// Gives back the pages behind a new length: like a release of these alone.
+__global__ void __launch_bounds__(kShareThreads)
+    block_truncate_kernel(const int32_t *__restrict__ seq_ids, const int32_t *__restrict__ new_lens,
+                          int n, int32_t *tables, int max_blocks, int32_t *lens, int B, int bs,
+                          int32_t *free_stack, int32_t *free_top, int64_t capacity,
+                          int32_t *extra_refs, int64_t num_blocks, int *err_flag) {
+    after_previous();
+    __shared__ ShareCounts counts;
+    cg::cluster_group cluster = cg::this_cluster();
+    const int rank = cluster.block_rank(), ranks = cluster.num_blocks();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t top = *free_top;
+    for (int k = rank + warp * ranks; k < n; k += ranks * static_cast<int>(blockDim.x >> 5)) {
+        const int b = seq_ids[k], to = new_lens[k];
+        // An entry of a slot that an earlier one has is not done.
+        bool again = false;
+        for (int i = lane; i < k; i += 32) again |= seq_ids[i] == b;
+        if (__any_sync(0xffffffffu, again) || b < 0 || b >= B) {
+            if (lane == 0) raise_flag(err_flag, XS_FLAG_BAD_SLOT);
+            continue;
+        }
+        const int len = lens[b];
+        if (to < 0 || to >= len) continue;
+        int32_t *row = tables + static_cast<int64_t>(b) * max_blocks;
+        const int pages = pages_of(len, bs, max_blocks);
+#pragma unroll 4
+        for (int col = pages_of(to, bs, max_blocks) + lane; col < pages; col += 32) {
+            const int32_t id = row[col];
+            if (id >= 0 && id < num_blocks)
+                atomicSub(extra_refs + id, 1);
+            else
+                raise_flag(err_flag, XS_FLAG_BAD_BLOCK);
+            if (XS_BOUNDS(col >= 0 && col < max_blocks, err_flag)) row[col] = -1;
+        }
+        __syncwarp();
+        if (lane == 0 && XS_BOUNDS(b >= 0 && b < B, err_flag)) lens[b] = to;
+    }
+    launch_sync(cluster);
+    push_freed(cluster, counts, free_stack, top, free_top, capacity, extra_refs, num_blocks, err_flag);
 }
 
 // remap first marks the live blocks (0), then holds the new ids.
@@ -520,6 +570,25 @@ extern "C" int xs_block_release(const int32_t *seq_ids, int n, int32_t *block_ta
                             stream, seq_ids, n, block_tables, max_blocks_per_seq, context_lens, B,
                             block_size, free_stack, free_top, stack_capacity, extra_refs,
                             num_blocks, err_flag);
+}
+
+extern "C" int xs_block_truncate(const int32_t *seq_ids, const int32_t *new_lens, int n,
+                                 int32_t *block_tables, int max_blocks_per_seq,
+                                 int32_t *context_lens, int B, int block_size, int32_t *free_stack,
+                                 int32_t *free_top, int64_t stack_capacity, int32_t *extra_refs,
+                                 int64_t num_blocks, int *err_flag, cudaStream_t stream) {
+    if (!seq_ids || !new_lens || !block_tables || !context_lens || !free_stack || !free_top ||
+        !extra_refs)
+        return XS_ENULL;
+    if (n < 0 || B < 0 || max_blocks_per_seq < 0 || block_size <= 0 || stack_capacity < 0 ||
+        num_blocks < 0 || num_blocks > INT_MAX)
+        return XS_ESHAPE;
+    if (n == 0) return XS_OK;
+    const int64_t entries = static_cast<int64_t>(n) * max_blocks_per_seq;
+    return xs::launch_share(xs::block_truncate_kernel, num_blocks > entries ? num_blocks : entries,
+                            stream, seq_ids, new_lens, n, block_tables, max_blocks_per_seq,
+                            context_lens, B, block_size, free_stack, free_top, stack_capacity,
+                            extra_refs, num_blocks, err_flag);
 }
 
 extern "C" int xs_block_compact(const int32_t *block_tables, int32_t *block_tables_out,

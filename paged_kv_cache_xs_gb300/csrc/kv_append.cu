@@ -184,7 +184,8 @@ int bounds_failures_append(int reset) {
     int total = 0;
     for (const int v : {bounds_failures_append_only(reset), bounds_failures_rope(reset),
                         bounds_failures_kv4_cache(reset), bounds_failures_kv4_decode(reset),
-                        bounds_failures_share(reset), bounds_failures_bounded(reset)}) {
+                        bounds_failures_share(reset), bounds_failures_bounded(reset),
+                        bounds_failures_evict(reset)}) {
         if (v < 0) return v;
         total += v;
     }

@@ -1,0 +1,344 @@
+// Eviction from a paged cache by accumulated attention weight: sequences longer
+// than a limit are cut to a budget of tokens, in every layer and for every KV
+// head by itself: the first ones, the last ones and, of those between, the ones
+// of largest score (of equal ones the earlier).  What is kept moves together to
+// the sequence's first pages, in order.
+//
+// Two launches.  The first ranks: a CTA for each (layer, sequence, KV head) finds
+// the score that is the last to be kept by radix selection on the scores' bits,
+// 11, 11 and 10 of them at a time, counted in shared memory (11 bits: sign,
+// exponent and two more, so that scores of one magnitude spread over bins), and
+// writes the kept positions.  The scores stay in shared memory for the passes.
+// Each warp counts, then writes, a contiguous part, so there are no barriers
+// within a pass and the order of atomics decides nothing.
+//
+// The second moves rows, in place.  Position j takes the row of position
+// kept[j] >= j, so a CTA that goes through j upwards and reads a tile before it
+// writes one overwrites nothing that is still to be read, and may have the tile
+// after it under way.  CTAs share a (layer, sequence, KV head) by K, V and slices
+// of the rows' bytes, never by tokens.  Rows that stay where they are (the first
+// tokens) are neither read nor written.
+#include <atomic>
+#include <climits>
+
+#include "xs_common.cuh"
+
+namespace xs {
+namespace {
+
+constexpr int kPage = 16;
+constexpr int kBins = 2048;
+constexpr int kMoveThreads = 256;
+constexpr int kMoveUnroll = 4;      // 16-byte pieces of a thread in a tile
+constexpr int kScoresHeld = 49152;  // in shared memory; of more, they are read again for each pass
+
+struct EvictParams {
+    const int32_t *seq_ids;
+    int n;
+    char *k_pools, *v_pools;
+    int64_t layer_bytes;        // between two layers' pools
+    float *scores;              // [layers, B, Hkv, max_blocks * 16]
+    const int32_t *tables, *lens, *extra;
+    int max_blocks, B, Hkv, layers, row_bytes;
+    int64_t num_blocks;
+    int first, recent, budget, limit;
+    int32_t *kept, *new_lens;
+    int *err_flag;
+};
+
+// Larger for a larger score; NaN as -infinity, -0 as 0.
+__device__ __forceinline__ uint32_t key_of(uint32_t bits) {
+    if ((bits & 0x7fffffffu) > 0x7f800000u) bits = 0xff800000u;
+    if (bits == 0x80000000u) bits = 0;
+    return bits & 0x80000000u ? ~bits : bits | 0x80000000u;
+}
+
+// Sum of v over the block's threads before this one; `total`: over all.
+template <int kThreads> __device__ __forceinline__ int scan_threads(int v, int *sm, int *total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int inc = v;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, inc, d);
+        if (lane >= d) inc += y;
+    }
+    __syncthreads();
+    if (lane == 31) sm[warp] = inc;
+    __syncthreads();
+    int before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+        if (w == warp) before = all;
+        all += sm[w];
+    }
+    *total = all;
+    return before + inc - v;
+}
+
+template <int kThreads>
+__global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_constant__ EvictParams p) {
+    after_previous();
+    extern __shared__ uint32_t held[];      // the scores' bits, where they fit
+    __shared__ int hist[kBins], sm[kThreads / 32], bin, left;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int hk = blockIdx.x % p.Hkv, entry = blockIdx.x / p.Hkv % p.n;
+    const int layer = blockIdx.x / p.Hkv / p.n;
+    const bool tells = layer == 0 && hk == 0;       // of this entry, what is not a head's own
+    int32_t *kept = p.kept + static_cast<int64_t>(blockIdx.x) * p.budget;
+
+    // Whether the sequence is cut: the same for all its heads and layers.
+    const int b = XS_BOUNDS(entry < p.n && layer < p.layers, p.err_flag) ? p.seq_ids[entry] : -1;
+    int flag = b < 0 || b >= p.B ? XS_FLAG_BAD_SLOT : 0, len = -1;
+    if (!flag) {
+        len = p.lens[b];
+        for (int i = tid; i < entry; i += kThreads)
+            if (p.seq_ids[i] == b) flag = XS_FLAG_BAD_SLOT;
+    }
+    const int n = min(len, p.max_blocks * kPage);
+    if (n > p.limit) {
+        const int32_t *row = p.tables + static_cast<int64_t>(b) * p.max_blocks;
+        for (int c = p.first / kPage + tid; c < (n + kPage - 1) / kPage; c += kThreads) {
+            const int32_t id = row[c];
+            if (id < 0 || id >= p.num_blocks)
+                flag |= XS_FLAG_BAD_BLOCK;
+            else if (p.extra && c <= (p.budget - 1) / kPage && p.extra[id] > 0)
+                flag |= XS_FLAG_SHARED;
+        }
+    }
+    const bool stop = __syncthreads_or(flag);
+    if (tells && flag) raise_flag(p.err_flag, flag);
+    if (tells && tid == 0 && len > n) raise_flag(p.err_flag, XS_FLAG_BAD_LEN);
+    const bool cut = !stop && n > p.limit;
+    if (tells && tid == 0) p.new_lens[entry] = cut ? p.budget : -1;
+    if (!cut) {
+        for (int j = tid; j < p.budget; j += kThreads) kept[j] = -1;
+        return;
+    }
+
+    const uint32_t *score = reinterpret_cast<const uint32_t *>(
+        p.scores + ((static_cast<int64_t>(layer) * p.B + b) * p.Hkv + hk) * p.max_blocks * kPage);
+    const int lo = p.first, hi = n - p.recent;      // [lo, hi) are chosen from
+    const bool fits = p.max_blocks * static_cast<int64_t>(kPage) <= kScoresHeld;
+    if (fits) {
+#pragma unroll 4
+        for (int t = lo + tid; t < hi; t += kThreads) held[t] = score[t];
+    }
+    auto key_at = [&](int t) { return key_of(fits ? held[t] : __ldg(score + t)); };
+
+    // The threshold: keys above it are kept, and `need` of those equal to it.
+    uint32_t threshold = 0xffffffffu;       // above every key
+    int need = p.budget - p.first - p.recent;
+    if (need > 0) {
+        uint32_t prefix = 0;
+        int shift = 32;
+#pragma unroll 1
+        for (int pass = 0; pass < 3; ++pass) {
+            const int bits = pass < 2 ? 11 : 10, above = shift;
+            shift -= bits;
+            for (int i = tid; i < kBins; i += kThreads) hist[i] = 0;
+            __syncthreads();
+            for (int t = lo + tid; t < hi; t += kThreads) {
+                const uint32_t key = key_at(t);
+                if (pass == 0 || key >> above == prefix) atomicAdd(&hist[key >> shift & ((1u << bits) - 1)], 1);
+            }
+            __syncthreads();
+            // A thread's bins, from the highest of all on.
+            constexpr int kPer = kBins / kThreads;
+            int mine = 0, total;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) mine += hist[kBins - 1 - (tid * kPer + i)];
+            int before = scan_threads<kThreads>(mine, sm, &total);
+            if (before < need && before + mine >= need) {
+                for (int i = 0; i < kPer; ++i) {
+                    const int at = kBins - 1 - (tid * kPer + i), c = hist[at];
+                    if (before < need && before + c >= need) bin = at, left = need - before;
+                    before += c;
+                }
+            }
+            __syncthreads();
+            prefix = pass == 0 ? static_cast<uint32_t>(bin) : prefix << bits | static_cast<uint32_t>(bin);
+            need = left;
+        }
+        threshold = prefix;
+    } else {
+        __syncthreads();
+    }
+
+    // Each warp's part of the positions, in order.
+    constexpr int kWarps = kThreads / 32;
+    const int per = ((n + kWarps - 1) / kWarps + 31) / 32 * 32;
+    const int from = min(warp * per, n), to = min(from + per, n);
+    auto look = [&](int t, uint32_t *over, uint32_t *even) {
+        bool o = false, e = false;
+        if (t < to) {
+            o = t < lo || t >= hi;
+            if (!o) {
+                const uint32_t key = key_at(t);
+                o = key > threshold, e = key == threshold;
+            }
+        }
+        *over = __ballot_sync(0xffffffffu, o);
+        *even = __ballot_sync(0xffffffffu, e);
+    };
+    int overs = 0, evens = 0;
+    for (int t = from; t < to; t += 32) {
+        uint32_t over, even;
+        look(t + lane, &over, &even);
+        overs += __popc(over), evens += __popc(even);
+    }
+    // (Both counts in one scan: a lane of each warp has them, the others 0.)
+    int total, overs0 = scan_threads<kThreads>(lane == 0 ? overs : 0, sm, &total);
+    int evens0 = scan_threads<kThreads>(lane == 0 ? evens : 0, sm, &total);
+    overs0 = __shfl_sync(0xffffffffu, overs0, 0), evens0 = __shfl_sync(0xffffffffu, evens0, 0);
+    int at = overs0 + min(evens0, need);
+    const uint32_t below = (1u << lane) - 1;
+    for (int t = from; t < to; t += 32) {
+        uint32_t over, even;
+        look(t + lane, &over, &even);
+        const bool yes = (over >> lane & 1) || ((even >> lane & 1) && evens0 + __popc(even & below) < need);
+        const uint32_t all = __ballot_sync(0xffffffffu, yes);
+        const int j = at + __popc(all & below);
+        if (yes && XS_BOUNDS(j >= 0 && j < p.budget, p.err_flag)) kept[j] = t + lane;
+        at += __popc(all);
+        evens0 += __popc(even);
+    }
+}
+
+// Goes through positions [first, budget) in tiles: position j's piece, as get(j,
+// kept[j]) has it, is put by put(j, piece) once the whole tile has been read.
+// kPer positions of a tile are a thread's own, kStep apart.
+template <typename V, int kPer, typename G, typename P>
+__device__ __forceinline__ void move_tiles(const int32_t *kept, int first, int budget, int own, int step, G &&get,
+                                           P &&put) {
+    V cur[kPer], next[kPer];
+    int cur_from[kPer], next_from[kPer];
+    auto load = [&](int base, V (&v)[kPer], int (&src)[kPer]) {
+#pragma unroll
+        for (int u = 0; u < kPer; ++u) {
+            const int j = base + u * step + own;
+            src[u] = j < budget ? __ldcg(kept + j) : j;
+        }
+#pragma unroll
+        for (int u = 0; u < kPer; ++u) {
+            const int j = base + u * step + own;
+            if (src[u] != j) v[u] = get(src[u]);
+        }
+    };
+    const int tile = kPer * step;
+    load(first, cur, cur_from);
+    for (int base = first; base < budget; base += tile) {
+        if (base + tile < budget) load(base + tile, next, next_from);
+        __syncthreads();
+#pragma unroll
+        for (int u = 0; u < kPer; ++u) {
+            const int j = base + u * step + own;
+            if (cur_from[u] != j) put(j, cur[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < kPer; ++u) cur[u] = next[u], cur_from[u] = next_from[u];
+    }
+}
+
+// CTAs (layer, entry, KV head) x (K's slices, V's slices, the scores).
+__global__ void __launch_bounds__(kMoveThreads)
+    evict_move_kernel(const __grid_constant__ EvictParams p, const int slices) {
+    after_previous();
+    const int32_t *kept = p.kept + static_cast<int64_t>(blockIdx.x) * p.budget;
+    if (__ldcg(kept) < 0) return;       // not cut
+    const int hk = blockIdx.x % p.Hkv, entry = blockIdx.x / p.Hkv % p.n;
+    const int layer = blockIdx.x / p.Hkv / p.n;
+    const int b = XS_BOUNDS(entry < p.n && layer < p.layers, p.err_flag) ? p.seq_ids[entry] : 0;
+    const int plane = blockIdx.y / slices, slice = blockIdx.y % slices, tid = threadIdx.x;
+    const int tokens = p.max_blocks * kPage;
+    if (plane == 2) {
+        float *score = p.scores + ((static_cast<int64_t>(layer) * p.B + b) * p.Hkv + hk) * tokens;
+        move_tiles<float, kMoveUnroll>(
+            kept, p.first, p.budget, tid, kMoveThreads,
+            [&](int t) { return XS_BOUNDS(t >= 0 && t < tokens, p.err_flag) ? score[t] : 0.0f; },
+            [&](int j, float v) { if (XS_BOUNDS(j < tokens, p.err_flag)) score[j] = v; });
+        return;
+    }
+    char *pool = (plane ? p.v_pools : p.k_pools) + layer * p.layer_bytes;
+    const int32_t *row = p.tables + static_cast<int64_t>(b) * p.max_blocks;
+    // A slice of a row: `wide` pieces of 16 bytes, one each for neighbouring threads.
+    const int wide = p.row_bytes / 16 / slices, piece = tid % wide;
+    const int64_t in_row = static_cast<int64_t>(slice * wide + piece) * 16;
+    auto at = [&](int t) {
+        int64_t id = 0;
+        if (XS_BOUNDS(t >= 0 && t < tokens, p.err_flag)) id = __ldg(row + t / kPage);
+        if (!XS_BOUNDS(id >= 0 && id < p.num_blocks, p.err_flag)) id = 0;
+        return reinterpret_cast<uint4 *>(pool + ((id * p.Hkv + hk) * kPage + t % kPage) * p.row_bytes + in_row);
+    };
+    move_tiles<uint4, kMoveUnroll>(
+        kept, p.first, p.budget, tid / wide, kMoveThreads / wide, [&](int t) { return *at(t); },
+        [&](int j, const uint4 &v) { *at(j) = v; });
+}
+
+}  // namespace
+XS_DEFINE_BOUNDS_COUNTER(bounds_failures_evict)
+
+}  // namespace xs
+
+extern "C" int xs_kv_evict(const int32_t *seq_ids, int n, void *k_pools, void *v_pools, int layers,
+                           int64_t layer_stride_bytes, float *scores, const int32_t *block_tables,
+                           int max_blocks_per_seq, const int32_t *context_lens, int B,
+                           const int32_t *extra_refs, int first, int recent, int budget, int limit, int Hkv,
+                           int D, int block_size, int64_t num_blocks, int dtype, int32_t *kept,
+                           int32_t *new_lens, int *err_flag, cudaStream_t stream) {
+    if (!seq_ids || !k_pools || !v_pools || !scores || !block_tables || !context_lens || !kept || !new_lens)
+        return XS_ENULL;
+    const int size = xs::elem_bytes(dtype);
+    if (!size) return XS_EDTYPE;
+    if (n < 0 || layers < 0 || B < 0 || Hkv <= 0 || D <= 0 || block_size <= 0 || max_blocks_per_seq < 0 ||
+        num_blocks < 0 || first < 0 || recent < 0 || budget <= 0 || limit < budget ||
+        static_cast<int64_t>(first) + recent > budget)
+        return XS_ESHAPE;
+    if ((D != 64 && D != 128) || block_size != xs::kPage || max_blocks_per_seq > (1 << 26) ||
+        layer_stride_bytes % 16 != 0)
+        return XS_EUNSUPPORTED;
+    const int row_bytes = D * size;
+    const int64_t block_bytes = static_cast<int64_t>(Hkv) * xs::kPage * row_bytes;
+    if (num_blocks > INT64_MAX / block_bytes || (layers > 1 && layer_stride_bytes < num_blocks * block_bytes))
+        return XS_ESHAPE;
+    if (!xs::aligned16(k_pools) || !xs::aligned16(v_pools)) return XS_EALIGN;
+    const int64_t heads = static_cast<int64_t>(layers) * n;
+    if (heads > INT_MAX / Hkv) return XS_EUNSUPPORTED;
+    if (heads == 0) return XS_OK;
+    xs::EvictParams p = {};
+    p.seq_ids = seq_ids, p.n = n;
+    p.k_pools = static_cast<char *>(k_pools), p.v_pools = static_cast<char *>(v_pools);
+    p.layer_bytes = layer_stride_bytes, p.scores = scores;
+    p.tables = block_tables, p.lens = context_lens, p.extra = extra_refs;
+    p.max_blocks = max_blocks_per_seq, p.B = B, p.Hkv = Hkv, p.layers = layers, p.row_bytes = row_bytes;
+    p.num_blocks = num_blocks;
+    p.first = first, p.recent = recent, p.budget = budget, p.limit = limit;
+    p.kept = kept, p.new_lens = new_lens, p.err_flag = err_flag;
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return XS_EDEVICE;
+    const int ctas = static_cast<int>(heads) * Hkv;
+    const int64_t tokens = static_cast<int64_t>(max_blocks_per_seq) * xs::kPage;
+    const size_t smem = tokens <= xs::kScoresHeld ? tokens * sizeof(uint32_t) : 0;
+    int rc;
+    if (tokens <= 4096) {
+        rc = xs::launch_after(xs::evict_select_kernel<256>, dim3(ctas), 256, smem, stream, 1, p);
+    } else {
+        static std::atomic<bool> may[64];      // each device has been told of its shared memory
+        if (dev >= 64 || !may[dev].load(std::memory_order_acquire)) {
+            if (cudaFuncSetAttribute(xs::evict_select_kernel<1024>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     xs::kScoresHeld * sizeof(uint32_t)) != cudaSuccess) {
+                cudaGetLastError();
+                return XS_EDEVICE;
+            }
+            if (dev < 64) may[dev].store(true, std::memory_order_release);
+        }
+        rc = xs::launch_after(xs::evict_select_kernel<1024>, dim3(ctas), 1024, smem, stream, 1, p);
+    }
+    if (rc != XS_OK) return rc;
+    // Slices of no less than 32 bytes, while they leave SMs without work.
+    int slices = 1;
+    while (row_bytes / slices > 32 && static_cast<int64_t>(ctas) * 2 * slices < 4 * sms) slices *= 2;
+    return xs::launch_after(xs::evict_move_kernel, dim3(ctas, 2 * slices + 1), xs::kMoveThreads, 0, stream, 1, p,
+                            slices);
+}

@@ -87,7 +87,8 @@ __device__ __forceinline__ bool bounds_ok(bool ok, int *err_flag) {
     int fn(int) { return 0; }
 #endif
 // Per translation unit (kv_append.cu, paged_decode.cu, paged_prefill_tc.cu,
-// qk_norm_rope.cu, kv4_cache.cu, kv4_decode.cu, block_share.cu, bounded_decode.cu).
+// qk_norm_rope.cu, kv4_cache.cu, kv4_decode.cu, block_share.cu, bounded_decode.cu,
+// kv_evict.cu).
 int bounds_failures_append(int reset);
 int bounds_failures_decode(int reset);
 int bounds_failures_prefill_tc(int reset);
@@ -96,6 +97,7 @@ int bounds_failures_kv4_cache(int reset);
 int bounds_failures_kv4_decode(int reset);
 int bounds_failures_share(int reset);
 int bounds_failures_bounded(int reset);
+int bounds_failures_evict(int reset);
 
 // ------------------------------------------------------------------ mbarrier + bulk copy
 

@@ -28,7 +28,7 @@ STATUS = {
 }
 NOALLOC_SCRATCH_BYTES = 64 << 20
 FLAG_BAD_BLOCK, FLAG_BAD_LEN, FLAG_BAD_SLOT, FLAG_TIMEOUT, FLAG_CONFIG = 1, 2, 4, 8, 16
-FLAG_POOL_EMPTY = 32
+FLAG_POOL_EMPTY, FLAG_SHARED = 32, 128
 
 # name -> (restype, argtypes)
 _P, _I, _L, _F, _S = (ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float,
@@ -104,6 +104,9 @@ SIGNATURES = {
     "xs_paged_decode_weights_workspace_bytes": (_S, [_I, _I, _I, _I, _I]),
     "xs_paged_decode_weights": (_I, [_P, _P, _P, _P, _L, _P, _P, _P, _I, _P, _P, _I, _I, _I, _I,
                                      _I, _L, _F, _P, _S, _I, _P, _P]),
+    "xs_kv_evict": (_I, [_P, _I, _P, _P, _I, _L, _P, _P, _I, _P, _I, _P, _I, _I, _I, _I, _I, _I,
+                         _I, _L, _I, _P, _P, _P, _P]),
+    "xs_block_truncate": (_I, [_P, _P, _I, _P, _I, _P, _I, _I, _P, _P, _L, _P, _L, _P, _P]),
     "xs_version": (_I, []),
     "xs_debug_bounds_failures": (_I, [_I]),
     "xs_debug_wait_injection": (_I, [_L, _I]),
@@ -685,6 +688,30 @@ def xs_paged_decode_weights(out, scores, q, k_cache, v_cache, block_tables, cont
         _entry("xs_paged_decode_weights"), out, scores, q, k_cache, v_cache, block_tables,
         context_lens, scale, w.buf, w.Hq, w.Hkv, w.D, scored_lens, sinks, err_flag,
         _handle(stream)))
+
+
+def xs_kv_evict(seq_ids, k_pools, v_pools, scores, block_tables, context_lens, kept, new_lens,
+                first, recent, limit, extra_refs=None, err_flag=None, stream=None):
+    """Cut the sequences in slots seq_ids (int32 [n]) that are longer than
+    ``limit`` to kept.shape[-1] tokens: the ``first`` first ones, the ``recent``
+    last ones and those of largest score between, by KV head and layer.  K and V
+    rows ([layers, num_blocks, Hkv, 16, D]) and scores ([layers, B, Hkv,
+    max_blocks * 16]) move to the front, in order.  Writes kept (int32 [layers,
+    n, Hkv, budget]) and new_lens (int32 [n]; -1: not cut), which
+    xs_block_truncate takes: it has to follow."""
+    _done("xs_kv_evict", (_bound or _bind()).xs_kv_evict(
+        _entry("xs_kv_evict"), seq_ids, k_pools, v_pools, scores, block_tables, context_lens, kept,
+        new_lens, first, recent, limit, extra_refs, err_flag, _handle(stream)))
+
+
+def xs_block_truncate(seq_ids, new_lens, block_tables, context_lens, free_stack, free_top,
+                      extra_refs, block_size=BLOCK_SIZE, err_flag=None, stream=None):
+    """Shorten the sequences in slots seq_ids to new_lens (int32 [n]; negative,
+    or not shorter: left alone) and give the pages behind back, as
+    xs_block_release does."""
+    _done("xs_block_truncate", (_bound or _bind()).xs_block_truncate(
+        _entry("xs_block_truncate"), seq_ids, new_lens, block_tables, context_lens, free_stack,
+        free_top, extra_refs, block_size, err_flag, _handle(stream)))
 
 
 def xs_version() -> int:

@@ -995,6 +995,20 @@ int xs_paged_decode_first(void *out, const void *q, int64_t q_stride, const void
                           int *err_flag, cudaStream_t stream);
 
 /*
+ * xs_paged_prefill_first - the same mask for a chunk of a prompt: xs_paged_
+ * prefill_tc in which the query at position p sees the keys t <= p with t < first
+ * or t > p - window (window 0: every t <= p).  block_ids entries of pages that no
+ * query of the chunk sees are never read.  bf16 only; scale > 0.
+ * Rows that no query of the chunk sees have no influence.  An infinity or a NaN
+ * in a V row that some of 256 Hkv / Hq neighbouring queries see and others do not
+ * may reach the outputs of all of them (as in xs_paged_prefill_tc).
+ */
+int xs_paged_prefill_first(void *out, const void *q, const void *k_cache, const void *v_cache,
+                           const int32_t *block_ids, int n_ids, int T, int start_pos, int first,
+                           int window, int Hq, int Hkv, int D, int block_size, int64_t num_blocks,
+                           float scale, int dtype, int *err_flag, cudaStream_t stream);
+
+/*
  * xs_paged_decode_weights - decode attention over all of each sequence's cache,
  * which also adds up the weight that each cached token gets: for t < n =
  * context_lens[b] and every KV head hk,

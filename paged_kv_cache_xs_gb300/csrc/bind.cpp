@@ -565,6 +565,37 @@ PyObject *decode_bounded(Args a, bool weights) {
     });
 }
 
+PyObject *prefill_first(Args a) {
+    void *entry = a.entry();
+    const at::Tensor &out = a.tensor("out"), &q = a.tensor("q");
+    const at::Tensor &kc = a.tensor("k_cache"), &vc = a.tensor("v_cache"), &ids = a.tensor("block_ids");
+    const int start = a.integer("start_pos");
+    const float scale = static_cast<float>(a.number());
+    const int first = a.integer("first"), window = a.integer("window");
+    const at::Tensor *err = a.maybe("err_flag");
+    PyObject *stream = a.next();
+    dims(q, 3, "q"), dims(kc, 4, "a pool");
+    const int64_t T = q.size(0), Hq = q.size(1), D = q.size(2), Hkv = kc.size(1), n = ids.numel();
+    want(out, q.scalar_type(), {T, Hq, D}, "out");
+    bool kv4 = false;
+    const int64_t blocks = pools(kc, vc, q.scalar_type(), Hkv, D, &kv4);
+    if (kv4) refuse("a 4-bit pool is not supported here");
+    want(ids, at::kInt, {n}, "block_ids");
+    want(err, at::kInt, {1}, "err_flag");
+    const int code = dtype_code(q), t = as_int(T, "q"), hq = as_int(Hq, "q"), hkv = as_int(Hkv, "k_cache"),
+              d = as_int(D, "q"), count = as_int(n, "block_ids");
+    const cudaStream_t s = stream_for(stream, {&q, &out, &kc, &vc, &ids, err});
+    void *op = whole(out, "out");
+    const void *qp = whole(q, "q"), *kcp = whole(kc, "k_cache"), *vcp = whole(vc, "v_cache");
+    const int32_t *ip = static_cast<int32_t *>(whole(ids, "block_ids"));
+    int *flag = static_cast<int *>(whole(err, "err_flag"));
+    if (T == 0) return PyLong_FromLong(XS_OK);
+    return status([&] {
+        return reinterpret_cast<decltype(&xs_paged_prefill_first)>(entry)(
+            op, qp, kcp, vcp, ip, count, t, start, first, window, hq, hkv, d, kPage, blocks, scale, code, flag, s);
+    });
+}
+
 PyObject *kv_evict(Args a) {
     void *entry = a.entry();
     const at::Tensor &ids = a.tensor("seq_ids");
@@ -640,6 +671,7 @@ XS_BIND(xs_block_compact, block_compact(a))
 XS_BIND(xs_block_copy, block_copy(a))
 XS_BIND(xs_paged_decode_first, decode_bounded(a, false))
 XS_BIND(xs_paged_decode_weights, decode_bounded(a, true))
+XS_BIND(xs_paged_prefill_first, prefill_first(a))
 
 #define XS_METHOD(name) \
     {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(py_##name)), METH_FASTCALL, nullptr}
@@ -658,6 +690,7 @@ PyMethodDef methods[] = {XS_METHOD(xs_qk_norm_rope),
                          XS_METHOD(xs_block_copy),
                          XS_METHOD(xs_paged_decode_first),
                          XS_METHOD(xs_paged_decode_weights),
+                         XS_METHOD(xs_paged_prefill_first),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "xs_bind", nullptr, -1, methods,
                       nullptr,               nullptr,   nullptr, nullptr};

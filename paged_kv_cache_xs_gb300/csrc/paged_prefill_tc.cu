@@ -49,6 +49,12 @@
 //    tiles never touch O.  Unwritten slots of the last page (any bits at all)
 //    are zeroed in the staged V tile, since 0 * NaN = NaN.  At the end:
 //    O / l, bf16, out.
+//  * With a window and first tokens (kFirst; xs_paged_prefill_first) query i
+//    sees the keys t <= i with t > i - window or t < first.  A CTA goes through
+//    the key tiles of the first tokens and those from its first query's window
+//    on, as one list; pages that none of its queries sees arrive as zeros, and
+//    rows of V that none sees are zeroed where they were staged.  4,096 tokens
+//    behind 28,672 under a window of 4,096 (32q/8kv x 128): 328 us.
 //  * TMEM: all 512 columns (per Q tile S/P 128, O 128).  Every wait is
 //    bounded; the MMA thread waits for its last MMA before the CTA frees TMEM.
 #include <cuda.h>
@@ -126,6 +132,7 @@ struct PParams {
     // end before position start are read before waiting for the previous
     // launch on the stream; the tiles from start on and every write after.
     int early;
+    int first, window;             // kFirst: what a query sees (window 0: every key)
 };
 
 // Shared-memory matrix descriptor: start, leading and stride byte offsets,
@@ -210,7 +217,7 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *tm,
         : "memory");
 }
 
-template <int D, int G>
+template <int D, int G, bool kFirst>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_tc_kernel(const __grid_constant__ CUtensorMap tmq,
                       const __grid_constant__ CUtensorMap tmk,
@@ -243,14 +250,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tok0 = (n_tok_tiles - 1 - static_cast<int>(blockIdx.x) / p.Hkv) * kQTiles * kTq;
     const int ntok = min(kQTiles * kTq, p.T - tok0);  // tokens of this CTA
     const int kmax = p.start + tok0 + ntok;            // keys [0, kmax) are read
-    const int ntiles = (kmax + kKeys - 1) / kKeys;
+    // kFirst: keys [low0, kmax) are in some query's window, and those below
+    // `first` are seen by all that come after them; tile kt of the CTA's list is
+    // the pool's tile kt (kt < nfirst) or kt + skipped.
+    const int low0 = kFirst && p.window > 0 ? max(0, p.start + tok0 - p.window + 1) : 0;
+    const int nfirst = kFirst ? min((min(p.first, low0) + kKeys - 1) / kKeys, low0 / kKeys) : 0;
+    const int skipped = kFirst ? low0 / kKeys - nfirst : 0;
+    auto key_tile = [&](int kt) { return kFirst && kt >= nfirst ? kt + skipped : kt; };
+    // Whether no query of the CTA sees key t.
+    auto hidden = [&](int t) { return t >= kmax || (kFirst && t >= p.first && t < low0); };
+    const int ntiles = (kmax + kKeys - 1) / kKeys - skipped;
     const int npages = (kmax + kBlock - 1) / kBlock;
     // Q tile qi holds tokens [qi * kTq, qi * kTq + tile_tokens(qi)) of the CTA
     // and attends to key tiles [0, tile_ntiles(qi)).
     auto tile_tokens = [&](int qi) { return max(0, min(kTq, ntok - qi * kTq)); };
     auto tile_ntiles = [&](int qi) {
         const int n = tile_tokens(qi);
-        return n > 0 ? (p.start + tok0 + qi * kTq + n + kKeys - 1) / kKeys : 0;
+        return n > 0 ? (p.start + tok0 + qi * kTq + n + kKeys - 1) / kKeys - skipped : 0;
     };
 
     if (tid == 0) {
@@ -303,8 +319,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             auto page_row = [&](int kt) {
                 int row = p.oob_row;
-                const int pg = kt * kPagesPerTile + lane;
-                if (lane < kPagesPerTile && pg < npages && XS_BOUNDS(pg < p.n_ids, p.err_flag)) {
+                const int pg = key_tile(kt) * kPagesPerTile + lane;
+                if (lane < kPagesPerTile && pg < npages &&
+                    !(kFirst && pg * kBlock >= p.first && pg * kBlock + kBlock <= low0) &&
+                    XS_BOUNDS(pg < p.n_ids, p.err_flag)) {
                     const int32_t blk = p.block_ids[pg];
                     if (blk < 0 || blk >= p.num_blocks)
                         raise_flag(p.err_flag, XS_FLAG_BAD_BLOCK);  // read as zeros
@@ -457,6 +475,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lane_off = static_cast<uint32_t>(32 * quad) << 16;
         const uint32_t cols = tmem + lane_off + qi * kGroupCols;
         float m_ref = 0.f, l = 0.f;
+        bool seen = false;                 // kFirst: this row has met a key that it sees
+        const int low = kFirst && p.window > 0 ? qpos - p.window + 1 : 0;
         bool ok = true;
         for (int kt = 0; kt < my_ntiles; ++kt) {
             ok = __all_sync(0xffffffffu, mbar_wait_bounded(s_full(qi), kt & 1, kWaitLimitNs)) &&
@@ -473,14 +493,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             // The maximum is taken on raw scores (qscale > 0), the exponent
             // is one fma: 2^(s * qscale - m).  Maximum and sums run as 8
             // independent chains.
-            const int k0 = kt * kKeys;
-            const bool need_mask = k0 + kKeys - 1 > p.start + tok0 + qi * kTq;
+            const int k0 = key_tile(kt) * kKeys;
+            const int q0 = p.start + tok0 + qi * kTq;      // the Q tile's first position
+            const bool need_mask = k0 + kKeys - 1 > q0 ||
+                                   (kFirst && p.window > 0 && k0 < q0 + kTq - p.window && k0 + kKeys > p.first);
             float v[kKeys];
 #pragma unroll
             for (int j = 0; j < kKeys; ++j) v[j] = __uint_as_float(sr[j >> 5][j & 31]);
             if (need_mask) {
 #pragma unroll
-                for (int j = 0; j < kKeys; ++j) v[j] = k0 + j <= qpos ? v[j] : -INFINITY;
+                for (int j = 0; j < kKeys; ++j) {
+                    const int t = k0 + j;
+                    v[j] = t <= qpos && (!kFirst || t >= low || t < p.first) ? v[j] : -INFINITY;
+                }
             }
             // Row maximum: 8 independent chains of three-input maxima.
             float mx8[8];
@@ -495,9 +520,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                                p.qscale;
             bool rescale = false;
             float m_new = m_ref;
-            if (kt == 0) {
+            // (A row that has seen no key yet has O = 0, which needs no rescaling.)
+            if (kFirst ? !seen : kt == 0) {
                 m_ref = tmax == -INFINITY ? 0.f : tmax;
                 m_new = m_ref;
+                seen = tmax != -INFINITY;
             } else if (tmax > m_ref + kHeadroom) {
                 rescale = true;
                 m_new = tmax;
@@ -537,9 +564,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_st32(cols + kColP, *reinterpret_cast<uint32_t(*)[32]>(&pr[0]));
             tmem_st32(cols + kColP + 32, *reinterpret_cast<uint32_t(*)[32]>(&pr[32]));
             tmem_wait_st();
-            if (kt == ntiles - 1 && npages * kBlock > kmax) {
-                // Unwritten slots of the CTA's last page: zero their V rows
-                // (128-byte lines, whole, so the swizzle inside a line does not
+            const bool ends = kt == ntiles - 1 && npages * kBlock > kmax;
+            if (ends || (kFirst && low0 > p.first && ((kt == nfirst && k0 < low0) || kt == nfirst - 1))) {
+                // Unwritten slots of the CTA's last page, and keys between the first
+                // tokens and the window that no query of the CTA sees: zero their V
+                // rows (128-byte lines, whole, so the swizzle inside a line does not
                 // matter), once the V tile has landed.  (Both Q tiles may end
                 // on this tile; each writes the same zeros before its P V.)
                 ok = __all_sync(0xffffffffu,
@@ -547,12 +576,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                   kWaitLimitNs));
                 if (!ok) break;
                 unsigned char *vt = sm + C::kVOff + (kt % kStages) * C::kTile;
-                const int first = kmax - k0, nrow = npages * kBlock - kmax;
-                for (int i = r; i < nrow * C::kHalves * 8; i += kRows) {
-                    const int line = i >> 3, chunk = i & 7;
-                    const int key = first + line % nrow, h = line / nrow;
-                    *reinterpret_cast<uint4 *>(vt + h * C::kKVHalf + key * 128 + chunk * 16) =
-                        make_uint4(0u, 0u, 0u, 0u);
+                if (kFirst) {
+                    // (One key of the tile for each of the Q tile's 128 threads.)
+                    if (hidden(k0 + r))
+                        for (int i = 0; i < C::kHalves * 8; ++i)
+                            *reinterpret_cast<uint4 *>(vt + (i >> 3) * C::kKVHalf + r * 128 + (i & 7) * 16) =
+                                make_uint4(0u, 0u, 0u, 0u);
+                } else {
+                    const int first = kmax - k0, nrow = npages * kBlock - kmax;
+                    for (int i = r; i < nrow * C::kHalves * 8; i += kRows) {
+                        const int line = i >> 3, chunk = i & 7;
+                        const int key = first + line % nrow, h = line / nrow;
+                        *reinterpret_cast<uint4 *>(vt + h * C::kKVHalf + key * 128 + chunk * 16) =
+                            make_uint4(0u, 0u, 0u, 0u);
+                    }
                 }
                 fence_proxy_async_shared();
             }
@@ -659,24 +696,122 @@ int encode(CUtensorMap *tm, const void *base, const cuuint64_t (&dims)[3],
 
 using KernelFn = void (*)(const CUtensorMap, const CUtensorMap, const CUtensorMap, const PParams);
 
-template <int D, int G>
-KernelFn kernel_for() {
-    return prefill_tc_kernel<D, G>;
-}
-
+template <bool kFirst>
 KernelFn pick(int D, int G) {
     if (D == 128) {
-        if (G == 1) return kernel_for<128, 1>();
-        if (G == 2) return kernel_for<128, 2>();
-        if (G == 4) return kernel_for<128, 4>();
-        if (G == 8) return kernel_for<128, 8>();
+        if (G == 1) return prefill_tc_kernel<128, 1, kFirst>;
+        if (G == 2) return prefill_tc_kernel<128, 2, kFirst>;
+        if (G == 4) return prefill_tc_kernel<128, 4, kFirst>;
+        if (G == 8) return prefill_tc_kernel<128, 8, kFirst>;
     } else if (D == 64) {
-        if (G == 1) return kernel_for<64, 1>();
-        if (G == 2) return kernel_for<64, 2>();
-        if (G == 4) return kernel_for<64, 4>();
-        if (G == 8) return kernel_for<64, 8>();
+        if (G == 1) return prefill_tc_kernel<64, 1, kFirst>;
+        if (G == 2) return prefill_tc_kernel<64, 2, kFirst>;
+        if (G == 4) return prefill_tc_kernel<64, 4, kFirst>;
+        if (G == 8) return prefill_tc_kernel<64, 8, kFirst>;
     }
     return nullptr;
+}
+
+// The call with its mask: kFirst, or every key up to the query's position.
+template <bool kFirst>
+int prefill(void *out, const void *q, const void *k_cache, const void *v_cache,
+            const int32_t *block_ids, int n_ids, int T, int start_pos, int first, int window, int Hq,
+            int Hkv, int D, int block_size, int64_t num_blocks, float scale, int flags, int dtype,
+            int *err_flag, cudaStream_t stream) {
+    if (flags & ~XS_PREFILL_OVERLAP) return XS_EUNSUPPORTED;
+    if (!out || !q || !k_cache || !v_cache || !block_ids) return XS_ENULL;
+    if (dtype != XS_BF16) return dtype == XS_F32 ? XS_EUNSUPPORTED : XS_EDTYPE;
+    if (T < 0 || start_pos < 0 || n_ids < 0 || Hq <= 0 || Hkv <= 0 || num_blocks < 0 ||
+        Hq % Hkv != 0 || first < 0 || window < 0)
+        return XS_ESHAPE;
+    const int G = Hq / Hkv;
+    if (block_size != kBlock || (D != 64 && D != 128) ||
+        (G != 1 && G != 2 && G != 4 && G != 8))
+        return XS_EUNSUPPORTED;
+    if (static_cast<int64_t>(start_pos) + T > static_cast<int64_t>(n_ids) * block_size)
+        return XS_ESHAPE;
+    if (kFirst && !(scale > 0.f)) return XS_EUNSUPPORTED;    // (0 would make NaN of a masked logit)
+    const int64_t rows = num_blocks * Hkv * kBlock;
+    if (rows + kBlock > 0x7fffffff) return XS_EUNSUPPORTED;  // 32-bit TMA row coordinate
+    if (!aligned16(out) || !aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache))
+        return XS_EALIGN;
+    if (T == 0 || num_blocks == 0) return XS_OK;
+    KernelFn fn = pick<kFirst>(D, G);
+    if (!fn) return XS_EUNSUPPORTED;
+    // q [T, Hq, D] as (D, Hq, T), box (64, G, 128 / G): one D half of a CTA's rows.
+    // Pools [num_blocks, Hkv, 16, D] as (64, rows, D / 64) with strides (2 D, 128)
+    // bytes, box (64, 16, 1): one D half of one page.
+    CUtensorMap tmq, tmk, tmv;
+    const cuuint64_t qdims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(Hq),
+                                 static_cast<cuuint64_t>(T)};
+    const cuuint64_t qstr[2] = {static_cast<cuuint64_t>(D) * 2,
+                                static_cast<cuuint64_t>(Hq) * D * 2};
+    const cuuint32_t qbox[3] = {64, static_cast<cuuint32_t>(G),
+                                static_cast<cuuint32_t>(kRows / G)};
+    const cuuint64_t pdims[3] = {64, static_cast<cuuint64_t>(rows),
+                                 static_cast<cuuint64_t>(D / 64)};
+    const cuuint64_t pstr[2] = {static_cast<cuuint64_t>(D) * 2, 128};
+    const cuuint32_t pbox[3] = {64, kBlock, 1};
+    int st = encode(&tmq, q, qdims, qstr, qbox);
+    if (st == XS_OK) st = encode(&tmk, k_cache, pdims, pstr, pbox);
+    if (st == XS_OK) st = encode(&tmv, v_cache, pdims, pstr, pbox);
+    if (st != XS_OK) return st;
+    const int smem = D == 128 ? TCfg<128>::kSmemBytes : TCfg<64>::kSmemBytes;
+    static std::mutex mu;
+    static KernelFn raised[8] = {};
+    {
+        std::lock_guard<std::mutex> lock(mu);
+        bool done = false;
+        for (KernelFn f : raised) done |= f == fn;
+        if (!done) {
+            if (cudaFuncSetAttribute(reinterpret_cast<const void *>(fn),
+                                     cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
+                cudaSuccess) {
+                cudaGetLastError();
+                return XS_ELAUNCH;
+            }
+            for (KernelFn &f : raised)
+                if (!f) {
+                    f = fn;
+                    break;
+                }
+        }
+    }
+    PParams p;
+    p.out = static_cast<__nv_bfloat16 *>(out);
+    p.block_ids = block_ids;
+    p.n_ids = n_ids;
+    p.T = T;
+    p.start = start_pos;
+    p.Hq = Hq;
+    p.Hkv = Hkv;
+    p.num_blocks = num_blocks;
+    p.oob_row = static_cast<int>(rows);
+    p.qscale = scale * kLog2e;
+    p.err_flag = err_flag;
+    p.first = first;
+    p.window = window;
+    p.early = (flags & XS_PREFILL_OVERLAP) ? 1 : 0;
+    const int tq = kQTiles * kRows / G;  // query tokens per CTA
+    const int64_t ctas = static_cast<int64_t>((T + tq - 1) / tq) * Hkv;
+    if (ctas > 0x7fffffff) return XS_EUNSUPPORTED;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    if (p.early) {
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+    }
+    if (cudaLaunchKernelEx(&cfg, fn, tmq, tmk, tmv, p) != cudaSuccess) {
+        cudaGetLastError();
+        return XS_ELAUNCH;
+    }
+    return launch_status();
 }
 
 }  // namespace pftc
@@ -701,95 +836,17 @@ extern "C" int xs_paged_prefill_tc_ex(void *out, const void *q, const void *k_ca
                                       int T, int start_pos, int Hq, int Hkv, int D,
                                       int block_size, int64_t num_blocks, float scale, int flags,
                                       int dtype, int *err_flag, cudaStream_t stream) {
-    if (flags & ~XS_PREFILL_OVERLAP) return XS_EUNSUPPORTED;
-    if (!out || !q || !k_cache || !v_cache || !block_ids) return XS_ENULL;
-    if (dtype != XS_BF16) return dtype == XS_F32 ? XS_EUNSUPPORTED : XS_EDTYPE;
-    if (T < 0 || start_pos < 0 || n_ids < 0 || Hq <= 0 || Hkv <= 0 || num_blocks < 0 ||
-        Hq % Hkv != 0)
-        return XS_ESHAPE;
-    const int G = Hq / Hkv;
-    if (block_size != pftc::kBlock || (D != 64 && D != 128) ||
-        (G != 1 && G != 2 && G != 4 && G != 8))
-        return XS_EUNSUPPORTED;
-    if (static_cast<int64_t>(start_pos) + T > static_cast<int64_t>(n_ids) * block_size)
-        return XS_ESHAPE;
-    const int64_t rows = num_blocks * Hkv * pftc::kBlock;
-    if (rows + pftc::kBlock > 0x7fffffff) return XS_EUNSUPPORTED;  // 32-bit TMA row coordinate
-    if (!aligned16(out) || !aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache))
-        return XS_EALIGN;
-    if (T == 0 || num_blocks == 0) return XS_OK;
-    pftc::KernelFn fn = pftc::pick(D, G);
-    if (!fn) return XS_EUNSUPPORTED;
-    // q [T, Hq, D] as (D, Hq, T), box (64, G, 128 / G): one D half of a CTA's rows.
-    // Pools [num_blocks, Hkv, 16, D] as (64, rows, D / 64) with strides (2 D, 128)
-    // bytes, box (64, 16, 1): one D half of one page.
-    CUtensorMap tmq, tmk, tmv;
-    const cuuint64_t qdims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(Hq),
-                                 static_cast<cuuint64_t>(T)};
-    const cuuint64_t qstr[2] = {static_cast<cuuint64_t>(D) * 2,
-                                static_cast<cuuint64_t>(Hq) * D * 2};
-    const cuuint32_t qbox[3] = {64, static_cast<cuuint32_t>(G),
-                                static_cast<cuuint32_t>(pftc::kRows / G)};
-    const cuuint64_t pdims[3] = {64, static_cast<cuuint64_t>(rows),
-                                 static_cast<cuuint64_t>(D / 64)};
-    const cuuint64_t pstr[2] = {static_cast<cuuint64_t>(D) * 2, 128};
-    const cuuint32_t pbox[3] = {64, pftc::kBlock, 1};
-    int st = pftc::encode(&tmq, q, qdims, qstr, qbox);
-    if (st == XS_OK) st = pftc::encode(&tmk, k_cache, pdims, pstr, pbox);
-    if (st == XS_OK) st = pftc::encode(&tmv, v_cache, pdims, pstr, pbox);
-    if (st != XS_OK) return st;
-    const int smem = D == 128 ? pftc::TCfg<128>::kSmemBytes : pftc::TCfg<64>::kSmemBytes;
-    static std::mutex mu;
-    static pftc::KernelFn raised[8] = {};
-    {
-        std::lock_guard<std::mutex> lock(mu);
-        bool done = false;
-        for (pftc::KernelFn f : raised) done |= f == fn;
-        if (!done) {
-            if (cudaFuncSetAttribute(reinterpret_cast<const void *>(fn),
-                                     cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
-                cudaSuccess) {
-                cudaGetLastError();
-                return XS_ELAUNCH;
-            }
-            for (pftc::KernelFn &f : raised)
-                if (!f) {
-                    f = fn;
-                    break;
-                }
-        }
-    }
-    pftc::PParams p;
-    p.out = static_cast<__nv_bfloat16 *>(out);
-    p.block_ids = block_ids;
-    p.n_ids = n_ids;
-    p.T = T;
-    p.start = start_pos;
-    p.Hq = Hq;
-    p.Hkv = Hkv;
-    p.num_blocks = num_blocks;
-    p.oob_row = static_cast<int>(rows);
-    p.qscale = scale * pftc::kLog2e;
-    p.err_flag = err_flag;
-    p.early = (flags & XS_PREFILL_OVERLAP) ? 1 : 0;
-    const int tq = pftc::kQTiles * pftc::kRows / G;  // query tokens per CTA
-    const int64_t ctas = static_cast<int64_t>((T + tq - 1) / tq) * Hkv;
-    if (ctas > 0x7fffffff) return XS_EUNSUPPORTED;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(ctas));
-    cfg.blockDim = dim3(pftc::kThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    if (p.early) {
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-    }
-    if (cudaLaunchKernelEx(&cfg, fn, tmq, tmk, tmv, p) != cudaSuccess) {
-        cudaGetLastError();
-        return XS_ELAUNCH;
-    }
-    return launch_status();
+    return pftc::prefill<false>(out, q, k_cache, v_cache, block_ids, n_ids, T, start_pos, 0, 0, Hq,
+                                Hkv, D, block_size, num_blocks, scale, flags, dtype, err_flag,
+                                stream);
+}
+
+extern "C" int xs_paged_prefill_first(void *out, const void *q, const void *k_cache,
+                                      const void *v_cache, const int32_t *block_ids, int n_ids,
+                                      int T, int start_pos, int first, int window, int Hq, int Hkv,
+                                      int D, int block_size, int64_t num_blocks, float scale,
+                                      int dtype, int *err_flag, cudaStream_t stream) {
+    return pftc::prefill<true>(out, q, k_cache, v_cache, block_ids, n_ids, T, start_pos, first,
+                               window, Hq, Hkv, D, block_size, num_blocks, scale, 0, dtype, err_flag,
+                               stream);
 }

@@ -101,6 +101,8 @@ SIGNATURES = {
     "xs_paged_decode_first_workspace_bytes": (_S, [_I, _I, _I, _I]),
     "xs_paged_decode_first": (_I, [_P, _P, _L, _P, _P, _P, _I, _P, _P, _I, _I, _I, _I, _I, _I, _I,
                                    _L, _F, _P, _S, _I, _P, _P]),
+    "xs_paged_prefill_first": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _L, _F,
+                                    _I, _P, _P]),
     "xs_paged_decode_weights_workspace_bytes": (_S, [_I, _I, _I, _I, _I]),
     "xs_paged_decode_weights": (_I, [_P, _P, _P, _P, _L, _P, _P, _P, _I, _P, _P, _I, _I, _I, _I,
                                      _I, _L, _F, _P, _S, _I, _P, _P]),
@@ -675,6 +677,16 @@ def xs_paged_decode_first(out, q, k_cache, v_cache, block_tables, context_lens, 
     _done("xs_paged_decode_first", (_bound or _bind()).xs_paged_decode_first(
         _entry("xs_paged_decode_first"), out, q, k_cache, v_cache, block_tables, context_lens,
         scale, w.buf, w.Hq, w.Hkv, w.D, first, window, sinks, err_flag, _handle(stream)))
+
+
+def xs_paged_prefill_first(out, q, k_cache, v_cache, block_ids, start_pos, scale, first=0, window=0,
+                           err_flag=None, stream=None):
+    """The same mask for a chunk of a prompt (bf16): the query at position p
+    (q [T, Hq, D] from start_pos on) sees t <= p with t < first or t > p -
+    window (window 0: all)."""
+    _done("xs_paged_prefill_first", (_bound or _bind()).xs_paged_prefill_first(
+        _entry("xs_paged_prefill_first"), out, q, k_cache, v_cache, block_ids, start_pos, scale,
+        first, window, err_flag, _handle(stream)))
 
 
 def xs_paged_decode_weights(out, scores, q, k_cache, v_cache, block_tables, context_lens, scale,

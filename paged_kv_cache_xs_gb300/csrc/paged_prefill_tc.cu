@@ -202,6 +202,10 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&v);
 }
+// The lowest n bits (n < 0: none, n > 32: all).
+__device__ __forceinline__ uint32_t below(int n) {
+    return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1;
+}
 // Maximum of three (one instruction).
 __device__ __forceinline__ float fmax3(float a, float b, float c) {
     float r;
@@ -501,10 +505,19 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int j = 0; j < kKeys; ++j) v[j] = __uint_as_float(sr[j >> 5][j & 31]);
             if (need_mask) {
+if constexpr (kFirst) {
+                    // One bit for each key: compared one by one, three bounds a key
+                    // become branches (5 us a tile).
 #pragma unroll
-                for (int j = 0; j < kKeys; ++j) {
-                    const int t = k0 + j;
-                    v[j] = t <= qpos && (!kFirst || t >= low || t < p.first) ? v[j] : -INFINITY;
+                    for (int c = 0; c < kKeys / 32; ++c) {
+                        const int at = k0 + 32 * c;
+                        const uint32_t bits = below(qpos + 1 - at) & (~below(low - at) | below(p.first - at));
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) v[32 * c + j] = bits >> j & 1 ? v[32 * c + j] : -INFINITY;
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < kKeys; ++j) v[j] = k0 + j <= qpos ? v[j] : -INFINITY;
                 }
             }
             // Row maximum: 8 independent chains of three-input maxima.

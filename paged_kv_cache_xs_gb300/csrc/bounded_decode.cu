@@ -51,6 +51,7 @@
 
 namespace xs {
 namespace bounded {
+namespace {     // (the release and the debug library may be loaded side by side)
 
 constexpr int kBlock = 16;
 constexpr int kLineWarps = 4;       // warps of a CTA of the line, two CTAs on an SM
@@ -1202,6 +1203,7 @@ int check_and_launch(Params &p, bool weights, int D, int block_size, float scale
                     : (weights ? launch<H, 64, true>(p, dev, sms, stream) : launch<H, 64, false>(p, dev, sms, stream));
 }
 
+}  // namespace
 }  // namespace bounded
 XS_DEFINE_BOUNDS_COUNTER(bounds_failures_bounded)
 

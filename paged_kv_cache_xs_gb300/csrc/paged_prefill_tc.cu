@@ -725,6 +725,7 @@ KernelFn pick(int D, int G) {
     return nullptr;
 }
 
+namespace {     // (the release and the debug library may be loaded side by side)
 // The call with its mask: kFirst, or every key up to the query's position.
 template <bool kFirst>
 int prefill(void *out, const void *q, const void *k_cache, const void *v_cache,
@@ -826,6 +827,7 @@ int prefill(void *out, const void *q, const void *k_cache, const void *v_cache,
     }
     return launch_status();
 }
+}  // namespace
 
 }  // namespace pftc
 XS_DEFINE_BOUNDS_COUNTER(bounds_failures_prefill_tc)

@@ -207,3 +207,77 @@ class Kv4DecodeStep:
     def error_flags(self) -> int:
         """Device error bits raised so far (synchronises)."""
         return int(self.err_flag.item())
+
+
+class BoundedDecodeStep:
+    """Decode steps on caches that are kept to a budget of tokens: each layer's
+    new rows are normed, rotated and appended, attention counts what weight each
+    cached token got (``run``, once a layer), and sequences that have grown
+    beyond ``limit`` tokens are cut to ``budget`` of them, the ``first`` first,
+    the ``recent`` last and the heaviest between (``bound``, once a step).
+
+    A sequence's length is then less than its position: positions (int32 [B],
+    the new tokens' places in their texts) are the caller's.  Owns the scores
+    [layers, B, Hkv, max_blocks * 16], the attention's workspace and the rotated
+    q.  ``start(slots)`` forgets the scores of slots whose sequences are new (or
+    were prefilled: a prompt's tokens begin to be counted with the next step)."""
+
+    def __init__(self, B: int, Hq: int, Hkv: int, D: int, max_blocks_per_seq: int, layers: int,
+                 dtype: torch.dtype, device, budget: int, limit: int | None = None,
+                 first: int = 4, recent: int | None = None, eps: float = 1e-6,
+                 interleaved: bool = False):
+        self.B, self.layers, self.budget = B, layers, int(budget)
+        self.limit = self.budget if limit is None else int(limit)
+        self.first = min(int(first), self.budget)
+        self.recent = (self.budget - self.first) // 2 if recent is None else int(recent)
+        if self.budget <= 0 or self.recent < 0 or self.first < 0 or self.limit < self.budget or \
+                self.first + self.recent > self.budget:
+            raise ValueError("0 <= first, recent; first + recent <= budget <= limit; budget > 0")
+        self.eps, self.interleaved = float(eps), bool(interleaved)
+        self.device = torch.device(device)
+        i32 = dict(dtype=torch.int32, device=self.device)
+        self.ws = ops.BoundedWorkspace(B, Hq, Hkv, D, self.device, max_blocks_per_seq)
+        self.scores = torch.zeros(layers, B, Hkv, max_blocks_per_seq * ops.BLOCK_SIZE,
+                                  dtype=torch.float32, device=self.device)
+        self.scored = torch.zeros(B, **i32)
+        self.kept = torch.empty(layers, B, Hkv, self.budget, **i32)
+        self.new_lens = torch.empty(B, **i32)
+        self.slots = torch.arange(B, **i32)
+        self.q = torch.zeros(B, Hq, D, dtype=dtype, device=self.device)
+        self.slot_mapping = torch.empty(B, dtype=torch.int64, device=self.device)
+        self.err_flag = torch.zeros(1, **i32)
+
+    def start(self, slots):
+        """Forget the scores of slots (int64 tensor or list)."""
+        self.scored[slots] = 0
+
+    def run(self, layer, out, q, k_new, v_new, q_weight, k_weight, cos_sin, positions, k_cache,
+            v_cache, block_tables, context_lens, scale):
+        """One layer: q [B, Hq, D], k_new and v_new [B, Hkv, D] may be slices of
+        one projection's output; sequence b's new token becomes row
+        context_lens[b] - 1 of its cache.  q_weight, k_weight (or None: no norm)
+        and cos_sin (``ops.rope_table``, or None: no rotation) as in
+        ``ops.xs_qk_norm_rope_append``."""
+        ops.xs_slot_mapping(block_tables, context_lens, ops.BLOCK_SIZE, k_cache.shape[0],
+                            self.slot_mapping, err_flag=self.err_flag)
+        ops.xs_qk_norm_rope_append(self.q, q, k_new, v_new, q_weight, k_weight, self.eps, cos_sin,
+                                   positions, k_cache, v_cache, self.slot_mapping,
+                                   interleaved=self.interleaved, err_flag=self.err_flag)
+        ops.xs_paged_decode_weights(out, self.scores[layer], self.q, k_cache, v_cache, block_tables,
+                                    context_lens, scale, self.ws, scored_lens=self.scored,
+                                    err_flag=self.err_flag)
+
+    def bound(self, k_pools, v_pools, block_tables, context_lens, free_stack, free_top, extra_refs):
+        """After the last layer: cut the sequences beyond the limit in all
+        layers' pools [layers, num_blocks, Hkv, 16, D] and give back their
+        pages."""
+        ops.xs_kv_evict(self.slots, k_pools, v_pools, self.scores, block_tables, context_lens,
+                        self.kept, self.new_lens, self.first, self.recent, self.limit,
+                        extra_refs=extra_refs, err_flag=self.err_flag)
+        ops.xs_block_truncate(self.slots, self.new_lens, block_tables, context_lens, free_stack,
+                              free_top, extra_refs, err_flag=self.err_flag)
+        self.scored.copy_(context_lens)
+
+    def error_flags(self) -> int:
+        """Device error bits raised so far (synchronises)."""
+        return int(self.err_flag.item())

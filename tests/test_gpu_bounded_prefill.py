@@ -1,0 +1,89 @@
+"""Prompt chunks with first tokens and a window, against 64 bits."""
+import pytest
+import torch
+
+from paged_kv_cache_xs_gb300 import ops
+from tests import plain_bounded as plain
+from tests.gpu_helpers import device
+
+pytestmark = pytest.mark.gpu
+BF = torch.bfloat16
+
+
+def chunk(T, start, Hq, Hkv, D, seed, first, window, std=1.0):
+    """Pages whose rows that no query sees are NaN (V) and junk (K); unseen pages have no block."""
+    g = torch.Generator().manual_seed(seed)
+    n = start + T
+    pages = -(-n // 16)
+    k, v = (torch.randn(pages + 2, Hkv, 16, D, generator=g).to(BF) for _ in range(2))
+    ids = torch.randperm(pages + 2, generator=g)[:pages].to(torch.int32)
+    low = max(0, start + 1 - window) if window else 0
+    seen = [t for t in range(n) if t < first or t >= low]
+    unseen = torch.ones(pages + 2, 16, dtype=torch.bool)
+    table = torch.full((pages,), -1, dtype=torch.int32)
+    for t in seen:
+        table[t // 16] = ids[t // 16]
+        unseen[int(ids[t // 16]), t % 16] = False
+    for x in (k, v):
+        x.permute(0, 2, 1, 3)[unseen] = float("nan")
+    q = (torch.randn(T, Hq, D, generator=g) * std).to(BF)
+    return q, k, v, table
+
+
+@pytest.mark.parametrize("first,window", [(0, 0), (4, 0), (0, 1), (4, 1), (1, 16), (4, 100), (130, 50), (5, 129), (300, 200),
+                                          (4, 5000)])
+@pytest.mark.parametrize("T,start,Hq,Hkv,D", [(1, 0, 4, 1, 128), (40, 3, 8, 2, 128), (130, 270, 2, 2, 64), (70, 500, 8, 1, 64),
+                                              (200, 129, 4, 2, 128)])
+def test_masks(T, start, Hq, Hkv, D, first, window):
+    q, k, v, ids = chunk(T, start, Hq, Hkv, D, T + first, first, window)
+    dev = device()
+    out = torch.full((T, Hq, D), 7.0, dtype=BF, device=dev)
+    err = torch.zeros(1, dtype=torch.int32, device=dev)
+    ops.xs_paged_prefill_first(out, q.to(dev), k.to(dev), v.to(dev), ids.to(dev), start, D ** -0.5, first=first,
+                               window=window, err_flag=err)
+    ref, bound = plain.prefill(q, k, v, ids.tolist(), start, D ** -0.5, first, window)
+    d = (out.cpu().double() - ref).abs()
+    assert bool((d <= bound).all()), f"off by {d.max():.3e}, {(d / bound).max():.2f} of the bound"
+    assert int(err) == 0
+
+
+def test_all_logits_far_below_zero():
+    # Rows whose first tile is wholly masked, with logits near -1000 behind it.
+    q, k, v, ids = chunk(64, 600, 4, 1, 64, 1, 0, 70, std=0.0)
+    q[:] = -16.0
+    k = torch.where(k.isnan(), k, 1.0 + 0.01 * k)
+    dev = device()
+    out = torch.empty(64, 4, 64, dtype=BF, device=dev)
+    ops.xs_paged_prefill_first(out, q.to(dev), k.to(dev), v.to(dev), ids.to(dev), 600, 1.0, window=70)
+    ref, bound = plain.prefill(q, k, v, ids.tolist(), 600, 1.0, 0, 70)
+    assert bool(((out.cpu().double() - ref).abs() <= bound).all())
+
+
+def test_without_a_window_it_is_the_causal_call():
+    q, k, v, ids = (x.to(device()) for x in chunk(300, 77, 8, 2, 128, 5, 0, 0))
+    a, b = torch.empty_like(q), torch.empty_like(q)
+    ops.xs_paged_prefill_first(a, q, k, v, ids, 77, 0.1, first=9)
+    v2 = torch.where(v.isnan(), torch.zeros_like(v), v)
+    ops.xs_paged_prefill_tc(b, q, k, v2, ids, 77, 0.1)
+    assert torch.equal(a, b)
+
+
+def test_captured_and_a_bad_block():
+    q, k, v, ids = (x.to(device()) for x in chunk(100, 300, 4, 2, 64, 6, 4, 90))
+    out, err = torch.empty_like(q), torch.zeros(1, dtype=torch.int32, device=device())
+    run = lambda: ops.xs_paged_prefill_first(out, q, k, v, ids, 300, 0.1, first=4, window=90, err_flag=err)  # noqa: E731
+    run()
+    want = out.clone()
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        run()
+    out.zero_()
+    graph.replay()
+    assert torch.equal(out, want) and int(err) == 0
+    ids[5] = 1 << 24        # a page that no query sees
+    run()
+    assert int(err) == 0 and torch.equal(out, want)
+    ids[16] = 1 << 24
+    run()
+    assert int(err) == ops.FLAG_BAD_BLOCK

@@ -43,6 +43,7 @@
 // turns them into weights itself; the line leaves them in the workspace, most
 // of it in L2, for a second kernel.
 #include <atomic>
+#include <type_traits>
 
 #include <cuda.h>
 
@@ -840,17 +841,50 @@ __global__ void __launch_bounds__(32 * kLineWarps, line_ctas<T, D>())
 
 // The weights of tokens [from, to) of a segment, whose logits start at token
 // `base`, added to their scores; ends: the G rows' references and factors.
+template <int G>
+__device__ __forceinline__ void add_weights_of(const Params &p, float *scores, const float *logits, int base,
+                                               int from, int to, int scored, const float2 *ends) {
+    using V = typename std::conditional<G == 1, float, typename std::conditional<G == 2, float2, float4>::type>::type;
+    constexpr int kPieces = G <= 4 ? 1 : 2, kAtOnce = 4;
+    float2 end[G];
+#pragma unroll
+    for (int h = 0; h < G; ++h) end[h] = ends[h];
+    for (int t0 = from + static_cast<int>(threadIdx.x); t0 < to; t0 += kAtOnce * blockDim.x) {
+        V x[kAtOnce][kPieces];
+        float old[kAtOnce];
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u) {
+            const int t = t0 + u * blockDim.x;
+            if (t >= to || !XS_BOUNDS(t >= 0 && t < p.max_blocks * kBlock, p.err_flag)) continue;
+#pragma unroll
+            for (int k = 0; k < kPieces; ++k)
+                x[u][k] = reinterpret_cast<const V *>(logits)[static_cast<int64_t>(t - base) * kPieces + k];
+            old[u] = t < scored ? scores[t] : 0.0f;
+        }
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u) {
+            const int t = t0 + u * blockDim.x;
+            if (t >= to || !XS_BOUNDS(t >= 0 && t < p.max_blocks * kBlock, p.err_flag)) continue;
+            const float *v = reinterpret_cast<const float *>(x[u]);
+            float w = 0.0f;
+#pragma unroll
+            for (int h = 0; h < G; ++h) w = fmaf(fast_exp2(v[h] - end[h].x), end[h].y, w);
+            scores[t] = old[u] + w;
+        }
+    }
+}
 __device__ __forceinline__ void add_weights(const Params &p, int b, int hk, const float *logits, int base,
                                             int from, int to, int scored, const float2 *ends) {
+    if (!XS_BOUNDS(b < p.B && hk < p.Hkv, p.err_flag)) return;
     float *scores = p.scores + (static_cast<int64_t>(b) * p.Hkv + hk) * p.max_blocks * kBlock;
-    for (int t = from + static_cast<int>(threadIdx.x); t < to; t += blockDim.x) {
-        if (!XS_BOUNDS(b < p.B && hk < p.Hkv && t >= 0 && t < p.max_blocks * kBlock, p.err_flag)) continue;
-        const float old = t < scored ? scores[t] : 0.0f;
-        const float *x = logits + static_cast<int64_t>(t - base) * p.G;
-        float w = 0.0f;
-        for (int h = 0; h < p.G; ++h) w = fmaf(fast_exp2(x[h] - ends[h].x), ends[h].y, w);
-        scores[t] = old + w;
-    }
+    if (p.G == 1)
+        add_weights_of<1>(p, scores, logits, base, from, to, scored, ends);
+    else if (p.G == 2)
+        add_weights_of<2>(p, scores, logits, base, from, to, scored, ends);
+    else if (p.G == 4)
+        add_weights_of<4>(p, scores, logits, base, from, to, scored, ends);
+    else
+        add_weights_of<8>(p, scores, logits, base, from, to, scored, ends);
 }
 
 constexpr int kWeightThreads = 256;
@@ -886,7 +920,7 @@ template <typename T, int D> struct alignas(1024) ClusterSmem {
     float rank_w[kMaxCluster][8];       // factors of the CTAs' values
     float2 ends[8];
     uint64_t full[kClusterWarps][cluster_stages<T, D>()];
-    float logits[kLogitFloats];         // (the form with weights has them)
+    alignas(16) float logits[kLogitFloats];     // (the form with weights has them)
 };
 template <typename T, int D> constexpr int cluster_smem(bool weights) {
     return 1024 + static_cast<int>(sizeof(ClusterSmem<T, D>)) - (weights ? 0 : static_cast<int>(kLogitFloats * sizeof(float)));

@@ -4,13 +4,15 @@
 // of largest score (of equal ones the earlier).  What is kept moves together to
 // the sequence's first pages, in order.
 //
-// Two launches.  The first ranks: a CTA for each (layer, sequence, KV head) finds
-// the score that is the last to be kept by radix selection on the scores' bits,
-// 11, 11 and 10 of them at a time, counted in shared memory (11 bits: sign,
-// exponent and two more, so that scores of one magnitude spread over bins), and
-// writes the kept positions.  The scores stay in shared memory for the passes.
-// Each warp counts, then writes, a contiguous part, so there are no barriers
-// within a pass and the order of atomics decides nothing.
+// Two launches.  The first ranks: a CTA for each (layer, sequence, KV head), or a
+// cluster of kRankCtas where tables are long, finds the score that is the last to
+// be kept by radix selection on the scores' bits, 11, 11 and 10 of them at a time,
+// counted in shared memory (11 bits: sign, exponent and two more, so that scores
+// of one magnitude spread over bins), and writes the kept positions.  Each CTA of
+// a cluster counts a contiguous part of the positions and adds the bins that it
+// has met to those of all the others.  The scores stay in shared memory for the
+// passes.  Each warp counts, then writes, a contiguous part, so there are no
+// barriers within a pass and the order of atomics decides nothing.
 //
 // The second moves rows, in place.  Position j takes the row of position
 // kept[j] >= j, so a CTA that goes through j upwards and reads a tile before it
@@ -29,8 +31,10 @@ namespace {
 constexpr int kPage = 16;
 constexpr int kBins = 2048;
 constexpr int kMoveThreads = 256;
-constexpr int kMoveUnroll = 4;      // 16-byte pieces of a thread in a tile
-constexpr int kScoresHeld = 49152;  // in shared memory; of more, they are read again for each pass
+constexpr int kMoveUnroll = 8;      // 16-byte pieces of a thread in a tile
+constexpr int kLongTokens = 4096;   // of a table: beyond, a cluster ranks
+constexpr int kRankCtas = 8;
+constexpr int kScoresHeld = 40960;  // of a CTA, in shared memory; of more, they are read again for each pass
 
 struct EvictParams {
     const int32_t *seq_ids;
@@ -42,6 +46,7 @@ struct EvictParams {
     int max_blocks, B, Hkv, layers, row_bytes;
     int64_t num_blocks;
     int first, recent, budget, limit;
+    int held;                   // scores that a CTA's shared memory has room for
     int32_t *kept, *new_lens;
     int *err_flag;
 };
@@ -75,16 +80,30 @@ template <int kThreads> __device__ __forceinline__ int scan_threads(int v, int *
     return before + inc - v;
 }
 
-template <int kThreads>
+// The threads of the launch's cluster (kCtas 1: of the CTA), and what they wrote.
+template <int kCtas> __device__ __forceinline__ void all_sync() {
+    if (kCtas == 1)
+        __syncthreads();
+    else
+        asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t peer_addr(const void *own, int rank) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(own)), "r"(rank));
+    return a;
+}
+
+template <int kThreads, int kCtas>
 __global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_constant__ EvictParams p) {
     after_previous();
-    extern __shared__ uint32_t held[];      // the scores' bits, where they fit
-    __shared__ int hist[kBins], sm[kThreads / 32], bin, left;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int hk = blockIdx.x % p.Hkv, entry = blockIdx.x / p.Hkv % p.n;
-    const int layer = blockIdx.x / p.Hkv / p.n;
-    const bool tells = layer == 0 && hk == 0;       // of this entry, what is not a head's own
-    int32_t *kept = p.kept + static_cast<int64_t>(blockIdx.x) * p.budget;
+    extern __shared__ uint32_t held[];      // the bits of this CTA's part of the scores, where they fit
+    __shared__ int hist[kBins], all_hist[kCtas > 1 ? kBins : 1], sm[kThreads / 32], bin, left, counts[2];
+    int *bins = kCtas > 1 ? all_hist : hist;        // of all the candidates
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rank = blockIdx.x % kCtas;
+    const int head = blockIdx.x / kCtas;
+    const int hk = head % p.Hkv, entry = head / p.Hkv % p.n, layer = head / p.Hkv / p.n;
+    const bool tells = layer == 0 && hk == 0 && rank == 0;      // of this entry, what is not a head's own
+    int32_t *kept = p.kept + static_cast<int64_t>(head) * p.budget;
 
     // Whether the sequence is cut: the same for all its heads and layers.
     const int b = XS_BOUNDS(entry < p.n && layer < p.layers, p.err_flag) ? p.seq_ids[entry] : -1;
@@ -95,6 +114,18 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_con
             if (p.seq_ids[i] == b) flag = XS_FLAG_BAD_SLOT;
     }
     const int n = min(len, p.max_blocks * kPage);
+    // (The scores are on their way while the pages are looked at.)
+    const uint32_t *score = reinterpret_cast<const uint32_t *>(
+        p.scores + ((static_cast<int64_t>(layer) * p.B + (n > p.limit ? b : 0)) * p.Hkv + hk) * p.max_blocks * kPage);
+    // This CTA's positions [mine, end), of which [lo, hi) are chosen from.
+    const int part = ((n + kCtas - 1) / kCtas + 31) / 32 * 32;
+    const int mine = min(rank * part, n), end = min(mine + part, n);
+    const int lo = max(p.first, mine), hi = min(n - p.recent, end);
+    const bool fits = part <= p.held;
+    if (n > p.limit && fits) {
+#pragma unroll 4
+        for (int t = lo + tid; t < hi; t += kThreads) held[t - mine] = score[t];
+    }
     if (n > p.limit) {
         const int32_t *row = p.tables + static_cast<int64_t>(b) * p.max_blocks;
         for (int c = p.first / kPage + tid; c < (n + kPage - 1) / kPage; c += kThreads) {
@@ -111,19 +142,11 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_con
     const bool cut = !stop && n > p.limit;
     if (tells && tid == 0) p.new_lens[entry] = cut ? p.budget : -1;
     if (!cut) {
-        for (int j = tid; j < p.budget; j += kThreads) kept[j] = -1;
-        return;
+        for (int j = rank * kThreads + tid; j < p.budget; j += kCtas * kThreads) kept[j] = -1;
+        return;         // the whole cluster
     }
 
-    const uint32_t *score = reinterpret_cast<const uint32_t *>(
-        p.scores + ((static_cast<int64_t>(layer) * p.B + b) * p.Hkv + hk) * p.max_blocks * kPage);
-    const int lo = p.first, hi = n - p.recent;      // [lo, hi) are chosen from
-    const bool fits = p.max_blocks * static_cast<int64_t>(kPage) <= kScoresHeld;
-    if (fits) {
-#pragma unroll 4
-        for (int t = lo + tid; t < hi; t += kThreads) held[t] = score[t];
-    }
-    auto key_at = [&](int t) { return key_of(fits ? held[t] : __ldg(score + t)); };
+    auto key_at = [&](int t) { return key_of(fits ? held[t - mine] : __ldg(score + t)); };
 
     // The threshold: keys above it are kept, and `need` of those equal to it.
     uint32_t threshold = 0xffffffffu;       // above every key
@@ -135,22 +158,39 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_con
         for (int pass = 0; pass < 3; ++pass) {
             const int bits = pass < 2 ? 11 : 10, above = shift;
             shift -= bits;
-            for (int i = tid; i < kBins; i += kThreads) hist[i] = 0;
-            __syncthreads();
+            for (int i = tid; i < kBins; i += kThreads) {
+                hist[i] = 0;
+                if (kCtas > 1) all_hist[i] = 0;
+            }
+            all_sync<kCtas>();
+#pragma unroll 4
             for (int t = lo + tid; t < hi; t += kThreads) {
                 const uint32_t key = key_at(t);
                 if (pass == 0 || key >> above == prefix) atomicAdd(&hist[key >> shift & ((1u << bits) - 1)], 1);
             }
             __syncthreads();
+            if (kCtas > 1) {
+                for (int i = tid; i < kBins; i += kThreads) {
+                    const int c = hist[i];
+                    if (!c) continue;
+#pragma unroll
+                    for (int r = 0; r < kCtas; ++r)
+                        asm volatile("red.relaxed.cluster.shared::cluster.add.s32 [%0], %1;" ::"r"(
+                                         peer_addr(&all_hist[i], r)),
+                                     "r"(c)
+                                     : "memory");
+                }
+                all_sync<kCtas>();
+            }
             // A thread's bins, from the highest of all on.
             constexpr int kPer = kBins / kThreads;
-            int mine = 0, total;
+            int sum = 0, total;
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) mine += hist[kBins - 1 - (tid * kPer + i)];
-            int before = scan_threads<kThreads>(mine, sm, &total);
-            if (before < need && before + mine >= need) {
+            for (int i = 0; i < kPer; ++i) sum += bins[kBins - 1 - (tid * kPer + i)];
+            int before = scan_threads<kThreads>(sum, sm, &total);
+            if (before < need && before + sum >= need) {
                 for (int i = 0; i < kPer; ++i) {
-                    const int at = kBins - 1 - (tid * kPer + i), c = hist[at];
+                    const int at = kBins - 1 - (tid * kPer + i), c = bins[at];
                     if (before < need && before + c >= need) bin = at, left = need - before;
                     before += c;
                 }
@@ -166,12 +206,12 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_con
 
     // Each warp's part of the positions, in order.
     constexpr int kWarps = kThreads / 32;
-    const int per = ((n + kWarps - 1) / kWarps + 31) / 32 * 32;
-    const int from = min(warp * per, n), to = min(from + per, n);
+    const int per = ((end - mine + kWarps - 1) / kWarps + 31) / 32 * 32;
+    const int from = min(mine + warp * per, end), to = min(from + per, end);
     auto look = [&](int t, uint32_t *over, uint32_t *even) {
         bool o = false, e = false;
         if (t < to) {
-            o = t < lo || t >= hi;
+            o = t < p.first || t >= n - p.recent;
             if (!o) {
                 const uint32_t key = key_at(t);
                 o = key > threshold, e = key == threshold;
@@ -181,17 +221,31 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_con
         *even = __ballot_sync(0xffffffffu, e);
     };
     int overs = 0, evens = 0;
+#pragma unroll 4
     for (int t = from; t < to; t += 32) {
         uint32_t over, even;
         look(t + lane, &over, &even);
         overs += __popc(over), evens += __popc(even);
     }
-    // (Both counts in one scan: a lane of each warp has them, the others 0.)
-    int total, overs0 = scan_threads<kThreads>(lane == 0 ? overs : 0, sm, &total);
-    int evens0 = scan_threads<kThreads>(lane == 0 ? evens : 0, sm, &total);
+    // (A lane of each warp has its counts, the others 0.)
+    int all_overs, overs0 = scan_threads<kThreads>(lane == 0 ? overs : 0, sm, &all_overs);
+    int all_evens, evens0 = scan_threads<kThreads>(lane == 0 ? evens : 0, sm, &all_evens);
     overs0 = __shfl_sync(0xffffffffu, overs0, 0), evens0 = __shfl_sync(0xffffffffu, evens0, 0);
+    if (kCtas > 1) {        // and what the CTAs before this one have
+        if (tid == 0) counts[0] = all_overs, counts[1] = all_evens;
+        all_sync<kCtas>();
+        int o = 0, e = 0;
+        if (lane < rank) {
+            asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(o) : "r"(peer_addr(&counts[0], lane)) : "memory");
+            asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(e) : "r"(peer_addr(&counts[1], lane)) : "memory");
+        }
+        overs0 += __reduce_add_sync(0xffffffffu, o), evens0 += __reduce_add_sync(0xffffffffu, e);
+        // No CTA leaves before all have read its counts.
+        asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
+    }
     int at = overs0 + min(evens0, need);
     const uint32_t below = (1u << lane) - 1;
+#pragma unroll 2
     for (int t = from; t < to; t += 32) {
         uint32_t over, even;
         look(t + lane, &over, &even);
@@ -202,47 +256,45 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_con
         at += __popc(all);
         evens0 += __popc(even);
     }
+    if (kCtas > 1) asm volatile("barrier.cluster.wait;" ::: "memory");
 }
 
-// Goes through positions [first, budget) in tiles: position j's piece, as get(j,
-// kept[j]) has it, is put by put(j, piece) once the whole tile has been read.
-// kPer positions of a tile are a thread's own, kStep apart.
-template <typename V, int kPer, typename G, typename P>
-__device__ __forceinline__ void move_tiles(const int32_t *kept, int first, int budget, int own, int step, G &&get,
+constexpr int kMoveChunk = 1024;    // positions whose places are looked up at a time
+
+// Goes through positions [first, budget) in tiles: where position j takes
+// another's piece, put(j, get(j)) - once the whole tile has been got.  A tile is
+// kMoveUnroll positions of each thread, `step` apart from `own` on.  look(j)
+// finds j's places for a chunk of positions; moves(j): whether it takes another's.
+template <typename V, typename L, typename M, typename G, typename P>
+__device__ __forceinline__ void move_tiles(int first, int budget, int own, int step, L &&look, M &&moves, G &&get,
                                            P &&put) {
-    V cur[kPer], next[kPer];
-    int cur_from[kPer], next_from[kPer];
-    auto load = [&](int base, V (&v)[kPer], int (&src)[kPer]) {
-#pragma unroll
-        for (int u = 0; u < kPer; ++u) {
-            const int j = base + u * step + own;
-            src[u] = j < budget ? __ldcg(kept + j) : j;
-        }
-#pragma unroll
-        for (int u = 0; u < kPer; ++u) {
-            const int j = base + u * step + own;
-            if (src[u] != j) v[u] = get(src[u]);
-        }
-    };
-    const int tile = kPer * step;
-    load(first, cur, cur_from);
-    for (int base = first; base < budget; base += tile) {
-        if (base + tile < budget) load(base + tile, next, next_from);
+    for (int chunk = first; chunk < budget; chunk += kMoveChunk) {
+        const int end = min(chunk + kMoveChunk, budget);
         __syncthreads();
+        look(chunk, end);
+        __syncthreads();
+        for (int base = chunk; base < end; base += kMoveUnroll * step) {
+            V v[kMoveUnroll];
+            bool yes[kMoveUnroll];
 #pragma unroll
-        for (int u = 0; u < kPer; ++u) {
-            const int j = base + u * step + own;
-            if (cur_from[u] != j) put(j, cur[u]);
+            for (int u = 0; u < kMoveUnroll; ++u) {
+                const int j = base + u * step + own;
+                yes[u] = j < end && moves(j);
+                if (yes[u]) v[u] = get(j);
+            }
+            __syncthreads();
+#pragma unroll
+            for (int u = 0; u < kMoveUnroll; ++u)
+                if (yes[u]) put(base + u * step + own, v[u]);
         }
-#pragma unroll
-        for (int u = 0; u < kPer; ++u) cur[u] = next[u], cur_from[u] = next_from[u];
     }
 }
 
 // CTAs (layer, entry, KV head) x (K's slices, V's slices, the scores).
-__global__ void __launch_bounds__(kMoveThreads)
+__global__ void __launch_bounds__(kMoveThreads, 4)
     evict_move_kernel(const __grid_constant__ EvictParams p, const int slices) {
     after_previous();
+    __shared__ int32_t from[kMoveChunk], from_id[kMoveChunk], to_id[kMoveChunk / kPage + 1];
     const int32_t *kept = p.kept + static_cast<int64_t>(blockIdx.x) * p.budget;
     if (__ldcg(kept) < 0) return;       // not cut
     const int hk = blockIdx.x % p.Hkv, entry = blockIdx.x / p.Hkv % p.n;
@@ -250,28 +302,48 @@ __global__ void __launch_bounds__(kMoveThreads)
     const int b = XS_BOUNDS(entry < p.n && layer < p.layers, p.err_flag) ? p.seq_ids[entry] : 0;
     const int plane = blockIdx.y / slices, slice = blockIdx.y % slices, tid = threadIdx.x;
     const int tokens = p.max_blocks * kPage;
+    int at = p.first;                   // of `from` and the others: the chunk's start
+    auto moves = [&](int j) { return from[j - at] != j; };
+    auto checked = [&](int t) { return XS_BOUNDS(t >= 0 && t < tokens, p.err_flag) ? t : 0; };
     if (plane == 2) {
         float *score = p.scores + ((static_cast<int64_t>(layer) * p.B + b) * p.Hkv + hk) * tokens;
-        move_tiles<float, kMoveUnroll>(
-            kept, p.first, p.budget, tid, kMoveThreads,
-            [&](int t) { return XS_BOUNDS(t >= 0 && t < tokens, p.err_flag) ? score[t] : 0.0f; },
-            [&](int j, float v) { if (XS_BOUNDS(j < tokens, p.err_flag)) score[j] = v; });
+        move_tiles<float>(
+            p.first, p.budget, tid, kMoveThreads,
+            [&](int chunk, int end) {
+                at = chunk;
+                for (int j = chunk + tid; j < end; j += kMoveThreads) from[j - chunk] = checked(__ldcg(kept + j));
+            },
+            moves, [&](int j) { return score[from[j - at]]; }, [&](int j, float v) { score[checked(j)] = v; });
         return;
     }
     char *pool = (plane ? p.v_pools : p.k_pools) + layer * p.layer_bytes;
     const int32_t *row = p.tables + static_cast<int64_t>(b) * p.max_blocks;
     // A slice of a row: `wide` pieces of 16 bytes, one each for neighbouring threads.
     const int wide = p.row_bytes / 16 / slices, piece = tid % wide;
-    const int64_t in_row = static_cast<int64_t>(slice * wide + piece) * 16;
-    auto at = [&](int t) {
-        int64_t id = 0;
-        if (XS_BOUNDS(t >= 0 && t < tokens, p.err_flag)) id = __ldg(row + t / kPage);
-        if (!XS_BOUNDS(id >= 0 && id < p.num_blocks, p.err_flag)) id = 0;
-        return reinterpret_cast<uint4 *>(pool + ((id * p.Hkv + hk) * kPage + t % kPage) * p.row_bytes + in_row);
+    const int64_t in_row = static_cast<int64_t>(slice * wide + piece) * 16 + hk * kPage * static_cast<int64_t>(p.row_bytes);
+    const int64_t block_bytes = static_cast<int64_t>(p.Hkv) * kPage * p.row_bytes;
+    auto place = [&](int id, int t) {
+        return reinterpret_cast<uint4 *>(pool + id * block_bytes + (t % kPage) * p.row_bytes + in_row);
     };
-    move_tiles<uint4, kMoveUnroll>(
-        kept, p.first, p.budget, tid / wide, kMoveThreads / wide, [&](int t) { return *at(t); },
-        [&](int j, const uint4 &v) { *at(j) = v; });
+    auto block_of = [&](int t) {
+        const int32_t id = __ldg(row + checked(t) / kPage);
+        return XS_BOUNDS(id >= 0 && id < p.num_blocks, p.err_flag) ? id : 0;
+    };
+    move_tiles<uint4>(
+        p.first, p.budget, tid / wide, kMoveThreads / wide,
+        [&](int chunk, int end) {
+            at = chunk;
+#pragma unroll 4
+            for (int j = chunk + tid; j < end; j += kMoveThreads) {
+                const int t = __ldcg(kept + j);
+                from[j - chunk] = t;
+                from_id[j - chunk] = block_of(t);
+            }
+            for (int c = chunk / kPage + tid; c <= (end - 1) / kPage; c += kMoveThreads)
+                to_id[c - chunk / kPage] = block_of(c * kPage);
+        },
+        moves, [&](int j) { return *place(from_id[j - at], from[j - at]); },
+        [&](int j, const uint4 &v) { *place(to_id[j / kPage - at / kPage], j) = v; });
 }
 
 }  // namespace
@@ -319,26 +391,32 @@ extern "C" int xs_kv_evict(const int32_t *seq_ids, int n, void *k_pools, void *v
         return XS_EDEVICE;
     const int ctas = static_cast<int>(heads) * Hkv;
     const int64_t tokens = static_cast<int64_t>(max_blocks_per_seq) * xs::kPage;
-    const size_t smem = tokens <= xs::kScoresHeld ? tokens * sizeof(uint32_t) : 0;
     int rc;
-    if (tokens <= 4096) {
-        rc = xs::launch_after(xs::evict_select_kernel<256>, dim3(ctas), 256, smem, stream, 1, p);
+    if (tokens <= xs::kLongTokens) {
+        p.held = static_cast<int>(tokens);
+        rc = xs::launch_after(xs::evict_select_kernel<256, 1>, dim3(ctas), 256, tokens * sizeof(uint32_t), stream, 1, p);
     } else {
+        if (ctas > INT_MAX / xs::kRankCtas) return XS_EUNSUPPORTED;
+        const auto select = xs::evict_select_kernel<256, xs::kRankCtas>;
         static std::atomic<bool> may[64];      // each device has been told of its shared memory
         if (dev >= 64 || !may[dev].load(std::memory_order_acquire)) {
-            if (cudaFuncSetAttribute(xs::evict_select_kernel<1024>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+            if (cudaFuncSetAttribute(select, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      xs::kScoresHeld * sizeof(uint32_t)) != cudaSuccess) {
                 cudaGetLastError();
                 return XS_EDEVICE;
             }
             if (dev < 64) may[dev].store(true, std::memory_order_release);
         }
-        rc = xs::launch_after(xs::evict_select_kernel<1024>, dim3(ctas), 1024, smem, stream, 1, p);
+        const int64_t part = (tokens + xs::kRankCtas - 1) / xs::kRankCtas + 32;
+        p.held = static_cast<int>(part < xs::kScoresHeld ? part : 0);
+        rc = xs::launch_after(select, dim3(ctas * xs::kRankCtas), 256, p.held * sizeof(uint32_t), stream,
+                              xs::kRankCtas, p);
     }
     if (rc != XS_OK) return rc;
-    // Slices of no less than 32 bytes, while they leave SMs without work.
+    // Slices of no less than 64 bytes (of 128: 10% slower, of 32 the same), while they
+    // leave SMs without work.
     int slices = 1;
-    while (row_bytes / slices > 32 && static_cast<int64_t>(ctas) * 2 * slices < 4 * sms) slices *= 2;
+    while (row_bytes / slices > 64 && static_cast<int64_t>(ctas) * 2 * slices < 4 * sms) slices *= 2;
     return xs::launch_after(xs::evict_move_kernel, dim3(ctas, 2 * slices + 1), xs::kMoveThreads, 0, stream, 1, p,
                             slices);
 }

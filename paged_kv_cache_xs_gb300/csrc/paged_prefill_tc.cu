@@ -133,6 +133,7 @@ struct PParams {
     // launch on the stream; the tiles from start on and every write after.
     int early;
     int first, window;             // kFirst: what a query sees (window 0: every key)
+    int units, whole;              // kFirst: pairs of Q tiles, and how many of them are one CTA's
 };
 
 // Shared-memory matrix descriptor: start, leading and stride byte offsets,
@@ -249,10 +250,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Longest first: CTA i takes token tile (tiles - 1 - i / Hkv) of KV head
     // i % Hkv, so the CTAs with the most keys start in the first wave and the
     // launch ends on the short ones.
-    const int n_tok_tiles = static_cast<int>(gridDim.x) / p.Hkv;
-    const int g = static_cast<int>(blockIdx.x) % p.Hkv;
-    const int tok0 = (n_tok_tiles - 1 - static_cast<int>(blockIdx.x) / p.Hkv) * kQTiles * kTq;
-    const int ntok = min(kQTiles * kTq, p.T - tok0);  // tokens of this CTA
+    // kFirst: CTAs from p.whole on take one Q tile each, two of them what others
+    // do as one CTA.
+    const int n_tok_tiles = (kFirst ? p.units : static_cast<int>(gridDim.x)) / p.Hkv;
+    const bool half = kFirst && static_cast<int>(blockIdx.x) >= p.whole;
+    const int unit = half ? p.whole + (static_cast<int>(blockIdx.x) - p.whole) / 2 : static_cast<int>(blockIdx.x);
+    const int g = unit % p.Hkv;
+    const int tok0 = (n_tok_tiles - 1 - unit / p.Hkv) * kQTiles * kTq +
+                     (half && ((static_cast<int>(blockIdx.x) - p.whole) & 1) ? kTq : 0);
+    const int ntok = kFirst ? max(0, min(half ? kTq : kQTiles * kTq, p.T - tok0))
+                            : min(kQTiles * kTq, p.T - tok0);  // tokens of this CTA
     const int kmax = p.start + tok0 + ntok;            // keys [0, kmax) are read
     // kFirst: keys [low0, kmax) are in some query's window, and those below
     // `first` are seen by all that come after them; tile kt of the CTA's list is
@@ -263,7 +270,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto key_tile = [&](int kt) { return kFirst && kt >= nfirst ? kt + skipped : kt; };
     // Whether no query of the CTA sees key t.
     auto hidden = [&](int t) { return t >= kmax || (kFirst && t >= p.first && t < low0); };
-    const int ntiles = (kmax + kKeys - 1) / kKeys - skipped;
+    const int ntiles = kFirst && ntok == 0 ? 0 : (kmax + kKeys - 1) / kKeys - skipped;
     const int npages = (kmax + kBlock - 1) / kBlock;
     // Q tile qi holds tokens [qi * kTq, qi * kTq + tile_tokens(qi)) of the CTA
     // and attends to key tiles [0, tile_ntiles(qi)).
@@ -478,9 +485,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int my_ntiles = tile_ntiles(qi);
         const uint32_t lane_off = static_cast<uint32_t>(32 * quad) << 16;
         const uint32_t cols = tmem + lane_off + qi * kGroupCols;
-        float m_ref = 0.f, l = 0.f;
-        bool seen = false;                 // kFirst: this row has met a key that it sees
-        const int low = kFirst && p.window > 0 ? qpos - p.window + 1 : 0;
+        // (kFirst: -infinity until the row has met a key that it sees.)
+        float m_ref = kFirst ? -INFINITY : 0.f, l = 0.f;
         bool ok = true;
         for (int kt = 0; kt < my_ntiles; ++kt) {
             ok = __all_sync(0xffffffffu, mbar_wait_bounded(s_full(qi), kt & 1, kWaitLimitNs)) &&
@@ -508,6 +514,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 if constexpr (kFirst) {
                     // One bit for each key: compared one by one, three bounds a key
                     // become branches (5 us a tile).
+                    int row = r;            // (so that its position takes no register elsewhere)
+                    asm volatile("" : "+r"(row));
+                    const int qpos = q0 + row / G, low = p.window > 0 ? qpos - p.window + 1 : 0;
 #pragma unroll
                     for (int c = 0; c < kKeys / 32; ++c) {
                         const int at = k0 + 32 * c;
@@ -534,10 +543,9 @@ if constexpr (kFirst) {
             bool rescale = false;
             float m_new = m_ref;
             // (A row that has seen no key yet has O = 0, which needs no rescaling.)
-            if (kFirst ? !seen : kt == 0) {
-                m_ref = tmax == -INFINITY ? 0.f : tmax;
-                m_new = m_ref;
-                seen = tmax != -INFINITY;
+            if (kFirst ? m_ref == -INFINITY : kt == 0) {
+                m_new = tmax == -INFINITY ? 0.f : tmax;
+                m_ref = kFirst ? tmax : m_new;
             } else if (tmax > m_ref + kHeadroom) {
                 rescale = true;
                 m_new = tmax;
@@ -577,8 +585,8 @@ if constexpr (kFirst) {
             tmem_st32(cols + kColP, *reinterpret_cast<uint32_t(*)[32]>(&pr[0]));
             tmem_st32(cols + kColP + 32, *reinterpret_cast<uint32_t(*)[32]>(&pr[32]));
             tmem_wait_st();
-            const bool ends = kt == ntiles - 1 && npages * kBlock > kmax;
-            if (ends || (kFirst && low0 > p.first && ((kt == nfirst && k0 < low0) || kt == nfirst - 1))) {
+            if (kFirst ? k0 + kKeys > kmax || (k0 < low0 && k0 + kKeys > p.first)
+                       : kt == ntiles - 1 && npages * kBlock > kmax) {
                 // Unwritten slots of the CTA's last page, and keys between the first
                 // tokens and the window that no query of the CTA sees: zero their V
                 // rows (128-byte lines, whole, so the swizzle inside a line does not
@@ -791,7 +799,7 @@ int prefill(void *out, const void *q, const void *k_cache, const void *v_cache,
                 }
         }
     }
-    PParams p;
+    PParams p = {};
     p.out = static_cast<__nv_bfloat16 *>(out);
     p.block_ids = block_ids;
     p.n_ids = n_ids;
@@ -807,8 +815,21 @@ int prefill(void *out, const void *q, const void *k_cache, const void *v_cache,
     p.window = window;
     p.early = (flags & XS_PREFILL_OVERLAP) ? 1 : 0;
     const int tq = kQTiles * kRows / G;  // query tokens per CTA
-    const int64_t ctas = static_cast<int64_t>((T + tq - 1) / tq) * Hkv;
-    if (ctas > 0x7fffffff) return XS_EUNSUPPORTED;
+    int64_t ctas = static_cast<int64_t>((T + tq - 1) / tq) * Hkv;
+    if (ctas > 0x3fffffff) return XS_EUNSUPPORTED;
+    if (kFirst) {
+        // Under a window all CTAs take about as long.  Where the last wave would
+        // fill no more than half of the SMs, its pairs of Q tiles are two CTAs each
+        // (512 pairs: 328 us as they are, HALVES_US with the last 56 as 112).
+        int dev = 0, sms = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess ||
+            cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+            return XS_EDEVICE;
+        const int last = static_cast<int>(ctas % sms);
+        p.units = static_cast<int>(ctas);
+        p.whole = last <= sms / 2 ? p.units - last : p.units;
+        ctas += p.units - p.whole;
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(ctas));
     cfg.blockDim = dim3(kThreads);

@@ -58,7 +58,7 @@ constexpr int kBlock = 16;
 constexpr int kLineWarps = 4;       // warps of a CTA of the line, two CTAs on an SM
 constexpr int kClusterWarps = 8;    // of a cluster's CTA, one on an SM
 constexpr int kMaxWarps = 1280;     // the workspace holds partials for so many
-constexpr int kSegmentCost = 4;     // pages
+constexpr int kSegmentCost = 6;     // pages (4: many short segments 8% faster, few long ones 4% slower; 8: the reverse)
 constexpr int kMinShare = 4;        // pages
 constexpr int kWholePages = 8;      // segments up to so many pages are not cut
 constexpr int kMaxCluster = 16;
@@ -110,6 +110,18 @@ struct Params {
     float *logits;      // [B, Hkv, max_blocks * 16, G], in powers of two
     float2 *ends;       // [B, Hq]: a row's reference and the reciprocal of its sum
 };
+
+// f(integral_constant<int, G>) for G in {1, 2, 4, 8}.
+template <typename F> __device__ __forceinline__ void by_heads(int G, F &&f) {
+    if (G == 1)
+        f(std::integral_constant<int, 1>());
+    else if (G == 2)
+        f(std::integral_constant<int, 2>());
+    else if (G == 4)
+        f(std::integral_constant<int, 4>());
+    else
+        f(std::integral_constant<int, 8>());
+}
 
 // A lane's registers of 8 heads x D values, then 8 references and 8 sums.
 __host__ __device__ constexpr int partial_floats(int D) { return 8 * D + 16; }
@@ -209,7 +221,7 @@ template <int D> struct State<__nv_bfloat16, D> {
 #pragma unroll
         for (int i = 0; i < D / 4; ++i) acc[i] *= f[i & 1];
     }
-    __device__ __forceinline__ void sum_up() {
+    __device__ __forceinline__ void sum_up(const Params &) {
 #pragma unroll
         for (int k = 0; k < 2; ++k)
 #pragma unroll
@@ -316,18 +328,25 @@ template <int D> struct State<__nv_bfloat16, D> {
 
 // fp32: 8 lanes share a key's dims in the logits; then lane (j, r) has the logits
 // of head r and keys j, j + 4, j + 8, j + 12.  In the values a lane has D / 32 dims
-// of every head, and the weights come through shared memory.
+// of every head, and the weights come through shared memory.  With one head in a
+// group (G = 1) a lane has the logit of one key, and its weight is passed by a
+// shuffle: 2.2 times fewer instructions.
 template <int D> struct State<float, D> {
     static constexpr int kHeads = 1;
     static constexpr int kDims = D / 32;
     const float *q;
+    float4 q1[D / 32];      // G = 1: dims 32 i + 4 r .. of the head
     float m[1], l[1], acc[D / 4];
 
     static __device__ __forceinline__ int head(int lane, int) { return lane & 7; }
     static __device__ __forceinline__ int head_of(int, int k, int c) { return (4 * k + c) / kDims; }
     static __device__ __forceinline__ int dim(int lane, int k, int c) { return lane * kDims + (4 * k + c) % kDims; }
-    __device__ __forceinline__ void load_q(const Params &, const void *q0, int) {
+    __device__ __forceinline__ void load_q(const Params &p, const void *q0, int lane) {
         q = static_cast<const float *>(q0);
+        if (p.G == 1) {
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) q1[i] = __ldg(reinterpret_cast<const float4 *>(q) + 8 * i + (lane & 7));
+        }
     }
     __device__ __forceinline__ void scale(const float (&f)[1]) {
 #pragma unroll
@@ -337,13 +356,72 @@ template <int D> struct State<float, D> {
             for (int i = 0; i < kDims; ++i) acc[h * kDims + i] *= fh;
         }
     }
-    __device__ __forceinline__ void sum_up() {
+    __device__ __forceinline__ void sum_up(const Params &p) {
         l[0] += __shfl_xor_sync(0xffffffffu, l[0], 8);
         l[0] += __shfl_xor_sync(0xffffffffu, l[0], 16);
+        if (p.G == 1) {     // keys r & 3, on lanes r and r + 4 alike
+            l[0] += __shfl_xor_sync(0xffffffffu, l[0], 1);
+            l[0] += __shfl_xor_sync(0xffffffffu, l[0], 2);
+        }
+    }
+    template <bool kWeights>
+    __device__ __forceinline__ void page1(const Params &p, uint32_t kp, uint32_t vp, const Span &sp, int tok0,
+                                          float *logits, int lane) {
+        const int j = lane >> 3, r = lane & 7;
+        float s[4] = {};
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const float4 k = lds128(kp + ((4 * u + j) * D + 32 * i + 4 * r) * 4);
+                s[u] = fmaf(k.w, q1[i].w, fmaf(k.z, q1[i].z, fmaf(k.y, q1[i].y, fmaf(k.x, q1[i].x, s[u]))));
+            }
+#pragma unroll
+        for (int d = 1; d < 8; d <<= 1)
+#pragma unroll
+            for (int u = 0; u < 4; ++u) s[u] += __shfl_xor_sync(0xffffffffu, s[u], d);
+        const int key = 4 * (r & 3) + j;
+        const float mine = r & 2 ? (r & 1 ? s[3] : s[2]) : (r & 1 ? s[1] : s[0]);
+        const float x = sp.sees(tok0 + key) ? mine * p.scale_log2 : -INFINITY;
+        if (kWeights && r < 4) logits[key] = x;
+        if (__any_sync(0xffffffffu, x > m[0])) {
+            float hi = x;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, d));
+            const float to = hi > m[0] ? hi + kLead : m[0];
+            const float f = fast_exp2(m[0] - to);
+            m[0] = to;
+            l[0] *= f;
+#pragma unroll
+            for (int i = 0; i < kDims; ++i) acc[i] *= f;
+        }
+        const float e = fast_exp2(x - m[0]);
+        l[0] += e;
+#pragma unroll
+        for (int t = 0; t < kBlock; ++t) {
+            const float w = __shfl_sync(0xffffffffu, e, (t & 3) * 8 + (t >> 2));
+            float v[kDims];
+            load_v(v, vp, t, lane);
+            const bool in = sp.sees(tok0 + t);      // a hidden row holds whatever it holds
+#pragma unroll
+            for (int i = 0; i < kDims; ++i) acc[i] = fmaf(w, in ? v[i] : 0.0f, acc[i]);
+        }
+    }
+    static __device__ __forceinline__ void load_v(float (&v)[kDims], uint32_t vp, int t, int lane) {
+        if constexpr (kDims == 4) {
+            const float4 y = lds128(vp + (t * D + 4 * lane) * 4);
+            v[0] = y.x, v[1] = y.y, v[2] = y.z, v[3] = y.w;
+        } else {
+            asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];"
+                         : "=f"(v[0]), "=f"(v[1])
+                         : "r"(vp + (t * D + 2 * lane) * 4)
+                         : "memory");
+        }
     }
     template <bool kWeights>
     __device__ __forceinline__ void page(const Params &p, uint32_t kp, uint32_t vp, const Span &sp,
                                          int tok0, float *logits, float *weights, int lane) {
+        if (p.G == 1) return page1<kWeights>(p, kp, vp, sp, tok0, logits, lane);
         const int j = lane >> 3, r = lane & 7;
         float s[4][8] = {};
 #pragma unroll
@@ -401,15 +479,7 @@ template <int D> struct State<float, D> {
             const float4 a = lds128(w0 + t * 32), b = lds128(w0 + t * 32 + 16);
             const float w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
             float v[kDims];
-            if constexpr (kDims == 4) {
-                const float4 y = lds128(vp + (t * D + 4 * lane) * 4);
-                v[0] = y.x, v[1] = y.y, v[2] = y.z, v[3] = y.w;
-            } else {
-                asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];"
-                             : "=f"(v[0]), "=f"(v[1])
-                             : "r"(vp + (t * D + 2 * lane) * 4)
-                             : "memory");
-            }
+            load_v(v, vp, t, lane);
 #pragma unroll
             for (int h = 0; h < 8; ++h) {
                 if (h >= p.G) break;
@@ -706,6 +776,7 @@ __global__ void __launch_bounds__(32 * kLineWarps, line_ctas<T, D>())
     mbar_fence_init();
     __syncwarp();
     griddep_wait();
+    if (kWeights) griddep_launch_dependents();      // the second kernel waits beside this one
 
     // The line's length, then the segment in which this warp's share begins.
     auto pages_at = [&](int b) { return b < p.B ? static_cast<uint32_t>(span_of(p, b).pages) : 0u; };
@@ -798,73 +869,73 @@ __global__ void __launch_bounds__(32 * kLineWarps, line_ctas<T, D>())
             __syncwarp();
             start();
         }
-        st.sum_up();
+        st.sum_up(p);
         if (ring.dead) {
 #pragma unroll
             for (int k = 0; k < State<T, D>::kHeads; ++k) st.l[k] = NAN;
         }
-        if (at.a == 0 && at.e == sp.pages) {
-            finish<T, D, kWeights>(p, st, at.b, at.hk, lane);
-            continue;
-        }
-        // A part: the last of the segment's warps joins them all.
-        float *part = partial_of(p, D, me, at.a == 0);
+        if (at.a > 0 || at.e < sp.pages) {
+            // A part: the last of the segment's warps joins them all.
+            float *part = partial_of(p, D, me, at.a == 0);
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-            __stcg(reinterpret_cast<float4 *>(part) + 32 * k + lane,
-                   make_float4(st.acc[4 * k], st.acc[4 * k + 1], st.acc[4 * k + 2], st.acc[4 * k + 3]));
-        if (lane < 8) {
+            for (int k = 0; k < D / 16; ++k)
+                __stcg(reinterpret_cast<float4 *>(part) + 32 * k + lane,
+                       make_float4(st.acc[4 * k], st.acc[4 * k + 1], st.acc[4 * k + 2], st.acc[4 * k + 3]));
+            if (lane < 8) {
 #pragma unroll
-            for (int k = 0; k < State<T, D>::kHeads; ++k) {
-                __stcg(part + 8 * D + State<T, D>::head(lane, k), st.m[k]);
-                __stcg(part + 8 * D + 8 + State<T, D>::head(lane, k), st.l[k]);
+                for (int k = 0; k < State<T, D>::kHeads; ++k) {
+                    __stcg(part + 8 * D + State<T, D>::head(lane, k), st.m[k]);
+                    __stcg(part + 8 * D + 8 + State<T, D>::head(lane, k), st.l[k]);
+                }
             }
-        }
-        const int f = static_cast<int>(at.start / share);
-        const int last = static_cast<int>((at.start + sp.pages - 1) / share);
-        __syncwarp();
-        int joins = 0;
-        if (lane == 0 && XS_BOUNDS(f >= 0 && f <= last && last < kMaxWarps, p.err_flag)) {
-            joins = atomic_add_acq_rel_gpu(p.counters + f, 1) == last - f;
-            if (joins) p.counters[f] = 0;
-        }
-        joins = __shfl_sync(0xffffffffu, joins, 0);
-        __syncwarp();
-        if (joins) {
+            const int f = static_cast<int>(at.start / share);
+            const int last = static_cast<int>((at.start + sp.pages - 1) / share);
+            __syncwarp();
+            int joins = 0;
+            if (lane == 0 && XS_BOUNDS(f >= 0 && f <= last && last < kMaxWarps, p.err_flag)) {
+                joins = atomic_add_acq_rel_gpu(p.counters + f, 1) == last - f;
+                if (joins) p.counters[f] = 0;
+            }
+            joins = __shfl_sync(0xffffffffu, joins, 0);
+            __syncwarp();
+            if (!joins) continue;
             join<T, D>(p, st, f, last, lane);
-            finish<T, D, kWeights>(p, st, at.b, at.hk, lane);
         }
+        finish<T, D, kWeights>(p, st, at.b, at.hk, lane);
     } while (at.advance(p, lo, hi));
 }
 
 // ------------------------------------------------------------------ weights from logits
 
-// The weights of tokens [from, to) of a segment, whose logits start at token
-// `base`, added to their scores; ends: the G rows' references and factors.
-template <int G>
-__device__ __forceinline__ void add_weights_of(const Params &p, float *scores, const float *logits, int base,
-                                               int from, int to, int scored, const float2 *ends) {
+// The weights of the tokens at(x), x < count, as far as they are below n, from
+// their G logits each (the place(x)-th ones), added to their scores; ends: the
+// G rows' references and factors.  A thread has kAtOnce tokens under way.
+template <int G, typename F, typename P>
+__device__ __forceinline__ void add_weights(const Params &p, int b, int hk, const float *logits, int count, F &&at,
+                                            P &&place, int n, int scored, const float2 *ends) {
     using V = typename std::conditional<G == 1, float, typename std::conditional<G == 2, float2, float4>::type>::type;
     constexpr int kPieces = G <= 4 ? 1 : 2, kAtOnce = 4;
-    float2 end[G];
-#pragma unroll
-    for (int h = 0; h < G; ++h) end[h] = ends[h];
-    for (int t0 = from + static_cast<int>(threadIdx.x); t0 < to; t0 += kAtOnce * blockDim.x) {
+    if (!XS_BOUNDS(b < p.B && hk < p.Hkv && n <= p.max_blocks * kBlock, p.err_flag)) return;
+    float *scores = p.scores + (static_cast<int64_t>(b) * p.Hkv + hk) * p.max_blocks * kBlock;
+    for (int x0 = threadIdx.x; x0 < count; x0 += kAtOnce * blockDim.x) {
         V x[kAtOnce][kPieces];
         float old[kAtOnce];
 #pragma unroll
         for (int u = 0; u < kAtOnce; ++u) {
-            const int t = t0 + u * blockDim.x;
-            if (t >= to || !XS_BOUNDS(t >= 0 && t < p.max_blocks * kBlock, p.err_flag)) continue;
+            const int y = x0 + u * blockDim.x, t = y < count ? at(y) : n;
+            if (t >= n) continue;
 #pragma unroll
             for (int k = 0; k < kPieces; ++k)
-                x[u][k] = reinterpret_cast<const V *>(logits)[static_cast<int64_t>(t - base) * kPieces + k];
+                x[u][k] = reinterpret_cast<const V *>(logits)[static_cast<int64_t>(place(y)) * kPieces + k];
             old[u] = t < scored ? scores[t] : 0.0f;
         }
+        float2 end[G];
+#pragma unroll
+        for (int h = 0; h < G; ++h) end[h] = ends[h];
 #pragma unroll
         for (int u = 0; u < kAtOnce; ++u) {
-            const int t = t0 + u * blockDim.x;
-            if (t >= to || !XS_BOUNDS(t >= 0 && t < p.max_blocks * kBlock, p.err_flag)) continue;
+            const int y = x0 + u * blockDim.x, t = y < count ? at(y) : n;
+            if (t >= n) continue;
             const float *v = reinterpret_cast<const float *>(x[u]);
             float w = 0.0f;
 #pragma unroll
@@ -873,36 +944,23 @@ __device__ __forceinline__ void add_weights_of(const Params &p, float *scores, c
         }
     }
 }
-__device__ __forceinline__ void add_weights(const Params &p, int b, int hk, const float *logits, int base,
-                                            int from, int to, int scored, const float2 *ends) {
-    if (!XS_BOUNDS(b < p.B && hk < p.Hkv, p.err_flag)) return;
-    float *scores = p.scores + (static_cast<int64_t>(b) * p.Hkv + hk) * p.max_blocks * kBlock;
-    if (p.G == 1)
-        add_weights_of<1>(p, scores, logits, base, from, to, scored, ends);
-    else if (p.G == 2)
-        add_weights_of<2>(p, scores, logits, base, from, to, scored, ends);
-    else if (p.G == 4)
-        add_weights_of<4>(p, scores, logits, base, from, to, scored, ends);
-    else
-        add_weights_of<8>(p, scores, logits, base, from, to, scored, ends);
-}
 
 constexpr int kWeightThreads = 256;
 constexpr int kWeightTokens = 1024;     // of a CTA at a time
 
 // Behind the line: CTAs (segment, y) take every gridDim.y-th piece of kWeightTokens.
+template <int G>
 __global__ void __launch_bounds__(kWeightThreads) bounded_weights_kernel(const __grid_constant__ Params p) {
-    after_previous();
-    __shared__ float2 ends[8];
+    // The lengths may be read at once: the line, which does not write them, lets
+    // this kernel be placed only after everything before it has completed.
     const int b = blockIdx.x / p.Hkv, hk = blockIdx.x - b * p.Hkv;
     const int n = min(XS_BOUNDS(b < p.B, p.err_flag) ? p.lens[b] : 0, p.max_blocks * kBlock);
-    if (n <= static_cast<int>(blockIdx.y) * kWeightTokens) return;
-    if (static_cast<int>(threadIdx.x) < p.G)
-        ends[threadIdx.x] = p.ends[static_cast<int64_t>(b) * p.Hq + hk * p.G + threadIdx.x];
     const int scored = p.scored ? p.scored[b] : n - 1;
-    __syncthreads();
+    after_previous();
     for (int from = blockIdx.y * kWeightTokens; from < n; from += gridDim.y * kWeightTokens)
-        add_weights(p, b, hk, p.logits + logits_at(p, b, hk, 0), 0, from, min(from + kWeightTokens, n), scored, ends);
+        add_weights<G>(
+            p, b, hk, p.logits + logits_at(p, b, hk, from), min(kWeightTokens, n - from),
+            [&](int x) { return from + x; }, [](int x) { return x; }, n, scored, p.ends + static_cast<int64_t>(b) * p.Hq + hk * G);
 }
 
 // ------------------------------------------------------------------ clusters
@@ -964,10 +1022,23 @@ __global__ void __launch_bounds__(32 * kClusterWarps, 1)
     __syncwarp();
     griddep_wait();
 
+    S st;
+    clear(st);
+    st.load_q(p, query_of<T, D>(p, b, hk), lane);
+    // The CTA's pages: every ctas-th group of kClusterWarps without a window, which
+    // are known before the length is, so that their ids come with it; or an equal
+    // run of the window's.
+    const bool all = p.window == 0;
+    const int32_t *row = p.tables + static_cast<int64_t>(b) * p.max_blocks;
+    const int stride = all ? ctas * kClusterWarps : kClusterWarps;
+    int at0 = rank * kClusterWarps + warp;      // this warp's first page, the next `stride` behind
+    int32_t ids = 0;
+    if (all && at0 + lane * stride < p.max_blocks && XS_BOUNDS(b < p.B, p.err_flag))
+        ids = __ldg(row + at0 + lane * stride);
+    const Span sp = span_of(p, b);
     // A length past its table is told of by the first CTA alone: it looks at all.
     if (blockIdx.x == 0)
         for (int i = tid; i < p.B; i += 32 * kClusterWarps) span_of(p, i);
-    const Span sp = span_of(p, b);
     if (sp.pages == 0) {
         if (rank == 0) {
             T *out = static_cast<T *>(out_of<T, D>(p, b, hk));
@@ -975,41 +1046,49 @@ __global__ void __launch_bounds__(32 * kClusterWarps, 1)
         }
         return;         // the whole cluster
     }
-    const int a = static_cast<int>(static_cast<int64_t>(sp.pages) * rank / ctas);
-    const int e = static_cast<int>(static_cast<int64_t>(sp.pages) * (rank + 1) / ctas);
-    const int mine = (e - a - warp + kClusterWarps - 1) / kClusterWarps;    // pages of this warp (or <= 0)
-    int32_t ids = load_ids(p, b, sp, a + warp + lane * kClusterWarps);      // (those past e are not used)
-    S st;
-    clear(st);
-    st.load_q(p, query_of<T, D>(p, b, hk), lane);
+    int end = sp.pages;
+    if (!all) {
+        at0 = static_cast<int>(static_cast<int64_t>(sp.pages) * rank / ctas) + warp;
+        end = static_cast<int>(static_cast<int64_t>(sp.pages) * (rank + 1) / ctas);
+        ids = load_ids(p, b, sp, at0 + lane * stride);      // (those past `end` are not used)
+    } else if (at0 + lane * stride < sp.pages) {
+        if (ids < 0 || ids >= p.num_blocks) {
+            raise_flag(p.err_flag, XS_FLAG_BAD_BLOCK);
+            ids = 0;
+        }
+    }
+    const int mine = (end - at0 + stride - 1) / stride;     // pages of this warp (or <= 0)
     int issued = 0;
     auto start = [&]() {
         if (issued >= mine) return;
-        if (issued && (issued & 31) == 0) ids = load_ids(p, b, sp, a + warp + (issued + lane) * kClusterWarps);
+        if (issued && (issued & 31) == 0) ids = load_ids(p, b, sp, at0 + (issued + lane) * stride);
         ring.start(p, &tmk, &tmv, __shfl_sync(0xffffffffu, ids, issued & 31), hk, lane);
         ++issued;
     };
 #pragma unroll 1
     for (int k = 0; k < kStages; ++k) start();
-    // The CTA's logits, from token 16 a on (with weights every page is seen).
+    // The CTA's logits, of `groups` groups of pages: together in shared memory, or
+    // by their tokens in the workspace.
+    constexpr int kGroup = kClusterWarps * kBlock;      // tokens
+    const int groups = kWeights ? (sp.pages - rank * kClusterWarps + stride - 1) / stride : 0;      // (or <= 0)
+    const bool held = kWeights && groups * kGroup * p.G <= kLogitFloats;
     float *logits = nullptr;
-    if (kWeights) {
-        const bool fits = (e - a) * kBlock * p.G <= kLogitFloats;
-        logits = fits ? sm.logits : p.logits + logits_at(p, b, hk, a * kBlock);
-    }
+    if (kWeights) logits = held ? sm.logits : p.logits + logits_at(p, b, hk, 0);
 #pragma unroll 1
     for (int k = 0; k < mine && !ring.dead; ++k) {
         const uint32_t kp = ring.next(p, lane);
         if (!kp) break;
-        const int i = warp + k * kClusterWarps;
-        st.template page<kWeights>(p, kp, kp + ring.kBytes / 2, sp, sp.page(a + i) * kBlock,
-                                   kWeights ? logits + i * kBlock * p.G : nullptr,
+        const int tok0 = sp.page(at0 + k * stride) * kBlock;
+        float *to = nullptr;
+        if (kWeights && XS_BOUNDS(tok0 + kBlock <= p.max_blocks * kBlock, p.err_flag))
+            to = logits + static_cast<int64_t>(held ? (k * kClusterWarps + warp) * kBlock : tok0) * p.G;
+        st.template page<kWeights>(p, kp, kp + ring.kBytes / 2, sp, tok0, to,
                                    sm.weights[sizeof(T) == 4 ? warp : 0], lane);
         ++ring.taken;
         __syncwarp();
         start();
     }
-    st.sum_up();
+    st.sum_up(p);
     if (ring.dead) {
 #pragma unroll
         for (int k = 0; k < S::kHeads; ++k) st.l[k] = NAN;
@@ -1102,8 +1181,12 @@ __global__ void __launch_bounds__(32 * kClusterWarps, 1)
     // been used above).
     asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
     if (kWeights)
-        add_weights(p, b, hk, logits, a * kBlock, a * kBlock, min(e * kBlock, sp.n),
-                    p.scored ? p.scored[b] : sp.n - 1, sm.ends);
+        by_heads(p.G, [&](auto heads) {
+            auto token = [&](int x) { return (x / kGroup * ctas + rank) * kGroup + x % kGroup; };
+            add_weights<decltype(heads)::value>(
+                p, b, hk, logits, groups * kGroup, token, [&](int x) { return held ? x : token(x); }, sp.n,
+                p.scored ? p.scored[b] : sp.n - 1, sm.ends);
+        });
     asm volatile("barrier.cluster.wait;" ::: "memory");
 }
 
@@ -1188,7 +1271,11 @@ template <typename T, int D, bool kWeights> int launch(const Params &p, int dev,
                       32 * kLineWarps, 1024 + sizeof(LineSmem<T, D>), stream, 1, tmk, tmv, p);
     if (!kWeights || rc != XS_OK) return rc;
     const int pieces = min((p.max_blocks * kBlock + kWeightTokens - 1) / kWeightTokens, 8);
-    return launch_after(bounded_weights_kernel, dim3(static_cast<int>(segments), pieces), kWeightThreads, 0, stream, 1, p);
+    const auto second = p.G == 1   ? bounded_weights_kernel<1>
+                        : p.G == 2 ? bounded_weights_kernel<2>
+                        : p.G == 4 ? bounded_weights_kernel<4>
+                                   : bounded_weights_kernel<8>;
+    return launch_after(second, dim3(static_cast<int>(segments), pieces), kWeightThreads, 0, stream, 1, p);
 }
 
 constexpr size_t kCounterBytes = kMaxWarps * sizeof(int);

@@ -979,7 +979,7 @@ int xs_block_copy(void *k_pools, void *v_pools, int layers, int64_t layer_stride
  * leaves it fit for the next.  Calls that share one must be ordered (one stream,
  * or one CUDA graph).
  * dtype XS_BF16 or XS_F32; block_size 16; D in {64, 128}; Hq / Hkv in {1, 2, 4,
- * 8}; num_blocks * Hkv < 2^31.
+ * 8}; Hkv <= 512; num_blocks * Hkv < 2^31.  out overlaps nothing else.
  * Device-side errors: XS_FLAG_BAD_BLOCK (block 0 was read instead),
  * XS_FLAG_BAD_LEN (the length was clamped to the table), XS_FLAG_TIMEOUT (a
  * page did not arrive within 4 s: the outputs of the sequence and KV head it
@@ -999,6 +999,8 @@ int xs_paged_decode_first(void *out, const void *q, int64_t q_stride, const void
  * prefill_tc in which the query at position p sees the keys t <= p with t < first
  * or t > p - window (window 0: every t <= p).  block_ids entries of pages that no
  * query of the chunk sees are never read.  bf16 only; scale > 0.
+ * Weights enter the product with V as bf16, as there (the output is off by 0.0024
+ * of its size where its own rounding leaves 0.0017).
  * Rows that no query of the chunk sees have no influence.  An infinity or a NaN
  * in a V row that some of 256 Hkv / Hq neighbouring queries see and others do not
  * may reach the outputs of all of them (as in xs_paged_prefill_tc).
@@ -1065,8 +1067,8 @@ int xs_paged_decode_weights(void *out, float *scores, const int32_t *scored_lens
  * or one that an earlier entry has (XS_FLAG_BAD_SLOT), and a sequence with a table
  * entry outside the pool behind the first tokens' whole pages (XS_FLAG_BAD_BLOCK).
  * A length beyond the table counts as the table's (XS_FLAG_BAD_LEN).
- * first, recent >= 0, first + recent <= budget <= limit, budget > 0; D in {64,
- * 128}; block_size 16.
+ * first, recent >= 0, first + recent <= budget <= limit, budget > 0, layers > 0; D
+ * in {64, 128}; block_size 16.
  */
 int xs_kv_evict(const int32_t *seq_ids, int n, void *k_pools, void *v_pools, int layers,
                 int64_t layer_stride_bytes, float *scores, const int32_t *block_tables,

@@ -630,7 +630,7 @@ PyObject *kv_evict(Args a) {
     const int32_t *ep = static_cast<int32_t *>(whole(extra, "extra_refs"));
     int32_t *at = static_cast<int32_t *>(whole(kept, "kept")), *np = static_cast<int32_t *>(whole(new_lens, "new_lens"));
     int *flag = static_cast<int *>(whole(err, "err_flag"));
-    if (n == 0 || L == 0) return PyLong_FromLong(XS_OK);
+    if (n == 0) return PyLong_FromLong(XS_OK);
     return status([&] {
         return reinterpret_cast<decltype(&xs_kv_evict)>(entry)(
             ip, count, kp, vp, layers, nb * hkv * kPage * d * k.element_size(), sp, tp, width, lp, b, ep, first,

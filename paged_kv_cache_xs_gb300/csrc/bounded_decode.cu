@@ -25,23 +25,36 @@
 // fragments' loads free of bank conflicts) that its lanes start ahead; a page
 // is waited for, read and given back with no barrier but the warp's own.
 //
-// Split.  Many segments (sequence, KV head): the pages of all segments form one
-// line, each segment with kSegmentCost more for its end, and the line is cut
-// into equal shares, one for each warp of the grid.  A warp finds its place
-// from the lengths themselves, so the host needs to know none of them and a
-// captured call follows them; its copies run on across the ends of segments.
-// A segment that one warp does is written at once; one that is cut leaves fp32
-// partials in the workspace, at most two for each warp, and the warp that
-// finishes it last joins them in order: the result does not depend on which
-// that is.  Few segments: a thread-block cluster for each, whose warps' states
-// meet in shared memory.
+// Split, over segments (sequence, KV head):
+//  - few: a thread-block cluster of 2, 4 or 8 CTAs for each, whose warps' states
+//    meet in shared memory;
+//  - more: a CTA for each, of 8 warps where the device holds all at once and tables
+//    are short, else of 4 warps, two on an SM, whose starts and ends hide behind
+//    one another's pages;
+//  - many of unlike lengths: the pages of all sequences form one line, each
+//    sequence with kSegmentCost more for its end, and the line is cut into equal
+//    shares, one for each group of Hkv warps of the grid, a warp for each KV head
+//    (so that a block's pages are read at about one time).  Copies run on across
+//    the ends of sequences.  A segment that one warp does is written at once; one
+//    that is cut leaves fp32 partials in the workspace, at most two for each warp,
+//    and the warp that finishes it last joins them in order: the result does not
+//    depend on which that is.
+// The lengths, on the device, decide between the last two, and where a warp works,
+// so the host needs to know none of them and a captured call follows them.
 //
 // Weights.  p_ht needs the final maximum and sum of its row, which no warp
 // knows while it has the logit.  So logits are kept, 4 bytes for a token and
-// head beside 4 D bytes of bf16 K and V for a token and KV head: a cluster
-// keeps them in shared memory (or, beyond its room, in the workspace) and
-// turns them into weights itself; the line leaves them in the workspace, most
-// of it in L2, for a second kernel.
+// head beside 4 D bytes of bf16 K and V for a token and KV head.  A CTA or cluster
+// with a whole segment keeps them in shared memory (or, beyond its room, in the
+// workspace) and turns them into weights itself; the line leaves them in the
+// workspace, most of it in L2, for a second kernel.  (The warp that ends a segment
+// doing that took 4 us more for 64 sequences of 17 to 8193 tokens than the kernel.)
+//
+// What bounds it: DRAM where there is enough of it (bf16, 32q/8kv x 128: 128 sequences
+// that see 4112 tokens each 307 us, 7.0 TB/s of 6.8 measured for a copy; 128 of 2049
+// to 4097 with weights 279 us, of which the logits' footprint in L2 takes 20 and
+// the scores 10), and the chain length - ids - page - join where there is not (one
+// sequence: 5.0 us up to 1K tokens, 7.1 at 4K, 8.1 with weights).
 #include <atomic>
 #include <type_traits>
 
@@ -60,9 +73,18 @@ constexpr int kClusterWarps = 8;    // of a cluster's CTA, one on an SM
 constexpr int kMaxWarps = 1280;     // the workspace holds partials for so many
 constexpr int kSegmentCost = 6;     // pages (4: many short segments 8% faster, few long ones 4% slower; 8: the reverse)
 constexpr int kMinShare = 4;        // pages
-constexpr int kWholePages = 8;      // segments up to so many pages are not cut
-constexpr int kMaxCluster = 16;
-constexpr int kLogitFloats = 6144;  // of a cluster's CTA, in shared memory
+constexpr int kShortTable = 128;    // pages
+constexpr int kScannedB = 256;      // sequences whose lengths a CTA for each segment may look at
+// Segments of up to so many pages are not cut (61 x 12 of 7 pages: 9.1 us so, 10.1 cut;
+// 61 x 12 of up to 64: 11.7 us, 12.8 with 16).
+constexpr int kWholePages = 8;
+constexpr int kMaxCluster = 8;
+// For the choice between the two forms of many segments, in units of a page at the
+// device's full rate (1.1 ns for 8 KB of K and V): what a page takes a CTA of
+// kLineWarps that has the device for itself, and a CTA's start and end.
+template <typename T, int D> constexpr int64_t kAlone = kBlock * D * sizeof(T) < 4096 ? 200 : 100;
+template <typename T, int D> constexpr int64_t kEnds = 2600 * 4096 / (kBlock * D * static_cast<int>(sizeof(T)));
+__host__ __device__ constexpr int logit_floats(int warps) { return warps == 8 ? 6144 : 2048; }   // in shared memory
 constexpr float kLead = 8.0f;       // of a reference before the largest logit
 constexpr float kLowest = -3.402823466e38f;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -109,6 +131,7 @@ struct Params {
     const int32_t *scored;  // [B] or null: n - 1
     float *logits;      // [B, Hkv, max_blocks * 16, G], in powers of two
     float2 *ends;       // [B, Hq]: a row's reference and the reciprocal of its sum
+    int *by_segment;    // how the call went (the second kernel has work behind the line alone)
 };
 
 // f(integral_constant<int, G>) for G in {1, 2, 4, 8}.
@@ -554,6 +577,14 @@ template <typename T, int D, int kStages> struct Ring {
     uint32_t issued = 0, taken = 0;
     bool dead = false;      // a wait ran out: nothing more is started, and all that follows is NaN
 
+    __device__ __forceinline__ void init(const void *places, uint64_t *full) {
+        at = smem_addr(places), bars = smem_addr(full);
+        const int lane = threadIdx.x & 31;
+        if (lane < kStages) mbar_init(full + lane, 1);
+        mbar_fence_init();
+        __syncwarp();
+    }
+
     __device__ __forceinline__ void start(const Params &p, const CUtensorMap *tmk, const CUtensorMap *tmv,
                                           int32_t id, int hk, int lane) {
         const uint32_t st = issued % kStages;
@@ -622,10 +653,10 @@ __device__ __forceinline__ int64_t logits_at(const Params &p, int b, int hk, int
 
 // ------------------------------------------------------------------ the line
 
-// A warp's place on the line: segment (b, hk), which starts at `start`, and the
-// warp's pages [a, e) of it.
+// A warp's place on the line: sequence b, which starts at `start`, and the warp's
+// pages [a, e) of it.
 struct Cursor {
-    int b, hk, a, e;
+    int b, a, e;
     int64_t start;
     Span sp;
     __device__ __forceinline__ void settle(const Params &p, int64_t lo, int64_t hi) {
@@ -634,11 +665,11 @@ struct Cursor {
         e = static_cast<int>(min(hi - start, static_cast<int64_t>(sp.pages)));
         if (sp.pages <= kWholePages) a = 0, e = start >= lo ? sp.pages : 0;
     }
-    // To the next segment; false at the end of the warp's share.
+    // To the next sequence; false at the end of the warp's share.
     __device__ __forceinline__ bool advance(const Params &p, int64_t lo, int64_t hi) {
         start += sp.pages + kSegmentCost;
         if (start >= hi) return false;
-        if (++hk == p.Hkv) hk = 0, ++b;
+        ++b;
         settle(p, lo, hi);
         return true;
     }
@@ -674,11 +705,11 @@ __device__ __forceinline__ void finish(const Params &p, State<T, D> &st, int b, 
     if (XS_BOUNDS(b < p.B && hk < p.Hkv, p.err_flag)) st.write(p, out_of<T, D>(p, b, hk), f, lane);
 }
 
-// Joins the partials that warps f .. last left of a segment, in order: warp f
-// its second, the others their first.  kAtOnce are on their way at a time (an
+// Joins the partials that KV head hk's warps of groups f .. last left of a segment,
+// in order: that of group f its second, the others their first.  kAtOnce are on their way at a time (an
 // access to another SM's fresh results takes about 1 us).
 template <typename T, int D>
-__device__ __forceinline__ void join(const Params &p, State<T, D> &st, int f, int last, int lane) {
+__device__ __forceinline__ void join(const Params &p, State<T, D> &st, int hk, int f, int last, int lane) {
     using S = State<T, D>;
     constexpr int kAtOnce = 4;
     clear(st);
@@ -688,7 +719,8 @@ __device__ __forceinline__ void join(const Params &p, State<T, D> &st, int f, in
 #pragma unroll
         for (int u = 0; u < kAtOnce; ++u) {
             const bool in = base + u <= last;
-            const float *src = partial_of(p, D, in ? base + u : last, (in ? base + u : last) == f);
+            const int group = in ? base + u : last;
+            const float *src = partial_of(p, D, static_cast<int64_t>(group) * p.Hkv + hk, group == f);
 #pragma unroll
             for (int k = 0; k < S::kHeads; ++k) {
                 m[u][k] = __ldcg(src + 8 * D + S::head(lane, k));
@@ -738,11 +770,7 @@ __device__ __forceinline__ void join(const Params &p, State<T, D> &st, int f, in
     }
 }
 
-template <typename T, int D> struct alignas(1024) LineSmem {
-    uint8_t ring[kLineWarps][line_stages<T, D>()][2 * kBlock * D * sizeof(T)];
-    float weights[sizeof(T) == 4 ? kLineWarps : 1][kBlock * 8];
-    uint64_t full[kLineWarps][line_stages<T, D>()];
-};
+// CTAs of the line on an SM (fp32 pages of 128 fill it with one's ring).
 template <typename T, int D> __host__ __device__ constexpr int line_ctas() {
     return sizeof(T) == 4 && D == 128 ? 1 : 2;
 }
@@ -760,149 +788,6 @@ template <typename S> __device__ __forceinline__ S &shared_of() {
     extern __shared__ __align__(1024) unsigned char bounded_smem[];
     // (The start of the dynamic shared memory need not be a multiple of 1024.)
     return *reinterpret_cast<S *>(bounded_smem + (-smem_addr(bounded_smem) & 1023u));
-}
-
-template <typename T, int D, bool kWeights>
-__global__ void __launch_bounds__(32 * kLineWarps, line_ctas<T, D>())
-    bounded_line_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
-                        const __grid_constant__ Params p) {
-    constexpr int kStages = line_stages<T, D>();
-    LineSmem<T, D> &sm = shared_of<LineSmem<T, D>>();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int me = blockIdx.x * kLineWarps + warp, warps = gridDim.x * kLineWarps;
-    Ring<T, D, kStages> ring;
-    ring.at = smem_addr(sm.ring[warp]), ring.bars = smem_addr(sm.full[warp]);
-    if (lane < kStages) mbar_init(&sm.full[warp][lane], 1);
-    mbar_fence_init();
-    __syncwarp();
-    griddep_wait();
-    if (kWeights) griddep_launch_dependents();      // the second kernel waits beside this one
-
-    // The line's length, then the segment in which this warp's share begins.
-    auto pages_at = [&](int b) { return b < p.B ? static_cast<uint32_t>(span_of(p, b).pages) : 0u; };
-    uint32_t pages0[4];
-    int64_t total = 0;
-#pragma unroll
-    for (int u = 0; u < 4; ++u) pages0[u] = pages_at(32 * u + lane);
-#pragma unroll
-    for (int u = 0; u < 4; ++u) total += __reduce_add_sync(0xffffffffu, pages0[u]);
-#pragma unroll 4
-    for (int base = 128; base < p.B; base += 32) total += __reduce_add_sync(0xffffffffu, pages_at(base + lane));
-    const int64_t line = (total + static_cast<int64_t>(p.B) * kSegmentCost) * p.Hkv;
-    const int64_t share = max((line + warps - 1) / warps, static_cast<int64_t>(kMinShare));
-    const int64_t lo = share * me, hi = min(lo + share, line);
-    if (lo >= line) return;
-    Cursor at;
-    {
-        int64_t before = 0;
-        bool found = false;
-        auto look = [&](int base, uint32_t pages) {     // among sequences base .. base + 31
-            const uint32_t units = base + lane < p.B ? pages + kSegmentCost : 0;
-            const uint32_t sum = warp_scan(units);
-            const int64_t end = (before + sum) * p.Hkv, s = end - static_cast<int64_t>(units) * p.Hkv;
-            before += __shfl_sync(0xffffffffu, sum, 31);
-            const uint32_t who = __ballot_sync(0xffffffffu, lo >= s && lo < end);
-            if (!who) return;
-            found = true;
-            const int src = __ffs(who) - 1;
-            const int64_t s0 = __shfl_sync(0xffffffffu, s, src);
-            const int n = __shfl_sync(0xffffffffu, units, src);
-            at.b = base + src;
-            at.hk = static_cast<int>((lo - s0) / n);
-            at.start = s0 + static_cast<int64_t>(at.hk) * n;
-        };
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-            if (!found && 32 * u < p.B) look(32 * u, pages0[u]);
-        for (int base = 128; !found && base < p.B; base += 32) look(base, pages_at(base + lane));
-        if (!found) return;
-    }
-    at.settle(p, lo, hi);
-
-    // Copies run ahead of the work, across the ends of segments.
-    Cursor ahead = at;
-    int next = ahead.a, chunk = next;
-    bool more = true;
-    int32_t ids = load_ids(p, ahead.b, ahead.sp, chunk + lane);
-    auto start = [&]() {
-        while (more && next >= ahead.e) {
-            more = ahead.advance(p, lo, hi);
-            if (!more) return;
-            next = chunk = ahead.a;
-            if (next < ahead.e) ids = load_ids(p, ahead.b, ahead.sp, chunk + lane);
-        }
-        if (!more) return;
-        if (next - chunk == 32) {
-            chunk = next;
-            ids = load_ids(p, ahead.b, ahead.sp, chunk + lane);
-        }
-        ring.start(p, &tmk, &tmv, __shfl_sync(0xffffffffu, ids, next - chunk), ahead.hk, lane);
-        ++next;
-    };
-#pragma unroll 1
-    for (int k = 0; k < kStages; ++k) start();
-
-    State<T, D> st;
-    do {
-        const Span &sp = at.sp;
-        if (sp.pages == 0) {
-            if (at.start >= lo && XS_BOUNDS(at.b < p.B && at.hk < p.Hkv, p.err_flag)) {
-                T *out = static_cast<T *>(out_of<T, D>(p, at.b, at.hk));
-                for (int x = lane; x < p.G * D; x += 32) out[x] = Elem<T>::from_f32(0.0f);
-            }
-            continue;
-        }
-        if (at.a >= at.e) continue;
-        clear(st);
-        st.load_q(p, query_of<T, D>(p, at.b, at.hk), lane);
-#pragma unroll 1
-        for (int k = at.a; k < at.e && !ring.dead; ++k) {
-            const uint32_t kp = ring.next(p, lane);
-            if (!kp) break;
-            const int tok0 = sp.page(k) * kBlock;
-            float *logits = nullptr;
-            if (kWeights && XS_BOUNDS(tok0 + kBlock <= p.max_blocks * kBlock, p.err_flag))
-                logits = p.logits + logits_at(p, at.b, at.hk, tok0);
-            st.template page<kWeights>(p, kp, kp + ring.kBytes / 2, sp, tok0, logits,
-                                       sm.weights[sizeof(T) == 4 ? warp : 0], lane);
-            ++ring.taken;
-            __syncwarp();
-            start();
-        }
-        st.sum_up(p);
-        if (ring.dead) {
-#pragma unroll
-            for (int k = 0; k < State<T, D>::kHeads; ++k) st.l[k] = NAN;
-        }
-        if (at.a > 0 || at.e < sp.pages) {
-            // A part: the last of the segment's warps joins them all.
-            float *part = partial_of(p, D, me, at.a == 0);
-#pragma unroll
-            for (int k = 0; k < D / 16; ++k)
-                __stcg(reinterpret_cast<float4 *>(part) + 32 * k + lane,
-                       make_float4(st.acc[4 * k], st.acc[4 * k + 1], st.acc[4 * k + 2], st.acc[4 * k + 3]));
-            if (lane < 8) {
-#pragma unroll
-                for (int k = 0; k < State<T, D>::kHeads; ++k) {
-                    __stcg(part + 8 * D + State<T, D>::head(lane, k), st.m[k]);
-                    __stcg(part + 8 * D + 8 + State<T, D>::head(lane, k), st.l[k]);
-                }
-            }
-            const int f = static_cast<int>(at.start / share);
-            const int last = static_cast<int>((at.start + sp.pages - 1) / share);
-            __syncwarp();
-            int joins = 0;
-            if (lane == 0 && XS_BOUNDS(f >= 0 && f <= last && last < kMaxWarps, p.err_flag)) {
-                joins = atomic_add_acq_rel_gpu(p.counters + f, 1) == last - f;
-                if (joins) p.counters[f] = 0;
-            }
-            joins = __shfl_sync(0xffffffffu, joins, 0);
-            __syncwarp();
-            if (!joins) continue;
-            join<T, D>(p, st, f, last, lane);
-        }
-        finish<T, D, kWeights>(p, st, at.b, at.hk, lane);
-    } while (at.advance(p, lo, hi));
 }
 
 // ------------------------------------------------------------------ weights from logits
@@ -948,7 +833,7 @@ __device__ __forceinline__ void add_weights(const Params &p, int b, int hk, cons
 constexpr int kWeightThreads = 256;
 constexpr int kWeightTokens = 1024;     // of a CTA at a time
 
-// Behind the line: CTAs (segment, y) take every gridDim.y-th piece of kWeightTokens.
+// Behind the line (nothing where it went by segments): CTAs (segment, y) take every gridDim.y-th piece of kWeightTokens.
 template <int G>
 __global__ void __launch_bounds__(kWeightThreads) bounded_weights_kernel(const __grid_constant__ Params p) {
     // The lengths may be read at once: the line, which does not write them, lets
@@ -957,31 +842,40 @@ __global__ void __launch_bounds__(kWeightThreads) bounded_weights_kernel(const _
     const int n = min(XS_BOUNDS(b < p.B, p.err_flag) ? p.lens[b] : 0, p.max_blocks * kBlock);
     const int scored = p.scored ? p.scored[b] : n - 1;
     after_previous();
+    if (__ldcg(p.by_segment)) return;
     for (int from = blockIdx.y * kWeightTokens; from < n; from += gridDim.y * kWeightTokens)
         add_weights<G>(
             p, b, hk, p.logits + logits_at(p, b, hk, from), min(kWeightTokens, n - from),
             [&](int x) { return from + x; }, [](int x) { return x; }, n, scored, p.ends + static_cast<int64_t>(b) * p.Hq + hk * G);
 }
 
-// ------------------------------------------------------------------ clusters
+// ------------------------------------------------------------------ a CTA's work on a segment
 
-template <typename T, int D> struct alignas(1024) ClusterSmem {
+template <typename T, int D, int W, int S> struct alignas(1024) CtaSmem {
     // The pages on their way; when all have been read, the warps' values meet there.
     union {
-        uint8_t ring[kClusterWarps][cluster_stages<T, D>()][2 * kBlock * D * sizeof(T)];
-        float4 o[kClusterWarps][8 * D / 4];
+        uint8_t ring[W][S][2 * kBlock * D * sizeof(T)];
+        float4 o[W][8 * D / 4];
     };
-    float weights[sizeof(T) == 4 ? kClusterWarps : 1][kBlock * 8];
+    float weights[sizeof(T) == 4 ? W : 1][kBlock * 8];
     float4 part[8 * D / 4];             // what the CTA has
     float m[8], l[8];
-    float warp_m[kClusterWarps][8], warp_l[kClusterWarps][8], warp_w[kClusterWarps][8];
+    float warp_m[W][8], warp_l[W][8], warp_w[W][8];
     float rank_w[kMaxCluster][8];       // factors of the CTAs' values
     float2 ends[8];
-    uint64_t full[kClusterWarps][cluster_stages<T, D>()];
-    alignas(16) float logits[kLogitFloats];     // (the form with weights has them)
+    uint64_t full[W][S];
+    alignas(16) float logits[logit_floats(W)];      // (the form with weights has them)
 };
+template <typename T, int D> using ClusterSmem = CtaSmem<T, D, kClusterWarps, cluster_stages<T, D>()>;
+template <typename T, int D> using LineSmem = CtaSmem<T, D, kLineWarps, line_stages<T, D>()>;
+// (The start of the dynamic shared memory need not be a multiple of 1024.)
 template <typename T, int D> constexpr int cluster_smem(bool weights) {
-    return 1024 + static_cast<int>(sizeof(ClusterSmem<T, D>)) - (weights ? 0 : static_cast<int>(kLogitFloats * sizeof(float)));
+    return 1024 + static_cast<int>(sizeof(ClusterSmem<T, D>)) -
+           (weights ? 0 : static_cast<int>(logit_floats(kClusterWarps) * sizeof(float)));
+}
+template <typename T, int D> constexpr int line_smem(bool weights) {
+    return 1024 + static_cast<int>(sizeof(LineSmem<T, D>)) -
+           (weights ? 0 : static_cast<int>(logit_floats(kLineWarps) * sizeof(float)));
 }
 
 __device__ __forceinline__ uint32_t peer_addr(const void *own, int rank) {
@@ -1003,136 +897,373 @@ __device__ __forceinline__ float4 peer_f32x4(uint32_t a) {
     return v;
 }
 
-// A cluster of `ctas` (a power of two) for each segment.
-template <typename T, int D, bool kWeights>
-__global__ void __launch_bounds__(32 * kClusterWarps, 1)
-    bounded_cluster_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
-                           const __grid_constant__ Params p, const int ctas) {
+// Segment (b, hk), or CTA `rank`'s part of it where `ctas` share it, by a CTA of W warps.
+template <typename T, int D, bool kWeights, int W, int kStages> struct Segment {
     using S = State<T, D>;
-    constexpr int kStages = cluster_stages<T, D>();
-    constexpr int kChunks = 8 * D / 4;
-    ClusterSmem<T, D> &sm = shared_of<ClusterSmem<T, D>>();
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int rank = blockIdx.x % ctas, segment = blockIdx.x / ctas;
-    const int b = segment / p.Hkv, hk = segment - b * p.Hkv;
-    Ring<T, D, kStages> ring;
-    ring.at = smem_addr(sm.ring[warp]), ring.bars = smem_addr(sm.full[warp]);
-    if (lane < kStages) mbar_init(&sm.full[warp][lane], 1);
-    mbar_fence_init();
-    __syncwarp();
-    griddep_wait();
+    static constexpr int kGroup = W * kBlock;       // tokens
+    static constexpr int kChunks = 8 * D / 4;
+    const Params &p;
+    CtaSmem<T, D, W, kStages> &sm;
+    const int b, hk, rank, ctas;
+    Span sp;
+    int groups;
+    bool held;
+    float *logits;
 
-    S st;
-    clear(st);
-    st.load_q(p, query_of<T, D>(p, b, hk), lane);
-    // The CTA's pages: every ctas-th group of kClusterWarps without a window, which
-    // are known before the length is, so that their ids come with it; or an equal
-    // run of the window's.
-    const bool all = p.window == 0;
-    const int32_t *row = p.tables + static_cast<int64_t>(b) * p.max_blocks;
-    const int stride = all ? ctas * kClusterWarps : kClusterWarps;
-    int at0 = rank * kClusterWarps + warp;      // this warp's first page, the next `stride` behind
-    int32_t ids = 0;
-    if (all && at0 + lane * stride < p.max_blocks && XS_BOUNDS(b < p.B, p.err_flag))
-        ids = __ldg(row + at0 + lane * stride);
-    const Span sp = span_of(p, b);
-    // A length past its table is told of by the first CTA alone: it looks at all.
-    if (blockIdx.x == 0)
-        for (int i = tid; i < p.B; i += 32 * kClusterWarps) span_of(p, i);
-    if (sp.pages == 0) {
-        if (rank == 0) {
-            T *out = static_cast<T *>(out_of<T, D>(p, b, hk));
-            for (int x = tid; x < p.G * D; x += 32 * kClusterWarps) out[x] = Elem<T>::from_f32(0.0f);
+    // The CTA's pages; what its warps have of them is left in shared memory.  False
+    // if the segment is empty (then its output is written).
+    __device__ __forceinline__ bool pages(Ring<T, D, kStages> &ring, const CUtensorMap *tmk, const CUtensorMap *tmv,
+                                          bool tells) {
+        const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+        S st;
+        clear(st);
+        st.load_q(p, query_of<T, D>(p, b, hk), lane);
+        // The CTA's pages: every ctas-th group of W without a window, which are
+        // known before the length is, so that their ids come with it; or an equal run
+        // of the window's.
+        const bool all = p.window == 0;
+        const int32_t *row = p.tables + static_cast<int64_t>(b) * p.max_blocks;
+        const int stride = all ? ctas * W : W;
+        int at0 = rank * W + warp;      // this warp's first page, the next `stride` behind
+        int32_t ids = 0;
+        if (all && at0 + lane * stride < p.max_blocks && XS_BOUNDS(b < p.B, p.err_flag))
+            ids = __ldg(row + at0 + lane * stride);
+        sp = span_of(p, b);
+        // A length past its table is told of by the first CTA alone: it looks at all.
+        if (tells)
+            for (int i = tid; i < p.B; i += 32 * W) span_of(p, i);
+        if (sp.pages == 0) {
+            if (rank == 0) {
+                T *out = static_cast<T *>(out_of<T, D>(p, b, hk));
+                for (int x = tid; x < p.G * D; x += 32 * W) out[x] = Elem<T>::from_f32(0.0f);
+            }
+            return false;       // the whole cluster
         }
-        return;         // the whole cluster
-    }
-    int end = sp.pages;
-    if (!all) {
-        at0 = static_cast<int>(static_cast<int64_t>(sp.pages) * rank / ctas) + warp;
-        end = static_cast<int>(static_cast<int64_t>(sp.pages) * (rank + 1) / ctas);
-        ids = load_ids(p, b, sp, at0 + lane * stride);      // (those past `end` are not used)
-    } else if (at0 + lane * stride < sp.pages) {
-        if (ids < 0 || ids >= p.num_blocks) {
-            raise_flag(p.err_flag, XS_FLAG_BAD_BLOCK);
-            ids = 0;
+        int end = sp.pages;
+        if (!all) {
+            at0 = static_cast<int>(static_cast<int64_t>(sp.pages) * rank / ctas) + warp;
+            end = static_cast<int>(static_cast<int64_t>(sp.pages) * (rank + 1) / ctas);
+            ids = load_ids(p, b, sp, at0 + lane * stride);      // (those past `end` are not used)
+        } else if (at0 + lane * stride < sp.pages) {
+            if (ids < 0 || ids >= p.num_blocks) {
+                raise_flag(p.err_flag, XS_FLAG_BAD_BLOCK);
+                ids = 0;
+            }
         }
-    }
-    const int mine = (end - at0 + stride - 1) / stride;     // pages of this warp (or <= 0)
-    int issued = 0;
-    auto start = [&]() {
-        if (issued >= mine) return;
-        if (issued && (issued & 31) == 0) ids = load_ids(p, b, sp, at0 + (issued + lane) * stride);
-        ring.start(p, &tmk, &tmv, __shfl_sync(0xffffffffu, ids, issued & 31), hk, lane);
-        ++issued;
-    };
+        const int mine = (end - at0 + stride - 1) / stride;     // pages of this warp (or <= 0)
+        int issued = 0;
+        auto start = [&]() {
+            if (issued >= mine || ring.dead) return;
+            if (issued && (issued & 31) == 0) ids = load_ids(p, b, sp, at0 + (issued + lane) * stride);
+            ring.start(p, tmk, tmv, __shfl_sync(0xffffffffu, ids, issued & 31), hk, lane);
+            ++issued;
+        };
 #pragma unroll 1
-    for (int k = 0; k < kStages; ++k) start();
-    // The CTA's logits, of `groups` groups of pages: together in shared memory, or
-    // by their tokens in the workspace.
-    constexpr int kGroup = kClusterWarps * kBlock;      // tokens
-    const int groups = kWeights ? (sp.pages - rank * kClusterWarps + stride - 1) / stride : 0;      // (or <= 0)
-    const bool held = kWeights && groups * kGroup * p.G <= kLogitFloats;
-    float *logits = nullptr;
-    if (kWeights) logits = held ? sm.logits : p.logits + logits_at(p, b, hk, 0);
+        for (int k = 0; k < kStages; ++k) start();
+        // The CTA's logits, of `groups` groups of pages: together in shared memory, or
+        // by their tokens in the workspace.
+        groups = kWeights ? (sp.pages - rank * W + stride - 1) / stride : 0;      // (or <= 0)
+        held = kWeights && groups * kGroup * p.G <= logit_floats(W);
+        if (kWeights) logits = held ? sm.logits : p.logits + logits_at(p, b, hk, 0);
 #pragma unroll 1
-    for (int k = 0; k < mine && !ring.dead; ++k) {
-        const uint32_t kp = ring.next(p, lane);
-        if (!kp) break;
-        const int tok0 = sp.page(at0 + k * stride) * kBlock;
-        float *to = nullptr;
-        if (kWeights && XS_BOUNDS(tok0 + kBlock <= p.max_blocks * kBlock, p.err_flag))
-            to = logits + static_cast<int64_t>(held ? (k * kClusterWarps + warp) * kBlock : tok0) * p.G;
-        st.template page<kWeights>(p, kp, kp + ring.kBytes / 2, sp, tok0, to,
-                                   sm.weights[sizeof(T) == 4 ? warp : 0], lane);
-        ++ring.taken;
-        __syncwarp();
-        start();
-    }
-    st.sum_up(p);
-    if (ring.dead) {
-#pragma unroll
-        for (int k = 0; k < S::kHeads; ++k) st.l[k] = NAN;
-    }
-    __syncthreads();    // all pages have been read
-#pragma unroll
-    for (int k = 0; k < D / 16; ++k)
-        sm.o[warp][32 * k + lane] = make_float4(st.acc[4 * k], st.acc[4 * k + 1], st.acc[4 * k + 2], st.acc[4 * k + 3]);
-    if (lane < 8) {
-#pragma unroll
-        for (int k = 0; k < S::kHeads; ++k) {
-            sm.warp_m[warp][S::head(lane, k)] = st.m[k];
-            sm.warp_l[warp][S::head(lane, k)] = st.l[k];
+        for (int k = 0; k < mine && !ring.dead; ++k) {
+            const uint32_t kp = ring.next(p, lane);
+            if (!kp) break;
+            const int tok0 = sp.page(at0 + k * stride) * kBlock;
+            float *to = nullptr;
+            if (kWeights && XS_BOUNDS(tok0 + kBlock <= p.max_blocks * kBlock, p.err_flag))
+                to = logits + static_cast<int64_t>(held ? (k * W + warp) * kBlock : tok0) * p.G;
+            st.template page<kWeights>(p, kp, kp + ring.kBytes / 2, sp, tok0, to,
+                                       sm.weights[sizeof(T) == 4 ? warp : 0], lane);
+            ++ring.taken;
+            __syncwarp();
+            start();
         }
-    }
-    __syncthreads();
-    if (tid < 8 * kClusterWarps) {
-        const int w = tid >> 3, h = tid & 7;
-        float top = sm.warp_m[0][h];
+        st.sum_up(p);
+        if (ring.dead) {
 #pragma unroll
-        for (int k = 1; k < kClusterWarps; ++k) top = fmaxf(top, sm.warp_m[k][h]);
-        sm.warp_w[w][h] = fast_exp2(sm.warp_m[w][h] - top);
-        if (w == 0) {
-            float total = 0.0f;
-#pragma unroll
-            for (int k = 0; k < kClusterWarps; ++k)
-                total = fmaf(fast_exp2(sm.warp_m[k][h] - top), sm.warp_l[k][h], total);
-            sm.m[h] = top, sm.l[h] = total;
+            for (int k = 0; k < S::kHeads; ++k) st.l[k] = NAN;
         }
+        __syncthreads();    // all pages have been read
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k)
+            sm.o[warp][32 * k + lane] = make_float4(st.acc[4 * k], st.acc[4 * k + 1], st.acc[4 * k + 2], st.acc[4 * k + 3]);
+        if (lane < 8) {
+#pragma unroll
+            for (int k = 0; k < S::kHeads; ++k) {
+                sm.warp_m[warp][S::head(lane, k)] = st.m[k];
+                sm.warp_l[warp][S::head(lane, k)] = st.l[k];
+            }
+        }
+        __syncthreads();
+        if (tid < 8 * W) {
+            const int w = tid >> 3, h = tid & 7;
+            float top = sm.warp_m[0][h];
+#pragma unroll
+            for (int k = 1; k < W; ++k) top = fmaxf(top, sm.warp_m[k][h]);
+            sm.warp_w[w][h] = fast_exp2(sm.warp_m[w][h] - top);
+            if (w == 0) {
+                float total = 0.0f;
+#pragma unroll
+                for (int k = 0; k < W; ++k)
+                    total = fmaf(fast_exp2(sm.warp_m[k][h] - top), sm.warp_l[k][h], total);
+                sm.m[h] = top, sm.l[h] = total;
+            }
+        }
+        __syncthreads();
+        return true;
     }
-    __syncthreads();
-    if (tid < kChunks) {
-        const int ln = tid & 31, k = tid >> 5;
+    // Four values of the CTA's (in the layout of the lanes' registers).
+    __device__ __forceinline__ float4 combined(int chunk) const {
+        const int ln = chunk & 31, k = chunk >> 5;
         float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-        for (int w = 0; w < kClusterWarps; ++w) {
-            const float4 v = sm.o[w][tid];
+        for (int w = 0; w < W; ++w) {
+            const float4 v = sm.o[w][chunk];
             o.x = fmaf(sm.warp_w[w][S::head_of(ln, k, 0)], v.x, o.x);
             o.y = fmaf(sm.warp_w[w][S::head_of(ln, k, 1)], v.y, o.y);
             o.z = fmaf(sm.warp_w[w][S::head_of(ln, k, 2)], v.z, o.z);
             o.w = fmaf(sm.warp_w[w][S::head_of(ln, k, 3)], v.w, o.w);
         }
-        sm.part[tid] = o;
+        return o;
     }
+    // Four values of the output, times the factors of CTA rank_of (-1: none).
+    __device__ __forceinline__ void write(int chunk, int rank_of, const float (&v)[4]) const {
+        T *out = static_cast<T *>(out_of<T, D>(p, b, hk));
+        if (!XS_BOUNDS(b < p.B && hk < p.Hkv, p.err_flag)) return;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const int h = S::head_of(chunk & 31, chunk >> 5, c);
+            if (h < p.G)
+                out[h * D + S::dim(chunk & 31, chunk >> 5, c)] =
+                    Elem<T>::from_f32(rank_of < 0 ? v[c] : v[c] * sm.rank_w[rank_of][h]);
+        }
+    }
+    __device__ __forceinline__ void weights() const {
+        by_heads(p.G, [&](auto heads) {
+            auto token = [&](int x) { return (x / kGroup * ctas + rank) * kGroup + x % kGroup; };
+            add_weights<decltype(heads)::value>(
+                p, b, hk, logits, groups * kGroup, token, [&](int x) { return held ? x : token(x); }, sp.n,
+                p.scored ? p.scored[b] : sp.n - 1, sm.ends);
+        });
+    }
+    // All of it was this CTA's: the output, and the weights.
+    __device__ __forceinline__ void whole() const {
+        const int tid = threadIdx.x;
+        if (tid < 8) {
+            float top = sm.m[tid], total = sm.l[tid], w = 1.0f;
+            if (p.sinks && tid < p.G) {
+                const float sink = sink_of(p, hk * p.G + tid, sizeof(T) == 4);
+                const float to = fmaxf(top, sink);
+                w = fast_exp2(top - to);
+                total = fmaf(total, w, fast_exp2(sink - to));
+                top = to;
+            }
+            sm.rank_w[0][tid] = w / total;
+            sm.ends[tid] = make_float2(top, 1.0f / total);
+        }
+        __syncthreads();
+        for (int chunk = tid; chunk < kChunks; chunk += 32 * W) {
+            const float4 o = combined(chunk);
+            const float v[4] = {o.x, o.y, o.z, o.w};
+            write(chunk, 0, v);
+        }
+        if (kWeights) weights();
+    }
+};
+
+template <typename T, int D, bool kWeights>
+__global__ void __launch_bounds__(32 * kLineWarps, line_ctas<T, D>())
+    bounded_many_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
+                        const __grid_constant__ Params p, const int line_grid) {
+    constexpr int kStages = line_stages<T, D>();
+    LineSmem<T, D> &sm = shared_of<LineSmem<T, D>>();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int me = blockIdx.x * kLineWarps + warp, warps = line_grid * kLineWarps;
+    Ring<T, D, kStages> ring;
+    ring.init(sm.ring[warp][0], sm.full[warp]);
+    griddep_wait();
+    if (kWeights) griddep_launch_dependents();      // the second kernel waits beside this one
+
+    // All pages, and the longest sequence's (every CTA looks at all lengths).
+    auto pages_at = [&](int b) { return b < p.B ? static_cast<uint32_t>(span_of(p, b).pages) : 0u; };
+    uint32_t pages0[4], longest = 0;
+    int64_t total = 0;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) pages0[u] = pages_at(32 * u + lane);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        total += __reduce_add_sync(0xffffffffu, pages0[u]);
+        longest = max(longest, pages0[u]);
+    }
+#pragma unroll 4
+    for (int base = 128; base < p.B; base += 32) {
+        const uint32_t pages = pages_at(base + lane);
+        total += __reduce_add_sync(0xffffffffu, pages);
+        longest = max(longest, pages);
+    }
+    longest = __reduce_max_sync(0xffffffffu, longest);
+    const int64_t segments = static_cast<int64_t>(p.B) * p.Hkv, all = total * p.Hkv;
+    // A CTA for each segment, unless the longest would keep its CTA much longer than
+    // the others need, or the CTAs' starts and ends would.  (us, a CTA for each
+    // and the line, bf16, 8 KV heads x 128, G = 4: 20 sequences of 300 tokens 6.3 and 10.4,
+    // of 2000 25 and 31; 64 of 1024 41 and 46, of 4096 151 and 161; 128 of 3000 220 and
+    // 233; 25 of 17 to 8193 76 and 35, 64 of them 90 and 60; 100 of 16 9.2 and 6.0.)
+    const int64_t waves = (segments + line_grid - 1) / line_grid;
+    const bool by_segment =
+        segments <= gridDim.x && static_cast<int64_t>(longest) * kAlone<T, D> <= (waves == 1 ? all + all / 4 : all / 2) + kEnds<T, D> &&
+        (waves - 1) * kEnds<T, D> <= all;
+    if (kWeights && me == 0 && lane == 0) *p.by_segment = by_segment;
+    if (by_segment) {
+        if (blockIdx.x >= segments) return;
+        const int b = blockIdx.x / p.Hkv, hk = blockIdx.x - b * p.Hkv;
+        Segment<T, D, kWeights, kLineWarps, kStages> seg{p, sm, b, hk, 0, 1};
+        if (seg.pages(ring, &tmk, &tmv, false)) seg.whole();
+        return;
+    }
+    if (static_cast<int>(blockIdx.x) >= line_grid) return;
+    // The line; then the sequence in which this warp's share begins.
+    const int64_t line = total + static_cast<int64_t>(p.B) * kSegmentCost;
+    // Shares no smaller than is best for the longest segment, whose n / share parts
+    // are joined one after the other while a part takes its share's time.
+    const int64_t least = max(kMinShare, static_cast<int>(sqrtf(0.5f * longest)));
+    const int64_t groups = min(static_cast<int64_t>(warps / p.Hkv), max(line / least, int64_t(1)));
+    const int group = me / p.Hkv, hk = me - group * p.Hkv;
+    if (group >= groups) return;
+    const int64_t lo = line * group / groups, hi = line * (group + 1) / groups;
+    auto group_at = [&](int64_t x) { return static_cast<int>(((x + 1) * groups - 1) / line); };
+    Cursor at;
+    {
+        int64_t before = 0;
+        bool found = false;
+        auto look = [&](int base, uint32_t pages) {     // among sequences base .. base + 31
+            const uint32_t units = base + lane < p.B ? pages + kSegmentCost : 0;
+            const uint32_t sum = warp_scan(units);
+            const int64_t end = before + sum, s = end - units;
+            before += __shfl_sync(0xffffffffu, sum, 31);
+            const uint32_t who = __ballot_sync(0xffffffffu, lo >= s && lo < end);
+            if (!who) return;
+            found = true;
+            const int src = __ffs(who) - 1;
+            at.b = base + src;
+            at.start = __shfl_sync(0xffffffffu, s, src);
+        };
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            if (!found && 32 * u < p.B) look(32 * u, pages0[u]);
+        for (int base = 128; !found && base < p.B; base += 32) look(base, pages_at(base + lane));
+        if (!found) return;
+    }
+    at.settle(p, lo, hi);
+
+    // Copies run ahead of the work, across the ends of segments.
+    Cursor ahead = at;
+    int next = ahead.a, chunk = next;
+    bool more = true;
+    int32_t ids = load_ids(p, ahead.b, ahead.sp, chunk + lane);
+    auto start = [&]() {
+        while (more && next >= ahead.e) {
+            more = ahead.advance(p, lo, hi);
+            if (!more) return;
+            next = chunk = ahead.a;
+            if (next < ahead.e) ids = load_ids(p, ahead.b, ahead.sp, chunk + lane);
+        }
+        if (!more) return;
+        if (next - chunk == 32) {
+            chunk = next;
+            ids = load_ids(p, ahead.b, ahead.sp, chunk + lane);
+        }
+        ring.start(p, &tmk, &tmv, __shfl_sync(0xffffffffu, ids, next - chunk), hk, lane);
+        ++next;
+    };
+#pragma unroll 1
+    for (int k = 0; k < kStages; ++k) start();
+
+    State<T, D> st;
+    do {
+        const Span &sp = at.sp;
+        if (sp.pages == 0) {
+            if (at.start >= lo && XS_BOUNDS(at.b < p.B && hk < p.Hkv, p.err_flag)) {
+                T *out = static_cast<T *>(out_of<T, D>(p, at.b, hk));
+                for (int x = lane; x < p.G * D; x += 32) out[x] = Elem<T>::from_f32(0.0f);
+            }
+            continue;
+        }
+        if (at.a >= at.e) continue;
+        clear(st);
+        st.load_q(p, query_of<T, D>(p, at.b, hk), lane);
+#pragma unroll 1
+        for (int k = at.a; k < at.e && !ring.dead; ++k) {
+            const uint32_t kp = ring.next(p, lane);
+            if (!kp) break;
+            const int tok0 = sp.page(k) * kBlock;
+            float *logits = nullptr;
+            if (kWeights && XS_BOUNDS(tok0 + kBlock <= p.max_blocks * kBlock, p.err_flag))
+                logits = p.logits + logits_at(p, at.b, hk, tok0);
+            st.template page<kWeights>(p, kp, kp + ring.kBytes / 2, sp, tok0, logits,
+                                       sm.weights[sizeof(T) == 4 ? warp : 0], lane);
+            ++ring.taken;
+            __syncwarp();
+            start();
+        }
+        st.sum_up(p);
+        if (ring.dead) {
+#pragma unroll
+            for (int k = 0; k < State<T, D>::kHeads; ++k) st.l[k] = NAN;
+        }
+        if (at.a > 0 || at.e < sp.pages) {
+            // A part: the last of the segment's warps joins them all.
+            float *part = partial_of(p, D, me, at.a == 0);
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k)
+                __stcg(reinterpret_cast<float4 *>(part) + 32 * k + lane,
+                       make_float4(st.acc[4 * k], st.acc[4 * k + 1], st.acc[4 * k + 2], st.acc[4 * k + 3]));
+            if (lane < 8) {
+#pragma unroll
+                for (int k = 0; k < State<T, D>::kHeads; ++k) {
+                    __stcg(part + 8 * D + State<T, D>::head(lane, k), st.m[k]);
+                    __stcg(part + 8 * D + 8 + State<T, D>::head(lane, k), st.l[k]);
+                }
+            }
+            const int f = group_at(at.start);
+            const int last = group_at(at.start + sp.pages - 1);
+            __syncwarp();
+            int joins = 0;
+            if (lane == 0 && XS_BOUNDS(f >= 0 && f <= last && last < groups, p.err_flag)) {
+                int *count = p.counters + f * p.Hkv + hk;
+                joins = atomic_add_acq_rel_gpu(count, 1) == last - f;
+                if (joins) *count = 0;
+            }
+            joins = __shfl_sync(0xffffffffu, joins, 0);
+            __syncwarp();
+            if (!joins) continue;
+            join<T, D>(p, st, hk, f, last, lane);
+        }
+        finish<T, D, kWeights>(p, st, at.b, hk, lane);
+    } while (at.advance(p, lo, hi));
+}
+
+// ------------------------------------------------------------------ clusters
+
+// A cluster of `ctas` (a power of two) for each segment.
+template <typename T, int D, bool kWeights>
+__global__ void __launch_bounds__(32 * kClusterWarps, 1)
+    bounded_cluster_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
+                           const __grid_constant__ Params p, const int ctas) {
+    using Seg = Segment<T, D, kWeights, kClusterWarps, cluster_stages<T, D>()>;
+    using S = State<T, D>;
+    constexpr int kChunks = Seg::kChunks;
+    ClusterSmem<T, D> &sm = shared_of<ClusterSmem<T, D>>();
+    const int tid = threadIdx.x;
+    Ring<T, D, cluster_stages<T, D>()> ring;
+    ring.init(sm.ring[tid >> 5][0], sm.full[tid >> 5]);
+    griddep_wait();
+    const int rank = blockIdx.x % ctas, segment = blockIdx.x / ctas;
+    const int b = segment / p.Hkv, hk = segment - b * p.Hkv;
+    Seg seg{p, sm, b, hk, rank, ctas};
+    if (!seg.pages(ring, &tmk, &tmv, blockIdx.x == 0)) return;
+    if (ctas == 1) return seg.whole();
+    if (tid < kChunks) sm.part[tid] = seg.combined(tid);
     // The CTAs' parts meet.
     asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
     const int per = (kChunks + ctas - 1) / ctas;        // chunks of this CTA
@@ -1168,25 +1299,12 @@ __global__ void __launch_bounds__(32 * kClusterWarps, 1)
             if (valid) v[c] *= sm.rank_w[from][S::head_of(ln, k, c)];
             for (int d = ctas / 2; d > 0; d >>= 1) v[c] += __shfl_xor_sync(0xffffffffu, v[c], d);
         }
-        if (valid && from == 0 && XS_BOUNDS(b < p.B && hk < p.Hkv, p.err_flag)) {
-            T *out = static_cast<T *>(out_of<T, D>(p, b, hk));
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const int h = S::head_of(ln, k, c);
-                if (h < p.G) out[h * D + S::dim(ln, k, c)] = Elem<T>::from_f32(v[c]);
-            }
-        }
+        if (valid && from == 0) seg.write(chunk, -1, v);
     }
     // No CTA leaves before all have read its shared memory (what they read has
     // been used above).
     asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
-    if (kWeights)
-        by_heads(p.G, [&](auto heads) {
-            auto token = [&](int x) { return (x / kGroup * ctas + rank) * kGroup + x % kGroup; };
-            add_weights<decltype(heads)::value>(
-                p, b, hk, logits, groups * kGroup, token, [&](int x) { return held ? x : token(x); }, sp.n,
-                p.scored ? p.scored[b] : sp.n - 1, sm.ends);
-        });
+    if (kWeights) seg.weights();
     asm volatile("barrier.cluster.wait;" ::: "memory");
 }
 
@@ -1211,33 +1329,32 @@ template <typename T, int D, bool kWeights> int clusters_held(int ctas) {
     return n;
 }
 
-// What a device holds of the cluster kernel at once, in clusters of 2, 4, 8 and
-// 16.  Asked for once for each device (by two threads at once: twice, with one answer).
+// What a device holds of the cluster kernel at once, in clusters of 2, 4 and 8.
+// Asked for once for each device (by two threads at once: twice, with one answer).
 struct Held {
-    int of[4];
+    int of[3];
 };
 template <typename T, int D, bool kWeights> int configure(int dev, Held *held) {
-    static std::atomic<uint64_t> known[64];     // 15 bits each, and 1 in the top one; 0: not yet
+    static std::atomic<uint64_t> known[64];     // 20 bits each, and 1 in the top one; 0: not yet
     uint64_t v = dev < 64 ? known[dev].load(std::memory_order_acquire) : 0;
     if (!v) {
-        if (cudaFuncSetAttribute(bounded_line_kernel<T, D, kWeights>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 1024 + sizeof(LineSmem<T, D>)) != cudaSuccess ||
-            cudaFuncSetAttribute(bounded_cluster_kernel<T, D, kWeights>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 cluster_smem<T, D>(kWeights)) != cudaSuccess ||
+        if (cudaFuncSetAttribute(bounded_many_kernel<T, D, kWeights>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 line_smem<T, D>(kWeights)) != cudaSuccess ||
             cudaFuncSetAttribute(bounded_cluster_kernel<T, D, kWeights>,
-                                 cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) {
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 cluster_smem<T, D>(kWeights)) != cudaSuccess) {
             cudaGetLastError();
             return XS_EDEVICE;
         }
         v = 1ull << 63;
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < 3; ++i) {
             const int n = clusters_held<T, D, kWeights>(2 << i);
             if (n < 0) return XS_EDEVICE;
-            v |= static_cast<uint64_t>(n < 0x7fff ? n : 0x7fff) << (15 * i);
+            v |= static_cast<uint64_t>(n) << (20 * i);
         }
         if (dev < 64) known[dev].store(v, std::memory_order_release);
     }
-    for (int i = 0; i < 4; ++i) held->of[i] = static_cast<int>(v >> (15 * i) & 0x7fff);
+    for (int i = 0; i < 3; ++i) held->of[i] = static_cast<int>(v >> (20 * i) & 0xfffff);
     return XS_OK;
 }
 
@@ -1256,21 +1373,33 @@ template <typename T, int D, bool kWeights> int launch(const Params &p, int dev,
         if (rc != XS_OK) return rc;
     }
     const int64_t segments = static_cast<int64_t>(p.B) * p.Hkv;
-    // Clusters of 16 cost more to start than of 8 and are for long tables alone.
     const int64_t most = p.window > 0 ? min(p.max_blocks, p.first / kBlock + p.window / kBlock + 3) : p.max_blocks;
+    // The largest clusters that the device holds at once (15 of 8 CTAs, 36 of 4 and 76
+    // of 2: their CTAs are of one group of SMs).  us, clusters of 8, 4, 2, and the line:
+    // one sequence of 8 KV heads and 4K tokens 7.1, 9.5, 14.6, 22.7; 16 KV heads, one
+    // too many for 8, 13.4, 9.6, 14.7; 36 (1K tokens) -, 5.9, 6.8, 12.3; 37 -, 10.2, 6.8.
     int ctas = 0;
-    for (int i = 0; i < 4; ++i)
-        if (segments <= held.of[i] && ((2 << i) < 16 || most > 512)) ctas = 2 << i;
+    for (int i = 0; i < 3; ++i)
+        if (segments <= held.of[i]) ctas = 2 << i;
+    // Or a CTA of 8 warps for each, all at once; under a wide table one long sequence
+    // could keep the others waiting.  (us, so and by the kernel for many: 100 segments of
+    // 300 tokens 4.9 and 5.4, of 1024 8.5 and 11.9; one of 4000 and 99 of 100 24 and 17.)
+    if (!ctas && segments <= sms && most <= kShortTable) ctas = 1;
     if (ctas)
         return launch_after(bounded_cluster_kernel<T, D, kWeights>, dim3(static_cast<int>(segments) * ctas),
                             32 * kClusterWarps, cluster_smem<T, D>(kWeights), stream, ctas, tmk, tmv, p, ctas);
     const int fill = min(sms * line_ctas<T, D>(), kMaxWarps / kLineWarps);
-    // The line is at most so long, and no warp takes less than kMinShare of it.
-    const int64_t want = ((segments * (most + kSegmentCost) + kMinShare - 1) / kMinShare + kLineWarps - 1) / kLineWarps;
-    rc = launch_after(bounded_line_kernel<T, D, kWeights>, dim3(static_cast<int>(want < fill ? want : fill)),
-                      32 * kLineWarps, 1024 + sizeof(LineSmem<T, D>), stream, 1, tmk, tmv, p);
+    if (p.Hkv > fill * kLineWarps) return XS_EUNSUPPORTED;
+    // The line is at most so long, and no group takes less than kMinShare of it.
+    const int64_t want_groups = (static_cast<int64_t>(p.B) * (most + kSegmentCost) + kMinShare - 1) / kMinShare;
+    const int64_t want = (want_groups * p.Hkv + kLineWarps - 1) / kLineWarps;
+    const int line_grid = static_cast<int>(want < fill ? want : fill);
+    rc = launch_after(bounded_many_kernel<T, D, kWeights>,
+                      dim3(static_cast<int>(p.B <= kScannedB && segments > line_grid ? segments : line_grid)),
+                      32 * kLineWarps,
+                      line_smem<T, D>(kWeights), stream, 1, tmk, tmv, p, line_grid);
     if (!kWeights || rc != XS_OK) return rc;
-    const int pieces = min((p.max_blocks * kBlock + kWeightTokens - 1) / kWeightTokens, 8);
+    const int pieces = max(1, min((p.max_blocks * kBlock + kWeightTokens - 1) / kWeightTokens, 8));
     const auto second = p.G == 1   ? bounded_weights_kernel<1>
                         : p.G == 2 ? bounded_weights_kernel<2>
                         : p.G == 4 ? bounded_weights_kernel<4>
@@ -1292,7 +1421,7 @@ int check_and_launch(Params &p, bool weights, int D, int block_size, float scale
         return XS_ESHAPE;
     p.G = p.Hq / p.Hkv;
     if ((D != 64 && D != 128) || block_size != kBlock || (p.G != 1 && p.G != 2 && p.G != 4 && p.G != 8) ||
-        p.max_blocks > (1 << 26) || p.q_stride * size % 16 != 0 ||
+        p.Hkv > 512 || p.max_blocks > (1 << 26) || p.q_stride * size % 16 != 0 ||
         p.num_blocks > 0x7fffffff / p.Hkv ||                                  // a tensor copy's coordinate
         static_cast<int64_t>(p.B) * p.Hkv > 0x7fffffff / kMaxCluster)
         return XS_EUNSUPPORTED;
@@ -1308,6 +1437,7 @@ int check_and_launch(Params &p, bool weights, int D, int block_size, float scale
     p.counters = reinterpret_cast<int *>(at), at += kCounterBytes;
     p.partials = reinterpret_cast<float *>(at), at += partial_bytes(D);
     if (weights) {
+        p.by_segment = reinterpret_cast<int *>(at), at += 16;
         p.ends = reinterpret_cast<float2 *>(at);
         at += (static_cast<size_t>(p.B) * p.Hq * sizeof(float2) + 15) / 16 * 16;
         p.logits = reinterpret_cast<float *>(at);
@@ -1354,7 +1484,7 @@ extern "C" size_t xs_paged_decode_first_workspace_bytes(int B, int Hq, int Hkv, 
 
 extern "C" size_t xs_paged_decode_weights_workspace_bytes(int B, int Hq, int Hkv, int D, int max_blocks_per_seq) {
     if (B <= 0 || Hq <= 0 || Hkv <= 0 || D <= 0 || max_blocks_per_seq < 0) return 0;
-    return xs_paged_decode_first_workspace_bytes(B, Hq, Hkv, D) +
+    return xs_paged_decode_first_workspace_bytes(B, Hq, Hkv, D) + 16 +
            (static_cast<size_t>(B) * Hq * sizeof(float2) + 15) / 16 * 16 +
            static_cast<size_t>(B) * Hq * max_blocks_per_seq * xs::bounded::kBlock * sizeof(float);
 }

@@ -132,7 +132,7 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_con
             const int32_t id = row[c];
             if (id < 0 || id >= p.num_blocks)
                 flag |= XS_FLAG_BAD_BLOCK;
-            else if (p.extra && c <= (p.budget - 1) / kPage && p.extra[id] > 0)
+            else if (p.extra && p.budget > p.first && c <= (p.budget - 1) / kPage && p.extra[id] > 0)
                 flag |= XS_FLAG_SHARED;
         }
     }
@@ -361,7 +361,7 @@ extern "C" int xs_kv_evict(const int32_t *seq_ids, int n, void *k_pools, void *v
         return XS_ENULL;
     const int size = xs::elem_bytes(dtype);
     if (!size) return XS_EDTYPE;
-    if (n < 0 || layers < 0 || B < 0 || Hkv <= 0 || D <= 0 || block_size <= 0 || max_blocks_per_seq < 0 ||
+    if (n < 0 || layers <= 0 || B < 0 || Hkv <= 0 || D <= 0 || block_size <= 0 || max_blocks_per_seq < 0 ||
         num_blocks < 0 || first < 0 || recent < 0 || budget <= 0 || limit < budget ||
         static_cast<int64_t>(first) + recent > budget)
         return XS_ESHAPE;

@@ -117,7 +117,7 @@ class Evicted:
             pages = range(first // BS, -(-n // BS))
             if any(row[c] < 0 or row[c] >= nb for c in pages):
                 self.flags |= 1
-            shared = extra is not None and any(0 <= row[c] < nb and extra[row[c]] > 0
+            shared = extra is not None and budget > first and any(0 <= row[c] < nb and extra[row[c]] > 0
                                                for c in pages if c <= (budget - 1) // BS)
             if shared:
                 self.flags |= 128

@@ -72,10 +72,10 @@ def test_evict(lib):
     d = dict(ids=A, n=0, k=A, v=A, layers=2, stride=4 * 2 * 16 * 256, scores=A, bt=A, maxb=4, lens=A, B=3, extra=None, first=4,
              recent=8, budget=16, limit=20, Hkv=2, D=128, bs=16, nb=4, dtype=1, kept=A, new=A, err=None, stream=None)
     f = caller(lib, "xs_kv_evict", list(d), **d)
-    assert f() == OK and f(layers=0, n=5) == OK
+    assert f() == OK                                    # n = 0: nothing is launched
     for n in ("ids", "k", "v", "scores", "bt", "lens", "kept", "new"):
         assert f(**{n: None}) == NULL, n
-    for kw in (dict(n=-1), dict(layers=-1), dict(B=-1), dict(Hkv=0), dict(first=-1), dict(recent=-1), dict(budget=0),
+    for kw in (dict(n=-1), dict(layers=0), dict(layers=-1), dict(B=-1), dict(Hkv=0), dict(first=-1), dict(recent=-1), dict(budget=0),
                dict(limit=15), dict(first=9), dict(nb=-1), dict(nb=5), dict(maxb=-1), dict(first=1 << 30, recent=(1 << 31) - 1)):
         assert f(**kw) == SHAPE, kw
     for kw in (dict(D=32), dict(bs=8), dict(stride=4 * 2 * 16 * 256 + 8), dict(n=1 << 30), dict(maxb=(1 << 26) + 1)):

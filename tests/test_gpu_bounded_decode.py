@@ -346,8 +346,9 @@ def test_wait_injection_host_checks():
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("weights", [False, True], ids=["first", "weights"])
-@pytest.mark.parametrize("lens,page", [([3000], 1), ([200] * 9, 0), ([1000] * 30, 6), ([100, 0, 130] * 20, 3)],
-                         ids=["cluster", "cluster-short", "line", "line-whole"])
+@pytest.mark.parametrize("lens,page", [([3000], 1), ([200] * 9, 0), ([1000] * 30, 6), ([100, 0, 130] * 20, 1),
+                                        ([3000, 17] * 30, 2)],
+                         ids=["cluster", "cluster-short", "segments", "segments-short", "line"])
 def test_a_wait_that_runs_out(lens, page, weights):
     # A page of CTA 0's first warp is left out: nothing is in flight for it.
     dev = device()
@@ -379,3 +380,42 @@ def test_a_wait_that_runs_out(lens, page, weights):
         assert ops.xs_debug_bounds_failures(reset=True, lib=dbg) == 0
     finally:
         ops.use_library(prev)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("weights", [False, True], ids=["first", "weights"])
+def test_a_very_large_batch(weights):
+    # More sequences than a CTA for each segment looks at; one long among short ones.
+    lens = [(37 * i) % 45 - 3 for i in range(600)]
+    lens[311] = 900
+    c = Case(lens, 2, 2, 64, BF, 77, first=0 if weights else 2, window=0 if weights else 600)
+    ws = c.workspace(weights)
+    ref, bound, w = c.plain()
+    scores = torch.zeros(600, 2, c.tables.shape[1] * 16, device=device())
+    for _ in range(2):
+        near(c.weights_call(ws, scores, torch.zeros(600, dtype=torch.int32, device=device())) if weights
+             else c.first_call(ws), ref, bound)
+    if weights:
+        for b, n in enumerate(lens):
+            if n > 0:
+                near(scores[b, :, :n], w[b][1], w[b][2] + 2.0 ** -22 * w[b][1] + 1e-30)
+    assert int(c.err) == 0 and int(ws.buf[:5120].count_nonzero()) == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("lens", [[1200] + [20] * 19, [300] * 20, [16] * 150, [40, 80] * 30 + [2500]],
+                         ids=["line-long", "segments", "short", "line"])
+def test_forms_of_many_segments(lens):
+    # Both forms of the kernel for many segments, one after the other on one workspace.
+    cs = [Case(x, 16, 8, 64, BF, len(x), width=160) for x in (lens, [100] * len(lens))]
+    ws = cs[0].workspace(True)
+    for c in cs * 2:
+        ref, bound, w = c.plain()
+        scores = torch.zeros(len(lens), 8, 2560, device=device())
+        near(c.weights_call(ws, scores), ref, bound)
+        for b in (0, len(lens) // 2, len(lens) - 1):
+            n = int(c.lens[b])
+            want, off = w[b][1].view(8, 2, n).sum(1), w[b][2].view(8, 2, n).sum(1)
+            near(scores[b, :, :n], want, off + 2.0 ** -22 * want + 1e-30)
+        near(c.first_call(ws), ref, bound)
+        assert int(ws.buf[:5120].count_nonzero()) == 0

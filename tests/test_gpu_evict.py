@@ -94,6 +94,10 @@ def test_entries_that_are_not_cut():
     w = s.run([0, 1, 2, 3, 4, 6, 0, -1, 5], 16, 10, 50, 50, extra)
     assert w.new_lens.tolist() == [50, -1, 50, 50, -1, -1, -1, -1, 50]
     assert w.flags == ops.FLAG_SHARED | ops.FLAG_BAD_BLOCK | ops.FLAG_BAD_SLOT
+    s = State([100, 100], 1, 2, 64, BF, 4)
+    extra = [0] * s.k.shape[1]
+    extra[int(s.tables[0, 1])] = 1          # shared, but nothing is written: the first tokens alone are kept
+    assert s.run([0, 1], 20, 0, 20, 20, extra).new_lens.tolist() == [20, 20]
     s = State([100, 90], 1, 2, 64, BF, 3, width=7)
     s.lens[0] = 200                         # beyond its table: the table's 112
     for c in range(7):

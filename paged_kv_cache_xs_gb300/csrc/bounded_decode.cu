@@ -84,7 +84,10 @@ constexpr int kMaxCluster = 8;
 // kLineWarps that has the device for itself, and a CTA's start and end.
 template <typename T, int D> constexpr int64_t kAlone = kBlock * D * sizeof(T) < 4096 ? 200 : 100;
 template <typename T, int D> constexpr int64_t kEnds = 2600 * 4096 / (kBlock * D * static_cast<int>(sizeof(T)));
-__host__ __device__ constexpr int logit_floats(int warps) { return warps == 8 ? 6144 : 2048; }   // in shared memory
+// Logits that a CTA keeps in shared memory (with weights).
+template <typename T, int D, int W> __host__ __device__ constexpr int logit_floats() {
+    return W == kClusterWarps ? 6144 : sizeof(T) == 4 && D == 128 ? 4096 : 10240;
+}
 constexpr float kLead = 8.0f;       // of a reference before the largest logit
 constexpr float kLowest = -3.402823466e38f;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -104,10 +107,14 @@ __device__ __forceinline__ constexpr bool skip_page(uint32_t) { return false; }
 #endif
 
 template <typename T, int D> constexpr int page_bytes() { return kBlock * D * static_cast<int>(sizeof(T)); }
-// Places (a K and a V page) of a warp's ring: 96 KB for a CTA of the line, so that
-// two share an SM, and 192 KB for a cluster's (fp32 pages of 128: 192 and 128 KB).
-template <typename T, int D> __host__ __device__ constexpr int line_stages() {
-    return sizeof(T) == 4 && D == 128 ? 3 : (96 << 10) / (kLineWarps * 2 * kBlock * D * static_cast<int>(sizeof(T)));
+// Places (a K and a V page) of a warp's ring: 96 KB for a CTA of four warps, so that
+// two share an SM, or 64 KB beside logits (64 sequences of 1K tokens 41.6 us with 96, 45.9
+// with 64; 128 of 3000 220 and 223), and 192 KB for a cluster's (fp32 pages of 128: 192
+// and 128 KB).
+template <typename T, int D, bool kWeights> __host__ __device__ constexpr int line_stages() {
+    return sizeof(T) == 4 && D == 128
+               ? 3
+               : ((kWeights ? 64 : 96) << 10) / (kLineWarps * 2 * kBlock * D * static_cast<int>(sizeof(T)));
 }
 template <typename T, int D> __host__ __device__ constexpr int cluster_stages() {
     return (192 << 10) / (kClusterWarps * 2 * kBlock * D * static_cast<int>(sizeof(T)));
@@ -793,11 +800,11 @@ template <typename S> __device__ __forceinline__ S &shared_of() {
 // ------------------------------------------------------------------ weights from logits
 
 // The weights of the tokens at(x), x < count, as far as they are below n, from
-// their G logits each (the place(x)-th ones), added to their scores; ends: the
-// G rows' references and factors.  A thread has kAtOnce tokens under way.
-template <int G, typename F, typename P>
-__device__ __forceinline__ void add_weights(const Params &p, int b, int hk, const float *logits, int count, F &&at,
-                                            P &&place, int n, int scored, const float2 *ends) {
+// their G logits each, at logits(x), added to their scores; ends: the G rows'
+// references and factors.  A thread has kAtOnce tokens under way.
+template <int G, typename F, typename L>
+__device__ __forceinline__ void add_weights(const Params &p, int b, int hk, int count, F &&at, L &&logits, int n,
+                                            int scored, const float2 *ends) {
     using V = typename std::conditional<G == 1, float, typename std::conditional<G == 2, float2, float4>::type>::type;
     constexpr int kPieces = G <= 4 ? 1 : 2, kAtOnce = 4;
     if (!XS_BOUNDS(b < p.B && hk < p.Hkv && n <= p.max_blocks * kBlock, p.err_flag)) return;
@@ -811,7 +818,7 @@ __device__ __forceinline__ void add_weights(const Params &p, int b, int hk, cons
             if (t >= n) continue;
 #pragma unroll
             for (int k = 0; k < kPieces; ++k)
-                x[u][k] = reinterpret_cast<const V *>(logits)[static_cast<int64_t>(place(y)) * kPieces + k];
+                x[u][k] = reinterpret_cast<const V *>(logits(y))[k];
             old[u] = t < scored ? scores[t] : 0.0f;
         }
         float2 end[G];
@@ -833,20 +840,25 @@ __device__ __forceinline__ void add_weights(const Params &p, int b, int hk, cons
 constexpr int kWeightThreads = 256;
 constexpr int kWeightTokens = 1024;     // of a CTA at a time
 
-// Behind the line (nothing where it went by segments): CTAs (segment, y) take every gridDim.y-th piece of kWeightTokens.
+// Behind the line (nothing where each segment had a CTA, so few CTAs that take
+// piece after piece of kWeightTokens: one for each piece cost 10 us there).
 template <int G>
-__global__ void __launch_bounds__(kWeightThreads) bounded_weights_kernel(const __grid_constant__ Params p) {
-    // The lengths may be read at once: the line, which does not write them, lets
-    // this kernel be placed only after everything before it has completed.
-    const int b = blockIdx.x / p.Hkv, hk = blockIdx.x - b * p.Hkv;
-    const int n = min(XS_BOUNDS(b < p.B, p.err_flag) ? p.lens[b] : 0, p.max_blocks * kBlock);
-    const int scored = p.scored ? p.scored[b] : n - 1;
+__global__ void __launch_bounds__(kWeightThreads)
+    bounded_weights_kernel(const __grid_constant__ Params p, const int pieces) {
     after_previous();
     if (__ldcg(p.by_segment)) return;
-    for (int from = blockIdx.y * kWeightTokens; from < n; from += gridDim.y * kWeightTokens)
-        add_weights<G>(
-            p, b, hk, p.logits + logits_at(p, b, hk, from), min(kWeightTokens, n - from),
-            [&](int x) { return from + x; }, [](int x) { return x; }, n, scored, p.ends + static_cast<int64_t>(b) * p.Hq + hk * G);
+    const int64_t items = static_cast<int64_t>(p.B) * p.Hkv * pieces;
+    for (int64_t i = blockIdx.x; i < items; i += gridDim.x) {
+        const int segment = static_cast<int>(i / pieces), piece = static_cast<int>(i - static_cast<int64_t>(segment) * pieces);
+        const int b = segment / p.Hkv, hk = segment - b * p.Hkv;
+        const int n = min(XS_BOUNDS(b < p.B, p.err_flag) ? p.lens[b] : 0, p.max_blocks * kBlock);
+        const int scored = p.scored ? p.scored[b] : n - 1;
+        for (int from = piece * kWeightTokens; from < n; from += pieces * kWeightTokens)
+            add_weights<G>(
+                p, b, hk, min(kWeightTokens, n - from), [&](int x) { return from + x; },
+                [&](int x) { return p.logits + logits_at(p, b, hk, from + x); }, n, scored,
+                p.ends + static_cast<int64_t>(b) * p.Hq + hk * G);
+    }
 }
 
 // ------------------------------------------------------------------ a CTA's work on a segment
@@ -864,18 +876,18 @@ template <typename T, int D, int W, int S> struct alignas(1024) CtaSmem {
     float rank_w[kMaxCluster][8];       // factors of the CTAs' values
     float2 ends[8];
     uint64_t full[W][S];
-    alignas(16) float logits[logit_floats(W)];      // (the form with weights has them)
+    alignas(16) float logits[logit_floats<T, D, W>()];      // (the form with weights has them)
 };
 template <typename T, int D> using ClusterSmem = CtaSmem<T, D, kClusterWarps, cluster_stages<T, D>()>;
-template <typename T, int D> using LineSmem = CtaSmem<T, D, kLineWarps, line_stages<T, D>()>;
+template <typename T, int D, bool kWeights> using LineSmem = CtaSmem<T, D, kLineWarps, line_stages<T, D, kWeights>()>;
 // (The start of the dynamic shared memory need not be a multiple of 1024.)
 template <typename T, int D> constexpr int cluster_smem(bool weights) {
     return 1024 + static_cast<int>(sizeof(ClusterSmem<T, D>)) -
-           (weights ? 0 : static_cast<int>(logit_floats(kClusterWarps) * sizeof(float)));
+           (weights ? 0 : static_cast<int>(logit_floats<T, D, kClusterWarps>() * sizeof(float)));
 }
-template <typename T, int D> constexpr int line_smem(bool weights) {
-    return 1024 + static_cast<int>(sizeof(LineSmem<T, D>)) -
-           (weights ? 0 : static_cast<int>(logit_floats(kLineWarps) * sizeof(float)));
+template <typename T, int D, bool kWeights> constexpr int line_smem() {
+    return 1024 + static_cast<int>(sizeof(LineSmem<T, D, kWeights>)) -
+           (kWeights ? 0 : static_cast<int>(logit_floats<T, D, kLineWarps>() * sizeof(float)));
 }
 
 __device__ __forceinline__ uint32_t peer_addr(const void *own, int rank) {
@@ -906,9 +918,7 @@ template <typename T, int D, bool kWeights, int W, int kStages> struct Segment {
     CtaSmem<T, D, W, kStages> &sm;
     const int b, hk, rank, ctas;
     Span sp;
-    int groups;
-    bool held;
-    float *logits;
+    int groups, held;       // groups of pages, and of how many the logits are in shared memory
 
     // The CTA's pages; what its warps have of them is left in shared memory.  False
     // if the segment is empty (then its output is written).
@@ -960,11 +970,10 @@ template <typename T, int D, bool kWeights, int W, int kStages> struct Segment {
         };
 #pragma unroll 1
         for (int k = 0; k < kStages; ++k) start();
-        // The CTA's logits, of `groups` groups of pages: together in shared memory, or
-        // by their tokens in the workspace.
-        groups = kWeights ? (sp.pages - rank * W + stride - 1) / stride : 0;      // (or <= 0)
-        held = kWeights && groups * kGroup * p.G <= logit_floats(W);
-        if (kWeights) logits = held ? sm.logits : p.logits + logits_at(p, b, hk, 0);
+        // The logits of the first groups of pages are kept together in shared memory, the
+        // others by their tokens in the workspace.
+        groups = kWeights ? max(0, (sp.pages - rank * W + stride - 1) / stride) : 0;
+        held = kWeights ? min(groups, logit_floats<T, D, W>() / (kGroup * p.G)) : 0;
 #pragma unroll 1
         for (int k = 0; k < mine && !ring.dead; ++k) {
             const uint32_t kp = ring.next(p, lane);
@@ -972,7 +981,7 @@ template <typename T, int D, bool kWeights, int W, int kStages> struct Segment {
             const int tok0 = sp.page(at0 + k * stride) * kBlock;
             float *to = nullptr;
             if (kWeights && XS_BOUNDS(tok0 + kBlock <= p.max_blocks * kBlock, p.err_flag))
-                to = logits + static_cast<int64_t>(held ? (k * W + warp) * kBlock : tok0) * p.G;
+                to = k < held ? sm.logits + (k * W + warp) * kBlock * p.G : p.logits + logits_at(p, b, hk, tok0);
             st.template page<kWeights>(p, kp, kp + ring.kBytes / 2, sp, tok0, to,
                                        sm.weights[sizeof(T) == 4 ? warp : 0], lane);
             ++ring.taken;
@@ -1041,10 +1050,12 @@ template <typename T, int D, bool kWeights, int W, int kStages> struct Segment {
     }
     __device__ __forceinline__ void weights() const {
         by_heads(p.G, [&](auto heads) {
+            constexpr int G = decltype(heads)::value;
             auto token = [&](int x) { return (x / kGroup * ctas + rank) * kGroup + x % kGroup; };
-            add_weights<decltype(heads)::value>(
-                p, b, hk, logits, groups * kGroup, token, [&](int x) { return held ? x : token(x); }, sp.n,
-                p.scored ? p.scored[b] : sp.n - 1, sm.ends);
+            auto logits = [&](int x) {
+                return x < held * kGroup ? sm.logits + x * G : p.logits + logits_at(p, b, hk, token(x));
+            };
+            add_weights<G>(p, b, hk, groups * kGroup, token, logits, sp.n, p.scored ? p.scored[b] : sp.n - 1, sm.ends);
         });
     }
     // All of it was this CTA's: the output, and the weights.
@@ -1076,8 +1087,8 @@ template <typename T, int D, bool kWeights>
 __global__ void __launch_bounds__(32 * kLineWarps, line_ctas<T, D>())
     bounded_many_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                         const __grid_constant__ Params p, const int line_grid) {
-    constexpr int kStages = line_stages<T, D>();
-    LineSmem<T, D> &sm = shared_of<LineSmem<T, D>>();
+    constexpr int kStages = line_stages<T, D, kWeights>();
+    LineSmem<T, D, kWeights> &sm = shared_of<LineSmem<T, D, kWeights>>();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int me = blockIdx.x * kLineWarps + warp, warps = line_grid * kLineWarps;
     Ring<T, D, kStages> ring;
@@ -1339,7 +1350,7 @@ template <typename T, int D, bool kWeights> int configure(int dev, Held *held) {
     uint64_t v = dev < 64 ? known[dev].load(std::memory_order_acquire) : 0;
     if (!v) {
         if (cudaFuncSetAttribute(bounded_many_kernel<T, D, kWeights>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 line_smem<T, D>(kWeights)) != cudaSuccess ||
+                                 line_smem<T, D, kWeights>()) != cudaSuccess ||
             cudaFuncSetAttribute(bounded_cluster_kernel<T, D, kWeights>,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  cluster_smem<T, D>(kWeights)) != cudaSuccess) {
@@ -1397,14 +1408,16 @@ template <typename T, int D, bool kWeights> int launch(const Params &p, int dev,
     rc = launch_after(bounded_many_kernel<T, D, kWeights>,
                       dim3(static_cast<int>(p.B <= kScannedB && segments > line_grid ? segments : line_grid)),
                       32 * kLineWarps,
-                      line_smem<T, D>(kWeights), stream, 1, tmk, tmv, p, line_grid);
+                      line_smem<T, D, kWeights>(), stream, 1, tmk, tmv, p, line_grid);
     if (!kWeights || rc != XS_OK) return rc;
     const int pieces = max(1, min((p.max_blocks * kBlock + kWeightTokens - 1) / kWeightTokens, 8));
     const auto second = p.G == 1   ? bounded_weights_kernel<1>
                         : p.G == 2 ? bounded_weights_kernel<2>
                         : p.G == 4 ? bounded_weights_kernel<4>
                                    : bounded_weights_kernel<8>;
-    return launch_after(second, dim3(static_cast<int>(segments), pieces), kWeightThreads, 0, stream, 1, p);
+    const int64_t items = segments * pieces, at_once = static_cast<int64_t>(sms) * 5;
+    return launch_after(second, dim3(static_cast<int>(items < at_once ? items : at_once)), kWeightThreads, 0, stream, 1,
+                        p, pieces);
 }
 
 constexpr size_t kCounterBytes = kMaxWarps * sizeof(int);

@@ -979,7 +979,8 @@ int xs_block_copy(void *k_pools, void *v_pools, int layers, int64_t layer_stride
  * leaves it fit for the next.  Calls that share one must be ordered (one stream,
  * or one CUDA graph).
  * dtype XS_BF16 or XS_F32; block_size 16; D in {64, 128}; Hq / Hkv in {1, 2, 4,
- * 8}; Hkv <= 512; num_blocks * Hkv < 2^31.  out overlaps nothing else.
+ * 8}; Hkv <= 512; num_blocks * Hkv and B * (max_blocks_per_seq + 6) < 2^31.  out
+ * overlaps nothing else.
  * Device-side errors: XS_FLAG_BAD_BLOCK (block 0 was read instead),
  * XS_FLAG_BAD_LEN (the length was clamped to the table), XS_FLAG_TIMEOUT (a
  * page did not arrive within 4 s: the outputs of the sequence and KV head it

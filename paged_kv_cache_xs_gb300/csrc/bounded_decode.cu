@@ -86,7 +86,7 @@ template <typename T, int D> constexpr int64_t kAlone = kBlock * D * sizeof(T) <
 template <typename T, int D> constexpr int64_t kEnds = 2600 * 4096 / (kBlock * D * static_cast<int>(sizeof(T)));
 // Logits that a CTA keeps in shared memory (with weights).
 template <typename T, int D, int W> __host__ __device__ constexpr int logit_floats() {
-    return W == kClusterWarps ? 6144 : sizeof(T) == 4 && D == 128 ? 4096 : 10240;
+    return W == kClusterWarps ? 6144 : sizeof(T) == 2 ? 10240 : D == 128 ? 4096 : 2048;
 }
 constexpr float kLead = 8.0f;       // of a reference before the largest logit
 constexpr float kLowest = -3.402823466e38f;
@@ -108,13 +108,13 @@ __device__ __forceinline__ constexpr bool skip_page(uint32_t) { return false; }
 
 template <typename T, int D> constexpr int page_bytes() { return kBlock * D * static_cast<int>(sizeof(T)); }
 // Places (a K and a V page) of a warp's ring: 96 KB for a CTA of four warps, so that
-// two share an SM, or 64 KB beside logits (64 sequences of 1K tokens 41.6 us with 96, 45.9
-// with 64; 128 of 3000 220 and 223), and 192 KB for a cluster's (fp32 pages of 128: 192
-// and 128 KB).
+// two share an SM, or 64 KB beside the logits of bf16 pages (128 sequences of 2K to 4K
+// tokens 244 us so, 258 with 96 and fewer logits; without logits 64 of 1K take 41.6 us with
+// 96, 45.9 with 64), and 192 KB for a cluster's (fp32 pages of 128: 192 and 128 KB).
 template <typename T, int D, bool kWeights> __host__ __device__ constexpr int line_stages() {
     return sizeof(T) == 4 && D == 128
                ? 3
-               : ((kWeights ? 64 : 96) << 10) / (kLineWarps * 2 * kBlock * D * static_cast<int>(sizeof(T)));
+               : ((kWeights && sizeof(T) == 2 ? 64 : 96) << 10) / (kLineWarps * 2 * kBlock * D * static_cast<int>(sizeof(T)));
 }
 template <typename T, int D> __host__ __device__ constexpr int cluster_stages() {
     return (192 << 10) / (kClusterWarps * 2 * kBlock * D * static_cast<int>(sizeof(T)));
@@ -663,17 +663,16 @@ __device__ __forceinline__ int64_t logits_at(const Params &p, int b, int hk, int
 // A warp's place on the line: sequence b, which starts at `start`, and the warp's
 // pages [a, e) of it.
 struct Cursor {
-    int b, a, e;
-    int64_t start;
+    int b, a, e, start;
     Span sp;
-    __device__ __forceinline__ void settle(const Params &p, int64_t lo, int64_t hi) {
+    __device__ __forceinline__ void settle(const Params &p, int lo, int hi) {
         sp = span_of(p, b);
-        a = static_cast<int>(min(max(lo - start, int64_t(0)), static_cast<int64_t>(sp.pages)));
-        e = static_cast<int>(min(hi - start, static_cast<int64_t>(sp.pages)));
+        a = min(max(lo - start, 0), sp.pages);
+        e = min(hi - start, sp.pages);
         if (sp.pages <= kWholePages) a = 0, e = start >= lo ? sp.pages : 0;
     }
     // To the next sequence; false at the end of the warp's share.
-    __device__ __forceinline__ bool advance(const Params &p, int64_t lo, int64_t hi) {
+    __device__ __forceinline__ bool advance(const Params &p, int lo, int hi) {
         start += sp.pages + kSegmentCost;
         if (start >= hi) return false;
         ++b;
@@ -846,13 +845,14 @@ template <int G>
 __global__ void __launch_bounds__(kWeightThreads)
     bounded_weights_kernel(const __grid_constant__ Params p, const int pieces) {
     after_previous();
-    if (__ldcg(p.by_segment)) return;
+    const bool idle = __ldcg(p.by_segment) != 0;
     const int64_t items = static_cast<int64_t>(p.B) * p.Hkv * pieces;
     for (int64_t i = blockIdx.x; i < items; i += gridDim.x) {
         const int segment = static_cast<int>(i / pieces), piece = static_cast<int>(i - static_cast<int64_t>(segment) * pieces);
         const int b = segment / p.Hkv, hk = segment - b * p.Hkv;
         const int n = min(XS_BOUNDS(b < p.B, p.err_flag) ? p.lens[b] : 0, p.max_blocks * kBlock);
         const int scored = p.scored ? p.scored[b] : n - 1;
+        if (idle) return;       // (the first length is on its way with the answer)
         for (int from = piece * kWeightTokens; from < n; from += pieces * kWeightTokens)
             add_weights<G>(
                 p, b, hk, min(kWeightTokens, n - from), [&](int x) { return from + x; },
@@ -1099,7 +1099,7 @@ __global__ void __launch_bounds__(32 * kLineWarps, line_ctas<T, D>())
     // All pages, and the longest sequence's (every CTA looks at all lengths).
     auto pages_at = [&](int b) { return b < p.B ? static_cast<uint32_t>(span_of(p, b).pages) : 0u; };
     uint32_t pages0[4], longest = 0;
-    int64_t total = 0;
+    uint32_t total = 0;
 #pragma unroll
     for (int u = 0; u < 4; ++u) pages0[u] = pages_at(32 * u + lane);
 #pragma unroll
@@ -1114,13 +1114,13 @@ __global__ void __launch_bounds__(32 * kLineWarps, line_ctas<T, D>())
         longest = max(longest, pages);
     }
     longest = __reduce_max_sync(0xffffffffu, longest);
-    const int64_t segments = static_cast<int64_t>(p.B) * p.Hkv, all = total * p.Hkv;
+    const int64_t segments = static_cast<int64_t>(p.B) * p.Hkv, all = static_cast<int64_t>(total) * p.Hkv;
     // A CTA for each segment, unless the longest would keep its CTA much longer than
     // the others need, or the CTAs' starts and ends would.  (us, a CTA for each
     // and the line, bf16, 8 KV heads x 128, G = 4: 20 sequences of 300 tokens 6.3 and 10.4,
     // of 2000 25 and 31; 64 of 1024 41 and 46, of 4096 151 and 161; 128 of 3000 220 and
     // 233; 25 of 17 to 8193 76 and 35, 64 of them 90 and 60; 100 of 16 9.2 and 6.0.)
-    const int64_t waves = (segments + line_grid - 1) / line_grid;
+    const int waves = (p.B * p.Hkv + line_grid - 1) / line_grid;
     const bool by_segment =
         segments <= gridDim.x && static_cast<int64_t>(longest) * kAlone<T, D> <= (waves == 1 ? all + all / 4 : all / 2) + kEnds<T, D> &&
         (waves - 1) * kEnds<T, D> <= all;
@@ -1134,24 +1134,28 @@ __global__ void __launch_bounds__(32 * kLineWarps, line_ctas<T, D>())
     }
     if (static_cast<int>(blockIdx.x) >= line_grid) return;
     // The line; then the sequence in which this warp's share begins.
-    const int64_t line = total + static_cast<int64_t>(p.B) * kSegmentCost;
+    const int line = static_cast<int>(total) + p.B * kSegmentCost;      // (32 bits hold it: checked by the host)
     // Shares no smaller than is best for the longest segment, whose n / share parts
     // are joined one after the other while a part takes its share's time.
-    const int64_t least = max(kMinShare, static_cast<int>(sqrtf(0.5f * longest)));
-    const int64_t groups = min(static_cast<int64_t>(warps / p.Hkv), max(line / least, int64_t(1)));
+    const int least = max(kMinShare, static_cast<int>(sqrtf(0.5f * longest)));
+    const int groups = min(warps / p.Hkv, max(line / least, 1));
     const int group = me / p.Hkv, hk = me - group * p.Hkv;
     if (group >= groups) return;
-    const int64_t lo = line * group / groups, hi = line * (group + 1) / groups;
-    auto group_at = [&](int64_t x) { return static_cast<int>(((x + 1) * groups - 1) / line); };
+    // The first `longer` shares are one page longer than the others.
+    const int share = line / groups, longer = line - share * groups;
+    const int lo = share * group + min(group, longer), hi = lo + share + (group < longer);
+    auto group_at = [&](int x) {
+        const int y = x - longer * (share + 1);
+        return y < 0 ? x / (share + 1) : longer + y / share;
+    };
     Cursor at;
     {
-        int64_t before = 0;
+        int before = 0;
         bool found = false;
         auto look = [&](int base, uint32_t pages) {     // among sequences base .. base + 31
-            const uint32_t units = base + lane < p.B ? pages + kSegmentCost : 0;
-            const uint32_t sum = warp_scan(units);
-            const int64_t end = before + sum, s = end - units;
-            before += __shfl_sync(0xffffffffu, sum, 31);
+            const int units = base + lane < p.B ? static_cast<int>(pages) + kSegmentCost : 0;
+            const int sum = static_cast<int>(warp_scan(units)), end = before + sum, s = end - units;
+            before = __shfl_sync(0xffffffffu, end, 31);
             const uint32_t who = __ballot_sync(0xffffffffu, lo >= s && lo < end);
             if (!who) return;
             found = true;
@@ -1436,7 +1440,8 @@ int check_and_launch(Params &p, bool weights, int D, int block_size, float scale
     if ((D != 64 && D != 128) || block_size != kBlock || (p.G != 1 && p.G != 2 && p.G != 4 && p.G != 8) ||
         p.Hkv > 512 || p.max_blocks > (1 << 26) || p.q_stride * size % 16 != 0 ||
         p.num_blocks > 0x7fffffff / p.Hkv ||                                  // a tensor copy's coordinate
-        static_cast<int64_t>(p.B) * p.Hkv > 0x7fffffff / kMaxCluster)
+        static_cast<int64_t>(p.B) * p.Hkv > 0x7fffffff / kMaxCluster ||
+        static_cast<int64_t>(p.B) * (p.max_blocks + kSegmentCost) > 0x7fffffff)    // the line, in pages
         return XS_EUNSUPPORTED;
     if (!aligned16(p.out) || !aligned16(p.q) || !aligned16(p.k_cache) || !aligned16(p.v_cache) || !aligned16(workspace))
         return XS_EALIGN;

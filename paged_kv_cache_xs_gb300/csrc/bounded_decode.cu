@@ -51,9 +51,9 @@
 // doing that took 4 us more for 64 sequences of 17 to 8193 tokens than the kernel.)
 //
 // What bounds it: DRAM where there is enough of it (bf16, 32q/8kv x 128: 128 sequences
-// that see 4112 tokens each 307 us, 7.0 TB/s of 6.8 measured for a copy; 128 of 2049
-// to 4097 with weights 279 us, of which the logits' footprint in L2 takes 20 and
-// the scores 10), and the chain length - ids - page - join where there is not (one
+// that see 4112 tokens each 301 us, 7.2 TB/s where a copy has 6.8; 128 of 2049 to 4097
+// with weights 265 us, of which the logits beyond shared memory take 8 and the scores
+// 10), and the chain length - ids - page - join where there is not (one
 // sequence: 5.0 us up to 1K tokens, 7.1 at 4K, 8.1 with weights).
 #include <atomic>
 #include <type_traits>

@@ -20,6 +20,11 @@
 // after it under way.  CTAs share a (layer, sequence, KV head) by K, V and slices
 // of the rows' bytes, never by tokens.  Rows that stay where they are (the first
 // tokens) are neither read nor written.
+//
+// What bounds it: the move its bytes (48 sequences cut to 2K tokens in 4 layers, 3.2 GB
+// read and written: 497 us of the call's 540, 6.5 TB/s; rows of 256 bytes at
+// random places), the ranking the instructions and latencies of its passes (38 us
+// there; of one sequence of 32K 20 of 47).
 #include <atomic>
 #include <climits>
 
@@ -33,7 +38,9 @@ constexpr int kBins = 2048;
 constexpr int kMoveThreads = 256;
 constexpr int kMoveUnroll = 8;      // 16-byte pieces of a thread in a tile
 constexpr int kLongTokens = 4096;   // of a table: beyond, a cluster ranks
-constexpr int kRankCtas = 8;
+// (Eviction of one sequence of 32K tokens in 4 layers, us: clusters of 4 CTAs of 512
+// threads 47, of 4 of 1024 48, of 8 of 256 54, of 8 of 1024 58, one CTA of 1024 67.)
+constexpr int kRankCtas = 4, kRankThreads = 512;
 constexpr int kScoresHeld = 40960;  // of a CTA, in shared memory; of more, they are read again for each pass
 
 struct EvictParams {
@@ -97,14 +104,19 @@ template <int kThreads, int kCtas>
 __global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_constant__ EvictParams p) {
     after_previous();
     extern __shared__ uint32_t held[];      // the bits of this CTA's part of the scores, where they fit
-    __shared__ int hist[kBins], all_hist[kCtas > 1 ? kBins : 1], sm[kThreads / 32], bin, left, counts[2];
-    int *bins = kCtas > 1 ? all_hist : hist;        // of all the candidates
+    // The CTA's counts, and of all the candidates for each pass.
+    __shared__ int hist[kBins], all_hist[kCtas > 1 ? 3 : 1][kCtas > 1 ? kBins : 1];
+    __shared__ int sm[kThreads / 32], bin, left, counts[2];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rank = blockIdx.x % kCtas;
     const int head = blockIdx.x / kCtas;
     const int hk = head % p.Hkv, entry = head / p.Hkv % p.n, layer = head / p.Hkv / p.n;
     const bool tells = layer == 0 && hk == 0 && rank == 0;      // of this entry, what is not a head's own
     int32_t *kept = p.kept + static_cast<int64_t>(head) * p.budget;
 
+    if (kCtas > 1) {        // (waited for before the first counts are added)
+        for (int i = tid; i < 3 * kBins; i += kThreads) (&all_hist[0][0])[i] = 0;
+        asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+    }
     // Whether the sequence is cut: the same for all its heads and layers.
     const int b = XS_BOUNDS(entry < p.n && layer < p.layers, p.err_flag) ? p.seq_ids[entry] : -1;
     int flag = b < 0 || b >= p.B ? XS_FLAG_BAD_SLOT : 0, len = -1;
@@ -142,6 +154,7 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_con
     const bool cut = !stop && n > p.limit;
     if (tells && tid == 0) p.new_lens[entry] = cut ? p.budget : -1;
     if (!cut) {
+        if (kCtas > 1) asm volatile("barrier.cluster.wait;" ::: "memory");
         for (int j = rank * kThreads + tid; j < p.budget; j += kCtas * kThreads) kept[j] = -1;
         return;         // the whole cluster
     }
@@ -158,25 +171,25 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_con
         for (int pass = 0; pass < 3; ++pass) {
             const int bits = pass < 2 ? 11 : 10, above = shift;
             shift -= bits;
-            for (int i = tid; i < kBins; i += kThreads) {
-                hist[i] = 0;
-                if (kCtas > 1) all_hist[i] = 0;
-            }
-            all_sync<kCtas>();
+            for (int i = tid; i < kBins; i += kThreads) hist[i] = 0;
+            __syncthreads();
 #pragma unroll 4
             for (int t = lo + tid; t < hi; t += kThreads) {
                 const uint32_t key = key_at(t);
                 if (pass == 0 || key >> above == prefix) atomicAdd(&hist[key >> shift & ((1u << bits) - 1)], 1);
             }
             __syncthreads();
+            const int *bins = hist;
             if (kCtas > 1) {
+                bins = all_hist[pass];
+                if (pass == 0) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
                 for (int i = tid; i < kBins; i += kThreads) {
                     const int c = hist[i];
                     if (!c) continue;
 #pragma unroll
                     for (int r = 0; r < kCtas; ++r)
                         asm volatile("red.relaxed.cluster.shared::cluster.add.s32 [%0], %1;" ::"r"(
-                                         peer_addr(&all_hist[i], r)),
+                                         peer_addr(&all_hist[pass][i], r)),
                                      "r"(c)
                                      : "memory");
                 }
@@ -201,6 +214,7 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_con
         }
         threshold = prefix;
     } else {
+        if (kCtas > 1) asm volatile("barrier.cluster.wait;" ::: "memory");
         __syncthreads();
     }
 
@@ -397,7 +411,7 @@ extern "C" int xs_kv_evict(const int32_t *seq_ids, int n, void *k_pools, void *v
         rc = xs::launch_after(xs::evict_select_kernel<256, 1>, dim3(ctas), 256, tokens * sizeof(uint32_t), stream, 1, p);
     } else {
         if (ctas > INT_MAX / xs::kRankCtas) return XS_EUNSUPPORTED;
-        const auto select = xs::evict_select_kernel<256, xs::kRankCtas>;
+        const auto select = xs::evict_select_kernel<xs::kRankThreads, xs::kRankCtas>;
         static std::atomic<bool> may[64];      // each device has been told of its shared memory
         if (dev >= 64 || !may[dev].load(std::memory_order_acquire)) {
             if (cudaFuncSetAttribute(select, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -409,7 +423,7 @@ extern "C" int xs_kv_evict(const int32_t *seq_ids, int n, void *k_pools, void *v
         }
         const int64_t part = (tokens + xs::kRankCtas - 1) / xs::kRankCtas + 32;
         p.held = static_cast<int>(part < xs::kScoresHeld ? part : 0);
-        rc = xs::launch_after(select, dim3(ctas * xs::kRankCtas), 256, p.held * sizeof(uint32_t), stream,
+        rc = xs::launch_after(select, dim3(ctas * xs::kRankCtas), xs::kRankThreads, p.held * sizeof(uint32_t), stream,
                               xs::kRankCtas, p);
     }
     if (rc != XS_OK) return rc;

@@ -54,7 +54,7 @@
 //    the key tiles of the first tokens and those from its first query's window
 //    on, as one list; pages that none of its queries sees arrive as zeros, and
 //    rows of V that none sees are zeroed where they were staged.  4,096 tokens
-//    behind 28,672 under a window of 4,096 (32q/8kv x 128): 328 us.
+//    behind 28,672 under a window of 4,096 (32q/8kv x 128): 279 us.
 //  * TMEM: all 512 columns (per Q tile S/P 128, O 128).  Every wait is
 //    bounded; the MMA thread waits for its last MMA before the CTA frees TMEM.
 #include <cuda.h>
@@ -818,16 +818,17 @@ int prefill(void *out, const void *q, const void *k_cache, const void *v_cache,
     int64_t ctas = static_cast<int64_t>((T + tq - 1) / tq) * Hkv;
     if (ctas > 0x3fffffff) return XS_EUNSUPPORTED;
     if (kFirst) {
-        // Under a window all CTAs take about as long.  Where the last wave would
-        // fill no more than half of the SMs, its pairs of Q tiles are two CTAs each
-        // (512 pairs: 328 us as they are, HALVES_US with the last 56 as 112).
+        // Under a window all CTAs take about as long.  Where the last wave would fill no
+        // more than half of the SMs, its pairs of Q tiles are two CTAs each, if it is
+        // the only one or small beside the others.  (us, so and as pairs: 36 pairs of 333
+        // queries 14.9 and 19.5, 512 of 4K 275 and 279; 192 of 1.5K 28 and 26.)
         int dev = 0, sms = 0;
         if (cudaGetDevice(&dev) != cudaSuccess ||
             cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
             return XS_EDEVICE;
         const int last = static_cast<int>(ctas % sms);
         p.units = static_cast<int>(ctas);
-        p.whole = last <= sms / 2 ? p.units - last : p.units;
+        p.whole = last <= sms / 2 && (ctas < sms || ctas >= 3 * sms) ? p.units - last : p.units;
         ctas += p.units - p.whole;
     }
     cudaLaunchConfig_t cfg = {};

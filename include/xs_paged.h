@@ -91,14 +91,14 @@ extern "C" {
 #define XS_FLAG_POOL_EMPTY 32 /* the free-block stack was empty (allocation)
                                  or full (release); that sequence was left
                                  as it was                                    */
-#define XS_FLAG_SHARED 128  /* a page that would be written belongs to another
-                               sequence too (xs_kv_evict); the sequence was left
-                               as it was                                      */
 #define XS_FLAG_BOUNDS 64   /* only in the debug build (libxs_paged_debug.so,
                                compiled with -DXS_DEBUG_BOUNDS): a computed
                                global-memory index fell outside its buffer;
                                the access was skipped.  Release builds never
                                set it (the checks compile away).              */
+#define XS_FLAG_SHARED 128  /* a page that would be written belongs to another
+                               sequence too (xs_kv_evict); the sequence was left
+                               as it was                                      */
 
 /*
  * xs_slot_mapping - where each sequence's new token goes (one decode step).
@@ -999,7 +999,8 @@ int xs_paged_decode_first(void *out, const void *q, int64_t q_stride, const void
  * xs_paged_prefill_first - the same mask for a chunk of a prompt: xs_paged_
  * prefill_tc in which the query at position p sees the keys t <= p with t < first
  * or t > p - window (window 0: every t <= p).  block_ids entries of pages that no
- * query of the chunk sees are never read.  bf16 only; scale > 0.
+ * query of the chunk sees are never read.  bf16 only; scale > 0; start_pos + T <
+ * 2^31 - 512.
  * Weights enter the product with V as bf16, as there (the output is off by 0.0024
  * of its size where its own rounding leaves 0.0017).
  * Rows that no query of the chunk sees have no influence.  An infinity or a NaN

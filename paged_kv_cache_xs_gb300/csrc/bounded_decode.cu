@@ -12,8 +12,8 @@
 //
 // A page of one KV head serves the G = Hq / Hkv query heads of its group.  bf16
 // pages are worked on with m16n8k16 matrix instructions, keys (and dims of the
-// output) on the rows, heads on the columns; fp32 pages with packed products
-// of the ordinary pipes.  The softmax is online, in fp32: its reference leads
+// output) on the rows, heads on the columns; fp32 pages with fp32 products and
+// sums of the ordinary pipes.  The softmax is online, in fp32: its reference leads
 // the largest logit by kLead powers of two and is set again only when a logit
 // exceeds it, so most pages take no exchange between lanes.  A weight enters
 // the second product of the bf16 form as the sum of two bf16 values (the
@@ -106,7 +106,6 @@ __device__ __forceinline__ constexpr uint64_t wait_limit() { return kWaitLimitNs
 __device__ __forceinline__ constexpr bool skip_page(uint32_t) { return false; }
 #endif
 
-template <typename T, int D> constexpr int page_bytes() { return kBlock * D * static_cast<int>(sizeof(T)); }
 // Places (a K and a V page) of a warp's ring: 96 KB for a CTA of four warps, so that
 // two share an SM, or 64 KB beside the logits of bf16 pages (128 sequences of 2K to 4K
 // tokens 244 us so, 258 with 96 and fewer logits; without logits 64 of 1K take 41.6 us with
@@ -620,8 +619,8 @@ template <typename T, int D, int kStages> struct Ring {
         }
         return __all_sync(0xffffffffu, ok);
     }
-    // Waits for the next page: its shared address, or 0 if it did not come (then
-    // what is on its way has landed, as far as it does).
+    // Waits for the next page: its shared address; or it did not come (dead) and what
+    // is on its way has landed, as far as it does.
     __device__ __forceinline__ uint32_t next(const Params &p, int lane) {
         const uint32_t st = taken % kStages;
         if (!wait(bars + 8 * st, (taken / kStages) & 1)) {
@@ -712,8 +711,9 @@ __device__ __forceinline__ void finish(const Params &p, State<T, D> &st, int b, 
 }
 
 // Joins the partials that KV head hk's warps of groups f .. last left of a segment,
-// in order: that of group f its second, the others their first.  kAtOnce are on their way at a time (an
-// access to another SM's fresh results takes about 1 us).
+// in order: that of group f its second, the others their first.  kAtOnce are on
+// their way at a time (an access to another SM's fresh results takes about 1 us;
+// with 6 the line takes up to 4% longer).
 template <typename T, int D>
 __device__ __forceinline__ void join(const Params &p, State<T, D> &st, int hk, int f, int last, int lane) {
     using S = State<T, D>;
@@ -977,7 +977,7 @@ template <typename T, int D, bool kWeights, int W, int kStages> struct Segment {
 #pragma unroll 1
         for (int k = 0; k < mine && !ring.dead; ++k) {
             const uint32_t kp = ring.next(p, lane);
-            if (!kp) break;
+            if (ring.dead) break;
             const int tok0 = sp.page(at0 + k * stride) * kBlock;
             float *to = nullptr;
             if (kWeights && XS_BOUNDS(tok0 + kBlock <= p.max_blocks * kBlock, p.err_flag))
@@ -1083,6 +1083,10 @@ template <typename T, int D, bool kWeights, int W, int kStages> struct Segment {
     }
 };
 
+// ------------------------------------------------------------ many segments
+
+// A CTA for each segment where the lengths allow it, else the line on the first
+// line_grid CTAs.
 template <typename T, int D, bool kWeights>
 __global__ void __launch_bounds__(32 * kLineWarps, line_ctas<T, D>())
     bounded_many_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
@@ -1122,7 +1126,8 @@ __global__ void __launch_bounds__(32 * kLineWarps, line_ctas<T, D>())
     // 233; 25 of 17 to 8193 76 and 35, 64 of them 90 and 60; 100 of 16 9.2 and 6.0.)
     const int waves = (p.B * p.Hkv + line_grid - 1) / line_grid;
     const bool by_segment =
-        segments <= gridDim.x && static_cast<int64_t>(longest) * kAlone<T, D> <= (waves == 1 ? all + all / 4 : all / 2) + kEnds<T, D> &&
+        segments <= gridDim.x &&
+        static_cast<int64_t>(longest) * kAlone<T, D> <= (waves == 1 ? all + all / 4 : all / 2) + kEnds<T, D> &&
         (waves - 1) * kEnds<T, D> <= all;
     if (kWeights && me == 0 && lane == 0) *p.by_segment = by_segment;
     if (by_segment) {
@@ -1210,7 +1215,7 @@ __global__ void __launch_bounds__(32 * kLineWarps, line_ctas<T, D>())
 #pragma unroll 1
         for (int k = at.a; k < at.e && !ring.dead; ++k) {
             const uint32_t kp = ring.next(p, lane);
-            if (!kp) break;
+            if (ring.dead) break;
             const int tok0 = sp.page(k) * kBlock;
             float *logits = nullptr;
             if (kWeights && XS_BOUNDS(tok0 + kBlock <= p.max_blocks * kBlock, p.err_flag))

@@ -511,7 +511,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int j = 0; j < kKeys; ++j) v[j] = __uint_as_float(sr[j >> 5][j & 31]);
             if (need_mask) {
-if constexpr (kFirst) {
+                if constexpr (kFirst) {
                     // One bit for each key: compared one by one, three bounds a key
                     // become branches (5 us a tile).
                     int row = r;            // (so that its position takes no register elsewhere)
@@ -753,6 +753,8 @@ int prefill(void *out, const void *q, const void *k_cache, const void *v_cache,
     if (static_cast<int64_t>(start_pos) + T > static_cast<int64_t>(n_ids) * block_size)
         return XS_ESHAPE;
     if (kFirst && !(scale > 0.f)) return XS_EUNSUPPORTED;    // (0 would make NaN of a masked logit)
+    // (The key behind the last tile is counted in 32 bits.)
+    if (kFirst && static_cast<int64_t>(start_pos) + T > 0x7fffffff - 4 * kKeys) return XS_EUNSUPPORTED;
     const int64_t rows = num_blocks * Hkv * kBlock;
     if (rows + kBlock > 0x7fffffff) return XS_EUNSUPPORTED;  // 32-bit TMA row coordinate
     if (!aligned16(out) || !aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache))

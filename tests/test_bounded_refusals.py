@@ -66,6 +66,7 @@ def test_prefill_first(lib):
     for kw in (dict(dtype=0), dict(D=32), dict(Hq=6), dict(bs=8), dict(scale=0.0), dict(scale=-1.0), dict(scale=float("nan"))):
         assert f(**kw) == UNSUP, kw
     assert f(dtype=5) == DTYPE and f(q=A + 8) == ALIGN
+    assert f(n=1 << 27, start=(1 << 31) - 512) == UNSUP and f(n=1 << 27, start=(1 << 31) - 513) == OK
 
 
 def test_evict(lib):

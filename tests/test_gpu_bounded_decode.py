@@ -419,3 +419,80 @@ def test_forms_of_many_segments(lens):
             near(scores[b, :, :n], want, off + 2.0 ** -22 * want + 1e-30)
         near(c.first_call(ws), ref, bound)
         assert int(ws.buf[:5120].count_nonzero()) == 0
+
+
+def check_scores(c, scores, weights, G, b, what=""):
+    n = max(int(c.lens[b]), 0)
+    if n:
+        want, off = weights[b][1].view(-1, G, n).sum(1), weights[b][2].view(-1, G, n).sum(1)
+        near(scores[b, :, :n], want, off + (G + 2) * 2.0 ** -24 * want + 1e-30, f"scores of {b} {what}")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("lens,Hq,Hkv", [([9001, 3], 8, 1), ([2000, 1999] * 40, 8, 1), ([1500] * 118 + [17, 900], 16, 2)],
+                         ids=["cluster", "cta", "segments"])
+def test_weights_of_more_logits_than_shared_memory_holds(lens, Hq, Hkv, dtype):
+    c = Case(lens, Hq, Hkv, 64, dtype, len(lens))
+    ws, scores = c.workspace(True), torch.full((len(lens), Hkv, c.tables.shape[1] * 16), 3.0, device=device())
+    scored = torch.zeros(len(lens), dtype=torch.int32, device=device())
+    ref, bound, w = c.plain()
+    for _ in range(2):
+        near(c.weights_call(ws, scores, scored), ref, bound)
+        for b, n in enumerate(lens):
+            check_scores(c, scores, w, Hq // Hkv, b)
+            assert bool((scores[b, :, n:] == 3.0).all())
+    assert int(c.err) == 0 and int(ws.buf[:5120].count_nonzero()) == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B", [2, 50], ids=["cluster", "many"])
+def test_weights_captured_beside_each_other(B):
+    # Two graphs of two calls each, on streams and workspaces of their own; between
+    # the replays lengths of one size (a CTA for each segment, where there are many)
+    # change to unlike ones (the line) and back.
+    cases = [Case([600] * B, 8, 4, 64, BF, 30 + i, width=150, nan=False, every=True) for i in range(2)]
+    ws = [c.workspace(True) for c in cases]
+    scores = [torch.zeros(B, 4, 2400, device=device()) for _ in cases]
+    scored = [torch.zeros(B, dtype=torch.int32, device=device()) for _ in cases]
+    streams, graphs = [torch.cuda.Stream() for _ in cases], []
+    torch.cuda.synchronize()
+    for c, w, x, n, s in zip(cases, ws, scores, scored, streams):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            c.weights_call(w, x, n)
+            c.weights_call(w, x, c.d["lens"])       # (every token has a score now)
+        graphs.append(graph)
+    r = random.Random(B)
+    for kind in ("same", "unlike", "short", "unlike", "same"):
+        for c in cases:
+            lens = [{"same": 600 - b % 5, "unlike": r.choice([1, 5, 40]), "short": 20}[kind] for b in range(B)]
+            if kind == "unlike":
+                lens[r.randrange(B)], lens[0] = 590, 0
+            c.lens.copy_(torch.tensor(lens, dtype=torch.int32))
+            c.d["lens"].copy_(c.lens)
+        torch.cuda.synchronize()
+        for graph, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                graph.replay()
+        torch.cuda.synchronize()
+        for c, x, w in zip(cases, scores, ws):
+            ref, bound, weights = c.plain()
+            near(c.out, ref, bound, kind)
+            for b in range(B):
+                check_scores(c, x / 2, weights, 2, b, kind)
+            assert int(c.err) == 0 and int(w.buf[:5120].count_nonzero()) == 0
+
+
+@pytest.mark.gpu
+def test_a_workspace_serves_smaller_calls():
+    ws = ops.BoundedWorkspace(64, 8, 4, 64, device(), 200)
+    for lens, width in (([700] * 60, 60), ([30, 900], 200), ([100, 1] * 25, 10), ([900] + [10] * 63, 200)):
+        c = Case(lens, 8, 4, 64, BF, len(lens), width=width)
+        scores = torch.zeros(len(lens), 4, width * 16, device=device())
+        ref, bound, w = c.plain()
+        near(c.weights_call(ws, scores), ref, bound)
+        for b in range(len(lens)):
+            check_scores(c, scores, w, 2, b)
+        near(c.first_call(ws), ref, bound)
+        assert int(ws.buf[:5120].count_nonzero()) == 0

@@ -241,3 +241,51 @@ def test_bounded_steps(dtype, Hq, Hkv, D):
         assert step.scored.tolist() == lens.tolist()
     assert evictions >= 6 and step.error_flags() == 0
     assert rng is not None
+
+
+def test_bounded_steps_captured():
+    """A step of two layers with its eviction as one graph, replayed over lengths
+    that reach the limit again and again: the same as the calls one by one."""
+    dev, layers, B, Hq, Hkv, D, width, nb = device(), 2, 3, 8, 2, 64, 6, 20
+    g = torch.Generator(device=dev).manual_seed(6)
+    x = torch.randn(60, layers, B, Hq + 2 * Hkv, D, generator=g, device=dev).to(BF)
+    table = ops.rope_table(100, D, 1e4, dev)
+    w = torch.ones(D, dtype=BF, device=dev)
+
+    class Loop:
+        def __init__(self):
+            self.step = BoundedDecodeStep(B, Hq, Hkv, D, width, layers, BF, dev, 40, 44, 2, 10)
+            self.k, self.v = (torch.zeros(layers, nb, Hkv, 16, D, dtype=BF, device=dev) for _ in range(2))
+            self.tables, self.lens = torch.full((B, width), -1, dtype=torch.int32, device=dev), i32([0, 0, -1])
+            self.stack, self.top, self.extra = i32(list(range(nb))), i32([nb]), i32([0] * nb)
+            self.pos, self.x = i32([0, 0, -1]), torch.empty_like(x[0])
+            self.out = torch.zeros(layers, B, Hq, D, dtype=BF, device=dev)
+
+        def run(self):
+            ops.xs_block_alloc_decode(self.tables, self.lens, self.stack, self.top)
+            for l in range(layers):
+                self.step.run(l, self.out[l], *self.x[l].split([Hq, Hkv, Hkv], 1), w, w, table, self.pos, self.k[l],
+                              self.v[l], self.tables, self.lens, D ** -0.5)
+            self.step.bound(self.k, self.v, self.tables, self.lens, self.stack, self.top, self.extra)
+
+    eager, captured = Loop(), Loop()
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=side):
+        captured.run()
+    shortened = 0
+    for t in range(60):
+        for loop in (eager, captured):
+            loop.x.copy_(x[t])
+        n = eager.lens.clone()
+        eager.run()
+        graph.replay()
+        torch.cuda.synchronize()
+        shortened += int((eager.lens < n).sum())
+        for a, b in ((eager.out, captured.out), (eager.lens, captured.lens), (eager.tables, captured.tables),
+                     (eager.k, captured.k), (eager.v, captured.v), (eager.top, captured.top),
+                     (eager.step.scores, captured.step.scores), (eager.step.kept, captured.step.kept)):
+            assert torch.equal(a, b), t
+        for loop in (eager, captured):
+            loop.pos[:2] += 1
+    assert shortened >= 6 and eager.step.error_flags() == 0 and captured.step.error_flags() == 0

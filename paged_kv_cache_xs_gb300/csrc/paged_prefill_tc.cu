@@ -53,8 +53,10 @@
 //    sees the keys t <= i with t > i - window or t < first.  A CTA goes through
 //    the key tiles of the first tokens and those from its first query's window
 //    on, as one list; pages that none of its queries sees arrive as zeros, and
-//    rows of V that none sees are zeroed where they were staged.  4,096 tokens
-//    behind 28,672 under a window of 4,096 (32q/8kv x 128): 279 us.
+//    rows of V that none sees are zeroed where they were staged.  The CTAs of a
+//    short last wave have one Q tile each, whose key tiles the two softmax groups
+//    take in turn (64 queries under a window of 4,096: 45 us, by one group 65).
+//    4,096 tokens behind 28,672 under a window of 4,096 (32q/8kv x 128): 249 us.
 //  * TMEM: all 512 columns (per Q tile S/P 128, O 128).  Every wait is
 //    bounded; the MMA thread waits for its last MMA before the CTA frees TMEM.
 #include <cuda.h>
@@ -62,6 +64,7 @@
 #include <algorithm>
 #include <cmath>
 #include <mutex>
+#include <type_traits>
 
 #include "xs_common.cuh"
 
@@ -251,7 +254,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     // i % Hkv, so the CTAs with the most keys start in the first wave and the
     // launch ends on the short ones.
     // kFirst: CTAs from p.whole on take one Q tile each, two of them what others
-    // do as one CTA.
+    // do as one CTA.  Both groups of softmax warps then work on it: the first on the
+    // list's even key tiles, the second on the odd ones, each with its own S, P and
+    // O, which meet at the end.
     const int n_tok_tiles = (kFirst ? p.units : static_cast<int>(gridDim.x)) / p.Hkv;
     const bool half = kFirst && static_cast<int>(blockIdx.x) >= p.whole;
     const int unit = half ? p.whole + (static_cast<int>(blockIdx.x) - p.whole) / 2 : static_cast<int>(blockIdx.x);
@@ -322,8 +327,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             // its ring on its own, a tile as soon as its slot is free.
             const int which = warp == 3;  // 0: K, 1: V
             if (which == 0 && lane == 0) {
-                mbar_arrive_expect_tx(q_full, C::kQBytes);
-                for (int qi = 0; qi < kQTiles; ++qi)
+                mbar_arrive_expect_tx(q_full, half ? C::kQTile : C::kQBytes);
+                for (int qi = 0; qi < (half ? 1 : kQTiles); ++qi)
                     for (int h = 0; h < C::kHalves; ++h)
                         tma_load_3d(smem_addr(qs + qi * C::kQTile + h * C::kQHalf), &tmq, 64 * h,
                                     g * G, tok0 + qi * kTq, q_full);
@@ -417,7 +422,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 static_assert(C::kQHalf == C::kKVHalf, "Q and K D-halves step alike");
                 auto issue_s = [&](int qi, int kt) {
                     const uint64_t kd = (kt % kStages) ? dk[1] : dk[0];
-                    const uint64_t qd = qi ? dq[1] : dq[0];
+                    const uint64_t qd = qi && !half ? dq[1] : dq[0];
 #pragma unroll
                     for (int ks = 0; ks < D / 16; ++ks) {
                         const uint64_t off = static_cast<uint64_t>(
@@ -427,19 +432,41 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     umma_commit(s_full(qi));
                 };
-                auto issue_pv = [&](int qi, int kt) {
+                auto issue_pv = [&](int qi, int kt, bool more) {     // more: added to what O holds
                     const uint64_t vd = (kt % kStages) ? dv[1] : dv[0];
                     const uint32_t cols = tmem + qi * kGroupCols;
 #pragma unroll
                     for (int kk = 0; kk < kKeys / 16; ++kk)
                         umma_ts(cols + kColO, cols + kColP + 8 * kk,
                                 vd + static_cast<uint64_t>((2048 * kk) >> 4), C::kIdPV,
-                                kt > 0 || kk > 0);
+                                more || kk > 0);
                     umma_commit(pv_done(qi));
                 };
                 bool ok = ntiles == 0 || (mbar_wait_bounded(q_full, 0, kWaitLimitNs) &&
                                           mbar_wait_bounded(&k_full[0], 0, kWaitLimitNs));
-                if (ok && ntiles > 0) {
+                if (half) {
+                    // Tile kt is of slot kt & 1 in the rings and of softmax group kt & 1
+                    // alike; V(kt) and K(kt + 2) have landed once P(kt) is published.
+                    for (int kt = 0; ok && kt < min(ntiles, 2); ++kt) {
+                        if (kt) ok = mbar_wait_bounded(&k_full[1], 0, kWaitLimitNs);
+                        if (!ok) break;
+                        tc_fence_after();
+                        issue_s(kt, kt);
+                        umma_commit(&k_empty[kt]);
+                    }
+                    for (int kt = 0; ok && kt < ntiles; ++kt) {
+                        const int qi = kt & 1;
+                        ok = mbar_wait_bounded(p_full(qi), (kt >> 1) & 1, kWaitLimitNs) && !aborted();
+                        if (!ok) break;
+                        tc_fence_after();
+                        issue_pv(qi, kt, kt > 1);
+                        umma_commit(&v_empty[qi]);
+                        if (kt + 2 < ntiles) {
+                            issue_s(qi, kt + 2);
+                            umma_commit(&k_empty[qi]);
+                        }
+                    }
+                } else if (ok && ntiles > 0) {
                     tc_fence_after();
                     for (int qi = 0; qi < kQTiles; ++qi)
                         if (nt_q[qi] > 0) issue_s(qi, 0);
@@ -448,7 +475,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // V(kt) and K(kt + 1) have landed once P(kt) is published.  A
                 // V slot is released after the step's last P V, before that
                 // tile's next scores; a K slot after both tiles' S(kt + 1).
-                for (int kt = 0; ok && kt < ntiles; ++kt) {
+                for (int kt = 0; !half && ok && kt < ntiles; ++kt) {
                     const int s = kt % kStages, s1 = (kt + 1) % kStages;
                     const int last_v = kt < nt_q[kQTiles - 1] ? kQTiles - 1 : 0;
                     bool k_used = false;
@@ -457,7 +484,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         ok = mbar_wait_bounded(p_full(qi), kt & 1, kWaitLimitNs) && !aborted();
                         if (!ok) break;
                         tc_fence_after();
-                        issue_pv(qi, kt);
+                        issue_pv(qi, kt, kt > 0);
                         if (qi == last_v) umma_commit(&v_empty[s]);
                         if (kt + 1 < nt_q[qi]) {
                             issue_s(qi, kt + 1);
@@ -479,169 +506,218 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int qi = (warp - 4) >> 2;    // Q tile of this warp group
         const int quad = warp & 3;         // TMEM lanes 32 * quad .. + 31 (warp rank in its warpgroup)
         const int r = 32 * quad + lane;    // this thread's row = TMEM lane
-        const int tl = qi * kTq + r / G;   // query token within the CTA
-        const bool valid = r / G < tile_tokens(qi);
+        const int tl = (half ? 0 : qi * kTq) + r / G;  // query token within the CTA
+        const bool valid = r / G < (half ? ntok : tile_tokens(qi));
         const int qpos = p.start + tok0 + tl;
-        const int my_ntiles = tile_ntiles(qi);
+        const int my_ntiles = half ? (ntiles + 1 - qi) / 2 : tile_ntiles(qi);
         const uint32_t lane_off = static_cast<uint32_t>(32 * quad) << 16;
         const uint32_t cols = tmem + lane_off + qi * kGroupCols;
         // (kFirst: -infinity until the row has met a key that it sees.)
         float m_ref = kFirst ? -INFINITY : 0.f, l = 0.f;
         bool ok = true;
-        for (int kt = 0; kt < my_ntiles; ++kt) {
-            ok = __all_sync(0xffffffffu, mbar_wait_bounded(s_full(qi), kt & 1, kWaitLimitNs)) &&
-                 !aborted();
-            if (!ok) break;
-            tc_fence_after();
-            uint32_t sr[4][32];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) tmem_ld32(cols + kColS + 32 * c, sr[c]);
-            tmem_wait_ld();
+        // (Two copies of the loop: as one, with both forms' indexes live, a pair's tile
+        // takes 2% longer.)
+        auto softmax = [&](auto as_half) {
+            constexpr bool kHalf = decltype(as_half)::value;
+            for (int it = 0; it < my_ntiles; ++it) {
+                ok = __all_sync(0xffffffffu, mbar_wait_bounded(s_full(qi), it & 1, kWaitLimitNs)) &&
+                     !aborted();
+                if (!ok) break;
+                tc_fence_after();
+                uint32_t sr[4][32];
+    #pragma unroll
+                for (int c = 0; c < 4; ++c) tmem_ld32(cols + kColS + 32 * c, sr[c]);
+                tmem_wait_ld();
 
-            // Causal mask (by selection: a masked slot may hold any bits) - only
-            // tiles that reach past the Q tile's first query position need one.
-            // The maximum is taken on raw scores (qscale > 0), the exponent
-            // is one fma: 2^(s * qscale - m).  Maximum and sums run as 8
-            // independent chains.
-            const int k0 = key_tile(kt) * kKeys;
-            const int q0 = p.start + tok0 + qi * kTq;      // the Q tile's first position
-            const bool need_mask = k0 + kKeys - 1 > q0 ||
-                                   (kFirst && p.window > 0 && k0 < q0 + kTq - p.window && k0 + kKeys > p.first);
-            float v[kKeys];
-#pragma unroll
-            for (int j = 0; j < kKeys; ++j) v[j] = __uint_as_float(sr[j >> 5][j & 31]);
-            if (need_mask) {
-                if constexpr (kFirst) {
-                    // One bit for each key: compared one by one, three bounds a key
-                    // become branches (5 us a tile).
-                    int row = r;            // (so that its position takes no register elsewhere)
-                    asm volatile("" : "+r"(row));
-                    const int qpos = q0 + row / G, low = p.window > 0 ? qpos - p.window + 1 : 0;
-#pragma unroll
-                    for (int c = 0; c < kKeys / 32; ++c) {
-                        const int at = k0 + 32 * c;
-                        const uint32_t bits = below(qpos + 1 - at) & (~below(low - at) | below(p.first - at));
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) v[32 * c + j] = bits >> j & 1 ? v[32 * c + j] : -INFINITY;
+                // Causal mask (by selection: a masked slot may hold any bits) - only
+                // tiles that reach past the Q tile's first query position need one.
+                // The maximum is taken on raw scores (qscale > 0), the exponent
+                // is one fma: 2^(s * qscale - m).  Maximum and sums run as 8
+                // independent chains.
+                const int kt = kHalf ? 2 * it + qi : it, k0 = key_tile(kt) * kKeys;
+                const int q0 = p.start + tok0 + (kHalf ? 0 : qi * kTq);    // the Q tile's first position
+                const bool need_mask = k0 + kKeys - 1 > q0 ||
+                                       (kFirst && p.window > 0 && k0 < q0 + kTq - p.window && k0 + kKeys > p.first);
+                float v[kKeys];
+    #pragma unroll
+                for (int j = 0; j < kKeys; ++j) v[j] = __uint_as_float(sr[j >> 5][j & 31]);
+                if (need_mask) {
+                    if constexpr (kFirst) {
+                        // One bit for each key: compared one by one, three bounds a key
+                        // become branches (5 us a tile).
+                        int row = r;            // (so that its position takes no register elsewhere)
+                        asm volatile("" : "+r"(row));
+                        const int qpos = q0 + row / G, low = p.window > 0 ? qpos - p.window + 1 : 0;
+    #pragma unroll
+                        for (int c = 0; c < kKeys / 32; ++c) {
+                            const int at = k0 + 32 * c;
+                            const uint32_t bits = below(qpos + 1 - at) & (~below(low - at) | below(p.first - at));
+    #pragma unroll
+                            for (int j = 0; j < 32; ++j) v[32 * c + j] = bits >> j & 1 ? v[32 * c + j] : -INFINITY;
+                        }
+                    } else {
+    #pragma unroll
+                        for (int j = 0; j < kKeys; ++j) v[j] = k0 + j <= qpos ? v[j] : -INFINITY;
                     }
-                } else {
-#pragma unroll
-                    for (int j = 0; j < kKeys; ++j) v[j] = k0 + j <= qpos ? v[j] : -INFINITY;
                 }
-            }
-            // Row maximum: 8 independent chains of three-input maxima.
-            float mx8[8];
-#pragma unroll
-            for (int c = 0; c < 8; ++c) mx8[c] = fmaxf(v[c], v[c + 8]);
-#pragma unroll
-            for (int base = 16; base < kKeys; base += 16)
-#pragma unroll
-                for (int c = 0; c < 8; ++c) mx8[c] = fmax3(mx8[c], v[base + c], v[base + 8 + c]);
-            const float tmax = fmax3(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(mx8[3], mx8[4], mx8[5]),
-                                     fmaxf(mx8[6], mx8[7])) *
-                               p.qscale;
-            bool rescale = false;
-            float m_new = m_ref;
-            // (A row that has seen no key yet has O = 0, which needs no rescaling.)
-            if (kFirst ? m_ref == -INFINITY : kt == 0) {
-                m_new = tmax == -INFINITY ? 0.f : tmax;
-                m_ref = kFirst ? tmax : m_new;
-            } else if (tmax > m_ref + kHeadroom) {
-                rescale = true;
-                m_new = tmax;
-            }
-            // 2^(s * qscale - m) for key pairs: the arguments as packed fp32x2
-            // fmas, the sums as 4 packed chains.
-            const float2 qs2 = make_float2(p.qscale, p.qscale), nm2 = make_float2(-m_new, -m_new);
-            float2 ps4[4];
-            uint32_t pr[kKeys / 2];
-#pragma unroll
-            for (int j = 0; j < kKeys / 2; ++j) {
-                const float2 t = __ffma2_rn(make_float2(v[2 * j], v[2 * j + 1]), qs2, nm2);
-                const float2 e = make_float2(fast_exp2(t.x), fast_exp2(t.y));
-                ps4[j & 3] = j < 4 ? e : __fadd2_rn(ps4[j & 3], e);
-                pr[j] = pack_bf16(e.x, e.y);
-            }
-            const float2 s01 = __fadd2_rn(__fadd2_rn(ps4[0], ps4[1]), __fadd2_rn(ps4[2], ps4[3]));
-            const float ps = s01.x + s01.y;
-            // A rescale reads and writes O: P V(t - 1) is done (S(t) was issued after it).
-            if (__any_sync(0xffffffffu, rescale)) {
-                const float corr = rescale ? fast_exp2(m_ref - m_new) : 1.f;
-                l *= corr;
-#pragma unroll 1
-                for (int c = 0; c < D; c += 32) {
-                    uint32_t o[32];
-                    tmem_ld32(cols + kColO + c, o);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        o[j] = __float_as_uint(__uint_as_float(o[j]) * corr);
-                    tmem_st32(cols + kColO + c, o);
+                // Row maximum: 8 independent chains of three-input maxima.
+                float mx8[8];
+    #pragma unroll
+                for (int c = 0; c < 8; ++c) mx8[c] = fmaxf(v[c], v[c + 8]);
+    #pragma unroll
+                for (int base = 16; base < kKeys; base += 16)
+    #pragma unroll
+                    for (int c = 0; c < 8; ++c) mx8[c] = fmax3(mx8[c], v[base + c], v[base + 8 + c]);
+                const float tmax = fmax3(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(mx8[3], mx8[4], mx8[5]),
+                                         fmaxf(mx8[6], mx8[7])) *
+                                   p.qscale;
+                bool rescale = false;
+                float m_new = m_ref;
+                // (A row that has seen no key yet has O = 0, which needs no rescaling.)
+                if (kFirst ? m_ref == -INFINITY : it == 0) {
+                    m_new = tmax == -INFINITY ? 0.f : tmax;
+                    m_ref = kFirst ? tmax : m_new;
+                } else if (tmax > m_ref + kHeadroom) {
+                    rescale = true;
+                    m_new = tmax;
                 }
-                if (rescale) m_ref = m_new;
-            }
-            l += ps;
-            // P over the first half of S's columns.
-            tmem_st32(cols + kColP, *reinterpret_cast<uint32_t(*)[32]>(&pr[0]));
-            tmem_st32(cols + kColP + 32, *reinterpret_cast<uint32_t(*)[32]>(&pr[32]));
-            tmem_wait_st();
-            if (kFirst ? k0 + kKeys > kmax || (k0 < low0 && k0 + kKeys > p.first)
-                       : kt == ntiles - 1 && npages * kBlock > kmax) {
-                // Unwritten slots of the CTA's last page, and keys between the first
-                // tokens and the window that no query of the CTA sees: zero their V
-                // rows (128-byte lines, whole, so the swizzle inside a line does not
-                // matter), once the V tile has landed.  (Both Q tiles may end
-                // on this tile; each writes the same zeros before its P V.)
-                ok = __all_sync(0xffffffffu,
-                                mbar_wait_bounded(&v_full[kt % kStages], (kt / kStages) & 1,
-                                                  kWaitLimitNs));
-                if (!ok) break;
-                unsigned char *vt = sm + C::kVOff + (kt % kStages) * C::kTile;
-                if (kFirst) {
-                    // (One key of the tile for each of the Q tile's 128 threads.)
-                    if (hidden(k0 + r))
-                        for (int i = 0; i < C::kHalves * 8; ++i)
-                            *reinterpret_cast<uint4 *>(vt + (i >> 3) * C::kKVHalf + r * 128 + (i & 7) * 16) =
+                // 2^(s * qscale - m) for key pairs: the arguments as packed fp32x2
+                // fmas, the sums as 4 packed chains.
+                const float2 qs2 = make_float2(p.qscale, p.qscale), nm2 = make_float2(-m_new, -m_new);
+                float2 ps4[4];
+                uint32_t pr[kKeys / 2];
+    #pragma unroll
+                for (int j = 0; j < kKeys / 2; ++j) {
+                    const float2 t = __ffma2_rn(make_float2(v[2 * j], v[2 * j + 1]), qs2, nm2);
+                    const float2 e = make_float2(fast_exp2(t.x), fast_exp2(t.y));
+                    ps4[j & 3] = j < 4 ? e : __fadd2_rn(ps4[j & 3], e);
+                    pr[j] = pack_bf16(e.x, e.y);
+                }
+                const float2 s01 = __fadd2_rn(__fadd2_rn(ps4[0], ps4[1]), __fadd2_rn(ps4[2], ps4[3]));
+                const float ps = s01.x + s01.y;
+                // A rescale reads and writes O: P V(t - 1) is done (S(t) was issued after it).
+                if (__any_sync(0xffffffffu, rescale)) {
+                    const float corr = rescale ? fast_exp2(m_ref - m_new) : 1.f;
+                    l *= corr;
+    #pragma unroll 1
+                    for (int c = 0; c < D; c += 32) {
+                        uint32_t o[32];
+                        tmem_ld32(cols + kColO + c, o);
+                        tmem_wait_ld();
+    #pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            o[j] = __float_as_uint(__uint_as_float(o[j]) * corr);
+                        tmem_st32(cols + kColO + c, o);
+                    }
+                    if (rescale) m_ref = m_new;
+                }
+                l += ps;
+                // P over the first half of S's columns.
+                tmem_st32(cols + kColP, *reinterpret_cast<uint32_t(*)[32]>(&pr[0]));
+                tmem_st32(cols + kColP + 32, *reinterpret_cast<uint32_t(*)[32]>(&pr[32]));
+                tmem_wait_st();
+                if (kFirst ? k0 + kKeys > kmax || (k0 < low0 && k0 + kKeys > p.first)
+                           : it == ntiles - 1 && npages * kBlock > kmax) {
+                    // Unwritten slots of the CTA's last page, and keys between the first
+                    // tokens and the window that no query of the CTA sees: zero their V
+                    // rows (128-byte lines, whole, so the swizzle inside a line does not
+                    // matter), once the V tile has landed.  (Both Q tiles may end
+                    // on this tile; each writes the same zeros before its P V.)
+                    ok = __all_sync(0xffffffffu,
+                                    mbar_wait_bounded(&v_full[kt % kStages], (kt / kStages) & 1,
+                                                      kWaitLimitNs));
+                    if (!ok) break;
+                    unsigned char *vt = sm + C::kVOff + (kt % kStages) * C::kTile;
+                    if (kFirst) {
+                        // (One key of the tile for each of the Q tile's 128 threads.)
+                        if (hidden(k0 + r))
+                            for (int i = 0; i < C::kHalves * 8; ++i)
+                                *reinterpret_cast<uint4 *>(vt + (i >> 3) * C::kKVHalf + r * 128 + (i & 7) * 16) =
+                                    make_uint4(0u, 0u, 0u, 0u);
+                    } else {
+                        const int first = kmax - k0, nrow = npages * kBlock - kmax;
+                        for (int i = r; i < nrow * C::kHalves * 8; i += kRows) {
+                            const int line = i >> 3, chunk = i & 7;
+                            const int key = first + line % nrow, h = line / nrow;
+                            *reinterpret_cast<uint4 *>(vt + h * C::kKVHalf + key * 128 + chunk * 16) =
                                 make_uint4(0u, 0u, 0u, 0u);
-                } else {
-                    const int first = kmax - k0, nrow = npages * kBlock - kmax;
-                    for (int i = r; i < nrow * C::kHalves * 8; i += kRows) {
-                        const int line = i >> 3, chunk = i & 7;
-                        const int key = first + line % nrow, h = line / nrow;
-                        *reinterpret_cast<uint4 *>(vt + h * C::kKVHalf + key * 128 + chunk * 16) =
-                            make_uint4(0u, 0u, 0u, 0u);
+                        }
                     }
+                    fence_proxy_async_shared();
                 }
-                fence_proxy_async_shared();
+                // The tiles this Q tile's next MMAs read, V(kt) and K(kt + 1), have
+                // landed before P(kt) is published, so the MMA thread waits for P
+                // alone: a barrier wait in the thread that issues the MMAs costs
+                // ~300 cycles of an idle tensor pipe, even on a completed phase.
+                // (Their copies were issued once every MMA that used the slots
+                // before was complete, which S(kt) being here implies.)
+                if (quad == 2) {
+                    const int next = kt + (kHalf ? 2 : 1);
+                    bool landed = true;
+                    if (lane == 0)
+                        landed = mbar_wait_bounded(&v_full[kt % kStages], (kt / kStages) & 1,
+                                                   kWaitLimitNs) &&
+                                 (it + 1 >= my_ntiles ||
+                                  mbar_wait_bounded(&k_full[next % kStages], (next / kStages) & 1,
+                                                    kWaitLimitNs));
+                    ok = __all_sync(0xffffffffu, landed);
+                    if (!ok) break;
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_full(qi));
             }
-            // The tiles this Q tile's next MMAs read, V(kt) and K(kt + 1), have
-            // landed before P(kt) is published, so the MMA thread waits for P
-            // alone: a barrier wait in the thread that issues the MMAs costs
-            // ~300 cycles of an idle tensor pipe, even on a completed phase.
-            // (Their copies were issued once every MMA that used the slots
-            // before was complete, which S(kt) being here implies.)
-            if (quad == 2) {
-                bool landed = true;
-                if (lane == 0)
-                    landed = mbar_wait_bounded(&v_full[kt % kStages], (kt / kStages) & 1,
-                                               kWaitLimitNs) &&
-                             (kt + 1 >= my_ntiles ||
-                              mbar_wait_bounded(&k_full[(kt + 1) % kStages],
-                                                ((kt + 1) / kStages) & 1, kWaitLimitNs));
-                ok = __all_sync(0xffffffffu, landed);
-                if (!ok) break;
-            }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(p_full(qi));
+        };
+        if constexpr (kFirst) {
+            if (half)
+                softmax(std::true_type());
+            else
+                softmax(std::false_type());
+        } else {
+            softmax(std::false_type());
         }
         if (ok && my_ntiles > 0) {
-            const int kt = my_ntiles - 1;
-            ok = __all_sync(0xffffffffu, mbar_wait_bounded(pv_done(qi), kt & 1, kWaitLimitNs));
+            ok = __all_sync(0xffffffffu, mbar_wait_bounded(pv_done(qi), (my_ntiles - 1) & 1, kWaitLimitNs));
             tc_fence_after();
         }
         if (p.early) griddep_wait();  // writes come after the previous launch (no-op otherwise)
-        if (!ok) {
+        if (kFirst && half && ntiles > 1) {
+            // The groups' rows meet: O0 2^(m0 - m) + O1 2^(m1 - m), each group writing
+            // half of the dims.  (A warp reads its lanes of any TMEM columns.)
+            if (!ok && lane == 0) abort_now();
+            __shared__ float2 s_ends[kQTiles][kRows];
+            s_ends[qi][r] = make_float2(m_ref, l);
+            tc_fence_before();
+            asm volatile("bar.sync 1, %0;" ::"n"(128 * kQTiles) : "memory");
+            tc_fence_after();
+            if (!aborted()) {
+                const float2 e0 = s_ends[0][r], e1 = s_ends[1][r];
+                const float m = fmaxf(e0.x, e1.x);
+                const float w0 = e0.x == -INFINITY ? 0.f : fast_exp2(e0.x - m);
+                const float w1 = e1.x == -INFINITY ? 0.f : fast_exp2(e1.x - m);
+                const float sum = e0.y * w0 + e1.y * w1, inv = sum > 0.f ? 1.f / sum : 0.f;
+                const float f0 = w0 * inv, f1 = w1 * inv;
+                __nv_bfloat16 *orow =
+                    p.out + (static_cast<int64_t>(tok0 + (valid ? tl : 0)) * p.Hq + g * G + r % G) * D;
+#pragma unroll 1
+                for (int c = qi * (D / 2); c < (qi + 1) * (D / 2); c += 32) {
+                    uint32_t a[32], b[32];
+                    tmem_ld32(tmem + lane_off + kColO + c, a);
+                    tmem_ld32(tmem + lane_off + kGroupCols + kColO + c, b);
+                    tmem_wait_ld();
+                    if (valid && XS_BOUNDS(tok0 + tl < p.T && (g + 1) * G <= p.Hq, p.err_flag)) {
+                        auto at = [&](int j) {
+                            return fmaf(__uint_as_float(b[j]), f1, __uint_as_float(a[j]) * f0);
+                        };
+#pragma unroll
+                        for (int j = 0; j < 32; j += 8)
+                            *reinterpret_cast<uint4 *>(orow + c + j) =
+                                make_uint4(pack_bf16(at(j), at(j + 1)), pack_bf16(at(j + 2), at(j + 3)),
+                                           pack_bf16(at(j + 4), at(j + 5)), pack_bf16(at(j + 6), at(j + 7)));
+                    }
+                }
+            }
+        } else if (!ok) {
             if (lane == 0) abort_now();
         } else if (my_ntiles > 0) {
             // out = O / l for this row
@@ -821,16 +897,17 @@ int prefill(void *out, const void *q, const void *k_cache, const void *v_cache,
     if (ctas > 0x3fffffff) return XS_EUNSUPPORTED;
     if (kFirst) {
         // Under a window all CTAs take about as long.  Where the last wave would fill no
-        // more than half of the SMs, its pairs of Q tiles are two CTAs each, if it is
-        // the only one or small beside the others.  (us, so and as pairs: 36 pairs of 333
-        // queries 14.9 and 19.5, 512 of 4K 275 and 279; 192 of 1.5K 28 and 26.)
+        // more than half of the SMs, its pairs of Q tiles are two CTAs each.  (us, so and
+        // as pairs, 32q/8kv x 128: 8 pairs of 64 queries under a window of 4096 45 and 73,
+        // 160 of 1280 111 and 140, 512 of 4096 246 and 280; with a longer last wave all
+        // halves are one wave more: 96 pairs 88 and 74, 256 69 and 66.)
         int dev = 0, sms = 0;
         if (cudaGetDevice(&dev) != cudaSuccess ||
             cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
             return XS_EDEVICE;
         const int last = static_cast<int>(ctas % sms);
         p.units = static_cast<int>(ctas);
-        p.whole = last <= sms / 2 && (ctas < sms || ctas >= 3 * sms) ? p.units - last : p.units;
+        p.whole = last <= sms / 2 ? p.units - last : p.units;
         ctas += p.units - p.whole;
     }
     cudaLaunchConfig_t cfg = {};

@@ -12,7 +12,9 @@
 // a cluster counts a contiguous part of the positions and adds the bins that it
 // has met to those of all the others.  The scores stay in shared memory for the
 // passes.  Each warp counts, then writes, a contiguous part, so there are no
-// barriers within a pass and the order of atomics decides nothing.
+// barriers within a pass and the order of atomics decides nothing.  What is kept
+// is found once, as bits, a lane for 32 positions, and written from these (looked
+// for again at the writing: 2 to 9 us more).
 //
 // The second moves rows, in place.  Position j takes the row of position
 // kept[j] >= j, so a CTA that goes through j upwards and reads a tile before it
@@ -22,9 +24,10 @@
 // tokens) are neither read nor written.
 //
 // What bounds it: the move its bytes (48 sequences cut to 2K tokens in 4 layers, 3.2 GB
-// read and written: 497 us of the call's 540, 6.5 TB/s; rows of 256 bytes at
-// random places), the ranking the instructions and latencies of its passes (38 us
-// there; of one sequence of 32K 20 of 47).
+// read and written: 497 us of the call's 532, 6.5 TB/s; rows of 256 bytes at
+// random places), the ranking the instructions and latencies of its passes (a
+// call that moves nothing takes 29 us there, and 15 for one sequence of 32K, whose
+// whole call takes 38).
 #include <atomic>
 #include <climits>
 
@@ -103,10 +106,11 @@ __device__ __forceinline__ uint32_t peer_addr(const void *own, int rank) {
 template <int kThreads, int kCtas>
 __global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_constant__ EvictParams p) {
     after_previous();
-    extern __shared__ uint32_t held[];      // the bits of this CTA's part of the scores, where they fit
+    extern __shared__ uint32_t held[];      // the keys of this CTA's part of the scores, where they fit
     // The CTA's counts, and of all the candidates for each pass.
     __shared__ int hist[kBins], all_hist[kCtas > 1 ? 3 : 1][kCtas > 1 ? kBins : 1];
     __shared__ int sm[kThreads / 32], bin, left, counts[2];
+    __shared__ int2 tally[kThreads / 32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rank = blockIdx.x % kCtas;
     const int head = blockIdx.x / kCtas;
     const int hk = head % p.Hkv, entry = head / p.Hkv % p.n, layer = head / p.Hkv / p.n;
@@ -136,7 +140,7 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_con
     const bool fits = part <= p.held;
     if (n > p.limit && fits) {
 #pragma unroll 4
-        for (int t = lo + tid; t < hi; t += kThreads) held[t - mine] = score[t];
+        for (int t = lo + tid; t < hi; t += kThreads) held[t - mine] = key_of(score[t]);
     }
     if (n > p.limit) {
         const int32_t *row = p.tables + static_cast<int64_t>(b) * p.max_blocks;
@@ -159,7 +163,7 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_con
         return;         // the whole cluster
     }
 
-    auto key_at = [&](int t) { return key_of(fits ? held[t - mine] : __ldg(score + t)); };
+    auto key_at = [&](int t) { return fits ? held[t - mine] : key_of(__ldg(score + t)); };
 
     // The threshold: keys above it are kept, and `need` of those equal to it.
     uint32_t threshold = 0xffffffffu;       // above every key
@@ -218,33 +222,43 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_con
         __syncthreads();
     }
 
-    // Each warp's part of the positions, in order.
-    constexpr int kWarps = kThreads / 32;
+    // Each warp's part of the positions, in order, 1,024 at a time: lane i has the bits
+    // of 32 of them from its 32 i on that are kept, and of those equal to the threshold.
+    constexpr int kWarps = kThreads / 32, kLook = 1024, kSparse = 4;
     const int per = ((end - mine + kWarps - 1) / kWarps + 31) / 32 * 32;
     const int from = min(mine + warp * per, end), to = min(from + per, end);
-    auto look = [&](int t, uint32_t *over, uint32_t *even) {
-        bool o = false, e = false;
-        if (t < to) {
-            o = t < p.first || t >= n - p.recent;
-            if (!o) {
-                const uint32_t key = key_at(t);
-                o = key > threshold, e = key == threshold;
+    uint32_t over, even;
+    auto look = [&](int base) {
+        over = even = 0;
+#pragma unroll 4
+        for (int i = 0; i < min((to - base + 31) / 32, 32); ++i) {
+            const int t = base + 32 * i + lane;
+            bool o = false, e = false;
+            if (t < to) {
+                o = t < p.first || t >= n - p.recent;
+                if (!o) {
+                    const uint32_t key = key_at(t);
+                    o = key > threshold, e = key == threshold;
+                }
             }
+            const uint32_t os = __ballot_sync(0xffffffffu, o), es = __ballot_sync(0xffffffffu, e);
+            if (lane == i) over = os, even = es;
         }
-        *over = __ballot_sync(0xffffffffu, o);
-        *even = __ballot_sync(0xffffffffu, e);
     };
     int overs = 0, evens = 0;
-#pragma unroll 4
-    for (int t = from; t < to; t += 32) {
-        uint32_t over, even;
-        look(t + lane, &over, &even);
+    for (int base = from; base < to; base += kLook) {
+        look(base);
         overs += __popc(over), evens += __popc(even);
     }
-    // (A lane of each warp has its counts, the others 0.)
-    int all_overs, overs0 = scan_threads<kThreads>(lane == 0 ? overs : 0, sm, &all_overs);
-    int all_evens, evens0 = scan_threads<kThreads>(lane == 0 ? evens : 0, sm, &all_evens);
-    overs0 = __shfl_sync(0xffffffffu, overs0, 0), evens0 = __shfl_sync(0xffffffffu, evens0, 0);
+    overs = __reduce_add_sync(0xffffffffu, overs), evens = __reduce_add_sync(0xffffffffu, evens);
+    if (lane == 0) tally[warp] = make_int2(overs, evens);
+    __syncthreads();
+    int overs0 = 0, evens0 = 0, all_overs = 0, all_evens = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        if (w == warp) overs0 = all_overs, evens0 = all_evens;
+        all_overs += tally[w].x, all_evens += tally[w].y;
+    }
     if (kCtas > 1) {        // and what the CTAs before this one have
         if (tid == 0) counts[0] = all_overs, counts[1] = all_evens;
         all_sync<kCtas>();
@@ -257,18 +271,35 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_con
         // No CTA leaves before all have read its counts.
         asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
     }
-    int at = overs0 + min(evens0, need);
-    const uint32_t below = (1u << lane) - 1;
-#pragma unroll 2
-    for (int t = from; t < to; t += 32) {
-        uint32_t over, even;
-        look(t + lane, &over, &even);
-        const bool yes = (over >> lane & 1) || ((even >> lane & 1) && evens0 + __popc(even & below) < need);
-        const uint32_t all = __ballot_sync(0xffffffffu, yes);
-        const int j = at + __popc(all & below);
-        if (yes && XS_BOUNDS(j >= 0 && j < p.budget, p.err_flag)) kept[j] = t + lane;
-        at += __popc(all);
-        evens0 += __popc(even);
+    for (int base = from; base < to; base += kLook) {
+        if (to - from > kLook) look(base);      // (else they are still there)
+        // What this lane's positions have before them, and all lanes' together.
+        const int mine_too = __popc(over) | __popc(even) << 16;
+        int upto = mine_too;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, upto, d);
+            if (lane >= d) upto += y;
+        }
+        const int all = __shfl_sync(0xffffffffu, upto, 31), before = upto - mine_too;
+        const int evens1 = evens0 + (before >> 16);
+        // Of those equal to the threshold the first `need` of all are kept.
+        uint32_t rest = even;
+        for (int i = min(max(need - evens1, 0), __popc(even)); i > 0; --i) rest &= rest - 1;
+        int j = overs0 + (before & 0xffff) + min(evens1, need);
+        uint32_t bits = over | (even ^ rest);
+        auto put = [&](int k, int t) {
+            if (XS_BOUNDS(k >= 0 && k < p.budget, p.err_flag)) kept[k] = t;
+        };
+        // A lane with many of them (the last tokens) has them written by the warp.
+        for (uint32_t dense = __ballot_sync(0xffffffffu, __popc(bits) > kSparse); dense; dense &= dense - 1) {
+            const int l = __ffs(dense) - 1, j0 = __shfl_sync(0xffffffffu, j, l);
+            const uint32_t set = __shfl_sync(0xffffffffu, bits, l);
+            if (set >> lane & 1) put(j0 + __popc(set & ((1u << lane) - 1)), base + 32 * l + lane);
+        }
+        if (__popc(bits) <= kSparse)
+            for (; bits; bits &= bits - 1, ++j) put(j, base + 32 * lane + __ffs(bits) - 1);
+        overs0 += all & 0xffff, evens0 += all >> 16;
     }
     if (kCtas > 1) asm volatile("barrier.cluster.wait;" ::: "memory");
 }

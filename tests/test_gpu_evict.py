@@ -84,6 +84,14 @@ def test_long(n, width, budget):
     s.run([1, 0], 4, 100, budget, budget)
 
 
+@pytest.mark.parametrize("n,budget,recent,draw", [(70000, 3001, 1500, "spread"), (70000, 9000, 40, "ties"), (66000, 65999, 7, "equal"),
+                                                  (170001, 2500, 900, "odd")])
+def test_very_long(n, budget, recent, draw):
+    # Each warp has more positions than it looks at at a time; more scores than shared memory holds.
+    s = State([n, 50], 1, 1, 64, BF, budget, draw=draw)
+    s.run([1, 0], 4, recent, budget, budget)
+
+
 def test_entries_that_are_not_cut():
     s = State([100, 100, 100, 100, 100, 300], 1, 2, 64, BF, 3)
     extra = [0] * s.k.shape[1]

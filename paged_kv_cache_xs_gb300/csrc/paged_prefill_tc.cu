@@ -55,8 +55,9 @@
 //    on, as one list; pages that none of its queries sees arrive as zeros, and
 //    rows of V that none sees are zeroed where they were staged.  The CTAs of a
 //    short last wave have one Q tile each, whose key tiles the two softmax groups
-//    take in turn (64 queries under a window of 4,096: 45 us, by one group 65).
-//    4,096 tokens behind 28,672 under a window of 4,096 (32q/8kv x 128): 249 us.
+//    take in turn (64 queries under a window of 4,096: 45 us, by one group 65), and
+//    where there are few CTAs a cluster of them shares those tiles (19).
+//    4,096 tokens behind 28,672 under a window of 4,096 (32q/8kv x 128): 248 us.
 //  * TMEM: all 512 columns (per Q tile S/P 128, O 128).  Every wait is
 //    bounded; the MMA thread waits for its last MMA before the CTA frees TMEM.
 #include <cuda.h>
@@ -137,6 +138,7 @@ struct PParams {
     int early;
     int first, window;             // kFirst: what a query sees (window 0: every key)
     int units, whole;              // kFirst: pairs of Q tiles, and how many of them are one CTA's
+    int parts_log2;                // kFirst: CTAs (a cluster) that share a Q tile's keys (whole = 0)
 };
 
 // Shared-memory matrix descriptor: start, leading and stride byte offsets,
@@ -225,12 +227,90 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *tm,
         : "memory");
 }
 
-template <int D, int G, bool kFirst>
+// Where a CTA's part of an output keeps four dims (`piece`) of a row: rows of
+// neighbouring threads in different banks.
+constexpr int kMinShared = 3;
+template <int D> __device__ __forceinline__ int part_offset(int row, int piece) {
+    return (row * (D / 4) + (piece ^ (row & 7))) * 16;
+}
+__device__ __forceinline__ uint32_t peer_addr(const void *own, int rank) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(own)), "r"(rank));
+    return a;
+}
+__device__ __forceinline__ float2 peer_f32x2(uint32_t a) {
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ float4 peer_f32x4(uint32_t a) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(a)
+                 : "memory");
+    return v;
+}
+__device__ __forceinline__ void cluster_sync_all() {
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+
+// A cluster's parts of a Q tile's outputs (`o`, each row relative to the reference
+// in `ends`, which has its sum too): this CTA's share of the rows, by the 256 threads
+// of the softmax groups.  A thread has eight pieces on their way.
+template <int D, int kParts, typename F>
+__device__ __forceinline__ void join_parts(const unsigned char *o, const float2 *ends, int rank, int thread,
+                                           F &&out_of) {
+    constexpr int kPieces = kRows / kParts * (D / 4), kThem = 128 * kQTiles, kAtOnce = 8 / kParts;
+    static_assert(kPieces % (kThem * kAtOnce) == 0, "the same number for each thread");
+#pragma unroll 1
+    for (int base = thread; base < kPieces; base += kThem * kAtOnce) {
+        float2 e[kAtOnce][kParts];
+        float4 v[kAtOnce][kParts];
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u) {
+            const int i = base + u * kThem, row = rank * (kRows / kParts) + i / (D / 4), piece = i % (D / 4);
+#pragma unroll
+            for (int k = 0; k < kParts; ++k) {
+                e[u][k] = peer_f32x2(peer_addr(&ends[row], k));
+                v[u][k] = peer_f32x4(peer_addr(o + part_offset<D>(row, piece), k));
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u) {
+            const int i = base + u * kThem, row = rank * (kRows / kParts) + i / (D / 4), piece = i % (D / 4);
+            float m = -INFINITY, sum = 0.f;
+#pragma unroll
+            for (int k = 0; k < kParts; ++k) m = fmaxf(m, e[u][k].x);
+            float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int k = 0; k < kParts; ++k) {
+                if (e[u][k].x == -INFINITY) continue;       // it saw nothing, and may have written nothing
+                const float w = fast_exp2(e[u][k].x - m);
+                sum = fmaf(e[u][k].y, w, sum);
+                t.x = fmaf(v[u][k].x, w, t.x), t.y = fmaf(v[u][k].y, w, t.y);
+                t.z = fmaf(v[u][k].z, w, t.z), t.w = fmaf(v[u][k].w, w, t.w);
+            }
+            const float inv = sum > 0.f ? 1.f / sum : sum == 0.f ? 0.f : sum;   // (NaN stays one)
+            if (__nv_bfloat16 *to = out_of(row))
+                *reinterpret_cast<uint2 *>(to + 4 * piece) =
+                    make_uint2(pack_bf16(t.x * inv, t.y * inv), pack_bf16(t.z * inv, t.w * inv));
+        }
+    }
+}
+
+// kForm: kCausal (every key up to the query's position); kMasked (the mask of first tokens
+// and a window); kShared (the same, every CTA with one Q tile and, in clusters of
+// 2^parts_log2, a part of its keys).  (With kMasked and kShared in one a pair's tile
+// takes 3% longer.)
+enum Form { kCausal, kMasked, kShared };
+template <int D, int G, int kForm>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_tc_kernel(const __grid_constant__ CUtensorMap tmq,
                       const __grid_constant__ CUtensorMap tmk,
                       const __grid_constant__ CUtensorMap tmv, const PParams p) {
     using C = TCfg<D>;
+    constexpr bool kFirst = kForm != kCausal;
     constexpr int kTq = kRows / G;  // query tokens per Q tile
     extern __shared__ unsigned char smem_raw[];
     unsigned char *sm = reinterpret_cast<unsigned char *>(
@@ -248,6 +328,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t *mma_idle = grp0 + 3 * kQTiles;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(mma_idle + 1);
     __shared__ int s_abort;
+    // kFirst: references and sums of the softmax groups' rows, and of the CTA's.
+    __shared__ float2 s_ends[kFirst ? kQTiles : 1][kRows], s_part[kRows];
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     // Longest first: CTA i takes token tile (tiles - 1 - i / Hkv) of KV head
@@ -256,15 +338,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     // kFirst: CTAs from p.whole on take one Q tile each, two of them what others
     // do as one CTA.  Both groups of softmax warps then work on it: the first on the
     // list's even key tiles, the second on the odd ones, each with its own S, P and
-    // O, which meet at the end.
+    // O, which meet at the end.  Where there are few, a cluster of CTAs shares the list.
     const int n_tok_tiles = (kFirst ? p.units : static_cast<int>(gridDim.x)) / p.Hkv;
-    const bool half = kFirst && static_cast<int>(blockIdx.x) >= p.whole;
-    const int unit = half ? p.whole + (static_cast<int>(blockIdx.x) - p.whole) / 2 : static_cast<int>(blockIdx.x);
+    const int block = static_cast<int>(blockIdx.x) >> (kForm == kShared ? p.parts_log2 : 0);
+    const int rank = kForm == kShared ? static_cast<int>(blockIdx.x) & ((1 << p.parts_log2) - 1) : 0;
+    const int whole = kForm == kShared ? 0 : p.whole;
+    const bool half = kForm == kShared || (kFirst && block >= whole);
+    const int unit = half ? whole + (block - whole) / 2 : block;
     const int g = unit % p.Hkv;
     const int tok0 = (n_tok_tiles - 1 - unit / p.Hkv) * kQTiles * kTq +
-                     (half && ((static_cast<int>(blockIdx.x) - p.whole) & 1) ? kTq : 0);
+                     (half && ((block - whole) & 1) ? kTq : 0);
     const int ntok = kFirst ? max(0, min(half ? kTq : kQTiles * kTq, p.T - tok0))
                             : min(kQTiles * kTq, p.T - tok0);  // tokens of this CTA
+    if (kForm == kShared && ntok == 0) return;         // (the whole cluster)
     const int kmax = p.start + tok0 + ntok;            // keys [0, kmax) are read
     // kFirst: keys [low0, kmax) are in some query's window, and those below
     // `first` are seen by all that come after them; tile kt of the CTA's list is
@@ -272,10 +358,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int low0 = kFirst && p.window > 0 ? max(0, p.start + tok0 - p.window + 1) : 0;
     const int nfirst = kFirst ? min((min(p.first, low0) + kKeys - 1) / kKeys, low0 / kKeys) : 0;
     const int skipped = kFirst ? low0 / kKeys - nfirst : 0;
-    auto key_tile = [&](int kt) { return kFirst && kt >= nfirst ? kt + skipped : kt; };
+    auto key_tile = [&](int x) { return kFirst && x >= nfirst ? x + skipped : x; };
     // Whether no query of the CTA sees key t.
     auto hidden = [&](int t) { return t >= kmax || (kFirst && t >= p.first && t < low0); };
-    const int ntiles = kFirst && ntok == 0 ? 0 : (kmax + kKeys - 1) / kKeys - skipped;
+    const int listed = kFirst && ntok == 0 ? 0 : (kmax + kKeys - 1) / kKeys - skipped;
+    // This CTA's tiles are those from kt0 on of the list.
+    const int kt0 = kForm == kShared ? listed * rank >> p.parts_log2 : 0;
+    const int ntiles = kForm == kShared ? (listed * (rank + 1) >> p.parts_log2) - kt0 : listed;
     const int npages = (kmax + kBlock - 1) / kBlock;
     // Q tile qi holds tokens [qi * kTq, qi * kTq + tile_tokens(qi)) of the CTA
     // and attends to key tiles [0, tile_ntiles(qi)).
@@ -313,6 +402,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    if (kFirst) after_previous();
     auto abort_now = [&]() {
         raise_flag(p.err_flag, XS_FLAG_TIMEOUT);
         atomicExch(&s_abort, 1);
@@ -335,7 +425,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             auto page_row = [&](int kt) {
                 int row = p.oob_row;
-                const int pg = key_tile(kt) * kPagesPerTile + lane;
+                const int pg = key_tile(kt0 + kt) * kPagesPerTile + lane;
                 if (lane < kPagesPerTile && pg < npages &&
                     !(kFirst && pg * kBlock >= p.first && pg * kBlock + kBlock <= low0) &&
                     XS_BOUNDS(pg < p.n_ids, p.err_flag)) {
@@ -534,7 +624,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // The maximum is taken on raw scores (qscale > 0), the exponent
                 // is one fma: 2^(s * qscale - m).  Maximum and sums run as 8
                 // independent chains.
-                const int kt = kHalf ? 2 * it + qi : it, k0 = key_tile(kt) * kKeys;
+                const int kt = kHalf ? 2 * it + qi : it, k0 = key_tile(kHalf ? kt0 + kt : kt) * kKeys;
                 const int q0 = p.start + tok0 + (kHalf ? 0 : qi * kTq);    // the Q tile's first position
                 const bool need_mask = k0 + kKeys - 1 > q0 ||
                                        (kFirst && p.window > 0 && k0 < q0 + kTq - p.window && k0 + kKeys > p.first);
@@ -668,7 +758,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0) mbar_arrive(p_full(qi));
             }
         };
-        if constexpr (kFirst) {
+        if constexpr (kForm == kShared) {
+            softmax(std::true_type());
+        } else if constexpr (kFirst) {
             if (half)
                 softmax(std::true_type());
             else
@@ -681,39 +773,61 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
         }
         if (p.early) griddep_wait();  // writes come after the previous launch (no-op otherwise)
-        if (kFirst && half && ntiles > 1) {
-            // The groups' rows meet: O0 2^(m0 - m) + O1 2^(m1 - m), each group writing
-            // half of the dims.  (A warp reads its lanes of any TMEM columns.)
+        const bool parted = kForm == kShared && p.parts_log2 > 0;
+        if (kFirst && half && (ntiles > 1 || parted)) {
+            // The groups' rows meet: O0 2^(m0 - m) + O1 2^(m1 - m), each group with half
+            // of the dims.  (A warp reads its lanes of any TMEM columns.)
             if (!ok && lane == 0) abort_now();
-            __shared__ float2 s_ends[kQTiles][kRows];
             s_ends[qi][r] = make_float2(m_ref, l);
             tc_fence_before();
             asm volatile("bar.sync 1, %0;" ::"n"(128 * kQTiles) : "memory");
             tc_fence_after();
-            if (!aborted()) {
-                const float2 e0 = s_ends[0][r], e1 = s_ends[1][r];
-                const float m = fmaxf(e0.x, e1.x);
-                const float w0 = e0.x == -INFINITY ? 0.f : fast_exp2(e0.x - m);
-                const float w1 = e1.x == -INFINITY ? 0.f : fast_exp2(e1.x - m);
-                const float sum = e0.y * w0 + e1.y * w1, inv = sum > 0.f ? 1.f / sum : 0.f;
-                const float f0 = w0 * inv, f1 = w1 * inv;
+            const bool lost = aborted();
+            const float2 e0 = s_ends[0][r], e1 = s_ends[1][r];
+            const float m = fmaxf(e0.x, e1.x);
+            const float w0 = e0.x == -INFINITY ? 0.f : fast_exp2(e0.x - m);
+            const float w1 = e1.x == -INFINITY ? 0.f : fast_exp2(e1.x - m);
+            const float sum = e0.y * w0 + e1.y * w1;
+            // Of dims c .. c + 31; what a group without a tile would have is not read.
+            auto met = [&](int c, float f0, float f1, float(&o)[32]) {
+                uint32_t a[32], b[32];
+                tmem_ld32(tmem + lane_off + kColO + c, a);
+                tmem_ld32(tmem + lane_off + kGroupCols + kColO + c, b);
+                tmem_wait_ld();
+#pragma unroll
+                for (int k = 0; k < 32; ++k)
+                    o[k] = ntiles > 1 ? fmaf(__uint_as_float(b[k]), f1, __uint_as_float(a[k]) * f0)
+                                      : __uint_as_float(a[k]) * f0;
+            };
+            if (!parted) {
+                const float inv = sum > 0.f ? 1.f / sum : 0.f;
                 __nv_bfloat16 *orow =
                     p.out + (static_cast<int64_t>(tok0 + (valid ? tl : 0)) * p.Hq + g * G + r % G) * D;
 #pragma unroll 1
                 for (int c = qi * (D / 2); c < (qi + 1) * (D / 2); c += 32) {
-                    uint32_t a[32], b[32];
-                    tmem_ld32(tmem + lane_off + kColO + c, a);
-                    tmem_ld32(tmem + lane_off + kGroupCols + kColO + c, b);
-                    tmem_wait_ld();
-                    if (valid && XS_BOUNDS(tok0 + tl < p.T && (g + 1) * G <= p.Hq, p.err_flag)) {
-                        auto at = [&](int j) {
-                            return fmaf(__uint_as_float(b[j]), f1, __uint_as_float(a[j]) * f0);
-                        };
+                    float o[32];
+                    met(c, w0 * inv, w1 * inv, o);
+                    if (!lost && valid && XS_BOUNDS(tok0 + tl < p.T && (g + 1) * G <= p.Hq, p.err_flag)) {
 #pragma unroll
-                        for (int j = 0; j < 32; j += 8)
-                            *reinterpret_cast<uint4 *>(orow + c + j) =
-                                make_uint4(pack_bf16(at(j), at(j + 1)), pack_bf16(at(j + 2), at(j + 3)),
-                                           pack_bf16(at(j + 4), at(j + 5)), pack_bf16(at(j + 6), at(j + 7)));
+                        for (int k = 0; k < 32; k += 8)
+                            *reinterpret_cast<uint4 *>(orow + c + k) =
+                                make_uint4(pack_bf16(o[k], o[k + 1]), pack_bf16(o[k + 2], o[k + 3]),
+                                           pack_bf16(o[k + 4], o[k + 5]), pack_bf16(o[k + 6], o[k + 7]));
+                    }
+                }
+            } else {
+                // For the cluster: over the tiles, which no MMA or copy uses any more
+                // (unless a wait ran out: then NaN comes of it, whatever is there).
+                if (qi == 0) s_part[r] = lost ? make_float2(INFINITY, NAN) : make_float2(m, sum);
+                if (ntiles > 0 && !lost) {
+#pragma unroll 1
+                    for (int c = qi * (D / 2); c < (qi + 1) * (D / 2); c += 32) {
+                        float o[32];
+                        met(c, w0, w1, o);
+#pragma unroll
+                        for (int k = 0; k < 32; k += 4)
+                            *reinterpret_cast<float4 *>(sm + part_offset<D>(r, (c + k) / 4)) =
+                                make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
                     }
                 }
             }
@@ -745,6 +859,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
         }
+    }
+    if (kForm == kShared && p.parts_log2 > 0) {
+        // The parts of the cluster's CTAs meet, in each a share of the rows.
+        __syncwarp();
+        cluster_sync_all();
+        if (warp >= 4) {
+            auto out_of = [&](int row) {
+                const int tl = row / G;
+                return tl < ntok && XS_BOUNDS(tok0 + tl < p.T && (g + 1) * G <= p.Hq, p.err_flag)
+                           ? p.out + (static_cast<int64_t>(tok0 + tl) * p.Hq + g * G + row % G) * D
+                           : nullptr;
+            };
+            if (p.parts_log2 == 1)
+                join_parts<D, 2>(sm, s_part, rank, tid - 128, out_of);
+            else if (p.parts_log2 == 2)
+                join_parts<D, 4>(sm, s_part, rank, tid - 128, out_of);
+            else
+                join_parts<D, 8>(sm, s_part, rank, tid - 128, out_of);
+        }
+        cluster_sync_all();         // no CTA leaves while another reads from it
     }
     tc_fence_before();
     __syncthreads();
@@ -793,18 +927,18 @@ int encode(CUtensorMap *tm, const void *base, const cuuint64_t (&dims)[3],
 
 using KernelFn = void (*)(const CUtensorMap, const CUtensorMap, const CUtensorMap, const PParams);
 
-template <bool kFirst>
+template <int kForm>
 KernelFn pick(int D, int G) {
     if (D == 128) {
-        if (G == 1) return prefill_tc_kernel<128, 1, kFirst>;
-        if (G == 2) return prefill_tc_kernel<128, 2, kFirst>;
-        if (G == 4) return prefill_tc_kernel<128, 4, kFirst>;
-        if (G == 8) return prefill_tc_kernel<128, 8, kFirst>;
+        if (G == 1) return prefill_tc_kernel<128, 1, kForm>;
+        if (G == 2) return prefill_tc_kernel<128, 2, kForm>;
+        if (G == 4) return prefill_tc_kernel<128, 4, kForm>;
+        if (G == 8) return prefill_tc_kernel<128, 8, kForm>;
     } else if (D == 64) {
-        if (G == 1) return prefill_tc_kernel<64, 1, kFirst>;
-        if (G == 2) return prefill_tc_kernel<64, 2, kFirst>;
-        if (G == 4) return prefill_tc_kernel<64, 4, kFirst>;
-        if (G == 8) return prefill_tc_kernel<64, 8, kFirst>;
+        if (G == 1) return prefill_tc_kernel<64, 1, kForm>;
+        if (G == 2) return prefill_tc_kernel<64, 2, kForm>;
+        if (G == 4) return prefill_tc_kernel<64, 4, kForm>;
+        if (G == 8) return prefill_tc_kernel<64, 8, kForm>;
     }
     return nullptr;
 }
@@ -836,7 +970,40 @@ int prefill(void *out, const void *q, const void *k_cache, const void *v_cache,
     if (!aligned16(out) || !aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache))
         return XS_EALIGN;
     if (T == 0 || num_blocks == 0) return XS_OK;
-    KernelFn fn = pick<kFirst>(D, G);
+    const int tq = kQTiles * kRows / G;  // query tokens per CTA
+    int64_t ctas = static_cast<int64_t>((T + tq - 1) / tq) * Hkv;
+    if (ctas > 0x3fffffff) return XS_EUNSUPPORTED;
+    PParams p = {};
+    if (kFirst) {
+        // Under a window all CTAs take about as long.  Where the last wave would fill no
+        // more than half of the SMs, its pairs of Q tiles are two CTAs each.  (us, so and
+        // as pairs, 32q/8kv x 128: 160 pairs of 1280 queries under a window of 4096 111 and
+        // 140, 512 of 4096 246 and 280; with a longer last wave all halves are one wave
+        // more: 96 pairs 88 and 74, 256 69 and 66.)
+        int dev = 0, sms = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess ||
+            cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+            return XS_EDEVICE;
+        const int last = static_cast<int>(ctas % sms);
+        p.units = static_cast<int>(ctas);
+        p.whole = last <= sms / 2 ? p.units - last : p.units;
+        ctas += p.units - p.whole;
+        if (p.whole == 0) {
+            const int64_t tiles = static_cast<int64_t>((T + kRows / G - 1) / (kRows / G)) * Hkv;
+            const int all = (start_pos + T + kKeys - 1) / kKeys;        // key tiles of a list, at most
+            const int64_t seen = static_cast<int64_t>(window) + first + kRows / G + 2 * kKeys;
+            const int list = window > 0 && seen / kKeys < all ? static_cast<int>(seen / kKeys) : all;
+            // Where these are few, as many CTAs share a list as the device holds at once
+            // in clusters (76 of 2, 36 of 4, 15 of 8) and as it has tiles.  (us, so and by one
+            // CTA, 8 KV heads x 128: 64 queries under a window of 255 10.3 and 13.1, of 4096
+            // 18.8 and 45, 16 behind 30,000 keys 45 and 280; a list of two tiles 9.5 and 8.6.)
+            const int held[4] = {sms, sms / 2, sms * 36 / 152, sms * 15 / 152};
+            if (list >= kMinShared)
+                while (p.parts_log2 < 3 && tiles <= held[p.parts_log2 + 1] && list >> (p.parts_log2 + 1) > 0) ++p.parts_log2;
+            ctas <<= p.parts_log2;
+        }
+    }
+    KernelFn fn = !kFirst ? pick<kCausal>(D, G) : p.whole == 0 ? pick<kShared>(D, G) : pick<kMasked>(D, G);
     if (!fn) return XS_EUNSUPPORTED;
     // q [T, Hq, D] as (D, Hq, T), box (64, G, 128 / G): one D half of a CTA's rows.
     // Pools [num_blocks, Hkv, 16, D] as (64, rows, D / 64) with strides (2 D, 128)
@@ -858,7 +1025,7 @@ int prefill(void *out, const void *q, const void *k_cache, const void *v_cache,
     if (st != XS_OK) return st;
     const int smem = D == 128 ? TCfg<128>::kSmemBytes : TCfg<64>::kSmemBytes;
     static std::mutex mu;
-    static KernelFn raised[8] = {};
+    static KernelFn raised[16] = {};
     {
         std::lock_guard<std::mutex> lock(mu);
         bool done = false;
@@ -877,7 +1044,6 @@ int prefill(void *out, const void *q, const void *k_cache, const void *v_cache,
                 }
         }
     }
-    PParams p = {};
     p.out = static_cast<__nv_bfloat16 *>(out);
     p.block_ids = block_ids;
     p.n_ids = n_ids;
@@ -892,24 +1058,9 @@ int prefill(void *out, const void *q, const void *k_cache, const void *v_cache,
     p.first = first;
     p.window = window;
     p.early = (flags & XS_PREFILL_OVERLAP) ? 1 : 0;
-    const int tq = kQTiles * kRows / G;  // query tokens per CTA
-    int64_t ctas = static_cast<int64_t>((T + tq - 1) / tq) * Hkv;
-    if (ctas > 0x3fffffff) return XS_EUNSUPPORTED;
-    if (kFirst) {
-        // Under a window all CTAs take about as long.  Where the last wave would fill no
-        // more than half of the SMs, its pairs of Q tiles are two CTAs each.  (us, so and
-        // as pairs, 32q/8kv x 128: 8 pairs of 64 queries under a window of 4096 45 and 73,
-        // 160 of 1280 111 and 140, 512 of 4096 246 and 280; with a longer last wave all
-        // halves are one wave more: 96 pairs 88 and 74, 256 69 and 66.)
-        int dev = 0, sms = 0;
-        if (cudaGetDevice(&dev) != cudaSuccess ||
-            cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-            return XS_EDEVICE;
-        const int last = static_cast<int>(ctas % sms);
-        p.units = static_cast<int>(ctas);
-        p.whole = last <= sms / 2 ? p.units - last : p.units;
-        ctas += p.units - p.whole;
-    }
+    if (kFirst)
+        return launch_after(fn, dim3(static_cast<unsigned>(ctas)), kThreads, smem, stream, 1 << p.parts_log2, tmq,
+                            tmk, tmv, p);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(ctas));
     cfg.blockDim = dim3(kThreads);

@@ -117,3 +117,77 @@ def test_captured_and_a_bad_block():
     ids[16] = 1 << 24
     run()
     assert int(err) == ops.FLAG_BAD_BLOCK
+
+
+@pytest.mark.parametrize("T,Hq,Hkv,D", [(1, 4, 1, 128), (20, 8, 1, 64), (33, 8, 8, 128), (130, 16, 4, 64), (250, 4, 4, 128),
+                                        (600, 8, 8, 64)])
+@pytest.mark.parametrize("first,window", [(0, 0), (40, 1500), (300, 700), (3, 260)])
+def test_keys_shared_by_a_cluster(T, Hq, Hkv, D, first, window):
+    # One to 40 Q tiles, with lists of 3 to 25 key tiles in 2 to 8 parts.
+    q, k, v, ids = chunk(T, 2317, Hq, Hkv, D, T + window, first, window, std=2.0)
+    dev = device()
+    out, err = torch.full((T, Hq, D), 7.0, dtype=BF, device=dev), torch.zeros(1, dtype=torch.int32, device=dev)
+    x = [y.to(dev) for y in (q, k, v, ids)]
+    run = lambda: ops.xs_paged_prefill_first(out, *x, 2317, 0.1, first=first, window=window, err_flag=err)  # noqa: E731
+    run()
+    ref, bound = plain.prefill(q, k, v, ids.tolist(), 2317, 0.1, first, window)
+    d = (out.cpu().double() - ref).abs()
+    assert bool((d <= bound).all()), f"off by {d.max():.3e}, {(d / bound).max():.2f} of the bound"
+    want = out.clone()
+    for _ in range(3):
+        out.fill_(7.0)
+        run()
+        assert torch.equal(out, want), "the same result on every run"
+    assert int(err) == 0
+
+
+def test_infinities_and_nan_that_are_seen():
+    # In one part of the keys: they reach the outputs that they concern, through the cluster's join.
+    q, k, v, ids = chunk(16, 1500, 4, 2, 64, 9, 0, 0)
+    v[int(ids[20]), 0, 3, 7] = float("nan")
+    v[int(ids[70]), 1, 0, 5] = float("inf")
+    out = torch.empty(16, 4, 64, dtype=BF, device=device())
+    ops.xs_paged_prefill_first(out, *(y.to(device()) for y in (q, k, v, ids)), 1500, 0.125)
+    out = out.float().cpu()
+    assert bool(out[:, :2, 7].isnan().all()) and bool((out[:, 2:, 5] == float("inf")).all())
+    rest = torch.ones(16, 4, 64, dtype=torch.bool)
+    rest[:, :2, 7] = rest[:, 2:, 5] = False
+    v[int(ids[20]), 0, 3, 7] = v[int(ids[70]), 1, 0, 5] = 0
+    ref, bound = plain.prefill(q, k, v, ids.tolist(), 1500, 0.125, 0, 0)
+    assert bool(((out.double() - ref).abs() <= bound)[rest].all())
+
+
+def test_streams_and_graphs_of_shared_keys():
+    # Two graphs of two calls each, replayed beside each other; a call behind other work.
+    xs = [chunk(T, 900, 8, 2, 128, T, 4, 700) for T in (48, 20)]
+    dx = [[y.to(device()) for y in x] for x in xs]
+    outs = [[torch.zeros_like(x[0]) for _ in range(2)] for x in dx]
+    streams, graphs = [torch.cuda.Stream() for _ in xs], []
+    torch.cuda.synchronize()
+    for x, o, s in zip(dx, outs, streams):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            for y in o:
+                ops.xs_paged_prefill_first(y, *x, 900, 0.1, first=4, window=700)
+        graphs.append(graph)
+    refs = [plain.prefill(*x[:3], x[3].tolist(), 900, 0.1, 4, 700) for x in xs]
+    for _ in range(3):
+        for graph, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                graph.replay()
+        torch.cuda.synchronize()
+        for o, (ref, bound) in zip(outs, refs):
+            for y in o:
+                assert bool(((y.cpu().double() - ref).abs() <= bound).all())
+                y.zero_()
+    # q is written on the stream just before the call, and out read just behind it.
+    x, s, late = dx[0], streams[1], torch.zeros_like(dx[0][0])
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(2_000_000)
+        late.copy_(x[0])
+        ops.xs_paged_prefill_first(outs[0][0], late, *x[1:], 900, 0.1, first=4, window=700)
+        got = outs[0][0] + 0
+        late.zero_()
+    s.synchronize()
+    assert bool(((got.cpu().double() - refs[0][0]).abs() <= refs[0][1]).all())

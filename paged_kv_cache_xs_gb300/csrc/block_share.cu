@@ -266,20 +266,51 @@ __device__ __forceinline__ void push_freed(cg::cluster_group &cluster, ShareCoun
                                            int32_t *free_stack, int64_t top, int32_t *free_top,
                                            int64_t capacity, int32_t *extra_refs, int64_t num_blocks,
                                            int *err_flag) {
-    const int rank = cluster.block_rank(), ranks = cluster.num_blocks();
+    const int rank = cluster.block_rank(), ranks = cluster.num_blocks(), lane = threadIdx.x & 31;
     const Part part = warp_part(num_blocks, rank, ranks);
-    auto freed = [&](int64_t i) { return __ldcg(extra_refs + (num_blocks - 1 - i)) < 0; };
+    // 1,024 ids at a time: lane i has the bits of 32 of them from its 32 i on, so that most
+    // pools are read once (twice: 200,000 blocks 5 us more).
+    constexpr int kLook = 1024, kAtOnce = 8;
+    uint32_t bits;
+    auto look = [&](int64_t base) {
+        bits = 0;
+        for (int c = 0; c < kLook / 32 && base + 32 * c < part.hi; c += kAtOnce) {
+            bool freed[kAtOnce];
+#pragma unroll
+            for (int u = 0; u < kAtOnce; ++u) {
+                const int64_t i = base + 32 * (c + u) + lane;
+                freed[u] = i < part.hi && __ldcg(extra_refs + (num_blocks - 1 - i)) < 0;
+            }
+#pragma unroll
+            for (int u = 0; u < kAtOnce; ++u) {
+                const uint32_t all = __ballot_sync(0xffffffffu, freed[u]);
+                if (lane == c + u) bits = all;
+            }
+        }
+    };
+    int mine = 0;
+    for (int64_t base = part.lo; base < part.hi; base += kLook) {
+        look(base);
+        mine += __popc(bits);
+    }
     int64_t total;
-    const int64_t before = cluster_scan(cluster, counts, count_part(part, freed), &total);
-    write_part(part, top + before, freed, [&](int64_t k, int64_t i) {
-        const int64_t id = num_blocks - 1 - i;
-        if (!XS_BOUNDS(k >= 0 && id >= 0 && id < num_blocks, err_flag)) return;
-        if (k < capacity)
-            free_stack[k] = static_cast<int32_t>(id);
-        else
-            raise_flag(err_flag, XS_FLAG_POOL_EMPTY);
-        extra_refs[id] = 0;
-    });
+    int64_t at = top + cluster_scan(cluster, counts, __reduce_add_sync(0xffffffffu, mine), &total);
+    for (int64_t base = part.lo; base < part.hi; base += kLook) {
+        if (part.hi - part.lo > kLook) look(base);      // (else they are still there)
+        for (uint32_t some = __ballot_sync(0xffffffffu, bits != 0); some; some &= some - 1) {
+            const int from = __ffs(some) - 1;
+            const uint32_t all = __shfl_sync(0xffffffffu, bits, from);
+            const int64_t id = num_blocks - 1 - (base + 32 * from + lane);
+            const int64_t k = at + __popc(all & ((1u << lane) - 1));
+            at += __popc(all);
+            if (!(all >> lane & 1) || !XS_BOUNDS(k >= 0 && id >= 0 && id < num_blocks, err_flag)) continue;
+            if (k < capacity)
+                free_stack[k] = static_cast<int32_t>(id);
+            else
+                raise_flag(err_flag, XS_FLAG_POOL_EMPTY);
+            extra_refs[id] = 0;
+        }
+    }
     if (rank == 0 && threadIdx.x == 0) *free_top = static_cast<int32_t>(min(top + total, capacity));
 }
 
@@ -355,14 +386,22 @@ __global__ void __launch_bounds__(kShareThreads)
         if (to < 0 || to >= len) continue;
         int32_t *row = tables + static_cast<int64_t>(b) * max_blocks;
         const int pages = pages_of(len, bs, max_blocks);
-#pragma unroll 4
-        for (int col = pages_of(to, bs, max_blocks) + lane; col < pages; col += 32) {
-            const int32_t id = row[col];
-            if (id >= 0 && id < num_blocks)
-                atomicSub(extra_refs + id, 1);
-            else
-                raise_flag(err_flag, XS_FLAG_BAD_BLOCK);
-            if (XS_BOUNDS(col >= 0 && col < max_blocks, err_flag)) row[col] = -1;
+        // (Read before any is written: one after another, 320 entries took 3 us more.)
+        constexpr int kAtOnce = 8;
+        for (int col0 = pages_of(to, bs, max_blocks) + lane; col0 - lane < pages; col0 += 32 * kAtOnce) {
+            int32_t id[kAtOnce];
+#pragma unroll
+            for (int u = 0; u < kAtOnce; ++u) id[u] = col0 + 32 * u < pages ? row[col0 + 32 * u] : -1;
+#pragma unroll
+            for (int u = 0; u < kAtOnce; ++u) {
+                const int col = col0 + 32 * u;
+                if (col >= pages) continue;
+                if (id[u] >= 0 && id[u] < num_blocks)
+                    atomicSub(extra_refs + id[u], 1);
+                else
+                    raise_flag(err_flag, XS_FLAG_BAD_BLOCK);
+                if (XS_BOUNDS(col >= 0 && col < max_blocks, err_flag)) row[col] = -1;
+            }
         }
         __syncwarp();
         if (lane == 0 && XS_BOUNDS(b >= 0 && b < B, err_flag)) lens[b] = to;

@@ -157,6 +157,35 @@ def test_truncate(nb, width):
     assert int(s.err) == ops.FLAG_BAD_SLOT and s.lens.tolist()[5] == 17
 
 
+@pytest.mark.parametrize("nb,n,width", [(300000, 40, 700), (41000, 64, 640), (263000, 3, 11)])
+@pytest.mark.parametrize("release", [False, True], ids=["truncate", "release"])
+def test_given_back_from_large_pools(nb, n, width, release):
+    # More block ids than each warp looks at at a time, some with a second owner.
+    g = torch.Generator().manual_seed(nb + n)
+    tables = torch.randperm(nb, generator=g)[:n * width].view(n, width).to(torch.int32)
+    lens = torch.full((n,), width * 16, dtype=torch.int32)
+    new = torch.randint(0, width * 16, (n,), generator=g).to(torch.int32)
+    extra = (torch.rand(nb, generator=g) < 0.2).to(torch.int32)
+    pages = torch.zeros_like(new) if release else -(-new // 16)
+    gone = torch.cat([tables[b, int(pages[b]):] for b in range(n)]).long()
+    want_extra, want_tables = extra.clone(), tables.clone()
+    want_extra[gone] -= 1
+    free = sorted((i for i in gone.tolist() if want_extra[i] < 0), reverse=True)
+    want_extra.clamp_(min=0)
+    for b in range(n):
+        want_tables[b, int(pages[b]):] = -1
+    stack, top, err = torch.full((nb,), 7, dtype=torch.int32, device=device()), i32([5]), i32([0])
+    t, x, c, ids = tables.to(device()), extra.to(device()), lens.to(device()), torch.arange(n, dtype=torch.int32, device=device())
+    if release:
+        ops.xs_block_release(ids, t, c, stack, top, x, err_flag=err)
+    else:
+        ops.xs_block_truncate(ids, new.to(device()), t, c, stack, top, x, err_flag=err)
+    assert int(top) == 5 + len(free) and int(err) == 0
+    assert stack[:5 + len(free)].tolist() == [7] * 5 + free and bool((stack[5 + len(free):] == 7).all())
+    assert torch.equal(x.cpu(), want_extra) and torch.equal(t.cpu(), want_tables)
+    assert torch.equal(c.cpu(), torch.full_like(new, -1) if release else new)
+
+
 def test_truncate_shared_pages():
     s = Cut([100, 70, -1, -1, -1], 8, 40, 3)
     s.fork([0, 0, 1], [2, 3, 4])

@@ -227,9 +227,9 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *tm,
         : "memory");
 }
 
+constexpr int kMinShared = 3;   // key tiles of a list that a cluster shares
 // Where a CTA's part of an output keeps four dims (`piece`) of a row: rows of
 // neighbouring threads in different banks.
-constexpr int kMinShared = 3;
 template <int D> __device__ __forceinline__ int part_offset(int row, int piece) {
     return (row * (D / 4) + (piece ^ (row & 7))) * 16;
 }
@@ -605,8 +605,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // (kFirst: -infinity until the row has met a key that it sees.)
         float m_ref = kFirst ? -INFINITY : 0.f, l = 0.f;
         bool ok = true;
-        // (Two copies of the loop: as one, with both forms' indexes live, a pair's tile
-        // takes 2% longer.)
+        // (kMasked has two copies of the loop: as one, with both forms' indexes live, a
+        // pair's tile takes 2% longer.)
         auto softmax = [&](auto as_half) {
             constexpr bool kHalf = decltype(as_half)::value;
             for (int it = 0; it < my_ntiles; ++it) {
@@ -615,7 +615,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!ok) break;
                 tc_fence_after();
                 uint32_t sr[4][32];
-    #pragma unroll
+#pragma unroll
                 for (int c = 0; c < 4; ++c) tmem_ld32(cols + kColS + 32 * c, sr[c]);
                 tmem_wait_ld();
 
@@ -629,7 +629,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const bool need_mask = k0 + kKeys - 1 > q0 ||
                                        (kFirst && p.window > 0 && k0 < q0 + kTq - p.window && k0 + kKeys > p.first);
                 float v[kKeys];
-    #pragma unroll
+#pragma unroll
                 for (int j = 0; j < kKeys; ++j) v[j] = __uint_as_float(sr[j >> 5][j & 31]);
                 if (need_mask) {
                     if constexpr (kFirst) {
@@ -638,25 +638,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                         int row = r;            // (so that its position takes no register elsewhere)
                         asm volatile("" : "+r"(row));
                         const int qpos = q0 + row / G, low = p.window > 0 ? qpos - p.window + 1 : 0;
-    #pragma unroll
+#pragma unroll
                         for (int c = 0; c < kKeys / 32; ++c) {
                             const int at = k0 + 32 * c;
                             const uint32_t bits = below(qpos + 1 - at) & (~below(low - at) | below(p.first - at));
-    #pragma unroll
+#pragma unroll
                             for (int j = 0; j < 32; ++j) v[32 * c + j] = bits >> j & 1 ? v[32 * c + j] : -INFINITY;
                         }
                     } else {
-    #pragma unroll
+#pragma unroll
                         for (int j = 0; j < kKeys; ++j) v[j] = k0 + j <= qpos ? v[j] : -INFINITY;
                     }
                 }
                 // Row maximum: 8 independent chains of three-input maxima.
                 float mx8[8];
-    #pragma unroll
+#pragma unroll
                 for (int c = 0; c < 8; ++c) mx8[c] = fmaxf(v[c], v[c + 8]);
-    #pragma unroll
+#pragma unroll
                 for (int base = 16; base < kKeys; base += 16)
-    #pragma unroll
+#pragma unroll
                     for (int c = 0; c < 8; ++c) mx8[c] = fmax3(mx8[c], v[base + c], v[base + 8 + c]);
                 const float tmax = fmax3(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(mx8[3], mx8[4], mx8[5]),
                                          fmaxf(mx8[6], mx8[7])) *
@@ -676,7 +676,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float2 qs2 = make_float2(p.qscale, p.qscale), nm2 = make_float2(-m_new, -m_new);
                 float2 ps4[4];
                 uint32_t pr[kKeys / 2];
-    #pragma unroll
+#pragma unroll
                 for (int j = 0; j < kKeys / 2; ++j) {
                     const float2 t = __ffma2_rn(make_float2(v[2 * j], v[2 * j + 1]), qs2, nm2);
                     const float2 e = make_float2(fast_exp2(t.x), fast_exp2(t.y));
@@ -689,12 +689,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (__any_sync(0xffffffffu, rescale)) {
                     const float corr = rescale ? fast_exp2(m_ref - m_new) : 1.f;
                     l *= corr;
-    #pragma unroll 1
+#pragma unroll 1
                     for (int c = 0; c < D; c += 32) {
                         uint32_t o[32];
                         tmem_ld32(cols + kColO + c, o);
                         tmem_wait_ld();
-    #pragma unroll
+#pragma unroll
                         for (int j = 0; j < 32; ++j)
                             o[j] = __float_as_uint(__uint_as_float(o[j]) * corr);
                         tmem_st32(cols + kColO + c, o);
@@ -999,7 +999,8 @@ int prefill(void *out, const void *q, const void *k_cache, const void *v_cache,
             // 18.8 and 45, 16 behind 30,000 keys 45 and 280; a list of two tiles 9.5 and 8.6.)
             const int held[4] = {sms, sms / 2, sms * 36 / 152, sms * 15 / 152};
             if (list >= kMinShared)
-                while (p.parts_log2 < 3 && tiles <= held[p.parts_log2 + 1] && list >> (p.parts_log2 + 1) > 0) ++p.parts_log2;
+                while (p.parts_log2 < 3 && tiles <= held[p.parts_log2 + 1] && list >> (p.parts_log2 + 1) > 0)
+                    ++p.parts_log2;
             ctas <<= p.parts_log2;
         }
     }

@@ -137,7 +137,6 @@ struct Params {
     const int32_t *scored;  // [B] or null: n - 1
     float *logits;      // [B, Hkv, max_blocks * 16, G], in powers of two
     float2 *ends;       // [B, Hq]: a row's reference and the reciprocal of its sum
-    int *by_segment;    // how the call went (the second kernel has work behind the line alone)
 };
 
 // f(integral_constant<int, G>) for G in {1, 2, 4, 8}.
@@ -836,23 +835,69 @@ __device__ __forceinline__ void add_weights(const Params &p, int b, int hk, int 
     }
 }
 
+// Whether the kernel for many segments gives each a CTA: so unless the longest would
+// keep its CTA much longer than the others need, or the CTAs' starts and ends would.
+// (us, a CTA for each and the line, bf16, 8 KV heads x 128, G = 4: 20 sequences of 300
+// tokens 6.3 and 10.4, of 2000 25 and 31; 64 of 1024 41 and 46, of 4096 151 and 161; 128 of
+// 3000 220 and 233; 25 of 17 to 8193 76 and 35, 64 of them 90 and 60; 100 of 16 9.2 and 6.0.)
+__device__ __forceinline__ bool each_alone(const Params &p, int grid, int line_grid, uint32_t total, uint32_t longest,
+                                           int64_t alone, int64_t ends) {
+    const int segments = p.B * p.Hkv, waves = (segments + line_grid - 1) / line_grid;  // (32 bits: checked by the host)
+    const int64_t all = static_cast<int64_t>(total) * p.Hkv;
+    return segments <= grid && longest * alone <= (waves == 1 ? all + all / 4 : all / 2) + ends &&
+           (waves - 1) * ends <= all;
+}
+
 constexpr int kWeightThreads = 256;
 constexpr int kWeightTokens = 1024;     // of a CTA at a time
 
+// How the first kernel was launched, and its constants.
+struct FirstKernel {
+    int grid, line_grid, alone, ends;
+};
+
 // Behind the line (nothing where each segment had a CTA, so few CTAs that take
-// piece after piece of kWeightTokens: one for each piece cost 10 us there).
+// piece after piece of kWeightTokens: one for each piece cost 10 us there).  The
+// lengths do not change behind the first kernel's own start, which this one's
+// follows: they are looked at, and the first piece's old scores fetched, while that
+// kernel works.
 template <int G>
 __global__ void __launch_bounds__(kWeightThreads)
-    bounded_weights_kernel(const __grid_constant__ Params p, const int pieces) {
-    after_previous();
-    const bool idle = __ldcg(p.by_segment) != 0;
+    bounded_weights_kernel(const __grid_constant__ Params p, const int pieces, const FirstKernel first) {
+    const int lane = threadIdx.x & 31;
+    auto length = [&](int b) {
+        return min(XS_BOUNDS(b >= 0 && b < p.B, p.err_flag) ? max(__ldcg(p.lens + b), 0) : 0, p.max_blocks * kBlock);
+    };
+    uint32_t total = 0, longest = 0;
+    // (As the first kernel, which gives no segment a CTA if there are more than CTAs.)
+    const int lengths = p.B * p.Hkv <= first.grid ? p.B : 0;
+    for (int base = 0; base < lengths; base += 32) {
+        const uint32_t pages = base + lane < p.B ? (length(base + lane) + kBlock - 1) / kBlock : 0;
+        total += __reduce_add_sync(0xffffffffu, pages);
+        longest = max(longest, pages);
+    }
+    longest = __reduce_max_sync(0xffffffffu, longest);
+    const bool idle = each_alone(p, first.grid, first.line_grid, total, longest, first.alone, first.ends);
     const int64_t items = static_cast<int64_t>(p.B) * p.Hkv * pieces;
+    int b = 0, hk = 0, piece = 0, n = 0, scored = 0;
+    auto take = [&](int64_t i) {
+        const int segment = static_cast<int>(i / pieces);
+        piece = static_cast<int>(i - static_cast<int64_t>(segment) * pieces);
+        b = segment / p.Hkv, hk = segment - b * p.Hkv;
+        n = length(b);
+        scored = p.scored ? __ldcg(p.scored + b) : n - 1;
+    };
+    if (!idle && blockIdx.x < items) {
+        take(blockIdx.x);
+        const int t = piece * kWeightTokens + 32 * static_cast<int>(threadIdx.x);
+        if (threadIdx.x < kWeightTokens / 32 && t < min(n, scored))
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(
+                p.scores + (static_cast<int64_t>(b) * p.Hkv + hk) * p.max_blocks * kBlock + t));
+    }
+    after_previous();
+    if (idle) return;
     for (int64_t i = blockIdx.x; i < items; i += gridDim.x) {
-        const int segment = static_cast<int>(i / pieces), piece = static_cast<int>(i - static_cast<int64_t>(segment) * pieces);
-        const int b = segment / p.Hkv, hk = segment - b * p.Hkv;
-        const int n = min(XS_BOUNDS(b < p.B, p.err_flag) ? p.lens[b] : 0, p.max_blocks * kBlock);
-        const int scored = p.scored ? p.scored[b] : n - 1;
-        if (idle) return;       // (the first length is on its way with the answer)
+        if (i != blockIdx.x) take(i);
         for (int from = piece * kWeightTokens; from < n; from += pieces * kWeightTokens)
             add_weights<G>(
                 p, b, hk, min(kWeightTokens, n - from), [&](int x) { return from + x; },
@@ -1118,20 +1163,8 @@ __global__ void __launch_bounds__(32 * kLineWarps, line_ctas<T, D>())
         longest = max(longest, pages);
     }
     longest = __reduce_max_sync(0xffffffffu, longest);
-    const int64_t segments = static_cast<int64_t>(p.B) * p.Hkv, all = static_cast<int64_t>(total) * p.Hkv;
-    // A CTA for each segment, unless the longest would keep its CTA much longer than
-    // the others need, or the CTAs' starts and ends would.  (us, a CTA for each
-    // and the line, bf16, 8 KV heads x 128, G = 4: 20 sequences of 300 tokens 6.3 and 10.4,
-    // of 2000 25 and 31; 64 of 1024 41 and 46, of 4096 151 and 161; 128 of 3000 220 and
-    // 233; 25 of 17 to 8193 76 and 35, 64 of them 90 and 60; 100 of 16 9.2 and 6.0.)
-    const int waves = (p.B * p.Hkv + line_grid - 1) / line_grid;
-    const bool by_segment =
-        segments <= gridDim.x &&
-        static_cast<int64_t>(longest) * kAlone<T, D> <= (waves == 1 ? all + all / 4 : all / 2) + kEnds<T, D> &&
-        (waves - 1) * kEnds<T, D> <= all;
-    if (kWeights && me == 0 && lane == 0) *p.by_segment = by_segment;
-    if (by_segment) {
-        if (blockIdx.x >= segments) return;
+    if (each_alone(p, static_cast<int>(gridDim.x), line_grid, total, longest, kAlone<T, D>, kEnds<T, D>)) {
+        if (static_cast<int>(blockIdx.x) >= p.B * p.Hkv) return;
         const int b = blockIdx.x / p.Hkv, hk = blockIdx.x - b * p.Hkv;
         Segment<T, D, kWeights, kLineWarps, kStages> seg{p, sm, b, hk, 0, 1};
         if (seg.pages(ring, &tmk, &tmv, false)) seg.whole();
@@ -1414,10 +1447,9 @@ template <typename T, int D, bool kWeights> int launch(const Params &p, int dev,
     const int64_t want_groups = (static_cast<int64_t>(p.B) * (most + kSegmentCost) + kMinShare - 1) / kMinShare;
     const int64_t want = (want_groups * p.Hkv + kLineWarps - 1) / kLineWarps;
     const int line_grid = static_cast<int>(want < fill ? want : fill);
-    rc = launch_after(bounded_many_kernel<T, D, kWeights>,
-                      dim3(static_cast<int>(p.B <= kScannedB && segments > line_grid ? segments : line_grid)),
-                      32 * kLineWarps,
-                      line_smem<T, D, kWeights>(), stream, 1, tmk, tmv, p, line_grid);
+    const int grid = static_cast<int>(p.B <= kScannedB && segments > line_grid ? segments : line_grid);
+    rc = launch_after(bounded_many_kernel<T, D, kWeights>, dim3(grid), 32 * kLineWarps, line_smem<T, D, kWeights>(),
+                      stream, 1, tmk, tmv, p, line_grid);
     if (!kWeights || rc != XS_OK) return rc;
     const int pieces = max(1, min((p.max_blocks * kBlock + kWeightTokens - 1) / kWeightTokens, 8));
     const auto second = p.G == 1   ? bounded_weights_kernel<1>
@@ -1426,7 +1458,8 @@ template <typename T, int D, bool kWeights> int launch(const Params &p, int dev,
                                    : bounded_weights_kernel<8>;
     const int64_t items = segments * pieces, at_once = static_cast<int64_t>(sms) * 5;
     return launch_after(second, dim3(static_cast<int>(items < at_once ? items : at_once)), kWeightThreads, 0, stream, 1,
-                        p, pieces);
+                        p, pieces,
+                        FirstKernel{grid, line_grid, static_cast<int>(kAlone<T, D>), static_cast<int>(kEnds<T, D>)});
 }
 
 constexpr size_t kCounterBytes = kMaxWarps * sizeof(int);
@@ -1460,7 +1493,6 @@ int check_and_launch(Params &p, bool weights, int D, int block_size, float scale
     p.counters = reinterpret_cast<int *>(at), at += kCounterBytes;
     p.partials = reinterpret_cast<float *>(at), at += partial_bytes(D);
     if (weights) {
-        p.by_segment = reinterpret_cast<int *>(at), at += 16;
         p.ends = reinterpret_cast<float2 *>(at);
         at += (static_cast<size_t>(p.B) * p.Hq * sizeof(float2) + 15) / 16 * 16;
         p.logits = reinterpret_cast<float *>(at);
@@ -1507,7 +1539,7 @@ extern "C" size_t xs_paged_decode_first_workspace_bytes(int B, int Hq, int Hkv, 
 
 extern "C" size_t xs_paged_decode_weights_workspace_bytes(int B, int Hq, int Hkv, int D, int max_blocks_per_seq) {
     if (B <= 0 || Hq <= 0 || Hkv <= 0 || D <= 0 || max_blocks_per_seq < 0) return 0;
-    return xs_paged_decode_first_workspace_bytes(B, Hq, Hkv, D) + 16 +
+    return xs_paged_decode_first_workspace_bytes(B, Hq, Hkv, D) +
            (static_cast<size_t>(B) * Hq * sizeof(float2) + 15) / 16 * 16 +
            static_cast<size_t>(B) * Hq * max_blocks_per_seq * xs::bounded::kBlock * sizeof(float);
 }

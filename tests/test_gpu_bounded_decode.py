@@ -496,3 +496,18 @@ def test_a_workspace_serves_smaller_calls():
             check_scores(c, scores, w, 2, b)
         near(c.first_call(ws), ref, bound)
         assert int(ws.buf[:5120].count_nonzero()) == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("lens", [[40] * 280, [700] + [3] * 279, [64] * 256, [1] * 257 + [2000] * 40], ids=["same", "one-long", "256", "long-last"])
+def test_weights_at_the_forms_limits(lens):
+    # Batches about as large as a CTA for each segment is given to, of one KV head.
+    c = Case(lens, 4, 1, 64, BF, len(lens), width=130)
+    ws, scores = c.workspace(True), torch.zeros(len(lens), 1, 2080, device=device())
+    ref, bound, w = c.plain()
+    for _ in range(2):
+        near(c.weights_call(ws, scores, torch.zeros(len(lens), dtype=torch.int32, device=device())), ref, bound)
+        for b in range(0, len(lens), 7):
+            check_scores(c, scores, w, 4, b)
+        check_scores(c, scores, w, 4, len(lens) - 1)
+    assert int(c.err) == 0 and int(ws.buf[:5120].count_nonzero()) == 0

@@ -45,8 +45,8 @@
 //    P = 2^(s - m) in base 2 (arguments and sums as packed fp32x2
 //    operations), write P back to TMEM for the P V step.  The reference m only
 //    moves when a tile's maximum exceeds it by more than 8 (log2 units), and
-//    only then is the row of O in TMEM rescaled, so P stays <= 2^8 and most
-//    tiles never touch O.  Unwritten slots of the last page (any bits at all)
+//    only then is the row of O in TMEM rescaled, so P stays <= 2^8 (kFirst: 1,
+//    its m leads the maximum by 8) and most tiles never touch O.  Unwritten slots of the last page (any bits at all)
 //    are zeroed in the staged V tile, since 0 * NaN = NaN.  At the end:
 //    O / l, bf16, out.
 //  * With a window and first tokens (kFirst; xs_paged_prefill_first) query i
@@ -91,7 +91,7 @@ constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kGroupCols = 256;     // per Q tile: S 128 (P written over its first 64), O 128
 constexpr uint32_t kColS = 0, kColP = 0, kColO = 128;
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kHeadroom = 8.f;         // log2 units P may exceed 1 before O is rescaled
+constexpr float kHeadroom = 8.f;         // log2 units the maximum may grow by before O is rescaled
 constexpr uint64_t kWaitLimitNs = 4000000000ull;
 
 template <int D>
@@ -664,12 +664,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 bool rescale = false;
                 float m_new = m_ref;
                 // (A row that has seen no key yet has O = 0, which needs no rescaling.)
+                // kFirst: the reference leads the maximum by kHeadroom, so that no weight
+                // exceeds 1: V from 2^120 on times one of up to 2^8 would be an infinity.
+                constexpr float kLead = kFirst ? kHeadroom : 0.f;
                 if (kFirst ? m_ref == -INFINITY : it == 0) {
-                    m_new = tmax == -INFINITY ? 0.f : tmax;
-                    m_ref = kFirst ? tmax : m_new;
-                } else if (tmax > m_ref + kHeadroom) {
+                    m_new = tmax == -INFINITY ? 0.f : tmax + kLead;
+                    m_ref = kFirst ? tmax + kLead : m_new;
+                } else if (tmax > m_ref + (kHeadroom - kLead)) {
                     rescale = true;
-                    m_new = tmax;
+                    m_new = tmax + kLead;
                 }
                 // 2^(s * qscale - m) for key pairs: the arguments as packed fp32x2
                 // fmas, the sums as 4 packed chains.

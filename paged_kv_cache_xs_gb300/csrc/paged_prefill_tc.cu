@@ -63,6 +63,7 @@
 #include <cuda.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <mutex>
 #include <type_traits>
@@ -976,6 +977,8 @@ int prefill(void *out, const void *q, const void *k_cache, const void *v_cache,
     const int tq = kQTiles * kRows / G;  // query tokens per CTA
     int64_t ctas = static_cast<int64_t>((T + tq - 1) / tq) * Hkv;
     if (ctas > 0x3fffffff) return XS_EUNSUPPORTED;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return XS_EDEVICE;
     PParams p = {};
     if (kFirst) {
         // Under a window all CTAs take about as long.  Where the last wave would fill no
@@ -983,9 +986,8 @@ int prefill(void *out, const void *q, const void *k_cache, const void *v_cache,
         // as pairs, 32q/8kv x 128: 160 pairs of 1280 queries under a window of 4096 111 and
         // 140, 512 of 4096 246 and 280; with a longer last wave all halves are one wave
         // more: 96 pairs 88 and 74, 256 69 and 66.)
-        int dev = 0, sms = 0;
-        if (cudaGetDevice(&dev) != cudaSuccess ||
-            cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        int sms = 0;
+        if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
             return XS_EDEVICE;
         const int last = static_cast<int>(ctas % sms);
         p.units = static_cast<int>(ctas);
@@ -1028,25 +1030,18 @@ int prefill(void *out, const void *q, const void *k_cache, const void *v_cache,
     if (st == XS_OK) st = encode(&tmv, v_cache, pdims, pstr, pbox);
     if (st != XS_OK) return st;
     const int smem = D == 128 ? TCfg<128>::kSmemBytes : TCfg<64>::kSmemBytes;
-    static std::mutex mu;
-    static KernelFn raised[16] = {};
-    {
-        std::lock_guard<std::mutex> lock(mu);
-        bool done = false;
-        for (KernelFn f : raised) done |= f == fn;
-        if (!done) {
-            if (cudaFuncSetAttribute(reinterpret_cast<const void *>(fn),
-                                     cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
-                cudaSuccess) {
-                cudaGetLastError();
-                return XS_ELAUNCH;
-            }
-            for (KernelFn &f : raised)
-                if (!f) {
-                    f = fn;
-                    break;
-                }
+    // A kernel's shared memory is a setting of each device: the devices (bits) that
+    // have been told of this one's.  (By two threads at once: twice.)
+    static std::atomic<uint64_t> told[2][2][4];     // by form, D and G
+    std::atomic<uint64_t> &devices = told[kFirst && p.whole == 0][D == 128][G <= 2 ? G - 1 : G / 4 + 1];
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    if (!(devices.load(std::memory_order_acquire) & bit)) {
+        if (cudaFuncSetAttribute(reinterpret_cast<const void *>(fn),
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
+            cudaGetLastError();
+            return XS_ELAUNCH;
         }
+        devices.fetch_or(bit, std::memory_order_release);
     }
     p.out = static_cast<__nv_bfloat16 *>(out);
     p.block_ids = block_ids;

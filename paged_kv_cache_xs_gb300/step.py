@@ -220,7 +220,13 @@ class BoundedDecodeStep:
     the new tokens' places in their texts) are the caller's.  Owns the scores
     [layers, B, Hkv, max_blocks * 16], the attention's workspace and the rotated
     q.  ``start(slots)`` forgets the scores of slots whose sequences are new (or
-    were prefilled: a prompt's tokens begin to be counted with the next step)."""
+    were prefilled: a prompt's tokens begin to be counted with the next step).
+
+    A step's first ``run`` (by layers: one that is not above the last) counts
+    no more scored tokens than the sequence has behind its new one, so a sequence
+    may be shortened between steps (``ops.xs_block_truncate``: a rejected draft):
+    the tokens that replace the lost ones start from zero.  If more than one token is
+    appended to it before the next ``run``, its slot needs ``start``."""
 
     def __init__(self, B: int, Hq: int, Hkv: int, D: int, max_blocks_per_seq: int, layers: int,
                  dtype: torch.dtype, device, budget: int, limit: int | None = None,
@@ -240,6 +246,8 @@ class BoundedDecodeStep:
         self.scores = torch.zeros(layers, B, Hkv, max_blocks_per_seq * ops.BLOCK_SIZE,
                                   dtype=torch.float32, device=self.device)
         self.scored = torch.zeros(B, **i32)
+        self.behind = torch.zeros(B, **i32)     # tokens behind the new one
+        self.layer = None                       # of the last run of this step
         self.kept = torch.empty(layers, B, Hkv, self.budget, **i32)
         self.new_lens = torch.empty(B, **i32)
         self.slots = torch.arange(B, **i32)
@@ -258,6 +266,10 @@ class BoundedDecodeStep:
         context_lens[b] - 1 of its cache.  q_weight, k_weight (or None: no norm)
         and cos_sin (``ops.rope_table``, or None: no rotation) as in
         ``ops.xs_qk_norm_rope_append``."""
+        if self.layer is None or layer <= self.layer:
+            torch.sub(context_lens, 1, out=self.behind)
+            torch.minimum(self.scored, self.behind, out=self.scored)
+        self.layer = layer
         ops.xs_slot_mapping(block_tables, context_lens, ops.BLOCK_SIZE, k_cache.shape[0],
                             self.slot_mapping, err_flag=self.err_flag)
         ops.xs_qk_norm_rope_append(self.q, q, k_new, v_new, q_weight, k_weight, self.eps, cos_sin,
@@ -277,6 +289,7 @@ class BoundedDecodeStep:
         ops.xs_block_truncate(self.slots, self.new_lens, block_tables, context_lens, free_stack,
                               free_top, extra_refs, err_flag=self.err_flag)
         self.scored.copy_(context_lens)
+        self.layer = None
 
     def error_flags(self) -> int:
         """Device error bits raised so far (synchronises)."""

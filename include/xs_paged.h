@@ -283,8 +283,10 @@ int xs_block_alloc_decode(int32_t *block_tables, int max_blocks_per_seq, int32_t
  * xs_block_free - release sequences (PagedKVCache::free_sequence): all blocks
  * of each listed slot (seq_ids int32 [n], distinct, on the device) are pushed
  * on the free stack, the slot's table row is set to -1 and its length to -1
- * (no sequence; write 0 to register a new, empty one).  A full stack sets
- * XS_FLAG_POOL_EMPTY; an id outside [0, B) sets XS_FLAG_BAD_SLOT.
+ * (no sequence; write 0 to register a new, empty one).  An entry of -1 is a page
+ * that was given back before: it is not pushed, nor is another negative one
+ * (XS_FLAG_BAD_BLOCK).  A full stack sets XS_FLAG_POOL_EMPTY; an id outside [0, B)
+ * sets XS_FLAG_BAD_SLOT.
  */
 int xs_block_free(const int32_t *seq_ids, int n, int32_t *block_tables, int max_blocks_per_seq,
                   int32_t *context_lens, int B, int block_size, int32_t *free_stack,

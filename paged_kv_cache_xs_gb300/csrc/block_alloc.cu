@@ -59,6 +59,10 @@ __global__ void block_free_kernel(const int32_t *__restrict__ seq_ids, int B,
     int32_t *row = block_tables + static_cast<int64_t>(b) * max_blocks;
     for (int pg = threadIdx.x; pg < pages; pg += blockDim.x) {
         const int32_t blk = row[pg];
+        if (blk < 0) {      // -1: the page was given back before; never an id to hand out again
+            if (blk != -1) raise_flag(err_flag, XS_FLAG_BAD_BLOCK);
+            continue;
+        }
         const int32_t idx = atomicAdd(free_top, 1);
         if (idx >= capacity) {
             atomicSub(free_top, 1);

@@ -881,6 +881,9 @@ int xs_debug_kv4_wait_injection(int64_t wait_limit_ns, int skip_page);
  * an unfinished one), so an append never meets a shared page.  A sequence
  * that was forked, or forked from, is released with xs_block_release:
  * xs_block_free knows nothing of extra_refs.
+ * An entry of -1 in a sequence's row is a page that was given back before, and
+ * is no error: it has no owner to count, to lose or to move (but a sequence whose
+ * unfinished last page is missing can't be forked: XS_FLAG_BAD_BLOCK).
  *
  * xs_block_fork - for every i < n the empty slot children[i] (a negative
  * length) becomes a copy of the sequence in slot parents[i]: its table lists
@@ -966,7 +969,10 @@ int xs_block_copy(void *k_pools, void *v_pools, int layers, int64_t layer_stride
  * xs_paged_decode_first - decode attention in which sequence b's query (its
  * token n - 1, n = context_lens[b]) sees the tokens t < first and t >= n -
  * window; window 0: every token.  Block table entries of pages without a seen
- * token are never read (they may be -1: such pages can be given back).  sinks
+ * token are never read.  They may be -1, for which the xs_block_* calls take a
+ * page that was given back; no call gives such pages back by itself: a caller
+ * whose layers all have the window puts a page's id on the free stack (or, if it
+ * is shared, takes one off its extra_refs) and -1 into the table.  sinks
  * [Hq] as in xs_paged_decode_sinks, or NULL.  context_lens[b] <= 0 gives out[b]
  * = 0.  Whatever the pages hold in hidden rows has no influence.  Logits,
  * weights and sums are held in fp32 (bf16: a weight enters the product with V

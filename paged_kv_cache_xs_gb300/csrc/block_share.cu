@@ -35,6 +35,7 @@ constexpr int kShareThreads = 1024;
 constexpr int kShareWarps = kShareThreads / 32;
 constexpr int kShareCluster = 8;
 constexpr int64_t kShareSmall = 4096;   // block ids, and table entries, of a single CTA
+constexpr int32_t kGivenBack = -1;      // in a sequence's row: its page was given back before
 
 // One warp's part [lo, hi) of [0, n), cut over the cluster's CTAs and warps.
 struct Part {
@@ -245,7 +246,7 @@ __global__ void __launch_bounds__(kShareThreads)
                     id = from[col];
                     if (id >= 0 && id < num_blocks)
                         atomicAdd(extra_refs + id, 1);
-                    else
+                    else if (id != kGivenBack)
                         raise_flag(err_flag, XS_FLAG_BAD_BLOCK);
                 } else if (col == full) {
                     id = row_new[k];
@@ -346,7 +347,7 @@ __global__ void __launch_bounds__(kShareThreads)
             if (col < pages) {
                 if (id >= 0 && id < num_blocks)
                     atomicSub(extra_refs + id, 1);
-                else
+                else if (id != kGivenBack)
                     raise_flag(err_flag, XS_FLAG_BAD_BLOCK);
             }
             if (XS_BOUNDS(col >= 0 && col < max_blocks, err_flag)) row[col] = -1;
@@ -398,7 +399,7 @@ __global__ void __launch_bounds__(kShareThreads)
                 if (col >= pages) continue;
                 if (id[u] >= 0 && id[u] < num_blocks)
                     atomicSub(extra_refs + id[u], 1);
-                else
+                else if (id[u] != kGivenBack)
                     raise_flag(err_flag, XS_FLAG_BAD_BLOCK);
                 if (XS_BOUNDS(col >= 0 && col < max_blocks, err_flag)) row[col] = -1;
             }
@@ -447,7 +448,7 @@ __global__ void __launch_bounds__(kShareThreads)
             if (!XS_BOUNDS(b < B && col0 + 32 * u + lane < max_blocks, err_flag)) continue;
             if (id[u] >= 0 && id[u] < num_blocks)
                 remap[id[u]] = 0;
-            else
+            else if (id[u] != kGivenBack)
                 raise_flag(err_flag, XS_FLAG_BAD_BLOCK);
         }
     }

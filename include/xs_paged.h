@@ -877,8 +877,9 @@ int xs_debug_kv4_wait_injection(int64_t wait_limit_ns, int skip_page);
 /*
  * Shared pages.  extra_refs int32 [num_blocks], zero at first, counts each
  * block's owners beyond the first; blocks that the other allocator calls hand
- * out have 0 and need no change.  Only whole pages are shared (a fork copies
- * an unfinished one), so an append never meets a shared page.  A sequence
+ * out have 0 and need no change.  A fork shares whole pages alone (it copies
+ * an unfinished one), so an append meets a shared page only where a sequence was
+ * shortened into one (xs_block_truncate).  A sequence
  * that was forked, or forked from, is released with xs_block_release:
  * xs_block_free knows nothing of extra_refs.
  * An entry of -1 in a sequence's row is a page that was given back before, and
@@ -1074,8 +1075,12 @@ int xs_paged_decode_weights(void *out, float *scores, const int32_t *scored_lens
  * or attention.  A token keeps the rotation of the position that it had; later
  * tokens are rotated by their own (xs_qk_norm_rope_append with positions).
  * extra_refs (int32 [num_blocks], or NULL: nothing is shared): a sequence of
- * which a page that is written has further owners is not cut (XS_FLAG_SHARED);
- * it has to have pages of its own first.  Not cut either: an id outside [0, B)
+ * which a page that is written has further owners is not cut (XS_FLAG_SHARED, in
+ * every call), so that it grows until they are released.  No call gives it whole
+ * pages of its own; a caller that does takes blocks off the free stack, copies the
+ * pages to them (xs_block_copy), lists them in its table and takes one off the old
+ * pages' extra_refs.  With budget = first nothing is written and nothing refused:
+ * see xs_block_truncate on the last page.  Not cut either: an id outside [0, B)
  * or one that an earlier entry has (XS_FLAG_BAD_SLOT), and a sequence with a table
  * entry outside the pool behind the first tokens' whole pages (XS_FLAG_BAD_BLOCK).
  * A length beyond the table counts as the table's (XS_FLAG_BAD_LEN).
@@ -1095,8 +1100,10 @@ int xs_kv_evict(const int32_t *seq_ids, int n, void *k_pools, void *v_pools, int
  * length lose one owner and leave its table (-1); those that lost their last one
  * go back on the free stack as by xs_block_release.  After an eviction, a
  * rejected draft or a rolled-back request.  An unfinished last page stays the
- * sequence's; one that is shared (a length cut into a forked prefix) must be
- * replaced before an append to it.
+ * sequence's, also if it is shared (a length cut into a forked prefix), of which no
+ * flag tells: an append would then write the other owners' rows.  Before one, the
+ * sequence is forked into an empty slot (xs_block_fork: a block of its own for the
+ * unfinished page; xs_block_copy), and the old slot released (xs_block_release).
  * XS_FLAG_BAD_SLOT: an id outside [0, B), or one that an earlier entry has (the
  * earlier one counts).  XS_FLAG_BAD_BLOCK, XS_FLAG_POOL_EMPTY as
  * xs_block_release.

@@ -5,8 +5,9 @@
 //
 // extra_refs counts a block's owners beyond the first.  A block in use by one
 // sequence, and a free one, has 0, so the allocator need not know of it.
-// Only full pages are ever shared: a fork gives each child its own copy of
-// the parent's unfinished page, so no append meets a shared page.
+// A fork shares full pages alone: it gives each child its own copy of the parent's
+// unfinished page.  A shared page becomes unfinished only where a truncation ends in
+// it; before the next append the sequence is forked once more, and its slot released.
 //
 // Every result is the same on every run: entries are ranked by scans over
 // the caller's order or over the block ids, never by the order in which

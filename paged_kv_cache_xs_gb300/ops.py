@@ -720,7 +720,8 @@ def xs_block_truncate(seq_ids, new_lens, block_tables, context_lens, free_stack,
                       extra_refs, block_size=BLOCK_SIZE, err_flag=None, stream=None):
     """Shorten the sequences in slots seq_ids to new_lens (int32 [n]; negative,
     or not shorter: left alone) and give the pages behind back, as
-    xs_block_release does."""
+    xs_block_release does.  A sequence cut into a page that it shares has to be
+    forked into another slot, and its own released, before it is appended to."""
     _done("xs_block_truncate", (_bound or _bind()).xs_block_truncate(
         _entry("xs_block_truncate"), seq_ids, new_lens, block_tables, context_lens, free_stack,
         free_top, extra_refs, block_size, err_flag, _handle(stream)))

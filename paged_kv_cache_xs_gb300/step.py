@@ -226,7 +226,10 @@ class BoundedDecodeStep:
     no more scored tokens than the sequence has behind its new one, so a sequence
     may be shortened between steps (``ops.xs_block_truncate``: a rejected draft):
     the tokens that replace the lost ones start from zero.  If more than one token is
-    appended to it before the next ``run``, its slot needs ``start``."""
+    appended to it before the next ``run``, its slot needs ``start``.
+
+    A sequence is not cut while it shares a page that it would write (``bound``
+    raises XS_FLAG_SHARED each time): it grows until the others are released."""
 
     def __init__(self, B: int, Hq: int, Hkv: int, D: int, max_blocks_per_seq: int, layers: int,
                  dtype: torch.dtype, device, budget: int, limit: int | None = None,
@@ -286,6 +289,14 @@ class BoundedDecodeStep:
         ops.xs_kv_evict(self.slots, k_pools, v_pools, self.scores, block_tables, context_lens,
                         self.kept, self.new_lens, self.first, self.recent, self.limit,
                         extra_refs=extra_refs, err_flag=self.err_flag)
+        if self.first == self.budget and self.budget % ops.BLOCK_SIZE:
+            # The first tokens alone are kept, so the eviction wrote nothing, but the next
+            # token is written to their last page.
+            page = block_tables[:, self.budget // ops.BLOCK_SIZE].clamp(0, extra_refs.numel() - 1)
+            shared = (extra_refs[page.long()] > 0) & (self.new_lens >= 0)
+            self.new_lens.masked_fill_(shared, -1)
+            self.kept.masked_fill_(shared.view(1, -1, 1, 1), -1)
+            self.err_flag.bitwise_or_(shared.any().to(torch.int32) * ops.FLAG_SHARED)
         ops.xs_block_truncate(self.slots, self.new_lens, block_tables, context_lens, free_stack,
                               free_top, extra_refs, err_flag=self.err_flag)
         self.scored.copy_(context_lens)

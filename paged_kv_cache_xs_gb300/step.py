@@ -242,6 +242,9 @@ class BoundedDecodeStep:
         if self.budget <= 0 or self.recent < 0 or self.first < 0 or self.limit < self.budget or \
                 self.first + self.recent > self.budget:
             raise ValueError("0 <= first, recent; first + recent <= budget <= limit; budget > 0")
+        if self.limit >= max_blocks_per_seq * ops.BLOCK_SIZE:
+            raise ValueError("no sequence grows beyond the limit: the table holds "
+                             f"{max_blocks_per_seq * ops.BLOCK_SIZE} tokens")
         self.eps, self.interleaved = float(eps), bool(interleaved)
         self.device = torch.device(device)
         i32 = dict(dtype=torch.int32, device=self.device)

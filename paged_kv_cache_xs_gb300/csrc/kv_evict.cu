@@ -137,7 +137,7 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_con
     const int part = ((n + kCtas - 1) / kCtas + 31) / 32 * 32;
     const int mine = min(rank * part, n), end = min(mine + part, n);
     const int lo = max(p.first, mine), hi = min(n - p.recent, end);
-    const bool fits = part <= p.held;
+    const bool fits = end - mine <= p.held;
     if (n > p.limit && fits) {
 #pragma unroll 4
         for (int t = lo + tid; t < hi; t += kThreads) held[t - mine] = key_of(score[t]);

@@ -954,6 +954,53 @@ KernelFn pick(int D, int G) {
 }
 
 namespace {     // (the release and the debug library may be loaded side by side)
+// A kernel's shared memory is a setting of each device: `told` has a bit for those
+// that know of this kernel's.  (By two threads at once: told twice.)
+int tell(KernelFn fn, int smem, int dev, std::atomic<uint64_t> &told) {
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    if (told.load(std::memory_order_acquire) & bit) return XS_OK;
+    if (cudaFuncSetAttribute(reinterpret_cast<const void *>(fn), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             smem) != cudaSuccess) {
+        cudaGetLastError();
+        return XS_ELAUNCH;
+    }
+    told.fetch_or(bit, std::memory_order_release);
+    return XS_OK;
+}
+
+// What the device holds of a kShared kernel at once, in clusters of 2, 4 and 8 (a
+// cluster's CTAs are of one group of SMs).  Asked for once for each device.
+struct Held {
+    int of[3];
+};
+int clusters_held(KernelFn fn, int smem, int dev, std::atomic<uint64_t> (&known)[64], Held *held) {
+    uint64_t v = dev < 64 ? known[dev].load(std::memory_order_acquire) : 0;
+    if (!v) {
+        v = 1ull << 63;
+        for (int i = 0; i < 3; ++i) {
+            cudaLaunchAttribute attr;
+            attr.id = cudaLaunchAttributeClusterDimension;
+            attr.val.clusterDim.x = 2 << i;
+            attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3(2 << i);
+            cfg.blockDim = dim3(kThreads);
+            cfg.dynamicSmemBytes = smem;
+            cfg.attrs = &attr;
+            cfg.numAttrs = 1;
+            int n = 0;
+            if (cudaOccupancyMaxActiveClusters(&n, fn, &cfg) != cudaSuccess) {
+                cudaGetLastError();
+                return XS_EDEVICE;
+            }
+            v |= static_cast<uint64_t>(n) << (20 * i);
+        }
+        if (dev < 64) known[dev].store(v, std::memory_order_release);
+    }
+    for (int i = 0; i < 3; ++i) held->of[i] = static_cast<int>(v >> (20 * i) & 0xfffff);
+    return XS_OK;
+}
+
 // The call with its mask: kFirst, or every key up to the query's position.
 template <bool kFirst>
 int prefill(void *out, const void *q, const void *k_cache, const void *v_cache,
@@ -985,6 +1032,9 @@ int prefill(void *out, const void *q, const void *k_cache, const void *v_cache,
     if (ctas > 0x3fffffff) return XS_EUNSUPPORTED;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return XS_EDEVICE;
+    const int smem = D == 128 ? TCfg<128>::kSmemBytes : TCfg<64>::kSmemBytes;
+    const int by_g = G <= 2 ? G - 1 : G / 4 + 1;
+    static std::atomic<uint64_t> told[2][2][4];     // by form, D and G
     PParams p = {};
     if (kFirst) {
         // Under a window all CTAs take about as long.  Where the last wave would fill no
@@ -1008,10 +1058,16 @@ int prefill(void *out, const void *q, const void *k_cache, const void *v_cache,
             // in clusters (76 of 2, 36 of 4, 15 of 8) and as it has tiles.  (us, so and by one
             // CTA, 8 KV heads x 128: 64 queries under a window of 255 10.3 and 13.1, of 4096
             // 18.8 and 45, 16 behind 30,000 keys 45 and 280; a list of two tiles 9.5 and 8.6.)
-            const int held[4] = {sms, sms / 2, sms * 36 / 152, sms * 15 / 152};
-            if (list >= kMinShared)
-                while (p.parts_log2 < 3 && tiles <= held[p.parts_log2 + 1] && list >> (p.parts_log2 + 1) > 0)
+            if (list >= kMinShared) {
+                const KernelFn shared = pick<kShared>(D, G);
+                static std::atomic<uint64_t> known[2][4][64];   // 20 bits each, and 1 in the top one; 0: not yet
+                Held held;
+                int rc = tell(shared, smem, dev, told[1][D == 128][by_g]);
+                if (rc == XS_OK) rc = clusters_held(shared, smem, dev, known[D == 128][by_g], &held);
+                if (rc != XS_OK) return rc;
+                while (p.parts_log2 < 3 && tiles <= held.of[p.parts_log2] && list >> (p.parts_log2 + 1) > 0)
                     ++p.parts_log2;
+            }
             ctas <<= p.parts_log2;
         }
     }
@@ -1035,20 +1091,8 @@ int prefill(void *out, const void *q, const void *k_cache, const void *v_cache,
     if (st == XS_OK) st = encode(&tmk, k_cache, pdims, pstr, pbox);
     if (st == XS_OK) st = encode(&tmv, v_cache, pdims, pstr, pbox);
     if (st != XS_OK) return st;
-    const int smem = D == 128 ? TCfg<128>::kSmemBytes : TCfg<64>::kSmemBytes;
-    // A kernel's shared memory is a setting of each device: the devices (bits) that
-    // have been told of this one's.  (By two threads at once: twice.)
-    static std::atomic<uint64_t> told[2][2][4];     // by form, D and G
-    std::atomic<uint64_t> &devices = told[kFirst && p.whole == 0][D == 128][G <= 2 ? G - 1 : G / 4 + 1];
-    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
-    if (!(devices.load(std::memory_order_acquire) & bit)) {
-        if (cudaFuncSetAttribute(reinterpret_cast<const void *>(fn),
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
-            cudaGetLastError();
-            return XS_ELAUNCH;
-        }
-        devices.fetch_or(bit, std::memory_order_release);
-    }
+    st = tell(fn, smem, dev, told[kFirst && p.whole == 0][D == 128][by_g]);
+    if (st != XS_OK) return st;
     p.out = static_cast<__nv_bfloat16 *>(out);
     p.block_ids = block_ids;
     p.n_ids = n_ids;

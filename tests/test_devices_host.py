@@ -119,3 +119,15 @@ for dev in (0, 1, 70, 0):
                 assert decode("first", B, 8, 2, D, dtype) == 0 and decode("weights", B, 8, 2, D, dtype) == 0, (dev, D, dtype, B)
     assert evict(4) == 0 and evict(4096) == 0, dev
 """)
+
+
+def test_prompt_clusters_are_what_the_device_holds(fake):
+    # 8 Q tiles of one query, their keys shared by the largest clusters that are held 8 at a time.
+    fake("""
+for dev, held, want in ((0, (76, 36, 15), 8), (1, (70, 30, 7), 4), (2, (60, 7, 8), 2), (3, (7, 20, 20), 1), (0, (0, 0, 0), 8)):
+    fake.fake_device(dev)
+    for i in range(3):
+        fake.fake_held(2 << i, held[i])
+    for D in (64, 128):
+        assert prompt(1, 3000, 32, 8, D) == 0 and fake.fake_cluster() == want, (dev, D, fake.fake_cluster())
+""")

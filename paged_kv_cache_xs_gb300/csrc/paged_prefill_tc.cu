@@ -38,7 +38,9 @@
 //    chunked prefills; 128-key tiles read 8 KB for twice the MACs: 809 / 986.)
 //  * Warp 2 idle.  Warpgroup 0 gives up registers to the softmax
 //    warpgroups with setmaxnreg (kRegsCtl a thread there, kRegsSoftmax in
-//    the softmax), so nothing spills at D = 128.
+//    the softmax), so nothing of the causal form spills at D = 128 (at 64 up to 8
+//    bytes of a thread are stored and 36 loaded; kFirst, whose masks and key list
+//    take more: 16 to 40 stored, 56 to 192 loaded).
 //  * Warps 4-11 (softmax, four per Q tile; warp w reads TMEM lanes
 //    32*(w%4)..+31, one row per thread): load the row of S, causal mask
 //    (diagonal tiles only), row max (8 chains of three-input maxima),
@@ -46,9 +48,9 @@
 //    operations), write P back to TMEM for the P V step.  The reference m only
 //    moves when a tile's maximum exceeds it by more than 8 (log2 units), and
 //    only then is the row of O in TMEM rescaled, so P stays <= 2^8 (kFirst: 1,
-//    its m leads the maximum by 8) and most tiles never touch O.  Unwritten slots of the last page (any bits at all)
-//    are zeroed in the staged V tile, since 0 * NaN = NaN.  At the end:
-//    O / l, bf16, out.
+//    its m leads the maximum by 8) and most tiles never touch O.  Unwritten
+//    slots of the last page (any bits at all) are zeroed in the staged V tile,
+//    since 0 * NaN = NaN.  At the end: O / l, bf16, out.
 //  * With a window and first tokens (kFirst; xs_paged_prefill_first) query i
 //    sees the keys t <= i with t > i - window or t < first.  A CTA goes through
 //    the key tiles of the first tokens and those from its first query's window

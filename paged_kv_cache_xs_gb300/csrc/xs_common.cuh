@@ -189,6 +189,12 @@ __device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wa
 // while the kernel before it ended; it reads and writes nothing before that one
 // has completed, and only then lets the next one be placed - so that a kernel
 // that does not wait for this one still comes after everything before it.
+// A kernel may read before this wait what only the work in front of its predecessor
+// writes, if the predecessor is always the same kernel, launched by the same
+// call, which lets it be placed only after a wait of its own: so
+// bounded_weights_kernel (lengths, scored lengths, a prefetch of scores) behind
+// bounded_many_kernel.  (Launches with an overlap flag read early what their caller
+// promises that the launch before does not write.)
 __device__ __forceinline__ void after_previous() {
     griddep_wait();
     griddep_launch_dependents();
@@ -283,7 +289,8 @@ inline int launch_status() {
 // while the kernel before it on the stream ends, which takes 0.7 to 2 us off a
 // sequence of short launches that are not in a graph.  Its wait is for the kernel
 // before it alone, so every kernel of this library that may run beside its
-// predecessor completes only after that one.
+// predecessor completes only after that one; what may be read before the wait:
+// after_previous().
 template <typename... P, typename... A>
 inline int launch_after(void (*kernel)(P...), dim3 grid, int threads, size_t smem,
                         cudaStream_t stream, int cluster, A &&...args) {

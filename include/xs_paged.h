@@ -1011,9 +1011,10 @@ int xs_paged_decode_first(void *out, const void *q, int64_t q_stride, const void
  * query of the chunk sees are never read.  bf16 only; scale > 0; start_pos + T <
  * 2^31 - 512.
  * Weights are at most 1 before their sum divides them and enter the product with
- * V as bf16, as there: the output is off by 0.0022 of its size (root mean square)
- * where its own rounding leaves 0.0017.  (Weights of 16 bits: xs_paged_decode_first
- * with each row as a sequence of its own length under the same table.)
+ * V as bf16, as there: the output is off by 0.0021 to 0.0024 of its size (root mean
+ * square) where its own rounding leaves 0.0017.  (Weights of 16 bits:
+ * xs_paged_decode_first with each row as a sequence of its own length under the same
+ * table.)
  * Rows that no query of the chunk sees have no influence.  An infinity or a NaN
  * in a V row that some of 256 Hkv / Hq neighbouring queries see and others do not
  * may reach the outputs of all of them (as in xs_paged_prefill_tc).

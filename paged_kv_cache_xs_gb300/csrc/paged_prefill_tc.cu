@@ -687,11 +687,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const float2 t = __ffma2_rn(make_float2(v[2 * j], v[2 * j + 1]), qs2, nm2);
                     const float2 e = make_float2(fast_exp2(t.x), fast_exp2(t.y));
                     ps4[j & 3] = j < 4 ? e : __fadd2_rn(ps4[j & 3], e);
-                    // Weights as bf16, for one product with V: outputs are off by 0.0022 of
-                    // their size (root mean square; 0.0017 is their own rounding).  As two
-                    // bf16 values (cut and rest, as in the decode attention) and two products
-                    // they are off by the 0.0017 alone, but a pair's tile takes 2.8 us, not
-                    // 2.0: 4,096 queries behind 28,672 tokens under a window of 4,096 351 us,
+                    // Weights as bf16, for one product with V: outputs are off by 0.0021
+                    // to 0.0024 of their size (root mean square; 0.0017 is their own rounding).
+                    // As two bf16 values (cut and rest, as in the decode attention) and two
+                    // products they are off by the 0.0017 alone, but a pair's tile takes 2.8 us,
+                    // not 2.0: 4,096 queries behind 28,672 tokens under a window of 4,096 351 us,
                     // not 248; 333 of 12 heads 10.1, not 8.9.
                     pr[j] = pack_bf16(e.x, e.y);
                 }
